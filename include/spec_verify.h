@@ -462,6 +462,165 @@ int spec_adapt_init(void *state, int B, int min_k, int max_k, int32_t *k_offsets
 int spec_adapt_update(void *state, const int32_t *num_accepted, int B, int min_k, int max_k,
                       int32_t *k_offsets_out, void *stream);
 
+/*
+ * Logit operators: what a server does to logits before they are sampled or
+ * verified.  Packed rows in, packed rows out, in the layouts of the calls
+ * above, so a round is: process (and truncate) the draft rows,
+ * spec_draft_sample, process (and truncate) the target rows, spec_verify,
+ * spec_penalty_update.  The rule is one for both sides: the verify is lossless for
+ * the target distribution as these calls leave it.  The pages have no
+ * counterpart; the definitions are this library's and stand below.
+ *
+ * Rows.  `rows` says which rows a call has:
+ *   SPEC_ROWS_TARGET  the target rows of a chain: offsets = k_offsets, sequence
+ *                     b owns rows offsets[b] + b .. offsets[b+1] + b; row i of b
+ *                     follows the first i of its drafted tokens
+ *   SPEC_ROWS_DRAFT   the draft rows: offsets = k_offsets, b owns rows
+ *                     offsets[b] .. offsets[b+1] - 1; row i follows i tokens
+ *   SPEC_ROWS_NEXT    one row per sequence, which follows all of the tokens
+ *                     offsets[b] .. offsets[b+1] - 1 (a drafting step)
+ *   SPEC_ROWS_TREE    one row per tree node: offsets = node_offsets, parent and
+ *                     draft_tokens per node as in spec_tree_verify; row g
+ *                     follows the tokens of g and of its ancestors but the root
+ * R is the number of rows of the buffers; rows behind the last sequence's are
+ * neither read nor written.  draft_tokens (n_tokens of them) are read by the
+ * penalties alone, parent by the penalties of a tree.
+ *
+ * Every call: `out` is `logits` itself (in place) or does not overlap it.
+ * Pointers 16-byte aligned, V * sizeof(element) a multiple of 16, dtype
+ * SPEC_F32 or SPEC_BF16, as for spec_verify.  No workspace: calls on
+ * different streams are independent.  B = 0 and R = 0 are no-ops.  Errors the
+ * host sees: SPEC_ERR_INVALID_ARG, SPEC_ERR_ALIGNMENT, SPEC_ERR_CUDA.  Data errors
+ * found on the device write NaN, which the verify and the draft sampling
+ * report as a data error of the sequence: an invalid sequence (below) has
+ * all its rows NaN, an invalid offsets array (as for spec_verify, or asking
+ * for more than R rows or n_tokens tokens) all R rows.
+ */
+#define SPEC_ROWS_TARGET 0
+#define SPEC_ROWS_DRAFT 1
+#define SPEC_ROWS_NEXT 2
+#define SPEC_ROWS_TREE 3
+
+typedef struct {
+    int rows;                    /* SPEC_ROWS_* */
+    int B;                       /* sequences */
+    int R;                       /* rows of logits and out */
+    const int32_t *offsets;      /* [B+1] k_offsets or node_offsets */
+    const int32_t *parent;       /* [R], SPEC_ROWS_TREE only */
+    const int32_t *draft_tokens; /* [n_tokens] */
+    int n_tokens;
+} spec_rows_t;
+
+/*
+ * Processing: penalties for repeated tokens, biases, grammar masks.  For row r
+ * of sequence b and token v, each step rounded to fp32, the last result
+ * rounded once to the logits' type:
+ *   c    = counts[slots[b], v] + occurrences of v among the drafted tokens
+ *          that row r follows
+ *   seen = c > 0, or v in the prompt
+ *   y    = seen ? (z > 0 ? z / repetition[b] : z * repetition[b]) : z
+ *   y    = (y - frequency[b] * c) - presence[b] * [c > 0]
+ *   y    = y + the biases of v in b's list, in list order
+ *   y    = -inf where r's mask has bit v clear (whatever z is, NaN included)
+ * A logit that nothing applies to keeps its bits.  A mask that allows nothing
+ * leaves a row of -inf, which the verify reports as a data error.
+ *
+ *   counts       int32 [S, V]    how often slot s has emitted v; NULL: no
+ *                                penalties (then repetition .. slots are NULL)
+ *   seen         int32 [S, 2, W] bit arrays, W = (V + 31) / 32, bit v % 32 of
+ *                                word v / 32: [s, 0] v is in the prompt,
+ *                                [s, 1] counts[s, v] > 0.  counts entries whose
+ *                                bit is clear are not read.  Both are kept by
+ *                                spec_penalty_reset and spec_penalty_update.
+ *   slots        int32 [B]       each sequence's slot in [0, S); NULL: b.  Two
+ *                                sequences may share one.
+ *   repetition   float [B] > 0; frequency, presence float [B]; all finite;
+ *                                NULL: 1, 0, 0
+ *   bias_offsets int32 [B+1]     sequence b has the entries bias_offsets[b] ..
+ *                                bias_offsets[b+1] - 1 of bias_tokens and
+ *                                bias_values [n_bias]; NULL: no biases.  Values
+ *                                are finite or -inf.
+ *   mask         int32 [M, W]    bit arrays, a set bit allows the token; NULL: none
+ *   mask_rows    int32 [R]       the mask of each row, -1: none; NULL: row r has
+ *                                mask r (then M >= R)
+ * Invalid sequences: a parameter, slot, drafted token, parent or bias entry
+ * outside the ranges above.  A mask_rows entry outside [-1, M) makes its row NaN.
+ */
+typedef struct {
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const int32_t *counts;
+    const int32_t *seen;
+    const int32_t *slots;
+    int S;
+    const int32_t *bias_offsets;
+    const int32_t *bias_tokens;
+    const float *bias_values;
+    int n_bias;
+    const int32_t *mask;
+    const int32_t *mask_rows;
+    int M;
+} spec_logits_t;
+
+int spec_logits_process(const void *logits, const spec_rows_t *rows, const spec_logits_t *process, int V, int dtype,
+                        void *out, void *stream);
+
+/*
+ * Truncation: tokens outside the kept set become -inf, the others keep their
+ * bits.  In the order z descending, then index ascending, with
+ * w = exp((z - zmax) / T_b):
+ *   top_k  int32 [B]  keep the first k; 0 (or k >= V): all
+ *   top_p  float [B]  in (0, 1]: of these, keep the tokens whose mass before them
+ *                     is < p * Z, Z the mass of the first k; 1: all
+ *   min_p  float [B]  in [0, 1]: of these, keep (z - zmax) / T_b >= ln(min_p); 0: all
+ * Any of the three may be NULL.  At least one token is kept.  The sums decide
+ * which token is the last one, so they are exact to about 2^-45 of the
+ * largest weight.  Rows of greedy sequences (T_b = 0: their arg-max is kept
+ * anyway), and rows that hold NaN or +inf or only -inf, keep their bits.
+ * Invalid sequences: T_b < 0, NaN or infinite, or a setting outside its range.
+ */
+typedef struct {
+    const float *temperature; /* [B] */
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+} spec_truncate_t;
+
+int spec_logits_truncate(const void *logits, const spec_rows_t *rows, const spec_truncate_t *truncate, int V,
+                         int dtype, void *out, void *stream);
+
+/* spec_logits_process, then spec_logits_truncate on its result, in one call;
+ * the output equals that of the two calls bit for bit. */
+int spec_logits_process_truncate(const void *logits, const spec_rows_t *rows, const spec_logits_t *process,
+                                 const spec_truncate_t *truncate, int V, int dtype, void *out, void *stream);
+
+/*
+ * The counts that the penalties read, kept on the device (layout above).
+ *
+ * spec_penalty_reset: n slots get new sequences.  Slot slots[i] forgets what it
+ * held; the prompt is prompt_tokens[prompt_offsets[i] .. prompt_offsets[i+1]-1],
+ * and output_tokens / output_offsets, likewise, are tokens emitted already (a
+ * resumed sequence).  Either pair may be NULL (none).  n <= SPEC_MAX_B.  A slot
+ * that is named twice gets the later entry.  An entry with a slot outside
+ * [0, S) or offsets outside [0, n_prompt] / [0, n_output] is skipped; tokens
+ * outside [0, V) are not counted.
+ *
+ * spec_penalty_update: after a verify, the n_b + 1 tokens that each sequence
+ * emitted are counted in its slot: rows SPEC_ROWS_TARGET with the verify's
+ * k_offsets, or SPEC_ROWS_TREE with its node_offsets; R the slots of
+ * out_tokens.  A sequence with num_accepted < 0 (or more than it drafted) or a
+ * slot outside [0, S) is skipped, tokens outside [0, V) are not counted, an invalid
+ * offsets array leaves the counts as they are.  Sequences that share a slot
+ * are both counted.
+ * Both are asynchronous on `stream`; calls on the same state must be ordered.
+ */
+int spec_penalty_reset(int32_t *counts, int32_t *seen, int S, int V, const int32_t *slots, int n,
+                       const int32_t *prompt_offsets, const int32_t *prompt_tokens, int n_prompt,
+                       const int32_t *output_offsets, const int32_t *output_tokens, int n_output, void *stream);
+int spec_penalty_update(int32_t *counts, int32_t *seen, int S, int V, const int32_t *slots, const spec_rows_t *rows,
+                        const int32_t *out_tokens, const int32_t *num_accepted, void *stream);
+
 /* Bytes of device workspace needed by spec_verify_ex / spec_draft_sample_ex
  * for a call with B sequences over vocabulary V (0 for invalid arguments). */
 size_t spec_workspace_bytes(int B, int V, int dtype);

@@ -21,6 +21,8 @@ from ._binding import (  # noqa: F401
     MAX_TREE_NODES,
     MAX_V,
     NOALLOC_SCRATCH_BYTES,
+    PenaltyState,
+    ROWS,
     SPEC_ERRORS,
     SpecError,
     exported_symbols,
@@ -33,6 +35,11 @@ from ._binding import (  # noqa: F401
     shutdown,
     spec_draft_sample,
     spec_draft_sample_lse,
+    spec_logits_process,
+    spec_logits_process_truncate,
+    spec_logits_truncate,
+    spec_penalty_reset,
+    spec_penalty_update,
     spec_round,
     spec_round_host,
     spec_shard_decide,

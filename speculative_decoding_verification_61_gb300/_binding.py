@@ -11,6 +11,7 @@ F32, BF16 = 0, 1
 MAX_K, MAX_B, MAX_V = 32, 4096, 1 << 24
 MAX_TREE_NODES = 64
 MAX_SHARDS = 64
+ROWS = {"target": 0, "draft": 1, "next": 2, "tree": 3}  # SPEC_ROWS_*
 NOALLOC_SCRATCH_BYTES = 48 << 20  # spec_verify_noalloc's fixed scratch array
 ABI_VERSION = 1
 SPEC_ERRORS = {0: "SPEC_OK", -1: "SPEC_ERR_INVALID_ARG", -2: "SPEC_ERR_ALIGNMENT",
@@ -23,7 +24,9 @@ EXPORTS = ("spec_verify", "spec_verify_ex", "spec_draft_sample", "spec_draft_sam
            "spec_noalloc_bytes", "spec_adapt_state_bytes", "spec_adapt_init", "spec_adapt_update",
            "spec_draft_sample_lse", "spec_verify_lse", "spec_round", "spec_tree_verify",
            "spec_tree_draft_sample", "spec_shard_workspace_bytes", "spec_shard_stats",
-           "spec_shard_decide", "spec_shard_draw", "spec_shutdown", "spec_selfcheck_wait_timeout")
+           "spec_shard_decide", "spec_shard_draw", "spec_shutdown", "spec_selfcheck_wait_timeout",
+           "spec_logits_process", "spec_logits_truncate", "spec_logits_process_truncate",
+           "spec_penalty_reset", "spec_penalty_update")
 
 
 class SpecError(RuntimeError):
@@ -35,6 +38,25 @@ class SpecError(RuntimeError):
 class _Aux(ctypes.Structure):
     _fields_ = [("accept_prob", ctypes.c_void_p), ("residual_mass", ctypes.c_void_p),
                 ("lse_target", ctypes.c_void_p), ("lse_draft", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("B", ctypes.c_int), ("R", ctypes.c_int),
+                ("offsets", ctypes.c_void_p), ("parent", ctypes.c_void_p),
+                ("draft_tokens", ctypes.c_void_p), ("n_tokens", ctypes.c_int)]
+
+
+class _Logits(ctypes.Structure):
+    _fields_ = [("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("seen", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("S", ctypes.c_int), ("bias_offsets", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("n_bias", ctypes.c_int), ("mask", ctypes.c_void_p),
+                ("mask_rows", ctypes.c_void_p), ("M", ctypes.c_int)]
+
+
+class _Truncate(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p)]
 
 
 _lib = None
@@ -94,6 +116,15 @@ def lib():
     L.spec_adapt_init.restype = ip
     L.spec_adapt_update.argtypes = [vp, vp, ip, ip, ip, vp, vp]
     L.spec_adapt_update.restype = ip
+    rp, gp, tp = ctypes.POINTER(_Rows), ctypes.POINTER(_Logits), ctypes.POINTER(_Truncate)
+    L.spec_logits_process.argtypes = [vp, rp, gp, ip, ip, vp, vp]
+    L.spec_logits_truncate.argtypes = [vp, rp, tp, ip, ip, vp, vp]
+    L.spec_logits_process_truncate.argtypes = [vp, rp, gp, tp, ip, ip, vp, vp]
+    L.spec_penalty_reset.argtypes = [vp, vp, ip, ip, vp, ip, vp, vp, ip, vp, vp, ip, vp]
+    L.spec_penalty_update.argtypes = [vp, vp, ip, ip, vp, rp, vp, vp, vp]
+    for name in ("spec_logits_process", "spec_logits_truncate", "spec_logits_process_truncate",
+                 "spec_penalty_reset", "spec_penalty_update"):
+        getattr(L, name).restype = ip
     for name in ("spec_verify", "spec_verify_ex", "spec_draft_sample", "spec_draft_sample_ex",
                  "spec_round_host", "spec_workspace_status", "spec_abi_version",
                  "spec_draft_sample_lse", "spec_verify_lse", "spec_round", "spec_tree_verify",
@@ -608,3 +639,229 @@ class AdaptiveK:
         _raise(lib().spec_adapt_update(_p(self.state), _p(num_accepted), self.B, self.min_k, self.max_k,
                                        _p(self.k_offsets), _stream(stream)), "spec_adapt_update")
         return self.k_offsets
+
+
+# ------------------------------------------------------------- logit operators
+def _check_all(dev, named, size=None):
+    """Each (name, tensor, dtype[, entries]) on the logits' device, contiguous and of its type; None is left out."""
+    for name, t, dtype, *n in named:
+        if t is None:
+            continue
+        _check_dev(name, t, dtype)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
+        if n and t.numel() != n[0]:
+            raise ValueError(f"{name} must have {n[0]} entries, got {t.numel()}")
+
+
+def _rows_arg(logits, offsets, rows, draft_tokens, parent):
+    import torch
+    if rows not in ROWS:
+        raise ValueError(f"rows must be one of {sorted(ROWS)}, got {rows!r}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, V]")
+    R, B = logits.shape[0], offsets.numel() - 1
+    if B < 0:
+        raise ValueError("offsets must have B + 1 entries")
+    _check_dev("logits", logits)
+    _check_all(logits.device, [("offsets", offsets, torch.int32), ("draft_tokens", draft_tokens, torch.int32),
+                               ("parent", parent, torch.int32)])
+    if rows == "tree" and parent is not None and parent.numel() > R:
+        raise ValueError("parent has more nodes than logits has rows")
+    n_tokens = 0 if draft_tokens is None else draft_tokens.numel()
+    if rows == "tree" and parent is not None:
+        n_tokens = min(n_tokens, parent.numel())
+    return _Rows(ROWS[rows], B, R, _p(offsets), _p(parent), _p(draft_tokens), n_tokens), B, R
+
+
+def _out_arg(logits, out):
+    import torch
+    if out is None:
+        return torch.empty_like(logits)
+    _check_all(logits.device, [("out", out, logits.dtype, logits.numel())])
+    return out
+
+
+def _logits_arg(logits, B, R, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
+                bias_offsets, bias_tokens, bias_values, mask, mask_rows):
+    import torch
+    i32, f32, V = torch.int32, torch.float32, logits.shape[1]
+    W, S, M, n_bias = (V + 31) // 32, 0, 0, 0
+    if counts is not None:
+        if seen is None or draft_tokens is None:
+            raise ValueError("penalties need counts, seen and draft_tokens")
+        if rows == "tree" and parent is None:
+            raise ValueError("penalties on a tree need parent")
+        S = counts.shape[0]
+    elif any(t is not None for t in (repetition, frequency, presence, seen, slots)):
+        raise ValueError("penalties need counts, seen and draft_tokens")
+    if bias_offsets is not None:
+        if bias_tokens is None or bias_values is None:
+            raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
+        n_bias = bias_tokens.numel()
+    elif bias_tokens is not None or bias_values is not None:
+        raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
+    if mask is not None:
+        M = mask.shape[0]
+        if mask_rows is None and M < R:
+            raise ValueError("mask needs a row for each row of logits, or mask_rows")
+    elif mask_rows is not None:
+        raise ValueError("mask_rows without mask")
+    _check_all(logits.device, [
+        ("repetition", repetition, f32, B), ("frequency", frequency, f32, B), ("presence", presence, f32, B),
+        ("counts", counts, i32, S * V), ("seen", seen, i32, S * 2 * W), ("slots", slots, i32, B),
+        ("bias_offsets", bias_offsets, i32, B + 1), ("bias_tokens", bias_tokens, i32),
+        ("bias_values", bias_values, f32, n_bias), ("mask", mask, i32, M * W), ("mask_rows", mask_rows, i32, R)])
+    return _Logits(_p(repetition), _p(frequency), _p(presence), _p(counts), _p(seen), _p(slots), S, _p(bias_offsets),
+                   _p(bias_tokens), _p(bias_values), n_bias, _p(mask), _p(mask_rows), M)
+
+
+def _truncate_arg(logits, B, temperature, top_k, top_p, min_p):
+    import torch
+    f32 = torch.float32
+    _check_all(logits.device, [("temperature", temperature, f32, B), ("top_k", top_k, torch.int32, B),
+                               ("top_p", top_p, f32, B), ("min_p", min_p, f32, B)])
+    return _Truncate(_p(temperature), _p(top_k), _p(top_p), _p(min_p))
+
+
+def _on(t):
+    import torch
+    return torch.cuda.device(t.device)
+
+
+def spec_logits_process(logits, offsets, draft_tokens=None, *, rows="target", parent=None, repetition=None,
+                        frequency=None, presence=None, counts=None, seen=None, slots=None, bias_offsets=None,
+                        bias_tokens=None, bias_values=None, mask=None, mask_rows=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on packed logit
+    rows [R, V] (device tensors).  rows: "target" or "draft" (offsets =
+    k_offsets), "next" (one row per sequence, after all its drafted tokens)
+    or "tree" (offsets = node_offsets).  counts [S, V] and seen [S, 2, W] are
+    a PenaltyState's; biases are a ragged list per sequence; mask [M, W] holds
+    a bit per token (set: allowed) and mask_rows [R] the mask of each row (-1:
+    none).  out: the result's buffer, logits itself for in place; else a new
+    one, whose rows behind the last sequence's are not written.  Returns out."""
+    rw, B, R = _rows_arg(logits, offsets, rows, draft_tokens, parent)
+    dt = _dtype_code(logits)
+    ps = _logits_arg(logits, B, R, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
+                     bias_offsets, bias_tokens, bias_values, mask, mask_rows)
+    out = _out_arg(logits, out)
+    with _on(logits):
+        rc = lib().spec_logits_process(_p(logits), ctypes.byref(rw), ctypes.byref(ps), logits.shape[1], dt, _p(out),
+                                       _stream(stream))
+    _raise(rc, "spec_logits_process")
+    return out
+
+
+def spec_logits_truncate(logits, temperature, offsets, *, rows="target", top_k=None, top_p=None, min_p=None,
+                         out=None, stream=None):
+    """Top-k, top-p and min-p on packed logit rows [R, V] (device tensors, a
+    setting per sequence): tokens outside the kept set become -inf, ties go
+    to the lowest index.  rows, out: as in spec_logits_process.  Greedy
+    sequences' rows (temperature 0) stay as they are.  Returns out."""
+    rw, B, R = _rows_arg(logits, offsets, rows, None, None)
+    dt = _dtype_code(logits)
+    tr = _truncate_arg(logits, B, temperature, top_k, top_p, min_p)
+    out = _out_arg(logits, out)
+    with _on(logits):
+        rc = lib().spec_logits_truncate(_p(logits), ctypes.byref(rw), ctypes.byref(tr), logits.shape[1], dt, _p(out),
+                                        _stream(stream))
+    _raise(rc, "spec_logits_truncate")
+    return out
+
+
+def spec_logits_process_truncate(logits, temperature, offsets, draft_tokens=None, *, rows="target", parent=None,
+                                 repetition=None, frequency=None, presence=None, counts=None, seen=None, slots=None,
+                                 bias_offsets=None, bias_tokens=None, bias_values=None, mask=None, mask_rows=None,
+                                 top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """spec_logits_process, then spec_logits_truncate on its result, in one
+    call (the same outputs, bit for bit).  Returns out."""
+    rw, B, R = _rows_arg(logits, offsets, rows, draft_tokens, parent)
+    dt = _dtype_code(logits)
+    ps = _logits_arg(logits, B, R, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
+                     bias_offsets, bias_tokens, bias_values, mask, mask_rows)
+    tr = _truncate_arg(logits, B, temperature, top_k, top_p, min_p)
+    out = _out_arg(logits, out)
+    with _on(logits):
+        rc = lib().spec_logits_process_truncate(_p(logits), ctypes.byref(rw), ctypes.byref(ps), ctypes.byref(tr),
+                                                logits.shape[1], dt, _p(out), _stream(stream))
+    _raise(rc, "spec_logits_process_truncate")
+    return out
+
+
+def _state_arg(counts, seen):
+    import torch
+    if counts.dim() != 2:
+        raise ValueError("counts must be [S, V]")
+    S, V = counts.shape
+    _check_dev("counts", counts, torch.int32)
+    _check_all(counts.device, [("seen", seen, torch.int32, S * 2 * ((V + 31) // 32))])
+    return S, V
+
+
+def spec_penalty_reset(counts, seen, slots, prompt_offsets=None, prompt_tokens=None, output_offsets=None,
+                       output_tokens=None, stream=None):
+    """New sequences in the given slots of a penalty state: their counts are
+    cleared, their prompts' tokens (a ragged list) marked, and tokens they
+    have emitted already counted.  Returns (counts, seen)."""
+    import torch
+    S, V = _state_arg(counts, seen)
+    n = slots.numel()
+    if (prompt_offsets is None) != (prompt_tokens is None) or (output_offsets is None) != (output_tokens is None):
+        raise ValueError("offsets and tokens go together")
+    _check_all(counts.device, [
+        ("slots", slots, torch.int32), ("prompt_offsets", prompt_offsets, torch.int32, n + 1),
+        ("prompt_tokens", prompt_tokens, torch.int32), ("output_offsets", output_offsets, torch.int32, n + 1),
+        ("output_tokens", output_tokens, torch.int32)])
+    with _on(counts):
+        rc = lib().spec_penalty_reset(_p(counts), _p(seen), S, V, _p(slots), n, _p(prompt_offsets), _p(prompt_tokens),
+                                      0 if prompt_tokens is None else prompt_tokens.numel(), _p(output_offsets),
+                                      _p(output_tokens), 0 if output_tokens is None else output_tokens.numel(),
+                                      _stream(stream))
+    _raise(rc, "spec_penalty_reset")
+    return counts, seen
+
+
+def spec_penalty_update(counts, seen, out_tokens, out_num_accepted, offsets, *, rows="target", slots=None,
+                        stream=None):
+    """Counts the tokens that a verify emitted (its out_tokens and
+    out_num_accepted, with its k_offsets, or node_offsets for rows="tree") in
+    the sequences' slots.  Returns (counts, seen)."""
+    import torch
+    S, V = _state_arg(counts, seen)
+    if rows not in ("target", "tree"):
+        raise ValueError(f"rows must be 'target' or 'tree', got {rows!r}")
+    B = offsets.numel() - 1
+    if B < 0:
+        raise ValueError("offsets must have B + 1 entries")
+    _check_all(counts.device, [("offsets", offsets, torch.int32), ("out_tokens", out_tokens, torch.int32),
+                               ("out_num_accepted", out_num_accepted, torch.int32, B), ("slots", slots, torch.int32, B)])
+    rw = _Rows(ROWS[rows], B, out_tokens.numel(), _p(offsets), None, None, 0)
+    with _on(counts):
+        rc = lib().spec_penalty_update(_p(counts), _p(seen), S, V, _p(slots), ctypes.byref(rw), _p(out_tokens),
+                                       _p(out_num_accepted), _stream(stream))
+    _raise(rc, "spec_penalty_update")
+    return counts, seen
+
+
+class PenaltyState:
+    """What S slots of a running batch have emitted and been prompted with:
+    counts [S, V] and the bit arrays seen [S, 2, W] that spec_logits_process
+    reads.  Starts empty."""
+
+    def __init__(self, S: int, V: int, device="cuda"):
+        import torch
+        if S <= 0 or not 0 < V <= MAX_V:
+            raise ValueError(f"invalid penalty state S={S}, V={V}")
+        self.counts = torch.zeros((S, V), dtype=torch.int32, device=device)
+        self.seen = torch.zeros((S, 2, (V + 31) // 32), dtype=torch.int32, device=device)
+
+    def reset(self, slots, prompt_offsets=None, prompt_tokens=None, output_offsets=None, output_tokens=None,
+              stream=None):
+        """spec_penalty_reset on this state."""
+        spec_penalty_reset(self.counts, self.seen, slots, prompt_offsets, prompt_tokens, output_offsets,
+                           output_tokens, stream)
+
+    def update(self, out_tokens, out_num_accepted, offsets, *, rows="target", slots=None, stream=None):
+        """spec_penalty_update on this state."""
+        spec_penalty_update(self.counts, self.seen, out_tokens, out_num_accepted, offsets, rows=rows, slots=slots,
+                            stream=stream)

@@ -1,8 +1,8 @@
 """Build the sm_103a CUDA library in-tree:
 speculative_decoding_verification_61_gb300/_build/libspecverify.so
 
-Five translation units (chain verify, tree verify, vocab-sharded verify, the adaptive-k
-controller, the allocation-free verify), one
+Seven translation units (chain verify, tree verify, vocab-sharded verify, the adaptive-k
+controller, the allocation-free verify, logit processing, logit truncation), one
 -gencode (sm_103a), static CUDA runtime, so the shared object loads with
 plain ctypes and needs no GPU at load time.
 """
@@ -20,8 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libspecverify.so")
 SOURCES = [os.path.join(CSRC, n)
-           for n in ("spec_verify.cu", "tree_verify.cu", "shard_verify.cu", "adapt_k.cu", "noalloc.cu")]
-DEPENDS = SOURCES + [os.path.join(CSRC, n) for n in ("device_utils.cuh", "verify_common.cuh", "host_common.h")] + [
+           for n in ("spec_verify.cu", "tree_verify.cu", "shard_verify.cu", "adapt_k.cu", "noalloc.cu",
+                     "logits_process.cu", "logits_truncate.cu")]
+DEPENDS = SOURCES + [os.path.join(CSRC, n) for n in ("device_utils.cuh", "verify_common.cuh", "host_common.h",
+                                                         "logits_common.cuh", "logits_host.h")] + [
     os.path.join(INCLUDE, "spec_verify.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

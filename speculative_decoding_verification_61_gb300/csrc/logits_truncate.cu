@@ -1,0 +1,643 @@
+// logits_truncate.cu -- top-k, top-p and min-p truncation of packed logit
+// rows behind the C ABI of include/spec_verify.h: tokens outside the kept set
+// become -inf.
+//
+// All three keep a prefix of one order, z descending and then index
+// ascending, so a row's result is one cut: the last kept (z, index).  With
+// w = exp((z - zmax) / T):
+//   top-k   the first k tokens;
+//   top-p   the tokens whose mass before them is < p Z, Z the mass of the
+//           first k tokens;
+//   min-p   the tokens with (z - zmax) / T >= ln(min_p).
+// A token on the wrong side of the top-p border is a wrong answer, however
+// small its mass, so masses are exact far below one token's mass: weights
+// come from a two-term fp32 exponential (relative error about 2^-46), and
+// are summed as 64-bit integers, whose sum does not depend on its order.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "logits_host.h"
+
+namespace speclog {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kList = 1024;        // elements of one bin that are sorted in shared memory
+constexpr int kBinsPerOctave = 32;  // first-level bins per halving of the weight
+
+struct Truncate {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+};
+
+// ------------------------------------------------------------- order of keys
+// Unsigned key in the order of the values (-0 and +0 alike).
+__device__ __forceinline__ uint32_t key_of(float z) {
+    const uint32_t u = __float_as_uint(__fadd_rn(z, 0.0f));
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+// Position in the order: a larger one comes first.
+__device__ __forceinline__ uint64_t place_of(uint32_t key, int index) {
+    return static_cast<uint64_t>(key) << 32 | ~static_cast<uint32_t>(index);
+}
+
+// ------------------------------------------------------------------- weights
+// exp((z - zmax) / T) as a 64-bit fixed-point number with `frac` bits behind
+// the point.  2^x, x = (z - zmax) log2(e) / T, by the split x = n + j / 64 + r,
+// |r| <= 1/128: a table of 2^(j/64) in two fp32 terms, and the Taylor
+// polynomial of e^(r ln 2) whose leading terms are carried in two fp32 terms
+// as well (error-free sums and products).  Relative error below 2^-45.
+struct Weights {
+    float zmax, ch, cl;  // log2(e) / T in two terms
+    int frac;
+    const float2 *table;  // shared memory: 2^(j/64), j = 0..63
+};
+
+// s + e = a + b exactly (|a| >= |b| or a = 0)
+__device__ __forceinline__ float fast_two_sum(float a, float b, float *e) {
+    const float s = __fadd_rn(a, b);
+    *e = __fsub_rn(b, __fsub_rn(s, a));
+    return s;
+}
+__device__ __forceinline__ float two_sum(float a, float b, float *e) {
+    const float s = __fadd_rn(a, b);
+    const float bb = __fsub_rn(s, a);
+    *e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+    return s;
+}
+
+// The weight as mantissa * 2^exponent: mantissa in [2^48, 2^50), exponent <= -48;
+// mantissa 0 where the weight is below 2^-120.
+__device__ __forceinline__ uint64_t weight_mantissa(const Weights &w, float z, int *exponent) {
+    float dl;
+    const float dh = two_sum(z, -w.zmax, &dl);
+    const float xh = __fmul_rn(dh, w.ch);
+    if (!(xh > -120.0f)) {
+        *exponent = 0;
+        return 0;
+    }
+    float xl = __fmaf_rn(dh, w.ch, -xh);
+    xl = __fmaf_rn(dh, w.cl, xl);
+    xl = __fmaf_rn(dl, w.ch, xl);
+    const int m = __float2int_rn(xh * 64.0f);
+    const float r0 = __fsub_rn(xh, static_cast<float>(m) * 0.015625f);  // exact
+    float rl;
+    const float rh = two_sum(r0, xl, &rl);
+    // t = r ln 2
+    constexpr float kLn2Hi = 0.693147180559945309417f;
+    constexpr float kLn2Lo = static_cast<float>(0.69314718055994530941723212145818 - static_cast<double>(kLn2Hi));
+    const float th = __fmul_rn(rh, kLn2Hi);
+    float tl = __fmaf_rn(rh, kLn2Hi, -th);
+    tl = __fmaf_rn(rh, kLn2Lo, tl);
+    tl = __fmaf_rn(rl, kLn2Hi, tl);
+    // e^t - 1 = t + t^2 / 2 + t^3 (1/6 + t / 24 + t^2 / 120)
+    const float sq = __fmul_rn(th, th);
+    float sql = __fmaf_rn(th, th, -sq);
+    sql = __fmaf_rn(2.0f * th, tl, sql);
+    const float q = __fmul_rn(__fmul_rn(sq, th), __fmaf_rn(th, __fmaf_rn(th, 1.0f / 120.0f, 1.0f / 24.0f), 1.0f / 6.0f));
+    float el;
+    const float eh = two_sum(th, 0.5f * sq, &el);
+    el = __fadd_rn(el, __fadd_rn(__fadd_rn(tl, 0.5f * sql), q));
+    // 2^(j/64) (1 + e)
+    const float2 tj = w.table[m & 63];
+    const float ph = __fmul_rn(tj.x, eh);
+    float pl = __fmaf_rn(tj.x, eh, -ph);
+    pl = __fmaf_rn(tj.x, el, pl);
+    pl = __fmaf_rn(tj.y, eh, pl);
+    float ul;
+    const float uh = fast_two_sum(tj.x, ph, &ul);
+    ul = __fadd_rn(ul, __fadd_rn(tj.y, pl));
+    *exponent = (m >> 6) - 48;
+    return (static_cast<uint64_t>(__float2uint_rn(uh * 8388608.0f)) << 25) +
+           static_cast<int64_t>(__float2int_rn(ul * 281474976710656.0f));
+}
+
+__device__ __forceinline__ uint64_t fixed_weight(const Weights &w, float z) {
+    int e;
+    const uint64_t m = weight_mantissa(w, z, &e);
+    const int shift = -(e + w.frac);  // at least 1: frac <= 47
+    return shift > 63 ? 0 : (m + (1ull << (shift - 1))) >> shift;
+}
+
+// ------------------------------------------------------------ block helpers
+struct Shared {
+    int seq;
+    float2 table[64];
+    uint32_t count[kBins], lo[kBins], hi[kBins];
+    uint64_t list[kList];
+    uint64_t warp_mass[kWarps];
+    uint32_t warp_count[kWarps];
+    uint32_t red[kWarps];
+    uint32_t n_list, key_lo, key_hi;
+    // where the scan of the bins stopped
+    int bin;
+    uint32_t above_count, bin_count;
+    uint64_t above_mass, total_mass, mass;
+    uint64_t cut;
+    // the row's constants, found by one thread (fp64 runs at a small fraction of fp32's rate)
+    float ch, cl;
+    uint32_t min_p_key;
+    uint64_t target;
+};
+
+// Exclusive prefix sums over the block of a count and a mass per thread.
+__device__ __forceinline__ void block_scan(Shared &sm, uint32_t &c, uint64_t &m) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t c0 = c;
+    const uint64_t m0 = m;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
+        const uint64_t mm = __shfl_up_sync(0xffffffffu, m, off);
+        if (lane >= off) {
+            c += cc;
+            m += mm;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) {
+        sm.warp_count[warp] = c;
+        sm.warp_mass[warp] = m;
+    }
+    __syncthreads();
+    uint32_t bc = 0;
+    uint64_t bm = 0;
+    for (int i = 0; i < warp; ++i) {
+        bc += sm.warp_count[i];
+        bm += sm.warp_mass[i];
+    }
+    c += bc - c0;
+    m += bm - m0;
+}
+
+// What a search looks for: the first place in the order where the tokens up
+// to and with it number `need` (count) or weigh `target` (mass).
+struct Goal {
+    bool by_mass;
+    uint32_t need;
+    uint64_t target;
+    __device__ __forceinline__ bool reached(uint32_t c, uint64_t m) const {
+        return by_mass ? m >= target : c >= need;
+    }
+};
+
+// Finds the goal's bin in the histogram, given what lies above the first bin;
+// leaves it with what lies above it in sm.bin, sm.above_*, sm.bin_count, and
+// the mass of everything in sm.total_mass.  Without a bin that reaches the
+// goal the last one that holds anything is taken.
+__device__ __noinline__ void find_bin(Shared &sm, const Goal &goal, uint32_t above_count, uint64_t above_mass) {
+    constexpr int kPer = kBins / kThreads;
+    uint32_t c = 0, ci[kPer];
+    uint64_t m = 0, mi[kPer];
+    const int first = threadIdx.x * kPer;
+    if (threadIdx.x == 0) sm.bin = -1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        ci[i] = sm.count[first + i];
+        mi[i] = static_cast<uint64_t>(sm.hi[first + i]) << 32 | sm.lo[first + i];
+        c += ci[i];
+        m += mi[i];
+    }
+    const uint32_t own_c = c;
+    const uint64_t own_m = m;
+    block_scan(sm, c, m);
+    c += above_count;
+    m += above_mass;
+    if (threadIdx.x == kThreads - 1) sm.total_mass = m + own_m;
+    const bool here = goal.reached(c + own_c, m + own_m) && !goal.reached(c, m);
+    if (here) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (goal.reached(c + ci[i], m + mi[i])) {
+                sm.bin = first + i;
+                sm.above_count = c;
+                sm.above_mass = m;
+                sm.bin_count = ci[i];
+                break;
+            }
+            c += ci[i];
+            m += mi[i];
+        }
+    }
+    __syncthreads();
+}
+
+template <int DT, typename F>
+__device__ __forceinline__ void for_each(const char *row, int V, F &&f) {
+    constexpr int kPer = Elem<DT>::kPerVec;
+    const uint4 *p = reinterpret_cast<const uint4 *>(row);
+    for (int v = threadIdx.x; v < V / kPer; v += kThreads) {
+        float x[kPer];
+        Elem<DT>::unpack(p[v], x);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) f(x[i], v * kPer + i);
+    }
+}
+
+__device__ __forceinline__ int first_bin(float z, float zmax, float scale) {
+    const float f = __fmul_rn(__fsub_rn(zmax, z), scale);
+    return f >= static_cast<float>(kBins - 1) ? kBins - 1 : static_cast<int>(f);
+}
+
+__device__ __forceinline__ void add_to_bin(Shared &sm, int bin, bool mass, uint64_t w) {
+    atomicAdd(&sm.count[bin], 1u);
+    if (mass) {
+        const uint32_t lo = static_cast<uint32_t>(w);
+        const uint32_t old = atomicAdd(&sm.lo[bin], lo);
+        const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1u : 0u);
+        if (hi) atomicAdd(&sm.hi[bin], hi);
+    }
+}
+
+__device__ __forceinline__ void clear_bins(Shared &sm) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sm.count[i] = sm.lo[i] = sm.hi[i] = 0;
+    __syncthreads();
+}
+
+// The goal's place inside the bin that find_bin left: the bin's elements are
+// sorted if they fit the list, else the bin is split by key until they do or
+// one value is left, whose ties go by index.  Leaves the place in sm.cut, and
+// the mass of the tokens up to it in sm.mass.
+template <int DT>
+__device__ __noinline__ void find_place(Shared &sm, const char *row, int V, const Weights &w, float scale,
+                                        const Goal &goal, bool mass) {
+    const int bin = sm.bin;
+    uint32_t above_count = sm.above_count, n = sm.bin_count;
+    uint64_t above_mass = sm.above_mass;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sm.n_list = 0;
+        sm.key_lo = 0xffffffffu;
+        sm.key_hi = 0;
+    }
+    __syncthreads();
+    uint32_t klo = 0xffffffffu, khi = 0;
+    for_each<DT>(row, V, [&](float z, int i) {
+        if (first_bin(z, w.zmax, scale) != bin) return;
+        const uint32_t key = key_of(z);
+        klo = min(klo, key);
+        khi = max(khi, key);
+        if (n <= kList) sm.list[atomicAdd(&sm.n_list, 1u)] = place_of(key, i);
+    });
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    if ((threadIdx.x & 31) == 0) {
+        atomicMin(&sm.key_lo, klo);
+        atomicMax(&sm.key_hi, khi);
+    }
+    __syncthreads();
+    klo = sm.key_lo;
+    khi = sm.key_hi;
+    bool listed = n <= kList;
+    while (!listed && klo < khi) {
+        // 2048 equal parts of the keys khi .. klo
+        const int shift = max(0, 32 - __clz(khi - klo) - 11);
+        clear_bins(sm);
+        for_each<DT>(row, V, [&](float z, int) {
+            const uint32_t key = key_of(z);
+            if (key < klo || key > khi) return;
+            add_to_bin(sm, static_cast<int>((khi - key) >> shift), mass, mass ? fixed_weight(w, z) : 0);
+        });
+        __syncthreads();
+        find_bin(sm, goal, above_count, above_mass);
+        const uint32_t j = static_cast<uint32_t>(sm.bin);
+        const uint32_t top = khi - (j << shift);
+        const uint32_t width = (1u << shift) - 1;
+        klo = top - klo > width ? top - width : klo;
+        khi = top;
+        above_count = sm.above_count;
+        above_mass = sm.above_mass;
+        n = sm.bin_count;
+        __syncthreads();
+        if (n <= kList) {
+            if (threadIdx.x == 0) sm.n_list = 0;
+            __syncthreads();
+            for_each<DT>(row, V, [&](float z, int i) {
+                const uint32_t key = key_of(z);
+                if (key >= klo && key <= khi) sm.list[atomicAdd(&sm.n_list, 1u)] = place_of(key, i);
+            });
+            __syncthreads();
+            listed = true;
+        }
+    }
+    if (listed) {
+        for (int i = n + threadIdx.x; i < kList; i += kThreads) sm.list[i] = 0;
+        int size = 2;
+        while (size < static_cast<int>(n)) size <<= 1;
+        __syncthreads();
+        for (int k = 2; k <= size; k <<= 1) {  // bitonic, largest first
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+                    const int a = 2 * t - (t & (j - 1)), b = a + j;
+                    const uint64_t x = sm.list[a], y = sm.list[b];
+                    if ((x < y) == ((a & k) == 0)) {
+                        sm.list[a] = y;
+                        sm.list[b] = x;
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        constexpr int kPer = kList / kThreads;
+        uint32_t c = 0, ci[kPer];
+        uint64_t m = 0, mi[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int t = threadIdx.x * kPer + i;
+            ci[i] = t < static_cast<int>(n) ? 1 : 0;
+            mi[i] = ci[i] && mass ? fixed_weight(w, value_of(static_cast<uint32_t>(sm.list[t] >> 32))) : 0;
+            c += ci[i];
+            m += mi[i];
+        }
+        block_scan(sm, c, m);
+        c += above_count;
+        m += above_mass;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (ci[i] && goal.reached(c + 1, m + mi[i]) && !goal.reached(c, m)) {
+                sm.cut = sm.list[threadIdx.x * kPer + i];
+                sm.mass = m + mi[i];
+            }
+            c += ci[i];
+            m += mi[i];
+        }
+        __syncthreads();
+        return;
+    }
+    // one value: how many of its ties the goal takes, and the last one's index
+    const uint64_t wt = mass ? fixed_weight(w, value_of(khi)) : 0;
+    uint32_t take = n;
+    if (!goal.by_mass) {
+        take = goal.need - above_count;
+    } else {
+        uint32_t lo = 1, hi = n;  // the fewest whose mass reaches the target
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            if (goal.reached(0, above_mass + mid * wt)) hi = mid;
+            else lo = mid + 1;
+        }
+        take = lo;
+    }
+    uint32_t last = 0xffffffffu;
+    if (take < n) {
+        // a thread owns a run of vectors: count its ties, then find the one
+        constexpr int kPer = Elem<DT>::kPerVec;
+        const int vecs = V / kPer, per = (vecs + kThreads - 1) / kThreads;
+        const int v0 = min(vecs, static_cast<int>(threadIdx.x) * per), v1 = min(vecs, v0 + per);
+        const uint4 *p = reinterpret_cast<const uint4 *>(row);
+        uint32_t c = 0;
+        uint64_t none = 0;
+        for (int v = v0; v < v1; ++v) {
+            float x[kPer];
+            Elem<DT>::unpack(p[v], x);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) c += key_of(x[i]) == khi;
+        }
+        const uint32_t own = c;
+        block_scan(sm, c, none);
+        if (c < take && c + own >= take) {
+            for (int v = v0; v < v1; ++v) {
+                float x[kPer];
+                Elem<DT>::unpack(p[v], x);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (key_of(x[i]) == khi && ++c == take) sm.red[0] = v * kPer + i;
+            }
+        }
+        __syncthreads();
+        last = sm.red[0];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sm.cut = place_of(khi, static_cast<int>(last));
+        sm.mass = above_mass + take * wt;
+    }
+    __syncthreads();
+}
+
+// The lowest key whose value passes min-p, by the definition's test in fp64:
+// the border's own value is at most a few keys off (one thread's work).
+__device__ __noinline__ uint32_t min_p_key(float zmax, float T, float min_p) {
+    const double border = log(static_cast<double>(min_p));
+    const uint32_t last = key_of(__int_as_float(0xff800000)), first = key_of(zmax);
+    auto passes = [&](uint32_t key) {
+        return (static_cast<double>(value_of(key)) - static_cast<double>(zmax)) / static_cast<double>(T) >= border;
+    };
+    uint32_t key = key_of(static_cast<float>(static_cast<double>(zmax) + static_cast<double>(T) * border));
+    key = min(max(key, last), first);
+    while (key < first && !passes(key)) ++key;
+    while (key > last && passes(key - 1)) --key;
+    return key;
+}
+
+// One row's settings.
+struct Settings {
+    float T;
+    int k;
+    float p, m;
+    bool valid, active;
+};
+
+__device__ __forceinline__ Settings load_settings(const Truncate &tr, int b, int V) {
+    Settings s;
+    s.T = __ldg(tr.temperature + b);
+    s.k = tr.top_k ? __ldg(tr.top_k + b) : 0;
+    s.p = tr.top_p ? __ldg(tr.top_p + b) : 1.0f;
+    s.m = tr.min_p ? __ldg(tr.min_p + b) : 0.0f;
+    const float c = specv::temp_scale(s.T);
+    s.valid = c == c && s.k >= 0 && s.p > 0.0f && s.p <= 1.0f && s.m >= 0.0f && s.m <= 1.0f;
+    if (s.k >= V) s.k = 0;
+    s.active = s.T != 0.0f && (s.k > 0 || s.p < 1.0f || s.m > 0.0f);
+    return s;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 2)
+    truncate_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
+    extern __shared__ char smem[];
+    Shared &sm = *reinterpret_cast<Shared *>(smem);
+    const int tid = threadIdx.x;
+    constexpr int kPer = Elem<DT>::kPerVec;
+    const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
+    const int vecs = V / kPer;
+    if (tid < 64) {
+        const double t = exp2(tid / 64.0);
+        const float h = static_cast<float>(t);
+        sm.table[tid] = make_float2(h, static_cast<float>(t - h));
+    }
+    const int oB = __ldg(rw.offsets + rw.B);
+    const int64_t rows_all = rw.first_row(rw.B, oB);
+    int64_t r = rows_all * blockIdx.x / gridDim.x;
+    const int64_t end = rows_all * (blockIdx.x + 1) / gridDim.x;
+    int64_t total;
+    if (!check_rows(rw, false, r, 1, &sm.seq, &total)) {
+        constexpr uint32_t kNan = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
+        const int64_t all = static_cast<int64_t>(rw.R) * vecs;
+        for (int64_t v = static_cast<int64_t>(blockIdx.x) * kThreads + tid; v < all;
+             v += static_cast<int64_t>(gridDim.x) * kThreads)
+            reinterpret_cast<uint4 *>(out)[v] = make_uint4(kNan, kNan, kNan, kNan);
+        return;
+    }
+    if (r >= end) return;
+    int b = sm.seq;
+    for (; r < end; ++r) {
+        while (r >= rw.first_row(b + 1)) ++b;
+        const char *row = logits + r * row_bytes;
+        uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
+        const Settings s = load_settings(tr, b, V);
+        // --- the largest value; NaN, +inf and rows of -inf alone are left as they are
+        uint32_t top = 0;
+        bool nan = false;
+        if (s.valid && s.active) {
+            for_each<DT>(row, V, [&](float z, int) {
+                nan |= z != z;
+                top = max(top, key_of(z));
+            });
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        __syncthreads();
+        if ((tid & 31) == 0) sm.red[tid >> 5] = top;
+        nan = __syncthreads_or(nan);
+        for (int i = 0; i < kWarps; ++i) top = max(top, sm.red[i]);
+        const float zmax = value_of(top);
+        uint64_t cut = 0;
+        if (s.valid && s.active && !nan && isfinite(zmax)) {
+            Weights w;
+            if (tid == 0) {
+                const double c = specv::kLog2eD / static_cast<double>(s.T);
+                sm.ch = static_cast<float>(c);
+                sm.cl = static_cast<float>(c - static_cast<double>(sm.ch));
+                if (s.m > 0.0f) sm.min_p_key = min_p_key(zmax, s.T, s.m);
+            }
+            __syncthreads();
+            w.zmax = zmax;
+            w.ch = sm.ch;
+            w.cl = sm.cl;
+            w.frac = min(47, 30 + __clz(V));  // V weights of at most 1 sum to less than 2^63
+            w.table = sm.table;
+            const float scale = w.ch * kBinsPerOctave;
+            const bool mass = s.p < 1.0f;
+            if (s.k > 0 || mass) {
+                clear_bins(sm);
+                for_each<DT>(row, V, [&](float z, int) {
+                    add_to_bin(sm, first_bin(z, zmax, scale), mass, mass ? fixed_weight(w, z) : 0);
+                });
+                __syncthreads();
+                Goal goal{false, static_cast<uint32_t>(s.k), 0};
+                uint64_t Z = 0;
+                if (s.k > 0) {
+                    find_bin(sm, goal, 0, 0);
+                    // find_place splits bins in the same arrays
+                    find_place<DT>(sm, row, V, w, scale, goal, mass);
+                    cut = sm.cut;
+                    Z = sm.mass;
+                    if (mass) {
+                        __syncthreads();
+                        clear_bins(sm);
+                        for_each<DT>(row, V, [&](float z, int) {
+                            add_to_bin(sm, first_bin(z, zmax, scale), true, fixed_weight(w, z));
+                        });
+                        __syncthreads();
+                    }
+                }
+                if (mass) {
+                    goal.by_mass = true;
+                    if (s.k == 0) {
+                        find_bin(sm, goal, 0, 0);
+                        Z = sm.total_mass;
+                        __syncthreads();
+                    }
+                    if (tid == 0) sm.target = __double2ull_ru(static_cast<double>(s.p) * static_cast<double>(Z));
+                    __syncthreads();
+                    goal.target = sm.target;
+                    find_bin(sm, goal, 0, 0);
+                    find_place<DT>(sm, row, V, w, scale, goal, true);
+                    cut = max(cut, sm.cut);
+                }
+            }
+            if (s.m > 0.0f) cut = max(cut, place_of(sm.min_p_key, -1));
+        }
+        // --- the row out
+        if (cut == 0 && s.valid && logits == out) continue;
+        const uint32_t ckey = static_cast<uint32_t>(cut >> 32), cidx = ~static_cast<uint32_t>(cut);
+        for (int v = tid; v < vecs; v += kThreads) {
+            uint4 q = reinterpret_cast<const uint4 *>(row)[v];
+            float x[kPer];
+            Elem<DT>::unpack(q, x);
+            uint32_t *word = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const uint32_t key = key_of(x[i]);
+                const bool keep = cut == 0 || key > ckey || (key == ckey && static_cast<uint32_t>(v * kPer + i) <= cidx);
+                if (DT == SPEC_F32) {
+                    if (!keep) word[DT == SPEC_F32 ? i : 0] = 0xff800000u;
+                    if (!s.valid) word[DT == SPEC_F32 ? i : 0] = 0x7fc00000u;
+                } else {
+                    const uint32_t bits = s.valid ? 0xff80u : 0x7fc0u;
+                    if (!keep || !s.valid)
+                        word[i / 2] = i & 1 ? (word[i / 2] & 0xffffu) | bits << 16 : (word[i / 2] & 0xffff0000u) | bits;
+                }
+            }
+            dst[v] = q;
+        }
+    }
+}
+
+template <int DT>
+int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms,
+                    cudaStream_t stream) {
+    const int grid = std::min(rw.R, sms * 2);
+    truncate_kernel<DT><<<grid, kThreads, sizeof(Shared), stream>>>(static_cast<const char *>(logits),
+                                                                    static_cast<char *>(out), rw, tr, V);
+    return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+inline int check_truncate_args(const spec_truncate_t *t, const Rows &rw, Truncate *tr) {
+    if (!t) return SPEC_ERR_INVALID_ARG;
+    *tr = Truncate{t->temperature, t->top_k, t->top_p, t->min_p};
+    return rw.B > 0 && rw.R > 0 && !t->temperature ? SPEC_ERR_INVALID_ARG : SPEC_OK;
+}
+
+}  // namespace
+}  // namespace speclog
+
+using namespace speclog;
+
+extern "C" {
+
+int spec_logits_truncate(const void *logits, const spec_rows_t *rows, const spec_truncate_t *truncate, int V,
+                         int dtype, void *out, void *stream) {
+    Rows rw;
+    Truncate tr;
+    int rc = check_rows_args(logits, rows, V, dtype, out, &rw);
+    if (rc == SPEC_OK) rc = check_truncate_args(truncate, rw, &tr);
+    if (rc != SPEC_OK || rw.B == 0 || rw.R == 0) return rc;
+    int dev;
+    specv::DeviceState *st = specv::device_state(&dev);
+    if (!st) return SPEC_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_F32 ? launch_truncate<SPEC_F32>(logits, out, rw, tr, V, st->sms, s)
+                             : launch_truncate<SPEC_BF16>(logits, out, rw, tr, V, st->sms, s);
+}
+
+int spec_logits_process_truncate(const void *logits, const spec_rows_t *rows, const spec_logits_t *process,
+                                 const spec_truncate_t *truncate, int V, int dtype, void *out, void *stream) {
+    Rows rw;
+    Truncate tr;
+    int rc = check_rows_args(logits, rows, V, dtype, out, &rw);
+    if (rc == SPEC_OK) rc = check_truncate_args(truncate, rw, &tr);
+    if (rc == SPEC_OK) rc = spec_logits_process(logits, rows, process, V, dtype, out, stream);
+    if (rc != SPEC_OK) return rc;
+    return spec_logits_truncate(out, rows, truncate, V, dtype, out, stream);
+}
+
+}  // extern "C"
