@@ -642,91 +642,102 @@ class AdaptiveK:
 
 
 # ------------------------------------------------------------- logit operators
-def _check_all(dev, named, size=None):
-    """Each (name, tensor, dtype[, entries]) on the logits' device, contiguous and of its type; None is left out."""
-    for name, t, dtype, *n in named:
-        if t is None:
-            continue
+# A decoding step's calls are microseconds on the device, so their checks are
+# written to cost little: one test per tensor, its reasons found when it fails.
+def _ptr(t, name, dtype, dev, n=-1):
+    """data_ptr of a contiguous tensor of its type on the call's device, with n entries if n >= 0; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous() or (n >= 0 and t.numel() != n):
         _check_dev(name, t, dtype)
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
-        if n and t.numel() != n[0]:
-            raise ValueError(f"{name} must have {n[0]} entries, got {t.numel()}")
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    return t.data_ptr()
 
 
-def _rows_arg(logits, offsets, rows, draft_tokens, parent):
+def _launch(dev, stream, fn, what, *args):
+    """Calls fn(*args, stream) with `dev` current, on its current stream if none is given."""
     import torch
-    if rows not in ROWS:
+    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != 0:
+        _raise(rc, what)
+
+
+def _rows_arg(logits, offsets, rows, draft_tokens, parent, i32):
+    mode = ROWS.get(rows)
+    if mode is None:
         raise ValueError(f"rows must be one of {sorted(ROWS)}, got {rows!r}")
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, V]")
+    dev = logits.device
+    if dev.type != "cuda" or not logits.is_contiguous():
+        _check_dev("logits", logits)
     R, B = logits.shape[0], offsets.numel() - 1
     if B < 0:
         raise ValueError("offsets must have B + 1 entries")
-    _check_dev("logits", logits)
-    _check_all(logits.device, [("offsets", offsets, torch.int32), ("draft_tokens", draft_tokens, torch.int32),
-                               ("parent", parent, torch.int32)])
-    if rows == "tree" and parent is not None and parent.numel() > R:
-        raise ValueError("parent has more nodes than logits has rows")
     n_tokens = 0 if draft_tokens is None else draft_tokens.numel()
-    if rows == "tree" and parent is not None:
+    if mode == 3 and parent is not None:
+        if parent.numel() > R:
+            raise ValueError("parent has more nodes than logits has rows")
         n_tokens = min(n_tokens, parent.numel())
-    return _Rows(ROWS[rows], B, R, _p(offsets), _p(parent), _p(draft_tokens), n_tokens), B, R
+    return _Rows(mode, B, R, _ptr(offsets, "offsets", i32, dev), _ptr(parent, "parent", i32, dev),
+                 _ptr(draft_tokens, "draft_tokens", i32, dev), n_tokens)
 
 
-def _out_arg(logits, out):
-    import torch
+def _out_arg(logits, out, torch):
     if out is None:
-        return torch.empty_like(logits)
-    _check_all(logits.device, [("out", out, logits.dtype, logits.numel())])
-    return out
+        out = torch.empty_like(logits)
+        return out, out.data_ptr()
+    return out, _ptr(out, "out", logits.dtype, logits.device, logits.numel())
 
 
-def _logits_arg(logits, B, R, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
-                bias_offsets, bias_tokens, bias_values, mask, mask_rows):
-    import torch
-    i32, f32, V = torch.int32, torch.float32, logits.shape[1]
-    W, S, M, n_bias = (V + 31) // 32, 0, 0, 0
+def _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
+                bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32):
+    dev, V, B, R = logits.device, logits.shape[1], rw.B, rw.R
+    W, ps = (V + 31) // 32, _Logits()
     if counts is not None:
         if seen is None or draft_tokens is None:
             raise ValueError("penalties need counts, seen and draft_tokens")
         if rows == "tree" and parent is None:
             raise ValueError("penalties on a tree need parent")
-        S = counts.shape[0]
-    elif any(t is not None for t in (repetition, frequency, presence, seen, slots)):
+        ps.S = S = counts.shape[0]
+        ps.repetition = _ptr(repetition, "repetition", f32, dev, B)
+        ps.frequency = _ptr(frequency, "frequency", f32, dev, B)
+        ps.presence = _ptr(presence, "presence", f32, dev, B)
+        ps.counts = _ptr(counts, "counts", i32, dev, S * V)
+        ps.seen = _ptr(seen, "seen", i32, dev, S * 2 * W)
+        ps.slots = _ptr(slots, "slots", i32, dev, B)
+    elif not (repetition is None and frequency is None and presence is None and seen is None and slots is None):
         raise ValueError("penalties need counts, seen and draft_tokens")
     if bias_offsets is not None:
         if bias_tokens is None or bias_values is None:
             raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
-        n_bias = bias_tokens.numel()
-    elif bias_tokens is not None or bias_values is not None:
+        ps.n_bias = n = bias_tokens.numel()
+        ps.bias_offsets = _ptr(bias_offsets, "bias_offsets", i32, dev, B + 1)
+        ps.bias_tokens = _ptr(bias_tokens, "bias_tokens", i32, dev)
+        ps.bias_values = _ptr(bias_values, "bias_values", f32, dev, n)
+    elif not (bias_tokens is None and bias_values is None):
         raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
     if mask is not None:
-        M = mask.shape[0]
+        ps.M = M = mask.shape[0]
         if mask_rows is None and M < R:
             raise ValueError("mask needs a row for each row of logits, or mask_rows")
+        ps.mask = _ptr(mask, "mask", i32, dev, M * W)
+        ps.mask_rows = _ptr(mask_rows, "mask_rows", i32, dev, R)
     elif mask_rows is not None:
         raise ValueError("mask_rows without mask")
-    _check_all(logits.device, [
-        ("repetition", repetition, f32, B), ("frequency", frequency, f32, B), ("presence", presence, f32, B),
-        ("counts", counts, i32, S * V), ("seen", seen, i32, S * 2 * W), ("slots", slots, i32, B),
-        ("bias_offsets", bias_offsets, i32, B + 1), ("bias_tokens", bias_tokens, i32),
-        ("bias_values", bias_values, f32, n_bias), ("mask", mask, i32, M * W), ("mask_rows", mask_rows, i32, R)])
-    return _Logits(_p(repetition), _p(frequency), _p(presence), _p(counts), _p(seen), _p(slots), S, _p(bias_offsets),
-                   _p(bias_tokens), _p(bias_values), n_bias, _p(mask), _p(mask_rows), M)
+    return ps
 
 
-def _truncate_arg(logits, B, temperature, top_k, top_p, min_p):
-    import torch
-    f32 = torch.float32
-    _check_all(logits.device, [("temperature", temperature, f32, B), ("top_k", top_k, torch.int32, B),
-                               ("top_p", top_p, f32, B), ("min_p", min_p, f32, B)])
-    return _Truncate(_p(temperature), _p(top_k), _p(top_p), _p(min_p))
-
-
-def _on(t):
-    import torch
-    return torch.cuda.device(t.device)
+def _truncate_arg(dev, B, temperature, top_k, top_p, min_p, i32, f32):
+    return _Truncate(_ptr(temperature, "temperature", f32, dev, B), _ptr(top_k, "top_k", i32, dev, B),
+                     _ptr(top_p, "top_p", f32, dev, B), _ptr(min_p, "min_p", f32, dev, B))
 
 
 def spec_logits_process(logits, offsets, draft_tokens=None, *, rows="target", parent=None, repetition=None,
@@ -740,15 +751,15 @@ def spec_logits_process(logits, offsets, draft_tokens=None, *, rows="target", pa
     a bit per token (set: allowed) and mask_rows [R] the mask of each row (-1:
     none).  out: the result's buffer, logits itself for in place; else a new
     one, whose rows behind the last sequence's are not written.  Returns out."""
-    rw, B, R = _rows_arg(logits, offsets, rows, draft_tokens, parent)
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    rw = _rows_arg(logits, offsets, rows, draft_tokens, parent, i32)
     dt = _dtype_code(logits)
-    ps = _logits_arg(logits, B, R, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
-                     bias_offsets, bias_tokens, bias_values, mask, mask_rows)
-    out = _out_arg(logits, out)
-    with _on(logits):
-        rc = lib().spec_logits_process(_p(logits), ctypes.byref(rw), ctypes.byref(ps), logits.shape[1], dt, _p(out),
-                                       _stream(stream))
-    _raise(rc, "spec_logits_process")
+    ps = _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
+                     bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32)
+    out, po = _out_arg(logits, out, torch)
+    _launch(logits.device, stream, lib().spec_logits_process, "spec_logits_process", logits.data_ptr(),
+            ctypes.byref(rw), ctypes.byref(ps), logits.shape[1], dt, po)
     return out
 
 
@@ -758,14 +769,13 @@ def spec_logits_truncate(logits, temperature, offsets, *, rows="target", top_k=N
     setting per sequence): tokens outside the kept set become -inf, ties go
     to the lowest index.  rows, out: as in spec_logits_process.  Greedy
     sequences' rows (temperature 0) stay as they are.  Returns out."""
-    rw, B, R = _rows_arg(logits, offsets, rows, None, None)
+    import torch
+    rw = _rows_arg(logits, offsets, rows, None, None, torch.int32)
     dt = _dtype_code(logits)
-    tr = _truncate_arg(logits, B, temperature, top_k, top_p, min_p)
-    out = _out_arg(logits, out)
-    with _on(logits):
-        rc = lib().spec_logits_truncate(_p(logits), ctypes.byref(rw), ctypes.byref(tr), logits.shape[1], dt, _p(out),
-                                        _stream(stream))
-    _raise(rc, "spec_logits_truncate")
+    tr = _truncate_arg(logits.device, rw.B, temperature, top_k, top_p, min_p, torch.int32, torch.float32)
+    out, po = _out_arg(logits, out, torch)
+    _launch(logits.device, stream, lib().spec_logits_truncate, "spec_logits_truncate", logits.data_ptr(),
+            ctypes.byref(rw), ctypes.byref(tr), logits.shape[1], dt, po)
     return out
 
 
@@ -775,27 +785,27 @@ def spec_logits_process_truncate(logits, temperature, offsets, draft_tokens=None
                                  top_k=None, top_p=None, min_p=None, out=None, stream=None):
     """spec_logits_process, then spec_logits_truncate on its result, in one
     call (the same outputs, bit for bit).  Returns out."""
-    rw, B, R = _rows_arg(logits, offsets, rows, draft_tokens, parent)
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    rw = _rows_arg(logits, offsets, rows, draft_tokens, parent, i32)
     dt = _dtype_code(logits)
-    ps = _logits_arg(logits, B, R, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
-                     bias_offsets, bias_tokens, bias_values, mask, mask_rows)
-    tr = _truncate_arg(logits, B, temperature, top_k, top_p, min_p)
-    out = _out_arg(logits, out)
-    with _on(logits):
-        rc = lib().spec_logits_process_truncate(_p(logits), ctypes.byref(rw), ctypes.byref(ps), ctypes.byref(tr),
-                                                logits.shape[1], dt, _p(out), _stream(stream))
-    _raise(rc, "spec_logits_process_truncate")
+    ps = _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
+                     bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32)
+    tr = _truncate_arg(logits.device, rw.B, temperature, top_k, top_p, min_p, i32, f32)
+    out, po = _out_arg(logits, out, torch)
+    _launch(logits.device, stream, lib().spec_logits_process_truncate, "spec_logits_process_truncate",
+            logits.data_ptr(), ctypes.byref(rw), ctypes.byref(ps), ctypes.byref(tr), logits.shape[1], dt, po)
     return out
 
 
-def _state_arg(counts, seen):
-    import torch
+def _state_arg(counts, seen, i32):
     if counts.dim() != 2:
         raise ValueError("counts must be [S, V]")
     S, V = counts.shape
-    _check_dev("counts", counts, torch.int32)
-    _check_all(counts.device, [("seen", seen, torch.int32, S * 2 * ((V + 31) // 32))])
-    return S, V
+    dev = counts.device
+    if dev.type != "cuda":
+        _check_dev("counts", counts)
+    return S, V, dev, _ptr(counts, "counts", i32, dev), _ptr(seen, "seen", i32, dev, S * 2 * ((V + 31) // 32))
 
 
 def spec_penalty_reset(counts, seen, slots, prompt_offsets=None, prompt_tokens=None, output_offsets=None,
@@ -804,20 +814,16 @@ def spec_penalty_reset(counts, seen, slots, prompt_offsets=None, prompt_tokens=N
     cleared, their prompts' tokens (a ragged list) marked, and tokens they
     have emitted already counted.  Returns (counts, seen)."""
     import torch
-    S, V = _state_arg(counts, seen)
+    i32 = torch.int32
+    S, V, dev, pc, ps = _state_arg(counts, seen, i32)
     n = slots.numel()
     if (prompt_offsets is None) != (prompt_tokens is None) or (output_offsets is None) != (output_tokens is None):
         raise ValueError("offsets and tokens go together")
-    _check_all(counts.device, [
-        ("slots", slots, torch.int32), ("prompt_offsets", prompt_offsets, torch.int32, n + 1),
-        ("prompt_tokens", prompt_tokens, torch.int32), ("output_offsets", output_offsets, torch.int32, n + 1),
-        ("output_tokens", output_tokens, torch.int32)])
-    with _on(counts):
-        rc = lib().spec_penalty_reset(_p(counts), _p(seen), S, V, _p(slots), n, _p(prompt_offsets), _p(prompt_tokens),
-                                      0 if prompt_tokens is None else prompt_tokens.numel(), _p(output_offsets),
-                                      _p(output_tokens), 0 if output_tokens is None else output_tokens.numel(),
-                                      _stream(stream))
-    _raise(rc, "spec_penalty_reset")
+    _launch(dev, stream, lib().spec_penalty_reset, "spec_penalty_reset", pc, ps, S, V, _ptr(slots, "slots", i32, dev), n,
+            _ptr(prompt_offsets, "prompt_offsets", i32, dev, n + 1), _ptr(prompt_tokens, "prompt_tokens", i32, dev),
+            0 if prompt_tokens is None else prompt_tokens.numel(),
+            _ptr(output_offsets, "output_offsets", i32, dev, n + 1), _ptr(output_tokens, "output_tokens", i32, dev),
+            0 if output_tokens is None else output_tokens.numel())
     return counts, seen
 
 
@@ -827,19 +833,17 @@ def spec_penalty_update(counts, seen, out_tokens, out_num_accepted, offsets, *, 
     out_num_accepted, with its k_offsets, or node_offsets for rows="tree") in
     the sequences' slots.  Returns (counts, seen)."""
     import torch
-    S, V = _state_arg(counts, seen)
+    i32 = torch.int32
+    S, V, dev, pc, ps = _state_arg(counts, seen, i32)
     if rows not in ("target", "tree"):
         raise ValueError(f"rows must be 'target' or 'tree', got {rows!r}")
     B = offsets.numel() - 1
     if B < 0:
         raise ValueError("offsets must have B + 1 entries")
-    _check_all(counts.device, [("offsets", offsets, torch.int32), ("out_tokens", out_tokens, torch.int32),
-                               ("out_num_accepted", out_num_accepted, torch.int32, B), ("slots", slots, torch.int32, B)])
-    rw = _Rows(ROWS[rows], B, out_tokens.numel(), _p(offsets), None, None, 0)
-    with _on(counts):
-        rc = lib().spec_penalty_update(_p(counts), _p(seen), S, V, _p(slots), ctypes.byref(rw), _p(out_tokens),
-                                       _p(out_num_accepted), _stream(stream))
-    _raise(rc, "spec_penalty_update")
+    rw = _Rows(ROWS[rows], B, out_tokens.numel(), _ptr(offsets, "offsets", i32, dev), None, None, 0)
+    _launch(dev, stream, lib().spec_penalty_update, "spec_penalty_update", pc, ps, S, V,
+            _ptr(slots, "slots", i32, dev, B), ctypes.byref(rw), _ptr(out_tokens, "out_tokens", i32, dev),
+            _ptr(out_num_accepted, "out_num_accepted", i32, dev, B))
     return counts, seen
 
 

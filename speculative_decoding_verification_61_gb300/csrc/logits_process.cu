@@ -29,29 +29,65 @@ template <int DT>
 constexpr int kUnroll = DT == SPEC_BF16 ? 4 : 2;  // rows in flight per thread
 
 template <int DT>
-struct Vec {  // a thread's 8 columns of one row
-    static constexpr int kN = DT == SPEC_BF16 ? 1 : 2;
-    uint4 q[kN];
+struct Vec {  // a thread's 8 columns of one row, as 32-bit words
+    static constexpr int kWords = DT == SPEC_BF16 ? 4 : 8;
+    uint32_t w[kWords];
 };
 
 template <int DT>
 __device__ __forceinline__ void load_cols(Vec<DT> &v, const char *row, int col, int ncol) {
     const uint4 *p = reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(col) * Elem<DT>::kBytes);
-    v.q[0] = p[0];
-    if (DT == SPEC_F32 && ncol > 4) v.q[Vec<DT>::kN - 1] = p[1];
+    uint4 q = p[0];
+    v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
+    if constexpr (DT == SPEC_F32) {
+        if (ncol > 4) q = p[1];
+        v.w[4] = q.x, v.w[5] = q.y, v.w[6] = q.z, v.w[7] = q.w;
+    }
 }
 
 template <int DT>
 __device__ __forceinline__ void store_cols(const Vec<DT> &v, char *row, int col, int ncol) {
     uint4 *p = reinterpret_cast<uint4 *>(row + static_cast<int64_t>(col) * Elem<DT>::kBytes);
-    p[0] = v.q[0];
-    if (DT == SPEC_F32 && ncol > 4) p[1] = v.q[Vec<DT>::kN - 1];
+    p[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    if constexpr (DT == SPEC_F32) {
+        if (ncol > 4) p[1] = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+    }
 }
 
 template <int DT>
 __device__ __forceinline__ void fill_cols(Vec<DT> &v, uint32_t word) {
 #pragma unroll
-    for (int i = 0; i < Vec<DT>::kN; ++i) v.q[i] = make_uint4(word, word, word, word);
+    for (int i = 0; i < Vec<DT>::kWords; ++i) v.w[i] = word;
+}
+
+// Column c of the 8, read and written without indexing registers.
+template <int DT>
+__device__ __forceinline__ float get_col(const Vec<DT> &v, int c) {
+    const int at = DT == SPEC_F32 ? c : c >> 1;
+    uint32_t x = v.w[0];
+#pragma unroll
+    for (int i = 1; i < Vec<DT>::kWords; ++i) x = i == at ? v.w[i] : x;
+    return __uint_as_float(DT == SPEC_F32 ? x : c & 1 ? x & 0xffff0000u : x << 16);
+}
+template <int DT>
+__device__ __forceinline__ void set_col(Vec<DT> &v, int c, float z) {
+    const int at = DT == SPEC_F32 ? c : c >> 1;
+    const uint32_t h = DT == SPEC_F32 ? __float_as_uint(z) : __bfloat16_as_ushort(__float2bfloat16_rn(z));
+    const uint32_t keep = DT == SPEC_F32 ? 0u : c & 1 ? 0xffffu : 0xffff0000u;
+    const uint32_t put = DT == SPEC_BF16 && (c & 1) ? h << 16 : h;
+#pragma unroll
+    for (int i = 0; i < Vec<DT>::kWords; ++i) v.w[i] = i == at ? (v.w[i] & keep) | put : v.w[i];
+}
+// -inf in the columns whose bit is clear
+template <int DT>
+__device__ __forceinline__ void mask_cols(Vec<DT> &v, uint32_t allowed) {
+#pragma unroll
+    for (int i = 0; i < Vec<DT>::kWords; ++i) {
+        uint32_t keep;
+        if (DT == SPEC_F32) keep = (allowed >> i) & 1 ? 0xffffffffu : 0u;
+        else keep = ((allowed >> (2 * i)) & 1 ? 0xffffu : 0u) | ((allowed >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+        v.w[i] = (v.w[i] & keep) | (Elem<DT>::kNegInfWord & ~keep);
+    }
 }
 
 template <int DT>
@@ -66,13 +102,15 @@ struct Shared {
     uint32_t biased[kChunk / 32];   // columns that a bias entry names
     int bias_token[kThreads];
     float bias_value[kThreads];
+    int count[kCols][kThreads];   // by column of the thread: a seen token's count
+    float bias[kCols][kThreads];  // and a biased token's bias
 };
 
 // A CTA takes an even share of the rows' chunks in the order (sequence,
 // chunk, row), so that what depends on the sequence and the columns alone
 // (its seen tokens, their counts, its biases) is read once for all its rows.
-// A thread keeps the same 8 columns over the rows: counts and biases stay in
-// registers.
+// A thread keeps the same 8 columns over the rows; its seen and biased columns
+// are few, so they are taken one at a time.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 8)
     process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int chunks) {
@@ -167,7 +205,6 @@ __global__ void __launch_bounds__(kThreads, 8)
             }
             sm.before[tid] = m;
         }
-        float bias[kCols];
         uint32_t bbits = 0;
         if (ps.bias_offsets) {
             const int e0 = __ldg(ps.bias_offsets + b), e1 = __ldg(ps.bias_offsets + b + 1);
@@ -185,26 +222,26 @@ __global__ void __launch_bounds__(kThreads, 8)
                     if (d >= 0 && d < kChunk) atomicOr(&sm.biased[d >> 5], 1u << (d & 31));
                 }
                 __syncthreads();
-                const uint32_t mine = reinterpret_cast<const unsigned char *>(sm.biased)[tid];
-                if (mine) {
+                if (reinterpret_cast<const unsigned char *>(sm.biased)[tid]) {
                     // the same token twice: the entries add, in list order
                     for (int j = 0; j < len; ++j) {
                         const int d = sm.bias_token[j] - tid * kCols;
                         if (d < 0 || d >= kCols) continue;
-#pragma unroll
-                        for (int c = 0; c < kCols; ++c)
-                            if (c == d)
-                                bias[c] = (bbits >> c) & 1 ? __fadd_rn(bias[c], sm.bias_value[j]) : sm.bias_value[j];
+                        sm.bias[d][tid] = (bbits >> d) & 1 ? __fadd_rn(sm.bias[d][tid], sm.bias_value[j]) : sm.bias_value[j];
                         bbits |= 1u << d;
                     }
                 }
                 __syncthreads();
             }
         }
-        int cnt[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-            cnt[c] = (obits >> c) & 1 && col + c < V ? __ldg(ps.counts + slot * V + col + c) : 0;
+        if (ncol < kCols) {  // bits behind the vocabulary say nothing
+            pbits &= 0x0fu;
+            obits &= 0x0fu;
+        }
+        for (uint32_t m = obits; m; m &= m - 1) {
+            const int c = __ffs(m) - 1;
+            sm.count[c][tid] = __ldg(ps.counts + slot * V + col + c);
+        }
         bad = __syncthreads_or(bad);
         const uint32_t dbits = pen ? reinterpret_cast<const unsigned char *>(sm.drafted)[tid] : 0;
         const uint32_t touched = pbits | obits | dbits | bbits;
@@ -238,29 +275,20 @@ __global__ void __launch_bounds__(kThreads, 8)
 #pragma unroll
             for (int u = 0; u < kUnroll<DT>; ++u) {
                 if (!write[u]) continue;
-                if ((touched || allowed[u] != 0xffu) && allowed[u] != 0x100u) {
-                    const uint64_t before = dbits ? sm.before[i + u] : 0;
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&v[u]);
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) {
-                        if (!((touched | ~allowed[u]) >> c & 1)) continue;
-                        float z = DT == SPEC_F32 ? __uint_as_float(w[DT == SPEC_F32 ? c : 0])
-                                                 : __uint_as_float(c & 1 ? w[c / 2] & 0xffff0000u : w[c / 2] << 16);
-                        int n_c = cnt[c];
+                if (allowed[u] != 0x100u) {
+                    for (uint32_t m = touched & allowed[u]; m; m &= m - 1) {
+                        const int c = __ffs(m) - 1;
+                        float z = get_col<DT>(v[u], c);
+                        int n_c = (obits >> c) & 1 ? sm.count[c][tid] : 0;
                         if ((dbits >> c) & 1) {
                             const int t = col + c;
-                            for (uint64_t m = before; m; m &= m - 1) n_c += sm.token[__ffsll(m) - 1] == t;
+                            for (uint64_t d = sm.before[i + u]; d; d &= d - 1) n_c += sm.token[__ffsll(d) - 1] == t;
                         }
                         if ((pbits >> c) & 1 || n_c > 0) z = penalised(z, n_c, p);
-                        if ((bbits >> c) & 1) z = __fadd_rn(z, bias[c]);
-                        if (!((allowed[u] >> c) & 1)) z = __int_as_float(0xff800000);
-                        if (DT == SPEC_F32) {
-                            w[DT == SPEC_F32 ? c : 0] = __float_as_uint(z);
-                        } else {
-                            const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-                            w[c / 2] = c & 1 ? (w[c / 2] & 0xffffu) | h << 16 : (w[c / 2] & 0xffff0000u) | h;
-                        }
+                        if ((bbits >> c) & 1) z = __fadd_rn(z, sm.bias[c][tid]);
+                        set_col<DT>(v[u], c, z);
                     }
+                    if (allowed[u] != 0xffu) mask_cols<DT>(v[u], allowed[u]);
                 }
                 store_cols<DT>(v[u], out + (row0 + i + u) * row_bytes, col, ncol);
             }

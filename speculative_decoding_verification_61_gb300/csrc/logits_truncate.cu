@@ -129,6 +129,13 @@ __device__ __forceinline__ uint64_t fixed_weight(const Weights &w, float z) {
 }
 
 // ------------------------------------------------------------ block helpers
+// What one thread finds for the row (fp64 runs at a small fraction of fp32's
+// rate, so no thread does it twice).
+struct RowConstants {
+    float ch, cl;  // log2(e) / T
+    uint32_t min_p_key;
+};
+
 struct Shared {
     int seq;
     float2 table[64];
@@ -143,10 +150,8 @@ struct Shared {
     uint32_t above_count, bin_count;
     uint64_t above_mass, total_mass, mass;
     uint64_t cut;
-    // the row's constants, found by one thread (fp64 runs at a small fraction of fp32's rate)
-    float ch, cl;
-    uint32_t min_p_key;
     uint64_t target;
+    RowConstants row;
 };
 
 // Exclusive prefix sums over the block of a count and a mass per thread.
@@ -460,31 +465,140 @@ __device__ __forceinline__ Settings load_settings(const Truncate &tr, int b, int
     return s;
 }
 
+__device__ __forceinline__ void set_row_constants(RowConstants &rc, const Settings &s, float zmax) {
+    const double c = specv::kLog2eD / static_cast<double>(s.T);
+    rc.ch = static_cast<float>(c);
+    rc.cl = static_cast<float>(c - static_cast<double>(rc.ch));
+    if (s.m > 0.0f) rc.min_p_key = min_p_key(zmax, s.T, s.m);
+}
+__device__ __forceinline__ Weights row_weights(const RowConstants &rc, float zmax, int V, const float2 *table) {
+    // V weights of at most 1 sum to less than 2^63
+    return Weights{zmax, rc.ch, rc.cl, min(47, 30 + __clz(V)), table};
+}
+// The least mass that is not below p Z.
+__device__ __forceinline__ uint64_t mass_target(float p, uint64_t Z) {
+    return __double2ull_ru(static_cast<double>(p) * static_cast<double>(Z));
+}
+__device__ __forceinline__ void fill_table(float2 *table) {
+    if (threadIdx.x < 64) {
+        const double t = exp2(threadIdx.x / 64.0);
+        const float h = static_cast<float>(t);
+        table[threadIdx.x] = make_float2(h, static_cast<float>(t - h));
+    }
+}
+
+// The cut of one row in memory, for rows of any kind: every token whose place is
+// below it goes; 0: the row stays as it is.  Passes over the row: its largest
+// value, a histogram over 32 bins per halving of the weight, the border bin's
+// elements, sorted.
+template <int DT>
+__device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, const Settings &s) {
+    const int tid = threadIdx.x;
+    uint32_t top = 0;
+    bool nan = false;
+    for_each<DT>(row, V, [&](float z, int) {
+        nan |= z != z;
+        top = max(top, key_of(z));
+    });
+    top = __reduce_max_sync(0xffffffffu, top);
+    __syncthreads();
+    if ((tid & 31) == 0) sm.red[tid >> 5] = top;
+    nan = __syncthreads_or(nan);
+    for (int i = 0; i < kWarps; ++i) top = max(top, sm.red[i]);
+    const float zmax = value_of(top);
+    if (nan || !isfinite(zmax)) return 0;  // NaN, +inf, or nothing but -inf
+    if (tid == 0) set_row_constants(sm.row, s, zmax);
+    __syncthreads();
+    const Weights w = row_weights(sm.row, zmax, V, sm.table);
+    const float scale = w.ch * kBinsPerOctave;
+    const bool mass = s.p < 1.0f;
+    uint64_t cut = 0;
+    if (s.k > 0 || mass) {
+        Goal goal{false, static_cast<uint32_t>(s.k), 0};
+        uint64_t Z = 0;
+        auto fill = [&]() {
+            clear_bins(sm);
+            for_each<DT>(row, V, [&](float z, int) {
+                add_to_bin(sm, first_bin(z, zmax, scale), mass, mass ? fixed_weight(w, z) : 0);
+            });
+            __syncthreads();
+        };
+        fill();
+        if (s.k > 0) {
+            find_bin(sm, goal, 0, 0);
+            const bool splits = sm.bin_count > kList;  // find_place then uses the bins itself
+            find_place<DT>(sm, row, V, w, scale, goal, mass);
+            cut = sm.cut;
+            Z = sm.mass;
+            __syncthreads();
+            if (mass && splits) fill();
+        }
+        if (mass) {
+            goal.by_mass = true;
+            if (s.k == 0) {
+                find_bin(sm, goal, 0, 0);
+                Z = sm.total_mass;
+                __syncthreads();
+            }
+            if (tid == 0) sm.target = mass_target(s.p, Z);
+            __syncthreads();
+            goal.target = sm.target;
+            find_bin(sm, goal, 0, 0);
+            find_place<DT>(sm, row, V, w, scale, goal, true);
+            cut = max(cut, sm.cut);
+        }
+    }
+    if (s.m > 0.0f) cut = max(cut, place_of(sm.row.min_p_key, -1));
+    __syncthreads();
+    return cut;
+}
+
+// The row with -inf below the cut.
+template <int DT>
+__device__ __forceinline__ void write_cut(const char *row, uint4 *dst, int V, uint64_t cut) {
+    constexpr int kPer = Elem<DT>::kPerVec;
+    const uint32_t ckey = static_cast<uint32_t>(cut >> 32), cidx = ~static_cast<uint32_t>(cut);
+    for (int v = threadIdx.x; v < V / kPer; v += kThreads) {
+        uint4 q = reinterpret_cast<const uint4 *>(row)[v];
+        float x[kPer];
+        Elem<DT>::unpack(q, x);
+        uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t key = key_of(x[i]);
+            const bool keep = cut == 0 || key > ckey || (key == ckey && static_cast<uint32_t>(v * kPer + i) <= cidx);
+            if (keep) continue;
+            if (DT == SPEC_F32) w[i % 4] = 0xff800000u;
+            else w[i / 2 % 4] = i & 1 ? (w[i / 2 % 4] & 0xffffu) | 0xff800000u : (w[i / 2 % 4] & 0xffff0000u) | 0xff80u;
+        }
+        dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void fill_nan(uint4 *dst, int64_t vecs, int64_t first, int64_t step) {
+    constexpr uint32_t kNan = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
+    for (int64_t v = first; v < vecs; v += step) dst[v] = make_uint4(kNan, kNan, kNan, kNan);
+}
+
+// A CTA takes an even share of the rows; rows of any kind.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 2)
     truncate_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
     extern __shared__ char smem[];
     Shared &sm = *reinterpret_cast<Shared *>(smem);
     const int tid = threadIdx.x;
-    constexpr int kPer = Elem<DT>::kPerVec;
     const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
-    const int vecs = V / kPer;
-    if (tid < 64) {
-        const double t = exp2(tid / 64.0);
-        const float h = static_cast<float>(t);
-        sm.table[tid] = make_float2(h, static_cast<float>(t - h));
-    }
+    const int vecs = V / Elem<DT>::kPerVec;
+    fill_table(sm.table);
     const int oB = __ldg(rw.offsets + rw.B);
     const int64_t rows_all = rw.first_row(rw.B, oB);
     int64_t r = rows_all * blockIdx.x / gridDim.x;
     const int64_t end = rows_all * (blockIdx.x + 1) / gridDim.x;
     int64_t total;
     if (!check_rows(rw, false, r, 1, &sm.seq, &total)) {
-        constexpr uint32_t kNan = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
-        const int64_t all = static_cast<int64_t>(rw.R) * vecs;
-        for (int64_t v = static_cast<int64_t>(blockIdx.x) * kThreads + tid; v < all;
-             v += static_cast<int64_t>(gridDim.x) * kThreads)
-            reinterpret_cast<uint4 *>(out)[v] = make_uint4(kNan, kNan, kNan, kNan);
+        fill_nan<DT>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
+                     static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
     }
     if (r >= end) return;
@@ -494,101 +608,443 @@ __global__ void __launch_bounds__(kThreads, 2)
         const char *row = logits + r * row_bytes;
         uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
         const Settings s = load_settings(tr, b, V);
-        // --- the largest value; NaN, +inf and rows of -inf alone are left as they are
-        uint32_t top = 0;
-        bool nan = false;
-        if (s.valid && s.active) {
-            for_each<DT>(row, V, [&](float z, int) {
-                nan |= z != z;
-                top = max(top, key_of(z));
-            });
+        if (!s.valid) {
+            fill_nan<DT>(dst, vecs, tid, kThreads);
+            continue;
         }
-        top = __reduce_max_sync(0xffffffffu, top);
+        const uint64_t cut = s.active ? cut_of_row<DT>(sm, row, V, s) : 0;
+        if (cut != 0 || logits != out) write_cut<DT>(row, dst, V, cut);
+    }
+}
+
+// ------------------------------------------------------------ bf16, in two passes
+// bf16 rows have few values, so a histogram with one bin per value settles
+// everything: counts are exact, and a weight is computed once per value
+// instead of once per token.  Bins in falling order: z in (2^16, 2^-24], 0,
+// [-2^-24, -2^16): 39 + 1 octaves of 128 values a side, 40 KB.  Values at or
+// below -2^16 (masked logits) have no weight and are not counted; rows with
+// other values outside the bins, with NaN or +inf, or whose border is not in
+// the bins, take cut_of_row.
+constexpr int kTiny = (127 - 24) << 7;   // magnitude bits of 2^-24
+constexpr int kHuge = (127 + 16) << 7;   // of 2^16
+constexpr int kSide = kHuge - kTiny;     // values a side
+constexpr int kZeroBin = kSide;
+constexpr int kValues = 2 * kSide + 1;
+constexpr int kSegs = (kValues + 31) / 32;
+constexpr int kSegsPerLane = (kSegs + 31) / 32;
+constexpr int kGroupCols = 256;           // a warp's 32 vectors
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxFastV = kGroupCols * kMaxGroups;
+constexpr int kAhead = 4;                 // vectors in flight per thread
+
+struct FastShared {
+    uint32_t hist[kSegs * 32];
+    uint32_t seg_count[kSegs];
+    uint64_t seg_mass[kSegs];
+    uint16_t group_max[kMaxGroups];   // order key of each group's largest value
+    int first;                        // the largest value's bin
+    // the border: tokens above `value` stay, `take` of its ties do
+    int value_bin, take, ties;
+    int cut_group, cut_index;
+    bool elsewhere;  // not in the bins
+
+    // how often each group holds the border value: written once the bins are done with
+    __device__ uint16_t *group_ties() { return reinterpret_cast<uint16_t *>(hist); }
+};
+
+struct BothShared {
+    union {
+        Shared any;
+        FastShared fast;
+    };
+    // apart from the union: kept over the rows
+    float2 table[64];
+    RowConstants row;
+    int seq;
+};
+
+__device__ __forceinline__ float bin_value(int bin) {
+    const uint32_t u = bin < kZeroBin ? kHuge - 1 - bin : bin == kZeroBin ? 0 : 0x8000 | (bin - kZeroBin - 1 + kTiny);
+    return __uint_as_float(u << 16);
+}
+// Unsigned 16-bit key in the order of the values (-0 below +0).
+__device__ __forceinline__ uint32_t key16(uint32_t u) { return u ^ (u & 0x8000u ? 0xffffu : 0x8000u); }
+
+// t tokens' weight: the product before the one rounding.
+__device__ __forceinline__ uint64_t weight_times(const Weights &w, float z, uint32_t t) {
+    int e;
+    const uint64_t m = weight_mantissa(w, z, &e);
+    const int shift = -(e + w.frac);
+    if (m == 0 || t == 0 || shift > 100) return 0;
+    uint64_t lo = m * t, hi = __umul64hi(m, t);
+    if (shift >= 64) return hi >> (shift - 64);
+    lo += 1ull << (shift - 1);
+    hi += lo < (1ull << (shift - 1));
+    return lo >> shift | (shift == 0 ? 0 : hi << (64 - shift));
+}
+
+// One token's bits into the histogram; what has no bin sets *odd, except
+// values at or below -2^16.
+__device__ __forceinline__ void count_value(FastShared &sm, uint32_t u, uint32_t *odd) {
+    const uint32_t m = u & 0x7fffu;
+    if (m - kTiny < static_cast<uint32_t>(kSide)) {
+        atomicAdd(&sm.hist[u & 0x8000u ? m + (kZeroBin + 1 - kTiny) : kHuge - 1 - m], 1u);
+    } else if (m == 0) {
+        atomicAdd(&sm.hist[kZeroBin], 1u);
+    } else if (!(u >= (0x8000u | kHuge) && u <= 0xff80u)) {
+        *odd = 1;
+    }
+}
+
+// Where the goal is reached in the histogram, by one warp: the bin, and what
+// lies above it.  False if the bins end before.
+__device__ __forceinline__ bool locate(FastShared &sm, const Weights &w, const Goal &goal, bool mass, int *bin,
+                                       uint32_t *above_count, uint64_t *above_mass) {
+    const int lane = threadIdx.x & 31;
+    const int s0 = lane * kSegsPerLane, s1 = min(kSegs, s0 + kSegsPerLane);
+    uint32_t c = 0;
+    uint64_t m = 0;
+    for (int s = s0; s < s1; ++s) {
+        c += sm.seg_count[s];
+        if (mass) m += sm.seg_mass[s];
+    }
+    const uint32_t c0 = c;
+    const uint64_t m0 = m;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
+        const uint64_t mm = __shfl_up_sync(0xffffffffu, m, off);
+        if (lane >= off) {
+            c += cc;
+            m += mm;
+        }
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, goal.reached(c, m));
+    if (!hit) return false;
+    const int owner = __ffs(hit) - 1;
+    c -= c0;
+    m -= m0;
+    int seg = s0;
+    if (lane == owner) {
+        for (; seg < s1 - 1; ++seg) {
+            const uint32_t cs = sm.seg_count[seg];
+            const uint64_t ms = mass ? sm.seg_mass[seg] : 0;
+            if (goal.reached(c + cs, m + ms)) break;
+            c += cs;
+            m += ms;
+        }
+    }
+    seg = __shfl_sync(0xffffffffu, seg, owner);
+    c = __shfl_sync(0xffffffffu, c, owner);
+    m = __shfl_sync(0xffffffffu, m, owner);
+    const int my = seg * 32 + lane;
+    const uint32_t n = sm.hist[my];
+    const uint64_t mine = mass && n ? weight_times(w, bin_value(my), n) : 0;
+    uint32_t ci = n;
+    uint64_t mi = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t cc = __shfl_up_sync(0xffffffffu, ci, off);
+        const uint64_t mm = __shfl_up_sync(0xffffffffu, mi, off);
+        if (lane >= off) {
+            ci += cc;
+            mi += mm;
+        }
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, goal.reached(c + ci, m + mi))) - 1;
+    *bin = seg * 32 + at;
+    *above_count = __shfl_sync(0xffffffffu, c + ci - n, at);
+    *above_mass = __shfl_sync(0xffffffffu, m + mi - mine, at);
+    return true;
+}
+
+// The fewest ties whose weight reaches the target.
+__device__ __forceinline__ uint32_t ties_for(const Weights &w, float z, uint32_t n, uint64_t above, uint64_t target) {
+    uint32_t lo = 1, hi = n;
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (above + weight_times(w, z, mid) >= target) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// A group's 32 vectors of 8: groups are counted in column order, group g by warp g % kWarps.
+template <typename F>
+__device__ __forceinline__ void for_groups(int groups, F &&f) {
+    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) f(g, g * 32 + static_cast<int>(threadIdx.x & 31));
+}
+
+__device__ __forceinline__ uint32_t max_word(const uint4 &q) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&q);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+
+// 0xffff in the halves of a that are greater than (or equal to) b's
+__device__ __forceinline__ uint32_t above_mask(uint32_t a, uint32_t b, bool equal) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
+    return equal ? __hge2_mask(x, y) : __hgt2_mask(x, y);
+}
+__device__ __forceinline__ uint32_t equal_mask(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
+    return __heq2_mask(x, y);
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+    truncate_bf16_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
+    extern __shared__ char smem[];
+    BothShared &all = *reinterpret_cast<BothShared *>(smem);
+    FastShared &sm = all.fast;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row_bytes = static_cast<int64_t>(V) * 2;
+    const int vecs = V / 8, groups = (vecs + 31) / 32;
+    fill_table(all.table);
+    const int oB = __ldg(rw.offsets + rw.B);
+    const int64_t rows_all = rw.first_row(rw.B, oB);
+    int64_t r = rows_all * blockIdx.x / gridDim.x;
+    const int64_t end = rows_all * (blockIdx.x + 1) / gridDim.x;
+    int64_t total;
+    if (!check_rows(rw, false, r, 1, &all.seq, &total)) {
+        fill_nan<SPEC_BF16>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
+                            static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
+        return;
+    }
+    if (r >= end) return;
+    int b = all.seq;
+    for (; r < end; ++r) {
+        while (r >= rw.first_row(b + 1)) ++b;
+        const uint4 *row = reinterpret_cast<const uint4 *>(logits + r * row_bytes);
+        uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
+        const Settings s = load_settings(tr, b, V);
+        if (!s.valid) {
+            fill_nan<SPEC_BF16>(dst, vecs, tid, kThreads);
+            continue;
+        }
+        if (!s.active) {
+            if (logits != out)
+                for (int v = tid; v < vecs; v += kThreads) dst[v] = row[v];
+            continue;
+        }
+        const bool mass = s.p < 1.0f, counted = mass || s.k > 0;
+        // --- one pass over the row: the histogram, the groups' largest values
+        __syncthreads();  // the last row is done with the shared arrays
+        for (int i = tid; i < kSegs * 32; i += kThreads) sm.hist[i] = 0;
+        if (tid == 0) {
+            sm.first = kSegs * 32;
+            sm.elsewhere = false;
+        }
         __syncthreads();
-        if ((tid & 31) == 0) sm.red[tid >> 5] = top;
-        nan = __syncthreads_or(nan);
-        for (int i = 0; i < kWarps; ++i) top = max(top, sm.red[i]);
-        const float zmax = value_of(top);
-        uint64_t cut = 0;
-        if (s.valid && s.active && !nan && isfinite(zmax)) {
-            Weights w;
-            if (tid == 0) {
-                const double c = specv::kLog2eD / static_cast<double>(s.T);
-                sm.ch = static_cast<float>(c);
-                sm.cl = static_cast<float>(c - static_cast<double>(sm.ch));
-                if (s.m > 0.0f) sm.min_p_key = min_p_key(zmax, s.T, s.m);
+        uint32_t odd = 0;
+        for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
+            uint4 q[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int v = (g0 + u * kWarps) * 32 + lane;
+                q[u] = v < vecs ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (g0 + u * kWarps >= groups) break;
+                const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        count_value(sm, w[i] & 0xffffu, &odd);
+                        count_value(sm, w[i] >> 16, &odd);
+                    }
+                }
+                const uint32_t m = max_word(q[u]);
+                const uint32_t key = __reduce_max_sync(0xffffffffu, max(key16(m & 0xffffu), key16(m >> 16)));
+                if (lane == 0) sm.group_max[g0 + u * kWarps] = static_cast<uint16_t>(key);
+            }
+        }
+        bool slow = __syncthreads_or(odd) != 0;
+        float zmax = 0.0f;
+        if (!slow) {
+            // --- the bins' sums by segments of 32
+            int first = kSegs * 32;
+            for (int g = warp; g < kSegs; g += kWarps) {
+                const uint32_t n = sm.hist[g * 32 + lane];
+                const uint32_t any = __ballot_sync(0xffffffffu, n > 0);
+                if (any) first = min(first, g * 32 + __ffs(any) - 1);
+                const uint32_t sum = __reduce_add_sync(0xffffffffu, n);
+                if (lane == 0) sm.seg_count[g] = sum;
+            }
+            if (lane == 0) atomicMin(&sm.first, first);
+            __syncthreads();
+            first = sm.first;
+            slow = first == kSegs * 32;
+            if (!slow) zmax = bin_value(first);
+        }
+        // (values at or below -2^16 have no weight, and min-p excludes them)
+        if (!slow && !((-65536.0f - zmax) * specv::temp_scale(s.T) < -150.0f)) slow = true;
+        Weights w{};
+        if (!slow) {
+            if (tid == 0) set_row_constants(all.row, s, zmax);
+            __syncthreads();
+            w = row_weights(all.row, zmax, V, all.table);
+            if (mass) {
+                for (int g = warp; g < kSegs; g += kWarps) {
+                    uint64_t m = 0;
+                    if (sm.seg_count[g]) {
+                        const uint32_t n = sm.hist[g * 32 + lane];
+                        m = n ? weight_times(w, bin_value(g * 32 + lane), n) : 0;
+#pragma unroll
+                        for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
+                    }
+                    if (lane == 0) sm.seg_mass[g] = m;
+                }
+                __syncthreads();
+            }
+            // --- the border, by one warp
+            if (warp == 0) {
+                int bin = kSegs * 32;
+                uint32_t take = 0, above_count = 0;
+                uint64_t above_mass = 0, Z = 0;
+                bool found = true;
+                if (s.k > 0) {
+                    found = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass, &bin, &above_count, &above_mass);
+                    if (found) {
+                        take = s.k - above_count;
+                        if (mass) Z = above_mass + weight_times(w, bin_value(bin), take);
+                    }
+                } else if (mass) {
+                    for (int g = lane; g < kSegs; g += 32) Z += sm.seg_mass[g];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, off);
+                }
+                if (found && mass) {
+                    uint64_t target = lane == 0 ? mass_target(s.p, Z) : 0;
+                    target = __shfl_sync(0xffffffffu, target, 0);
+                    int pbin = 0;
+                    found = locate(sm, w, Goal{true, 0, target}, true, &pbin, &above_count, &above_mass);
+                    if (found) {
+                        const uint32_t t = ties_for(w, bin_value(pbin), sm.hist[pbin], above_mass, target);
+                        if (pbin < bin || t < take) take = t;
+                        bin = min(bin, pbin);
+                    }
+                }
+                if (lane == 0) {
+                    sm.elsewhere = !found;
+                    sm.value_bin = bin;
+                    sm.take = static_cast<int>(take);
+                    sm.ties = bin < kSegs * 32 ? static_cast<int>(sm.hist[bin]) : 0;
+                }
             }
             __syncthreads();
-            w.zmax = zmax;
-            w.ch = sm.ch;
-            w.cl = sm.cl;
-            w.frac = min(47, 30 + __clz(V));  // V weights of at most 1 sum to less than 2^63
-            w.table = sm.table;
-            const float scale = w.ch * kBinsPerOctave;
-            const bool mass = s.p < 1.0f;
-            if (s.k > 0 || mass) {
-                clear_bins(sm);
-                for_each<DT>(row, V, [&](float z, int) {
-                    add_to_bin(sm, first_bin(z, zmax, scale), mass, mass ? fixed_weight(w, z) : 0);
-                });
-                __syncthreads();
-                Goal goal{false, static_cast<uint32_t>(s.k), 0};
-                uint64_t Z = 0;
-                if (s.k > 0) {
-                    find_bin(sm, goal, 0, 0);
-                    // find_place splits bins in the same arrays
-                    find_place<DT>(sm, row, V, w, scale, goal, mass);
-                    cut = sm.cut;
-                    Z = sm.mass;
-                    if (mass) {
-                        __syncthreads();
-                        clear_bins(sm);
-                        for_each<DT>(row, V, [&](float z, int) {
-                            add_to_bin(sm, first_bin(z, zmax, scale), true, fixed_weight(w, z));
-                        });
-                        __syncthreads();
+            slow = sm.elsewhere;
+        }
+        if (slow) {
+            __syncthreads();
+            if (tid < 64) all.any.table[tid] = all.table[tid];
+            __syncthreads();
+            const uint64_t cut = cut_of_row<SPEC_BF16>(all.any, reinterpret_cast<const char *>(row), V, s);
+            if (cut != 0 || logits != out) write_cut<SPEC_BF16>(reinterpret_cast<const char *>(row), dst, V, cut);
+            continue;
+        }
+        // --- the border value: the lowest one kept, and how its ties go
+        uint32_t border = 0xff80u;  // -inf: everything
+        bool split = false;
+        if (counted) {
+            border = __float_as_uint(bin_value(sm.value_bin)) >> 16;
+            split = sm.take < sm.ties;
+        }
+        if (s.m > 0.0f) {
+            // the lowest bf16 value at or above min-p's border
+            const float f = value_of(all.row.min_p_key);
+            uint32_t h = __bfloat16_as_ushort(__float2bfloat16_ru(f));
+            if ((h & 0x7fffu) == 0) h = 0;
+            if (!counted || __uint_as_float(h << 16) > __uint_as_float(border << 16)) {
+                border = h;
+                split = false;
+            }
+        }
+        const uint32_t pair = border | border << 16;
+        // groups below the border (as keys; a zero border takes -0 too)
+        const uint32_t low = key16(border == 0 ? 0x8000u : border);
+        int cut_group = groups, cut_index = 0;
+        if (split) {
+            const int take = sm.take;
+            for_groups(groups, [&](int g, int v) {
+                uint32_t n = 0;
+                if (sm.group_max[g] >= low) {
+                    if (v < vecs) {
+                        const uint4 q = row[v];
+                        n = __popc(equal_mask(q.x, pair)) + __popc(equal_mask(q.y, pair)) + __popc(equal_mask(q.z, pair)) +
+                            __popc(equal_mask(q.w, pair));
                     }
+                    n = __reduce_add_sync(0xffffffffu, n >> 4);
                 }
-                if (mass) {
-                    goal.by_mass = true;
-                    if (s.k == 0) {
-                        find_bin(sm, goal, 0, 0);
-                        Z = sm.total_mass;
-                        __syncthreads();
-                    }
-                    if (tid == 0) sm.target = __double2ull_ru(static_cast<double>(s.p) * static_cast<double>(Z));
-                    __syncthreads();
-                    goal.target = sm.target;
-                    find_bin(sm, goal, 0, 0);
-                    find_place<DT>(sm, row, V, w, scale, goal, true);
-                    cut = max(cut, sm.cut);
+                if (lane == 0) sm.group_ties()[g] = static_cast<uint16_t>(n);
+            });
+            __syncthreads();
+            if (warp == 0) {
+                // the group where the ties run out, then the token
+                constexpr int kRun = kMaxGroups / 32;
+                uint32_t n = 0;
+                const int g0 = lane * kRun, g1 = min(groups, g0 + kRun);
+                for (int g = g0; g < g1; ++g) n += sm.group_ties()[g];
+                uint32_t c = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
+                    if (lane >= off) c += cc;
+                }
+                const int owner = __ffs(__ballot_sync(0xffffffffu, c >= static_cast<uint32_t>(take))) - 1;
+                c -= n;
+                int g = g0;
+                if (lane == owner)
+                    while (c + sm.group_ties()[g] < static_cast<uint32_t>(take)) c += sm.group_ties()[g++];
+                g = __shfl_sync(0xffffffffu, g, owner);
+                c = __shfl_sync(0xffffffffu, c, owner);
+                const int v = g * 32 + lane;
+                uint32_t bits = 0;  // a bit per tie of this lane's vector
+                if (v < vecs) {
+                    const uint4 q = row[v];
+                    const uint32_t e[4] = {equal_mask(q.x, pair), equal_mask(q.y, pair), equal_mask(q.z, pair), equal_mask(q.w, pair)};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) bits |= (e[i] & 1u) << (2 * i) | (e[i] >> 31) << (2 * i + 1);
+                }
+                uint32_t before = __popc(bits);
+                const uint32_t own = before;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const uint32_t cc = __shfl_up_sync(0xffffffffu, before, off);
+                    if (lane >= off) before += cc;
+                }
+                before += c - own;
+                if (before < static_cast<uint32_t>(take) && before + own >= static_cast<uint32_t>(take)) {
+                    for (int left = take - before; left > 1; --left) bits &= bits - 1;
+                    sm.cut_group = g;
+                    sm.cut_index = v * 8 + __ffs(bits) - 1;
                 }
             }
-            if (s.m > 0.0f) cut = max(cut, place_of(sm.min_p_key, -1));
+            __syncthreads();
+            cut_group = sm.cut_group;
+            cut_index = sm.cut_index;
         }
-        // --- the row out
-        if (cut == 0 && s.valid && logits == out) continue;
-        const uint32_t ckey = static_cast<uint32_t>(cut >> 32), cidx = ~static_cast<uint32_t>(cut);
-        for (int v = tid; v < vecs; v += kThreads) {
-            uint4 q = reinterpret_cast<const uint4 *>(row)[v];
-            float x[kPer];
-            Elem<DT>::unpack(q, x);
-            uint32_t *word = reinterpret_cast<uint32_t *>(&q);
+        // --- the row out: groups below the border need not be read again
+        for_groups(groups, [&](int g, int v) {
+            if (v >= vecs) return;
+            uint4 q = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            if (sm.group_max[g] >= low) {
+                q = row[v];
+                uint32_t *x = reinterpret_cast<uint32_t *>(&q);
+                const bool equal = g < cut_group;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const uint32_t key = key_of(x[i]);
-                const bool keep = cut == 0 || key > ckey || (key == ckey && static_cast<uint32_t>(v * kPer + i) <= cidx);
-                if (DT == SPEC_F32) {
-                    if (!keep) word[DT == SPEC_F32 ? i : 0] = 0xff800000u;
-                    if (!s.valid) word[DT == SPEC_F32 ? i : 0] = 0x7fc00000u;
-                } else {
-                    const uint32_t bits = s.valid ? 0xff80u : 0x7fc0u;
-                    if (!keep || !s.valid)
-                        word[i / 2] = i & 1 ? (word[i / 2] & 0xffffu) | bits << 16 : (word[i / 2] & 0xffff0000u) | bits;
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t keep = above_mask(x[i], pair, equal);
+                    if (g == cut_group) {
+                        const uint32_t e = equal_mask(x[i], pair);
+                        if (v * 8 + 2 * i <= cut_index) keep |= e & 0xffffu;
+                        if (v * 8 + 2 * i + 1 <= cut_index) keep |= e & 0xffff0000u;
+                    }
+                    x[i] = (x[i] & keep) | (0xff80ff80u & ~keep);
                 }
             }
             dst[v] = q;
-        }
+        });
     }
 }
 
@@ -596,8 +1052,14 @@ template <int DT>
 int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms,
                     cudaStream_t stream) {
     const int grid = std::min(rw.R, sms * 2);
-    truncate_kernel<DT><<<grid, kThreads, sizeof(Shared), stream>>>(static_cast<const char *>(logits),
-                                                                    static_cast<char *>(out), rw, tr, V);
+    const char *in = static_cast<const char *>(logits);
+    char *to = static_cast<char *>(out);
+    if (DT == SPEC_BF16 && V <= kMaxFastV) {
+        static_assert(sizeof(BothShared) <= 48 * 1024, "fits without an attribute");
+        truncate_bf16_kernel<<<grid, kThreads, sizeof(BothShared), stream>>>(in, to, rw, tr, V);
+    } else {
+        truncate_kernel<DT><<<grid, kThreads, sizeof(Shared), stream>>>(in, to, rw, tr, V);
+    }
     return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
