@@ -10,8 +10,11 @@
 //   y    = y + bias_b(v);  y = allowed_r(v) ? y : -inf;  rounded once.
 //
 // The pass reads and writes every logit once and computes next to nothing, so
-// memory bounds it.
-
+// memory bounds it.  Few columns of a sequence are seen, drafted or biased
+// (some hundreds of a vocabulary of 10^5), so the work is split in two: a
+// stream that copies the rows and applies the masks, 16 bytes a lane, and a
+// list of the few columns, whose logits are taken one a lane afterwards.  In
+// place the stream touches only what a mask takes away.
 #include <algorithm>
 #include <cstdint>
 
@@ -24,289 +27,386 @@ namespace speclog {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kChunk = kThreads * kCols;  // columns of one unit
-template <int DT>
-constexpr int kUnroll = DT == SPEC_BF16 ? 4 : 2;  // rows in flight per thread
-
-template <int DT>
-struct Vec {  // a thread's 8 columns of one row, as 32-bit words
-    static constexpr int kWords = DT == SPEC_BF16 ? 4 : 8;
-    uint32_t w[kWords];
-};
-
-template <int DT>
-__device__ __forceinline__ void load_cols(Vec<DT> &v, const char *row, int col, int ncol) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(col) * Elem<DT>::kBytes);
-    uint4 q = p[0];
-    v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
-    if constexpr (DT == SPEC_F32) {
-        if (ncol > 4) q = p[1];
-        v.w[4] = q.x, v.w[5] = q.y, v.w[6] = q.z, v.w[7] = q.w;
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ void store_cols(const Vec<DT> &v, char *row, int col, int ncol) {
-    uint4 *p = reinterpret_cast<uint4 *>(row + static_cast<int64_t>(col) * Elem<DT>::kBytes);
-    p[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-    if constexpr (DT == SPEC_F32) {
-        if (ncol > 4) p[1] = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ void fill_cols(Vec<DT> &v, uint32_t word) {
-#pragma unroll
-    for (int i = 0; i < Vec<DT>::kWords; ++i) v.w[i] = word;
-}
-
-// Column c of the 8, read and written without indexing registers.
-template <int DT>
-__device__ __forceinline__ float get_col(const Vec<DT> &v, int c) {
-    const int at = DT == SPEC_F32 ? c : c >> 1;
-    uint32_t x = v.w[0];
-#pragma unroll
-    for (int i = 1; i < Vec<DT>::kWords; ++i) x = i == at ? v.w[i] : x;
-    return __uint_as_float(DT == SPEC_F32 ? x : c & 1 ? x & 0xffff0000u : x << 16);
-}
-template <int DT>
-__device__ __forceinline__ void set_col(Vec<DT> &v, int c, float z) {
-    const int at = DT == SPEC_F32 ? c : c >> 1;
-    const uint32_t h = DT == SPEC_F32 ? __float_as_uint(z) : __bfloat16_as_ushort(__float2bfloat16_rn(z));
-    const uint32_t keep = DT == SPEC_F32 ? 0u : c & 1 ? 0xffffu : 0xffff0000u;
-    const uint32_t put = DT == SPEC_BF16 && (c & 1) ? h << 16 : h;
-#pragma unroll
-    for (int i = 0; i < Vec<DT>::kWords; ++i) v.w[i] = i == at ? (v.w[i] & keep) | put : v.w[i];
-}
-// -inf in the columns whose bit is clear
-template <int DT>
-__device__ __forceinline__ void mask_cols(Vec<DT> &v, uint32_t allowed) {
-#pragma unroll
-    for (int i = 0; i < Vec<DT>::kWords; ++i) {
-        uint32_t keep;
-        if (DT == SPEC_F32) keep = (allowed >> i) & 1 ? 0xffffffffu : 0u;
-        else keep = ((allowed >> (2 * i)) & 1 ? 0xffffu : 0u) | ((allowed >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
-        v.w[i] = (v.w[i] & keep) | (Elem<DT>::kNegInfWord & ~keep);
-    }
-}
+constexpr int kWarps = kThreads / 32;
+constexpr int kList = 256;    // columns listed at once
+#ifndef SPEC_PROCESS_PER_SM
+#define SPEC_PROCESS_PER_SM 8
+#endif
+constexpr int kPerSm = SPEC_PROCESS_PER_SM;  // resident CTAs
 
 template <int DT>
 constexpr uint32_t kNanWord = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
 
-struct Shared {
-    int seq;
-    int mask_row[kMaxPath];
-    int token[kMaxPath];
-    uint64_t before[kMaxPath];      // by row: the tokens that precede it
-    uint32_t drafted[kChunk / 32];  // columns that a drafted token names
-    uint32_t biased[kChunk / 32];   // columns that a bias entry names
-    int bias_token[kThreads];
-    float bias_value[kThreads];
-    int count[kCols][kThreads];   // by column of the thread: a seen token's count
-    float bias[kCols][kThreads];  // and a biased token's bias
+// How a group of threads takes a unit of columns.  With the stream a CTA takes
+// 4096 columns in a row; without it (in place, no masks) a warp takes 128
+// words spread over the vocabulary: ids are often ordered by frequency, and
+// so every warp gets its share of the frequent ones.
+template <bool STREAM>
+struct Group {
+    static constexpr int kSize = STREAM ? kThreads : 32;
+    static constexpr int kWordsEach = STREAM ? 1 : 4;
+    static constexpr int kWords = kSize * kWordsEach;
+    static constexpr int kCount = kThreads / kSize;  // groups per CTA
+
+    static __device__ __forceinline__ int self() { return threadIdx.x / kSize; }
+    static __device__ __forceinline__ int thread() { return threadIdx.x % kSize; }
+    static __device__ __forceinline__ void sync() {
+        if (STREAM) __syncthreads();
+        else __syncwarp();
+    }
+    static __device__ __forceinline__ bool any(bool x) {
+        return STREAM ? __syncthreads_or(x) != 0 : __any_sync(0xffffffffu, x) != 0;
+    }
+    // the word of the bit arrays that the unit's place i stands for, and back (-1: another unit's)
+    static __device__ __forceinline__ int word(int unit, int units, int i) { return STREAM ? unit * kWords + i : unit + units * i; }
+    static __device__ __forceinline__ int place(int unit, int units, int word) {
+        if (STREAM) return word >= unit * kWords && word < (unit + 1) * kWords ? word - unit * kWords : -1;
+        return word % units == unit ? word / units : -1;
+    }
 };
 
-// A CTA takes an even share of the rows' chunks in the order (sequence,
-// chunk, row), so that what depends on the sequence and the columns alone
-// (its seen tokens, their counts, its biases) is read once for all its rows.
-// A thread keeps the same 8 columns over the rows; its seen and biased columns
-// are few, so they are taken one at a time.
+template <bool STREAM>
+struct GroupShared {
+    int token[kMaxPath];
+    int up[kMaxPath];           // tree: parent within the sequence
+    uint64_t before[kMaxPath];  // tree: the nodes whose tokens a row follows
+    uint32_t drafted[Group<STREAM>::kWords], biased[Group<STREAM>::kWords];
+    int warp_sum[kWarps];
+    int column[kList], count[kList];
+    uint8_t flags[kList];
+};
+enum { kSeen = 1, kDrafted = 2, kBiased = 4 };
+
+// The sequence that holds item `at`, from b on, by each warp.
+__device__ __forceinline__ int advance(const Rows &rw, int b, int64_t at, int per_row) {
+    for (;;) {
+        const int j = min(b + static_cast<int>(threadIdx.x & 31), rw.B - 1);
+        const uint32_t hit = __ballot_sync(0xffffffffu, at < static_cast<int64_t>(rw.first_row(j + 1)) * per_row);
+        if (hit) return min(b + __ffs(hit) - 1, rw.B - 1);
+        b += 32;
+        if (b >= rw.B) return rw.B - 1;  // not reached: `at` lies before the last row's end
+    }
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 8)
-    process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int chunks) {
-    __shared__ Shared sm;
-    const int tid = threadIdx.x;
+__device__ __forceinline__ float load_logit(const char *row, int col) {
+    if (DT == SPEC_F32) return reinterpret_cast<const float *>(row)[col];
+    return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[col]) << 16);
+}
+template <int DT>
+__device__ __forceinline__ void store_logit(char *row, int col, float z) {
+    if (DT == SPEC_F32) reinterpret_cast<float *>(row)[col] = z;
+    else reinterpret_cast<uint16_t *>(row)[col] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
+}
+
+// -inf in the columns of a vector whose bit is clear.
+template <int DT>
+__device__ __forceinline__ void mask_vec(uint4 &q, uint32_t allowed) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t keep;
+        if (DT == SPEC_F32) keep = (allowed >> i) & 1 ? 0xffffffffu : 0u;
+        else keep = ((allowed >> (2 * i)) & 1 ? 0xffffu : 0u) | ((allowed >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+        w[i] = (w[i] & keep) | (Elem<DT>::kNegInfWord & ~keep);
+    }
+}
+
+// The stream over rows row0 + i0 .. row0 + i1 - 1 of a CTA's columns: a copy with
+// the masks applied; in place only what a mask takes away.
+template <int DT>
+__device__ __forceinline__ void stream_rows(const char *logits, char *out, const Process &ps, int V, int64_t row0, int i0,
+                                            int i1, int c0, bool inplace) {
+    constexpr int kPer = Elem<DT>::kPerVec;
+    constexpr int kVecs = 32 / kPer;                // a thread's vectors of one row
+    constexpr int kRows = DT == SPEC_BF16 ? 2 : 1;  // rows in flight
+    constexpr uint32_t kAll = (1u << kPer) - 1;
+    const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
+    const int W = (V + 31) / 32;
+    const int c = c0 + static_cast<int>(threadIdx.x) * kPer;  // + j * kThreads * kPer
+    for (int i = i0; i < i1; i += kRows) {
+        uint32_t allowed[kRows][kVecs];
+        uint4 q[kRows][kVecs];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            int m = -1;
+            if (ps.mask && i + u < i1) {
+                m = ps.mask_rows ? __ldg(ps.mask_rows + row0 + i + u) : static_cast<int>(row0 + i + u);
+                if (m >= ps.M) m = -1;  // (an error: the row becomes NaN later)
+            }
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int col = c + j * kThreads * kPer;
+                allowed[u][j] = kAll;
+                if (m >= 0 && col < V)
+                    allowed[u][j] = bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7) & kAll;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int col = c + j * kThreads * kPer;
+                const bool need = allowed[u][j] != 0 && !(inplace && allowed[u][j] == kAll);
+                q[u][j] = make_uint4(0, 0, 0, 0);
+                if (need && col < V && i + u < i1)
+                    q[u][j] = *reinterpret_cast<const uint4 *>(logits + (row0 + i + u) * row_bytes +
+                                                               static_cast<int64_t>(col) * Elem<DT>::kBytes);
+            }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int col = c + j * kThreads * kPer;
+                if (col >= V || i + u >= i1 || (inplace && allowed[u][j] == kAll)) continue;
+                if (allowed[u][j] != kAll) mask_vec<DT>(q[u][j], allowed[u][j]);
+                *reinterpret_cast<uint4 *>(out + (row0 + i + u) * row_bytes + static_cast<int64_t>(col) * Elem<DT>::kBytes) = q[u][j];
+            }
+    }
+}
+
+// A unit's columns of some rows as NaN.
+template <int DT, bool STREAM>
+__device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0, int i1, int unit, int units) {
+    using G = Group<STREAM>;
+    const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
+    constexpr uint32_t w = kNanWord<DT>;
+    constexpr int kPer = Elem<DT>::kPerVec;
+    for (int i = i0; i < i1; ++i)
+        for (int x = G::thread(); x < G::kWords * 32 / kPer; x += G::kSize) {
+            const int col = G::word(unit, units, x / (32 / kPer)) * 32 + x % (32 / kPer) * kPer;
+            if (col < V)
+                *reinterpret_cast<uint4 *>(out + (row0 + i) * row_bytes + static_cast<int64_t>(col) * Elem<DT>::kBytes) =
+                    make_uint4(w, w, w, w);
+        }
+}
+
+// A group of threads takes an even share of the rows' units of columns in the
+// order (sequence, unit, row), so that what depends on the sequence and the
+// columns alone (its seen tokens, their counts, its biases) is read once for
+// the unit's rows.
+template <int DT, bool STREAM>
+__global__ void __launch_bounds__(kThreads, kPerSm)
+    process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int units) {
+    using G = Group<STREAM>;
+    __shared__ int s_seq;
+    __shared__ GroupShared<STREAM> s_group[G::kCount];
+    const int me = G::thread(), lane = threadIdx.x & 31;
+    GroupShared<STREAM> &sm = s_group[G::self()];
     const bool inplace = logits == out;
     const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
     const int W = (V + 31) / 32;
-    const bool pen = ps.counts != nullptr;
+    const bool pen = ps.counts != nullptr, tree = rw.mode == SPEC_ROWS_TREE;
 
     int64_t total;
-    const int64_t all = static_cast<int64_t>(__ldg(rw.offsets + rw.B));
-    const int64_t rows_all = rw.mode == SPEC_ROWS_TARGET ? all + rw.B : rw.mode == SPEC_ROWS_NEXT ? rw.B : all;
-    int64_t at = rows_all * chunks * blockIdx.x / gridDim.x;
-    const int64_t end = rows_all * chunks * (blockIdx.x + 1) / gridDim.x;
-    const bool ok = check_rows(rw, pen, at, chunks, &sm.seq, &total);
-    if (!ok) {  // the call fails: every row is NaN
-        Vec<DT> nan;
-        fill_cols<DT>(nan, kNanWord<DT>);
-        for (int64_t u = blockIdx.x; u < static_cast<int64_t>(rw.R) * chunks; u += gridDim.x) {
-            const int col = static_cast<int>(u % chunks) * kChunk + tid * kCols;
-            if (col < V) store_cols<DT>(nan, out + u / chunks * row_bytes, col, min(kCols, V - col));
-        }
+    const int64_t items = static_cast<int64_t>(rw.first_row(rw.B)) * units;
+    const int64_t groups = static_cast<int64_t>(gridDim.x) * G::kCount;
+    const int64_t self = static_cast<int64_t>(blockIdx.x) * G::kCount + G::self();
+    if (!check_rows(rw, pen, items * blockIdx.x / gridDim.x, units, &s_seq, &total)) {
+        // the call fails: every row is NaN
+        for (int64_t u = self; u < static_cast<int64_t>(rw.R) * units; u += groups)
+            nan_rows<DT, STREAM>(out, V, u / units, 0, 1, static_cast<int>(u % units), units);
         return;
     }
+    int64_t at = items * self / groups;
+    const int64_t end = items * (self + 1) / groups;
     if (at >= end) return;
-    int b = sm.seq;
+    int b = advance(rw, s_seq, at, units);
 
-    while (at < end) {
+    for (;;) {
         const int o0 = __ldg(rw.offsets + b), o1 = __ldg(rw.offsets + b + 1);
         const int k = o1 - o0;  // drafted tokens, or tree nodes
         const int row0 = rw.first_row(b, o0), n = rw.first_row(b + 1, o1) - row0;
-        const int64_t rel = at - static_cast<int64_t>(row0) * chunks;
-        const int chunk = static_cast<int>(rel / n), i0 = static_cast<int>(rel % n);
+        const int64_t rel = at - static_cast<int64_t>(row0) * units;
+        const int unit = static_cast<int>(rel / n), i0 = static_cast<int>(rel - static_cast<int64_t>(unit) * n);
         const int i1 = static_cast<int>(min(static_cast<int64_t>(n), i0 + (end - at)));
-        const int c0 = chunk * kChunk, col = c0 + tid * kCols;
-        const int ncol = max(0, min(kCols, V - col));
 
-        // --- what the unit's rows share -----------------------------------
-        __syncthreads();  // the last unit is done with the shared arrays
-        if (tid < kChunk / 32) sm.drafted[tid] = sm.biased[tid] = 0;
-        bool bad = false;
-        if (tid < n) {
-            int m = -1;
-            if (ps.mask) {
-                m = ps.mask_rows ? __ldg(ps.mask_rows + row0 + tid) : row0 + tid;
-                if (m < -1 || m >= ps.M) m = -2;  // no such mask: the row is an error
-            }
-            sm.mask_row[tid] = m;
-        }
-        Penalty p;
+        // --- what the sequence and the columns say: asked for before the stream, used after it
+        Penalty p{1.0f, 0.0f, 0.0f};
         int64_t slot = b;
-        uint32_t pbits = 0, obits = 0;
+        uint32_t prompt[G::kWordsEach], emitted[G::kWordsEach];
+        constexpr int kTokens = (kMaxPath + G::kSize - 1) / G::kSize;
+        int token[kTokens], up[kTokens];
+        bool bad = false;
+        if (pen && ps.slots) slot = __ldg(ps.slots + b);
+        const bool there = pen && slot >= 0 && slot < ps.S;
+#pragma unroll
+        for (int i = 0; i < G::kWordsEach; ++i) {
+            const int word = G::word(unit, units, i * G::kSize + me);
+            prompt[i] = emitted[i] = 0;
+            if (there && word < W) {
+                prompt[i] = static_cast<uint32_t>(__ldg(ps.seen + slot * 2 * W + word));
+                emitted[i] = static_cast<uint32_t>(__ldg(ps.seen + (slot * 2 + 1) * W + word));
+            }
+        }
         if (pen) {
-            bad |= !load_penalty(ps, b, &p);
-            if (ps.slots) slot = __ldg(ps.slots + b);
-            if (slot < 0 || slot >= ps.S) {
-                bad = true;
-            } else if (ncol > 0) {
-                pbits = bit_byte(ps.seen, slot * 2 * W, col);
-                obits = bit_byte(ps.seen, (slot * 2 + 1) * W, col);
-            }
-            if (tid < k) {
-                const int t = __ldg(rw.tokens + o0 + tid);
-                const bool root = rw.mode == SPEC_ROWS_TREE && tid == 0;
-                sm.token[tid] = t;
-                bad |= !root && (t < 0 || t >= V);
-                if (rw.mode == SPEC_ROWS_TREE) {
-                    const int up = __ldg(rw.parent + o0 + tid);
-                    bad |= root ? up != -1 : (up < o0 || up >= o0 + tid);
+            bad |= !there || !load_penalty(ps, b, &p);
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                token[t] = up[t] = 0;
+                if (me + G::kSize * t < k) {
+                    token[t] = __ldg(rw.tokens + o0 + me + G::kSize * t);
+                    if (tree) up[t] = __ldg(rw.parent + o0 + me + G::kSize * t);
                 }
             }
         }
-        __syncthreads();
-        if (pen && tid < k && !(rw.mode == SPEC_ROWS_TREE && tid == 0)) {
-            const int d = sm.token[tid] - c0;
-            if (d >= 0 && d < kChunk) atomicOr(&sm.drafted[d >> 5], 1u << (d & 31));
-        }
-        if (pen && tid < n) {
-            uint64_t m = 0;
-            if (rw.mode == SPEC_ROWS_NEXT) {
-                m = k == 64 ? ~0ull : (1ull << k) - 1;
-            } else if (rw.mode == SPEC_ROWS_TREE) {
-                // a bad parent ends the walk: it is reported above
-                for (int g = tid, left = kMaxPath; g > 0 && left > 0; --left) {
-                    m |= 1ull << g;
-                    const int up = __ldg(rw.parent + o0 + g) - o0;
-                    g = up < g ? up : 0;
-                }
-            } else {
-                m = (1ull << tid) - 1;  // tid <= SPEC_MAX_K
-            }
-            sm.before[tid] = m;
-        }
-        uint32_t bbits = 0;
+        int e0 = 0, e1 = 0;
         if (ps.bias_offsets) {
-            const int e0 = __ldg(ps.bias_offsets + b), e1 = __ldg(ps.bias_offsets + b + 1);
-            const bool range = e0 >= 0 && e1 >= e0 && e1 <= ps.n_bias;
-            bad |= !range;
-            for (int e = e0; range && e < e1; e += kThreads) {
-                const int len = min(kThreads, e1 - e);
-                if (tid < len) {
-                    const int t = __ldg(ps.bias_tokens + e + tid);
-                    const float v = __ldg(ps.bias_values + e + tid);
-                    bad |= t < 0 || t >= V || !(v < __int_as_float(0x7f800000));  // NaN and +inf
-                    sm.bias_token[tid] = t - c0;
-                    sm.bias_value[tid] = v;
-                    const int d = t - c0;
-                    if (d >= 0 && d < kChunk) atomicOr(&sm.biased[d >> 5], 1u << (d & 31));
+            e0 = __ldg(ps.bias_offsets + b), e1 = __ldg(ps.bias_offsets + b + 1);
+            if (e0 < 0 || e1 < e0 || e1 > ps.n_bias) {
+                bad = true;
+                e1 = e0 = 0;
+            }
+        }
+        if (STREAM) stream_rows<DT>(logits, out, ps, V, row0, i0, i1, unit * G::kWords * 32, inplace);
+
+        // --- the unit's columns that anything applies to
+#pragma unroll
+        for (int i = 0; i < G::kWordsEach; ++i) sm.drafted[i * G::kSize + me] = sm.biased[i * G::kSize + me] = 0;
+        G::sync();
+        if (pen) {
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                const int j = me + G::kSize * t;
+                if (j >= k) continue;
+                const bool root = tree && j == 0;
+                sm.token[j] = token[t];
+                if (!root) {
+                    const bool in = token[t] >= 0 && token[t] < V;
+                    bad |= !in;
+                    const int d = in ? G::place(unit, units, token[t] >> 5) : -1;
+                    if (d >= 0) atomicOr(&sm.drafted[d], 1u << (token[t] & 31));
                 }
+                if (tree) {
+                    bad |= root ? up[t] != -1 : (up[t] < o0 || up[t] >= o0 + j);
+                    sm.up[j] = up[t] - o0;
+                }
+            }
+        }
+        for (int e = e0 + me; e < e1; e += G::kSize) {
+            const int t = __ldg(ps.bias_tokens + e);
+            const bool in = t >= 0 && t < V;
+            bad |= !in || !(__ldg(ps.bias_values + e) < __int_as_float(0x7f800000));  // NaN and +inf
+            const int d = in ? G::place(unit, units, t >> 5) : -1;
+            if (d >= 0) atomicOr(&sm.biased[d], 1u << (t & 31));
+        }
+        bad = G::any(bad);
+        G::sync();  // the shared arrays are whole, the stream's stores done
+        if (bad) {
+            nan_rows<DT, STREAM>(out, V, row0, i0, i1, unit, units);
+        } else {
+            uint32_t touched[G::kWordsEach], drafted[G::kWordsEach], biased[G::kWordsEach];
+            int rank = 0;
+#pragma unroll
+            for (int i = 0; i < G::kWordsEach; ++i) {
+                const int word = G::word(unit, units, i * G::kSize + me);
+                // bits behind the vocabulary say nothing
+                const uint32_t in_v = word >= W ? 0u : word == W - 1 && (V & 31) ? (1u << (V & 31)) - 1 : 0xffffffffu;
+                drafted[i] = sm.drafted[i * G::kSize + me];
+                biased[i] = sm.biased[i * G::kSize + me];
+                touched[i] = (prompt[i] | emitted[i] | drafted[i] | biased[i]) & in_v;
+                rank += __popc(touched[i]);
+            }
+            const int own = rank;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, rank, off);
+                if (lane >= off) rank += x;
+            }
+            int listed = __shfl_sync(0xffffffffu, rank, 31);
+            rank -= own;
+            if (STREAM) {
+                if (lane == 0) sm.warp_sum[threadIdx.x >> 5] = listed;
                 __syncthreads();
-                if (reinterpret_cast<const unsigned char *>(sm.biased)[tid]) {
-                    // the same token twice: the entries add, in list order
-                    for (int j = 0; j < len; ++j) {
-                        const int d = sm.bias_token[j] - tid * kCols;
-                        if (d < 0 || d >= kCols) continue;
-                        sm.bias[d][tid] = (bbits >> d) & 1 ? __fadd_rn(sm.bias[d][tid], sm.bias_value[j]) : sm.bias_value[j];
-                        bbits |= 1u << d;
+                listed = 0;
+                for (int i = 0; i < kWarps; ++i) {
+                    if (i == static_cast<int>(threadIdx.x >> 5)) rank += listed;
+                    listed += sm.warp_sum[i];
+                }
+            }
+            if (listed && tree && pen) {
+                for (int j = me; j < n; j += G::kSize) {
+                    uint64_t m = 0;
+                    for (int g = j; g > 0; g = sm.up[g]) m |= 1ull << g;  // parents are earlier nodes
+                    sm.before[j] = m;
+                }
+            }
+            for (int base = 0; base < listed; base += kList) {
+                const int len = min(kList, listed - base);
+                G::sync();
+                int at_rank = rank - base;
+#pragma unroll
+                for (int i = 0; i < G::kWordsEach; ++i) {
+                    const int col0 = G::word(unit, units, i * G::kSize + me) * 32;
+                    for (uint32_t m = touched[i]; m; m &= m - 1, ++at_rank) {
+                        if (at_rank < 0 || at_rank >= kList) continue;
+                        const int bit = __ffs(m) - 1;
+                        sm.column[at_rank] = col0 + bit;
+                        sm.flags[at_rank] = static_cast<uint8_t>((prompt[i] >> bit & 1) * kSeen | (drafted[i] >> bit & 1) * kDrafted |
+                                                                 (biased[i] >> bit & 1) * kBiased);
+                        sm.count[at_rank] = emitted[i] >> bit & 1 ? __ldg(ps.counts + slot * V + col0 + bit) : 0;
                     }
                 }
-                __syncthreads();
-            }
-        }
-        if (ncol < kCols) {  // bits behind the vocabulary say nothing
-            pbits &= 0x0fu;
-            obits &= 0x0fu;
-        }
-        for (uint32_t m = obits; m; m &= m - 1) {
-            const int c = __ffs(m) - 1;
-            sm.count[c][tid] = __ldg(ps.counts + slot * V + col + c);
-        }
-        bad = __syncthreads_or(bad);
-        const uint32_t dbits = pen ? reinterpret_cast<const unsigned char *>(sm.drafted)[tid] : 0;
-        const uint32_t touched = pbits | obits | dbits | bbits;
-
-        // --- the rows -------------------------------------------------------
-        for (int i = i0; i < i1 && ncol > 0; i += kUnroll<DT>) {
-            Vec<DT> v[kUnroll<DT>];
-            uint32_t allowed[kUnroll<DT>];
-            bool write[kUnroll<DT>];
-#pragma unroll
-            for (int u = 0; u < kUnroll<DT>; ++u) {
-                write[u] = i + u < i1;
-                allowed[u] = 0xffu;
-                if (!write[u]) continue;
-                const int m = ps.mask ? sm.mask_row[i + u] : -1;
-                if (m >= 0) allowed[u] = bit_byte(ps.mask, static_cast<int64_t>(m) * W, col);
-                if (ncol < kCols) allowed[u] |= 0xf0u;
-                if (bad || m == -2) {
-                    fill_cols<DT>(v[u], kNanWord<DT>);
-                    allowed[u] = 0x100u;
-                    continue;
-                }
-                write[u] = !inplace || touched || allowed[u] != 0xffu;
-                if ((allowed[u] & (ncol < kCols ? 0x0fu : 0xffu)) == 0) {
-                    fill_cols<DT>(v[u], Elem<DT>::kNegInfWord);  // nothing of the input is needed
-                    allowed[u] = 0x100u;
-                } else if (write[u]) {
-                    load_cols<DT>(v[u], logits + (row0 + i + u) * row_bytes, col, ncol);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll<DT>; ++u) {
-                if (!write[u]) continue;
-                if (allowed[u] != 0x100u) {
-                    for (uint32_t m = touched & allowed[u]; m; m &= m - 1) {
-                        const int c = __ffs(m) - 1;
-                        float z = get_col<DT>(v[u], c);
-                        int n_c = (obits >> c) & 1 ? sm.count[c][tid] : 0;
-                        if ((dbits >> c) & 1) {
-                            const int t = col + c;
-                            for (uint64_t d = sm.before[i + u]; d; d &= d - 1) n_c += sm.token[__ffsll(d) - 1] == t;
+                G::sync();
+                // a thread takes a column, all its rows
+                for (int e = me; e < len; e += G::kSize) {
+                    const int col = sm.column[e], count = sm.count[e];
+                    const uint32_t f = sm.flags[e];
+                    float bias = 0.0f;
+                    if (f & kBiased) {
+                        // the same token twice: the entries add, in list order
+                        bool any = false;
+                        for (int x = e0; x < e1; ++x) {
+                            if (__ldg(ps.bias_tokens + x) != col) continue;
+                            const float v = __ldg(ps.bias_values + x);
+                            bias = any ? __fadd_rn(bias, v) : v;
+                            any = true;
                         }
-                        if ((pbits >> c) & 1 || n_c > 0) z = penalised(z, n_c, p);
-                        if ((bbits >> c) & 1) z = __fadd_rn(z, sm.bias[c][tid]);
-                        set_col<DT>(v[u], c, z);
                     }
-                    if (allowed[u] != 0xffu) mask_cols<DT>(v[u], allowed[u]);
+                    constexpr int kRows = 4;  // in flight
+                    for (int i = i0; i < i1; i += kRows) {
+                        float z[kRows];
+                        bool go[kRows];
+#pragma unroll
+                        for (int u = 0; u < kRows; ++u) {
+                            go[u] = i + u < i1;
+                            if (go[u] && ps.mask) {
+                                const int m = ps.mask_rows ? __ldg(ps.mask_rows + row0 + i + u) : row0 + i + u;
+                                go[u] = m < 0 || m >= ps.M || ((bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7)) & 1);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < kRows; ++u)
+                            z[u] = go[u] ? load_logit<DT>(logits + static_cast<int64_t>(row0 + i + u) * row_bytes, col) : 0.0f;
+#pragma unroll
+                        for (int u = 0; u < kRows; ++u) {
+                            if (!go[u]) continue;
+                            int c = count;
+                            if (f & kDrafted) {
+                                const uint64_t before = tree ? sm.before[i + u] : rw.mode == SPEC_ROWS_NEXT ? (1ull << k) - 1 : (1ull << (i + u)) - 1;
+                                for (uint64_t d = before; d; d &= d - 1) c += sm.token[__ffsll(d) - 1] == col;
+                            }
+                            if ((f & kSeen) || c > 0) z[u] = penalised(z[u], c, p);
+                            if (f & kBiased) z[u] = __fadd_rn(z[u], bias);
+                            store_logit<DT>(out + static_cast<int64_t>(row0 + i + u) * row_bytes, col, z[u]);
+                        }
+                    }
                 }
-                store_cols<DT>(v[u], out + (row0 + i + u) * row_bytes, col, ncol);
             }
+            if (ps.mask_rows)  // rows that name no mask there is
+                for (int i = i0; i < i1; ++i) {
+                    const int m = __ldg(ps.mask_rows + row0 + i);
+                    if (m >= -1 && m < ps.M) continue;
+                    G::sync();
+                    nan_rows<DT, STREAM>(out, V, row0, i, i + 1, unit, units);
+                }
         }
 
-        // --- the next unit ----------------------------------------------------
+        // --- the next unit
         at += i1 - i0;
-        if (at < end && at == static_cast<int64_t>(row0 + n) * chunks) {
-            ++b;
-            if (rw.first_row(b + 1) == rw.first_row(b)) {  // a sequence without rows: look further
-                for (int j = b + tid; j < rw.B; j += kThreads)
-                    if (at >= static_cast<int64_t>(rw.first_row(j)) * chunks &&
-                        at < static_cast<int64_t>(rw.first_row(j + 1)) * chunks)
-                        sm.seq = j;
-                __syncthreads();
-                b = sm.seq;
-            }
-        }
+        if (at >= end) return;
+        G::sync();
+        if (at >= static_cast<int64_t>(row0 + n) * units) b = advance(rw, b + 1, at, units);
     }
 }
 
@@ -381,14 +481,15 @@ __global__ void __launch_bounds__(kResetThreads)
     }
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 int launch_process(const void *logits, void *out, const Rows &rw, const Process &ps, int V, int sms,
                    cudaStream_t stream) {
-    const int chunks = (V + kChunk - 1) / kChunk;
-    const int64_t units = static_cast<int64_t>(rw.R) * chunks;
-    const int grid = static_cast<int>(std::min<int64_t>(units, static_cast<int64_t>(sms) * 8));
-    process_kernel<DT><<<grid, kThreads, 0, stream>>>(static_cast<const char *>(logits), static_cast<char *>(out), rw,
-                                                      ps, V, chunks);
+    using G = Group<STREAM>;
+    const int words = (V + 31) / 32, units = (words + G::kWords - 1) / G::kWords;
+    const int64_t ctas = (static_cast<int64_t>(rw.R) * units + G::kCount - 1) / G::kCount;
+    const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(sms) * kPerSm));
+    process_kernel<DT, STREAM><<<grid, kThreads, 0, stream>>>(static_cast<const char *>(logits), static_cast<char *>(out),
+                                                              rw, ps, V, units);
     return specv::cuda_ok(cudaGetLastError(), "launch process_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
@@ -410,8 +511,12 @@ int spec_logits_process(const void *logits, const spec_rows_t *rows, const spec_
     specv::DeviceState *st = specv::device_state(&dev);
     if (!st) return SPEC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == SPEC_F32 ? launch_process<SPEC_F32>(logits, out, rw, ps, V, st->sms, s)
-                             : launch_process<SPEC_BF16>(logits, out, rw, ps, V, st->sms, s);
+    const bool sparse = logits == out && !ps.mask;  // only the listed columns change
+    if (dtype == SPEC_F32)
+        return sparse ? launch_process<SPEC_F32, false>(logits, out, rw, ps, V, st->sms, s)
+                      : launch_process<SPEC_F32, true>(logits, out, rw, ps, V, st->sms, s);
+    return sparse ? launch_process<SPEC_BF16, false>(logits, out, rw, ps, V, st->sms, s)
+                  : launch_process<SPEC_BF16, true>(logits, out, rw, ps, V, st->sms, s);
 }
 
 int spec_penalty_update(int32_t *counts, int32_t *seen, int S, int V, const int32_t *slots, const spec_rows_t *rows,
