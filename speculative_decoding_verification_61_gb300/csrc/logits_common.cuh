@@ -17,7 +17,6 @@ using specv::Elem;
 
 constexpr int kMaxPath = SPEC_MAX_TREE_NODES;  // drafted tokens (or tree nodes) of one sequence
 static_assert(kMaxPath >= SPEC_MAX_K, "one word of 64 bits holds the tokens before a row");
-constexpr int kCols = 8;  // columns per thread: one byte of every bit array
 
 // The rows of a call: sequence b owns first_row(b) .. first_row(b + 1) - 1.
 struct Rows {
@@ -34,27 +33,26 @@ struct Rows {
 };
 
 // Whether the offsets are what the call's layout allows, found by the whole
-// block, and in the same pass the sequence that holds item `at`, when each
-// row stands for `per_row` items (its columns' chunks; 1: the row itself).
-// *total: the items of all sequences.  Needs every thread of the block; s_seq
-// is one int of shared memory.
-__device__ __forceinline__ bool check_rows(const Rows &rw, bool need_tokens, int64_t at, int per_row, int *s_seq,
-                                           int64_t *total) {
+// block.
+__device__ __forceinline__ bool check_rows(const Rows &rw, bool need_tokens) {
     const int lo = rw.mode == SPEC_ROWS_TREE ? 1 : 0;
     const int hi = rw.mode == SPEC_ROWS_TREE ? SPEC_MAX_TREE_NODES : SPEC_MAX_K;
     const int o0 = __ldg(rw.offsets), oB = __ldg(rw.offsets + rw.B);
     bool bad = o0 != 0;
     for (int b = threadIdx.x; b < rw.B; b += blockDim.x) {
-        const int a = __ldg(rw.offsets + b), z = __ldg(rw.offsets + b + 1);
-        bad |= z < a || z - a < lo || z - a > hi;
-        const int64_t f0 = static_cast<int64_t>(rw.first_row(b, a)) * per_row;
-        const int64_t f1 = static_cast<int64_t>(rw.first_row(b + 1, z)) * per_row;
-        if (at >= f0 && at < f1) *s_seq = b;
+        const int n = __ldg(rw.offsets + b + 1) - __ldg(rw.offsets + b);
+        bad |= n < lo || n > hi;
     }
     const int end = rw.first_row(rw.B, oB);
     bad |= end < 0 || end > rw.R || (need_tokens && oB > rw.n_tokens);
-    *total = static_cast<int64_t>(end) * per_row;
     return __syncthreads_or(bad) == 0;
+}
+
+// The same, and the sequence that holds row r into *s_seq (shared memory).
+__device__ __forceinline__ bool check_rows(const Rows &rw, int64_t r, int *s_seq) {
+    for (int b = threadIdx.x; b < rw.B; b += blockDim.x)
+        if (r >= rw.first_row(b) && r < rw.first_row(b + 1)) *s_seq = b;
+    return check_rows(rw, false);
 }
 
 // What the processing of logits reads beside them (spec_logits_t).

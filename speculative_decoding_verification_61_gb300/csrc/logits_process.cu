@@ -30,22 +30,23 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 256;    // columns listed at once
 #ifndef SPEC_PROCESS_PER_SM
-#define SPEC_PROCESS_PER_SM 8
+#define SPEC_PROCESS_PER_SM 6
 #endif
 constexpr int kPerSm = SPEC_PROCESS_PER_SM;  // resident CTAs
 
 template <int DT>
 constexpr uint32_t kNanWord = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
 
-// How a group of threads takes a unit of columns.  With the stream a CTA takes
-// 4096 columns in a row; without it (in place, no masks) a warp takes 128
-// words spread over the vocabulary: ids are often ordered by frequency, and
-// so every warp gets its share of the frequent ones.
+// How a group of threads takes a unit of 128 words of the bit arrays (4096
+// columns): with the stream a CTA takes them in a row, without it (in place, no
+// masks) a warp takes words spread over the vocabulary: ids are often ordered
+// by frequency, and so every warp gets its share of the frequent ones, whose
+// columns are all its work.
 template <bool STREAM>
 struct Group {
     static constexpr int kSize = STREAM ? kThreads : 32;
-    static constexpr int kWordsEach = STREAM ? 1 : 4;
-    static constexpr int kWords = kSize * kWordsEach;
+    static constexpr int kWords = 128;
+    static constexpr int kWordsEach = kWords / kSize;
     static constexpr int kCount = kThreads / kSize;  // groups per CTA
 
     static __device__ __forceinline__ int self() { return threadIdx.x / kSize; }
@@ -57,12 +58,16 @@ struct Group {
     static __device__ __forceinline__ bool any(bool x) {
         return STREAM ? __syncthreads_or(x) != 0 : __any_sync(0xffffffffu, x) != 0;
     }
-    // the word of the bit arrays that the unit's place i stands for, and back (-1: another unit's)
-    static __device__ __forceinline__ int word(int unit, int units, int i) { return STREAM ? unit * kWords + i : unit + units * i; }
-    static __device__ __forceinline__ int place(int unit, int units, int word) {
-        if (STREAM) return word >= unit * kWords && word < (unit + 1) * kWords ? word - unit * kWords : -1;
-        return word % units == unit ? word / units : -1;
+    // the word that the unit's place i stands for, and back (-1: another unit's)
+    static __device__ __forceinline__ int word(int unit, int units, int i) {
+        return STREAM ? unit * kWords + i : unit + units * i;
     }
+    static __device__ __forceinline__ int place(int unit, int units, int word) {
+        const int turn = STREAM ? word / kWords : word / units;
+        if (STREAM) return turn == unit ? word % kWords : -1;
+        return word - turn * units == unit ? turn : -1;
+    }
+    static __host__ int units(int V) { return (V + 32 * kWords - 1) / (32 * kWords); }
 };
 
 template <bool STREAM>
@@ -76,17 +81,6 @@ struct GroupShared {
     uint8_t flags[kList];
 };
 enum { kSeen = 1, kDrafted = 2, kBiased = 4 };
-
-// The sequence that holds item `at`, from b on, by each warp.
-__device__ __forceinline__ int advance(const Rows &rw, int b, int64_t at, int per_row) {
-    for (;;) {
-        const int j = min(b + static_cast<int>(threadIdx.x & 31), rw.B - 1);
-        const uint32_t hit = __ballot_sync(0xffffffffu, at < static_cast<int64_t>(rw.first_row(j + 1)) * per_row);
-        if (hit) return min(b + __ffs(hit) - 1, rw.B - 1);
-        b += 32;
-        if (b >= rw.B) return rw.B - 1;  // not reached: `at` lies before the last row's end
-    }
-}
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const char *row, int col) {
@@ -102,66 +96,98 @@ __device__ __forceinline__ void store_logit(char *row, int col, float z) {
 // -inf in the columns of a vector whose bit is clear.
 template <int DT>
 __device__ __forceinline__ void mask_vec(uint4 &q, uint32_t allowed) {
-    uint32_t *w = reinterpret_cast<uint32_t *>(&q);
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t keep;
-        if (DT == SPEC_F32) keep = (allowed >> i) & 1 ? 0xffffffffu : 0u;
-        else keep = ((allowed >> (2 * i)) & 1 ? 0xffffu : 0u) | ((allowed >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+        if (DT == SPEC_F32) keep = 0u - ((allowed >> i) & 1u);
+        else keep = (((allowed >> (2 * i)) & 1u) | ((allowed << (15 - 2 * i)) & 0x10000u)) * 0xffffu;  // a bit per half
         w[i] = (w[i] & keep) | (Elem<DT>::kNegInfWord & ~keep);
     }
+    q = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The mask of a row: its number, -1 for none, -2 where it names none there is.
+__device__ __forceinline__ int mask_of(const Process &ps, int row) {
+    if (!ps.mask) return -1;
+    const int m = ps.mask_rows ? __ldg(ps.mask_rows + row) : row;
+    return m < -1 || m >= ps.M ? -2 : m;
 }
 
 // The stream over rows row0 + i0 .. row0 + i1 - 1 of a CTA's columns: a copy with
 // the masks applied; in place only what a mask takes away.
 template <int DT>
-__device__ __forceinline__ void stream_rows(const char *logits, char *out, const Process &ps, int V, int64_t row0, int i0,
-                                            int i1, int c0, bool inplace) {
+__device__ __forceinline__ void stream_rows(const char *logits, char *out, const Process &ps, int V, int row0, int i0,
+                                            int i1, int unit, int units, bool inplace) {
+    using G = Group<true>;
     constexpr int kPer = Elem<DT>::kPerVec;
     constexpr int kVecs = 32 / kPer;                // a thread's vectors of one row
     constexpr int kRows = DT == SPEC_BF16 ? 2 : 1;  // rows in flight
     constexpr uint32_t kAll = (1u << kPer) - 1;
     const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
-    const int W = (V + 31) / 32;
-    const int c = c0 + static_cast<int>(threadIdx.x) * kPer;  // + j * kThreads * kPer
-    for (int i = i0; i < i1; i += kRows) {
+    int col[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+        const int x = j * kThreads + static_cast<int>(threadIdx.x);
+        col[j] = G::word(unit, units, x / (32 / kPer)) * 32 + x % (32 / kPer) * kPer;
+    }
+    const char *src = logits + (static_cast<int64_t>(row0) + i0) * row_bytes;
+    char *dst = out + (static_cast<int64_t>(row0) + i0) * row_bytes;
+    if (!ps.mask) {
+        for (int i = i0; i < i1; i += kRows, src += kRows * row_bytes, dst += kRows * row_bytes) {
+            uint4 q[kRows][kVecs];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+                    if (col[j] < V && (u == 0 || i + u < i1))
+                        q[u][j] = *reinterpret_cast<const uint4 *>(src + u * row_bytes + static_cast<int64_t>(col[j]) * Elem<DT>::kBytes);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+                    if (col[j] < V && (u == 0 || i + u < i1))
+                        *reinterpret_cast<uint4 *>(dst + u * row_bytes + static_cast<int64_t>(col[j]) * Elem<DT>::kBytes) = q[u][j];
+        }
+        return;
+    }
+    const int64_t mask_bytes = static_cast<int64_t>((V + 31) / 32) * 4;
+    const char *masks = reinterpret_cast<const char *>(ps.mask);
+    for (int i = i0; i < i1; i += kRows, src += kRows * row_bytes, dst += kRows * row_bytes) {
         uint32_t allowed[kRows][kVecs];
         uint4 q[kRows][kVecs];
+        int m[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) m[u] = i + u < i1 ? mask_of(ps, row0 + i + u) : -3;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                allowed[u][j] = m[u] == -1 ? kAll : 0u;
+                if (m[u] >= 0 && col[j] < V)
+                    allowed[u][j] = static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned char *>(masks + m[u] * mask_bytes + (col[j] >> 3)))) >>
+                                        (col[j] & 7) & kAll;
+            }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                // nothing of the input is needed where nothing is allowed
+                constexpr uint32_t f = Elem<DT>::kNegInfWord, x = kNanWord<DT>;
+                q[u][j] = m[u] == -2 ? make_uint4(x, x, x, x) : make_uint4(f, f, f, f);
+                if (allowed[u][j] != 0 && !(inplace && allowed[u][j] == kAll) && col[j] < V)
+                    q[u][j] = *reinterpret_cast<const uint4 *>(src + u * row_bytes + static_cast<int64_t>(col[j]) * Elem<DT>::kBytes);
+            }
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            int m = -1;
-            if (ps.mask && i + u < i1) {
-                m = ps.mask_rows ? __ldg(ps.mask_rows + row0 + i + u) : static_cast<int>(row0 + i + u);
-                if (m >= ps.M) m = -1;  // (an error: the row becomes NaN later)
-            }
+            if (m[u] == -3) continue;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const int col = c + j * kThreads * kPer;
-                allowed[u][j] = kAll;
-                if (m >= 0 && col < V)
-                    allowed[u][j] = bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7) & kAll;
+                if (col[j] >= V || (inplace && allowed[u][j] == kAll)) continue;
+                if (m[u] >= 0 && allowed[u][j] != kAll) mask_vec<DT>(q[u][j], allowed[u][j]);
+                *reinterpret_cast<uint4 *>(dst + u * row_bytes + static_cast<int64_t>(col[j]) * Elem<DT>::kBytes) = q[u][j];
             }
         }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u)
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int col = c + j * kThreads * kPer;
-                const bool need = allowed[u][j] != 0 && !(inplace && allowed[u][j] == kAll);
-                q[u][j] = make_uint4(0, 0, 0, 0);
-                if (need && col < V && i + u < i1)
-                    q[u][j] = *reinterpret_cast<const uint4 *>(logits + (row0 + i + u) * row_bytes +
-                                                               static_cast<int64_t>(col) * Elem<DT>::kBytes);
-            }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u)
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int col = c + j * kThreads * kPer;
-                if (col >= V || i + u >= i1 || (inplace && allowed[u][j] == kAll)) continue;
-                if (allowed[u][j] != kAll) mask_vec<DT>(q[u][j], allowed[u][j]);
-                *reinterpret_cast<uint4 *>(out + (row0 + i + u) * row_bytes + static_cast<int64_t>(col) * Elem<DT>::kBytes) = q[u][j];
-            }
     }
 }
 
@@ -181,15 +207,15 @@ __device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0,
         }
 }
 
-// A group of threads takes an even share of the rows' units of columns in the
-// order (sequence, unit, row), so that what depends on the sequence and the
-// columns alone (its seen tokens, their counts, its biases) is read once for
-// the unit's rows.
+// A group takes one unit of one sequence's columns, for all its rows or an even
+// part of them, so that what depends on the sequence and the columns alone
+// (its seen tokens, their counts, its biases) is read once.  CTAs in the order
+// (sequence, unit): the ones that run at a time stream through one window of
+// memory.
 template <int DT, bool STREAM>
 __global__ void __launch_bounds__(kThreads, kPerSm)
-    process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int units) {
+    process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int units, int parts) {
     using G = Group<STREAM>;
-    __shared__ int s_seq;
     __shared__ GroupShared<STREAM> s_group[G::kCount];
     const int me = G::thread(), lane = threadIdx.x & 31;
     GroupShared<STREAM> &sm = s_group[G::self()];
@@ -198,28 +224,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     const int W = (V + 31) / 32;
     const bool pen = ps.counts != nullptr, tree = rw.mode == SPEC_ROWS_TREE;
 
-    int64_t total;
-    const int64_t items = static_cast<int64_t>(rw.first_row(rw.B)) * units;
     const int64_t groups = static_cast<int64_t>(gridDim.x) * G::kCount;
     const int64_t self = static_cast<int64_t>(blockIdx.x) * G::kCount + G::self();
-    if (!check_rows(rw, pen, items * blockIdx.x / gridDim.x, units, &s_seq, &total)) {
+    if (!check_rows(rw, pen)) {
         // the call fails: every row is NaN
         for (int64_t u = self; u < static_cast<int64_t>(rw.R) * units; u += groups)
             nan_rows<DT, STREAM>(out, V, u / units, 0, 1, static_cast<int>(u % units), units);
         return;
     }
-    int64_t at = items * self / groups;
-    const int64_t end = items * (self + 1) / groups;
-    if (at >= end) return;
-    int b = advance(rw, s_seq, at, units);
-
-    for (;;) {
+    const int64_t pair = self / parts;
+    const int part = static_cast<int>(self - pair * parts), b = static_cast<int>(pair / units);
+    const int unit = static_cast<int>(pair - static_cast<int64_t>(b) * units);
+    if (b >= rw.B) return;
+    {
         const int o0 = __ldg(rw.offsets + b), o1 = __ldg(rw.offsets + b + 1);
         const int k = o1 - o0;  // drafted tokens, or tree nodes
         const int row0 = rw.first_row(b, o0), n = rw.first_row(b + 1, o1) - row0;
-        const int64_t rel = at - static_cast<int64_t>(row0) * units;
-        const int unit = static_cast<int>(rel / n), i0 = static_cast<int>(rel - static_cast<int64_t>(unit) * n);
-        const int i1 = static_cast<int>(min(static_cast<int64_t>(n), i0 + (end - at)));
+        const int i0 = n * part / parts, i1 = n * (part + 1) / parts;
+        if (i0 == i1) return;
 
         // --- what the sequence and the columns say: asked for before the stream, used after it
         Penalty p{1.0f, 0.0f, 0.0f};
@@ -258,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 e1 = e0 = 0;
             }
         }
-        if (STREAM) stream_rows<DT>(logits, out, ps, V, row0, i0, i1, unit * G::kWords * 32, inplace);
+        if (STREAM) stream_rows<DT>(logits, out, ps, V, row0, i0, i1, unit, units, inplace);
 
         // --- the unit's columns that anything applies to
 #pragma unroll
@@ -371,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                         for (int u = 0; u < kRows; ++u) {
                             go[u] = i + u < i1;
                             if (go[u] && ps.mask) {
-                                const int m = ps.mask_rows ? __ldg(ps.mask_rows + row0 + i + u) : row0 + i + u;
-                                go[u] = m < 0 || m >= ps.M || ((bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7)) & 1);
+                                const int m = mask_of(ps, row0 + i + u);
+                                go[u] = m == -1 || (m >= 0 && ((bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7)) & 1));
                             }
                         }
 #pragma unroll
@@ -393,20 +415,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                     }
                 }
             }
-            if (ps.mask_rows)  // rows that name no mask there is
-                for (int i = i0; i < i1; ++i) {
-                    const int m = __ldg(ps.mask_rows + row0 + i);
-                    if (m >= -1 && m < ps.M) continue;
-                    G::sync();
-                    nan_rows<DT, STREAM>(out, V, row0, i, i + 1, unit, units);
-                }
         }
-
-        // --- the next unit
-        at += i1 - i0;
-        if (at >= end) return;
-        G::sync();
-        if (at >= static_cast<int64_t>(row0 + n) * units) b = advance(rw, b + 1, at, units);
     }
 }
 
@@ -418,9 +427,7 @@ constexpr int kUpdateThreads = 256;
 __global__ void __launch_bounds__(kUpdateThreads)
     update_kernel(int32_t *counts, int32_t *seen, int S, int V, const int32_t *__restrict__ slots, Rows rw,
                   const int32_t *__restrict__ out_tokens, const int32_t *__restrict__ num_accepted) {
-    __shared__ int s_seq;
-    int64_t total;
-    if (!check_rows(rw, false, 0, 1, &s_seq, &total)) return;
+    if (!check_rows(rw, false)) return;
     const int b = blockIdx.x * (kUpdateThreads / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
     if (b >= rw.B) return;
     const int o0 = __ldg(rw.offsets + b), k = __ldg(rw.offsets + b + 1) - o0;
@@ -485,11 +492,14 @@ template <int DT, bool STREAM>
 int launch_process(const void *logits, void *out, const Rows &rw, const Process &ps, int V, int sms,
                    cudaStream_t stream) {
     using G = Group<STREAM>;
-    const int words = (V + 31) / 32, units = (words + G::kWords - 1) / G::kWords;
-    const int64_t ctas = (static_cast<int64_t>(rw.R) * units + G::kCount - 1) / G::kCount;
-    const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(sms) * kPerSm));
-    process_kernel<DT, STREAM><<<grid, kThreads, 0, stream>>>(static_cast<const char *>(logits), static_cast<char *>(out),
-                                                              rw, ps, V, units);
+    const int units = G::units(V);
+    const int64_t pairs = static_cast<int64_t>(rw.B) * units;
+    // few sequences: their rows are split until every SM has its CTAs
+    const int64_t room = static_cast<int64_t>(sms) * kPerSm * G::kCount;
+    const int parts = static_cast<int>(std::clamp<int64_t>(room / pairs, 1, std::max(1, rw.R / rw.B)));
+    const int64_t ctas = (pairs * parts + G::kCount - 1) / G::kCount;
+    process_kernel<DT, STREAM><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(
+        static_cast<const char *>(logits), static_cast<char *>(out), rw, ps, V, units, parts);
     return specv::cuda_ok(cudaGetLastError(), "launch process_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

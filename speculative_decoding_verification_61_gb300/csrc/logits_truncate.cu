@@ -595,8 +595,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t rows_all = rw.first_row(rw.B, oB);
     int64_t r = rows_all * blockIdx.x / gridDim.x;
     const int64_t end = rows_all * (blockIdx.x + 1) / gridDim.x;
-    int64_t total;
-    if (!check_rows(rw, false, r, 1, &sm.seq, &total)) {
+    if (!check_rows(rw, r, &sm.seq)) {
         fill_nan<DT>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                      static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
@@ -804,8 +803,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t rows_all = rw.first_row(rw.B, oB);
     int64_t r = rows_all * blockIdx.x / gridDim.x;
     const int64_t end = rows_all * (blockIdx.x + 1) / gridDim.x;
-    int64_t total;
-    if (!check_rows(rw, false, r, 1, &all.seq, &total)) {
+    if (!check_rows(rw, r, &all.seq)) {
         fill_nan<SPEC_BF16>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                             static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
