@@ -44,6 +44,8 @@ extern thread_local char g_last_error[kLastErrorBytes];
 bool cuda_ok(cudaError_t e, const char *what);
 
 bool make_geometry(int V, int dtype, Geometry *g);
+// Shared-memory attributes of the logit kernels, for the current device.
+bool set_logits_attrs();
 // Per-device state of the chain kernels (attributes set once per device).
 DeviceState *device_state(int *dev_out);
 

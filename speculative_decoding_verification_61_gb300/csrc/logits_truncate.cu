@@ -51,6 +51,42 @@ __device__ __forceinline__ uint64_t place_of(uint32_t key, int index) {
 }
 
 // ------------------------------------------------------------------- weights
+// 2^(j/64) in two fp32 terms, j = 0..63, rounded from 60 digits.
+__constant__ float2 kExp2Table[64] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.02c9a40000000p+0f, -0x1.887fa00000000p-28f},
+    {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0874520000000p+0f, -0x1.e2990e0000000p-26f},
+    {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.0e3ec40000000p+0f, -0x1.a585cc0000000p-25f},
+    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.1429aa0000000p+0f, 0x1.d525bc0000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1a35be0000000p+0f, 0x1.6df96e0000000p-25f},
+    {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, {0x1.2063b80000000p+0f, 0x1.0c519a0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.26b4560000000p+0f, 0x1.789f380000000p-26f},
+    {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.2d285a0000000p+0f, 0x1.b900c20000000p-26f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.33c08c0000000p+0f, -0x1.b37d200000000p-25f},
+    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3a7db40000000p+0f, -0x1.634c020000000p-25f},
+    {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.4160a20000000p+0f, 0x1.f72e2a0000000p-28f},
+    {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f}, {0x1.486a2c0000000p+0f, -0x1.47d8660000000p-25f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.4f9b280000000p+0f, -0x1.2c5a6c0000000p-25f},
+    {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.56f4740000000p+0f, -0x1.295b040000000p-25f},
+    {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.5e76f20000000p+0f, -0x1.4a5bd60000000p-25f},
+    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6623880000000p+0f, 0x1.2a91120000000p-27f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.6dfb240000000p+0f, -0x1.cd72e80000000p-27f},
+    {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, {0x1.75feb60000000p+0f, -0x1.37b3060000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.7e2f340000000p+0f, -0x1.2616340000000p-25f},
+    {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.868d9a0000000p+0f, -0x1.2edb440000000p-26f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.8f1aea0000000p+0f, -0x1.baa2320000000p-26f},
+    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.97d82a0000000p+0f, -0x1.0d8d840000000p-31f},
+    {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a0c6680000000p+0f, -0x1.2886a60000000p-26f},
+    {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f}, {0x1.a9e6b60000000p+0f, -0x1.50c0480000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b33a2c0000000p+0f, -0x1.ec3a820000000p-26f},
+    {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.bcc1ea0000000p+0f, -0x1.f687c60000000p-25f},
+    {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.c67f120000000p+0f, 0x1.cafa2a0000000p-25f},
+    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d072d40000000p+0f, 0x1.40f1300000000p-25f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.da9e600000000p+0f, 0x1.ed99420000000p-27f},
+    {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.e502ee0000000p+0f, 0x1.e2cffe0000000p-26f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.efa1be0000000p+0f, 0x1.cc2b440000000p-25f},
+    {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f},
+};
+
 // exp((z - zmax) / T) as a 64-bit fixed-point number with `frac` bits behind
 // the point.  2^x, x = (z - zmax) log2(e) / T, by the split x = n + j / 64 + r,
 // |r| <= 1/128: a table of 2^(j/64) in two fp32 terms, and the Taylor
@@ -137,7 +173,6 @@ struct RowConstants {
 };
 
 struct Shared {
-    int seq;
     float2 table[64];
     uint32_t count[kBins], lo[kBins], hi[kBins];
     uint64_t list[kList];
@@ -480,10 +515,16 @@ __device__ __forceinline__ uint64_t mass_target(float p, uint64_t Z) {
     return __double2ull_ru(static_cast<double>(p) * static_cast<double>(Z));
 }
 __device__ __forceinline__ void fill_table(float2 *table) {
-    if (threadIdx.x < 64) {
-        const double t = exp2(threadIdx.x / 64.0);
-        const float h = static_cast<float>(t);
-        table[threadIdx.x] = make_float2(h, static_cast<float>(t - h));
+    if (threadIdx.x < 64) table[threadIdx.x] = kExp2Table[threadIdx.x];
+}
+
+// The sequence of row r, which is at or behind sequence b, by each warp.
+__device__ __forceinline__ int sequence_of(const Rows &rw, int b, int64_t r) {
+    for (;; b += 32) {
+        const int j = min(b + static_cast<int>(threadIdx.x & 31), rw.B - 1);
+        const uint32_t hit = __ballot_sync(0xffffffffu, r < rw.first_row(j + 1));
+        if (hit) return min(b + __ffs(hit) - 1, rw.B - 1);
+        if (b + 32 >= rw.B) return rw.B - 1;  // not reached: r lies before the last row's end
     }
 }
 
@@ -581,7 +622,7 @@ __device__ __forceinline__ void fill_nan(uint4 *dst, int64_t vecs, int64_t first
     for (int64_t v = first; v < vecs; v += step) dst[v] = make_uint4(kNan, kNan, kNan, kNan);
 }
 
-// A CTA takes an even share of the rows; rows of any kind.
+// Rows of any kind, a CTA per row at a time, neighbouring rows at the same time.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 2)
     truncate_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
@@ -593,17 +634,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     fill_table(sm.table);
     const int oB = __ldg(rw.offsets + rw.B);
     const int64_t rows_all = rw.first_row(rw.B, oB);
-    int64_t r = rows_all * blockIdx.x / gridDim.x;
-    const int64_t end = rows_all * (blockIdx.x + 1) / gridDim.x;
-    if (!check_rows(rw, r, &sm.seq)) {
+    int64_t r = blockIdx.x;
+    if (!check_rows(rw, false)) {
         fill_nan<DT>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                      static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
     }
-    if (r >= end) return;
-    int b = sm.seq;
-    for (; r < end; ++r) {
-        while (r >= rw.first_row(b + 1)) ++b;
+    int b = 0;
+    for (; r < rows_all; r += gridDim.x) {
+        b = sequence_of(rw, b, r);
         const char *row = logits + r * row_bytes;
         uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
         const Settings s = load_settings(tr, b, V);
@@ -619,36 +658,46 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ------------------------------------------------------------ bf16, in two passes
 // bf16 rows have few values, so a histogram with one bin per value settles
 // everything: counts are exact, and a weight is computed once per value
-// instead of once per token.  Bins in falling order: z in (2^16, 2^-24], 0,
-// [-2^-24, -2^16): 39 + 1 octaves of 128 values a side, 40 KB.  Values at or
-// below -2^16 (masked logits) have no weight and are not counted; rows with
-// other values outside the bins, with NaN or +inf, or whose border is not in
-// the bins, take cut_of_row.
-constexpr int kTiny = (127 - 24) << 7;   // magnitude bits of 2^-24
+// instead of once per token.  A bin per value of magnitude 2^-48 .. 2^16, 8192
+// a side, 64 KB; zeros have a counter of their own.  Values at or below -2^16
+// (masked logits) have no weight and are not counted.  Rows with other values
+// outside the bins, with NaN or +inf, or whose border is not in the bins, take
+// cut_of_row.
+constexpr int kTiny = (127 - 48) << 7;   // magnitude bits of 2^-48
 constexpr int kHuge = (127 + 16) << 7;   // of 2^16
 constexpr int kSide = kHuge - kTiny;     // values a side
-constexpr int kZeroBin = kSide;
-constexpr int kValues = 2 * kSide + 1;
-constexpr int kSegs = (kValues + 31) / 32;
+static_assert(kSide == 1 << 13, "a bin is 13 magnitude bits and the sign");
+// The order: positive values falling, zero, negative values falling, in
+// segments of 32 places.
+constexpr int kSideSegs = kSide / 32;
+constexpr int kSegs = 2 * kSideSegs + 1;
 constexpr int kSegsPerLane = (kSegs + 31) / 32;
+constexpr int kPlaces = kSegs * 32;
 constexpr int kGroupCols = 256;           // a warp's 32 vectors
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxFastV = kGroupCols * kMaxGroups;
 constexpr int kAhead = 4;                 // vectors in flight per thread
 
 struct FastShared {
-    uint32_t hist[kSegs * 32];
+    uint32_t hist[2 * kSide];  // bin: the sign above 13 bits of (magnitude - kTiny)
+    uint32_t zeros;
     uint32_t seg_count[kSegs];
     uint64_t seg_mass[kSegs];
-    uint16_t group_max[kMaxGroups];   // order key of each group's largest value
-    int first;                        // the largest value's bin
-    // the border: tokens above `value` stay, `take` of its ties do
-    int value_bin, take, ties;
+    uint16_t group_max[kMaxGroups];  // order key of each group's largest value
+    int first;                       // the largest value's place
+    // the border: tokens above its value stay, `take` of its ties do
+    int place, take, ties;
     int cut_group, cut_index;
     bool elsewhere;  // not in the bins
 
     // how often each group holds the border value: written once the bins are done with
     __device__ uint16_t *group_ties() { return reinterpret_cast<uint16_t *>(hist); }
+    // tokens at a place of segment seg, lane `lane`
+    __device__ __forceinline__ uint32_t at(int seg, int lane) const {
+        if (seg < kSideSegs) return hist[kSide - 1 - (seg * 32 + lane)];
+        if (seg == kSideSegs) return lane == 0 ? zeros : 0;
+        return hist[kSide + (seg - kSideSegs - 1) * 32 + lane];
+    }
 };
 
 struct BothShared {
@@ -659,113 +708,131 @@ struct BothShared {
     // apart from the union: kept over the rows
     float2 table[64];
     RowConstants row;
-    int seq;
 };
 
-__device__ __forceinline__ float bin_value(int bin) {
-    const uint32_t u = bin < kZeroBin ? kHuge - 1 - bin : bin == kZeroBin ? 0 : 0x8000 | (bin - kZeroBin - 1 + kTiny);
+__device__ __forceinline__ float place_value(int place) {
+    const int neg = place - (kSideSegs + 1) * 32;
+    const uint32_t u = place < kSide ? kHuge - 1 - place : neg < 0 ? 0 : 0x8000 | (neg + kTiny);
     return __uint_as_float(u << 16);
 }
 // Unsigned 16-bit key in the order of the values (-0 below +0).
 __device__ __forceinline__ uint32_t key16(uint32_t u) { return u ^ (u & 0x8000u ? 0xffffu : 0x8000u); }
 
 // t tokens' weight: the product before the one rounding.
-__device__ __forceinline__ uint64_t weight_times(const Weights &w, float z, uint32_t t) {
-    int e;
-    const uint64_t m = weight_mantissa(w, z, &e);
-    const int shift = -(e + w.frac);
-    if (m == 0 || t == 0 || shift > 100) return 0;
-    uint64_t lo = m * t, hi = __umul64hi(m, t);
-    if (shift >= 64) return hi >> (shift - 64);
-    lo += 1ull << (shift - 1);
-    hi += lo < (1ull << (shift - 1));
-    return lo >> shift | (shift == 0 ? 0 : hi << (64 - shift));
-}
+struct TokenWeight {
+    uint64_t mantissa;
+    int shift;
+    __device__ __forceinline__ TokenWeight(const Weights &w, float z) {
+        int e;
+        mantissa = weight_mantissa(w, z, &e);
+        shift = -(e + w.frac);  // at least 1: frac <= 47
+    }
+    __device__ __forceinline__ uint64_t times(uint32_t t) const {
+        if (mantissa == 0 || t == 0 || shift > 100) return 0;
+        uint64_t lo = mantissa * t, hi = __umul64hi(mantissa, t);
+        if (shift >= 64) return hi >> (shift - 64);
+        const uint64_t half = 1ull << (shift - 1);
+        lo += half;
+        hi += lo < half;
+        return lo >> shift | hi << (64 - shift);
+    }
+};
 
-// One token's bits into the histogram; what has no bin sets *odd, except
-// values at or below -2^16.
-__device__ __forceinline__ void count_value(FastShared &sm, uint32_t u, uint32_t *odd) {
-    const uint32_t m = u & 0x7fffu;
-    if (m - kTiny < static_cast<uint32_t>(kSide)) {
-        atomicAdd(&sm.hist[u & 0x8000u ? m + (kZeroBin + 1 - kTiny) : kHuge - 1 - m], 1u);
-    } else if (m == 0) {
-        atomicAdd(&sm.hist[kZeroBin], 1u);
-    } else if (!(u >= (0x8000u | kHuge) && u <= 0xff80u)) {
-        *odd = 1;
+// A vector's 8 values into the histogram.
+__device__ __forceinline__ void count_values(FastShared &sm, const uint4 &q, uint32_t *odd) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t t[4], outside = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // both halves at once; a half below kTiny borrows from its neighbour, and is seen to be outside itself
+        t[i] = (w[i] & 0x7fff7fffu) - kTiny * 0x10001u;
+        outside |= t[i];
+    }
+    if ((outside & 0xe000e000u) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = t[i] | ((w[i] >> 2) & 0x20002000u);
+            atomicAdd(&sm.hist[c & 0xffffu], 1u);
+            atomicAdd(&sm.hist[c >> 16], 1u);
+        }
+        return;
+    }
+    if ((w[0] & w[1] & w[2] & w[3]) == 0xff80ff80u && (w[0] | w[1] | w[2] | w[3]) == 0xff80ff80u) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu, m = u & 0x7fffu;
+        if (m - kTiny < static_cast<uint32_t>(kSide)) atomicAdd(&sm.hist[(m - kTiny) | (u & 0x8000u) >> 2], 1u);
+        else if (m == 0) atomicAdd(&sm.zeros, 1u);
+        else if (!(u >= (0x8000u | kHuge) && u <= 0xff80u)) *odd = 1;
     }
 }
 
-// Where the goal is reached in the histogram, by one warp: the bin, and what
-// lies above it.  False if the bins end before.
-__device__ __forceinline__ bool locate(FastShared &sm, const Weights &w, const Goal &goal, bool mass, int *bin,
-                                       uint32_t *above_count, uint64_t *above_mass) {
+// The first lane whose running sums reach the goal, and what lies above it; -1: none.
+__device__ __forceinline__ int first_reached(const Goal &goal, uint32_t n, uint64_t mass, uint32_t *c, uint64_t *m) {
     const int lane = threadIdx.x & 31;
-    const int s0 = lane * kSegsPerLane, s1 = min(kSegs, s0 + kSegsPerLane);
-    uint32_t c = 0;
-    uint64_t m = 0;
-    for (int s = s0; s < s1; ++s) {
-        c += sm.seg_count[s];
-        if (mass) m += sm.seg_mass[s];
-    }
-    const uint32_t c0 = c;
-    const uint64_t m0 = m;
+    uint32_t cs = n;
+    uint64_t ms = mass;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
-        const uint64_t mm = __shfl_up_sync(0xffffffffu, m, off);
+        const uint32_t cc = __shfl_up_sync(0xffffffffu, cs, off);
+        const uint64_t mm = __shfl_up_sync(0xffffffffu, ms, off);
         if (lane >= off) {
-            c += cc;
-            m += mm;
+            cs += cc;
+            ms += mm;
         }
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, goal.reached(c, m));
-    if (!hit) return false;
-    const int owner = __ffs(hit) - 1;
-    c -= c0;
-    m -= m0;
-    int seg = s0;
-    if (lane == owner) {
-        for (; seg < s1 - 1; ++seg) {
-            const uint32_t cs = sm.seg_count[seg];
-            const uint64_t ms = mass ? sm.seg_mass[seg] : 0;
-            if (goal.reached(c + cs, m + ms)) break;
-            c += cs;
-            m += ms;
-        }
-    }
-    seg = __shfl_sync(0xffffffffu, seg, owner);
-    c = __shfl_sync(0xffffffffu, c, owner);
-    m = __shfl_sync(0xffffffffu, m, owner);
-    const int my = seg * 32 + lane;
-    const uint32_t n = sm.hist[my];
-    const uint64_t mine = mass && n ? weight_times(w, bin_value(my), n) : 0;
-    uint32_t ci = n;
-    uint64_t mi = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t cc = __shfl_up_sync(0xffffffffu, ci, off);
-        const uint64_t mm = __shfl_up_sync(0xffffffffu, mi, off);
-        if (lane >= off) {
-            ci += cc;
-            mi += mm;
-        }
-    }
-    const int at = __ffs(__ballot_sync(0xffffffffu, goal.reached(c + ci, m + mi))) - 1;
-    *bin = seg * 32 + at;
-    *above_count = __shfl_sync(0xffffffffu, c + ci - n, at);
-    *above_mass = __shfl_sync(0xffffffffu, m + mi - mine, at);
-    return true;
+    const uint32_t hit = __ballot_sync(0xffffffffu, goal.reached(*c + cs, *m + ms));
+    if (!hit) return -1;
+    const int at = __ffs(hit) - 1;
+    *c += __shfl_sync(0xffffffffu, cs - n, at);
+    *m += __shfl_sync(0xffffffffu, ms - mass, at);
+    return at;
 }
 
-// The fewest ties whose weight reaches the target.
-__device__ __forceinline__ uint32_t ties_for(const Weights &w, float z, uint32_t n, uint64_t above, uint64_t target) {
-    uint32_t lo = 1, hi = n;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (above + weight_times(w, z, mid) >= target) hi = mid;
-        else lo = mid + 1;
+// Where the goal is reached in the histogram, by one warp: the place, and what
+// lies above it; -1 if the bins end before.
+__device__ __forceinline__ int locate(FastShared &sm, const Weights &w, const Goal &goal, bool mass, uint32_t *above_count,
+                                      uint64_t *above_mass) {
+    const int lane = threadIdx.x & 31;
+    uint32_t c = 0, n = 0;
+    uint64_t m = 0, nm = 0;
+    const int s0 = lane * kSegsPerLane;
+#pragma unroll
+    for (int i = 0; i < kSegsPerLane; ++i) {
+        if (s0 + i >= kSegs) break;
+        n += sm.seg_count[s0 + i];
+        if (mass) nm += sm.seg_mass[s0 + i];
     }
-    return lo;
+    const int owner = first_reached(goal, n, nm, &c, &m);
+    if (owner < 0) return -1;
+    const int s = owner * kSegsPerLane + lane;
+    const bool in = lane < kSegsPerLane && s < kSegs;
+    const int seg = owner * kSegsPerLane + first_reached(goal, in ? sm.seg_count[s] : 0, in && mass ? sm.seg_mass[s] : 0, &c, &m);
+    n = sm.at(seg, lane);
+    nm = mass && n ? TokenWeight(w, place_value(seg * 32 + lane)).times(n) : 0;
+    const int at = first_reached(goal, n, nm, &c, &m);
+    *above_count = c;
+    *above_mass = m;
+    return seg * 32 + at;
+}
+
+// The fewest of n ties whose weight reaches the target, by one warp.
+__device__ __forceinline__ uint32_t ties_for(const TokenWeight &w, uint32_t n, uint64_t above, uint64_t target) {
+    uint32_t lo = 1, hi = n;  // the answer lies in [lo, hi]
+    while (lo < hi) {
+        const uint32_t step = (hi - lo + 31) / 32;
+        const uint32_t t = min(lo + step * (threadIdx.x & 31), hi);
+        const uint32_t hit = __ballot_sync(0xffffffffu, above + w.times(t) >= target);
+        if (!hit) {
+            lo = min(lo + step * 31, hi) + 1;  // (hi reaches it)
+            continue;
+        }
+        const int at = __ffs(hit) - 1;
+        hi = min(lo + step * at, hi);
+        if (at > 0) lo = min(lo + step * (at - 1) + 1, hi);
+        else break;
+    }
+    return hi;
 }
 
 // A group's 32 vectors of 8: groups are counted in column order, group g by warp g % kWarps.
@@ -774,10 +841,11 @@ __device__ __forceinline__ void for_groups(int groups, F &&f) {
     for (int g = threadIdx.x >> 5; g < groups; g += kWarps) f(g, g * 32 + static_cast<int>(threadIdx.x & 31));
 }
 
-__device__ __forceinline__ uint32_t max_word(const uint4 &q) {
+// Order key of a vector's largest value.
+__device__ __forceinline__ uint32_t max_key(const uint4 &q) {
     const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&q);
     const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return *reinterpret_cast<const uint32_t *>(&m);
+    return key16(__bfloat16_as_ushort(__hmax(__low2bfloat16(m), __high2bfloat16(m))));
 }
 
 // 0xffff in the halves of a that are greater than (or equal to) b's
@@ -801,17 +869,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     fill_table(all.table);
     const int oB = __ldg(rw.offsets + rw.B);
     const int64_t rows_all = rw.first_row(rw.B, oB);
-    int64_t r = rows_all * blockIdx.x / gridDim.x;
-    const int64_t end = rows_all * (blockIdx.x + 1) / gridDim.x;
-    if (!check_rows(rw, r, &all.seq)) {
+    int64_t r = blockIdx.x;
+    if (!check_rows(rw, false)) {
         fill_nan<SPEC_BF16>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                             static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
     }
-    if (r >= end) return;
-    int b = all.seq;
-    for (; r < end; ++r) {
-        while (r >= rw.first_row(b + 1)) ++b;
+    int b = 0;
+    for (; r < rows_all; r += gridDim.x) {
+        b = sequence_of(rw, b, r);
         const uint4 *row = reinterpret_cast<const uint4 *>(logits + r * row_bytes);
         uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
         const Settings s = load_settings(tr, b, V);
@@ -827,9 +893,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const bool mass = s.p < 1.0f, counted = mass || s.k > 0;
         // --- one pass over the row: the histogram, the groups' largest values
         __syncthreads();  // the last row is done with the shared arrays
-        for (int i = tid; i < kSegs * 32; i += kThreads) sm.hist[i] = 0;
+        for (int i = tid; i < 2 * kSide / 4; i += kThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
         if (tid == 0) {
-            sm.first = kSegs * 32;
+            sm.zeros = 0;
+            sm.first = kPlaces;
             sm.elsewhere = false;
         }
         __syncthreads();
@@ -844,16 +911,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (g0 + u * kWarps >= groups) break;
-                const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-                {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        count_value(sm, w[i] & 0xffffu, &odd);
-                        count_value(sm, w[i] >> 16, &odd);
-                    }
-                }
-                const uint32_t m = max_word(q[u]);
-                const uint32_t key = __reduce_max_sync(0xffffffffu, max(key16(m & 0xffffu), key16(m >> 16)));
+                count_values(sm, q[u], &odd);
+                const uint32_t key = __reduce_max_sync(0xffffffffu, max_key(q[u]));
                 if (lane == 0) sm.group_max[g0 + u * kWarps] = static_cast<uint16_t>(key);
             }
         }
@@ -861,9 +920,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         float zmax = 0.0f;
         if (!slow) {
             // --- the bins' sums by segments of 32
-            int first = kSegs * 32;
+            int first = kPlaces;
             for (int g = warp; g < kSegs; g += kWarps) {
-                const uint32_t n = sm.hist[g * 32 + lane];
+                const uint32_t n = sm.at(g, lane);
                 const uint32_t any = __ballot_sync(0xffffffffu, n > 0);
                 if (any) first = min(first, g * 32 + __ffs(any) - 1);
                 const uint32_t sum = __reduce_add_sync(0xffffffffu, n);
@@ -872,8 +931,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (lane == 0) atomicMin(&sm.first, first);
             __syncthreads();
             first = sm.first;
-            slow = first == kSegs * 32;
-            if (!slow) zmax = bin_value(first);
+            slow = first == kPlaces;
+            if (!slow) zmax = place_value(first);
         }
         // (values at or below -2^16 have no weight, and min-p excludes them)
         if (!slow && !((-65536.0f - zmax) * specv::temp_scale(s.T) < -150.0f)) slow = true;
@@ -886,8 +945,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int g = warp; g < kSegs; g += kWarps) {
                     uint64_t m = 0;
                     if (sm.seg_count[g]) {
-                        const uint32_t n = sm.hist[g * 32 + lane];
-                        m = n ? weight_times(w, bin_value(g * 32 + lane), n) : 0;
+                        const uint32_t n = sm.at(g, lane);
+                        m = n ? TokenWeight(w, place_value(g * 32 + lane)).times(n) : 0;
 #pragma unroll
                         for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
                     }
@@ -897,15 +956,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             // --- the border, by one warp
             if (warp == 0) {
-                int bin = kSegs * 32;
+                int place = kPlaces;
                 uint32_t take = 0, above_count = 0;
                 uint64_t above_mass = 0, Z = 0;
                 bool found = true;
                 if (s.k > 0) {
-                    found = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass, &bin, &above_count, &above_mass);
+                    place = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass, &above_count, &above_mass);
+                    found = place >= 0;
                     if (found) {
                         take = s.k - above_count;
-                        if (mass) Z = above_mass + weight_times(w, bin_value(bin), take);
+                        if (mass) Z = above_mass + TokenWeight(w, place_value(place)).times(take);
                     }
                 } else if (mass) {
                     for (int g = lane; g < kSegs; g += 32) Z += sm.seg_mass[g];
@@ -915,19 +975,19 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (found && mass) {
                     uint64_t target = lane == 0 ? mass_target(s.p, Z) : 0;
                     target = __shfl_sync(0xffffffffu, target, 0);
-                    int pbin = 0;
-                    found = locate(sm, w, Goal{true, 0, target}, true, &pbin, &above_count, &above_mass);
+                    const int at = locate(sm, w, Goal{true, 0, target}, true, &above_count, &above_mass);
+                    found = at >= 0;
                     if (found) {
-                        const uint32_t t = ties_for(w, bin_value(pbin), sm.hist[pbin], above_mass, target);
-                        if (pbin < bin || t < take) take = t;
-                        bin = min(bin, pbin);
+                        const uint32_t t = ties_for(TokenWeight(w, place_value(at)), sm.at(at / 32, at % 32), above_mass, target);
+                        if (at < place || t < take) take = t;
+                        place = min(place, at);
                     }
                 }
                 if (lane == 0) {
                     sm.elsewhere = !found;
-                    sm.value_bin = bin;
+                    sm.place = place;
                     sm.take = static_cast<int>(take);
-                    sm.ties = bin < kSegs * 32 ? static_cast<int>(sm.hist[bin]) : 0;
+                    sm.ties = found && place < kPlaces ? static_cast<int>(sm.at(place / 32, place % 32)) : 0;
                 }
             }
             __syncthreads();
@@ -945,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t border = 0xff80u;  // -inf: everything
         bool split = false;
         if (counted) {
-            border = __float_as_uint(bin_value(sm.value_bin)) >> 16;
+            border = __float_as_uint(place_value(sm.place)) >> 16;
             split = sm.take < sm.ties;
         }
         if (s.m > 0.0f) {
@@ -1053,7 +1113,6 @@ int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncat
     const char *in = static_cast<const char *>(logits);
     char *to = static_cast<char *>(out);
     if (DT == SPEC_BF16 && V <= kMaxFastV) {
-        static_assert(sizeof(BothShared) <= 48 * 1024, "fits without an attribute");
         truncate_bf16_kernel<<<grid, kThreads, sizeof(BothShared), stream>>>(in, to, rw, tr, V);
     } else {
         truncate_kernel<DT><<<grid, kThreads, sizeof(Shared), stream>>>(in, to, rw, tr, V);
@@ -1069,6 +1128,14 @@ inline int check_truncate_args(const spec_truncate_t *t, const Rows &rw, Truncat
 
 }  // namespace
 }  // namespace speclog
+
+namespace specv {
+bool set_logits_attrs() {
+    return cuda_ok(cudaFuncSetAttribute(speclog::truncate_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        sizeof(speclog::BothShared)),
+                   "cudaFuncSetAttribute(truncate_bf16_kernel)");
+}
+}  // namespace specv
 
 using namespace speclog;
 

@@ -1016,7 +1016,7 @@ DeviceState *device_state(int *dev_out) {
             !cuda_ok(cudaDeviceGetAttribute(&st.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev),
                      "cudaDeviceGetAttribute"))
             return nullptr;
-        if (!set_stats_attrs_all<SPEC_F32>(st) || !set_stats_attrs_all<SPEC_BF16>(st))
+        if (!set_stats_attrs_all<SPEC_F32>(st) || !set_stats_attrs_all<SPEC_BF16>(st) || !set_logits_attrs())
             return nullptr;
         st.smem_optin -= 1024;  // headroom for the kernels' static shared memory
         st.init = true;
