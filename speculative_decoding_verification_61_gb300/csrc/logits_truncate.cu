@@ -24,7 +24,14 @@
 namespace speclog {
 namespace {
 
-constexpr int kThreads = 512;
+#ifndef SPEC_TRUNCATE_THREADS
+#define SPEC_TRUNCATE_THREADS 512
+#endif
+#ifndef SPEC_TRUNCATE_PER_SM
+#define SPEC_TRUNCATE_PER_SM 2
+#endif
+constexpr int kThreads = SPEC_TRUNCATE_THREADS;
+constexpr int kPerSm = SPEC_TRUNCATE_PER_SM;  // resident CTAs
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 1024;        // elements of one bin that are sorted in shared memory
@@ -235,15 +242,16 @@ struct Goal {
 // the mass of everything in sm.total_mass.  Without a bin that reaches the
 // goal the last one that holds anything is taken.
 __device__ __noinline__ void find_bin(Shared &sm, const Goal &goal, uint32_t above_count, uint64_t above_mass) {
-    constexpr int kPer = kBins / kThreads;
+    constexpr int kPer = (kBins + kThreads - 1) / kThreads;
     uint32_t c = 0, ci[kPer];
     uint64_t m = 0, mi[kPer];
     const int first = threadIdx.x * kPer;
     if (threadIdx.x == 0) sm.bin = -1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        ci[i] = sm.count[first + i];
-        mi[i] = static_cast<uint64_t>(sm.hi[first + i]) << 32 | sm.lo[first + i];
+        const bool in = first + i < kBins;
+        ci[i] = in ? sm.count[first + i] : 0;
+        mi[i] = in ? static_cast<uint64_t>(sm.hi[first + i]) << 32 | sm.lo[first + i] : 0;
         c += ci[i];
         m += mi[i];
     }
@@ -387,7 +395,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
                 __syncthreads();
             }
         }
-        constexpr int kPer = kList / kThreads;
+        constexpr int kPer = (kList + kThreads - 1) / kThreads;
         uint32_t c = 0, ci[kPer];
         uint64_t m = 0, mi[kPer];
 #pragma unroll
@@ -469,10 +477,13 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
 __device__ __noinline__ uint32_t min_p_key(float zmax, float T, float min_p) {
     const double border = log(static_cast<double>(min_p));
     const uint32_t last = key_of(__int_as_float(0xff800000)), first = key_of(zmax);
+    const double shift = static_cast<double>(T) * border;
     auto passes = [&](uint32_t key) {
-        return (static_cast<double>(value_of(key)) - static_cast<double>(zmax)) / static_cast<double>(T) >= border;
+        const double d = static_cast<double>(value_of(key)) - static_cast<double>(zmax), gap = d - shift;
+        if (fabs(gap) > 1e-12 * fabs(shift)) return gap > 0.0;  // the division would say the same
+        return d / static_cast<double>(T) >= border;
     };
-    uint32_t key = key_of(static_cast<float>(static_cast<double>(zmax) + static_cast<double>(T) * border));
+    uint32_t key = key_of(static_cast<float>(static_cast<double>(zmax) + shift));
     key = min(max(key, last), first);
     while (key < first && !passes(key)) ++key;
     while (key > last && passes(key - 1)) --key;
@@ -500,11 +511,10 @@ __device__ __forceinline__ Settings load_settings(const Truncate &tr, int b, int
     return s;
 }
 
-__device__ __forceinline__ void set_row_constants(RowConstants &rc, const Settings &s, float zmax) {
+__device__ __forceinline__ void set_scale(RowConstants &rc, const Settings &s) {
     const double c = specv::kLog2eD / static_cast<double>(s.T);
     rc.ch = static_cast<float>(c);
     rc.cl = static_cast<float>(c - static_cast<double>(rc.ch));
-    if (s.m > 0.0f) rc.min_p_key = min_p_key(zmax, s.T, s.m);
 }
 __device__ __forceinline__ Weights row_weights(const RowConstants &rc, float zmax, int V, const float2 *table) {
     // V weights of at most 1 sum to less than 2^63
@@ -548,7 +558,10 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
     for (int i = 0; i < kWarps; ++i) top = max(top, sm.red[i]);
     const float zmax = value_of(top);
     if (nan || !isfinite(zmax)) return 0;  // NaN, +inf, or nothing but -inf
-    if (tid == 0) set_row_constants(sm.row, s, zmax);
+    if (tid == 0) {
+        set_scale(sm.row, s);
+        if (s.m > 0.0f) sm.row.min_p_key = min_p_key(zmax, s.T, s.m);
+    }
     __syncthreads();
     const Weights w = row_weights(sm.row, zmax, V, sm.table);
     const float scale = w.ch * kBinsPerOctave;
@@ -624,7 +637,7 @@ __device__ __forceinline__ void fill_nan(uint4 *dst, int64_t vecs, int64_t first
 
 // Rows of any kind, a CTA per row at a time, neighbouring rows at the same time.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kPerSm)
     truncate_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
     extern __shared__ char smem[];
     Shared &sm = *reinterpret_cast<Shared *>(smem);
@@ -658,31 +671,35 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ------------------------------------------------------------ bf16, in two passes
 // bf16 rows have few values, so a histogram with one bin per value settles
 // everything: counts are exact, and a weight is computed once per value
-// instead of once per token.  A bin per value of magnitude 2^-48 .. 2^16, 8192
-// a side, 64 KB; zeros have a counter of their own.  Values at or below -2^16
+// instead of once per token.  A bin per value of magnitude 2^-32 .. 2^16, 6144
+// a side, 48 KB; zeros have a counter of their own.  Values at or below -2^16
 // (masked logits) have no weight and are not counted.  Rows with other values
 // outside the bins, with NaN or +inf, or whose border is not in the bins, take
 // cut_of_row.
-constexpr int kTiny = (127 - 48) << 7;   // magnitude bits of 2^-48
+constexpr int kTiny = (127 - 32) << 7;   // magnitude bits of 2^-32
 constexpr int kHuge = (127 + 16) << 7;   // of 2^16
 constexpr int kSide = kHuge - kTiny;     // values a side
-static_assert(kSide == 1 << 13, "a bin is 13 magnitude bits and the sign");
 // The order: positive values falling, zero, negative values falling, in
-// segments of 32 places.
-constexpr int kSideSegs = kSide / 32;
+// segments of 128 places (an octave), 4 a lane.
+constexpr int kSegPlaces = 128;
+constexpr int kSideSegs = kSide / kSegPlaces;
 constexpr int kSegs = 2 * kSideSegs + 1;
 constexpr int kSegsPerLane = (kSegs + 31) / 32;
-constexpr int kPlaces = kSegs * 32;
+constexpr int kPlaces = kSegs * kSegPlaces;
 constexpr int kGroupCols = 256;           // a warp's 32 vectors
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxFastV = kGroupCols * kMaxGroups;
-constexpr int kAhead = 4;                 // vectors in flight per thread
+#ifndef SPEC_TRUNCATE_AHEAD
+#define SPEC_TRUNCATE_AHEAD 4
+#endif
+constexpr int kAhead = SPEC_TRUNCATE_AHEAD;  // vectors in flight per thread, beside the ones at work
 
 struct FastShared {
-    uint32_t hist[2 * kSide];  // bin: the sign above 13 bits of (magnitude - kTiny)
+    alignas(16) uint32_t hist[2 * kSide];  // bin: magnitude - kTiny, + kSide if negative
     uint32_t zeros;
-    uint32_t seg_count[kSegs];
-    uint64_t seg_mass[kSegs];
+    // of each segment, then (by the warp that finds the border) of it and those before
+    uint32_t seg_count[32 * kSegsPerLane];
+    uint64_t seg_mass[32 * kSegsPerLane];
     uint16_t group_max[kMaxGroups];  // order key of each group's largest value
     int first;                       // the largest value's place
     // the border: tokens above its value stay, `take` of its ties do
@@ -692,11 +709,21 @@ struct FastShared {
 
     // how often each group holds the border value: written once the bins are done with
     __device__ uint16_t *group_ties() { return reinterpret_cast<uint16_t *>(hist); }
-    // tokens at a place of segment seg, lane `lane`
-    __device__ __forceinline__ uint32_t at(int seg, int lane) const {
-        if (seg < kSideSegs) return hist[kSide - 1 - (seg * 32 + lane)];
-        if (seg == kSideSegs) return lane == 0 ? zeros : 0;
-        return hist[kSide + (seg - kSideSegs - 1) * 32 + lane];
+    // the tokens at a lane's 4 places of a segment
+    __device__ __forceinline__ void counts(int seg, uint32_t (&n)[4]) const {
+        const int lane = threadIdx.x & 31;
+        if (seg == kSideSegs) {
+            n[0] = lane == 0 ? zeros : 0;
+            n[1] = n[2] = n[3] = 0;
+            return;
+        }
+        const bool up = seg < kSideSegs;  // positive values lie in rising order
+        const int at = up ? kSide - 4 - (seg * kSegPlaces + lane * 4) : kSide + (seg - kSideSegs - 1) * kSegPlaces + lane * 4;
+        const uint4 q = *reinterpret_cast<const uint4 *>(hist + at);
+        n[0] = up ? q.w : q.x;
+        n[1] = up ? q.z : q.y;
+        n[2] = up ? q.y : q.z;
+        n[3] = up ? q.x : q.w;
     }
 };
 
@@ -711,7 +738,7 @@ struct BothShared {
 };
 
 __device__ __forceinline__ float place_value(int place) {
-    const int neg = place - (kSideSegs + 1) * 32;
+    const int neg = place - (kSideSegs + 1) * kSegPlaces;
     const uint32_t u = place < kSide ? kHuge - 1 - place : neg < 0 ? 0 : 0x8000 | (neg + kTiny);
     return __uint_as_float(u << 16);
 }
@@ -721,22 +748,38 @@ __device__ __forceinline__ uint32_t key16(uint32_t u) { return u ^ (u & 0x8000u 
 // t tokens' weight: the product before the one rounding.
 struct TokenWeight {
     uint64_t mantissa;
-    int shift;
+    int by;
     __device__ __forceinline__ TokenWeight(const Weights &w, float z) {
         int e;
         mantissa = weight_mantissa(w, z, &e);
-        shift = -(e + w.frac);  // at least 1: frac <= 47
+        by = min(-(e + w.frac), 127);  // at least 1: frac <= 47
     }
     __device__ __forceinline__ uint64_t times(uint32_t t) const {
-        if (mantissa == 0 || t == 0 || shift > 100) return 0;
         uint64_t lo = mantissa * t, hi = __umul64hi(mantissa, t);
-        if (shift >= 64) return hi >> (shift - 64);
-        const uint64_t half = 1ull << (shift - 1);
+        if (by >= 64) lo = hi, hi = 0;
+        const int left = by & 63;  // 0 where by is 64: nothing to round by
+        const uint64_t half = left ? 1ull << (left - 1) : 0;
         lo += half;
         hi += lo < half;
-        return lo >> shift | hi << (64 - shift);
+        return left ? lo >> left | hi << (64 - left) : lo;
     }
 };
+
+// A vector with values outside the bins: 1 if one of them is not zero and not
+// at or below -2^16.
+__device__ __noinline__ uint32_t count_rare(FastShared &sm, uint4 q) {
+    uint32_t odd = 0;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = q.x & 0xffffu, m = u & 0x7fffu;
+        if (m - kTiny < static_cast<uint32_t>(kSide)) atomicAdd(&sm.hist[m - kTiny + (u >> 15) * kSide], 1u);
+        else if (m == 0) atomicAdd(&sm.zeros, 1u);
+        else if (!(u >= (0x8000u | kHuge) && u <= 0xff80u)) odd = 1;
+        q.x >>= 16;
+        if (i & 1) q.x = q.y, q.y = q.z, q.z = q.w;
+    }
+    return odd;
+}
 
 // A vector's 8 values into the histogram.
 __device__ __forceinline__ void count_values(FastShared &sm, const uint4 &q, uint32_t *odd) {
@@ -746,74 +789,123 @@ __device__ __forceinline__ void count_values(FastShared &sm, const uint4 &q, uin
     for (int i = 0; i < 4; ++i) {
         // both halves at once; a half below kTiny borrows from its neighbour, and is seen to be outside itself
         t[i] = (w[i] & 0x7fff7fffu) - kTiny * 0x10001u;
-        outside |= t[i];
+        outside |= t[i] | (t[i] + (0x8000 - kSide) * 0x10001u);
     }
-    if ((outside & 0xe000e000u) == 0) {
+    if ((outside & 0x80008000u) == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t c = t[i] | ((w[i] >> 2) & 0x20002000u);
-            atomicAdd(&sm.hist[c & 0xffffu], 1u);
-            atomicAdd(&sm.hist[c >> 16], 1u);
+            // bins as byte offsets
+            static_assert(8 * kSide < 1 << 16, "a byte offset in 16 bits");
+            const uint32_t c = t[i] * 4 + ((w[i] >> 15) & 0x10001u) * (4 * kSide);
+            atomicAdd(reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.hist) + (c & 0xffffu)), 1u);
+            atomicAdd(reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.hist) + (c >> 16)), 1u);
         }
         return;
     }
     if ((w[0] & w[1] & w[2] & w[3]) == 0xff80ff80u && (w[0] | w[1] | w[2] | w[3]) == 0xff80ff80u) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t u = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu, m = u & 0x7fffu;
-        if (m - kTiny < static_cast<uint32_t>(kSide)) atomicAdd(&sm.hist[(m - kTiny) | (u & 0x8000u) >> 2], 1u);
-        else if (m == 0) atomicAdd(&sm.zeros, 1u);
-        else if (!(u >= (0x8000u | kHuge) && u <= 0xff80u)) *odd = 1;
-    }
+    *odd |= count_rare(sm, q);
 }
 
-// The first lane whose running sums reach the goal, and what lies above it; -1: none.
-__device__ __forceinline__ int first_reached(const Goal &goal, uint32_t n, uint64_t mass, uint32_t *c, uint64_t *m) {
+// Inclusive sums over the lanes.
+__device__ __forceinline__ void warp_scan(uint32_t &c, uint64_t &m) {
     const int lane = threadIdx.x & 31;
-    uint32_t cs = n;
-    uint64_t ms = mass;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t cc = __shfl_up_sync(0xffffffffu, cs, off);
-        const uint64_t mm = __shfl_up_sync(0xffffffffu, ms, off);
+        const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
+        const uint64_t mm = __shfl_up_sync(0xffffffffu, m, off);
         if (lane >= off) {
-            cs += cc;
-            ms += mm;
+            c += cc;
+            m += mm;
         }
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, goal.reached(*c + cs, *m + ms));
-    if (!hit) return -1;
-    const int at = __ffs(hit) - 1;
-    *c += __shfl_sync(0xffffffffu, cs - n, at);
-    *m += __shfl_sync(0xffffffffu, ms - mass, at);
-    return at;
 }
 
-// Where the goal is reached in the histogram, by one warp: the place, and what
-// lies above it; -1 if the bins end before.
-__device__ __forceinline__ int locate(FastShared &sm, const Weights &w, const Goal &goal, bool mass, uint32_t *above_count,
-                                      uint64_t *above_mass) {
-    const int lane = threadIdx.x & 31;
-    uint32_t c = 0, n = 0;
-    uint64_t m = 0, nm = 0;
-    const int s0 = lane * kSegsPerLane;
+// The segments' sums into running sums, by one warp.
+__device__ __forceinline__ void scan_segments(FastShared &sm, bool mass) {
+    const int s0 = (threadIdx.x & 31) * kSegsPerLane;
+    uint32_t n[kSegsPerLane], c = 0;
+    uint64_t nm[kSegsPerLane], m = 0;
 #pragma unroll
     for (int i = 0; i < kSegsPerLane; ++i) {
-        if (s0 + i >= kSegs) break;
-        n += sm.seg_count[s0 + i];
-        if (mass) nm += sm.seg_mass[s0 + i];
+        n[i] = sm.seg_count[s0 + i];
+        nm[i] = mass ? sm.seg_mass[s0 + i] : 0;
+        c += n[i];
+        m += nm[i];
     }
-    const int owner = first_reached(goal, n, nm, &c, &m);
-    if (owner < 0) return -1;
-    const int s = owner * kSegsPerLane + lane;
-    const bool in = lane < kSegsPerLane && s < kSegs;
-    const int seg = owner * kSegsPerLane + first_reached(goal, in ? sm.seg_count[s] : 0, in && mass ? sm.seg_mass[s] : 0, &c, &m);
-    n = sm.at(seg, lane);
-    nm = mass && n ? TokenWeight(w, place_value(seg * 32 + lane)).times(n) : 0;
-    const int at = first_reached(goal, n, nm, &c, &m);
-    *above_count = c;
-    *above_mass = m;
-    return seg * 32 + at;
+    const uint32_t own_c = c;
+    const uint64_t own_m = m;
+    warp_scan(c, m);
+    c -= own_c;
+    m -= own_m;
+#pragma unroll
+    for (int i = 0; i < kSegsPerLane; ++i) {
+        sm.seg_count[s0 + i] = c += n[i];
+        sm.seg_mass[s0 + i] = m += nm[i];
+    }
+    __syncwarp();
+}
+
+// A place in the order: what lies above it, and the tokens there.
+struct Border {
+    int place;
+    uint32_t above_count, n;
+    uint64_t above_mass;
+};
+
+// Where the goal is reached in the histogram, by one warp, from the running
+// sums; place -1 if the bins end before.  (Shared-memory round trips are what
+// this costs beside another CTA's histogram, so it makes few.)
+__device__ __forceinline__ Border locate(const FastShared &sm, const Weights &w, const Goal &goal, bool mass) {
+    const int lane = threadIdx.x & 31, s0 = lane * kSegsPerLane;
+    uint32_t c = lane ? sm.seg_count[s0 - 1] : 0;
+    uint64_t m = lane ? sm.seg_mass[s0 - 1] : 0;
+    int seg = -1;
+#pragma unroll
+    for (int i = 0; i < kSegsPerLane; ++i) {
+        const uint32_t c1 = sm.seg_count[s0 + i];
+        const uint64_t m1 = sm.seg_mass[s0 + i];
+        if (seg < 0) {
+            if (goal.reached(c1, m1)) {
+                seg = s0 + i;
+            } else {
+                c = c1;
+                m = m1;
+            }
+        }
+    }
+    uint32_t hit = __ballot_sync(0xffffffffu, seg >= 0);
+    if (!hit) return Border{-1, 0, 0, 0};
+    int at = __ffs(hit) - 1;
+    seg = __shfl_sync(0xffffffffu, seg, at);
+    c = __shfl_sync(0xffffffffu, c, at);
+    m = __shfl_sync(0xffffffffu, m, at);
+    uint32_t n[4];
+    uint64_t nm[4];
+    sm.counts(seg, n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nm[i] = mass ? TokenWeight(w, place_value(seg * kSegPlaces + lane * 4 + i)).times(n[i]) : 0;
+    uint32_t cs = n[0] + n[1] + n[2] + n[3];
+    uint64_t ms = nm[0] + nm[1] + nm[2] + nm[3];
+    const uint32_t own_c = cs;
+    const uint64_t own_m = ms;
+    warp_scan(cs, ms);
+    cs += c;
+    ms += m;
+    at = __ffs(__ballot_sync(0xffffffffu, goal.reached(cs, ms))) - 1;
+    cs -= own_c;
+    ms -= own_m;
+    int place = seg * kSegPlaces + lane * 4;
+    uint32_t here = n[0];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        if (place != seg * kSegPlaces + lane * 4 + i || goal.reached(cs + n[i], ms + nm[i])) continue;
+        cs += n[i];
+        ms += nm[i];
+        here = n[i + 1];
+        ++place;
+    }
+    return Border{__shfl_sync(0xffffffffu, place, at), __shfl_sync(0xffffffffu, cs, at), __shfl_sync(0xffffffffu, here, at),
+                  __shfl_sync(0xffffffffu, ms, at)};
 }
 
 // The fewest of n ties whose weight reaches the target, by one warp.
@@ -858,7 +950,7 @@ __device__ __forceinline__ uint32_t equal_mask(uint32_t a, uint32_t b) {
     return __heq2_mask(x, y);
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kPerSm)
     truncate_bf16_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
     extern __shared__ char smem[];
     BothShared &all = *reinterpret_cast<BothShared *>(smem);
@@ -894,6 +986,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         // --- one pass over the row: the histogram, the groups' largest values
         __syncthreads();  // the last row is done with the shared arrays
         for (int i = tid; i < 2 * kSide / 4; i += kThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
+        if (tid < 32 * kSegsPerLane - kSegs) {
+            sm.seg_count[kSegs + tid] = 0;
+            sm.seg_mass[kSegs + tid] = 0;
+        }
+        if (tid == kThreads - 1) set_scale(all.row, s);
         if (tid == 0) {
             sm.zeros = 0;
             sm.first = kPlaces;
@@ -901,19 +998,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncthreads();
         uint32_t odd = 0;
-        for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
-            uint4 q[kAhead];
+        {
+            uint4 q[kAhead], next[kAhead];
+            auto load = [&](uint4 (&to)[kAhead], int g0) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int v = (g0 + u * kWarps) * 32 + lane;
-                q[u] = v < vecs ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-            }
+                for (int u = 0; u < kAhead; ++u) {
+                    const int v = (g0 + u * kWarps) * 32 + lane;
+                    to[u] = v < vecs ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                }
+            };
+            load(q, warp);
+            for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
+                load(next, g0 + kWarps * kAhead);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (g0 + u * kWarps >= groups) break;
-                count_values(sm, q[u], &odd);
-                const uint32_t key = __reduce_max_sync(0xffffffffu, max_key(q[u]));
-                if (lane == 0) sm.group_max[g0 + u * kWarps] = static_cast<uint16_t>(key);
+                for (int u = 0; u < kAhead; ++u) {
+                    if (g0 + u * kWarps >= groups) break;
+                    count_values(sm, q[u], &odd);
+                    const uint32_t key = __reduce_max_sync(0xffffffffu, max_key(q[u]));
+                    if (lane == 0) sm.group_max[g0 + u * kWarps] = static_cast<uint16_t>(key);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) q[u] = next[u];
             }
         }
         bool slow = __syncthreads_or(odd) != 0;
@@ -922,10 +1027,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             // --- the bins' sums by segments of 32
             int first = kPlaces;
             for (int g = warp; g < kSegs; g += kWarps) {
-                const uint32_t n = sm.at(g, lane);
-                const uint32_t any = __ballot_sync(0xffffffffu, n > 0);
-                if (any) first = min(first, g * 32 + __ffs(any) - 1);
-                const uint32_t sum = __reduce_add_sync(0xffffffffu, n);
+                uint32_t n[4];
+                sm.counts(g, n);
+                const uint32_t own = n[0] + n[1] + n[2] + n[3];
+                const uint32_t any = __ballot_sync(0xffffffffu, own > 0);
+                uint32_t sum = 0;
+                if (any) {
+                    if (first == kPlaces) {
+                        const int i = n[0] ? 0 : n[1] ? 1 : n[2] ? 2 : 3, at = __ffs(any) - 1;
+                        first = g * kSegPlaces + at * 4 + __shfl_sync(0xffffffffu, i, at);
+                    }
+                    sum = __reduce_add_sync(0xffffffffu, own);
+                }
                 if (lane == 0) sm.seg_count[g] = sum;
             }
             if (lane == 0) atomicMin(&sm.first, first);
@@ -938,15 +1051,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!slow && !((-65536.0f - zmax) * specv::temp_scale(s.T) < -150.0f)) slow = true;
         Weights w{};
         if (!slow) {
-            if (tid == 0) set_row_constants(all.row, s, zmax);
-            __syncthreads();
             w = row_weights(all.row, zmax, V, all.table);
             if (mass) {
                 for (int g = warp; g < kSegs; g += kWarps) {
                     uint64_t m = 0;
                     if (sm.seg_count[g]) {
-                        const uint32_t n = sm.at(g, lane);
-                        m = n ? TokenWeight(w, place_value(g * 32 + lane)).times(n) : 0;
+                        uint32_t n[4];
+                        sm.counts(g, n);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m += TokenWeight(w, place_value(g * kSegPlaces + lane * 4 + i)).times(n[i]);
 #pragma unroll
                         for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
                     }
@@ -955,40 +1068,34 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncthreads();
             }
             // --- the border, by one warp
-            if (warp == 0) {
-                int place = kPlaces;
-                uint32_t take = 0, above_count = 0;
-                uint64_t above_mass = 0, Z = 0;
-                bool found = true;
+            if (warp == 0 && counted) {
+                scan_segments(sm, mass);
+                Border k{kPlaces, 0, 0, 0};
+                uint32_t take = 0;
+                uint64_t Z = mass ? sm.seg_mass[kSegs - 1] : 0;
                 if (s.k > 0) {
-                    place = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass, &above_count, &above_mass);
-                    found = place >= 0;
-                    if (found) {
-                        take = s.k - above_count;
-                        if (mass) Z = above_mass + TokenWeight(w, place_value(place)).times(take);
-                    }
-                } else if (mass) {
-                    for (int g = lane; g < kSegs; g += 32) Z += sm.seg_mass[g];
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, off);
+                    k = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass);
+                    take = s.k - k.above_count;
+                    if (mass && k.place >= 0) Z = k.above_mass + TokenWeight(w, place_value(k.place)).times(take);
                 }
-                if (found && mass) {
+                if (mass && k.place >= 0) {
                     uint64_t target = lane == 0 ? mass_target(s.p, Z) : 0;
                     target = __shfl_sync(0xffffffffu, target, 0);
-                    const int at = locate(sm, w, Goal{true, 0, target}, true, &above_count, &above_mass);
-                    found = at >= 0;
-                    if (found) {
-                        const uint32_t t = ties_for(TokenWeight(w, place_value(at)), sm.at(at / 32, at % 32), above_mass, target);
-                        if (at < place || t < take) take = t;
-                        place = min(place, at);
+                    const Border p = locate(sm, w, Goal{true, 0, target}, true);
+                    if (p.place >= 0) {
+                        const uint32_t t = ties_for(TokenWeight(w, place_value(p.place)), p.n, p.above_mass, target);
+                        take = p.place < k.place ? t : min(t, take);
                     }
+                    k = p;
                 }
                 if (lane == 0) {
-                    sm.elsewhere = !found;
-                    sm.place = place;
+                    sm.elsewhere = k.place < 0;
+                    sm.place = k.place;
                     sm.take = static_cast<int>(take);
-                    sm.ties = found && place < kPlaces ? static_cast<int>(sm.at(place / 32, place % 32)) : 0;
+                    sm.ties = static_cast<int>(k.n);
                 }
+            } else if (tid == 32 && s.m > 0.0f) {
+                all.row.min_p_key = min_p_key(zmax, s.T, s.m);
             }
             __syncthreads();
             slow = sm.elsewhere;
@@ -1083,33 +1190,48 @@ __global__ void __launch_bounds__(kThreads, 2)
             cut_index = sm.cut_index;
         }
         // --- the row out: groups below the border need not be read again
-        for_groups(groups, [&](int g, int v) {
-            if (v >= vecs) return;
-            uint4 q = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-            if (sm.group_max[g] >= low) {
-                q = row[v];
-                uint32_t *x = reinterpret_cast<uint32_t *>(&q);
-                const bool equal = g < cut_group;
+        for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
+            uint4 q[kAhead];
+            bool kept[kAhead];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t keep = above_mask(x[i], pair, equal);
-                    if (g == cut_group) {
-                        const uint32_t e = equal_mask(x[i], pair);
-                        if (v * 8 + 2 * i <= cut_index) keep |= e & 0xffffu;
-                        if (v * 8 + 2 * i + 1 <= cut_index) keep |= e & 0xffff0000u;
-                    }
-                    x[i] = (x[i] & keep) | (0xff80ff80u & ~keep);
-                }
+            for (int u = 0; u < kAhead; ++u) {
+                const int g = g0 + u * kWarps;
+                kept[u] = g < groups && sm.group_max[g] >= low;
             }
-            dst[v] = q;
-        });
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int v = (g0 + u * kWarps) * 32 + lane;
+                q[u] = kept[u] && v < vecs ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int g = g0 + u * kWarps, v = g * 32 + lane;
+                if (v >= vecs) continue;
+                if (kept[u]) {
+                    uint32_t x[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                    const bool equal = g < cut_group;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t keep = above_mask(x[i], pair, equal);
+                        if (g == cut_group) {
+                            const uint32_t e = equal_mask(x[i], pair);
+                            if (v * 8 + 2 * i <= cut_index) keep |= e & 0xffffu;
+                            if (v * 8 + 2 * i + 1 <= cut_index) keep |= e & 0xffff0000u;
+                        }
+                        x[i] = (x[i] & keep) | (0xff80ff80u & ~keep);
+                    }
+                    q[u] = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+                dst[v] = q[u];
+            }
+        }
     }
 }
 
 template <int DT>
 int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms,
                     cudaStream_t stream) {
-    const int grid = std::min(rw.R, sms * 2);
+    const int grid = std::min(rw.R, sms * kPerSm);
     const char *in = static_cast<const char *>(logits);
     char *to = static_cast<char *>(out);
     if (DT == SPEC_BF16 && V <= kMaxFastV) {
