@@ -765,6 +765,20 @@ struct TokenWeight {
     }
 };
 
+// 0xffff in the halves of a that are greater than (or equal to) b's
+__device__ __forceinline__ uint32_t above_mask(uint32_t a, uint32_t b, bool equal) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
+    return equal ? __hge2_mask(x, y) : __hgt2_mask(x, y);
+}
+__device__ __forceinline__ uint32_t equal_mask(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
+    return __heq2_mask(x, y);
+}
+__device__ __forceinline__ uint32_t below_mask(uint32_t a, uint32_t b) {  // or equal
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
+    return __hle2_mask(x, y);
+}
+
 // A vector with values outside the bins: 1 if one of them is not zero and not
 // at or below -2^16.
 __device__ __noinline__ uint32_t count_rare(FastShared &sm, uint4 q) {
@@ -802,8 +816,27 @@ __device__ __forceinline__ void count_values(FastShared &sm, const uint4 &q, uin
         }
         return;
     }
-    if ((w[0] & w[1] & w[2] & w[3]) == 0xff80ff80u && (w[0] | w[1] | w[2] | w[3]) == 0xff80ff80u) return;
-    *odd |= count_rare(sm, q);
+    // values at or below -2^16, as masks leave them, are passed over
+    uint32_t low[4], none = ~0u;
+    outside = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        low[i] = below_mask(w[i], (0x8000u | kHuge) * 0x10001u);
+        outside |= (t[i] | (t[i] + (0x8000 - kSide) * 0x10001u)) & ~low[i];
+        none &= low[i];
+    }
+    if (none == ~0u) return;
+    if (outside & 0x80008000u) {
+        *odd |= count_rare(sm, q);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // (without the halves passed over, whose offsets would carry into their neighbours)
+        const uint32_t c = (t[i] & ~low[i]) * 4 + ((w[i] >> 15) & 0x10001u) * (4 * kSide);
+        if (!(low[i] & 0xffffu)) atomicAdd(reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.hist) + (c & 0xffffu)), 1u);
+        if (!(low[i] >> 16)) atomicAdd(reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.hist) + (c >> 16)), 1u);
+    }
 }
 
 // Inclusive sums over the lanes.
@@ -927,27 +960,11 @@ __device__ __forceinline__ uint32_t ties_for(const TokenWeight &w, uint32_t n, u
     return hi;
 }
 
-// A group's 32 vectors of 8: groups are counted in column order, group g by warp g % kWarps.
-template <typename F>
-__device__ __forceinline__ void for_groups(int groups, F &&f) {
-    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) f(g, g * 32 + static_cast<int>(threadIdx.x & 31));
-}
-
 // Order key of a vector's largest value.
 __device__ __forceinline__ uint32_t max_key(const uint4 &q) {
     const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&q);
     const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return key16(__bfloat16_as_ushort(__hmax(__low2bfloat16(m), __high2bfloat16(m))));
-}
-
-// 0xffff in the halves of a that are greater than (or equal to) b's
-__device__ __forceinline__ uint32_t above_mask(uint32_t a, uint32_t b, bool equal) {
-    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
-    return equal ? __hge2_mask(x, y) : __hgt2_mask(x, y);
-}
-__device__ __forceinline__ uint32_t equal_mask(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&a), y = *reinterpret_cast<const __nv_bfloat162 *>(&b);
-    return __heq2_mask(x, y);
 }
 
 __global__ void __launch_bounds__(kThreads, kPerSm)
@@ -1131,18 +1148,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         int cut_group = groups, cut_index = 0;
         if (split) {
             const int take = sm.take;
-            for_groups(groups, [&](int g, int v) {
-                uint32_t n = 0;
-                if (sm.group_max[g] >= low) {
-                    if (v < vecs) {
-                        const uint4 q = row[v];
-                        n = __popc(equal_mask(q.x, pair)) + __popc(equal_mask(q.y, pair)) + __popc(equal_mask(q.z, pair)) +
-                            __popc(equal_mask(q.w, pair));
-                    }
-                    n = __reduce_add_sync(0xffffffffu, n >> 4);
+            for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
+                uint4 q[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int g = g0 + u * kWarps, v = g * 32 + lane;
+                    q[u] = make_uint4(~pair, ~pair, ~pair, ~pair);
+                    if (g < groups && sm.group_max[g] >= low && v < vecs) q[u] = row[v];
                 }
-                if (lane == 0) sm.group_ties()[g] = static_cast<uint16_t>(n);
-            });
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int g = g0 + u * kWarps;
+                    if (g >= groups) break;
+                    uint32_t n = __popc(equal_mask(q[u].x, pair)) + __popc(equal_mask(q[u].y, pair)) +
+                                 __popc(equal_mask(q[u].z, pair)) + __popc(equal_mask(q[u].w, pair));
+                    n = __reduce_add_sync(0xffffffffu, n >> 4);
+                    if (lane == 0) sm.group_ties()[g] = static_cast<uint16_t>(n);
+                }
+            }
             __syncthreads();
             if (warp == 0) {
                 // the group where the ties run out, then the token
