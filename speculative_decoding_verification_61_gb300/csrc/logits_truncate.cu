@@ -706,6 +706,7 @@ struct FastShared {
     int place, take, ties;
     int cut_group, cut_index;
     bool elsewhere;  // not in the bins
+    bool finite_low;  // a value at or below -2^16 that is not -inf
 
     // how often each group holds the border value: written once the bins are done with
     __device__ uint16_t *group_ties() { return reinterpret_cast<uint16_t *>(hist); }
@@ -779,8 +780,10 @@ __device__ __forceinline__ uint32_t below_mask(uint32_t a, uint32_t b) {  // or 
     return __hle2_mask(x, y);
 }
 
-// A vector with values outside the bins: 1 if one of them is not zero and not
-// at or below -2^16.
+// What a row holds beside the values of the bins and -inf.
+enum { kOdd = 1, kFiniteLow = 2 };
+
+// A vector with values outside the bins.
 __device__ __noinline__ uint32_t count_rare(FastShared &sm, uint4 q) {
     uint32_t odd = 0;
 #pragma unroll 1
@@ -788,7 +791,8 @@ __device__ __noinline__ uint32_t count_rare(FastShared &sm, uint4 q) {
         const uint32_t u = q.x & 0xffffu, m = u & 0x7fffu;
         if (m - kTiny < static_cast<uint32_t>(kSide)) atomicAdd(&sm.hist[m - kTiny + (u >> 15) * kSide], 1u);
         else if (m == 0) atomicAdd(&sm.zeros, 1u);
-        else if (!(u >= (0x8000u | kHuge) && u <= 0xff80u)) odd = 1;
+        else if (u < (0x8000u | kHuge) || u > 0xff80u) odd |= kOdd;
+        else if (u != 0xff80u) odd |= kFiniteLow;
         q.x >>= 16;
         if (i & 1) q.x = q.y, q.y = q.z, q.z = q.w;
     }
@@ -817,14 +821,16 @@ __device__ __forceinline__ void count_values(FastShared &sm, const uint4 &q, uin
         return;
     }
     // values at or below -2^16, as masks leave them, are passed over
-    uint32_t low[4], none = ~0u;
+    uint32_t low[4], none = ~0u, finite = 0;
     outside = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         low[i] = below_mask(w[i], (0x8000u | kHuge) * 0x10001u);
         outside |= (t[i] | (t[i] + (0x8000 - kSide) * 0x10001u)) & ~low[i];
         none &= low[i];
+        finite |= low[i] & ~equal_mask(w[i], 0xff80ff80u);
     }
+    if (finite) *odd |= kFiniteLow;
     if (none == ~0u) return;
     if (outside & 0x80008000u) {
         *odd |= count_rare(sm, q);
@@ -1012,6 +1018,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             sm.zeros = 0;
             sm.first = kPlaces;
             sm.elsewhere = false;
+            sm.finite_low = false;
         }
         __syncthreads();
         uint32_t odd = 0;
@@ -1038,7 +1045,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 for (int u = 0; u < kAhead; ++u) q[u] = next[u];
             }
         }
-        bool slow = __syncthreads_or(odd) != 0;
+        if (odd & kFiniteLow) sm.finite_low = true;
+        bool slow = __syncthreads_or(odd & kOdd) != 0;
         float zmax = 0.0f;
         if (!slow) {
             // --- the bins' sums by segments of 32
@@ -1092,8 +1100,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 uint64_t Z = mass ? sm.seg_mass[kSegs - 1] : 0;
                 if (s.k > 0) {
                     k = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass);
-                    take = s.k - k.above_count;
-                    if (mass && k.place >= 0) Z = k.above_mass + TokenWeight(w, place_value(k.place)).times(take);
+                    if (k.place >= 0) {
+                        take = s.k - k.above_count;
+                        if (mass) Z = k.above_mass + TokenWeight(w, place_value(k.place)).times(take);
+                    } else if (!sm.finite_low) {
+                        k = Border{kPlaces, 0, 0, 0};  // fewer than k tokens are not -inf: all of them
+                    }
                 }
                 if (mass && k.place >= 0) {
                     uint64_t target = lane == 0 ? mass_target(s.p, Z) : 0;
@@ -1129,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         uint32_t border = 0xff80u;  // -inf: everything
         bool split = false;
         if (counted) {
-            border = __float_as_uint(place_value(sm.place)) >> 16;
+            if (sm.place < kPlaces) border = __float_as_uint(place_value(sm.place)) >> 16;
             split = sm.take < sm.ties;
         }
         if (s.m > 0.0f) {
