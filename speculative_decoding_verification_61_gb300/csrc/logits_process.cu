@@ -29,8 +29,15 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 256;    // columns listed at once
+constexpr int kBias = 64;     // bias entries kept in shared memory
 #ifndef SPEC_PROCESS_PER_SM
 #define SPEC_PROCESS_PER_SM 6
+#endif
+#ifndef SPEC_PROCESS_PIECE
+#define SPEC_PROCESS_PIECE 1  // 2 words: a 128-byte line of bf16
+#endif
+#ifndef SPEC_PROCESS_SPREAD_MB
+#define SPEC_PROCESS_SPREAD_MB 300
 #endif
 constexpr int kPerSm = SPEC_PROCESS_PER_SM;  // resident CTAs
 
@@ -38,10 +45,14 @@ template <int DT>
 constexpr uint32_t kNanWord = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
 
 // How a group of threads takes a unit of 128 words of the bit arrays (4096
-// columns): with the stream a CTA takes them in a row, without it (in place, no
-// masks) a warp takes words spread over the vocabulary: ids are often ordered
-// by frequency, and so every warp gets its share of the frequent ones, whose
-// columns are all its work.
+// columns): a CTA with the stream, a warp without it (in place, no masks).  A
+// unit's words come in pieces of 2^piece words, spread over the vocabulary:
+// ids are often ordered by frequency, and so every unit gets its share of the
+// frequent ones, whose columns are the work beside the stream.
+struct Units {
+    int self, n, piece;
+};
+
 template <bool STREAM>
 struct Group {
     static constexpr int kSize = STREAM ? kThreads : 32;
@@ -59,15 +70,17 @@ struct Group {
         return STREAM ? __syncthreads_or(x) != 0 : __any_sync(0xffffffffu, x) != 0;
     }
     // the word that the unit's place i stands for, and back (-1: another unit's)
-    static __device__ __forceinline__ int word(int unit, int units, int i) {
-        return STREAM ? unit * kWords + i : unit + units * i;
+    static __device__ __forceinline__ int word(const Units &un, int i) {
+        return (un.self + un.n * (i >> un.piece) << un.piece) + (i & ((1 << un.piece) - 1));
     }
-    static __device__ __forceinline__ int place(int unit, int units, int word) {
-        const int turn = STREAM ? word / kWords : word / units;
-        if (STREAM) return turn == unit ? word % kWords : -1;
-        return word - turn * units == unit ? turn : -1;
+    static __device__ __forceinline__ int place(const Units &un, int word) {
+        const int piece = word >> un.piece, turn = piece / un.n;
+        return piece - turn * un.n == un.self ? (turn << un.piece) + (word & ((1 << un.piece) - 1)) : -1;
     }
-    static __host__ int units(int V) { return (V + 32 * kWords - 1) / (32 * kWords); }
+    static __host__ int units(int V, int piece) {
+        const int pieces = (V + (32 << piece) - 1) / (32 << piece);
+        return (pieces + (kWords >> piece) - 1) / (kWords >> piece);
+    }
 };
 
 template <bool STREAM>
@@ -79,6 +92,8 @@ struct GroupShared {
     int warp_sum[kWarps];
     int column[kList], count[kList];
     uint8_t flags[kList];
+    int bias_token[kBias];
+    float bias_value[kBias];
 };
 enum { kSeen = 1, kDrafted = 2, kBiased = 4 };
 
@@ -118,7 +133,7 @@ __device__ __forceinline__ int mask_of(const Process &ps, int row) {
 // the masks applied; in place only what a mask takes away.
 template <int DT>
 __device__ __forceinline__ void stream_rows(const char *logits, char *out, const Process &ps, int V, int row0, int i0,
-                                            int i1, int unit, int units, bool inplace) {
+                                            int i1, const Units &un, bool inplace) {
     using G = Group<true>;
     constexpr int kPer = Elem<DT>::kPerVec;
     constexpr int kVecs = 32 / kPer;                // a thread's vectors of one row
@@ -129,7 +144,7 @@ __device__ __forceinline__ void stream_rows(const char *logits, char *out, const
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
         const int x = j * kThreads + static_cast<int>(threadIdx.x);
-        col[j] = G::word(unit, units, x / (32 / kPer)) * 32 + x % (32 / kPer) * kPer;
+        col[j] = G::word(un, x / (32 / kPer)) * 32 + x % (32 / kPer) * kPer;
     }
     const char *src = logits + (static_cast<int64_t>(row0) + i0) * row_bytes;
     char *dst = out + (static_cast<int64_t>(row0) + i0) * row_bytes;
@@ -193,14 +208,14 @@ __device__ __forceinline__ void stream_rows(const char *logits, char *out, const
 
 // A unit's columns of some rows as NaN.
 template <int DT, bool STREAM>
-__device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0, int i1, int unit, int units) {
+__device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0, int i1, const Units &un) {
     using G = Group<STREAM>;
     const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
     constexpr uint32_t w = kNanWord<DT>;
     constexpr int kPer = Elem<DT>::kPerVec;
     for (int i = i0; i < i1; ++i)
         for (int x = G::thread(); x < G::kWords * 32 / kPer; x += G::kSize) {
-            const int col = G::word(unit, units, x / (32 / kPer)) * 32 + x % (32 / kPer) * kPer;
+            const int col = G::word(un, x / (32 / kPer)) * 32 + x % (32 / kPer) * kPer;
             if (col < V)
                 *reinterpret_cast<uint4 *>(out + (row0 + i) * row_bytes + static_cast<int64_t>(col) * Elem<DT>::kBytes) =
                     make_uint4(w, w, w, w);
@@ -214,7 +229,7 @@ __device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0,
 // memory.
 template <int DT, bool STREAM>
 __global__ void __launch_bounds__(kThreads, kPerSm)
-    process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int units, int parts) {
+    process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int units, int piece, int parts) {
     using G = Group<STREAM>;
     __shared__ GroupShared<STREAM> s_group[G::kCount];
     const int me = G::thread(), lane = threadIdx.x & 31;
@@ -229,12 +244,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     if (!check_rows(rw, pen)) {
         // the call fails: every row is NaN
         for (int64_t u = self; u < static_cast<int64_t>(rw.R) * units; u += groups)
-            nan_rows<DT, STREAM>(out, V, u / units, 0, 1, static_cast<int>(u % units), units);
+            nan_rows<DT, STREAM>(out, V, u / units, 0, 1, Units{static_cast<int>(u % units), units, piece});
         return;
     }
     const int64_t pair = self / parts;
     const int part = static_cast<int>(self - pair * parts), b = static_cast<int>(pair / units);
-    const int unit = static_cast<int>(pair - static_cast<int64_t>(b) * units);
+    const Units un{static_cast<int>(pair - static_cast<int64_t>(b) * units), units, piece};
     if (b >= rw.B) return;
     {
         const int o0 = __ldg(rw.offsets + b), o1 = __ldg(rw.offsets + b + 1);
@@ -254,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         const bool there = pen && slot >= 0 && slot < ps.S;
 #pragma unroll
         for (int i = 0; i < G::kWordsEach; ++i) {
-            const int word = G::word(unit, units, i * G::kSize + me);
+            const int word = G::word(un, i * G::kSize + me);
             prompt[i] = emitted[i] = 0;
             if (there && word < W) {
                 prompt[i] = static_cast<uint32_t>(__ldg(ps.seen + slot * 2 * W + word));
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 e1 = e0 = 0;
             }
         }
-        if (STREAM) stream_rows<DT>(logits, out, ps, V, row0, i0, i1, unit, units, inplace);
+        if (STREAM) stream_rows<DT>(logits, out, ps, V, row0, i0, i1, un, inplace);
 
         // --- the unit's columns that anything applies to
 #pragma unroll
@@ -296,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 if (!root) {
                     const bool in = token[t] >= 0 && token[t] < V;
                     bad |= !in;
-                    const int d = in ? G::place(unit, units, token[t] >> 5) : -1;
+                    const int d = in ? G::place(un, token[t] >> 5) : -1;
                     if (d >= 0) atomicOr(&sm.drafted[d], 1u << (token[t] & 31));
                 }
                 if (tree) {
@@ -308,20 +323,25 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         for (int e = e0 + me; e < e1; e += G::kSize) {
             const int t = __ldg(ps.bias_tokens + e);
             const bool in = t >= 0 && t < V;
-            bad |= !in || !(__ldg(ps.bias_values + e) < __int_as_float(0x7f800000));  // NaN and +inf
-            const int d = in ? G::place(unit, units, t >> 5) : -1;
+            const float v = __ldg(ps.bias_values + e);
+            bad |= !in || !(v < __int_as_float(0x7f800000));  // NaN and +inf
+            if (e - e0 < kBias) {
+                sm.bias_token[e - e0] = t;
+                sm.bias_value[e - e0] = v;
+            }
+            const int d = in ? G::place(un, t >> 5) : -1;
             if (d >= 0) atomicOr(&sm.biased[d], 1u << (t & 31));
         }
         bad = G::any(bad);
         G::sync();  // the shared arrays are whole, the stream's stores done
         if (bad) {
-            nan_rows<DT, STREAM>(out, V, row0, i0, i1, unit, units);
+            nan_rows<DT, STREAM>(out, V, row0, i0, i1, un);
         } else {
             uint32_t touched[G::kWordsEach], drafted[G::kWordsEach], biased[G::kWordsEach];
             int rank = 0;
 #pragma unroll
             for (int i = 0; i < G::kWordsEach; ++i) {
-                const int word = G::word(unit, units, i * G::kSize + me);
+                const int word = G::word(un, i * G::kSize + me);
                 // bits behind the vocabulary say nothing
                 const uint32_t in_v = word >= W ? 0u : word == W - 1 && (V & 31) ? (1u << (V & 31)) - 1 : 0xffffffffu;
                 drafted[i] = sm.drafted[i * G::kSize + me];
@@ -359,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 int at_rank = rank - base;
 #pragma unroll
                 for (int i = 0; i < G::kWordsEach; ++i) {
-                    const int col0 = G::word(unit, units, i * G::kSize + me) * 32;
+                    const int col0 = G::word(un, i * G::kSize + me) * 32;
                     for (uint32_t m = touched[i]; m; m &= m - 1, ++at_rank) {
                         if (at_rank < 0 || at_rank >= kList) continue;
                         const int bit = __ffs(m) - 1;
@@ -378,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                     if (f & kBiased) {
                         // the same token twice: the entries add, in list order
                         bool any = false;
-                        for (int x = e0; x < e1; ++x) {
-                            if (__ldg(ps.bias_tokens + x) != col) continue;
-                            const float v = __ldg(ps.bias_values + x);
+                        for (int x = 0; x < e1 - e0; ++x) {
+                            if ((x < kBias ? sm.bias_token[x] : __ldg(ps.bias_tokens + e0 + x)) != col) continue;
+                            const float v = x < kBias ? sm.bias_value[x] : __ldg(ps.bias_values + e0 + x);
                             bias = any ? __fadd_rn(bias, v) : v;
                             any = true;
                         }
@@ -492,14 +512,18 @@ template <int DT, bool STREAM>
 int launch_process(const void *logits, void *out, const Rows &rw, const Process &ps, int V, int sms,
                    cudaStream_t stream) {
     using G = Group<STREAM>;
-    const int units = G::units(V);
+    // Spread pieces even out the frequent ids, whole units keep the CTAs that run at
+    // a time in one window of memory: SPREAD_COMMENT
+    const bool spread = !STREAM || static_cast<int64_t>(rw.R) * V * Elem<DT>::kBytes <= static_cast<int64_t>(SPEC_PROCESS_SPREAD_MB) << 20;
+    const int piece = !STREAM ? 0 : spread ? SPEC_PROCESS_PIECE : 7;
+    const int units = G::units(V, piece);
     const int64_t pairs = static_cast<int64_t>(rw.B) * units;
     // few sequences: their rows are split until every SM has its CTAs
     const int64_t room = static_cast<int64_t>(sms) * kPerSm * G::kCount;
     const int parts = static_cast<int>(std::clamp<int64_t>(room / pairs, 1, std::max(1, rw.R / rw.B)));
     const int64_t ctas = (pairs * parts + G::kCount - 1) / G::kCount;
     process_kernel<DT, STREAM><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(
-        static_cast<const char *>(logits), static_cast<char *>(out), rw, ps, V, units, parts);
+        static_cast<const char *>(logits), static_cast<char *>(out), rw, ps, V, units, piece, parts);
     return specv::cuda_ok(cudaGetLastError(), "launch process_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
