@@ -648,19 +648,19 @@ def _ptr(t, name, dtype, dev, n=-1):
     """data_ptr of a contiguous tensor of its type on the call's device, with n entries if n >= 0; None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.device != dev or not t.is_contiguous() or (n >= 0 and t.numel() != n):
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (n >= 0 and t.numel() != n):
         _check_dev(name, t, dtype)
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
         raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
     return t.data_ptr()
 
 
 def _launch(dev, stream, fn, what, *args):
-    """Calls fn(*args, stream) with `dev` current, on its current stream if none is given."""
+    """Calls fn(*args, stream) with device `dev` current, on its current stream if none is given."""
     import torch
-    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev.index:
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -675,9 +675,9 @@ def _rows_arg(logits, offsets, rows, draft_tokens, parent, i32):
         raise ValueError(f"rows must be one of {sorted(ROWS)}, got {rows!r}")
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, V]")
-    dev = logits.device
-    if dev.type != "cuda" or not logits.is_contiguous():
+    if not logits.is_cuda or not logits.is_contiguous():
         _check_dev("logits", logits)
+    dev = logits.get_device()
     R, B = logits.shape[0], offsets.numel() - 1
     if B < 0:
         raise ValueError("offsets must have B + 1 entries")
@@ -694,45 +694,41 @@ def _out_arg(logits, out, torch):
     if out is None:
         out = torch.empty_like(logits)
         return out, out.data_ptr()
-    return out, _ptr(out, "out", logits.dtype, logits.device, logits.numel())
+    return out, _ptr(out, "out", logits.dtype, logits.get_device(), logits.numel())
 
 
 def _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
                 bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32):
-    dev, V, B, R = logits.device, logits.shape[1], rw.B, rw.R
-    W, ps = (V + 31) // 32, _Logits()
+    dev, V, B, R = logits.get_device(), logits.shape[1], rw.B, rw.R
+    W = (V + 31) // 32
+    pen, bias, masks = (None, None, None, None, None, None, 0), (None, None, None, 0), (None, None, 0)
     if counts is not None:
         if seen is None or draft_tokens is None:
             raise ValueError("penalties need counts, seen and draft_tokens")
         if rows == "tree" and parent is None:
             raise ValueError("penalties on a tree need parent")
-        ps.S = S = counts.shape[0]
-        ps.repetition = _ptr(repetition, "repetition", f32, dev, B)
-        ps.frequency = _ptr(frequency, "frequency", f32, dev, B)
-        ps.presence = _ptr(presence, "presence", f32, dev, B)
-        ps.counts = _ptr(counts, "counts", i32, dev, S * V)
-        ps.seen = _ptr(seen, "seen", i32, dev, S * 2 * W)
-        ps.slots = _ptr(slots, "slots", i32, dev, B)
+        S = counts.shape[0]
+        pen = (_ptr(repetition, "repetition", f32, dev, B), _ptr(frequency, "frequency", f32, dev, B),
+               _ptr(presence, "presence", f32, dev, B), _ptr(counts, "counts", i32, dev, S * V),
+               _ptr(seen, "seen", i32, dev, S * 2 * W), _ptr(slots, "slots", i32, dev, B), S)
     elif not (repetition is None and frequency is None and presence is None and seen is None and slots is None):
         raise ValueError("penalties need counts, seen and draft_tokens")
     if bias_offsets is not None:
         if bias_tokens is None or bias_values is None:
             raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
-        ps.n_bias = n = bias_tokens.numel()
-        ps.bias_offsets = _ptr(bias_offsets, "bias_offsets", i32, dev, B + 1)
-        ps.bias_tokens = _ptr(bias_tokens, "bias_tokens", i32, dev)
-        ps.bias_values = _ptr(bias_values, "bias_values", f32, dev, n)
+        n = bias_tokens.numel()
+        bias = (_ptr(bias_offsets, "bias_offsets", i32, dev, B + 1), _ptr(bias_tokens, "bias_tokens", i32, dev),
+                _ptr(bias_values, "bias_values", f32, dev, n), n)
     elif not (bias_tokens is None and bias_values is None):
         raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
     if mask is not None:
-        ps.M = M = mask.shape[0]
+        M = mask.shape[0]
         if mask_rows is None and M < R:
             raise ValueError("mask needs a row for each row of logits, or mask_rows")
-        ps.mask = _ptr(mask, "mask", i32, dev, M * W)
-        ps.mask_rows = _ptr(mask_rows, "mask_rows", i32, dev, R)
+        masks = _ptr(mask, "mask", i32, dev, M * W), _ptr(mask_rows, "mask_rows", i32, dev, R), M
     elif mask_rows is not None:
         raise ValueError("mask_rows without mask")
-    return ps
+    return _Logits(*pen, *bias, *masks)
 
 
 def _truncate_arg(dev, B, temperature, top_k, top_p, min_p, i32, f32):
@@ -758,7 +754,7 @@ def spec_logits_process(logits, offsets, draft_tokens=None, *, rows="target", pa
     ps = _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
                      bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32)
     out, po = _out_arg(logits, out, torch)
-    _launch(logits.device, stream, lib().spec_logits_process, "spec_logits_process", logits.data_ptr(),
+    _launch(logits.get_device(), stream, lib().spec_logits_process, "spec_logits_process", logits.data_ptr(),
             ctypes.byref(rw), ctypes.byref(ps), logits.shape[1], dt, po)
     return out
 
@@ -772,9 +768,9 @@ def spec_logits_truncate(logits, temperature, offsets, *, rows="target", top_k=N
     import torch
     rw = _rows_arg(logits, offsets, rows, None, None, torch.int32)
     dt = _dtype_code(logits)
-    tr = _truncate_arg(logits.device, rw.B, temperature, top_k, top_p, min_p, torch.int32, torch.float32)
+    tr = _truncate_arg(logits.get_device(), rw.B, temperature, top_k, top_p, min_p, torch.int32, torch.float32)
     out, po = _out_arg(logits, out, torch)
-    _launch(logits.device, stream, lib().spec_logits_truncate, "spec_logits_truncate", logits.data_ptr(),
+    _launch(logits.get_device(), stream, lib().spec_logits_truncate, "spec_logits_truncate", logits.data_ptr(),
             ctypes.byref(rw), ctypes.byref(tr), logits.shape[1], dt, po)
     return out
 
@@ -791,9 +787,9 @@ def spec_logits_process_truncate(logits, temperature, offsets, draft_tokens=None
     dt = _dtype_code(logits)
     ps = _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
                      bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32)
-    tr = _truncate_arg(logits.device, rw.B, temperature, top_k, top_p, min_p, i32, f32)
+    tr = _truncate_arg(logits.get_device(), rw.B, temperature, top_k, top_p, min_p, i32, f32)
     out, po = _out_arg(logits, out, torch)
-    _launch(logits.device, stream, lib().spec_logits_process_truncate, "spec_logits_process_truncate",
+    _launch(logits.get_device(), stream, lib().spec_logits_process_truncate, "spec_logits_process_truncate",
             logits.data_ptr(), ctypes.byref(rw), ctypes.byref(ps), ctypes.byref(tr), logits.shape[1], dt, po)
     return out
 
@@ -802,9 +798,9 @@ def _state_arg(counts, seen, i32):
     if counts.dim() != 2:
         raise ValueError("counts must be [S, V]")
     S, V = counts.shape
-    dev = counts.device
-    if dev.type != "cuda":
+    if not counts.is_cuda:
         _check_dev("counts", counts)
+    dev = counts.get_device()
     return S, V, dev, _ptr(counts, "counts", i32, dev), _ptr(seen, "seen", i32, dev, S * 2 * ((V + 31) // 32))
 
 

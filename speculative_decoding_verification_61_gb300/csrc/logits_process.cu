@@ -90,12 +90,12 @@ struct GroupShared {
     uint64_t before[kMaxPath];  // tree: the nodes whose tokens a row follows
     uint32_t drafted[Group<STREAM>::kWords], biased[Group<STREAM>::kWords];
     int warp_sum[kWarps];
-    int column[kList], count[kList];
+    int column[kList];
     uint8_t flags[kList];
     int bias_token[kBias];
     float bias_value[kBias];
 };
-enum { kSeen = 1, kDrafted = 2, kBiased = 4 };
+enum { kPrompt = 1, kEmitted = 2, kDrafted = 4, kBiased = 8 };
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const char *row, int col) {
@@ -384,16 +384,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                         if (at_rank < 0 || at_rank >= kList) continue;
                         const int bit = __ffs(m) - 1;
                         sm.column[at_rank] = col0 + bit;
-                        sm.flags[at_rank] = static_cast<uint8_t>((prompt[i] >> bit & 1) * kSeen | (drafted[i] >> bit & 1) * kDrafted |
-                                                                 (biased[i] >> bit & 1) * kBiased);
-                        sm.count[at_rank] = emitted[i] >> bit & 1 ? __ldg(ps.counts + slot * V + col0 + bit) : 0;
+                        sm.flags[at_rank] = static_cast<uint8_t>((prompt[i] >> bit & 1) * kPrompt | (emitted[i] >> bit & 1) * kEmitted |
+                                                                 (drafted[i] >> bit & 1) * kDrafted | (biased[i] >> bit & 1) * kBiased);
                     }
                 }
                 G::sync();
                 // a thread takes a column, all its rows
                 for (int e = me; e < len; e += G::kSize) {
-                    const int col = sm.column[e], count = sm.count[e];
+                    const int col = sm.column[e];
                     const uint32_t f = sm.flags[e];
+                    const int count = f & kEmitted ? __ldg(ps.counts + slot * V + col) : 0;
                     float bias = 0.0f;
                     if (f & kBiased) {
                         // the same token twice: the entries add, in list order
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                                 const uint64_t before = tree ? sm.before[i + u] : rw.mode == SPEC_ROWS_NEXT ? (1ull << k) - 1 : (1ull << (i + u)) - 1;
                                 for (uint64_t d = before; d; d &= d - 1) c += sm.token[__ffsll(d) - 1] == col;
                             }
-                            if ((f & kSeen) || c > 0) z[u] = penalised(z[u], c, p);
+                            if ((f & kPrompt) || c > 0) z[u] = penalised(z[u], c, p);
                             if (f & kBiased) z[u] = __fadd_rn(z[u], bias);
                             store_logit<DT>(out + static_cast<int64_t>(row0 + i + u) * row_bytes, col, z[u]);
                         }
@@ -469,7 +469,11 @@ __global__ void __launch_bounds__(kUpdateThreads)
 // in shared memory from the entry's tokens and writes them out whole, so the
 // state is written once and needs no clearing before.
 constexpr int kResetThreads = 256;
-constexpr int kResetChunk = 4096;
+#ifndef SPEC_RESET_CHUNK
+#define SPEC_RESET_CHUNK 8192
+#endif
+constexpr int kResetChunk = SPEC_RESET_CHUNK;
+constexpr int kResetAhead = 8;  // tokens in flight per thread
 
 __global__ void __launch_bounds__(kResetThreads)
     reset_kernel(int32_t *counts, int32_t *seen, int S, int V, const int32_t *__restrict__ slots, int n,
@@ -487,24 +491,32 @@ __global__ void __launch_bounds__(kResetThreads)
     for (int i = tid; i < kResetChunk; i += kResetThreads) s_count[i] = 0;
     for (int i = tid; i < kResetChunk / 32; i += kResetThreads) s_prompt[i] = 0;
     if (__syncthreads_or(skip)) return;
-    for (int i = p0 + tid; i < p1; i += kResetThreads) {
-        const int t = __ldg(prompt_tokens + i);
-        if (t >= c0 && t < c0 + kResetChunk && t < V) atomicOr(&s_prompt[(t - c0) >> 5], 1u << (t & 31));
-    }
-    for (int i = q0 + tid; i < q1; i += kResetThreads) {
-        const int t = __ldg(output_tokens + i);
-        if (t >= c0 && t < c0 + kResetChunk && t < V) atomicAdd(&s_count[t - c0], 1);
-    }
+    // every chunk's CTA reads the whole lists (from L2), several tokens in flight a thread
+    auto each = [&](const int32_t *tokens, int first, int end, auto &&f) {
+        for (int i = first + tid; i < end; i += kResetThreads * kResetAhead) {
+            int t[kResetAhead];
+#pragma unroll
+            for (int u = 0; u < kResetAhead; ++u) t[u] = i + u * kResetThreads < end ? __ldg(tokens + i + u * kResetThreads) : -1;
+#pragma unroll
+            for (int u = 0; u < kResetAhead; ++u)
+                if (t[u] >= c0 && t[u] < c0 + kResetChunk && t[u] < V) f(t[u] - c0);
+        }
+    };
+    each(prompt_tokens, p0, p1, [&](int c) { atomicOr(&s_prompt[c >> 5], 1u << (c & 31)); });
+    each(output_tokens, q0, q1, [&](int c) { atomicAdd(&s_count[c], 1); });
     __syncthreads();
     const int64_t W = (V + 31) / 32;
     const int cols = min(kResetChunk, V - c0);
     int32_t *crow = counts + static_cast<int64_t>(slot) * V + c0;
-    for (int i = tid; i < cols; i += kResetThreads) crow[i] = s_count[i];
-    for (int w = tid; w < (cols + 31) / 32; w += kResetThreads) {
-        uint32_t m = 0;
-        for (int j = 0; j < 32; ++j) m |= (s_count[w * 32 + j] > 0 ? 1u : 0u) << j;
-        seen[static_cast<int64_t>(slot) * 2 * W + c0 / 32 + w] = static_cast<int32_t>(s_prompt[w]);
-        seen[(static_cast<int64_t>(slot) * 2 + 1) * W + c0 / 32 + w] = static_cast<int32_t>(m);
+    int32_t *srow = seen + static_cast<int64_t>(slot) * 2 * W + c0 / 32;
+    for (int i = tid; i < (cols + 31) / 32 * 32; i += kResetThreads) {
+        const int n = s_count[i];
+        if (i < cols) crow[i] = n;
+        const uint32_t m = __ballot_sync(0xffffffffu, n > 0);
+        if ((i & 31) == 0) {
+            srow[i >> 5] = static_cast<int32_t>(s_prompt[i >> 5]);
+            srow[W + (i >> 5)] = static_cast<int32_t>(m);
+        }
     }
 }
 
