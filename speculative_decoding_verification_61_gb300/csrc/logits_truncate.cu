@@ -183,9 +183,9 @@ struct Shared {
     float2 table[64];
     uint32_t count[kBins], lo[kBins], hi[kBins];
     uint64_t list[kList];
-    uint64_t warp_mass[kWarps];
-    uint32_t warp_count[kWarps];
-    uint32_t red[kWarps];
+    uint64_t warp_mass[32];
+    uint32_t warp_count[32];
+    uint32_t red[32];
     uint32_t n_list, key_lo, key_hi;
     // where the scan of the bins stopped
     int bin;
@@ -241,17 +241,17 @@ struct Goal {
 // leaves it with what lies above it in sm.bin, sm.above_*, sm.bin_count, and
 // the mass of everything in sm.total_mass.  Without a bin that reaches the
 // goal the last one that holds anything is taken.
+template <int T>
 __device__ __noinline__ void find_bin(Shared &sm, const Goal &goal, uint32_t above_count, uint64_t above_mass) {
-    constexpr int kPer = (kBins + kThreads - 1) / kThreads;
+    constexpr int kPer = kBins / T;
     uint32_t c = 0, ci[kPer];
     uint64_t m = 0, mi[kPer];
     const int first = threadIdx.x * kPer;
     if (threadIdx.x == 0) sm.bin = -1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const bool in = first + i < kBins;
-        ci[i] = in ? sm.count[first + i] : 0;
-        mi[i] = in ? static_cast<uint64_t>(sm.hi[first + i]) << 32 | sm.lo[first + i] : 0;
+        ci[i] = sm.count[first + i];
+        mi[i] = static_cast<uint64_t>(sm.hi[first + i]) << 32 | sm.lo[first + i];
         c += ci[i];
         m += mi[i];
     }
@@ -260,7 +260,7 @@ __device__ __noinline__ void find_bin(Shared &sm, const Goal &goal, uint32_t abo
     block_scan(sm, c, m);
     c += above_count;
     m += above_mass;
-    if (threadIdx.x == kThreads - 1) sm.total_mass = m + own_m;
+    if (threadIdx.x == T - 1) sm.total_mass = m + own_m;
     const bool here = goal.reached(c + own_c, m + own_m) && !goal.reached(c, m);
     if (here) {
 #pragma unroll
@@ -279,15 +279,27 @@ __device__ __noinline__ void find_bin(Shared &sm, const Goal &goal, uint32_t abo
     __syncthreads();
 }
 
-template <int DT, typename F>
+// f(value, index) for a row's elements, a thread's next vectors loaded before it works on these.
+template <int DT, int T, typename F>
 __device__ __forceinline__ void for_each(const char *row, int V, F &&f) {
-    constexpr int kPer = Elem<DT>::kPerVec;
+    // (bf16 rows come here rarely: small code, beside the pass that they usually take)
+    constexpr int kPer = Elem<DT>::kPerVec, kFlight = DT == SPEC_F32 ? 2 : 1;
     const uint4 *p = reinterpret_cast<const uint4 *>(row);
-    for (int v = threadIdx.x; v < V / kPer; v += kThreads) {
-        float x[kPer];
-        Elem<DT>::unpack(p[v], x);
+    const int vecs = V / kPer;
+    for (int v0 = threadIdx.x; v0 < vecs; v0 += T * kFlight) {
+        uint4 q[kFlight];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) f(x[i], v * kPer + i);
+        for (int u = 0; u < kFlight; ++u)
+            if (v0 + u * T < vecs) q[u] = p[v0 + u * T];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int v = v0 + u * T;
+            if (v >= vecs) break;
+            float x[kPer];
+            Elem<DT>::unpack(q[u], x);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) f(x[i], v * kPer + i);
+        }
     }
 }
 
@@ -306,8 +318,62 @@ __device__ __forceinline__ void add_to_bin(Shared &sm, int bin, bool mass, uint6
     }
 }
 
+template <int T>
 __device__ __forceinline__ void clear_bins(Shared &sm) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sm.count[i] = sm.lo[i] = sm.hi[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += T) sm.count[i] = sm.lo[i] = sm.hi[i] = 0;
+    __syncthreads();
+}
+
+// The list's n elements in the order, largest first (bitonic).
+template <int T>
+__device__ __noinline__ void sort_list(Shared &sm, uint32_t n) {
+    for (int i = n + threadIdx.x; i < kList; i += T) sm.list[i] = 0;
+    int size = 2;
+    while (size < static_cast<int>(n)) size <<= 1;
+    __syncthreads();
+    for (int k = 2; k <= size; k <<= 1) {  // bitonic, largest first
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            for (int t = threadIdx.x; t < size / 2; t += T) {
+                const int a = 2 * t - (t & (j - 1)), b = a + j;
+                const uint64_t x = sm.list[a], y = sm.list[b];
+                if ((x < y) == ((a & k) == 0)) {
+                    sm.list[a] = y;
+                    sm.list[b] = x;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// The goal's place in the sorted list, given what lies above it: sm.cut, and the
+// mass up to it in sm.mass.
+template <int T>
+__device__ __noinline__ void place_in_list(Shared &sm, uint32_t n, const Weights &w, Goal goal, bool mass, uint32_t above_count,
+                                           uint64_t above_mass) {
+    constexpr int kPer = kList / T;
+    uint32_t c = 0, ci[kPer];
+    uint64_t m = 0, mi[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int t = threadIdx.x * kPer + i;
+        ci[i] = t < static_cast<int>(n) ? 1 : 0;
+        mi[i] = ci[i] && mass ? fixed_weight(w, value_of(static_cast<uint32_t>(sm.list[t] >> 32))) : 0;
+        c += ci[i];
+        m += mi[i];
+    }
+    block_scan(sm, c, m);
+    c += above_count;
+    m += above_mass;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (ci[i] && goal.reached(c + 1, m + mi[i]) && !goal.reached(c, m)) {
+            sm.cut = sm.list[threadIdx.x * kPer + i];
+            sm.mass = m + mi[i];
+        }
+        c += ci[i];
+        m += mi[i];
+    }
     __syncthreads();
 }
 
@@ -315,7 +381,7 @@ __device__ __forceinline__ void clear_bins(Shared &sm) {
 // sorted if they fit the list, else the bin is split by key until they do or
 // one value is left, whose ties go by index.  Leaves the place in sm.cut, and
 // the mass of the tokens up to it in sm.mass.
-template <int DT>
+template <int DT, int T>
 __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, const Weights &w, float scale,
                                         const Goal &goal, bool mass) {
     const int bin = sm.bin;
@@ -329,7 +395,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
     }
     __syncthreads();
     uint32_t klo = 0xffffffffu, khi = 0;
-    for_each<DT>(row, V, [&](float z, int i) {
+    for_each<DT, T>(row, V, [&](float z, int i) {
         if (first_bin(z, w.zmax, scale) != bin) return;
         const uint32_t key = key_of(z);
         klo = min(klo, key);
@@ -349,14 +415,14 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
     while (!listed && klo < khi) {
         // 2048 equal parts of the keys khi .. klo
         const int shift = max(0, 32 - __clz(khi - klo) - 11);
-        clear_bins(sm);
-        for_each<DT>(row, V, [&](float z, int) {
+        clear_bins<T>(sm);
+        for_each<DT, T>(row, V, [&](float z, int) {
             const uint32_t key = key_of(z);
             if (key < klo || key > khi) return;
             add_to_bin(sm, static_cast<int>((khi - key) >> shift), mass, mass ? fixed_weight(w, z) : 0);
         });
         __syncthreads();
-        find_bin(sm, goal, above_count, above_mass);
+        find_bin<T>(sm, goal, above_count, above_mass);
         const uint32_t j = static_cast<uint32_t>(sm.bin);
         const uint32_t top = khi - (j << shift);
         const uint32_t width = (1u << shift) - 1;
@@ -369,7 +435,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
         if (n <= kList) {
             if (threadIdx.x == 0) sm.n_list = 0;
             __syncthreads();
-            for_each<DT>(row, V, [&](float z, int i) {
+            for_each<DT, T>(row, V, [&](float z, int i) {
                 const uint32_t key = key_of(z);
                 if (key >= klo && key <= khi) sm.list[atomicAdd(&sm.n_list, 1u)] = place_of(key, i);
             });
@@ -378,47 +444,8 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
         }
     }
     if (listed) {
-        for (int i = n + threadIdx.x; i < kList; i += kThreads) sm.list[i] = 0;
-        int size = 2;
-        while (size < static_cast<int>(n)) size <<= 1;
-        __syncthreads();
-        for (int k = 2; k <= size; k <<= 1) {  // bitonic, largest first
-            for (int j = k >> 1; j > 0; j >>= 1) {
-                for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-                    const int a = 2 * t - (t & (j - 1)), b = a + j;
-                    const uint64_t x = sm.list[a], y = sm.list[b];
-                    if ((x < y) == ((a & k) == 0)) {
-                        sm.list[a] = y;
-                        sm.list[b] = x;
-                    }
-                }
-                __syncthreads();
-            }
-        }
-        constexpr int kPer = (kList + kThreads - 1) / kThreads;
-        uint32_t c = 0, ci[kPer];
-        uint64_t m = 0, mi[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int t = threadIdx.x * kPer + i;
-            ci[i] = t < static_cast<int>(n) ? 1 : 0;
-            mi[i] = ci[i] && mass ? fixed_weight(w, value_of(static_cast<uint32_t>(sm.list[t] >> 32))) : 0;
-            c += ci[i];
-            m += mi[i];
-        }
-        block_scan(sm, c, m);
-        c += above_count;
-        m += above_mass;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (ci[i] && goal.reached(c + 1, m + mi[i]) && !goal.reached(c, m)) {
-                sm.cut = sm.list[threadIdx.x * kPer + i];
-                sm.mass = m + mi[i];
-            }
-            c += ci[i];
-            m += mi[i];
-        }
-        __syncthreads();
+        sort_list<T>(sm, n);
+        place_in_list<T>(sm, n, w, goal, mass, above_count, above_mass);
         return;
     }
     // one value: how many of its ties the goal takes, and the last one's index
@@ -439,7 +466,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
     if (take < n) {
         // a thread owns a run of vectors: count its ties, then find the one
         constexpr int kPer = Elem<DT>::kPerVec;
-        const int vecs = V / kPer, per = (vecs + kThreads - 1) / kThreads;
+        const int vecs = V / kPer, per = (vecs + T - 1) / T;
         const int v0 = min(vecs, static_cast<int>(threadIdx.x) * per), v1 = min(vecs, v0 + per);
         const uint4 *p = reinterpret_cast<const uint4 *>(row);
         uint32_t c = 0;
@@ -542,12 +569,12 @@ __device__ __forceinline__ int sequence_of(const Rows &rw, int b, int64_t r) {
 // below it goes; 0: the row stays as it is.  Passes over the row: its largest
 // value, a histogram over 32 bins per halving of the weight, the border bin's
 // elements, sorted.
-template <int DT>
+template <int DT, int T>
 __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, const Settings &s) {
     const int tid = threadIdx.x;
     uint32_t top = 0;
     bool nan = false;
-    for_each<DT>(row, V, [&](float z, int) {
+    for_each<DT, T>(row, V, [&](float z, int) {
         nan |= z != z;
         top = max(top, key_of(z));
     });
@@ -555,7 +582,7 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
     __syncthreads();
     if ((tid & 31) == 0) sm.red[tid >> 5] = top;
     nan = __syncthreads_or(nan);
-    for (int i = 0; i < kWarps; ++i) top = max(top, sm.red[i]);
+    for (int i = 0; i < T / 32; ++i) top = max(top, sm.red[i]);
     const float zmax = value_of(top);
     if (nan || !isfinite(zmax)) return 0;  // NaN, +inf, or nothing but -inf
     if (tid == 0) {
@@ -570,35 +597,65 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
     if (s.k > 0 || mass) {
         Goal goal{false, static_cast<uint32_t>(s.k), 0};
         uint64_t Z = 0;
-        auto fill = [&]() {
-            clear_bins(sm);
-            for_each<DT>(row, V, [&](float z, int) {
+        auto fill = [&](bool mass) {
+            clear_bins<T>(sm);
+            for_each<DT, T>(row, V, [&](float z, int) {
                 add_to_bin(sm, first_bin(z, zmax, scale), mass, mass ? fixed_weight(w, z) : 0);
             });
             __syncthreads();
         };
-        fill();
-        if (s.k > 0) {
-            find_bin(sm, goal, 0, 0);
+        bool done = false;
+        if (s.k > 0 && s.k <= kList) {
+            // few tokens: they are listed and sorted, and only theirs are the weights that matter
+            fill(false);
+            find_bin<T>(sm, goal, 0, 0);
+            const int bin = sm.bin;
+            const uint32_t n = sm.above_count + sm.bin_count;
+            __syncthreads();
+            done = n <= kList;
+            if (done) {
+                if (tid == 0) sm.n_list = 0;
+                __syncthreads();
+                for_each<DT, T>(row, V, [&](float z, int i) {
+                    if (first_bin(z, zmax, scale) <= bin) sm.list[atomicAdd(&sm.n_list, 1u)] = place_of(key_of(z), i);
+                });
+                __syncthreads();
+                sort_list<T>(sm, n);
+                place_in_list<T>(sm, n, w, goal, mass, 0, 0);
+                cut = sm.cut;
+                Z = sm.mass;
+                __syncthreads();
+                if (mass) {
+                    if (tid == 0) sm.target = mass_target(s.p, Z);
+                    __syncthreads();
+                    place_in_list<T>(sm, s.k, w, Goal{true, 0, sm.target}, true, 0, 0);
+                    cut = sm.cut;
+                    __syncthreads();
+                }
+            }
+        }
+        if (!done) fill(mass);
+        if (s.k > 0 && !done) {
+            find_bin<T>(sm, goal, 0, 0);
             const bool splits = sm.bin_count > kList;  // find_place then uses the bins itself
-            find_place<DT>(sm, row, V, w, scale, goal, mass);
+            find_place<DT, T>(sm, row, V, w, scale, goal, mass);
             cut = sm.cut;
             Z = sm.mass;
             __syncthreads();
-            if (mass && splits) fill();
+            if (mass && splits) fill(true);
         }
-        if (mass) {
+        if (mass && !done) {
             goal.by_mass = true;
             if (s.k == 0) {
-                find_bin(sm, goal, 0, 0);
+                find_bin<T>(sm, goal, 0, 0);
                 Z = sm.total_mass;
                 __syncthreads();
             }
             if (tid == 0) sm.target = mass_target(s.p, Z);
             __syncthreads();
             goal.target = sm.target;
-            find_bin(sm, goal, 0, 0);
-            find_place<DT>(sm, row, V, w, scale, goal, true);
+            find_bin<T>(sm, goal, 0, 0);
+            find_place<DT, T>(sm, row, V, w, scale, goal, true);
             cut = max(cut, sm.cut);
         }
     }
@@ -608,11 +665,11 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
 }
 
 // The row with -inf below the cut.
-template <int DT>
+template <int DT, int T>
 __device__ __forceinline__ void write_cut(const char *row, uint4 *dst, int V, uint64_t cut) {
     constexpr int kPer = Elem<DT>::kPerVec;
     const uint32_t ckey = static_cast<uint32_t>(cut >> 32), cidx = ~static_cast<uint32_t>(cut);
-    for (int v = threadIdx.x; v < V / kPer; v += kThreads) {
+    for (int v = threadIdx.x; v < V / kPer; v += T) {
         uint4 q = reinterpret_cast<const uint4 *>(row)[v];
         float x[kPer];
         Elem<DT>::unpack(q, x);
@@ -636,35 +693,51 @@ __device__ __forceinline__ void fill_nan(uint4 *dst, int64_t vecs, int64_t first
 }
 
 // Rows of any kind, a CTA per row at a time, neighbouring rows at the same time.
-template <int DT>
-__global__ void __launch_bounds__(kThreads, kPerSm)
-    truncate_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
-    extern __shared__ char smem[];
+// A row that fits stays in shared memory from the first pass on (`held`).
+template <int DT, int T>
+__global__ void __launch_bounds__(T, 1024 / T)
+    truncate_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V, bool held) {
+    extern __shared__ __align__(16) char smem[];
     Shared &sm = *reinterpret_cast<Shared *>(smem);
+    char *hold = smem + (sizeof(Shared) + 15) / 16 * 16;
     const int tid = threadIdx.x;
     const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
     const int vecs = V / Elem<DT>::kPerVec;
     fill_table(sm.table);
     const int oB = __ldg(rw.offsets + rw.B);
     const int64_t rows_all = rw.first_row(rw.B, oB);
-    int64_t r = blockIdx.x;
     if (!check_rows(rw, false)) {
         fill_nan<DT>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
-                     static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
+                     static_cast<int64_t>(blockIdx.x) * T + tid, static_cast<int64_t>(gridDim.x) * T);
         return;
     }
     int b = 0;
-    for (; r < rows_all; r += gridDim.x) {
+    for (int64_t r = blockIdx.x; r < rows_all; r += gridDim.x) {
         b = sequence_of(rw, b, r);
         const char *row = logits + r * row_bytes;
         uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
         const Settings s = load_settings(tr, b, V);
         if (!s.valid) {
-            fill_nan<DT>(dst, vecs, tid, kThreads);
+            fill_nan<DT>(dst, vecs, tid, T);
             continue;
         }
-        const uint64_t cut = s.active ? cut_of_row<DT>(sm, row, V, s) : 0;
-        if (cut != 0 || logits != out) write_cut<DT>(row, dst, V, cut);
+        if (s.active && held) {
+            __syncthreads();  // the last row has been written
+            constexpr int kFlight = 4;
+            for (int v0 = tid; v0 < vecs; v0 += T * kFlight) {
+                uint4 q[kFlight];
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u)
+                    if (v0 + u * T < vecs) q[u] = reinterpret_cast<const uint4 *>(row)[v0 + u * T];
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u)
+                    if (v0 + u * T < vecs) reinterpret_cast<uint4 *>(hold)[v0 + u * T] = q[u];
+            }
+            __syncthreads();
+            row = hold;
+        }
+        const uint64_t cut = s.active ? cut_of_row<DT, T>(sm, row, V, s) : 0;
+        if (cut != 0 || logits != out) write_cut<DT, T>(row, dst, V, cut);
     }
 }
 
@@ -1133,8 +1206,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             __syncthreads();
             if (tid < 64) all.any.table[tid] = all.table[tid];
             __syncthreads();
-            const uint64_t cut = cut_of_row<SPEC_BF16>(all.any, reinterpret_cast<const char *>(row), V, s);
-            if (cut != 0 || logits != out) write_cut<SPEC_BF16>(reinterpret_cast<const char *>(row), dst, V, cut);
+            const uint64_t cut = cut_of_row<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), V, s);
+            if (cut != 0 || logits != out) write_cut<SPEC_BF16, kThreads>(reinterpret_cast<const char *>(row), dst, V, cut);
             continue;
         }
         // --- the border value: the lowest one kept, and how its ties go
@@ -1263,16 +1336,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     }
 }
 
+constexpr int kMostHeld = 190 * 1024;  // bytes of a row kept in shared memory
+constexpr int kAnyShared = (sizeof(Shared) + 15) / 16 * 16;
+constexpr int any_threads(int dt) { return dt == SPEC_F32 ? 1024 : kThreads; }
+
 template <int DT>
 int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms,
                     cudaStream_t stream) {
-    const int grid = std::min(rw.R, sms * kPerSm);
     const char *in = static_cast<const char *>(logits);
     char *to = static_cast<char *>(out);
     if (DT == SPEC_BF16 && V <= kMaxFastV) {
-        truncate_bf16_kernel<<<grid, kThreads, sizeof(BothShared), stream>>>(in, to, rw, tr, V);
+        truncate_bf16_kernel<<<std::min(rw.R, sms * kPerSm), kThreads, sizeof(BothShared), stream>>>(in, to, rw, tr, V);
     } else {
-        truncate_kernel<DT><<<grid, kThreads, sizeof(Shared), stream>>>(in, to, rw, tr, V);
+        constexpr int T = any_threads(DT);
+        const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
+        const bool held = DT == SPEC_F32 && bytes <= kMostHeld;
+        truncate_kernel<DT, T><<<std::min(rw.R, sms * 1024 / T), T, kAnyShared + (held ? bytes : 0), stream>>>(in, to, rw, tr,
+                                                                                                          V, held);
     }
     return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
@@ -1290,7 +1370,10 @@ namespace specv {
 bool set_logits_attrs() {
     return cuda_ok(cudaFuncSetAttribute(speclog::truncate_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         sizeof(speclog::BothShared)),
-                   "cudaFuncSetAttribute(truncate_bf16_kernel)");
+                   "cudaFuncSetAttribute(truncate_bf16_kernel)") &&
+           cuda_ok(cudaFuncSetAttribute(speclog::truncate_kernel<SPEC_F32, speclog::any_threads(SPEC_F32)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        speclog::kAnyShared + speclog::kMostHeld),
+                   "cudaFuncSetAttribute(truncate_kernel)");
 }
 }  // namespace specv
 
