@@ -216,14 +216,23 @@ __device__ __forceinline__ void block_scan(Shared &sm, uint32_t &c, uint64_t &m)
         sm.warp_mass[warp] = m;
     }
     __syncthreads();
-    uint32_t bc = 0;
-    uint64_t bm = 0;
-    for (int i = 0; i < warp; ++i) {
-        bc += sm.warp_count[i];
-        bm += sm.warp_mass[i];
+    // the sums of the warps before: every warp scans them for itself
+    const int warps = static_cast<int>(blockDim.x) >> 5;
+    uint32_t bc = lane < warps ? sm.warp_count[lane] : 0;
+    uint64_t bm = lane < warps ? sm.warp_mass[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t cc = __shfl_up_sync(0xffffffffu, bc, off);
+        const uint64_t mm = __shfl_up_sync(0xffffffffu, bm, off);
+        if (lane >= off) {
+            bc += cc;
+            bm += mm;
+        }
     }
-    c += bc - c0;
-    m += bm - m0;
+    bc = __shfl_sync(0xffffffffu, bc, (warp + 31) & 31);
+    bm = __shfl_sync(0xffffffffu, bm, (warp + 31) & 31);
+    c += (warp ? bc : 0) - c0;
+    m += (warp ? bm : 0) - m0;
 }
 
 // What a search looks for: the first place in the order where the tokens up
@@ -303,9 +312,9 @@ __device__ __forceinline__ void for_each(const char *row, int V, F &&f) {
     }
 }
 
+// (scale is finite, so the largest value is in bin 0)
 __device__ __forceinline__ int first_bin(float z, float zmax, float scale) {
-    const float f = __fmul_rn(__fsub_rn(zmax, z), scale);
-    return f >= static_cast<float>(kBins - 1) ? kBins - 1 : static_cast<int>(f);
+    return static_cast<int>(fminf(__fmul_rn(__fsub_rn(zmax, z), scale), static_cast<float>(kBins - 1)));
 }
 
 __device__ __forceinline__ void add_to_bin(Shared &sm, int bin, bool mass, uint64_t w) {
@@ -572,26 +581,25 @@ __device__ __forceinline__ int sequence_of(const Rows &rw, int b, int64_t r) {
 template <int DT, int T>
 __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, const Settings &s) {
     const int tid = threadIdx.x;
-    uint32_t top = 0;
-    bool nan = false;
-    for_each<DT, T>(row, V, [&](float z, int) {
-        nan |= z != z;
-        top = max(top, key_of(z));
-    });
-    top = __reduce_max_sync(0xffffffffu, top);
+    float top = __int_as_float(0xff800000);
+    for_each<DT, T>(row, V, [&](float z, int) { top = specv::fmax_nan(top, z); });
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = specv::fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
     __syncthreads();
-    if ((tid & 31) == 0) sm.red[tid >> 5] = top;
-    nan = __syncthreads_or(nan);
-    for (int i = 0; i < T / 32; ++i) top = max(top, sm.red[i]);
-    const float zmax = value_of(top);
-    if (nan || !isfinite(zmax)) return 0;  // NaN, +inf, or nothing but -inf
+    if ((tid & 31) == 0) sm.red[tid >> 5] = __float_as_uint(top);
+    __syncthreads();
+    top = __uint_as_float(sm.red[tid & (T / 32 - 1)]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = specv::fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float zmax = value_of(key_of(top));  // (+0 for -0)
+    if (!isfinite(top)) return 0;  // NaN, +inf, or nothing but -inf
     if (tid == 0) {
         set_scale(sm.row, s);
         if (s.m > 0.0f) sm.row.min_p_key = min_p_key(zmax, s.T, s.m);
     }
     __syncthreads();
     const Weights w = row_weights(sm.row, zmax, V, sm.table);
-    const float scale = w.ch * kBinsPerOctave;
+    const float scale = fminf(w.ch * kBinsPerOctave, 3.0e38f);
     const bool mass = s.p < 1.0f;
     uint64_t cut = 0;
     if (s.k > 0 || mass) {
