@@ -787,7 +787,6 @@ struct FastShared {
     int place, take, ties;
     int cut_group, cut_index;
     bool elsewhere;  // not in the bins
-    bool finite_low;  // a value at or below -2^16 that is not -inf
 
     // how often each group holds the border value: written once the bins are done with
     __device__ uint16_t *group_ties() { return reinterpret_cast<uint16_t *>(hist); }
@@ -817,7 +816,28 @@ struct BothShared {
     // apart from the union: kept over the rows
     float2 table[64];
     RowConstants row;
+    // in a cluster, CTA 0's: what the CTAs' shares of a row hold, what it found, each CTA's ties
+    uint32_t odd;
+    int place, take, ties;
+    bool slow;
+    uint32_t rank_ties[8];
 };
+
+// The cluster's barrier, this CTA's number in it, another CTA's copy of a shared object.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+template <typename X>
+__device__ __forceinline__ X *cluster_map(X *p, uint32_t rank) {
+    uint64_t a;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(p), "r"(rank));
+    return reinterpret_cast<X *>(a);
+}
 
 __device__ __forceinline__ float place_value(int place) {
     const int neg = place - (kSideSegs + 1) * kSegPlaces;
@@ -1054,6 +1074,9 @@ __device__ __forceinline__ uint32_t max_key(const uint4 &q) {
     return key16(__bfloat16_as_ushort(__hmax(__low2bfloat16(m), __high2bfloat16(m))));
 }
 
+// CL CTAs of a cluster share a row, each a run of its groups: CTA 0 adds up the
+// histograms and finds the border for all.
+template <int CL>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     truncate_bf16_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
     extern __shared__ char smem[];
@@ -1062,28 +1085,36 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row_bytes = static_cast<int64_t>(V) * 2;
     const int vecs = V / 8, groups = (vecs + 31) / 32;
+    // this CTA's groups, and CTA 0's shared memory
+    const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0, part = (groups + CL - 1) / CL;
+    const int gb = min(groups, rank * part), ge = min(groups, gb + part), vb = gb * 32, ve = min(vecs, ge * 32);
+    BothShared &lead = CL > 1 ? *cluster_map(&all, 0) : all;
     fill_table(all.table);
     const int oB = __ldg(rw.offsets + rw.B);
     const int64_t rows_all = rw.first_row(rw.B, oB);
-    int64_t r = blockIdx.x;
+    int64_t r = blockIdx.x / CL;
     if (!check_rows(rw, false)) {
         fill_nan<SPEC_BF16>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                             static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
     }
+    if (CL > 1) {
+        if (tid == 0) all.odd = 0;
+        cluster_sync();
+    }
     int b = 0;
-    for (; r < rows_all; r += gridDim.x) {
+    for (; r < rows_all; r += gridDim.x / CL) {
         b = sequence_of(rw, b, r);
         const uint4 *row = reinterpret_cast<const uint4 *>(logits + r * row_bytes);
         uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
         const Settings s = load_settings(tr, b, V);
         if (!s.valid) {
-            fill_nan<SPEC_BF16>(dst, vecs, tid, kThreads);
+            fill_nan<SPEC_BF16>(dst, ve, vb + tid, kThreads);
             continue;
         }
         if (!s.active) {
             if (logits != out)
-                for (int v = tid; v < vecs; v += kThreads) dst[v] = row[v];
+                for (int v = vb + tid; v < ve; v += kThreads) dst[v] = row[v];
             continue;
         }
         const bool mass = s.p < 1.0f, counted = mass || s.k > 0;
@@ -1099,7 +1130,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             sm.zeros = 0;
             sm.first = kPlaces;
             sm.elsewhere = false;
-            sm.finite_low = false;
         }
         __syncthreads();
         uint32_t odd = 0;
@@ -1109,27 +1139,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int v = (g0 + u * kWarps) * 32 + lane;
-                    to[u] = v < vecs ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                    to[u] = v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
                 }
             };
-            load(q, warp);
-            for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
+            load(q, gb + warp);
+            for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
                 load(next, g0 + kWarps * kAhead);
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    if (g0 + u * kWarps >= groups) break;
+                    if (g0 + u * kWarps >= ge) break;
                     count_values(sm, q[u], &odd);
                     const uint32_t key = __reduce_max_sync(0xffffffffu, max_key(q[u]));
-                    if (lane == 0) sm.group_max[g0 + u * kWarps] = static_cast<uint16_t>(key);
+                    if (lane == 0) sm.group_max[g0 + u * kWarps - gb] = static_cast<uint16_t>(key);
                 }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) q[u] = next[u];
             }
         }
-        if (odd & kFiniteLow) sm.finite_low = true;
-        bool slow = __syncthreads_or(odd & kOdd) != 0;
+        const uint32_t odd_all = (__syncthreads_or(odd & kOdd) ? kOdd : 0) | (__syncthreads_or(odd & kFiniteLow) ? kFiniteLow : 0);
+        bool slow = (odd_all & kOdd) != 0;
+        if (CL > 1) {
+            if (tid == 0 && odd_all) atomicOr(&lead.odd, odd_all);
+            cluster_sync();  // CTA 0's histogram is there to be added to
+            if (rank > 0) {
+                for (int i = tid; i < 2 * kSide; i += kThreads)
+                    if (const uint32_t n = sm.hist[i]) atomicAdd(&lead.fast.hist[i], n);
+                if (tid == 0 && sm.zeros) atomicAdd(&lead.fast.zeros, sm.zeros);
+            }
+            cluster_sync();
+            slow = (lead.odd & kOdd) != 0;
+        }
+        const bool finite_low = ((CL > 1 ? all.odd : odd_all) & kFiniteLow) != 0;  // (CTA 0's is meant)
         float zmax = 0.0f;
-        if (!slow) {
+        if (!slow && rank == 0) {
             // --- the bins' sums by segments of 32
             int first = kPlaces;
             for (int g = warp; g < kSegs; g += kWarps) {
@@ -1154,9 +1196,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             if (!slow) zmax = place_value(first);
         }
         // (values at or below -2^16 have no weight, and min-p excludes them)
-        if (!slow && !((-65536.0f - zmax) * specv::temp_scale(s.T) < -150.0f)) slow = true;
+        if (rank == 0 && !slow && !((-65536.0f - zmax) * specv::temp_scale(s.T) < -150.0f)) slow = true;
         Weights w{};
-        if (!slow) {
+        if (!slow && rank == 0) {
             w = row_weights(all.row, zmax, V, all.table);
             if (mass) {
                 for (int g = warp; g < kSegs; g += kWarps) {
@@ -1184,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                     if (k.place >= 0) {
                         take = s.k - k.above_count;
                         if (mass) Z = k.above_mass + TokenWeight(w, place_value(k.place)).times(take);
-                    } else if (!sm.finite_low) {
+                    } else if (!finite_low) {
                         k = Border{kPlaces, 0, 0, 0};  // fewer than k tokens are not -inf: all of them
                     }
                 }
@@ -1210,7 +1252,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             __syncthreads();
             slow = sm.elsewhere;
         }
+        if (CL > 1) {
+            __syncthreads();  // every thread of CTA 0 has read `odd`
+            if (rank == 0 && tid == 0) {
+                all.place = sm.place;
+                all.take = sm.take;
+                all.ties = sm.ties;
+                all.slow = slow;
+                all.odd = 0;
+            }
+            cluster_sync();
+            slow = lead.slow;
+        }
         if (slow) {
+            if (rank > 0) continue;
             __syncthreads();
             if (tid < 64) all.any.table[tid] = all.table[tid];
             __syncthreads();
@@ -1222,12 +1277,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         uint32_t border = 0xff80u;  // -inf: everything
         bool split = false;
         if (counted) {
-            if (sm.place < kPlaces) border = __float_as_uint(place_value(sm.place)) >> 16;
-            split = sm.take < sm.ties;
+            const int place = CL > 1 ? lead.place : sm.place;
+            if (place < kPlaces) border = __float_as_uint(place_value(place)) >> 16;
+            split = CL > 1 ? lead.take < lead.ties : sm.take < sm.ties;
         }
         if (s.m > 0.0f) {
             // the lowest bf16 value at or above min-p's border
-            const float f = value_of(all.row.min_p_key);
+            const float f = value_of(lead.row.min_p_key);
             uint32_t h = __bfloat16_as_ushort(__float2bfloat16_ru(f));
             if ((h & 0x7fffu) == 0) h = 0;
             if (!counted || __uint_as_float(h << 16) > __uint_as_float(border << 16)) {
@@ -1238,40 +1294,51 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         const uint32_t pair = border | border << 16;
         // groups below the border (as keys; a zero border takes -0 too)
         const uint32_t low = key16(border == 0 ? 0x8000u : border);
-        int cut_group = groups, cut_index = 0;
+        int cut_group = ge, cut_index = -1;
         if (split) {
-            const int take = sm.take;
-            for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
+            int take = CL > 1 ? lead.take : sm.take;
+            for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
                 uint4 q[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int g = g0 + u * kWarps, v = g * 32 + lane;
                     q[u] = make_uint4(~pair, ~pair, ~pair, ~pair);
-                    if (g < groups && sm.group_max[g] >= low && v < vecs) q[u] = row[v];
+                    if (g < ge && sm.group_max[g - gb] >= low && v < ve) q[u] = row[v];
                 }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int g = g0 + u * kWarps;
-                    if (g >= groups) break;
+                    if (g >= ge) break;
                     uint32_t n = __popc(equal_mask(q[u].x, pair)) + __popc(equal_mask(q[u].y, pair)) +
                                  __popc(equal_mask(q[u].z, pair)) + __popc(equal_mask(q[u].w, pair));
                     n = __reduce_add_sync(0xffffffffu, n >> 4);
-                    if (lane == 0) sm.group_ties()[g] = static_cast<uint16_t>(n);
+                    if (lane == 0) sm.group_ties()[g - gb] = static_cast<uint16_t>(n);
                 }
             }
             __syncthreads();
+            // a warp's running sums of the groups' ties
+            constexpr int kRun = kMaxGroups / 32;
+            uint32_t n = 0, c = 0;
+            const int g0 = lane * kRun, g1 = min(ge - gb, g0 + kRun);
             if (warp == 0) {
-                // the group where the ties run out, then the token
-                constexpr int kRun = kMaxGroups / 32;
-                uint32_t n = 0;
-                const int g0 = lane * kRun, g1 = min(groups, g0 + kRun);
                 for (int g = g0; g < g1; ++g) n += sm.group_ties()[g];
-                uint32_t c = n;
+                c = n;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
                     const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
                     if (lane >= off) c += cc;
                 }
+            }
+            bool here = true;  // the ties run out in this CTA's groups
+            if (CL > 1) {
+                if (tid == 31) lead.rank_ties[rank] = c;
+                cluster_sync();
+                for (int i = 0; i < rank; ++i) take -= lead.rank_ties[i];
+                here = take > 0 && take < static_cast<int>(lead.rank_ties[rank]);
+                if (take <= 0) cut_group = gb;
+            }
+            if (here && warp == 0) {
+                // the group where they do, then the token
                 const int owner = __ffs(__ballot_sync(0xffffffffu, c >= static_cast<uint32_t>(take))) - 1;
                 c -= n;
                 int g = g0;
@@ -1279,9 +1346,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                     while (c + sm.group_ties()[g] < static_cast<uint32_t>(take)) c += sm.group_ties()[g++];
                 g = __shfl_sync(0xffffffffu, g, owner);
                 c = __shfl_sync(0xffffffffu, c, owner);
-                const int v = g * 32 + lane;
+                const int v = (gb + g) * 32 + lane;
                 uint32_t bits = 0;  // a bit per tie of this lane's vector
-                if (v < vecs) {
+                if (v < ve) {
                     const uint4 q = row[v];
                     const uint32_t e[4] = {equal_mask(q.x, pair), equal_mask(q.y, pair), equal_mask(q.z, pair), equal_mask(q.w, pair)};
 #pragma unroll
@@ -1297,32 +1364,34 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 before += c - own;
                 if (before < static_cast<uint32_t>(take) && before + own >= static_cast<uint32_t>(take)) {
                     for (int left = take - before; left > 1; --left) bits &= bits - 1;
-                    sm.cut_group = g;
+                    sm.cut_group = gb + g;
                     sm.cut_index = v * 8 + __ffs(bits) - 1;
                 }
             }
             __syncthreads();
-            cut_group = sm.cut_group;
-            cut_index = sm.cut_index;
+            if (here) {
+                cut_group = sm.cut_group;
+                cut_index = sm.cut_index;
+            }
         }
         // --- the row out: groups below the border need not be read again
-        for (int g0 = warp; g0 < groups; g0 += kWarps * kAhead) {
+        for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
             uint4 q[kAhead];
             bool kept[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int g = g0 + u * kWarps;
-                kept[u] = g < groups && sm.group_max[g] >= low;
+                kept[u] = g < ge && sm.group_max[g - gb] >= low;
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int v = (g0 + u * kWarps) * 32 + lane;
-                q[u] = kept[u] && v < vecs ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                q[u] = kept[u] && v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int g = g0 + u * kWarps, v = g * 32 + lane;
-                if (v >= vecs) continue;
+                if (v >= ve) continue;
                 if (kept[u]) {
                     uint32_t x[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
                     const bool equal = g < cut_group;
@@ -1342,6 +1411,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             }
         }
     }
+    if (CL > 1) cluster_sync();  // CTA 0's shared memory is read until here
+}
+
+template <int CL>
+cudaError_t launch_bf16(const char *in, char *to, const Rows &rw, const Truncate &tr, int V, int sms, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(rw.R, sms * kPerSm / CL) * CL);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(BothShared);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CL;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, truncate_bf16_kernel<CL>, in, to, rw, tr, V);
 }
 
 constexpr int kMostHeld = 190 * 1024;  // bytes of a row kept in shared memory
@@ -1354,7 +1440,11 @@ int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncat
     const char *in = static_cast<const char *>(logits);
     char *to = static_cast<char *>(out);
     if (DT == SPEC_BF16 && V <= kMaxFastV) {
-        truncate_bf16_kernel<<<std::min(rw.R, sms * kPerSm), kThreads, sizeof(BothShared), stream>>>(in, to, rw, tr, V);
+        // few rows: clusters of CTAs share them, while every warp has groups of its own
+        int cl = 1;
+        while (cl < 8 && static_cast<int64_t>(rw.R) * cl * 2 <= static_cast<int64_t>(sms) * kPerSm && V >= cl * 2 * kWarps * kGroupCols) cl *= 2;
+        const auto launch = cl == 8 ? launch_bf16<8> : cl == 4 ? launch_bf16<4> : cl == 2 ? launch_bf16<2> : launch_bf16<1>;
+        return specv::cuda_ok(launch(in, to, rw, tr, V, sms, stream), "launch truncate_bf16_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
     } else {
         constexpr int T = any_threads(DT);
         const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
@@ -1376,9 +1466,12 @@ inline int check_truncate_args(const spec_truncate_t *t, const Rows &rw, Truncat
 
 namespace specv {
 bool set_logits_attrs() {
-    return cuda_ok(cudaFuncSetAttribute(speclog::truncate_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        sizeof(speclog::BothShared)),
-                   "cudaFuncSetAttribute(truncate_bf16_kernel)") &&
+    const auto bf16 = [](auto kernel) {
+        return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(speclog::BothShared)),
+                       "cudaFuncSetAttribute(truncate_bf16_kernel)");
+    };
+    return bf16(speclog::truncate_bf16_kernel<1>) && bf16(speclog::truncate_bf16_kernel<2>) &&
+           bf16(speclog::truncate_bf16_kernel<4>) && bf16(speclog::truncate_bf16_kernel<8>) &&
            cuda_ok(cudaFuncSetAttribute(speclog::truncate_kernel<SPEC_F32, speclog::any_threads(SPEC_F32)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         speclog::kAnyShared + speclog::kMostHeld),
                    "cudaFuncSetAttribute(truncate_kernel)");
