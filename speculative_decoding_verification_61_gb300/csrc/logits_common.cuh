@@ -95,18 +95,4 @@ __device__ __forceinline__ uint32_t bit_byte(const int32_t *words, int64_t first
     return __ldg(reinterpret_cast<const unsigned char *>(words + first_word) + (col >> 3));
 }
 
-// -inf in the columns of a vector whose bit is clear.
-template <int DT>
-__device__ __forceinline__ void mask_vec(uint4 &q, uint32_t allowed) {
-    uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t keep;
-        if (DT == SPEC_F32) keep = 0u - ((allowed >> i) & 1u);
-        else keep = (((allowed >> (2 * i)) & 1u) | ((allowed << (15 - 2 * i)) & 0x10000u)) * 0xffffu;  // a bit per half
-        w[i] = (w[i] & keep) | (Elem<DT>::kNegInfWord & ~keep);
-    }
-    q = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 }  // namespace speclog

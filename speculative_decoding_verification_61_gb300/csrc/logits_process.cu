@@ -108,6 +108,20 @@ __device__ __forceinline__ void store_logit(char *row, int col, float z) {
     else reinterpret_cast<uint16_t *>(row)[col] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
 }
 
+// -inf in the columns of a vector whose bit is clear.
+template <int DT>
+__device__ __forceinline__ void mask_vec(uint4 &q, uint32_t allowed) {
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t keep;
+        if (DT == SPEC_F32) keep = 0u - ((allowed >> i) & 1u);
+        else keep = (((allowed >> (2 * i)) & 1u) | ((allowed << (15 - 2 * i)) & 0x10000u)) * 0xffffu;  // a bit per half
+        w[i] = (w[i] & keep) | (Elem<DT>::kNegInfWord & ~keep);
+    }
+    q = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The mask of a row: its number, -1 for none, -2 where it names none there is.
 __device__ __forceinline__ int mask_of(const Process &ps, int row) {
     if (!ps.mask) return -1;

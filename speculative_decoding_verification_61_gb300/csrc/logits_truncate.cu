@@ -781,16 +781,15 @@ struct FastShared {
     // of each segment, then (by the warp that finds the border) of it and those before
     uint32_t seg_count[32 * kSegsPerLane];
     uint64_t seg_mass[32 * kSegsPerLane];
-    uint32_t group_max[kMaxGroups];  // order key of each group's largest value
+    uint16_t group_max[kMaxGroups];  // order key of each group's largest value
     int first;                       // the largest value's place
     // the border: tokens above its value stay, `take` of its ties do
     int place, take, ties;
     int cut_group, cut_index;
     bool elsewhere;  // not in the bins
-    bool finite_low; // a value at or below -2^16 that is not -inf
 
     // how often each group holds the border value: written once the bins are done with
-    __device__ uint32_t *group_ties() { return hist; }
+    __device__ uint16_t *group_ties() { return reinterpret_cast<uint16_t *>(hist); }
     // the tokens at a lane's 4 places of a segment
     __device__ __forceinline__ void counts(int seg, uint32_t (&n)[4]) const {
         const int lane = threadIdx.x & 31;
@@ -1075,276 +1074,14 @@ __device__ __forceinline__ uint32_t max_key(const uint4 &q) {
     return key16(__bfloat16_as_ushort(__hmax(__low2bfloat16(m), __high2bfloat16(m))));
 }
 
-// ------------------------------------------------------ the processing, in the same pass
-// The rows' columns that a penalty or bias applies to are few: they are listed
-// by their bits and taken one a thread.  The passes over the row see its
-// masked logits; the items' own values are put in where they count: the
-// histogram, the groups' largest values and ties, and the row out.
-constexpr int kMaxItems = 4096;  // of a CTA's groups; rows with more are processed into `out` first
-constexpr int kMaxBias = 64;     // bias entries kept in shared memory
-constexpr uint32_t kNoItem = 0xffffu;  // value of an item that the mask takes away (a NaN that no rounding gives)
-enum { kPrompt = 1, kEmitted = 2, kDrafted = 4, kBiased = 8 };
-
-struct ItemShared {
-    uint32_t item[kMaxItems];   // column << 4 | flags
-    uint32_t value[kMaxItems];  // the logit's bits below, the item's above
-    int token[kMaxPath], up[kMaxPath];
-    uint64_t before;  // the drafted tokens that the row follows
-    int bias_token[kMaxBias];
-    float bias_value[kMaxBias];
-    uint32_t cut_bits[32];
-    int warp_sum[kWarps];
-};
-__device__ __forceinline__ int item_column(const ItemShared &it, int e) { return static_cast<int>(it.item[e] >> 4); }
-
-// What a row's processing needs beside the shared lists.
-struct RowProcess {
-    Penalty p;
-    int64_t slot;
-    int V, k, e0, e1, mask;
-};
-
-// A row's processing: its sequence's parameters, drafted tokens and biases.
-// False if they are not what the call allows.
-__device__ __noinline__ bool load_row_process(ItemShared &it, const Rows &rw, const Process &ps, int b, int r, int V,
-                                              RowProcess *rp) {
-    const int tid = threadIdx.x, o0 = __ldg(rw.offsets + b), k = __ldg(rw.offsets + b + 1) - o0, i = r - rw.first_row(b, o0);
-    const bool tree = rw.mode == SPEC_ROWS_TREE;
-    bool bad = false;
-    rp->V = V;
-    rp->k = ps.counts ? k : 0;
-    rp->p = Penalty{1.0f, 0.0f, 0.0f};
-    rp->slot = b;
-    rp->mask = -1;
-    if (ps.mask) {
-        rp->mask = ps.mask_rows ? __ldg(ps.mask_rows + r) : r;
-        bad |= rp->mask < -1 || rp->mask >= ps.M;
-    }
-    if (ps.counts) {
-        if (ps.slots) rp->slot = __ldg(ps.slots + b);
-        bad |= rp->slot < 0 || rp->slot >= ps.S || !load_penalty(ps, b, &rp->p);
-        if (tid < k) {
-            const int t = __ldg(rw.tokens + o0 + tid);
-            const bool root = tree && tid == 0;
-            it.token[tid] = t;
-            bad |= !root && (t < 0 || t >= V);
-            if (tree) {
-                const int up = __ldg(rw.parent + o0 + tid);
-                bad |= root ? up != -1 : (up < o0 || up >= o0 + tid);
-                it.up[tid] = up - o0;
-            }
-        }
-    }
-    rp->e0 = rp->e1 = 0;
-    if (ps.bias_offsets) {
-        const int e0 = __ldg(ps.bias_offsets + b), e1 = __ldg(ps.bias_offsets + b + 1);
-        if (e0 < 0 || e1 < e0 || e1 > ps.n_bias) {
-            bad = true;
-        } else {
-            rp->e0 = e0;
-            rp->e1 = e1;
-            for (int e = e0 + tid; e < e1; e += kThreads) {
-                const int t = __ldg(ps.bias_tokens + e);
-                const float v = __ldg(ps.bias_values + e);
-                bad |= t < 0 || t >= V || !(v < __int_as_float(0x7f800000));  // NaN and +inf
-                if (e - e0 < kMaxBias) {
-                    it.bias_token[e - e0] = t;
-                    it.bias_value[e - e0] = v;
-                }
-            }
-        }
-    }
-    bad = __syncthreads_or(bad);
-    if (!bad && tid == 0 && ps.counts) {
-        uint64_t m = 0;
-        if (rw.mode == SPEC_ROWS_NEXT) {
-            m = (1ull << k) - 1;
-        } else if (tree) {
-            for (int g = i; g > 0; g = it.up[g]) m |= 1ull << g;  // parents are earlier nodes
-        } else {
-            m = (1ull << i) - 1;  // i <= SPEC_MAX_K
-        }
-        it.before = m;
-    }
-    return !bad;
-}
-
-// Lists the items number base .. base + kMaxItems - 1 of vectors vb .. ve - 1,
-// and returns how many there are in all.  `bits`: V / 32 words, zeroed here, for
-// the columns that a drafted token or a bias names.
-__device__ __noinline__ int list_items(ItemShared &it, uint32_t *bits, const Process &ps, const RowProcess &rp, int V, int vb,
-                                       int ve, int base) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int W = (V + 31) / 32, w0 = vb / 4, w1 = min(W, (ve + 3) / 4);
-    const bool special = rp.k > 0 || rp.e1 > rp.e0;
-    __syncthreads();
-    if (special) {
-        for (int w = w0 + tid; w < w1; w += kThreads) bits[w] = 0;
-        __syncthreads();
-        // (all drafted tokens: those that the row does not follow add nothing)
-        if (tid < rp.k) {
-            const int t = it.token[tid], w = t >> 5;
-            if (((it.before >> tid) & 1) && w >= w0 && w < w1) atomicOr(&bits[w], 1u << (t & 31));
-        }
-        for (int e = rp.e0 + tid; e < rp.e1; e += kThreads) {
-            const int t = __ldg(ps.bias_tokens + e), w = t >> 5;
-            if (w >= w0 && w < w1) atomicOr(&bits[w], 1u << (t & 31));
-        }
-        __syncthreads();
-    }
-    int done = 0;  // items of the words before
-    for (int wb = w0; wb < w1; wb += kThreads) {
-        const int w = wb + tid;
-        uint32_t prompt = 0, emitted = 0, named = 0;
-        if (w < w1) {
-            if (ps.counts) {
-                prompt = static_cast<uint32_t>(__ldg(ps.seen + rp.slot * 2 * W + w));
-                emitted = static_cast<uint32_t>(__ldg(ps.seen + (rp.slot * 2 + 1) * W + w));
-            }
-            if (special) named = bits[w];
-            if (w == W - 1 && (V & 31)) {  // bits behind the vocabulary say nothing
-                prompt &= (1u << (V & 31)) - 1;
-                emitted &= (1u << (V & 31)) - 1;
-            }
-        }
-        const uint32_t touched = prompt | emitted | named;
-        int rank = __popc(touched);
-        const int own = rank;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, rank, off);
-            if (lane >= off) rank += x;
-        }
-        __syncthreads();
-        if (lane == 31) it.warp_sum[warp] = rank;
-        __syncthreads();
-        int sum = lane < kWarps ? it.warp_sum[lane] : 0, before = lane < warp ? sum : 0;
-        sum = __reduce_add_sync(0xffffffffu, sum);
-        before = __reduce_add_sync(0xffffffffu, before);
-        rank += done + before - own - base;
-        for (uint32_t m = touched; m; m &= m - 1, ++rank) {
-            if (rank < 0 || rank >= kMaxItems) continue;
-            const int bit = __ffs(m) - 1;
-            uint32_t f = (prompt >> bit & 1) * kPrompt | (emitted >> bit & 1) * kEmitted;
-            if (named >> bit & 1) f |= kDrafted | kBiased;  // one of them
-            it.item[rank] = static_cast<uint32_t>(w * 32 + bit) << 4 | f;
-        }
-        done += sum;
-    }
-    __syncthreads();
-    return done;
-}
-
-// Item e's value, kept as it.value[e]: the logit's bits below, the item's above,
-// kNoItem where the mask takes the column away.
-__device__ __noinline__ uint32_t item_value(ItemShared &it, const Process &ps, const RowProcess &rp, const uint4 *row, int mask,
-                                            const unsigned char *mask_row, int e) {
-    const uint32_t item = it.item[e];
-    const int col = static_cast<int>(item >> 4);
-    if (mask >= 0 && !((mask_row[col >> 3] >> (col & 7)) & 1)) {
-        return it.value[e] = kNoItem << 16;
-    }
-    const uint32_t raw = reinterpret_cast<const uint16_t *>(row)[col];
-    float z = __uint_as_float(raw << 16);
-    int c = item & kEmitted ? __ldg(ps.counts + rp.slot * rp.V + col) : 0;
-    if (item & kDrafted)
-        for (uint64_t d = rp.k ? it.before : 0; d; d &= d - 1) c += it.token[__ffsll(d) - 1] == col;
-    bool changed = false;
-    if ((item & kPrompt) || c > 0) {
-        z = penalised(z, c, rp.p);
-        changed = true;
-    }
-    if (item & kBiased) {
-        // the same token twice: the entries add, in list order
-        float bias = 0.0f;
-        bool any = false;
-        for (int x = 0; x < rp.e1 - rp.e0; ++x) {
-            if ((x < kMaxBias ? it.bias_token[x] : __ldg(ps.bias_tokens + rp.e0 + x)) != col) continue;
-            const float v = x < kMaxBias ? it.bias_value[x] : __ldg(ps.bias_values + rp.e0 + x);
-            bias = any ? __fadd_rn(bias, v) : v;
-            any = true;
-        }
-        if (any) z = __fadd_rn(z, bias);
-        changed |= any;
-    }
-    const uint32_t y = changed ? __bfloat16_as_ushort(__float2bfloat16_rn(z)) : raw;
-    return it.value[e] = raw | y << 16;
-}
-
-// A thread's next kAhead vectors of the row, and the bytes of its mask for them.
-// pred(u, g): whether group g, its u-th, is wanted; elsewhere -inf.
-template <bool PROC, typename F>
-__device__ __forceinline__ void load_vectors(uint4 (&q)[kAhead], uint32_t (&allowed)[kAhead], const uint4 *row, int mask,
-                                             const unsigned char *mask_row, int g0, int ve, F &&pred) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-        const int g = g0 + u * kWarps, v = g * 32 + lane;
-        allowed[u] = v < ve && pred(u, g) ? 0xffu : 0u;
-        if (PROC && mask >= 0 && allowed[u]) allowed[u] = __ldg(mask_row + v);
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-        const int v = (g0 + u * kWarps) * 32 + lane;
-        q[u] = allowed[u] ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-    }
-}
-template <bool PROC>
-__device__ __forceinline__ void apply_mask(uint4 &q, uint32_t allowed) {
-    if (PROC && allowed != 0xffu && allowed != 0) mask_vec<SPEC_BF16>(q, allowed);
-}
-
-// Vectors vb .. ve - 1 of a row processed into dst (the row itself, or another
-// buffer); its first items are listed, `listed` of them in all.
-__device__ __noinline__ void process_row(ItemShared &it, uint32_t *bits, const Process &ps, const RowProcess &rp, const uint4 *row,
-                                         uint4 *dst, int vb, int ve, int listed) {
-    const unsigned char *mask_row =
-        reinterpret_cast<const unsigned char *>(ps.mask) + (rp.mask < 0 ? 0 : static_cast<int64_t>(rp.mask) * ((rp.V + 31) / 32) * 4);
-    if (row != dst || rp.mask >= 0) {
-        for (int g0 = vb / 32 + (threadIdx.x >> 5); g0 * 32 < ve; g0 += kWarps * kAhead) {
-            uint4 q[kAhead];
-            uint32_t allowed[kAhead];
-            load_vectors<true>(q, allowed, row, rp.mask, mask_row, g0, ve, [](int, int) { return true; });
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int v = (g0 + u * kWarps) * 32 + static_cast<int>(threadIdx.x & 31);
-                apply_mask<true>(q[u], allowed[u]);
-                if (v < ve) dst[v] = q[u];
-            }
-        }
-    }
-    __syncthreads();
-    for (int base = 0; base < listed; base += kMaxItems) {
-        if (base > 0) list_items(it, bits, ps, rp, rp.V, vb, ve, base);
-        for (int e = threadIdx.x; e < min(kMaxItems, listed - base); e += kThreads) {
-            const uint32_t y = item_value(it, ps, rp, row, rp.mask, mask_row, e) >> 16;
-            if (y != kNoItem) reinterpret_cast<uint16_t *>(dst)[item_column(it, e)] = static_cast<uint16_t>(y);
-        }
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ bool same_value(uint32_t a, uint32_t b) {  // of bf16 bits
-    return __uint_as_float(a << 16) == __uint_as_float(b << 16);
-}
-// One value's bits added to the histogram, or taken from it again.
-__device__ __forceinline__ void count_one(FastShared &sm, uint32_t u, bool add, uint32_t *odd) {
-    const uint32_t m = u & 0x7fffu, one = add ? 1u : ~0u;
-    if (m - kTiny < static_cast<uint32_t>(kSide)) atomicAdd(&sm.hist[m - kTiny + (u >> 15) * kSide], one);
-    else if (m == 0) atomicAdd(&sm.zeros, one);
-    else if (!add || u == 0xff80u) return;
-    else *odd |= u >= (0x8000u | kHuge) && u < 0xff80u ? kFiniteLow : kOdd;
-}
-
 // CL CTAs of a cluster share a row, each a run of its groups: CTA 0 adds up the
 // histograms and finds the border for all.
-template <int CL, bool PROC>
+template <int CL>
 __global__ void __launch_bounds__(kThreads, kPerSm)
-    truncate_bf16_kernel(const char *logits, char *out, Rows rw, Process ps, Truncate tr, int V) {
+    truncate_bf16_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
     extern __shared__ char smem[];
     BothShared &all = *reinterpret_cast<BothShared *>(smem);
     FastShared &sm = all.fast;
-    ItemShared &items = *reinterpret_cast<ItemShared *>(smem + (sizeof(BothShared) + 15) / 16 * 16);  // PROC only
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row_bytes = static_cast<int64_t>(V) * 2;
     const int vecs = V / 8, groups = (vecs + 31) / 32;
@@ -1356,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     const int oB = __ldg(rw.offsets + rw.B);
     const int64_t rows_all = rw.first_row(rw.B, oB);
     int64_t r = blockIdx.x / CL;
-    if (!check_rows(rw, PROC && ps.counts)) {
+    if (!check_rows(rw, false)) {
         fill_nan<SPEC_BF16>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                             static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
@@ -1371,40 +1108,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         const uint4 *row = reinterpret_cast<const uint4 *>(logits + r * row_bytes);
         uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
         const Settings s = load_settings(tr, b, V);
-        // with the processing: the row's items (touched columns of this CTA's groups), its mask (-1: none)
-        RowProcess rp{};
-        int listed = 0, mask = -1;
-        bool processed = !PROC;  // `row` is what is truncated
-        if (PROC) {
-            __syncthreads();  // the last row is done with the shared arrays
-            const bool bad = !load_row_process(items, rw, ps, b, static_cast<int>(r), V, &rp);
-            if (bad || !s.valid) {
-                fill_nan<SPEC_BF16>(dst, ve, vb + tid, kThreads);
-                continue;
-            }
-            listed = list_items(items, sm.hist, ps, rp, V, vb, ve, 0);
-            mask = rp.mask;
-            if (!s.active || listed > kMaxItems) {
-                process_row(items, sm.hist, ps, rp, row, dst, vb, ve, listed);
-                if (!s.active) continue;
-                __syncthreads();
-                row = dst;
-                processed = true;
-                listed = 0;
-                mask = -1;
-            }
-        } else {
-            if (!s.valid) {
-                fill_nan<SPEC_BF16>(dst, ve, vb + tid, kThreads);
-                continue;
-            }
-            if (!s.active) {
-                if (logits != out)
-                    for (int v = vb + tid; v < ve; v += kThreads) dst[v] = row[v];
-                continue;
-            }
+        if (!s.valid) {
+            fill_nan<SPEC_BF16>(dst, ve, vb + tid, kThreads);
+            continue;
         }
-        const unsigned char *mask_row = reinterpret_cast<const unsigned char *>(ps.mask) + (mask < 0 ? 0 : static_cast<int64_t>(mask) * ((V + 31) / 32) * 4);
+        if (!s.active) {
+            if (logits != out)
+                for (int v = vb + tid; v < ve; v += kThreads) dst[v] = row[v];
+            continue;
+        }
         const bool mass = s.p < 1.0f, counted = mass || s.k > 0;
         // --- one pass over the row: the histogram, the groups' largest values
         __syncthreads();  // the last row is done with the shared arrays
@@ -1418,46 +1130,33 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             sm.zeros = 0;
             sm.first = kPlaces;
             sm.elsewhere = false;
-            sm.finite_low = false;
         }
         __syncthreads();
         uint32_t odd = 0;
         {
             uint4 q[kAhead], next[kAhead];
-            uint32_t allowed[kAhead], next_allowed[kAhead];
-            const auto all_of_them = [](int, int) { return true; };
-            load_vectors<PROC>(q, allowed, row, mask, mask_row, gb + warp, ve, all_of_them);
+            auto load = [&](uint4 (&to)[kAhead], int g0) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int v = (g0 + u * kWarps) * 32 + lane;
+                    to[u] = v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                }
+            };
+            load(q, gb + warp);
             for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
-                load_vectors<PROC>(next, next_allowed, row, mask, mask_row, g0 + kWarps * kAhead, ve, all_of_them);
+                load(next, g0 + kWarps * kAhead);
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     if (g0 + u * kWarps >= ge) break;
-                    apply_mask<PROC>(q[u], allowed[u]);
                     count_values(sm, q[u], &odd);
                     const uint32_t key = __reduce_max_sync(0xffffffffu, max_key(q[u]));
-                    if (lane == 0) sm.group_max[g0 + u * kWarps - gb] = key;
+                    if (lane == 0) sm.group_max[g0 + u * kWarps - gb] = static_cast<uint16_t>(key);
                 }
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    q[u] = next[u];
-                    if (PROC) allowed[u] = next_allowed[u];
-                }
+                for (int u = 0; u < kAhead; ++u) q[u] = next[u];
             }
         }
-        if (PROC && listed) {
-            __syncthreads();
-            // the items' values replace the ones that the pass counted
-            for (int e = tid; e < listed; e += kThreads) {
-                const uint32_t x = item_value(items, ps, rp, row, mask, mask_row, e);
-                if (x >> 16 == kNoItem) continue;
-                count_one(sm, x & 0xffffu, false, &odd);
-                count_one(sm, x >> 16, true, &odd);
-                atomicMax(&sm.group_max[(item_column(items, e) >> 8) - gb], key16(x >> 16));
-            }
-        }
-        if (odd & kFiniteLow) sm.finite_low = true;
-        const bool any_odd = __syncthreads_or(odd & kOdd) != 0;
-        const uint32_t odd_all = (any_odd ? kOdd : 0) | (sm.finite_low ? kFiniteLow : 0);
+        const uint32_t odd_all = (__syncthreads_or(odd & kOdd) ? kOdd : 0) | (__syncthreads_or(odd & kFiniteLow) ? kFiniteLow : 0);
         bool slow = (odd_all & kOdd) != 0;
         if (CL > 1) {
             if (tid == 0 && odd_all) atomicOr(&lead.odd, odd_all);
@@ -1566,19 +1265,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             slow = lead.slow;
         }
         if (slow) {
-            if (PROC && !processed) {
-                __syncthreads();
-                listed = list_items(items, sm.hist, ps, rp, V, vb, ve, 0);
-                process_row(items, sm.hist, ps, rp, row, dst, vb, ve, listed);
-            }
-            if (PROC && CL > 1) cluster_sync();
-            if (PROC) row = dst;
             if (rank > 0) continue;
             __syncthreads();
             if (tid < 64) all.any.table[tid] = all.table[tid];
             __syncthreads();
             const uint64_t cut = cut_of_row<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), V, s);
-            if (cut != 0 || (!PROC && logits != out)) write_cut<SPEC_BF16, kThreads>(reinterpret_cast<const char *>(row), dst, V, cut);
+            if (cut != 0 || logits != out) write_cut<SPEC_BF16, kThreads>(reinterpret_cast<const char *>(row), dst, V, cut);
             continue;
         }
         // --- the border value: the lowest one kept, and how its ties go
@@ -1607,29 +1299,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             int take = CL > 1 ? lead.take : sm.take;
             for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
                 uint4 q[kAhead];
-                uint32_t allowed[kAhead];
-                load_vectors<PROC>(q, allowed, row, mask, mask_row, g0, ve, [&](int, int g) { return g < ge && sm.group_max[g - gb] >= low; });
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int g = g0 + u * kWarps, v = g * 32 + lane;
+                    q[u] = make_uint4(~pair, ~pair, ~pair, ~pair);
+                    if (g < ge && sm.group_max[g - gb] >= low && v < ve) q[u] = row[v];
+                }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int g = g0 + u * kWarps;
                     if (g >= ge) break;
-                    apply_mask<PROC>(q[u], allowed[u]);
                     uint32_t n = __popc(equal_mask(q[u].x, pair)) + __popc(equal_mask(q[u].y, pair)) +
                                  __popc(equal_mask(q[u].z, pair)) + __popc(equal_mask(q[u].w, pair));
                     n = __reduce_add_sync(0xffffffffu, n >> 4);
-                    if (lane == 0) sm.group_ties()[g - gb] = n;
+                    if (lane == 0) sm.group_ties()[g - gb] = static_cast<uint16_t>(n);
                 }
             }
             __syncthreads();
-            if (PROC && listed) {
-                for (int e = tid; e < listed; e += kThreads) {
-                    const uint32_t v = items.value[e];
-                    if (v >> 16 == kNoItem) continue;
-                    const int change = (same_value(v >> 16, border) ? 1 : 0) - (same_value(v & 0xffffu, border) ? 1 : 0);
-                    if (change) atomicAdd(&sm.group_ties()[(item_column(items, e) >> 8) - gb], static_cast<uint32_t>(change));
-                }
-                __syncthreads();
-            }
             // a warp's running sums of the groups' ties
             constexpr int kRun = kMaxGroups / 32;
             uint32_t n = 0, c = 0;
@@ -1663,25 +1349,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 const int v = (gb + g) * 32 + lane;
                 uint32_t bits = 0;  // a bit per tie of this lane's vector
                 if (v < ve) {
-                    uint4 q = row[v];
-                    if (PROC && mask >= 0) mask_vec<SPEC_BF16>(q, mask_row[v]);
+                    const uint4 q = row[v];
                     const uint32_t e[4] = {equal_mask(q.x, pair), equal_mask(q.y, pair), equal_mask(q.z, pair), equal_mask(q.w, pair)};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) bits |= (e[i] & 1u) << (2 * i) | (e[i] >> 31) << (2 * i + 1);
-                }
-                if (PROC && listed) {
-                    // the group's items, each by its own value
-                    items.cut_bits[lane] = bits;
-                    __syncwarp();
-                    for (int e = lane; e < listed; e += 32) {
-                        const int col = item_column(items, e);
-                        const uint32_t x = items.value[e];
-                        if (col >> 8 != gb + g || x >> 16 == kNoItem) continue;
-                        if (same_value(x >> 16, border)) atomicOr(&items.cut_bits[(col >> 3) & 31], 1u << (col & 7));
-                        else atomicAnd(&items.cut_bits[(col >> 3) & 31], ~(1u << (col & 7)));
-                    }
-                    __syncwarp();
-                    bits = items.cut_bits[lane];
                 }
                 uint32_t before = __popc(bits);
                 const uint32_t own = before;
@@ -1712,14 +1383,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 const int g = g0 + u * kWarps;
                 kept[u] = g < ge && sm.group_max[g - gb] >= low;
             }
-            uint32_t allowed[kAhead];
-            load_vectors<PROC>(q, allowed, row, mask, mask_row, g0, ve, [&](int u, int) { return kept[u]; });
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int v = (g0 + u * kWarps) * 32 + lane;
+                q[u] = kept[u] && v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int g = g0 + u * kWarps, v = g * 32 + lane;
                 if (v >= ve) continue;
                 if (kept[u]) {
-                    apply_mask<PROC>(q[u], allowed[u]);
                     uint32_t x[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
                     const bool equal = g < cut_group;
 #pragma unroll
@@ -1737,33 +1410,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 dst[v] = q[u];
             }
         }
-        if (PROC && listed) {
-            __syncthreads();
-            uint16_t *to = reinterpret_cast<uint16_t *>(dst);
-            const float edge = __uint_as_float(border << 16);
-            for (int e = tid; e < listed; e += kThreads) {
-                const uint32_t y = items.value[e] >> 16;
-                if (y == kNoItem) continue;
-                const int col = item_column(items, e), g = col >> 8;
-                const float f = __uint_as_float(y << 16);
-                const bool keep = f > edge || (f == edge && (g < cut_group || (g == cut_group && col <= cut_index)));
-                to[col] = keep ? static_cast<uint16_t>(y) : 0xff80u;
-            }
-        }
     }
     if (CL > 1) cluster_sync();  // CTA 0's shared memory is read until here
 }
 
-template <bool PROC>
-constexpr int kBf16Shared = (sizeof(BothShared) + 15) / 16 * 16 + (PROC ? sizeof(ItemShared) : 0);
-
-template <int CL, bool PROC>
-cudaError_t launch_bf16(const char *in, char *to, const Rows &rw, const Process &ps, const Truncate &tr, int V, int sms,
-                        cudaStream_t stream) {
+template <int CL>
+cudaError_t launch_bf16(const char *in, char *to, const Rows &rw, const Truncate &tr, int V, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min(rw.R, sms * kPerSm / CL) * CL);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kBf16Shared<PROC>;
+    cfg.dynamicSmemBytes = sizeof(BothShared);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1771,20 +1427,7 @@ cudaError_t launch_bf16(const char *in, char *to, const Rows &rw, const Process 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CL > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, truncate_bf16_kernel<CL, PROC>, in, to, rw, ps, tr, V);
-}
-
-template <bool PROC>
-int launch_rows_bf16(const void *logits, void *out, const Rows &rw, const Process &ps, const Truncate &tr, int V, int sms,
-                     cudaStream_t stream) {
-    // few rows: clusters of CTAs share them, while every warp has groups of its own
-    int cl = 1;
-    while (cl < 8 && static_cast<int64_t>(rw.R) * cl * 2 <= static_cast<int64_t>(sms) * kPerSm && V >= cl * 2 * kWarps * kGroupCols) cl *= 2;
-    const auto launch = cl == 8 ? launch_bf16<8, PROC> : cl == 4 ? launch_bf16<4, PROC> : cl == 2 ? launch_bf16<2, PROC> : launch_bf16<1, PROC>;
-    return specv::cuda_ok(launch(static_cast<const char *>(logits), static_cast<char *>(out), rw, ps, tr, V, sms, stream),
-                          "launch truncate_bf16_kernel")
-               ? SPEC_OK
-               : SPEC_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, truncate_bf16_kernel<CL>, in, to, rw, tr, V);
 }
 
 constexpr int kMostHeld = 190 * 1024;  // bytes of a row kept in shared memory
@@ -1794,12 +1437,21 @@ constexpr int any_threads(int dt) { return dt == SPEC_F32 ? 1024 : kThreads; }
 template <int DT>
 int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms,
                     cudaStream_t stream) {
-    if (DT == SPEC_BF16 && V <= kMaxFastV) return launch_rows_bf16<false>(logits, out, rw, Process{}, tr, V, sms, stream);
-    constexpr int T = any_threads(DT);
-    const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
-    const bool held = DT == SPEC_F32 && bytes <= kMostHeld;
-    truncate_kernel<DT, T><<<std::min(rw.R, sms * 1024 / T), T, kAnyShared + (held ? bytes : 0), stream>>>(
-        static_cast<const char *>(logits), static_cast<char *>(out), rw, tr, V, held);
+    const char *in = static_cast<const char *>(logits);
+    char *to = static_cast<char *>(out);
+    if (DT == SPEC_BF16 && V <= kMaxFastV) {
+        // few rows: clusters of CTAs share them, while every warp has groups of its own
+        int cl = 1;
+        while (cl < 8 && static_cast<int64_t>(rw.R) * cl * 2 <= static_cast<int64_t>(sms) * kPerSm && V >= cl * 2 * kWarps * kGroupCols) cl *= 2;
+        const auto launch = cl == 8 ? launch_bf16<8> : cl == 4 ? launch_bf16<4> : cl == 2 ? launch_bf16<2> : launch_bf16<1>;
+        return specv::cuda_ok(launch(in, to, rw, tr, V, sms, stream), "launch truncate_bf16_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
+    } else {
+        constexpr int T = any_threads(DT);
+        const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
+        const bool held = DT == SPEC_F32 && bytes <= kMostHeld;
+        truncate_kernel<DT, T><<<std::min(rw.R, sms * 1024 / T), T, kAnyShared + (held ? bytes : 0), stream>>>(in, to, rw, tr,
+                                                                                                          V, held);
+    }
     return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
@@ -1814,15 +1466,12 @@ inline int check_truncate_args(const spec_truncate_t *t, const Rows &rw, Truncat
 
 namespace specv {
 bool set_logits_attrs() {
-    const auto bf16 = [](auto kernel, int bytes) {
-        return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+    const auto bf16 = [](auto kernel) {
+        return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(speclog::BothShared)),
                        "cudaFuncSetAttribute(truncate_bf16_kernel)");
     };
-    constexpr int alone = speclog::kBf16Shared<false>, with = speclog::kBf16Shared<true>;
-    return bf16(speclog::truncate_bf16_kernel<1, false>, alone) && bf16(speclog::truncate_bf16_kernel<2, false>, alone) &&
-           bf16(speclog::truncate_bf16_kernel<4, false>, alone) && bf16(speclog::truncate_bf16_kernel<8, false>, alone) &&
-           bf16(speclog::truncate_bf16_kernel<1, true>, with) && bf16(speclog::truncate_bf16_kernel<2, true>, with) &&
-           bf16(speclog::truncate_bf16_kernel<4, true>, with) && bf16(speclog::truncate_bf16_kernel<8, true>, with) &&
+    return bf16(speclog::truncate_bf16_kernel<1>) && bf16(speclog::truncate_bf16_kernel<2>) &&
+           bf16(speclog::truncate_bf16_kernel<4>) && bf16(speclog::truncate_bf16_kernel<8>) &&
            cuda_ok(cudaFuncSetAttribute(speclog::truncate_kernel<SPEC_F32, speclog::any_threads(SPEC_F32)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         speclog::kAnyShared + speclog::kMostHeld),
                    "cudaFuncSetAttribute(truncate_kernel)");
@@ -1854,17 +1503,9 @@ int spec_logits_process_truncate(const void *logits, const spec_rows_t *rows, co
     Truncate tr;
     int rc = check_rows_args(logits, rows, V, dtype, out, &rw);
     if (rc == SPEC_OK) rc = check_truncate_args(truncate, rw, &tr);
-    Process ps;
-    if (rc == SPEC_OK) rc = check_process_args(rows, process, &rw, &ps);
-    if (rc != SPEC_OK || rw.B == 0 || rw.R == 0) return rc;
-    if (dtype == SPEC_BF16 && V <= kMaxFastV) {
-        int dev;
-        specv::DeviceState *st = specv::device_state(&dev);
-        if (!st) return SPEC_ERR_CUDA;
-        return launch_rows_bf16<true>(logits, out, rw, ps, tr, V, st->sms, static_cast<cudaStream_t>(stream));
-    }
-    rc = spec_logits_process(logits, rows, process, V, dtype, out, stream);
-    return rc != SPEC_OK ? rc : spec_logits_truncate(out, rows, truncate, V, dtype, out, stream);
+    if (rc == SPEC_OK) rc = spec_logits_process(logits, rows, process, V, dtype, out, stream);
+    if (rc != SPEC_OK) return rc;
+    return spec_logits_truncate(out, rows, truncate, V, dtype, out, stream);
 }
 
 }  // extern "C"
