@@ -48,8 +48,11 @@ __device__ __forceinline__ bool check_rows(const Rows &rw, bool need_tokens) {
     return __syncthreads_or(bad) == 0;
 }
 
-// The same, and the sequence that holds row r into *s_seq (shared memory).
+// The same, and the sequence that holds row r into *s_seq (shared memory; -1:
+// the row lies behind the last sequence's).
 __device__ __forceinline__ bool check_rows(const Rows &rw, int64_t r, int *s_seq) {
+    if (threadIdx.x == 0) *s_seq = -1;
+    __syncthreads();
     for (int b = threadIdx.x; b < rw.B; b += blockDim.x)
         if (r >= rw.first_row(b) && r < rw.first_row(b + 1)) *s_seq = b;
     return check_rows(rw, false);

@@ -180,6 +180,7 @@ struct RowConstants {
 };
 
 struct Shared {
+    int seq;
     float2 table[64];
     uint32_t count[kBins], lo[kBins], hi[kBins];
     uint64_t list[kList];
@@ -564,16 +565,6 @@ __device__ __forceinline__ void fill_table(float2 *table) {
     if (threadIdx.x < 64) table[threadIdx.x] = kExp2Table[threadIdx.x];
 }
 
-// The sequence of row r, which is at or behind sequence b, by each warp.
-__device__ __forceinline__ int sequence_of(const Rows &rw, int b, int64_t r) {
-    for (;; b += 32) {
-        const int j = min(b + static_cast<int>(threadIdx.x & 31), rw.B - 1);
-        const uint32_t hit = __ballot_sync(0xffffffffu, r < rw.first_row(j + 1));
-        if (hit) return min(b + __ffs(hit) - 1, rw.B - 1);
-        if (b + 32 >= rw.B) return rw.B - 1;  // not reached: r lies before the last row's end
-    }
-}
-
 // The cut of one row in memory, for rows of any kind: every token whose place is
 // below it goes; 0: the row stays as it is.  Passes over the row: its largest
 // value, a histogram over 32 bins per halving of the weight, the border bin's
@@ -700,7 +691,7 @@ __device__ __forceinline__ void fill_nan(uint4 *dst, int64_t vecs, int64_t first
     for (int64_t v = first; v < vecs; v += step) dst[v] = make_uint4(kNan, kNan, kNan, kNan);
 }
 
-// Rows of any kind, a CTA per row at a time, neighbouring rows at the same time.
+// Rows of any kind, a CTA per row: neighbouring rows at a time, whatever each takes.
 // A row that fits stays in shared memory from the first pass on (`held`).
 template <int DT, int T>
 __global__ void __launch_bounds__(T, 1024 / T)
@@ -712,41 +703,37 @@ __global__ void __launch_bounds__(T, 1024 / T)
     const int64_t row_bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
     const int vecs = V / Elem<DT>::kPerVec;
     fill_table(sm.table);
-    const int oB = __ldg(rw.offsets + rw.B);
-    const int64_t rows_all = rw.first_row(rw.B, oB);
-    if (!check_rows(rw, false)) {
-        fill_nan<DT>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
-                     static_cast<int64_t>(blockIdx.x) * T + tid, static_cast<int64_t>(gridDim.x) * T);
+    const int64_t r = blockIdx.x;
+    if (!check_rows(rw, r, &sm.seq)) {
+        fill_nan<DT>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs, r * T + tid,
+                     static_cast<int64_t>(gridDim.x) * T);
         return;
     }
-    int b = 0;
-    for (int64_t r = blockIdx.x; r < rows_all; r += gridDim.x) {
-        b = sequence_of(rw, b, r);
-        const char *row = logits + r * row_bytes;
-        uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
-        const Settings s = load_settings(tr, b, V);
-        if (!s.valid) {
-            fill_nan<DT>(dst, vecs, tid, T);
-            continue;
-        }
-        if (s.active && held) {
-            __syncthreads();  // the last row has been written
-            constexpr int kFlight = 4;
-            for (int v0 = tid; v0 < vecs; v0 += T * kFlight) {
-                uint4 q[kFlight];
-#pragma unroll
-                for (int u = 0; u < kFlight; ++u)
-                    if (v0 + u * T < vecs) q[u] = reinterpret_cast<const uint4 *>(row)[v0 + u * T];
-#pragma unroll
-                for (int u = 0; u < kFlight; ++u)
-                    if (v0 + u * T < vecs) reinterpret_cast<uint4 *>(hold)[v0 + u * T] = q[u];
-            }
-            __syncthreads();
-            row = hold;
-        }
-        const uint64_t cut = s.active ? cut_of_row<DT, T>(sm, row, V, s) : 0;
-        if (cut != 0 || logits != out) write_cut<DT, T>(row, dst, V, cut);
+    const int b = sm.seq;
+    if (b < 0) return;  // behind the last sequence's rows
+    const char *row = logits + r * row_bytes;
+    uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
+    const Settings s = load_settings(tr, b, V);
+    if (!s.valid) {
+        fill_nan<DT>(dst, vecs, tid, T);
+        return;
     }
+    if (s.active && held) {
+        constexpr int kFlight = 4;
+        for (int v0 = tid; v0 < vecs; v0 += T * kFlight) {
+            uint4 q[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (v0 + u * T < vecs) q[u] = reinterpret_cast<const uint4 *>(row)[v0 + u * T];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (v0 + u * T < vecs) reinterpret_cast<uint4 *>(hold)[v0 + u * T] = q[u];
+        }
+        __syncthreads();
+        row = hold;
+    }
+    const uint64_t cut = s.active ? cut_of_row<DT, T>(sm, row, V, s) : 0;
+    if (cut != 0 || logits != out) write_cut<DT, T>(row, dst, V, cut);
 }
 
 // ------------------------------------------------------------ bf16, in two passes
@@ -816,6 +803,7 @@ struct BothShared {
     // apart from the union: kept over the rows
     float2 table[64];
     RowConstants row;
+    int seq;
     // in a cluster, CTA 0's: what the CTAs' shares of a row hold, what it found, each CTA's ties
     uint32_t odd;
     int place, take, ties;
@@ -1090,325 +1078,318 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     const int gb = min(groups, rank * part), ge = min(groups, gb + part), vb = gb * 32, ve = min(vecs, ge * 32);
     BothShared &lead = CL > 1 ? *cluster_map(&all, 0) : all;
     fill_table(all.table);
-    const int oB = __ldg(rw.offsets + rw.B);
-    const int64_t rows_all = rw.first_row(rw.B, oB);
-    int64_t r = blockIdx.x / CL;
-    if (!check_rows(rw, false)) {
+    const int64_t r = blockIdx.x / CL;
+    if (tid == 0) all.odd = 0;
+    if (!check_rows(rw, r, &all.seq)) {
         fill_nan<SPEC_BF16>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                             static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
     }
-    if (CL > 1) {
-        if (tid == 0) all.odd = 0;
-        cluster_sync();
+    const int b = all.seq;
+    if (b < 0) return;  // behind the last sequence's rows
+    const uint4 *row = reinterpret_cast<const uint4 *>(logits + r * row_bytes);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
+    const Settings s = load_settings(tr, b, V);
+    if (!s.valid) {
+        fill_nan<SPEC_BF16>(dst, ve, vb + tid, kThreads);
+        return;
     }
-    int b = 0;
-    for (; r < rows_all; r += gridDim.x / CL) {
-        b = sequence_of(rw, b, r);
-        const uint4 *row = reinterpret_cast<const uint4 *>(logits + r * row_bytes);
-        uint4 *dst = reinterpret_cast<uint4 *>(out + r * row_bytes);
-        const Settings s = load_settings(tr, b, V);
-        if (!s.valid) {
-            fill_nan<SPEC_BF16>(dst, ve, vb + tid, kThreads);
-            continue;
-        }
-        if (!s.active) {
-            if (logits != out)
-                for (int v = vb + tid; v < ve; v += kThreads) dst[v] = row[v];
-            continue;
-        }
-        const bool mass = s.p < 1.0f, counted = mass || s.k > 0;
-        // --- one pass over the row: the histogram, the groups' largest values
-        __syncthreads();  // the last row is done with the shared arrays
-        for (int i = tid; i < 2 * kSide / 4; i += kThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
-        if (tid < 32 * kSegsPerLane - kSegs) {
-            sm.seg_count[kSegs + tid] = 0;
-            sm.seg_mass[kSegs + tid] = 0;
-        }
-        if (tid == kThreads - 1) set_scale(all.row, s);
-        if (tid == 0) {
-            sm.zeros = 0;
-            sm.first = kPlaces;
-            sm.elsewhere = false;
-        }
-        __syncthreads();
-        uint32_t odd = 0;
-        {
-            uint4 q[kAhead], next[kAhead];
-            auto load = [&](uint4 (&to)[kAhead], int g0) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int v = (g0 + u * kWarps) * 32 + lane;
-                    to[u] = v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-                }
-            };
-            load(q, gb + warp);
-            for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
-                load(next, g0 + kWarps * kAhead);
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (g0 + u * kWarps >= ge) break;
-                    count_values(sm, q[u], &odd);
-                    const uint32_t key = __reduce_max_sync(0xffffffffu, max_key(q[u]));
-                    if (lane == 0) sm.group_max[g0 + u * kWarps - gb] = static_cast<uint16_t>(key);
-                }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) q[u] = next[u];
-            }
-        }
-        const uint32_t odd_all = (__syncthreads_or(odd & kOdd) ? kOdd : 0) | (__syncthreads_or(odd & kFiniteLow) ? kFiniteLow : 0);
-        bool slow = (odd_all & kOdd) != 0;
-        if (CL > 1) {
-            if (tid == 0 && odd_all) atomicOr(&lead.odd, odd_all);
-            cluster_sync();  // CTA 0's histogram is there to be added to
-            if (rank > 0) {
-                for (int i = tid; i < 2 * kSide; i += kThreads)
-                    if (const uint32_t n = sm.hist[i]) atomicAdd(&lead.fast.hist[i], n);
-                if (tid == 0 && sm.zeros) atomicAdd(&lead.fast.zeros, sm.zeros);
-            }
-            cluster_sync();
-            slow = (lead.odd & kOdd) != 0;
-        }
-        const bool finite_low = ((CL > 1 ? all.odd : odd_all) & kFiniteLow) != 0;  // (CTA 0's is meant)
-        float zmax = 0.0f;
-        if (!slow && rank == 0) {
-            // --- the bins' sums by segments of 32
-            int first = kPlaces;
-            for (int g = warp; g < kSegs; g += kWarps) {
-                uint32_t n[4];
-                sm.counts(g, n);
-                const uint32_t own = n[0] + n[1] + n[2] + n[3];
-                const uint32_t any = __ballot_sync(0xffffffffu, own > 0);
-                uint32_t sum = 0;
-                if (any) {
-                    if (first == kPlaces) {
-                        const int i = n[0] ? 0 : n[1] ? 1 : n[2] ? 2 : 3, at = __ffs(any) - 1;
-                        first = g * kSegPlaces + at * 4 + __shfl_sync(0xffffffffu, i, at);
-                    }
-                    sum = __reduce_add_sync(0xffffffffu, own);
-                }
-                if (lane == 0) sm.seg_count[g] = sum;
-            }
-            if (lane == 0) atomicMin(&sm.first, first);
-            __syncthreads();
-            first = sm.first;
-            slow = first == kPlaces;
-            if (!slow) zmax = place_value(first);
-        }
-        // (values at or below -2^16 have no weight, and min-p excludes them)
-        if (rank == 0 && !slow && !((-65536.0f - zmax) * specv::temp_scale(s.T) < -150.0f)) slow = true;
-        Weights w{};
-        if (!slow && rank == 0) {
-            w = row_weights(all.row, zmax, V, all.table);
-            if (mass) {
-                for (int g = warp; g < kSegs; g += kWarps) {
-                    uint64_t m = 0;
-                    if (sm.seg_count[g]) {
-                        uint32_t n[4];
-                        sm.counts(g, n);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m += TokenWeight(w, place_value(g * kSegPlaces + lane * 4 + i)).times(n[i]);
-#pragma unroll
-                        for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
-                    }
-                    if (lane == 0) sm.seg_mass[g] = m;
-                }
-                __syncthreads();
-            }
-            // --- the border, by one warp
-            if (warp == 0 && counted) {
-                scan_segments(sm, mass);
-                Border k{kPlaces, 0, 0, 0};
-                uint32_t take = 0;
-                uint64_t Z = mass ? sm.seg_mass[kSegs - 1] : 0;
-                if (s.k > 0) {
-                    k = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass);
-                    if (k.place >= 0) {
-                        take = s.k - k.above_count;
-                        if (mass) Z = k.above_mass + TokenWeight(w, place_value(k.place)).times(take);
-                    } else if (!finite_low) {
-                        k = Border{kPlaces, 0, 0, 0};  // fewer than k tokens are not -inf: all of them
-                    }
-                }
-                if (mass && k.place >= 0) {
-                    uint64_t target = lane == 0 ? mass_target(s.p, Z) : 0;
-                    target = __shfl_sync(0xffffffffu, target, 0);
-                    const Border p = locate(sm, w, Goal{true, 0, target}, true);
-                    if (p.place >= 0) {
-                        const uint32_t t = ties_for(TokenWeight(w, place_value(p.place)), p.n, p.above_mass, target);
-                        take = p.place < k.place ? t : min(t, take);
-                    }
-                    k = p;
-                }
-                if (lane == 0) {
-                    sm.elsewhere = k.place < 0;
-                    sm.place = k.place;
-                    sm.take = static_cast<int>(take);
-                    sm.ties = static_cast<int>(k.n);
-                }
-            } else if (tid == 32 && s.m > 0.0f) {
-                all.row.min_p_key = min_p_key(zmax, s.T, s.m);
-            }
-            __syncthreads();
-            slow = sm.elsewhere;
-        }
-        if (CL > 1) {
-            __syncthreads();  // every thread of CTA 0 has read `odd`
-            if (rank == 0 && tid == 0) {
-                all.place = sm.place;
-                all.take = sm.take;
-                all.ties = sm.ties;
-                all.slow = slow;
-                all.odd = 0;
-            }
-            cluster_sync();
-            slow = lead.slow;
-        }
-        if (slow) {
-            if (rank > 0) continue;
-            __syncthreads();
-            if (tid < 64) all.any.table[tid] = all.table[tid];
-            __syncthreads();
-            const uint64_t cut = cut_of_row<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), V, s);
-            if (cut != 0 || logits != out) write_cut<SPEC_BF16, kThreads>(reinterpret_cast<const char *>(row), dst, V, cut);
-            continue;
-        }
-        // --- the border value: the lowest one kept, and how its ties go
-        uint32_t border = 0xff80u;  // -inf: everything
-        bool split = false;
-        if (counted) {
-            const int place = CL > 1 ? lead.place : sm.place;
-            if (place < kPlaces) border = __float_as_uint(place_value(place)) >> 16;
-            split = CL > 1 ? lead.take < lead.ties : sm.take < sm.ties;
-        }
-        if (s.m > 0.0f) {
-            // the lowest bf16 value at or above min-p's border
-            const float f = value_of(lead.row.min_p_key);
-            uint32_t h = __bfloat16_as_ushort(__float2bfloat16_ru(f));
-            if ((h & 0x7fffu) == 0) h = 0;
-            if (!counted || __uint_as_float(h << 16) > __uint_as_float(border << 16)) {
-                border = h;
-                split = false;
-            }
-        }
-        const uint32_t pair = border | border << 16;
-        // groups below the border (as keys; a zero border takes -0 too)
-        const uint32_t low = key16(border == 0 ? 0x8000u : border);
-        int cut_group = ge, cut_index = -1;
-        if (split) {
-            int take = CL > 1 ? lead.take : sm.take;
-            for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
-                uint4 q[kAhead];
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int g = g0 + u * kWarps, v = g * 32 + lane;
-                    q[u] = make_uint4(~pair, ~pair, ~pair, ~pair);
-                    if (g < ge && sm.group_max[g - gb] >= low && v < ve) q[u] = row[v];
-                }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int g = g0 + u * kWarps;
-                    if (g >= ge) break;
-                    uint32_t n = __popc(equal_mask(q[u].x, pair)) + __popc(equal_mask(q[u].y, pair)) +
-                                 __popc(equal_mask(q[u].z, pair)) + __popc(equal_mask(q[u].w, pair));
-                    n = __reduce_add_sync(0xffffffffu, n >> 4);
-                    if (lane == 0) sm.group_ties()[g - gb] = static_cast<uint16_t>(n);
-                }
-            }
-            __syncthreads();
-            // a warp's running sums of the groups' ties
-            constexpr int kRun = kMaxGroups / 32;
-            uint32_t n = 0, c = 0;
-            const int g0 = lane * kRun, g1 = min(ge - gb, g0 + kRun);
-            if (warp == 0) {
-                for (int g = g0; g < g1; ++g) n += sm.group_ties()[g];
-                c = n;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
-                    if (lane >= off) c += cc;
-                }
-            }
-            bool here = true;  // the ties run out in this CTA's groups
-            if (CL > 1) {
-                if (tid == 31) lead.rank_ties[rank] = c;
-                cluster_sync();
-                for (int i = 0; i < rank; ++i) take -= lead.rank_ties[i];
-                here = take > 0 && take < static_cast<int>(lead.rank_ties[rank]);
-                if (take <= 0) cut_group = gb;
-            }
-            if (here && warp == 0) {
-                // the group where they do, then the token
-                const int owner = __ffs(__ballot_sync(0xffffffffu, c >= static_cast<uint32_t>(take))) - 1;
-                c -= n;
-                int g = g0;
-                if (lane == owner)
-                    while (c + sm.group_ties()[g] < static_cast<uint32_t>(take)) c += sm.group_ties()[g++];
-                g = __shfl_sync(0xffffffffu, g, owner);
-                c = __shfl_sync(0xffffffffu, c, owner);
-                const int v = (gb + g) * 32 + lane;
-                uint32_t bits = 0;  // a bit per tie of this lane's vector
-                if (v < ve) {
-                    const uint4 q = row[v];
-                    const uint32_t e[4] = {equal_mask(q.x, pair), equal_mask(q.y, pair), equal_mask(q.z, pair), equal_mask(q.w, pair)};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) bits |= (e[i] & 1u) << (2 * i) | (e[i] >> 31) << (2 * i + 1);
-                }
-                uint32_t before = __popc(bits);
-                const uint32_t own = before;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const uint32_t cc = __shfl_up_sync(0xffffffffu, before, off);
-                    if (lane >= off) before += cc;
-                }
-                before += c - own;
-                if (before < static_cast<uint32_t>(take) && before + own >= static_cast<uint32_t>(take)) {
-                    for (int left = take - before; left > 1; --left) bits &= bits - 1;
-                    sm.cut_group = gb + g;
-                    sm.cut_index = v * 8 + __ffs(bits) - 1;
-                }
-            }
-            __syncthreads();
-            if (here) {
-                cut_group = sm.cut_group;
-                cut_index = sm.cut_index;
-            }
-        }
-        // --- the row out: groups below the border need not be read again
-        for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
-            uint4 q[kAhead];
-            bool kept[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int g = g0 + u * kWarps;
-                kept[u] = g < ge && sm.group_max[g - gb] >= low;
-            }
+    if (!s.active) {
+        if (logits != out)
+            for (int v = vb + tid; v < ve; v += kThreads) dst[v] = row[v];
+        return;
+    }
+    const bool mass = s.p < 1.0f, counted = mass || s.k > 0;
+    // --- one pass over the row: the histogram, the groups' largest values
+    __syncthreads();  // the last row is done with the shared arrays
+    for (int i = tid; i < 2 * kSide / 4; i += kThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
+    if (tid < 32 * kSegsPerLane - kSegs) {
+        sm.seg_count[kSegs + tid] = 0;
+        sm.seg_mass[kSegs + tid] = 0;
+    }
+    if (tid == kThreads - 1) set_scale(all.row, s);
+    if (tid == 0) {
+        sm.zeros = 0;
+        sm.first = kPlaces;
+        sm.elsewhere = false;
+    }
+    __syncthreads();
+    uint32_t odd = 0;
+    {
+        uint4 q[kAhead], next[kAhead];
+        auto load = [&](uint4 (&to)[kAhead], int g0) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int v = (g0 + u * kWarps) * 32 + lane;
-                q[u] = kept[u] && v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                to[u] = v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
             }
+        };
+        load(q, gb + warp);
+        for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
+            load(next, g0 + kWarps * kAhead);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (g0 + u * kWarps >= ge) break;
+                count_values(sm, q[u], &odd);
+                const uint32_t key = __reduce_max_sync(0xffffffffu, max_key(q[u]));
+                if (lane == 0) sm.group_max[g0 + u * kWarps - gb] = static_cast<uint16_t>(key);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) q[u] = next[u];
+        }
+    }
+    const uint32_t odd_all = (__syncthreads_or(odd & kOdd) ? kOdd : 0) | (__syncthreads_or(odd & kFiniteLow) ? kFiniteLow : 0);
+    bool slow = (odd_all & kOdd) != 0;
+    if (CL > 1) {
+        cluster_sync();  // CTA 0's sums are there to be added to
+        if (tid == 0 && odd_all) atomicOr(&lead.odd, odd_all);
+        if (rank > 0) {
+            for (int i = tid; i < 2 * kSide; i += kThreads)
+                if (const uint32_t n = sm.hist[i]) atomicAdd(&lead.fast.hist[i], n);
+            if (tid == 0 && sm.zeros) atomicAdd(&lead.fast.zeros, sm.zeros);
+        }
+        cluster_sync();
+        slow = (lead.odd & kOdd) != 0;
+    }
+    const bool finite_low = ((CL > 1 ? all.odd : odd_all) & kFiniteLow) != 0;  // (CTA 0's is meant)
+    float zmax = 0.0f;
+    if (!slow && rank == 0) {
+        // --- the bins' sums by segments of 32
+        int first = kPlaces;
+        for (int g = warp; g < kSegs; g += kWarps) {
+            uint32_t n[4];
+            sm.counts(g, n);
+            const uint32_t own = n[0] + n[1] + n[2] + n[3];
+            const uint32_t any = __ballot_sync(0xffffffffu, own > 0);
+            uint32_t sum = 0;
+            if (any) {
+                if (first == kPlaces) {
+                    const int i = n[0] ? 0 : n[1] ? 1 : n[2] ? 2 : 3, at = __ffs(any) - 1;
+                    first = g * kSegPlaces + at * 4 + __shfl_sync(0xffffffffu, i, at);
+                }
+                sum = __reduce_add_sync(0xffffffffu, own);
+            }
+            if (lane == 0) sm.seg_count[g] = sum;
+        }
+        if (lane == 0) atomicMin(&sm.first, first);
+        __syncthreads();
+        first = sm.first;
+        slow = first == kPlaces;
+        if (!slow) zmax = place_value(first);
+    }
+    // (values at or below -2^16 have no weight, and min-p excludes them)
+    if (rank == 0 && !slow && !((-65536.0f - zmax) * specv::temp_scale(s.T) < -150.0f)) slow = true;
+    Weights w{};
+    if (!slow && rank == 0) {
+        w = row_weights(all.row, zmax, V, all.table);
+        if (mass) {
+            for (int g = warp; g < kSegs; g += kWarps) {
+                uint64_t m = 0;
+                if (sm.seg_count[g]) {
+                    uint32_t n[4];
+                    sm.counts(g, n);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m += TokenWeight(w, place_value(g * kSegPlaces + lane * 4 + i)).times(n[i]);
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
+                }
+                if (lane == 0) sm.seg_mass[g] = m;
+            }
+            __syncthreads();
+        }
+        // --- the border, by one warp
+        if (warp == 0 && counted) {
+            scan_segments(sm, mass);
+            Border k{kPlaces, 0, 0, 0};
+            uint32_t take = 0;
+            uint64_t Z = mass ? sm.seg_mass[kSegs - 1] : 0;
+            if (s.k > 0) {
+                k = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass);
+                if (k.place >= 0) {
+                    take = s.k - k.above_count;
+                    if (mass) Z = k.above_mass + TokenWeight(w, place_value(k.place)).times(take);
+                } else if (!finite_low) {
+                    k = Border{kPlaces, 0, 0, 0};  // fewer than k tokens are not -inf: all of them
+                }
+            }
+            if (mass && k.place >= 0) {
+                uint64_t target = lane == 0 ? mass_target(s.p, Z) : 0;
+                target = __shfl_sync(0xffffffffu, target, 0);
+                const Border p = locate(sm, w, Goal{true, 0, target}, true);
+                if (p.place >= 0) {
+                    const uint32_t t = ties_for(TokenWeight(w, place_value(p.place)), p.n, p.above_mass, target);
+                    take = p.place < k.place ? t : min(t, take);
+                }
+                k = p;
+            }
+            if (lane == 0) {
+                sm.elsewhere = k.place < 0;
+                sm.place = k.place;
+                sm.take = static_cast<int>(take);
+                sm.ties = static_cast<int>(k.n);
+            }
+        } else if (tid == 32 && s.m > 0.0f) {
+            all.row.min_p_key = min_p_key(zmax, s.T, s.m);
+        }
+        __syncthreads();
+        slow = sm.elsewhere;
+    }
+    if (CL > 1) {
+        __syncthreads();  // every thread of CTA 0 has read `odd`
+        if (rank == 0 && tid == 0) {
+            all.place = sm.place;
+            all.take = sm.take;
+            all.ties = sm.ties;
+            all.slow = slow;
+        }
+        cluster_sync();
+        slow = lead.slow;
+    }
+    if (slow) {
+        if (CL > 1) cluster_sync();  // CTA 0's shared memory has been read
+        if (rank > 0) return;
+        __syncthreads();
+        if (tid < 64) all.any.table[tid] = all.table[tid];
+        __syncthreads();
+        const uint64_t cut = cut_of_row<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), V, s);
+        if (cut != 0 || logits != out) write_cut<SPEC_BF16, kThreads>(reinterpret_cast<const char *>(row), dst, V, cut);
+        return;
+    }
+    // --- the border value: the lowest one kept, and how its ties go
+    uint32_t border = 0xff80u;  // -inf: everything
+    bool split = false;
+    if (counted) {
+        const int place = CL > 1 ? lead.place : sm.place;
+        if (place < kPlaces) border = __float_as_uint(place_value(place)) >> 16;
+        split = CL > 1 ? lead.take < lead.ties : sm.take < sm.ties;
+    }
+    if (s.m > 0.0f) {
+        // the lowest bf16 value at or above min-p's border
+        const float f = value_of(lead.row.min_p_key);
+        uint32_t h = __bfloat16_as_ushort(__float2bfloat16_ru(f));
+        if ((h & 0x7fffu) == 0) h = 0;
+        if (!counted || __uint_as_float(h << 16) > __uint_as_float(border << 16)) {
+            border = h;
+            split = false;
+        }
+    }
+    const uint32_t pair = border | border << 16;
+    // groups below the border (as keys; a zero border takes -0 too)
+    const uint32_t low = key16(border == 0 ? 0x8000u : border);
+    int cut_group = ge, cut_index = -1;
+    if (split) {
+        int take = CL > 1 ? lead.take : sm.take;
+        for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
+            uint4 q[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int g = g0 + u * kWarps, v = g * 32 + lane;
-                if (v >= ve) continue;
-                if (kept[u]) {
-                    uint32_t x[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-                    const bool equal = g < cut_group;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t keep = above_mask(x[i], pair, equal);
-                        if (g == cut_group) {
-                            const uint32_t e = equal_mask(x[i], pair);
-                            if (v * 8 + 2 * i <= cut_index) keep |= e & 0xffffu;
-                            if (v * 8 + 2 * i + 1 <= cut_index) keep |= e & 0xffff0000u;
-                        }
-                        x[i] = (x[i] & keep) | (0xff80ff80u & ~keep);
-                    }
-                    q[u] = make_uint4(x[0], x[1], x[2], x[3]);
-                }
-                dst[v] = q[u];
+                q[u] = make_uint4(~pair, ~pair, ~pair, ~pair);
+                if (g < ge && sm.group_max[g - gb] >= low && v < ve) q[u] = row[v];
             }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int g = g0 + u * kWarps;
+                if (g >= ge) break;
+                uint32_t n = __popc(equal_mask(q[u].x, pair)) + __popc(equal_mask(q[u].y, pair)) +
+                             __popc(equal_mask(q[u].z, pair)) + __popc(equal_mask(q[u].w, pair));
+                n = __reduce_add_sync(0xffffffffu, n >> 4);
+                if (lane == 0) sm.group_ties()[g - gb] = static_cast<uint16_t>(n);
+            }
+        }
+        __syncthreads();
+        // a warp's running sums of the groups' ties
+        constexpr int kRun = kMaxGroups / 32;
+        uint32_t n = 0, c = 0;
+        const int g0 = lane * kRun, g1 = min(ge - gb, g0 + kRun);
+        if (warp == 0) {
+            for (int g = g0; g < g1; ++g) n += sm.group_ties()[g];
+            c = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
+                if (lane >= off) c += cc;
+            }
+        }
+        bool here = true;  // the ties run out in this CTA's groups
+        if (CL > 1) {
+            if (tid == 31) lead.rank_ties[rank] = c;
+            cluster_sync();
+            for (int i = 0; i < rank; ++i) take -= lead.rank_ties[i];
+            here = take > 0 && take < static_cast<int>(lead.rank_ties[rank]);
+            if (take <= 0) cut_group = gb;
+        }
+        if (here && warp == 0) {
+            // the group where they do, then the token
+            const int owner = __ffs(__ballot_sync(0xffffffffu, c >= static_cast<uint32_t>(take))) - 1;
+            c -= n;
+            int g = g0;
+            if (lane == owner)
+                while (c + sm.group_ties()[g] < static_cast<uint32_t>(take)) c += sm.group_ties()[g++];
+            g = __shfl_sync(0xffffffffu, g, owner);
+            c = __shfl_sync(0xffffffffu, c, owner);
+            const int v = (gb + g) * 32 + lane;
+            uint32_t bits = 0;  // a bit per tie of this lane's vector
+            if (v < ve) {
+                const uint4 q = row[v];
+                const uint32_t e[4] = {equal_mask(q.x, pair), equal_mask(q.y, pair), equal_mask(q.z, pair), equal_mask(q.w, pair)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bits |= (e[i] & 1u) << (2 * i) | (e[i] >> 31) << (2 * i + 1);
+            }
+            uint32_t before = __popc(bits);
+            const uint32_t own = before;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t cc = __shfl_up_sync(0xffffffffu, before, off);
+                if (lane >= off) before += cc;
+            }
+            before += c - own;
+            if (before < static_cast<uint32_t>(take) && before + own >= static_cast<uint32_t>(take)) {
+                for (int left = take - before; left > 1; --left) bits &= bits - 1;
+                sm.cut_group = gb + g;
+                sm.cut_index = v * 8 + __ffs(bits) - 1;
+            }
+        }
+        __syncthreads();
+        if (here) {
+            cut_group = sm.cut_group;
+            cut_index = sm.cut_index;
+        }
+    }
+    // --- the row out: groups below the border need not be read again
+    for (int g0 = gb + warp; g0 < ge; g0 += kWarps * kAhead) {
+        uint4 q[kAhead];
+        bool kept[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int g = g0 + u * kWarps;
+            kept[u] = g < ge && sm.group_max[g - gb] >= low;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int v = (g0 + u * kWarps) * 32 + lane;
+            q[u] = kept[u] && v < ve ? row[v] : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int g = g0 + u * kWarps, v = g * 32 + lane;
+            if (v >= ve) continue;
+            if (kept[u]) {
+                uint32_t x[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                const bool equal = g < cut_group;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t keep = above_mask(x[i], pair, equal);
+                    if (g == cut_group) {
+                        const uint32_t e = equal_mask(x[i], pair);
+                        if (v * 8 + 2 * i <= cut_index) keep |= e & 0xffffu;
+                        if (v * 8 + 2 * i + 1 <= cut_index) keep |= e & 0xffff0000u;
+                    }
+                    x[i] = (x[i] & keep) | (0xff80ff80u & ~keep);
+                }
+                q[u] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            dst[v] = q[u];
         }
     }
     if (CL > 1) cluster_sync();  // CTA 0's shared memory is read until here
@@ -1417,7 +1398,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 template <int CL>
 cudaError_t launch_bf16(const char *in, char *to, const Rows &rw, const Truncate &tr, int V, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(std::min(rw.R, sms * kPerSm / CL) * CL);
+    cfg.gridDim = dim3(rw.R * CL);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(BothShared);
     cfg.stream = stream;
@@ -1449,7 +1430,7 @@ int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncat
         constexpr int T = any_threads(DT);
         const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
         const bool held = DT == SPEC_F32 && bytes <= kMostHeld;
-        truncate_kernel<DT, T><<<std::min(rw.R, sms * 1024 / T), T, kAnyShared + (held ? bytes : 0), stream>>>(in, to, rw, tr,
+        truncate_kernel<DT, T><<<rw.R, T, kAnyShared + (held ? bytes : 0), stream>>>(in, to, rw, tr,
                                                                                                           V, held);
     }
     return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
