@@ -39,7 +39,14 @@ constexpr int kBias = 64;     // bias entries kept in shared memory
 #ifndef SPEC_PROCESS_SPREAD_MB
 #define SPEC_PROCESS_SPREAD_MB 300
 #endif
-constexpr int kPerSm = SPEC_PROCESS_PER_SM;  // resident CTAs
+#ifndef SPEC_SPARSE_WORDS
+#define SPEC_SPARSE_WORDS 128
+#endif
+#ifndef SPEC_SPARSE_PER_SM
+#define SPEC_SPARSE_PER_SM 6
+#endif
+template <bool STREAM>
+constexpr int kPerSm = STREAM ? SPEC_PROCESS_PER_SM : SPEC_SPARSE_PER_SM;  // resident CTAs
 
 template <int DT>
 constexpr uint32_t kNanWord = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
@@ -56,7 +63,7 @@ struct Units {
 template <bool STREAM>
 struct Group {
     static constexpr int kSize = STREAM ? kThreads : 32;
-    static constexpr int kWords = 128;
+    static constexpr int kWords = STREAM ? 128 : SPEC_SPARSE_WORDS;
     static constexpr int kWordsEach = kWords / kSize;
     static constexpr int kCount = kThreads / kSize;  // groups per CTA
 
@@ -85,6 +92,7 @@ struct Group {
 
 template <bool STREAM>
 struct GroupShared {
+    int mask[kMaxPath + 1];     // by row: its mask, -1: none, -2: none there is
     int token[kMaxPath];
     int up[kMaxPath];           // tree: parent within the sequence
     uint64_t before[kMaxPath];  // tree: the nodes whose tokens a row follows
@@ -124,7 +132,6 @@ __device__ __forceinline__ void mask_vec(uint4 &q, uint32_t allowed) {
 
 // The mask of a row: its number, -1 for none, -2 where it names none there is.
 __device__ __forceinline__ int mask_of(const Process &ps, int row) {
-    if (!ps.mask) return -1;
     const int m = ps.mask_rows ? __ldg(ps.mask_rows + row) : row;
     return m < -1 || m >= ps.M ? -2 : m;
 }
@@ -132,8 +139,8 @@ __device__ __forceinline__ int mask_of(const Process &ps, int row) {
 // The stream over rows row0 + i0 .. row0 + i1 - 1 of a CTA's columns: a copy with
 // the masks applied; in place only what a mask takes away.
 template <int DT>
-__device__ __forceinline__ void stream_rows(const char *logits, char *out, const Process &ps, int V, int row0, int i0,
-                                            int i1, const Units &un, bool inplace) {
+__device__ __forceinline__ void stream_rows(const char *logits, char *out, const Process &ps, const int *mask_rows, int V, int row0,
+                                            int i0, int i1, const Units &un, bool inplace) {
     using G = Group<true>;
     constexpr int kPer = Elem<DT>::kPerVec;
     constexpr int kVecs = 32 / kPer;                // a thread's vectors of one row
@@ -173,7 +180,7 @@ __device__ __forceinline__ void stream_rows(const char *logits, char *out, const
         uint4 q[kRows][kVecs];
         int m[kRows];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) m[u] = i + u < i1 ? mask_of(ps, row0 + i + u) : -3;
+        for (int u = 0; u < kRows; ++u) m[u] = i + u < i1 ? mask_rows[i + u] : -3;
 #pragma unroll
         for (int u = 0; u < kRows; ++u)
 #pragma unroll
@@ -228,7 +235,7 @@ __device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0,
 // (sequence, unit): the ones that run at a time stream through one window of
 // memory.
 template <int DT, bool STREAM>
-__global__ void __launch_bounds__(kThreads, kPerSm)
+__global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
     process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int units, int piece, int parts) {
     using G = Group<STREAM>;
     __shared__ GroupShared<STREAM> s_group[G::kCount];
@@ -239,17 +246,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     const int W = (V + 31) / 32;
     const bool pen = ps.counts != nullptr, tree = rw.mode == SPEC_ROWS_TREE;
 
-    const int64_t groups = static_cast<int64_t>(gridDim.x) * G::kCount;
-    const int64_t self = static_cast<int64_t>(blockIdx.x) * G::kCount + G::self();
+    // (32 bits hold the number of a group: it is at most 64 times the rows' units)
+    const uint32_t self = blockIdx.x * G::kCount + G::self();
     if (!check_rows(rw, pen)) {
         // the call fails: every row is NaN
-        for (int64_t u = self; u < static_cast<int64_t>(rw.R) * units; u += groups)
+        for (int64_t u = self; u < static_cast<int64_t>(rw.R) * units; u += static_cast<int64_t>(gridDim.x) * G::kCount)
             nan_rows<DT, STREAM>(out, V, u / units, 0, 1, Units{static_cast<int>(u % units), units, piece});
         return;
     }
-    const int64_t pair = self / parts;
+    const uint32_t pair = self / parts;
     const int part = static_cast<int>(self - pair * parts), b = static_cast<int>(pair / units);
-    const Units un{static_cast<int>(pair - static_cast<int64_t>(b) * units), units, piece};
+    const Units un{static_cast<int>(pair - static_cast<uint32_t>(b) * units), units, piece};
     if (b >= rw.B) return;
     {
         const int o0 = __ldg(rw.offsets + b), o1 = __ldg(rw.offsets + b + 1);
@@ -295,7 +302,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                 e1 = e0 = 0;
             }
         }
-        if (STREAM) stream_rows<DT>(logits, out, ps, V, row0, i0, i1, un, inplace);
+        if (ps.mask) {
+            for (int i = i0 + me; i < i1; i += G::kSize) sm.mask[i] = mask_of(ps, row0 + i);
+            G::sync();
+        }
+        if (STREAM) stream_rows<DT>(logits, out, ps, sm.mask, V, row0, i0, i1, un, inplace);
 
         // --- the unit's columns that anything applies to
 #pragma unroll
@@ -376,17 +387,31 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             for (int base = 0; base < listed; base += kList) {
                 const int len = min(kList, listed - base);
                 G::sync();
-                int at_rank = rank - base;
+                int at = rank - base;  // the place of the thread's next column in the list
+                auto put = [&](int to, int col, int bit, uint32_t p, uint32_t e, uint32_t d, uint32_t x) {
+                    if (to < 0 || to >= kList) return;
+                    sm.column[to] = col + bit;
+                    sm.flags[to] = static_cast<uint8_t>((p >> bit & 1) * kPrompt | (e >> bit & 1) * kEmitted | (d >> bit & 1) * kDrafted |
+                                                        (x >> bit & 1) * kBiased);
+                };
 #pragma unroll
                 for (int i = 0; i < G::kWordsEach; ++i) {
-                    const int col0 = G::word(un, i * G::kSize + me) * 32;
-                    for (uint32_t m = touched[i]; m; m &= m - 1, ++at_rank) {
-                        if (at_rank < 0 || at_rank >= kList) continue;
-                        const int bit = __ffs(m) - 1;
-                        sm.column[at_rank] = col0 + bit;
-                        sm.flags[at_rank] = static_cast<uint8_t>((prompt[i] >> bit & 1) * kPrompt | (emitted[i] >> bit & 1) * kEmitted |
-                                                                 (drafted[i] >> bit & 1) * kDrafted | (biased[i] >> bit & 1) * kBiased);
+                    // words with few columns by their threads, full ones (frequent ids) by the warp
+                    const int col = G::word(un, i * G::kSize + me) * 32, n_i = __popc(touched[i]);
+                    const bool full = n_i > 4;
+                    if (!full) {
+                        int to = at;
+                        for (uint32_t m = touched[i]; m; m &= m - 1) put(to++, col, __ffs(m) - 1, prompt[i], emitted[i], drafted[i], biased[i]);
                     }
+                    for (uint32_t m = __ballot_sync(0xffffffffu, full); m; m &= m - 1) {
+                        const int src = __ffs(m) - 1;
+                        const uint32_t word = __shfl_sync(0xffffffffu, touched[i], src);
+                        const int first = __shfl_sync(0xffffffffu, at, src), c = __shfl_sync(0xffffffffu, col, src);
+                        const uint32_t p = __shfl_sync(0xffffffffu, prompt[i], src), e = __shfl_sync(0xffffffffu, emitted[i], src);
+                        const uint32_t d = __shfl_sync(0xffffffffu, drafted[i], src), x = __shfl_sync(0xffffffffu, biased[i], src);
+                        if (word >> lane & 1) put(first + __popc(word & ((1u << lane) - 1)), c, lane, p, e, d, x);
+                    }
+                    at += n_i;
                 }
                 G::sync();
                 // a thread takes a column, all its rows
@@ -413,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                         for (int u = 0; u < kRows; ++u) {
                             go[u] = i + u < i1;
                             if (go[u] && ps.mask) {
-                                const int m = mask_of(ps, row0 + i + u);
+                                const int m = sm.mask[i + u];
                                 go[u] = m == -1 || (m >= 0 && ((bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7)) & 1));
                             }
                         }
@@ -488,7 +513,9 @@ __global__ void __launch_bounds__(kResetThreads)
     const int p0 = prompt_offsets ? __ldg(prompt_offsets + e) : 0, p1 = prompt_offsets ? __ldg(prompt_offsets + e + 1) : 0;
     const int q0 = output_offsets ? __ldg(output_offsets + e) : 0, q1 = output_offsets ? __ldg(output_offsets + e + 1) : 0;
     skip |= p0 < 0 || p1 < p0 || p1 > n_prompt || q0 < 0 || q1 < q0 || q1 > n_output;
-    for (int i = tid; i < kResetChunk; i += kResetThreads) s_count[i] = 0;
+    const bool emitted = q1 > q0;  // (uniform) else the counts are zero
+    if (emitted)
+        for (int i = tid; i < kResetChunk; i += kResetThreads) s_count[i] = 0;
     for (int i = tid; i < kResetChunk / 32; i += kResetThreads) s_prompt[i] = 0;
     if (__syncthreads_or(skip)) return;
     // every chunk's CTA reads the whole lists (from L2), several tokens in flight a thread
@@ -509,6 +536,17 @@ __global__ void __launch_bounds__(kResetThreads)
     const int cols = min(kResetChunk, V - c0);
     int32_t *crow = counts + static_cast<int64_t>(slot) * V + c0;
     int32_t *srow = seen + static_cast<int64_t>(slot) * 2 * W + c0 / 32;
+    if (!emitted) {
+        if (V % 4 == 0 && reinterpret_cast<uintptr_t>(counts) % 16 == 0)
+            for (int i = tid; i < cols / 4; i += kResetThreads) reinterpret_cast<int4 *>(crow)[i] = make_int4(0, 0, 0, 0);
+        else
+            for (int i = tid; i < cols; i += kResetThreads) crow[i] = 0;
+        for (int i = tid; i < (cols + 31) / 32; i += kResetThreads) {
+            srow[i] = static_cast<int32_t>(s_prompt[i]);
+            srow[W + i] = 0;
+        }
+        return;
+    }
     for (int i = tid; i < (cols + 31) / 32 * 32; i += kResetThreads) {
         const int n = s_count[i];
         if (i < cols) crow[i] = n;
@@ -531,7 +569,7 @@ int launch_process(const void *logits, void *out, const Rows &rw, const Process 
     const int units = G::units(V, piece);
     const int64_t pairs = static_cast<int64_t>(rw.B) * units;
     // few sequences: their rows are split until every SM has its CTAs
-    const int64_t room = static_cast<int64_t>(sms) * kPerSm * G::kCount;
+    const int64_t room = static_cast<int64_t>(sms) * kPerSm<STREAM> * G::kCount;
     const int parts = static_cast<int>(std::clamp<int64_t>(room / pairs, 1, std::max(1, rw.R / rw.B)));
     const int64_t ctas = (pairs * parts + G::kCount - 1) / G::kCount;
     process_kernel<DT, STREAM><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(
