@@ -30,23 +30,8 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 256;    // columns listed at once
 constexpr int kBias = 64;     // bias entries kept in shared memory
-#ifndef SPEC_PROCESS_PER_SM
-#define SPEC_PROCESS_PER_SM 6
-#endif
-#ifndef SPEC_PROCESS_PIECE
-#define SPEC_PROCESS_PIECE 1  // 2 words: a 128-byte line of bf16
-#endif
-#ifndef SPEC_PROCESS_SPREAD_MB
-#define SPEC_PROCESS_SPREAD_MB 300
-#endif
-#ifndef SPEC_SPARSE_WORDS
-#define SPEC_SPARSE_WORDS 128
-#endif
-#ifndef SPEC_SPARSE_PER_SM
-#define SPEC_SPARSE_PER_SM 6
-#endif
 template <bool STREAM>
-constexpr int kPerSm = STREAM ? SPEC_PROCESS_PER_SM : SPEC_SPARSE_PER_SM;  // resident CTAs
+constexpr int kPerSm = STREAM ? 6 : 8;  // resident CTAs
 
 template <int DT>
 constexpr uint32_t kNanWord = DT == SPEC_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
@@ -63,7 +48,7 @@ struct Units {
 template <bool STREAM>
 struct Group {
     static constexpr int kSize = STREAM ? kThreads : 32;
-    static constexpr int kWords = STREAM ? 128 : SPEC_SPARSE_WORDS;
+    static constexpr int kWords = 128;
     static constexpr int kWordsEach = kWords / kSize;
     static constexpr int kCount = kThreads / kSize;  // groups per CTA
 
@@ -494,10 +479,7 @@ __global__ void __launch_bounds__(kUpdateThreads)
 // in shared memory from the entry's tokens and writes them out whole, so the
 // state is written once and needs no clearing before.
 constexpr int kResetThreads = 256;
-#ifndef SPEC_RESET_CHUNK
-#define SPEC_RESET_CHUNK 8192
-#endif
-constexpr int kResetChunk = SPEC_RESET_CHUNK;
+constexpr int kResetChunk = 8192;
 constexpr int kResetAhead = 8;  // tokens in flight per thread
 
 __global__ void __launch_bounds__(kResetThreads)
@@ -563,9 +545,10 @@ int launch_process(const void *logits, void *out, const Rows &rw, const Process 
                    cudaStream_t stream) {
     using G = Group<STREAM>;
     // Spread pieces even out the frequent ids, whole units keep the CTAs that run at
-    // a time in one window of memory: SPREAD_COMMENT
-    const bool spread = !STREAM || static_cast<int64_t>(rw.R) * V * Elem<DT>::kBytes <= static_cast<int64_t>(SPEC_PROCESS_SPREAD_MB) << 20;
-    const int piece = !STREAM ? 0 : spread ? SPEC_PROCESS_PIECE : 7;
+    // a time in one window of memory.  384 rows of 128256 bf16 (98 MB) took 48 us spread
+    // and 62 whole, 1024 rows 119 and 130; 3267 rows (838 MB) 620 spread and 349 whole.
+    const bool spread = !STREAM || static_cast<int64_t>(rw.R) * V * Elem<DT>::kBytes <= static_cast<int64_t>(300) << 20;
+    const int piece = !STREAM ? 0 : spread ? 1 : 7;
     const int units = G::units(V, piece);
     const int64_t pairs = static_cast<int64_t>(rw.B) * units;
     // few sequences: their rows are split until every SM has its CTAs

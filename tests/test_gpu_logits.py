@@ -144,6 +144,48 @@ def test_process_in_place_and_padded(sv, dtype, V):
     assert same_bits(host(out)[:R], want[:R]).all() and (host(out)[R:] == 7).all()
 
 
+@pytest.mark.parametrize("mode", ["target", "next", "tree"])
+@pytest.mark.parametrize("dtype,V", [("bf16", 264), ("bf16", 32000), ("fp32", 9004)])
+def test_process_in_place_without_masks(sv, mode, dtype, V):
+    """In place and without masks only the touched columns are visited (another kernel); frequent ids are the lowest."""
+    rng = np.random.default_rng(15)
+    rows = make_rows(rng, mode, KS["ragged"], V)
+    z = make_logits(rng, rows.count(), V, dtype)
+    p = make_params(rng, rows, len(z), V, mask=False)
+    p["counts"][:, :200] = 3  # dense words
+    p["seen"][:, 1] = ref.pack(p["counts"] > 0)
+    want, _, _ = ref.process(z, rows, p, dtype)
+    x = dev(z, dtype)
+    sv.spec_logits_process(x, dev(rows.offsets), dev(rows.tokens), rows=mode, parent=None if rows.parent is None else dev(rows.parent),
+                           out=x, **{k: dev(v) for k, v in p.items()})
+    assert same_bits(host(x), want).all()
+    bad = host(process(sv, z, rows, {**p, "repetition": np.where(np.arange(rows.B) == 2, f32(-1), p["repetition"])}, dtype, out=dev(z, dtype)))
+    seq = ref.row_sequences(rows)
+    assert np.isnan(bad[seq == 2]).all() and same_bits(bad[seq != 2], want[seq != 2]).all()
+
+
+def test_process_spread_and_whole_units(sv):
+    """The layouts for small calls and for large ones (over 300 MB) give the same rows."""
+    rng = np.random.default_rng(16)
+    V, B = 64008, 700
+    rows = make_rows(rng, "target", [3] * B, V)
+    z = make_logits(rng, 64, V, "bf16")
+    z = z[rng.integers(0, 64, rows.count())]
+    p = make_params(rng, rows, len(z), V, S=5, mask=False)
+    p["mask"] = ref.pack(rng.random((7, V)) < 0.5)
+    p["mask_rows"] = rng.integers(-1, 7, len(z)).astype(i32)
+    got = host(process(sv, z, rows, p, "bf16"))
+    at = rng.choice(B, 6, replace=False)
+    for b in at:
+        one = ref.Rows("target", i32([0, 3]), rows.tokens[3 * b:3 * b + 3])
+        sl = slice(4 * b, 4 * b + 4)
+        e = p["bias_offsets"]
+        q = {k: v for k, v in p.items() if k in ("counts", "seen", "mask")}
+        q.update({k: p[k][b:b + 1] for k in ("slots", "repetition", "frequency", "presence")}, mask_rows=p["mask_rows"][sl],
+                 bias_offsets=i32([0, e[b + 1] - e[b]]), bias_tokens=p["bias_tokens"][e[b]:e[b + 1]], bias_values=p["bias_values"][e[b]:e[b + 1]])
+        assert same_bits(got[sl], ref.process(z[sl], one, q, "bf16")[0]).all()
+
+
 def broken(name, rows, p, V):
     """Makes one sequence (its number is returned) or one row (as ~row) invalid."""
     o = rows.offsets
@@ -444,6 +486,22 @@ def test_truncate_hard_rows(sv, what, dtype, V):
         check_truncate(got, z, np.arange(B), T, s)
 
 
+@pytest.mark.parametrize("V", [10000, 20000, 70000])
+@pytest.mark.parametrize("B", [3, 60, 120, 330])
+def test_truncate_rows_shared_or_not(sv, V, B):
+    """Few rows are shared by clusters of 2, 4 and 8 CTAs, many are not; ties across the CTAs' parts of a row."""
+    rng = np.random.default_rng(B + V)
+    z = zipf(rng, min(B, 24), V, "bf16", 0.25)
+    z[1, 5] = 2.0 ** -40  # a value without a bin
+    z[2, ::2] = -np.inf
+    rows = np.arange(B) % len(z)
+    off, T = np.zeros(B + 1, i32), rng.choice(f32([0.5, 1.0]), B)
+    s = settings(rng, "kp", B, V)
+    got = host(truncate(sv, z[rows], off, T, s, "bf16"))
+    check = np.arange(B) if B < 30 else np.concatenate([np.arange(12), rng.choice(np.arange(12, B), 12, replace=False)])
+    check_truncate(got[check], z[rows[check]], check, T, s)
+
+
 @pytest.mark.parametrize("dtype,V", [("bf16", 1032), ("fp32", 4100)])
 def test_truncate_left_alone(sv, dtype, V):
     """Greedy rows, rows with NaN or +inf, rows of -inf: their own bits.  And nothing set: every row."""
@@ -493,6 +551,50 @@ def test_truncate_layouts(sv, mode):
     x = dev(z, "bf16")
     sv.spec_logits_truncate(x, dev(T), dev(rows.offsets), rows=mode, out=x, **{k: dev(v) for k, v in s.items()})
     assert same_bits(host(x)[:-2], got[:-2]).all() and same_bits(host(x)[-2:], z[-2:]).all()
+
+
+# ------------------------------------------------------------------- the limits
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_largest_vocabulary(sv, dtype):
+    """MAX_V columns, processed and truncated."""
+    rng = np.random.default_rng(31)
+    V = sv.MAX_V
+    rows = ref.Rows("target", i32([0, 1]), i32([V - 1]))
+    z = zipf(rng, 2, V, dtype)
+    st = sv.PenaltyState(1, V)
+    prompt = rng.integers(0, V, 5000).astype(i32)
+    st.reset(dev(i32([0])), dev(i32([0, 5000])), dev(prompt), dev(i32([0, 3])), dev(i32([7, V - 1, 7])))
+    p = dict(counts=st.counts.cpu().numpy(), seen=st.seen.cpu().numpy(), repetition=f32([1.5]), frequency=f32([0.5]))
+    assert p["counts"].sum() == 3 and p["counts"][0, V - 1] == 1
+    want, _, _ = ref.process(z, rows, p, dtype)
+    x = process(sv, z, rows, {k: v for k, v in p.items()}, dtype)
+    assert same_bits(host(x), want).all()
+    s = dict(top_p=f32([0.9]), min_p=f32([1e-5]))
+    got = host(sv.spec_logits_truncate(x, dev(f32([0.8])), dev(rows.offsets), **{k: dev(v) for k, v in s.items()}))
+    check_truncate(got, want, [0, 0], f32([0.8]), s)
+
+
+def test_offsets_past_32_bits(sv):
+    """Rows that start behind 4 GB: the last ones as the same rows alone."""
+    V, B = sv.MAX_V, 140  # 4.7 GB of bf16
+    x = torch.empty(B, V, dtype=torch.bfloat16, device="cuda")
+    x.copy_(torch.randn(1, V, device="cuda"))
+    x[-2:] = torch.randn(2, V, device="cuda").to(torch.bfloat16)
+    last = x[-2:].clone()
+    off = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    tok = torch.zeros(0, dtype=torch.int32, device="cuda")
+    bias = dict(bias_tokens=torch.full((B,), V - 1, dtype=torch.int32, device="cuda"), bias_values=torch.full((B,), 9.0, device="cuda"))
+    count = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    y = sv.spec_logits_process(x, off, tok, bias_offsets=count, **bias)
+    one = sv.spec_logits_process(last, off[:3], tok, bias_offsets=count[:3], **{k: v[:2] for k, v in bias.items()})
+    assert torch.equal(y[-2:], one) and float(one[0, -1]) == float((last[0, -1].float() + 9).to(torch.bfloat16))
+    assert torch.equal(y[:-2, :-1], x[:-2, :-1])
+    sv.spec_logits_process(x, off, tok, bias_offsets=count, out=x, **bias)
+    assert torch.equal(x, y)
+    k = torch.full((B,), 40, dtype=torch.int32, device="cuda")
+    sv.spec_logits_truncate(x, torch.ones(B, device="cuda"), off, top_k=k, out=x)
+    alone = sv.spec_logits_truncate(one, torch.ones(2, device="cuda"), off[:3], top_k=k[:2])
+    assert torch.equal(x[-2:], alone) and bool((torch.isfinite(x).sum(1) == 40).all())
 
 
 # ------------------------------------------------------------------------- both
