@@ -29,6 +29,7 @@ constexpr int kPerSm = 2;  // resident CTAs
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 1024;        // elements of one bin that are sorted in shared memory
+constexpr int kAnyGroups = 2048;   // groups of 32 vectors whose largest values are kept
 constexpr int kBinsPerOctave = 32;  // first-level bins per halving of the weight
 
 struct Truncate {
@@ -178,6 +179,7 @@ struct Shared {
     float2 table[64];
     uint32_t count[kBins], lo[kBins], hi[kBins];
     uint64_t list[kList];
+    uint32_t group_max[kAnyGroups];  // of rows with at most so many groups
     uint64_t warp_mass[32];
     uint32_t warp_count[32];
     uint32_t red[32];
@@ -283,34 +285,71 @@ __device__ __noinline__ void find_bin(Shared &sm, const Goal &goal, uint32_t abo
     __syncthreads();
 }
 
-// f(value, index) for a row's elements, a thread's next vectors loaded before it works on these.
-template <int DT, int T, typename F>
-__device__ __forceinline__ void for_each(const char *row, int V, F &&f) {
-    // (bf16 rows come here rarely: small code, beside the pass that they usually take)
-    constexpr int kPer = Elem<DT>::kPerVec, kFlight = DT == SPEC_F32 ? 2 : 1;
+// f(value, index) for a row's elements, several vectors of a thread in flight;
+// groups (a warp's 32 vectors) whose largest key is below `low` are passed over.
+// (bf16 rows come here rarely: small code, beside the pass that they usually take)
+template <int DT>
+constexpr int kFlight = DT == SPEC_F32 ? 4 : 1;
+template <int DT, int T, int FLIGHT, typename F>
+__device__ __forceinline__ void for_each(const Shared &sm, const char *row, int V, uint32_t low, F &&f) {
+    constexpr int kPer = Elem<DT>::kPerVec;
     const uint4 *p = reinterpret_cast<const uint4 *>(row);
     const int vecs = V / kPer;
-    for (int v0 = threadIdx.x; v0 < vecs; v0 += T * kFlight) {
-        uint4 q[kFlight];
+    for (int v0 = threadIdx.x; v0 < vecs; v0 += T * FLIGHT) {
+        uint4 q[FLIGHT];
+        bool in[FLIGHT];
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u)
-            if (v0 + u * T < vecs) q[u] = p[v0 + u * T];
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
+        for (int u = 0; u < FLIGHT; ++u) {
             const int v = v0 + u * T;
-            if (v >= vecs) break;
+            in[u] = v < vecs && (low == 0 || sm.group_max[v >> 5] >= low);
+            if (in[u]) q[u] = p[v];
+        }
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            if (!in[u]) continue;
             float x[kPer];
             Elem<DT>::unpack(q[u], x);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) f(x[i], v * kPer + i);
+            for (int i = 0; i < kPer; ++i) f(x[i], (v0 + u * T) * kPer + i);
         }
     }
+}
+// The largest value (NaN if there is one) and the groups' largest keys.
+template <int DT, int T>
+__device__ __forceinline__ float largest(Shared &sm, const char *row, int V, bool grouped) {
+    constexpr int kPer = Elem<DT>::kPerVec, FLIGHT = kFlight<DT>;
+    const uint4 *p = reinterpret_cast<const uint4 *>(row);
+    const int vecs = V / kPer, lane = threadIdx.x & 31;
+    float top = __int_as_float(0xff800000);
+    for (int v0 = threadIdx.x; v0 - lane < vecs; v0 += T * FLIGHT) {
+        uint4 q[FLIGHT];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u)
+            if (v0 + u * T < vecs) q[u] = p[v0 + u * T];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            const int v = v0 + u * T;
+            if (v - lane >= vecs) break;
+            const float m = v < vecs ? Elem<DT>::vmax_nan(q[u]) : __int_as_float(0xff800000);
+            top = specv::fmax_nan(top, m);
+            const uint32_t key = __reduce_max_sync(0xffffffffu, key_of(m));
+            if (grouped && lane == 0) sm.group_max[v >> 5] = key;
+        }
+    }
+    return top;
 }
 
 // (scale is finite, so the largest value is in bin 0)
 __device__ __forceinline__ int first_bin(float z, float zmax, float scale) {
     // to the nearest whole number, by the bits of 2^23 + x (a conversion is slower)
     return __float_as_int(__fadd_rn(fminf(__fmul_rn(__fsub_rn(zmax, z), scale), static_cast<float>(kBins - 1)), 8388608.0f)) & (kBins - 1);
+}
+
+// A key that no element of the bins up to `bin` is below (0 where groups are not kept).
+__device__ __forceinline__ uint32_t bin_low(int bin, float zmax, float scale, bool grouped) {
+    if (!grouped || bin >= kBins - 1) return 0;
+    const float z = zmax - (static_cast<float>(bin) + 1.0f) / scale;  // half a bin lower than need be
+    return isfinite(z) ? key_of(z - fabsf(z) * 1e-6f) : 0;
 }
 
 __device__ __forceinline__ void add_to_bin(Shared &sm, int bin, bool mass, uint64_t w) {
@@ -388,7 +427,7 @@ __device__ __noinline__ void place_in_list(Shared &sm, uint32_t n, const Weights
 // the mass of the tokens up to it in sm.mass.
 template <int DT, int T>
 __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, const Weights &w, float scale,
-                                        const Goal &goal, bool mass) {
+                                        const Goal &goal, bool mass, bool grouped) {
     const int bin = sm.bin;
     uint32_t above_count = sm.above_count, n = sm.bin_count;
     uint64_t above_mass = sm.above_mass;
@@ -400,7 +439,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
     }
     __syncthreads();
     uint32_t klo = 0xffffffffu, khi = 0;
-    for_each<DT, T>(row, V, [&](float z, int i) {
+    for_each<DT, T, kFlight<DT>>(sm, row, V, bin_low(bin, w.zmax, scale, grouped), [&](float z, int i) {
         if (first_bin(z, w.zmax, scale) != bin) return;
         const uint32_t key = key_of(z);
         klo = min(klo, key);
@@ -421,7 +460,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
         // 2048 equal parts of the keys khi .. klo
         const int shift = max(0, 32 - __clz(khi - klo) - 11);
         clear_bins<T>(sm);
-        for_each<DT, T>(row, V, [&](float z, int) {
+        for_each<DT, T, 1>(sm, row, V, grouped ? klo : 0, [&](float z, int) {
             const uint32_t key = key_of(z);
             if (key < klo || key > khi) return;
             add_to_bin(sm, static_cast<int>((khi - key) >> shift), mass, mass ? fixed_weight(w, z) : 0);
@@ -440,7 +479,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
         if (n <= kList) {
             if (threadIdx.x == 0) sm.n_list = 0;
             __syncthreads();
-            for_each<DT, T>(row, V, [&](float z, int i) {
+            for_each<DT, T, 1>(sm, row, V, grouped ? klo : 0, [&](float z, int i) {
                 const uint32_t key = key_of(z);
                 if (key >= klo && key <= khi) sm.list[atomicAdd(&sm.n_list, 1u)] = place_of(key, i);
             });
@@ -567,8 +606,8 @@ __device__ __forceinline__ void fill_table(float2 *table) {
 template <int DT, int T>
 __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, const Settings &s) {
     const int tid = threadIdx.x;
-    float top = __int_as_float(0xff800000);
-    for_each<DT, T>(row, V, [&](float z, int) { top = specv::fmax_nan(top, z); });
+    const bool grouped = V <= kAnyGroups * 32 * Elem<DT>::kPerVec;
+    float top = largest<DT, T>(sm, row, V, grouped);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = specv::fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
     __syncthreads();
@@ -593,9 +632,10 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
         uint64_t Z = 0;
         auto fill = [&](bool mass) {
             clear_bins<T>(sm);
-            for_each<DT, T>(row, V, [&](float z, int) {
-                add_to_bin(sm, first_bin(z, zmax, scale), mass, mass ? fixed_weight(w, z) : 0);
-            });
+            if (mass)
+                for_each<DT, T, 1>(sm, row, V, 0, [&](float z, int) { add_to_bin(sm, first_bin(z, zmax, scale), true, fixed_weight(w, z)); });
+            else
+                for_each<DT, T, kFlight<DT>>(sm, row, V, 0, [&](float z, int) { atomicAdd(&sm.count[first_bin(z, zmax, scale)], 1u); });
             __syncthreads();
         };
         bool done = false;
@@ -610,7 +650,7 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
             if (done) {
                 if (tid == 0) sm.n_list = 0;
                 __syncthreads();
-                for_each<DT, T>(row, V, [&](float z, int i) {
+                for_each<DT, T, kFlight<DT>>(sm, row, V, bin_low(bin, zmax, scale, grouped), [&](float z, int i) {
                     if (first_bin(z, zmax, scale) <= bin) sm.list[atomicAdd(&sm.n_list, 1u)] = place_of(key_of(z), i);
                 });
                 __syncthreads();
@@ -632,7 +672,7 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
         if (s.k > 0 && !done) {
             find_bin<T>(sm, goal, 0, 0);
             const bool splits = sm.bin_count > kList;  // find_place then uses the bins itself
-            find_place<DT, T>(sm, row, V, w, scale, goal, mass);
+            find_place<DT, T>(sm, row, V, w, scale, goal, mass, grouped);
             cut = sm.cut;
             Z = sm.mass;
             __syncthreads();
@@ -649,7 +689,7 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
             __syncthreads();
             goal.target = sm.target;
             find_bin<T>(sm, goal, 0, 0);
-            find_place<DT, T>(sm, row, V, w, scale, goal, true);
+            find_place<DT, T>(sm, row, V, w, scale, goal, true, grouped);
             cut = max(cut, sm.cut);
         }
     }
@@ -660,23 +700,42 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
 
 // The row with -inf below the cut.
 template <int DT, int T>
-__device__ __forceinline__ void write_cut(const char *row, uint4 *dst, int V, uint64_t cut) {
-    constexpr int kPer = Elem<DT>::kPerVec;
+__device__ __forceinline__ void write_cut(const Shared &sm, const char *row, uint4 *dst, int V, uint64_t cut) {
+    constexpr int kPer = Elem<DT>::kPerVec, FLIGHT = kFlight<DT>;
     const uint32_t ckey = static_cast<uint32_t>(cut >> 32), cidx = ~static_cast<uint32_t>(cut);
-    for (int v = threadIdx.x; v < V / kPer; v += T) {
-        uint4 q = reinterpret_cast<const uint4 *>(row)[v];
-        float x[kPer];
-        Elem<DT>::unpack(q, x);
-        uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t low = V <= kAnyGroups * 32 * kPer ? ckey : 0;  // (0: all groups)
+    constexpr uint32_t kNone = Elem<DT>::kNegInfWord;
+    const int vecs = V / kPer;
+    for (int v0 = threadIdx.x; v0 < vecs; v0 += T * FLIGHT) {
+        uint4 q[FLIGHT];
+        bool in[FLIGHT];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const uint32_t key = key_of(x[i]);
-            const bool keep = cut == 0 || key > ckey || (key == ckey && static_cast<uint32_t>(v * kPer + i) <= cidx);
-            if (keep) continue;
-            if (DT == SPEC_F32) w[i % 4] = 0xff800000u;
-            else w[i / 2 % 4] = i & 1 ? (w[i / 2 % 4] & 0xffffu) | 0xff800000u : (w[i / 2 % 4] & 0xffff0000u) | 0xff80u;
+        for (int u = 0; u < FLIGHT; ++u) {
+            const int v = v0 + u * T;
+            q[u] = make_uint4(kNone, kNone, kNone, kNone);
+            in[u] = v < vecs && (low == 0 || sm.group_max[v >> 5] >= low);
+            if (in[u]) q[u] = reinterpret_cast<const uint4 *>(row)[v];
         }
-        dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            const int v = v0 + u * T;
+            if (v >= vecs) break;
+            if (in[u]) {
+                float x[kPer];
+                Elem<DT>::unpack(q[u], x);
+                uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const uint32_t key = key_of(x[i]);
+                    const bool keep = cut == 0 || key > ckey || (key == ckey && static_cast<uint32_t>(v * kPer + i) <= cidx);
+                    if (keep) continue;
+                    if (DT == SPEC_F32) w[i % 4] = 0xff800000u;
+                    else w[i / 2 % 4] = i & 1 ? (w[i / 2 % 4] & 0xffffu) | 0xff800000u : (w[i / 2 % 4] & 0xffff0000u) | 0xff80u;
+                }
+                q[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            dst[v] = q[u];
+        }
     }
 }
 
@@ -728,7 +787,7 @@ __global__ void __launch_bounds__(T, 1024 / T)
         row = hold;
     }
     const uint64_t cut = s.active ? cut_of_row<DT, T>(sm, row, V, s) : 0;
-    if (cut != 0 || logits != out) write_cut<DT, T>(row, dst, V, cut);
+    if (cut != 0 || logits != out) write_cut<DT, T>(sm, row, dst, V, cut);
 }
 
 // ------------------------------------------------------------ bf16, in two passes
@@ -1244,7 +1303,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         if (tid < 64) all.any.table[tid] = all.table[tid];
         __syncthreads();
         const uint64_t cut = cut_of_row<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), V, s);
-        if (cut != 0 || logits != out) write_cut<SPEC_BF16, kThreads>(reinterpret_cast<const char *>(row), dst, V, cut);
+        if (cut != 0 || logits != out) write_cut<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), dst, V, cut);
         return;
     }
     // --- the border value: the lowest one kept, and how its ties go
@@ -1403,9 +1462,16 @@ cudaError_t launch_bf16(const char *in, char *to, const Rows &rw, const Truncate
     return cudaLaunchKernelEx(&cfg, truncate_bf16_kernel<CL>, in, to, rw, tr, V);
 }
 
-constexpr int kMostHeld = 190 * 1024;  // bytes of a row kept in shared memory
+constexpr int kMostHeld = 180 * 1024;  // bytes of a row kept in shared memory
 constexpr int kAnyShared = (sizeof(Shared) + 15) / 16 * 16;
-constexpr int any_threads(int dt) { return dt == SPEC_F32 ? 1024 : kThreads; }
+
+template <int DT, int T>
+int launch_any(const char *in, char *to, const Rows &rw, const Truncate &tr, int V, cudaStream_t stream) {
+    const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
+    const bool held = DT == SPEC_F32 && bytes <= kMostHeld;
+    truncate_kernel<DT, T><<<rw.R, T, kAnyShared + (held ? bytes : 0), stream>>>(in, to, rw, tr, V, held);
+    return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
+}
 
 template <int DT>
 int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms,
@@ -1418,14 +1484,11 @@ int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncat
         while (cl < 8 && static_cast<int64_t>(rw.R) * cl * 2 <= static_cast<int64_t>(sms) * kPerSm && V >= cl * 2 * kWarps * kGroupCols) cl *= 2;
         const auto launch = cl == 8 ? launch_bf16<8> : cl == 4 ? launch_bf16<4> : cl == 2 ? launch_bf16<2> : launch_bf16<1>;
         return specv::cuda_ok(launch(in, to, rw, tr, V, sms, stream), "launch truncate_bf16_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
-    } else {
-        constexpr int T = any_threads(DT);
-        const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
-        const bool held = DT == SPEC_F32 && bytes <= kMostHeld;
-        truncate_kernel<DT, T><<<rw.R, T, kAnyShared + (held ? bytes : 0), stream>>>(in, to, rw, tr,
-                                                                                                          V, held);
     }
-    return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
+    // short rows: small CTAs, several to an SM
+    return V <= 8192 ? launch_any<DT, 256>(in, to, rw, tr, V, stream)
+           : V <= 16384 ? launch_any<DT, 512>(in, to, rw, tr, V, stream)
+                        : launch_any<DT, 1024>(in, to, rw, tr, V, stream);
 }
 
 inline int check_truncate_args(const spec_truncate_t *t, const Rows &rw, Truncate *tr) {
@@ -1443,11 +1506,15 @@ bool set_logits_attrs() {
         return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(speclog::BothShared)),
                        "cudaFuncSetAttribute(truncate_bf16_kernel)");
     };
+    const auto any = [](auto kernel) {
+        return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            speclog::kAnyShared + speclog::kMostHeld),
+                       "cudaFuncSetAttribute(truncate_kernel)");
+    };
     return bf16(speclog::truncate_bf16_kernel<1>) && bf16(speclog::truncate_bf16_kernel<2>) &&
            bf16(speclog::truncate_bf16_kernel<4>) && bf16(speclog::truncate_bf16_kernel<8>) &&
-           cuda_ok(cudaFuncSetAttribute(speclog::truncate_kernel<SPEC_F32, speclog::any_threads(SPEC_F32)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        speclog::kAnyShared + speclog::kMostHeld),
-                   "cudaFuncSetAttribute(truncate_kernel)");
+           any(speclog::truncate_kernel<SPEC_F32, 256>) && any(speclog::truncate_kernel<SPEC_F32, 512>) &&
+           any(speclog::truncate_kernel<SPEC_F32, 1024>);
 }
 }  // namespace specv
 
