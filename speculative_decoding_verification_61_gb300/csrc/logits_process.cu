@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
 
     // (32 bits hold the number of a group: it is at most 64 times the rows' units)
     const uint32_t self = blockIdx.x * G::kCount + G::self();
+    specv::grid_launch_dependents();  // a truncation behind this may get ready while it drains
     if (!check_rows(rw, pen)) {
         // the call fails: every row is NaN
         for (int64_t u = self; u < static_cast<int64_t>(rw.R) * units; u += static_cast<int64_t>(gridDim.x) * G::kCount)

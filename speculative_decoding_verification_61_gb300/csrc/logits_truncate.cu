@@ -760,7 +760,9 @@ __global__ void __launch_bounds__(T, 1024 / T)
     const int vecs = V / Elem<DT>::kPerVec;
     fill_table(sm.table);
     const int64_t r = blockIdx.x;
-    if (!check_rows(rw, r, &sm.seq)) {
+    const bool rows_ok = check_rows(rw, r, &sm.seq);
+    specv::grid_dependency_wait();  // behind the processing: its rows are there from here on
+    if (!rows_ok) {
         fill_nan<DT>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs, r * T + tid,
                      static_cast<int64_t>(gridDim.x) * T);
         return;
@@ -1144,7 +1146,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     fill_table(all.table);
     const int64_t r = blockIdx.x / CL;
     if (tid == 0) all.odd = 0;
-    if (!check_rows(rw, r, &all.seq)) {
+    const bool rows_ok = check_rows(rw, r, &all.seq);
+    specv::grid_dependency_wait();  // behind the processing: its rows are there from here on
+    if (!rows_ok) {
         fill_nan<SPEC_BF16>(reinterpret_cast<uint4 *>(out), static_cast<int64_t>(rw.R) * vecs,
                             static_cast<int64_t>(blockIdx.x) * kThreads + tid, static_cast<int64_t>(gridDim.x) * kThreads);
         return;
@@ -1459,49 +1463,65 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     if (CL > 1) cluster_sync();  // CTA 0's shared memory is read until here
 }
 
-template <int CL>
-cudaError_t launch_bf16(const char *in, char *to, const Rows &rw, const Truncate &tr, int V, int sms, cudaStream_t stream) {
+// `behind`: launched to start while the processing before it on the stream drains
+// (it reads the call's inputs, which were there before that, and then waits).
+template <typename K, typename... Args>
+cudaError_t launch_rows(K kernel, int grid, int threads, size_t smem, int cluster, bool behind, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(rw.R * CL);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(BothShared);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CL;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (behind) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = CL > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, truncate_bf16_kernel<CL>, in, to, rw, tr, V);
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 constexpr int kMostHeld = 180 * 1024;  // bytes of a row kept in shared memory
 constexpr int kAnyShared = (sizeof(Shared) + 15) / 16 * 16;
 
 template <int DT, int T>
-int launch_any(const char *in, char *to, const Rows &rw, const Truncate &tr, int V, cudaStream_t stream) {
+cudaError_t launch_any(const char *in, char *to, const Rows &rw, const Truncate &tr, int V, bool behind, cudaStream_t stream) {
     const int64_t bytes = static_cast<int64_t>(V) * Elem<DT>::kBytes;
     const bool held = DT == SPEC_F32 && bytes <= kMostHeld;
-    truncate_kernel<DT, T><<<rw.R, T, kAnyShared + (held ? bytes : 0), stream>>>(in, to, rw, tr, V, held);
-    return specv::cuda_ok(cudaGetLastError(), "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_rows(truncate_kernel<DT, T>, rw.R, T, kAnyShared + (held ? bytes : 0), 1, behind, stream, in, to, rw, tr, V, held);
 }
 
 template <int DT>
-int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms,
+int launch_truncate(const void *logits, void *out, const Rows &rw, const Truncate &tr, int V, int sms, bool behind,
                     cudaStream_t stream) {
     const char *in = static_cast<const char *>(logits);
     char *to = static_cast<char *>(out);
+    cudaError_t e;
     if (DT == SPEC_BF16 && V <= kMaxFastV) {
         // few rows: clusters of CTAs share them, while every warp has groups of its own
         int cl = 1;
         while (cl < 8 && static_cast<int64_t>(rw.R) * cl * 2 <= static_cast<int64_t>(sms) * kPerSm && V >= cl * 2 * kWarps * kGroupCols) cl *= 2;
-        const auto launch = cl == 8 ? launch_bf16<8> : cl == 4 ? launch_bf16<4> : cl == 2 ? launch_bf16<2> : launch_bf16<1>;
-        return specv::cuda_ok(launch(in, to, rw, tr, V, sms, stream), "launch truncate_bf16_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
+        const auto kernel = cl == 8   ? truncate_bf16_kernel<8>
+                            : cl == 4 ? truncate_bf16_kernel<4>
+                            : cl == 2 ? truncate_bf16_kernel<2>
+                                      : truncate_bf16_kernel<1>;
+        e = launch_rows(kernel, rw.R * cl, kThreads, sizeof(BothShared), cl, behind, stream, in, to, rw, tr, V);
+    } else {
+        // short rows: small CTAs, several to an SM
+        e = V <= 8192    ? launch_any<DT, 256>(in, to, rw, tr, V, behind, stream)
+            : V <= 16384 ? launch_any<DT, 512>(in, to, rw, tr, V, behind, stream)
+                         : launch_any<DT, 1024>(in, to, rw, tr, V, behind, stream);
     }
-    // short rows: small CTAs, several to an SM
-    return V <= 8192 ? launch_any<DT, 256>(in, to, rw, tr, V, stream)
-           : V <= 16384 ? launch_any<DT, 512>(in, to, rw, tr, V, stream)
-                        : launch_any<DT, 1024>(in, to, rw, tr, V, stream);
+    return specv::cuda_ok(e, "launch truncate_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 inline int check_truncate_args(const spec_truncate_t *t, const Rows &rw, Truncate *tr) {
@@ -1533,10 +1553,9 @@ bool set_logits_attrs() {
 
 using namespace speclog;
 
-extern "C" {
-
-int spec_logits_truncate(const void *logits, const spec_rows_t *rows, const spec_truncate_t *truncate, int V,
-                         int dtype, void *out, void *stream) {
+namespace {
+int truncate_call(const void *logits, const spec_rows_t *rows, const spec_truncate_t *truncate, int V, int dtype, void *out,
+                  bool behind, void *stream) {
     Rows rw;
     Truncate tr;
     int rc = check_rows_args(logits, rows, V, dtype, out, &rw);
@@ -1546,8 +1565,16 @@ int spec_logits_truncate(const void *logits, const spec_rows_t *rows, const spec
     specv::DeviceState *st = specv::device_state(&dev);
     if (!st) return SPEC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == SPEC_F32 ? launch_truncate<SPEC_F32>(logits, out, rw, tr, V, st->sms, s)
-                             : launch_truncate<SPEC_BF16>(logits, out, rw, tr, V, st->sms, s);
+    return dtype == SPEC_F32 ? launch_truncate<SPEC_F32>(logits, out, rw, tr, V, st->sms, behind, s)
+                             : launch_truncate<SPEC_BF16>(logits, out, rw, tr, V, st->sms, behind, s);
+}
+}  // namespace
+
+extern "C" {
+
+int spec_logits_truncate(const void *logits, const spec_rows_t *rows, const spec_truncate_t *truncate, int V,
+                         int dtype, void *out, void *stream) {
+    return truncate_call(logits, rows, truncate, V, dtype, out, false, stream);
 }
 
 int spec_logits_process_truncate(const void *logits, const spec_rows_t *rows, const spec_logits_t *process,
@@ -1558,7 +1585,7 @@ int spec_logits_process_truncate(const void *logits, const spec_rows_t *rows, co
     if (rc == SPEC_OK) rc = check_truncate_args(truncate, rw, &tr);
     if (rc == SPEC_OK) rc = spec_logits_process(logits, rows, process, V, dtype, out, stream);
     if (rc != SPEC_OK) return rc;
-    return spec_logits_truncate(out, rows, truncate, V, dtype, out, stream);
+    return truncate_call(out, rows, truncate, V, dtype, out, true, stream);
 }
 
 }  // extern "C"
