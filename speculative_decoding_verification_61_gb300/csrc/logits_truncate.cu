@@ -314,9 +314,10 @@ __device__ __forceinline__ void for_each(const Shared &sm, const char *row, int 
         }
     }
 }
-// The largest value (NaN if there is one) and the groups' largest keys.
+// The largest value (NaN if there is one) and the groups' largest keys; the row
+// into `hold` on the way, if given.
 template <int DT, int T>
-__device__ __forceinline__ float largest(Shared &sm, const char *row, int V, bool grouped) {
+__device__ __forceinline__ float largest(Shared &sm, const char *row, int V, bool grouped, uint4 *hold) {
     constexpr int kPer = Elem<DT>::kPerVec, FLIGHT = kFlight<DT>;
     const uint4 *p = reinterpret_cast<const uint4 *>(row);
     const int vecs = V / kPer, lane = threadIdx.x & 31;
@@ -331,6 +332,7 @@ __device__ __forceinline__ float largest(Shared &sm, const char *row, int V, boo
             const int v = v0 + u * T;
             if (v - lane >= vecs) break;
             const float m = v < vecs ? Elem<DT>::vmax_nan(q[u]) : __int_as_float(0xff800000);
+            if (DT == SPEC_F32 && hold && v < vecs) hold[v] = q[u];
             top = specv::fmax_nan(top, m);
             const uint32_t key = __reduce_max_sync(0xffffffffu, key_of(m));
             if (grouped && lane == 0) sm.group_max[v >> 5] = key;
@@ -601,15 +603,16 @@ __device__ __forceinline__ void fill_table(float2 *table) {
 
 // The cut of one row in memory, for rows of any kind: every token whose place is
 // below it goes; 0: the row stays as it is.  Passes over the row: its largest
-// value, a histogram over 32 bins per halving of the weight, the border bin's
-// elements, sorted.  fp32 logits have no few values, so top-p computes a weight
+// value (and its copy in `hold`, if given, which the others then read), a histogram
+// over 32 bins per halving of the weight, the border bin's elements, sorted.  fp32 logits have no few values, so top-p computes a weight
 // per token (about 45 instructions): 384 rows of 128256 take 152 us with top-k
 // (2.6 TB/s), 378 with top-p alone (1.0 TB/s), where instructions bound it.
 template <int DT, int T>
-__device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, const Settings &s) {
+__device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, const Settings &s, char *hold) {
     const int tid = threadIdx.x;
     const bool grouped = V <= kAnyGroups * 32 * Elem<DT>::kPerVec;
-    float top = largest<DT, T>(sm, row, V, grouped);
+    float top = largest<DT, T>(sm, row, V, grouped, reinterpret_cast<uint4 *>(hold));
+    if (hold) row = hold;  // (the block meets below before it is read)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = specv::fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
     __syncthreads();
@@ -776,21 +779,8 @@ __global__ void __launch_bounds__(T, 1024 / T)
         fill_nan<DT>(dst, vecs, tid, T);
         return;
     }
-    if (s.active && held) {
-        constexpr int kFlight = 4;
-        for (int v0 = tid; v0 < vecs; v0 += T * kFlight) {
-            uint4 q[kFlight];
-#pragma unroll
-            for (int u = 0; u < kFlight; ++u)
-                if (v0 + u * T < vecs) q[u] = reinterpret_cast<const uint4 *>(row)[v0 + u * T];
-#pragma unroll
-            for (int u = 0; u < kFlight; ++u)
-                if (v0 + u * T < vecs) reinterpret_cast<uint4 *>(hold)[v0 + u * T] = q[u];
-        }
-        __syncthreads();
-        row = hold;
-    }
-    const uint64_t cut = s.active ? cut_of_row<DT, T>(sm, row, V, s) : 0;
+    const uint64_t cut = s.active ? cut_of_row<DT, T>(sm, row, V, s, held ? hold : nullptr) : 0;
+    if (s.active && held) row = hold;
     if (cut != 0 || logits != out) write_cut<DT, T>(sm, row, dst, V, cut);
 }
 
@@ -1319,7 +1309,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         __syncthreads();
         if (tid < 64) all.any.table[tid] = all.table[tid];
         __syncthreads();
-        const uint64_t cut = cut_of_row<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), V, s);
+        const uint64_t cut = cut_of_row<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), V, s, nullptr);
         if (cut != 0 || logits != out) write_cut<SPEC_BF16, kThreads>(all.any, reinterpret_cast<const char *>(row), dst, V, cut);
         return;
     }
