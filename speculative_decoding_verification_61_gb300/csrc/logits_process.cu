@@ -249,205 +249,203 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
     const int part = static_cast<int>(self - pair * parts), b = static_cast<int>(pair / units);
     const Units un{static_cast<int>(pair - static_cast<uint32_t>(b) * units), units, piece};
     if (b >= rw.B) return;
-    {
-        const int o0 = __ldg(rw.offsets + b), o1 = __ldg(rw.offsets + b + 1);
-        const int k = o1 - o0;  // drafted tokens, or tree nodes
-        const int row0 = rw.first_row(b, o0), n = rw.first_row(b + 1, o1) - row0;
-        const int i0 = n * part / parts, i1 = n * (part + 1) / parts;
-        if (i0 == i1) return;
+    const int o0 = __ldg(rw.offsets + b), o1 = __ldg(rw.offsets + b + 1);
+    const int k = o1 - o0;  // drafted tokens, or tree nodes
+    const int row0 = rw.first_row(b, o0), n = rw.first_row(b + 1, o1) - row0;
+    const int i0 = n * part / parts, i1 = n * (part + 1) / parts;
+    if (i0 == i1) return;
 
-        // --- what the sequence and the columns say: asked for before the stream, used after it
-        Penalty p{1.0f, 0.0f, 0.0f};
-        int64_t slot = b;
-        uint32_t prompt[G::kWordsEach], emitted[G::kWordsEach];
-        constexpr int kTokens = (kMaxPath + G::kSize - 1) / G::kSize;
-        int token[kTokens], up[kTokens];
-        bool bad = false;
-        if (pen && ps.slots) slot = __ldg(ps.slots + b);
-        const bool there = pen && slot >= 0 && slot < ps.S;
+    // --- what the sequence and the columns say: asked for before the stream, used after it
+    Penalty p{1.0f, 0.0f, 0.0f};
+    int64_t slot = b;
+    uint32_t prompt[G::kWordsEach], emitted[G::kWordsEach];
+    constexpr int kTokens = (kMaxPath + G::kSize - 1) / G::kSize;
+    int token[kTokens], up[kTokens];
+    bool bad = false;
+    if (pen && ps.slots) slot = __ldg(ps.slots + b);
+    const bool there = pen && slot >= 0 && slot < ps.S;
+#pragma unroll
+    for (int i = 0; i < G::kWordsEach; ++i) {
+        const int word = G::word(un, i * G::kSize + me);
+        prompt[i] = emitted[i] = 0;
+        if (there && word < W) {
+            prompt[i] = static_cast<uint32_t>(__ldg(ps.seen + slot * 2 * W + word));
+            emitted[i] = static_cast<uint32_t>(__ldg(ps.seen + (slot * 2 + 1) * W + word));
+        }
+    }
+    if (pen) {
+        bad |= !there || !load_penalty(ps, b, &p);
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t) {
+            token[t] = up[t] = 0;
+            if (me + G::kSize * t < k) {
+                token[t] = __ldg(rw.tokens + o0 + me + G::kSize * t);
+                if (tree) up[t] = __ldg(rw.parent + o0 + me + G::kSize * t);
+            }
+        }
+    }
+    int e0 = 0, e1 = 0;
+    if (ps.bias_offsets) {
+        e0 = __ldg(ps.bias_offsets + b), e1 = __ldg(ps.bias_offsets + b + 1);
+        if (e0 < 0 || e1 < e0 || e1 > ps.n_bias) {
+            bad = true;
+            e1 = e0 = 0;
+        }
+    }
+    if (ps.mask) {
+        for (int i = i0 + me; i < i1; i += G::kSize) sm.mask[i] = mask_of(ps, row0 + i);
+        G::sync();
+    }
+    if (STREAM) stream_rows<DT>(logits, out, ps, sm.mask, V, row0, i0, i1, un, inplace);
+
+    // --- the unit's columns that anything applies to
+#pragma unroll
+    for (int i = 0; i < G::kWordsEach; ++i) sm.drafted[i * G::kSize + me] = sm.biased[i * G::kSize + me] = 0;
+    G::sync();
+    if (pen) {
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t) {
+            const int j = me + G::kSize * t;
+            if (j >= k) continue;
+            const bool root = tree && j == 0;
+            sm.token[j] = token[t];
+            if (!root) {
+                const bool in = token[t] >= 0 && token[t] < V;
+                bad |= !in;
+                const int d = in ? G::place(un, token[t] >> 5) : -1;
+                if (d >= 0) atomicOr(&sm.drafted[d], 1u << (token[t] & 31));
+            }
+            if (tree) {
+                bad |= root ? up[t] != -1 : (up[t] < o0 || up[t] >= o0 + j);
+                sm.up[j] = up[t] - o0;
+            }
+        }
+    }
+    for (int e = e0 + me; e < e1; e += G::kSize) {
+        const int t = __ldg(ps.bias_tokens + e);
+        const bool in = t >= 0 && t < V;
+        const float v = __ldg(ps.bias_values + e);
+        bad |= !in || !(v < __int_as_float(0x7f800000));  // NaN and +inf
+        if (e - e0 < kBias) {
+            sm.bias_token[e - e0] = t;
+            sm.bias_value[e - e0] = v;
+        }
+        const int d = in ? G::place(un, t >> 5) : -1;
+        if (d >= 0) atomicOr(&sm.biased[d], 1u << (t & 31));
+    }
+    bad = G::any(bad);
+    G::sync();  // the shared arrays are whole, the stream's stores done
+    if (bad) {
+        nan_rows<DT, STREAM>(out, V, row0, i0, i1, un);
+    } else {
+        uint32_t touched[G::kWordsEach], drafted[G::kWordsEach], biased[G::kWordsEach];
+        int rank = 0;
 #pragma unroll
         for (int i = 0; i < G::kWordsEach; ++i) {
             const int word = G::word(un, i * G::kSize + me);
-            prompt[i] = emitted[i] = 0;
-            if (there && word < W) {
-                prompt[i] = static_cast<uint32_t>(__ldg(ps.seen + slot * 2 * W + word));
-                emitted[i] = static_cast<uint32_t>(__ldg(ps.seen + (slot * 2 + 1) * W + word));
-            }
+            // bits behind the vocabulary say nothing
+            const uint32_t in_v = word >= W ? 0u : word == W - 1 && (V & 31) ? (1u << (V & 31)) - 1 : 0xffffffffu;
+            drafted[i] = sm.drafted[i * G::kSize + me];
+            biased[i] = sm.biased[i * G::kSize + me];
+            touched[i] = (prompt[i] | emitted[i] | drafted[i] | biased[i]) & in_v;
+            rank += __popc(touched[i]);
         }
-        if (pen) {
-            bad |= !there || !load_penalty(ps, b, &p);
+        const int own = rank;
 #pragma unroll
-            for (int t = 0; t < kTokens; ++t) {
-                token[t] = up[t] = 0;
-                if (me + G::kSize * t < k) {
-                    token[t] = __ldg(rw.tokens + o0 + me + G::kSize * t);
-                    if (tree) up[t] = __ldg(rw.parent + o0 + me + G::kSize * t);
-                }
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, rank, off);
+            if (lane >= off) rank += x;
+        }
+        int listed = __shfl_sync(0xffffffffu, rank, 31);
+        rank -= own;
+        if (STREAM) {
+            if (lane == 0) sm.warp_sum[threadIdx.x >> 5] = listed;
+            __syncthreads();
+            listed = 0;
+            for (int i = 0; i < kWarps; ++i) {
+                if (i == static_cast<int>(threadIdx.x >> 5)) rank += listed;
+                listed += sm.warp_sum[i];
             }
         }
-        int e0 = 0, e1 = 0;
-        if (ps.bias_offsets) {
-            e0 = __ldg(ps.bias_offsets + b), e1 = __ldg(ps.bias_offsets + b + 1);
-            if (e0 < 0 || e1 < e0 || e1 > ps.n_bias) {
-                bad = true;
-                e1 = e0 = 0;
+        if (listed && tree && pen) {
+            for (int j = me; j < n; j += G::kSize) {
+                uint64_t m = 0;
+                for (int g = j; g > 0; g = sm.up[g]) m |= 1ull << g;  // parents are earlier nodes
+                sm.before[j] = m;
             }
         }
-        if (ps.mask) {
-            for (int i = i0 + me; i < i1; i += G::kSize) sm.mask[i] = mask_of(ps, row0 + i);
+        for (int base = 0; base < listed; base += kList) {
+            const int len = min(kList, listed - base);
             G::sync();
-        }
-        if (STREAM) stream_rows<DT>(logits, out, ps, sm.mask, V, row0, i0, i1, un, inplace);
-
-        // --- the unit's columns that anything applies to
-#pragma unroll
-        for (int i = 0; i < G::kWordsEach; ++i) sm.drafted[i * G::kSize + me] = sm.biased[i * G::kSize + me] = 0;
-        G::sync();
-        if (pen) {
-#pragma unroll
-            for (int t = 0; t < kTokens; ++t) {
-                const int j = me + G::kSize * t;
-                if (j >= k) continue;
-                const bool root = tree && j == 0;
-                sm.token[j] = token[t];
-                if (!root) {
-                    const bool in = token[t] >= 0 && token[t] < V;
-                    bad |= !in;
-                    const int d = in ? G::place(un, token[t] >> 5) : -1;
-                    if (d >= 0) atomicOr(&sm.drafted[d], 1u << (token[t] & 31));
-                }
-                if (tree) {
-                    bad |= root ? up[t] != -1 : (up[t] < o0 || up[t] >= o0 + j);
-                    sm.up[j] = up[t] - o0;
-                }
-            }
-        }
-        for (int e = e0 + me; e < e1; e += G::kSize) {
-            const int t = __ldg(ps.bias_tokens + e);
-            const bool in = t >= 0 && t < V;
-            const float v = __ldg(ps.bias_values + e);
-            bad |= !in || !(v < __int_as_float(0x7f800000));  // NaN and +inf
-            if (e - e0 < kBias) {
-                sm.bias_token[e - e0] = t;
-                sm.bias_value[e - e0] = v;
-            }
-            const int d = in ? G::place(un, t >> 5) : -1;
-            if (d >= 0) atomicOr(&sm.biased[d], 1u << (t & 31));
-        }
-        bad = G::any(bad);
-        G::sync();  // the shared arrays are whole, the stream's stores done
-        if (bad) {
-            nan_rows<DT, STREAM>(out, V, row0, i0, i1, un);
-        } else {
-            uint32_t touched[G::kWordsEach], drafted[G::kWordsEach], biased[G::kWordsEach];
-            int rank = 0;
+            int at = rank - base;  // the place of the thread's next column in the list
+            auto put = [&](int to, int col, int bit, uint32_t p, uint32_t e, uint32_t d, uint32_t x) {
+                if (to < 0 || to >= kList) return;
+                sm.column[to] = col + bit;
+                sm.flags[to] = static_cast<uint8_t>((p >> bit & 1) * kPrompt | (e >> bit & 1) * kEmitted | (d >> bit & 1) * kDrafted |
+                                                    (x >> bit & 1) * kBiased);
+            };
 #pragma unroll
             for (int i = 0; i < G::kWordsEach; ++i) {
-                const int word = G::word(un, i * G::kSize + me);
-                // bits behind the vocabulary say nothing
-                const uint32_t in_v = word >= W ? 0u : word == W - 1 && (V & 31) ? (1u << (V & 31)) - 1 : 0xffffffffu;
-                drafted[i] = sm.drafted[i * G::kSize + me];
-                biased[i] = sm.biased[i * G::kSize + me];
-                touched[i] = (prompt[i] | emitted[i] | drafted[i] | biased[i]) & in_v;
-                rank += __popc(touched[i]);
-            }
-            const int own = rank;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, rank, off);
-                if (lane >= off) rank += x;
-            }
-            int listed = __shfl_sync(0xffffffffu, rank, 31);
-            rank -= own;
-            if (STREAM) {
-                if (lane == 0) sm.warp_sum[threadIdx.x >> 5] = listed;
-                __syncthreads();
-                listed = 0;
-                for (int i = 0; i < kWarps; ++i) {
-                    if (i == static_cast<int>(threadIdx.x >> 5)) rank += listed;
-                    listed += sm.warp_sum[i];
+                // words with few columns by their threads, full ones (frequent ids) by the warp
+                const int col = G::word(un, i * G::kSize + me) * 32, n_i = __popc(touched[i]);
+                const bool full = n_i > 4;
+                if (!full) {
+                    int to = at;
+                    for (uint32_t m = touched[i]; m; m &= m - 1) put(to++, col, __ffs(m) - 1, prompt[i], emitted[i], drafted[i], biased[i]);
                 }
-            }
-            if (listed && tree && pen) {
-                for (int j = me; j < n; j += G::kSize) {
-                    uint64_t m = 0;
-                    for (int g = j; g > 0; g = sm.up[g]) m |= 1ull << g;  // parents are earlier nodes
-                    sm.before[j] = m;
+                for (uint32_t m = __ballot_sync(0xffffffffu, full); m; m &= m - 1) {
+                    const int src = __ffs(m) - 1;
+                    const uint32_t word = __shfl_sync(0xffffffffu, touched[i], src);
+                    const int first = __shfl_sync(0xffffffffu, at, src), c = __shfl_sync(0xffffffffu, col, src);
+                    const uint32_t p = __shfl_sync(0xffffffffu, prompt[i], src), e = __shfl_sync(0xffffffffu, emitted[i], src);
+                    const uint32_t d = __shfl_sync(0xffffffffu, drafted[i], src), x = __shfl_sync(0xffffffffu, biased[i], src);
+                    if (word >> lane & 1) put(first + __popc(word & ((1u << lane) - 1)), c, lane, p, e, d, x);
                 }
+                at += n_i;
             }
-            for (int base = 0; base < listed; base += kList) {
-                const int len = min(kList, listed - base);
-                G::sync();
-                int at = rank - base;  // the place of the thread's next column in the list
-                auto put = [&](int to, int col, int bit, uint32_t p, uint32_t e, uint32_t d, uint32_t x) {
-                    if (to < 0 || to >= kList) return;
-                    sm.column[to] = col + bit;
-                    sm.flags[to] = static_cast<uint8_t>((p >> bit & 1) * kPrompt | (e >> bit & 1) * kEmitted | (d >> bit & 1) * kDrafted |
-                                                        (x >> bit & 1) * kBiased);
-                };
-#pragma unroll
-                for (int i = 0; i < G::kWordsEach; ++i) {
-                    // words with few columns by their threads, full ones (frequent ids) by the warp
-                    const int col = G::word(un, i * G::kSize + me) * 32, n_i = __popc(touched[i]);
-                    const bool full = n_i > 4;
-                    if (!full) {
-                        int to = at;
-                        for (uint32_t m = touched[i]; m; m &= m - 1) put(to++, col, __ffs(m) - 1, prompt[i], emitted[i], drafted[i], biased[i]);
+            G::sync();
+            // a thread takes a column, all its rows
+            for (int e = me; e < len; e += G::kSize) {
+                const int col = sm.column[e];
+                const uint32_t f = sm.flags[e];
+                const int count = f & kEmitted ? __ldg(ps.counts + slot * V + col) : 0;
+                float bias = 0.0f;
+                if (f & kBiased) {
+                    // the same token twice: the entries add, in list order
+                    bool any = false;
+                    for (int x = 0; x < e1 - e0; ++x) {
+                        if ((x < kBias ? sm.bias_token[x] : __ldg(ps.bias_tokens + e0 + x)) != col) continue;
+                        const float v = x < kBias ? sm.bias_value[x] : __ldg(ps.bias_values + e0 + x);
+                        bias = any ? __fadd_rn(bias, v) : v;
+                        any = true;
                     }
-                    for (uint32_t m = __ballot_sync(0xffffffffu, full); m; m &= m - 1) {
-                        const int src = __ffs(m) - 1;
-                        const uint32_t word = __shfl_sync(0xffffffffu, touched[i], src);
-                        const int first = __shfl_sync(0xffffffffu, at, src), c = __shfl_sync(0xffffffffu, col, src);
-                        const uint32_t p = __shfl_sync(0xffffffffu, prompt[i], src), e = __shfl_sync(0xffffffffu, emitted[i], src);
-                        const uint32_t d = __shfl_sync(0xffffffffu, drafted[i], src), x = __shfl_sync(0xffffffffu, biased[i], src);
-                        if (word >> lane & 1) put(first + __popc(word & ((1u << lane) - 1)), c, lane, p, e, d, x);
-                    }
-                    at += n_i;
                 }
-                G::sync();
-                // a thread takes a column, all its rows
-                for (int e = me; e < len; e += G::kSize) {
-                    const int col = sm.column[e];
-                    const uint32_t f = sm.flags[e];
-                    const int count = f & kEmitted ? __ldg(ps.counts + slot * V + col) : 0;
-                    float bias = 0.0f;
-                    if (f & kBiased) {
-                        // the same token twice: the entries add, in list order
-                        bool any = false;
-                        for (int x = 0; x < e1 - e0; ++x) {
-                            if ((x < kBias ? sm.bias_token[x] : __ldg(ps.bias_tokens + e0 + x)) != col) continue;
-                            const float v = x < kBias ? sm.bias_value[x] : __ldg(ps.bias_values + e0 + x);
-                            bias = any ? __fadd_rn(bias, v) : v;
-                            any = true;
+                constexpr int kRows = 4;  // in flight
+                for (int i = i0; i < i1; i += kRows) {
+                    float z[kRows];
+                    bool go[kRows];
+#pragma unroll
+                    for (int u = 0; u < kRows; ++u) {
+                        go[u] = i + u < i1;
+                        if (go[u] && ps.mask) {
+                            const int m = sm.mask[i + u];
+                            go[u] = m == -1 || (m >= 0 && ((bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7)) & 1));
                         }
                     }
-                    constexpr int kRows = 4;  // in flight
-                    for (int i = i0; i < i1; i += kRows) {
-                        float z[kRows];
-                        bool go[kRows];
 #pragma unroll
-                        for (int u = 0; u < kRows; ++u) {
-                            go[u] = i + u < i1;
-                            if (go[u] && ps.mask) {
-                                const int m = sm.mask[i + u];
-                                go[u] = m == -1 || (m >= 0 && ((bit_byte(ps.mask, static_cast<int64_t>(m) * W, col) >> (col & 7)) & 1));
-                            }
+                    for (int u = 0; u < kRows; ++u)
+                        z[u] = go[u] ? load_logit<DT>(logits + static_cast<int64_t>(row0 + i + u) * row_bytes, col) : 0.0f;
+#pragma unroll
+                    for (int u = 0; u < kRows; ++u) {
+                        if (!go[u]) continue;
+                        int c = count;
+                        if (f & kDrafted) {
+                            const uint64_t before = tree ? sm.before[i + u] : rw.mode == SPEC_ROWS_NEXT ? (1ull << k) - 1 : (1ull << (i + u)) - 1;
+                            for (uint64_t d = before; d; d &= d - 1) c += sm.token[__ffsll(d) - 1] == col;
                         }
-#pragma unroll
-                        for (int u = 0; u < kRows; ++u)
-                            z[u] = go[u] ? load_logit<DT>(logits + static_cast<int64_t>(row0 + i + u) * row_bytes, col) : 0.0f;
-#pragma unroll
-                        for (int u = 0; u < kRows; ++u) {
-                            if (!go[u]) continue;
-                            int c = count;
-                            if (f & kDrafted) {
-                                const uint64_t before = tree ? sm.before[i + u] : rw.mode == SPEC_ROWS_NEXT ? (1ull << k) - 1 : (1ull << (i + u)) - 1;
-                                for (uint64_t d = before; d; d &= d - 1) c += sm.token[__ffsll(d) - 1] == col;
-                            }
-                            if ((f & kPrompt) || c > 0) z[u] = penalised(z[u], c, p);
-                            if (f & kBiased) z[u] = __fadd_rn(z[u], bias);
-                            store_logit<DT>(out + static_cast<int64_t>(row0 + i + u) * row_bytes, col, z[u]);
-                        }
+                        if ((f & kPrompt) || c > 0) z[u] = penalised(z[u], c, p);
+                        if (f & kBiased) z[u] = __fadd_rn(z[u], bias);
+                        store_logit<DT>(out + static_cast<int64_t>(row0 + i + u) * row_bytes, col, z[u]);
                     }
                 }
             }
