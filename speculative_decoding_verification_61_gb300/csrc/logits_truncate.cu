@@ -294,13 +294,35 @@ __device__ __forceinline__ void for_each(const Shared &sm, const char *row, int 
     constexpr int kPer = Elem<DT>::kPerVec;
     const uint4 *p = reinterpret_cast<const uint4 *>(row);
     const int vecs = V / kPer;
+    const auto wanted = [&](int v) { return v < vecs && (low == 0 || sm.group_max[v >> 5] >= low); };
+    if (FLIGHT == 1) {  // much work per vector: the next one comes meanwhile
+        int v = threadIdx.x;
+        bool in = wanted(v);
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (in) q = p[v];
+#pragma unroll 1
+        for (; v < vecs; v += T) {
+            const bool in_next = wanted(v + T);
+            uint4 next = make_uint4(0, 0, 0, 0);
+            if (in_next) next = p[v + T];
+            if (in) {
+                float x[kPer];
+                Elem<DT>::unpack(q, x);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) f(x[i], v * kPer + i);
+            }
+            q = next;
+            in = in_next;
+        }
+        return;
+    }
     for (int v0 = threadIdx.x; v0 < vecs; v0 += T * FLIGHT) {
         uint4 q[FLIGHT];
         bool in[FLIGHT];
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
             const int v = v0 + u * T;
-            in[u] = v < vecs && (low == 0 || sm.group_max[v >> 5] >= low);
+            in[u] = wanted(v);
             if (in[u]) q[u] = p[v];
         }
 #pragma unroll
