@@ -381,7 +381,7 @@ __device__ __forceinline__ void add_to_bin(Shared &sm, int bin, bool mass, uint6
         const uint32_t lo = static_cast<uint32_t>(w);
         const uint32_t old = atomicAdd(&sm.lo[bin], lo);
         const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1u : 0u);
-        if (hi) atomicAdd(&sm.hi[bin], hi);  // (one 64-bit atomic instead: 378 -> 515 us)
+        if (hi) atomicAdd(&sm.hi[bin], hi);  // (one 64-bit atomic for both: 378 -> 515 us)
     }
 }
 
@@ -626,8 +626,10 @@ __device__ __forceinline__ void fill_table(float2 *table) {
 // below it goes; 0: the row stays as it is.  Passes over the row: its largest
 // value (and its copy in `hold`, if given, which the others then read), a histogram
 // over 32 bins per halving of the weight, the border bin's elements, sorted.  fp32 logits have no few values, so top-p computes a weight
-// per token (about 45 instructions): 384 rows of 128256 take 152 us with top-k
-// (2.6 TB/s), 378 with top-p alone (1.0 TB/s), where instructions bound it.
+// per token (about 45 instructions): 384 rows of 128256 take 151 us with top-k
+// (2.6 TB/s), 361 with top-p alone (1.1 TB/s), where those instructions bound it:
+// exact masses for the bins around the border alone, the rest summed in
+// registers, took 427.
 template <int DT, int T>
 __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, const Settings &s, char *hold) {
     const int tid = threadIdx.x;
