@@ -11,7 +11,7 @@
 //   min-p   the tokens with (z - zmax) / T >= ln(min_p).
 // A token on the wrong side of the top-p border is a wrong answer, however
 // small its mass, so masses are exact far below one token's mass: weights
-// come from a two-term fp32 exponential (relative error about 2^-46), and
+// come from a two-term fp32 exponential (relative error below 2^-42 down to e^-20), and
 // are summed as 64-bit integers, whose sum does not depend on its order.
 #include <algorithm>
 #include <cstdint>
@@ -93,7 +93,9 @@ __constant__ float2 kExp2Table[64] = {
 // the point.  2^x, x = (z - zmax) log2(e) / T, by the split x = n + j / 64 + r,
 // |r| <= 1/128: a table of 2^(j/64) in two fp32 terms, and the Taylor
 // polynomial of e^(r ln 2) whose leading terms are carried in two fp32 terms
-// as well (error-free sums and products).  Relative error below 2^-45.
+// as well (error-free sums and products).  Relative error below 2^-46 + x 2^-47,
+// x = (zmax - z) / T, of 1.5 million weights (2^-42.6 up to x = 20); the
+// second part is x's own, a product of two fp32 terms.
 struct Weights {
     float zmax, ch, cl;  // log2(e) / T in two terms
     int frac;
@@ -113,7 +115,7 @@ __device__ __forceinline__ float two_sum(float a, float b, float *e) {
     return s;
 }
 
-// The weight as mantissa * 2^exponent: mantissa in [2^48, 2^50), exponent <= -48;
+// The weight as mantissa * 2^exponent: mantissa in (0.99 2^48, 2^49), exponent <= -48;
 // mantissa 0 where the weight is below 2^-120.
 __device__ __forceinline__ uint64_t weight_mantissa(const Weights &w, float z, int *exponent) {
     float dl;
@@ -155,7 +157,8 @@ __device__ __forceinline__ uint64_t weight_mantissa(const Weights &w, float z, i
     const float uh = fast_two_sum(tj.x, ph, &ul);
     ul = __fadd_rn(ul, __fadd_rn(tj.y, pl));
     *exponent = (m >> 6) - 48;
-    return (static_cast<uint64_t>(__float2uint_rn(uh * 8388608.0f)) << 25) +
+    // (uh is a whole number of 2^-24: below 1 where j = 0 and t < 0, whose steps are half of those from 1 on)
+    return (static_cast<uint64_t>(__float2uint_rn(uh * 16777216.0f)) << 24) +
            static_cast<int64_t>(__float2int_rn(ul * 281474976710656.0f));
 }
 
