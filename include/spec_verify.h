@@ -574,9 +574,13 @@ int spec_logits_process(const void *logits, const spec_rows_t *rows, const spec_
  *   top_p  float [B]  in (0, 1]: of these, keep the tokens whose mass before them
  *                     is < p * Z, Z the mass of the first k; 1: all
  *   min_p  float [B]  in [0, 1]: of these, keep (z - zmax) / T_b >= ln(min_p); 0: all
- * Any of the three may be NULL.  At least one token is kept.  The sums decide
- * which token is the last one, so they are exact to about 2^-45 of the
- * largest weight.  Rows of greedy sequences (T_b = 0: their arg-max is kept
+ * Any of the three may be NULL.  At least one token is kept.  The masses decide
+ * which token is the last one, so they are exact far below a token's: a
+ * weight e^-x is off by less than 2^-46 + x 2^-47 of itself (T_b from 2^-100 to
+ * 2^100; the largest is exactly 1, below 2^-120 they are 0), a sum of weights adds
+ * less than 2^-45 of itself below 2^17 columns, 2^-37 at SPEC_MAX_V.  The kept
+ * set is the defined one unless the border lies as near as that to another
+ * token's, and the same on every run.  Rows of greedy sequences (T_b = 0: their arg-max is kept
  * anyway), and rows that hold NaN or +inf or only -inf, keep their bits.
  * Invalid sequences: T_b < 0, NaN or infinite, or a setting outside its range.
  */

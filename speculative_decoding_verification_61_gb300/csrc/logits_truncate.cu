@@ -12,7 +12,8 @@
 // A token on the wrong side of the top-p border is a wrong answer, however
 // small its mass, so masses are exact far below one token's mass: weights
 // come from a two-term fp32 exponential (relative error below 2^-42 down to e^-20), and
-// are summed as 64-bit integers, whose sum does not depend on its order.
+// are summed as integers of up to 125 bits, whose sum does not depend on its order and
+// keeps a small weight's bits beside a large one.
 #include <algorithm>
 #include <cstdint>
 
@@ -31,6 +32,8 @@ constexpr int kBins = 2048;
 constexpr int kList = 1024;        // elements of one bin that are sorted in shared memory
 constexpr int kAnyGroups = 2048;   // groups of 32 vectors whose largest values are kept
 constexpr int kBinsPerOctave = 32;  // first-level bins per halving of the weight
+
+using Mass = unsigned __int128;  // a fixed-point sum of weights
 
 struct Truncate {
     const float *temperature;
@@ -89,8 +92,7 @@ __constant__ float2 kExp2Table[64] = {
     {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f},
 };
 
-// exp((z - zmax) / T) as a 64-bit fixed-point number with `frac` bits behind
-// the point.  2^x, x = (z - zmax) log2(e) / T, by the split x = n + j / 64 + r,
+// exp((z - zmax) / T).  2^x, x = (z - zmax) log2(e) / T, by the split x = n + j / 64 + r,
 // |r| <= 1/128: a table of 2^(j/64) in two fp32 terms, and the Taylor
 // polynomial of e^(r ln 2) whose leading terms are carried in two fp32 terms
 // as well (error-free sums and products).  Relative error below 2^-46 + x 2^-47,
@@ -98,7 +100,7 @@ __constant__ float2 kExp2Table[64] = {
 // second part is x's own, a product of two fp32 terms.
 struct Weights {
     float zmax, ch, cl;  // log2(e) / T in two terms
-    int frac;
+    int frac;            // of cut_of_row's bins
     const float2 *table;  // shared memory: 2^(j/64), j = 0..63
 };
 
@@ -162,11 +164,30 @@ __device__ __forceinline__ uint64_t weight_mantissa(const Weights &w, float z, i
            static_cast<int64_t>(__float2int_rn(ul * 281474976710656.0f));
 }
 
-__device__ __forceinline__ uint64_t fixed_weight(const Weights &w, float z) {
+// A token's weight in the sums of cut_of_row, in units of 2^-(frac + octave).
+// `octave` is the one of its first-level bin, which it is at most a hair above,
+// so V of them fit 64 bits, and a tail of V tokens however small is summed to
+// a relative error of 2^-frac (2^-45 below 2^17 columns, 2^-37 at 2^24).  With the one
+// unit of the largest weights for all, a flat tail's tokens are all rounded the same way,
+// by up to V 2^-(frac + 1) of the largest weight together.
+__device__ __forceinline__ uint64_t bin_weight(const Weights &w, float z, int octave) {
     int e;
     const uint64_t m = weight_mantissa(w, z, &e);
-    const int shift = -(e + w.frac);  // at least 1: frac <= 47
+    const int shift = -(e + w.frac + octave);  // at least 1: frac <= 47
     return shift > 63 ? 0 : (m + (1ull << (shift - 1))) >> shift;
+}
+// The same in units of 2^-(frac + kMostOctave), in which sums over several octaves
+// are kept: no bit is lost, 125 of them are used at most.
+constexpr int kMostOctave = kBins / kBinsPerOctave - 1;
+__device__ __forceinline__ Mass wide_mass(uint64_t units, int octave) { return static_cast<Mass>(units) << (kMostOctave - octave); }
+
+__device__ __forceinline__ Mass shfl(Mass m, int src) {
+    const uint64_t hi = __shfl_sync(0xffffffffu, static_cast<uint64_t>(m >> 64), src);
+    return static_cast<Mass>(hi) << 64 | __shfl_sync(0xffffffffu, static_cast<uint64_t>(m), src);
+}
+__device__ __forceinline__ Mass shfl_up(Mass m, int off) {
+    const uint64_t hi = __shfl_up_sync(0xffffffffu, static_cast<uint64_t>(m >> 64), off);
+    return static_cast<Mass>(hi) << 64 | __shfl_up_sync(0xffffffffu, static_cast<uint64_t>(m), off);
 }
 
 // ------------------------------------------------------------ block helpers
@@ -183,105 +204,119 @@ struct Shared {
     uint32_t count[kBins], lo[kBins], hi[kBins];
     uint64_t list[kList];
     uint32_t group_max[kAnyGroups];  // of rows with at most so many groups
-    uint64_t warp_mass[32];
+    Mass warp_mass[32];
     uint32_t warp_count[32];
     uint32_t red[32];
     uint32_t n_list, key_lo, key_hi;
     // where the scan of the bins stopped
     int bin;
     uint32_t above_count, bin_count;
-    uint64_t above_mass, total_mass, mass;
+    Mass above_mass, total_mass;
+    // what lies above the first bin or the list
+    uint32_t base_count;
+    Mass base_mass;
+    Mass target;  // of a search by mass
     uint64_t cut;
-    uint64_t target;
+    Mass mass;    // up to the cut
     RowConstants row;
 };
 
-// Exclusive prefix sums over the block of a count and a mass per thread.
-__device__ __forceinline__ void block_scan(Shared &sm, uint32_t &c, uint64_t &m) {
+// What a search looks for: the first place in the order where the tokens up to and
+// with it number `need`, without or with their mass, or weigh sm.target.
+enum Search { kCount, kCountMass, kMass };
+
+template <Search S>
+__device__ __forceinline__ bool reached(uint32_t need, Mass target, uint32_t c, Mass m) {
+    return S == kMass ? m >= target : c >= need;
+}
+
+// Sums over the block of the threads before of a count and (not in a search by count
+// alone) a mass per thread.
+template <Search S>
+__device__ __forceinline__ void block_scan(Shared &sm, uint32_t &c, Mass &m) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t c0 = c;
-    const uint64_t m0 = m;
+    const Mass m0 = m;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
-        const uint64_t mm = __shfl_up_sync(0xffffffffu, m, off);
-        if (lane >= off) {
-            c += cc;
-            m += mm;
+        if (lane >= off) c += cc;
+        if (S != kCount) {
+            const Mass mm = shfl_up(m, off);
+            if (lane >= off) m += mm;
         }
     }
     __syncthreads();
     if (lane == 31) {
         sm.warp_count[warp] = c;
-        sm.warp_mass[warp] = m;
+        if (S != kCount) sm.warp_mass[warp] = m;
     }
     __syncthreads();
     // the sums of the warps before: every warp scans them for itself
     const int warps = static_cast<int>(blockDim.x) >> 5;
     uint32_t bc = lane < warps ? sm.warp_count[lane] : 0;
-    uint64_t bm = lane < warps ? sm.warp_mass[lane] : 0;
+    Mass bm = 0;
+    if (S != kCount && lane < warps) bm = sm.warp_mass[lane];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t cc = __shfl_up_sync(0xffffffffu, bc, off);
-        const uint64_t mm = __shfl_up_sync(0xffffffffu, bm, off);
-        if (lane >= off) {
-            bc += cc;
-            bm += mm;
+        if (lane >= off) bc += cc;
+        if (S != kCount) {
+            const Mass mm = shfl_up(bm, off);
+            if (lane >= off) bm += mm;
         }
     }
     bc = __shfl_sync(0xffffffffu, bc, (warp + 31) & 31);
-    bm = __shfl_sync(0xffffffffu, bm, (warp + 31) & 31);
     c += (warp ? bc : 0) - c0;
-    m += (warp ? bm : 0) - m0;
+    if (S != kCount) {
+        bm = shfl(bm, (warp + 31) & 31);
+        m += (warp ? bm : 0) - m0;
+    }
 }
 
-// What a search looks for: the first place in the order where the tokens up
-// to and with it number `need` (count) or weigh `target` (mass).
-struct Goal {
-    bool by_mass;
-    uint32_t need;
-    uint64_t target;
-    __device__ __forceinline__ bool reached(uint32_t c, uint64_t m) const {
-        return by_mass ? m >= target : c >= need;
-    }
-};
+__device__ __forceinline__ uint64_t bin_mass(const Shared &sm, int bin) { return static_cast<uint64_t>(sm.hi[bin]) << 32 | sm.lo[bin]; }
 
-// Finds the goal's bin in the histogram, given what lies above the first bin;
-// leaves it with what lies above it in sm.bin, sm.above_*, sm.bin_count, and
-// the mass of everything in sm.total_mass; sm.bin is -1 if none reaches it.
-template <int T>
-__device__ __noinline__ void find_bin(Shared &sm, const Goal &goal, uint32_t above_count, uint64_t above_mass) {
+// Finds the search's bin in the histogram, given what lies above the first bin
+// (sm.base_*); leaves it with what lies above it in sm.bin, sm.above_*, sm.bin_count,
+// and the mass of everything in sm.total_mass; sm.bin is -1 if none reaches it.
+// The bins are of one octave, or (-1) the first-level ones, each of its own.
+template <int T, Search S>
+__device__ __noinline__ void find_bin(Shared &sm, uint32_t need, int octave) {
     constexpr int kPer = kBins / T;
-    uint32_t c = 0, ci[kPer];
-    uint64_t m = 0, mi[kPer];
-    const int first = threadIdx.x * kPer;
+    static_assert(kBinsPerOctave % kPer == 0, "a thread's bins are of one octave");
+    const int first = threadIdx.x * kPer, oct = octave < 0 ? first / kBinsPerOctave : octave;
     if (threadIdx.x == 0) sm.bin = -1;
+    uint32_t c = 0;
+    uint64_t units = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        ci[i] = sm.count[first + i];
-        mi[i] = static_cast<uint64_t>(sm.hi[first + i]) << 32 | sm.lo[first + i];
-        c += ci[i];
-        m += mi[i];
+        c += sm.count[first + i];
+        if (S != kCount) units += bin_mass(sm, first + i);
     }
     const uint32_t own_c = c;
-    const uint64_t own_m = m;
-    block_scan(sm, c, m);
-    c += above_count;
-    m += above_mass;
-    if (threadIdx.x == T - 1) sm.total_mass = m + own_m;
-    const bool here = goal.reached(c + own_c, m + own_m) && !goal.reached(c, m);
-    if (here) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (goal.reached(c + ci[i], m + mi[i])) {
-                sm.bin = first + i;
+    const Mass own_m = wide_mass(units, oct);
+    Mass m = own_m, target = 0;
+    block_scan<S>(sm, c, m);
+    c += sm.base_count;
+    if (S != kCount) {
+        m += sm.base_mass;
+        if (S == kMass) target = sm.target;
+        if (threadIdx.x == T - 1) sm.total_mass = m + own_m;
+    }
+    if (reached<S>(need, target, c + own_c, m + own_m) && !reached<S>(need, target, c, m)) {
+#pragma unroll 1
+        for (int i = first;; ++i) {  // (in one of the thread's)
+            const uint32_t n = sm.count[i];
+            const Mass here = S != kCount ? wide_mass(bin_mass(sm, i), oct) : 0;
+            if (reached<S>(need, target, c + n, m + here)) {
+                sm.bin = i;
                 sm.above_count = c;
-                sm.above_mass = m;
-                sm.bin_count = ci[i];
+                if (S != kCount) sm.above_mass = m;
+                sm.bin_count = n;
                 break;
             }
-            c += ci[i];
-            m += mi[i];
+            c += n;
+            m += here;
         }
     }
     __syncthreads();
@@ -416,50 +451,59 @@ __device__ __noinline__ void sort_list(Shared &sm, uint32_t n) {
     }
 }
 
-// The goal's place in the sorted list, given what lies above it: sm.cut, and the
-// mass up to it in sm.mass.
-template <int T>
-__device__ __noinline__ void place_in_list(Shared &sm, uint32_t n, const Weights &w, Goal goal, bool mass, uint32_t above_count,
-                                           uint64_t above_mass) {
+// The search's place in the sorted list, given what lies above it (sm.base_*): sm.cut,
+// and the mass up to it in sm.mass.
+template <int T, Search S>
+__device__ __noinline__ void place_in_list(Shared &sm, uint32_t n, const Weights w, float scale, uint32_t need) {
     constexpr int kPer = kList / T;
-    uint32_t c = 0, ci[kPer];
-    uint64_t m = 0, mi[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int t = threadIdx.x * kPer + i;
-        ci[i] = t < static_cast<int>(n) ? 1 : 0;
-        mi[i] = ci[i] && mass ? fixed_weight(w, value_of(static_cast<uint32_t>(sm.list[t] >> 32))) : 0;
-        c += ci[i];
-        m += mi[i];
-    }
-    block_scan(sm, c, m);
-    c += above_count;
-    m += above_mass;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (ci[i] && goal.reached(c + 1, m + mi[i]) && !goal.reached(c, m)) {
-            sm.cut = sm.list[threadIdx.x * kPer + i];
-            sm.mass = m + mi[i];
+    const auto mass_at = [&](int t) {  // as the bins have it
+        const float z = value_of(static_cast<uint32_t>(sm.list[t] >> 32));
+        const int octave = first_bin(z, w.zmax, scale) / kBinsPerOctave;
+        return wide_mass(bin_weight(w, z, octave), octave);
+    };
+    const int first = threadIdx.x * kPer, end = min(first + kPer, static_cast<int>(n));
+    uint32_t c = max(end - first, 0);
+    Mass m = 0, target = 0;
+    if (S != kCount)
+        for (int t = first; t < end; ++t) m += mass_at(t);
+    const uint32_t own_c = c;
+    const Mass own_m = m;
+    block_scan<S>(sm, c, m);
+    c += sm.base_count;
+    if (S != kCount) m += sm.base_mass;
+    if (S == kMass) target = sm.target;
+    if (reached<S>(need, target, c + own_c, m + own_m) && !reached<S>(need, target, c, m)) {
+#pragma unroll 1
+        for (int t = first; t < end; ++t) {
+            ++c;
+            if (S != kCount) m += mass_at(t);
+            if (reached<S>(need, target, c, m)) {
+                sm.cut = sm.list[t];
+                sm.mass = m;
+                break;
+            }
         }
-        c += ci[i];
-        m += mi[i];
     }
     __syncthreads();
 }
 
-// The goal's place inside the bin that find_bin left: the bin's elements are
+// The search's place inside the bin that find_bin left: the bin's elements are
 // sorted if they fit the list, else the bin is split by key until they do or
 // one value is left, whose ties go by index.  Leaves the place in sm.cut, and
 // the mass of the tokens up to it in sm.mass.
-template <int DT, int T>
-__device__ __noinline__ void find_place(Shared &sm, const char *row, int V, const Weights &w, float scale,
-                                        const Goal &goal, bool mass, bool grouped) {
-    const int bin = sm.bin;
-    uint32_t above_count = sm.above_count, n = sm.bin_count;
-    uint64_t above_mass = sm.above_mass;
+template <int DT, int T, Search S>
+__device__ __noinline__ void find_place(Shared &sm, const char *row, int V, const Weights w, float scale, uint32_t need, bool grouped) {
+    constexpr bool mass = S != kCount;
+    const int bin = sm.bin, octave = bin / kBinsPerOctave;
+    uint32_t n = sm.bin_count;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    const auto step_down = [&] {  // into the bin found
+        sm.base_count = sm.above_count;
+        if (mass) sm.base_mass = sm.above_mass;
         sm.n_list = 0;
+    };
+    if (threadIdx.x == 0) {
+        step_down();
         sm.key_lo = 0xffffffffu;
         sm.key_hi = 0;
     }
@@ -489,22 +533,20 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
         for_each<DT, T, 1>(sm, row, V, grouped ? klo : 0, [&](float z, int) {
             const uint32_t key = key_of(z);
             if (key < klo || key > khi) return;
-            add_to_bin(sm, static_cast<int>((khi - key) >> shift), mass, mass ? fixed_weight(w, z) : 0);
+            add_to_bin(sm, static_cast<int>((khi - key) >> shift), mass, mass ? bin_weight(w, z, octave) : 0);
         });
         __syncthreads();
-        find_bin<T>(sm, goal, above_count, above_mass);
+        find_bin<T, S>(sm, need, octave);
         const uint32_t j = static_cast<uint32_t>(sm.bin);
         const uint32_t top = khi - (j << shift);
         const uint32_t width = (1u << shift) - 1;
         klo = top - klo > width ? top - width : klo;
         khi = top;
-        above_count = sm.above_count;
-        above_mass = sm.above_mass;
         n = sm.bin_count;
         __syncthreads();
+        if (threadIdx.x == 0) step_down();
+        __syncthreads();
         if (n <= kList) {
-            if (threadIdx.x == 0) sm.n_list = 0;
-            __syncthreads();
             for_each<DT, T, 1>(sm, row, V, grouped ? klo : 0, [&](float z, int i) {
                 const uint32_t key = key_of(z);
                 if (key >= klo && key <= khi) sm.list[atomicAdd(&sm.n_list, 1u)] = place_of(key, i);
@@ -515,19 +557,20 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
     }
     if (listed) {
         sort_list<T>(sm, n);
-        place_in_list<T>(sm, n, w, goal, mass, above_count, above_mass);
+        place_in_list<T, S>(sm, n, w, scale, need);
         return;
     }
-    // one value: how many of its ties the goal takes, and the last one's index
-    const uint64_t wt = mass ? fixed_weight(w, value_of(khi)) : 0;
+    // one value: how many of its ties the search takes, and the last one's index
+    const uint64_t wt = mass ? bin_weight(w, value_of(khi), octave) : 0;
     uint32_t take = n;
-    if (!goal.by_mass) {
-        take = goal.need - above_count;
+    if (S != kMass) {
+        take = need - sm.base_count;
     } else {
+        const Mass base = sm.base_mass, target = sm.target;
         uint32_t lo = 1, hi = n;  // the fewest whose mass reaches the target
         while (lo < hi) {
             const uint32_t mid = lo + (hi - lo) / 2;
-            if (goal.reached(0, above_mass + mid * wt)) hi = mid;
+            if (base + wide_mass(mid * wt, octave) >= target) hi = mid;
             else lo = mid + 1;
         }
         take = lo;
@@ -540,7 +583,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
         const int v0 = min(vecs, static_cast<int>(threadIdx.x) * per), v1 = min(vecs, v0 + per);
         const uint4 *p = reinterpret_cast<const uint4 *>(row);
         uint32_t c = 0;
-        uint64_t none = 0;
+        Mass none = 0;
         for (int v = v0; v < v1; ++v) {
             float x[kPer];
             Elem<DT>::unpack(p[v], x);
@@ -548,7 +591,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
             for (int i = 0; i < kPer; ++i) c += key_of(x[i]) == khi;
         }
         const uint32_t own = c;
-        block_scan(sm, c, none);
+        block_scan<kCount>(sm, c, none);
         if (c < take && c + own >= take) {
             for (int v = v0; v < v1; ++v) {
                 float x[kPer];
@@ -564,7 +607,7 @@ __device__ __noinline__ void find_place(Shared &sm, const char *row, int V, cons
     __syncthreads();
     if (threadIdx.x == 0) {
         sm.cut = place_of(khi, static_cast<int>(last));
-        sm.mass = above_mass + take * wt;
+        if (mass) sm.mass = sm.base_mass + wide_mass(take * wt, octave);
     }
     __syncthreads();
 }
@@ -614,12 +657,19 @@ __device__ __forceinline__ void set_scale(RowConstants &rc, const Settings &s) {
     rc.cl = static_cast<float>(c - static_cast<double>(rc.ch));
 }
 __device__ __forceinline__ Weights row_weights(const RowConstants &rc, float zmax, int V, const float2 *table) {
-    // V weights of at most 1 sum to less than 2^63
+    // V weights of at most 1.02 sum to less than 2^63
     return Weights{zmax, rc.ch, rc.cl, min(47, 30 + __clz(V)), table};
 }
-// The least mass that is not below p Z.
-__device__ __forceinline__ uint64_t mass_target(float p, uint64_t Z) {
-    return __double2ull_ru(static_cast<double>(p) * static_cast<double>(Z));
+// The least mass that is not below p Z, exactly: p = mantissa 2^-q, 24 <= q <= 149.
+__device__ __forceinline__ Mass mass_target(float p, Mass Z) {
+    const uint32_t u = __float_as_uint(p), ex = u >> 23;  // (0 < p < 1)
+    const uint32_t mantissa = ex ? (u & 0x7fffffu) | 0x800000u : u;
+    const int q = ex ? 150 - static_cast<int>(ex) : 149;
+    const Mass lo = static_cast<Mass>(static_cast<uint64_t>(Z)) * mantissa;
+    const Mass hi = static_cast<Mass>(static_cast<uint64_t>(Z >> 64)) * mantissa + (lo >> 64);  // the product: hi 2^64 + l
+    const uint64_t l = static_cast<uint64_t>(lo);
+    if (q < 64) return (hi << (64 - q) | l >> q) + (l << (64 - q) != 0);
+    return (hi >> (q - 64)) + (l != 0 || (hi & ((static_cast<Mass>(1) << (q - 64)) - 1)) != 0);
 }
 __device__ __forceinline__ void fill_table(float2 *table) {
     if (threadIdx.x < 64) table[threadIdx.x] = kExp2Table[threadIdx.x];
@@ -629,8 +679,8 @@ __device__ __forceinline__ void fill_table(float2 *table) {
 // below it goes; 0: the row stays as it is.  Passes over the row: its largest
 // value (and its copy in `hold`, if given, which the others then read), a histogram
 // over 32 bins per halving of the weight, the border bin's elements, sorted.  fp32 logits have no few values, so top-p computes a weight
-// per token (about 45 instructions): 384 rows of 128256 take 151 us with top-k
-// (2.6 TB/s), 361 with top-p alone (1.1 TB/s), where those instructions bound it:
+// per token (about 45 instructions): 384 rows of 128256 take 139 us with top-k
+// (2.8 TB/s), 340 with top-p alone (1.2 TB/s), where those instructions bound it:
 // exact masses for the bins around the border alone, the rest summed in
 // registers, took 427.
 template <int DT, int T>
@@ -659,21 +709,30 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
     const bool mass = s.p < 1.0f;
     uint64_t cut = 0;
     if (s.k > 0 || mass) {
-        Goal goal{false, static_cast<uint32_t>(s.k), 0};
-        uint64_t Z = 0;
+        const uint32_t k = s.k;
         auto fill = [&](bool mass) {
             clear_bins<T>(sm);
             if (mass)
-                for_each<DT, T, 1>(sm, row, V, 0, [&](float z, int) { add_to_bin(sm, first_bin(z, zmax, scale), true, fixed_weight(w, z)); });
+                for_each<DT, T, 1>(sm, row, V, 0, [&](float z, int) {
+                    const int bin = first_bin(z, zmax, scale);
+                    add_to_bin(sm, bin, true, bin_weight(w, z, bin / kBinsPerOctave));
+                });
             else
                 for_each<DT, T, kFlight<DT>>(sm, row, V, 0, [&](float z, int) { atomicAdd(&sm.count[first_bin(z, zmax, scale)], 1u); });
             __syncthreads();
         };
+        auto from_top = [&] {  // nothing above the first bin
+            if (tid == 0) {
+                sm.base_count = 0;
+                sm.base_mass = 0;
+            }
+        };
         bool done = false;
+        from_top();
         if (s.k > 0 && s.k <= kList) {
             // few tokens: they are listed and sorted, and only theirs are the weights that matter
             fill(false);
-            find_bin<T>(sm, goal, 0, 0);
+            find_bin<T, kCount>(sm, k, -1);
             const int bin = sm.bin;
             const uint32_t n = sm.above_count + sm.bin_count;
             __syncthreads();
@@ -686,41 +745,40 @@ __device__ __noinline__ uint64_t cut_of_row(Shared &sm, const char *row, int V, 
                 });
                 __syncthreads();
                 sort_list<T>(sm, n);
-                place_in_list<T>(sm, n, w, goal, mass, 0, 0);
-                cut = sm.cut;
-                Z = sm.mass;
-                __syncthreads();
                 if (mass) {
-                    if (tid == 0) sm.target = mass_target(s.p, Z);
+                    place_in_list<T, kCountMass>(sm, n, w, scale, k);
+                    if (tid == 0) sm.target = mass_target(s.p, sm.mass);
                     __syncthreads();
-                    place_in_list<T>(sm, s.k, w, Goal{true, 0, sm.target}, true, 0, 0);
+                    place_in_list<T, kMass>(sm, k, w, scale, 0);
                     cut = sm.cut;
-                    __syncthreads();
+                } else {
+                    cut = sm.list[k - 1];
                 }
+                __syncthreads();
             }
         }
         if (!done) fill(mass);
         if (s.k > 0 && !done) {
-            find_bin<T>(sm, goal, 0, 0);
-            const bool splits = sm.bin_count > kList;  // find_place then uses the bins itself
-            find_place<DT, T>(sm, row, V, w, scale, goal, mass, grouped);
-            cut = sm.cut;
-            Z = sm.mass;
-            __syncthreads();
-            if (mass && splits) fill(true);
+            if (mass) {
+                find_bin<T, kCountMass>(sm, k, -1);
+                const bool splits = sm.bin_count > kList;  // find_place then uses the bins itself
+                find_place<DT, T, kCountMass>(sm, row, V, w, scale, k, grouped);
+                cut = sm.cut;
+                __syncthreads();
+                from_top();
+                if (splits) fill(true);
+            } else {
+                find_bin<T, kCount>(sm, k, -1);
+                find_place<DT, T, kCount>(sm, row, V, w, scale, k, grouped);
+                cut = sm.cut;
+            }
         }
         if (mass && !done) {
-            goal.by_mass = true;
-            if (s.k == 0) {
-                find_bin<T>(sm, goal, 0, 0);
-                Z = sm.total_mass;
-                __syncthreads();
-            }
-            if (tid == 0) sm.target = mass_target(s.p, Z);
+            if (s.k == 0) find_bin<T, kCountMass>(sm, 0xffffffffu, -1);  // (none reaches it) the mass of everything
+            if (tid == 0) sm.target = mass_target(s.p, s.k > 0 ? sm.mass : sm.total_mass);
             __syncthreads();
-            goal.target = sm.target;
-            find_bin<T>(sm, goal, 0, 0);
-            find_place<DT, T>(sm, row, V, w, scale, goal, true, grouped);
+            find_bin<T, kMass>(sm, 0, -1);
+            find_place<DT, T, kMass>(sm, row, V, w, scale, 0, grouped);
             cut = max(cut, sm.cut);
         }
     }
@@ -838,7 +896,7 @@ struct FastShared {
     uint32_t zeros;
     // of each segment, then (by the warp that finds the border) of it and those before
     uint32_t seg_count[32 * kSegsPerLane];
-    uint64_t seg_mass[32 * kSegsPerLane];
+    alignas(16) Mass seg_mass[32 * kSegsPerLane];
     uint16_t group_max[kMaxGroups];  // order key of each group's largest value
     int first;                       // the largest value's place
     // the border: tokens above its value stay, `take` of its ties do
@@ -906,25 +964,36 @@ __device__ __forceinline__ float place_value(int place) {
 // Unsigned 16-bit key in the order of the values (-0 below +0).
 __device__ __forceinline__ uint32_t key16(uint32_t u) { return u ^ (u & 0x8000u ? 0xffffu : 0x8000u); }
 
-// t tokens' weight: the product before the one rounding.
+// t tokens' weight in units of 2^-100: no bit of a weight above 2^-52 is lost, and
+// 2^18 of the largest fit.  (In 64 bits the values' sums are rounded at 2^-46 at 128256
+// columns: thousands of small values around zero, a token each, lose the same way,
+// 2^-33 of the largest weight together.)
 struct TokenWeight {
     uint64_t mantissa;
-    int by;
+    int up;
     __device__ __forceinline__ TokenWeight(const Weights &w, float z) {
         int e;
         mantissa = weight_mantissa(w, z, &e);
-        by = min(-(e + w.frac), 127);  // at least 1: frac <= 47
+        up = e + 100;  // -68 .. 52
+        if (up < 0) {
+            mantissa = up > -64 ? mantissa >> -up : 0;
+            up = 0;
+        }
     }
-    __device__ __forceinline__ uint64_t times(uint32_t t) const {
-        uint64_t lo = mantissa * t, hi = __umul64hi(mantissa, t);
-        if (by >= 64) lo = hi, hi = 0;
-        const int left = by & 63;  // 0 where by is 64: nothing to round by
-        const uint64_t half = left ? 1ull << (left - 1) : 0;
-        lo += half;
-        hi += lo < half;
-        return left ? lo >> left | hi << (64 - left) : lo;
+    __device__ __forceinline__ Mass times(uint32_t t) const {
+        const uint64_t lo = mantissa * t, hi = __umul64hi(mantissa, t);
+        return static_cast<Mass>(hi << up | lo >> 1 >> (63 - up)) << 64 | lo << up;
     }
 };
+
+// The sum over the lanes of masses below 2^120: 27 bits at a time, so that 32 of them fit 32 bits.
+__device__ __forceinline__ Mass warp_sum(Mass m) {
+    Mass sum = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        sum += static_cast<Mass>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(m >> (27 * i)) & 0x7ffffffu)) << (27 * i);
+    return sum;
+}
 
 // 0xffff in the halves of a that are greater than (or equal to) b's
 __device__ __forceinline__ uint32_t above_mask(uint32_t a, uint32_t b, bool equal) {
@@ -1005,41 +1074,43 @@ __device__ __forceinline__ void count_values(FastShared &sm, const uint4 &q, uin
     }
 }
 
-// Inclusive sums over the lanes.
-__device__ __forceinline__ void warp_scan(uint32_t &c, uint64_t &m) {
+// Inclusive sums over the lanes of a count and, if wanted, a mass.
+template <bool MASS>
+__device__ __forceinline__ void warp_scan(uint32_t &c, Mass &m) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t cc = __shfl_up_sync(0xffffffffu, c, off);
-        const uint64_t mm = __shfl_up_sync(0xffffffffu, m, off);
-        if (lane >= off) {
-            c += cc;
-            m += mm;
+        if (lane >= off) c += cc;
+        if (MASS) {
+            const Mass mm = shfl_up(m, off);
+            if (lane >= off) m += mm;
         }
     }
 }
 
 // The segments' sums into running sums, by one warp.
-__device__ __forceinline__ void scan_segments(FastShared &sm, bool mass) {
+template <bool MASS>
+__device__ __forceinline__ void scan_segments(FastShared &sm) {
     const int s0 = (threadIdx.x & 31) * kSegsPerLane;
     uint32_t n[kSegsPerLane], c = 0;
-    uint64_t nm[kSegsPerLane], m = 0;
+    Mass nm[kSegsPerLane], m = 0;
 #pragma unroll
     for (int i = 0; i < kSegsPerLane; ++i) {
         n[i] = sm.seg_count[s0 + i];
-        nm[i] = mass ? sm.seg_mass[s0 + i] : 0;
+        nm[i] = MASS ? sm.seg_mass[s0 + i] : 0;
         c += n[i];
         m += nm[i];
     }
     const uint32_t own_c = c;
-    const uint64_t own_m = m;
-    warp_scan(c, m);
+    const Mass own_m = m;
+    warp_scan<MASS>(c, m);
     c -= own_c;
     m -= own_m;
 #pragma unroll
     for (int i = 0; i < kSegsPerLane; ++i) {
         sm.seg_count[s0 + i] = c += n[i];
-        sm.seg_mass[s0 + i] = m += nm[i];
+        if (MASS) sm.seg_mass[s0 + i] = m += nm[i];
     }
     __syncwarp();
 }
@@ -1048,23 +1119,25 @@ __device__ __forceinline__ void scan_segments(FastShared &sm, bool mass) {
 struct Border {
     int place;
     uint32_t above_count, n;
-    uint64_t above_mass;
+    Mass above_mass;
 };
 
-// Where the goal is reached in the histogram, by one warp, from the running
+// Where the search ends in the histogram, by one warp, from the running
 // sums; place -1 if the bins end before.  (Shared-memory round trips are what
 // this costs beside another CTA's histogram, so it makes few.)
-__device__ __forceinline__ Border locate(const FastShared &sm, const Weights &w, const Goal &goal, bool mass) {
+template <Search S>
+__device__ __forceinline__ Border locate(const FastShared &sm, const Weights &w, uint32_t need, Mass target) {
+    constexpr bool mass = S != kCount;
     const int lane = threadIdx.x & 31, s0 = lane * kSegsPerLane;
     uint32_t c = lane ? sm.seg_count[s0 - 1] : 0;
-    uint64_t m = lane ? sm.seg_mass[s0 - 1] : 0;
+    Mass m = mass && lane ? sm.seg_mass[s0 - 1] : 0;
     int seg = -1;
 #pragma unroll
     for (int i = 0; i < kSegsPerLane; ++i) {
         const uint32_t c1 = sm.seg_count[s0 + i];
-        const uint64_t m1 = sm.seg_mass[s0 + i];
+        const Mass m1 = mass ? sm.seg_mass[s0 + i] : 0;
         if (seg < 0) {
-            if (goal.reached(c1, m1)) {
+            if (reached<S>(need, target, c1, m1)) {
                 seg = s0 + i;
             } else {
                 c = c1;
@@ -1077,38 +1150,38 @@ __device__ __forceinline__ Border locate(const FastShared &sm, const Weights &w,
     int at = __ffs(hit) - 1;
     seg = __shfl_sync(0xffffffffu, seg, at);
     c = __shfl_sync(0xffffffffu, c, at);
-    m = __shfl_sync(0xffffffffu, m, at);
+    if (mass) m = shfl(m, at);
     uint32_t n[4];
-    uint64_t nm[4];
+    Mass nm[4];
     sm.counts(seg, n);
 #pragma unroll
     for (int i = 0; i < 4; ++i) nm[i] = mass ? TokenWeight(w, place_value(seg * kSegPlaces + lane * 4 + i)).times(n[i]) : 0;
     uint32_t cs = n[0] + n[1] + n[2] + n[3];
-    uint64_t ms = nm[0] + nm[1] + nm[2] + nm[3];
+    Mass ms = nm[0] + nm[1] + nm[2] + nm[3];
     const uint32_t own_c = cs;
-    const uint64_t own_m = ms;
-    warp_scan(cs, ms);
+    const Mass own_m = ms;
+    warp_scan<mass>(cs, ms);
     cs += c;
     ms += m;
-    at = __ffs(__ballot_sync(0xffffffffu, goal.reached(cs, ms))) - 1;
+    at = __ffs(__ballot_sync(0xffffffffu, reached<S>(need, target, cs, ms))) - 1;
     cs -= own_c;
     ms -= own_m;
     int place = seg * kSegPlaces + lane * 4;
     uint32_t here = n[0];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        if (place != seg * kSegPlaces + lane * 4 + i || goal.reached(cs + n[i], ms + nm[i])) continue;
+        if (place != seg * kSegPlaces + lane * 4 + i || reached<S>(need, target, cs + n[i], ms + nm[i])) continue;
         cs += n[i];
         ms += nm[i];
         here = n[i + 1];
         ++place;
     }
     return Border{__shfl_sync(0xffffffffu, place, at), __shfl_sync(0xffffffffu, cs, at), __shfl_sync(0xffffffffu, here, at),
-                  __shfl_sync(0xffffffffu, ms, at)};
+                  mass ? shfl(ms, at) : 0};
 }
 
 // The fewest of n ties whose weight reaches the target, by one warp.
-__device__ __forceinline__ uint32_t ties_for(const TokenWeight &w, uint32_t n, uint64_t above, uint64_t target) {
+__device__ __forceinline__ uint32_t ties_for(const TokenWeight &w, uint32_t n, Mass above, Mass target) {
     uint32_t lo = 1, hi = n;  // the answer lies in [lo, hi]
     while (lo < hi) {
         const uint32_t step = (hi - lo + 31) / 32;
@@ -1149,7 +1222,7 @@ __device__ __forceinline__ uint32_t max_key(const uint4 &q) {
 template <int CL>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     truncate_bf16_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
-    extern __shared__ char smem[];
+    extern __shared__ __align__(16) char smem[];
     BothShared &all = *reinterpret_cast<BothShared *>(smem);
     FastShared &sm = all.fast;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1268,14 +1341,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         w = row_weights(all.row, zmax, V, all.table);
         if (mass) {
             for (int g = warp; g < kSegs; g += kWarps) {
-                uint64_t m = 0;
+                Mass m = 0;
                 if (sm.seg_count[g]) {
                     uint32_t n[4];
                     sm.counts(g, n);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) m += TokenWeight(w, place_value(g * kSegPlaces + lane * 4 + i)).times(n[i]);
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
+                    m = warp_sum(m);
                 }
                 if (lane == 0) sm.seg_mass[g] = m;
             }
@@ -1283,23 +1355,28 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         }
         // --- the border, by one warp
         if (warp == 0 && counted) {
-            scan_segments(sm, mass);
             Border k{kPlaces, 0, 0, 0};
             uint32_t take = 0;
-            uint64_t Z = mass ? sm.seg_mass[kSegs - 1] : 0;
+            Mass Z = 0;
+            if (mass) {
+                scan_segments<true>(sm);
+                Z = sm.seg_mass[kSegs - 1];
+            } else {
+                scan_segments<false>(sm);
+            }
             if (s.k > 0) {
-                k = locate(sm, w, Goal{false, static_cast<uint32_t>(s.k), 0}, mass);
+                const uint32_t need = s.k;
+                k = mass ? locate<kCountMass>(sm, w, need, 0) : locate<kCount>(sm, w, need, 0);
                 if (k.place >= 0) {
-                    take = s.k - k.above_count;
+                    take = need - k.above_count;
                     if (mass) Z = k.above_mass + TokenWeight(w, place_value(k.place)).times(take);
                 } else if (!finite_low) {
                     k = Border{kPlaces, 0, 0, 0};  // fewer than k tokens are not -inf: all of them
                 }
             }
             if (mass && k.place >= 0) {
-                uint64_t target = lane == 0 ? mass_target(s.p, Z) : 0;
-                target = __shfl_sync(0xffffffffu, target, 0);
-                const Border p = locate(sm, w, Goal{true, 0, target}, true);
+                const Mass target = mass_target(s.p, Z);
+                const Border p = locate<kMass>(sm, w, 0, target);
                 if (p.place >= 0) {
                     const uint32_t t = ties_for(TokenWeight(w, place_value(p.place)), p.n, p.above_mass, target);
                     take = p.place < k.place ? t : min(t, take);

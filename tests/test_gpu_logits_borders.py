@@ -182,3 +182,131 @@ def test_top_p_of_the_first_k(sv, dtype, V, k):
             ps.append(p), want.append(n)
     z = np.stack(rows)
     check(run(sv, z, np.ones(len(z)), ps, dtype, np.full(len(z), k)), z, want)
+
+
+# ------------------------------------------------------------------ flat tails
+# Many tokens of the same small weight: what is lost of each is lost of all alike.
+def tail_borders(Z1, w, n1, least):
+    """top_p that cut a tail of n1 tokens of about weight w behind a mass of 1 (Z1 in all): the fp32
+    values nearest to a whole number of them on either side, and some others."""
+    lo = f32(1 / Z1)
+    bits = np.arange(int(lo.view(np.uint32)), int(f32(1).view(np.uint32)), dtype=np.uint32)
+    p = bits.view(f32)[:1 << 16]
+    x = (p.astype(np.float64) * Z1 - 1) / w
+    frac = x - np.floor(x)
+    ok = np.flatnonzero((x > 1) & (x < n1 - 1) & (frac > least) & (frac < 1 - least))
+    order = ok[np.argsort(frac[ok], kind="stable")]
+    return p[np.concatenate([order[:3], order[-3:], order[len(order) // 2:][:2]])]
+
+
+# V, distance; the sums' rounding in a row of 2^24 columns is 2^-37, so that the bound
+# is 2 n1 (2^-37 + 2^-41) of a token there
+TAILS = [("fp32", 128256, -22.7), ("fp32", 128256, -25.0), ("fp32", 128256, -18.25), ("fp32", 4104, -20.3),
+         ("bf16", 128256, -22.75), ("bf16", 128256, -18.25), ("fp32", 1 << 24, -24.3), ("bf16 any", 128256, -22.75)]
+
+
+@pytest.mark.parametrize("dtype,V,d", TAILS)
+def test_top_p_within_a_flat_tail(sv, dtype, V, d):
+    rng = np.random.default_rng(V)
+    top = f32(0)
+    if dtype == "bf16 any":  # a value without a bin sends the row down the path for any row
+        dtype, top = "bf16", f32(2.0 ** -40)
+    d, n1 = float(f32(d)), V - 1
+    w = weight(d, top, 1)
+    least = 2 * n1 * (EPS if V < 1 << 20 else 2.0 ** -36.9)
+    ps = tail_borders(float(1 + n1 * w), float(w), n1, max(least, 2.0 ** -9))
+    assert len(ps) == 8
+    want = []
+    for p in ps:
+        n, far = kept([(1, Decimal(1)), (n1, w)], p)
+        assert far > least
+        want.append(n)
+    if V < 1 << 20:
+        z = np.stack([rows_of(rng, V, [(1, top), (n1, d)], dtype) for _ in ps])
+        check(run(sv, z, np.ones(8), ps, dtype), z, want)
+    else:  # the order is the index's, but for the first token
+        z = np.full((8, V), d, f32)
+        z[:, 1000] = top
+        got = run(sv, z, np.ones(8), ps, dtype)
+        for r, n in enumerate(want):
+            assert np.isfinite(got[r]).sum() == n and got[r, 1000] == 0 and np.isfinite(got[r, :n - 1]).all()
+
+
+def test_top_p_within_thousands_of_small_values(sv):
+    """bf16: 3840 values of either sign next to zero, a token each, far below one large value: their weights are
+    the same to 2^-16, so that a rounding of each goes the same way."""
+    V = 262144
+    m = (2.0 ** np.arange(-32, -17)[:, None] * (1 + np.arange(128) / 128)).ravel()
+    small = np.sort(np.concatenate([m, -m]).astype(f32))[::-1]
+    rng = np.random.default_rng(8)
+    rows, ps, want = [], [], []
+    for top in (16.0, 18.0, 19.0, 19.5, 20.0, 20.25, 20.5):
+        levels = [(1, Decimal(1))] + [(1, weight(v, top, 1)) for v in small]
+        tail = sum(w for _, w in levels[1:])
+        least = 2 * len(small) * EPS
+        for p in tail_borders(float(1 + tail), float(tail) / len(small), len(small), 0.0):
+            n, far = kept(levels, p)
+            if far <= least:
+                continue
+            rows.append(rows_of(rng, V, [(1, top)] + [(1, v) for v in small], "bf16"))
+            ps.append(p), want.append(n)
+    z = np.stack(rows)
+    assert len(z) >= 40
+    check(run(sv, z, np.ones(len(z)), ps, "bf16"), z, want)
+
+
+# -------------------------------------------------- rows near several borders at once
+def lengths(row, T, k, p, m, delta):
+    """The order, and the fewest and the most tokens kept if the masses are off by up to delta Z."""
+    V = len(row)
+    order = np.lexsort((np.arange(V), -row.astype(np.float64)))
+    s = row[order].astype(np.float64)
+    x = (s - s[0]) / float(T)
+    most = V if k == 0 else min(k, V)
+    w = np.exp(x[:most]).astype(np.longdouble)
+    before = np.concatenate([[0], np.cumsum(w)[:-1]])
+    Z = w.sum()
+    short = max(int((before < (float(p) - delta) * Z).sum()), 1) if p < 1 else most
+    long = max(int((before < (float(p) + delta) * Z).sum()), 1) if p < 1 else most
+    by_min = int((x >= np.log(float(m))).sum()) if m > 0 else V
+    return order, min(short, by_min), min(long, by_min)
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 4104), ("fp32", 4104), ("fp32", 32000), ("bf16", 152064)])
+@pytest.mark.parametrize("what", ["ties", "coarse", "equal", "masked", "flat", "steps", "both_signs"])
+def test_kept_tokens_are_a_prefix(sv, what, dtype, V):
+    """Whatever the row, a prefix of the order is kept, and its length is the one of exact masses unless tokens
+    within 2^-40 of the border are concerned (the masses' relative error, with a factor of two to spare)."""
+    rng = np.random.default_rng(len(what) + V)
+    B = 16
+    z = (-1.1 * np.log1p(rng.random((B, V)) * V) + rng.standard_normal((B, V))).astype(f32)
+    if what == "ties":
+        z = (np.round(z * 4) / 4).astype(f32)
+    elif what == "coarse":
+        z = (np.round(z / 4) * 4).astype(f32)
+    elif what == "equal":
+        z[:] = f32(-1.5)
+    elif what == "masked":
+        z[rng.random(z.shape) < 0.98] = -np.inf
+    elif what == "flat":
+        z[:, V // 16:] = f32(-16.0)
+    elif what == "steps":
+        z = (z.max(axis=1, keepdims=True) - f32(0.6953125) * rng.integers(0, 20, z.shape)).astype(f32)
+    elif what == "both_signs":
+        z = (z * rng.choice(f32([1, -1]), z.shape) * f32(0.02)).astype(f32)
+    z = to_bf16(z) if dtype == "bf16" else z
+    T = rng.choice(f32([0.3, 1.0, 2.0]), B)
+    for with_k, with_m in ((False, False), (True, False), (True, True)):
+        p = rng.choice(f32([0.1, 0.5, 0.9, 0.99, 0.9999, 1 - 2.0 ** -20, 1 - 2.0 ** -24]), B)
+        k = rng.choice(i32([0, 1, 60, V // 3, V - 1]), B) if with_k else np.zeros(B, i32)
+        m = rng.choice(f32([0, 1e-6, 0.01]), B) if with_m else np.zeros(B, f32)
+        x = torch.from_numpy(z).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+        dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+        got = sv.spec_logits_truncate(x, dev(T), torch.zeros(B + 1, dtype=torch.int32, device="cuda"), top_p=dev(p), top_k=dev(k),
+                                      min_p=dev(m)).float().cpu().numpy()
+        for r in range(B):
+            order, fewest, most = lengths(z[r], T[r], k[r], p[r], m[r], 2.0 ** -40)
+            there = int(np.isfinite(z[r]).sum())
+            n = int(np.isfinite(got[r]).sum())
+            assert min(fewest, there) <= n <= most, (r, fewest, n, most)
+            assert (got[r][order[:n]] == z[r][order[:n]]).all()
