@@ -562,7 +562,9 @@ int launch_process(const void *logits, void *out, const Rows &rw, const Process 
     // few sequences: their rows are split until every SM has its CTAs; long ones into parts
     // of about 8 rows, so that the last CTAs are short (64 trees of 16 rows: 119 us whole,
     // 108 in halves; halves of 6 rows cost more set-up than they gain: 320 and 367 us at B=512)
-    const int64_t room = static_cast<int64_t>(sms) * kPerSm<STREAM> * G::kCount, each = rw.R / rw.B;
+    // (a buffer may have more rows than its sequences can own)
+    const int64_t most = rw.mode == SPEC_ROWS_TREE ? SPEC_MAX_TREE_NODES : rw.mode == SPEC_ROWS_NEXT ? 1 : SPEC_MAX_K + 1;
+    const int64_t room = static_cast<int64_t>(sms) * kPerSm<STREAM> * G::kCount, each = std::min<int64_t>(rw.R / rw.B, most);
     const int parts = static_cast<int>(std::max<int64_t>({1, std::min(room / pairs, each), each / 8}));
     const int64_t ctas = (pairs * parts + G::kCount - 1) / G::kCount;
     process_kernel<DT, STREAM><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(

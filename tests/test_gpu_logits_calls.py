@@ -1,0 +1,81 @@
+"""Calls of the logit operators that their documentation allows and that lie at
+its edges: padded buffers, streams, empty arguments, long lists."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import logits_ref as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+f32, i32 = np.float32, np.int32
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verification_61_gb300 as m
+    m.lib()
+    return m
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to({"fp32": torch.float32, "bf16": torch.bfloat16}[dtype])
+
+
+def host(t):
+    return t.float().cpu().numpy()
+
+
+def tree(n):
+    """One tree of n nodes, each a child of the one before."""
+    return ref.Rows("tree", i32([0, n]), np.arange(n) % 8, np.arange(n) - 1)
+
+
+# ------------------------------------------------------------------ padded buffers
+@pytest.mark.parametrize("in_place", [False, True])
+def test_buffer_of_many_more_rows_than_sequences(sv, in_place):
+    """2^28 + 40 rows of 8 columns for one tree of 64 nodes: how a sequence's rows are split goes by what a
+    sequence can own (by the buffer's rows, a part's first row would pass 32 bits)."""
+    R, V, n = (1 << 28) + 40, 8, 64
+    rng = np.random.default_rng(0)
+    rows = tree(n)
+    z = ref.to_bf16(rng.standard_normal((n, V)).astype(f32))
+    counts = rng.integers(0, 3, (1, V)).astype(i32)
+    p = dict(counts=counts, seen=ref.pack(np.stack([rng.random((1, V)) < 0.3, counts > 0], 1)), repetition=f32([1.3]),
+             frequency=f32([0.2]), presence=f32([0.1]))
+    want, _, _ = ref.process(z, rows, p, ref.BF16)
+    x = torch.full((R, V), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[:n] = dev(z, "bf16")
+    out = x if in_place else torch.full_like(x, 2.0)
+    sv.spec_logits_process(x, dev(rows.offsets), dev(rows.tokens.astype(i32)), rows="tree", parent=dev(rows.parent.astype(i32)), out=out,
+                           **{k: dev(v) for k, v in p.items()})
+    assert np.array_equal(host(out[:n]), want)
+    assert bool((out[n:] == 2.0).all())
+
+
+@pytest.mark.parametrize("mode", ["target", "draft", "next", "tree"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_padded_buffers(sv, mode, in_place):
+    """Buffers of ten times the rows, as a captured graph keeps them."""
+    rng = np.random.default_rng(len(mode))
+    V, ks = 4104, np.array([3, 0, 5, 32])
+    per = ks + (mode == "tree")
+    off = np.concatenate([[0], np.cumsum(per)]).astype(i32)
+    tokens = rng.integers(0, V, off[-1]).astype(i32)
+    parent = np.concatenate([[-1] + [off[b] + rng.integers(0, g) for g in range(1, m)] for b, m in enumerate(per)]).astype(i32) if mode == "tree" else None
+    rows = ref.Rows(mode, off, tokens, parent)
+    n = rows.count()
+    z = ref.to_bf16(rng.standard_normal((10 * n, V)).astype(f32))
+    counts = np.where(rng.random((4, V)) < 0.2, rng.integers(1, 4, (4, V)), 0).astype(i32)
+    p = dict(counts=counts, seen=ref.pack(np.stack([rng.random((4, V)) < 0.1, counts > 0], 1)), repetition=f32([1.3, 1, 2, 0.8]))
+    want, _, _ = ref.process(z, rows, p, ref.BF16)
+    x = dev(z, "bf16")
+    out = x if in_place else x.clone()
+    sv.spec_logits_process(x, dev(off), dev(tokens), rows=mode, parent=None if parent is None else dev(parent), out=out,
+                           **{k: dev(v) for k, v in p.items()})
+    assert np.array_equal(host(out), np.concatenate([want[:n], z[n:]]))
