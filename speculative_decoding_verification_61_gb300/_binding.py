@@ -168,6 +168,23 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _new(shape, dtype, dev, stream, fill=None):
+    """A call's output: memory of the stream that the call runs on (what the current stream has freed may still
+    be in use there), not given to others before the current stream, too, is done with it."""
+    import torch
+
+    def make():
+        return torch.empty(shape, dtype=dtype, device=dev) if fill is None else torch.full(shape, fill, dtype=dtype, device=dev)
+
+    here = None if stream is None else torch.cuda.current_stream(dev)
+    if here is None or here.cuda_stream == stream.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
 def _raise(rc, what):
     if rc != 0:
         detail = lib().spec_last_error().decode() if rc == -3 else ""
@@ -690,9 +707,9 @@ def _rows_arg(logits, offsets, rows, draft_tokens, parent, i32):
                  _ptr(draft_tokens, "draft_tokens", i32, dev), n_tokens)
 
 
-def _out_arg(logits, out, torch):
+def _out_arg(logits, out, stream):
     if out is None:
-        out = torch.empty_like(logits)
+        out = _new(logits.shape, logits.dtype, logits.device, stream)
         return out, out.data_ptr()
     return out, _ptr(out, "out", logits.dtype, logits.get_device(), logits.numel())
 
@@ -753,7 +770,7 @@ def spec_logits_process(logits, offsets, draft_tokens=None, *, rows="target", pa
     dt = _dtype_code(logits)
     ps = _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
                      bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32)
-    out, po = _out_arg(logits, out, torch)
+    out, po = _out_arg(logits, out, stream)
     _launch(logits.get_device(), stream, lib().spec_logits_process, "spec_logits_process", logits.data_ptr(),
             ctypes.byref(rw), ctypes.byref(ps), logits.shape[1], dt, po)
     return out
@@ -769,7 +786,7 @@ def spec_logits_truncate(logits, temperature, offsets, *, rows="target", top_k=N
     rw = _rows_arg(logits, offsets, rows, None, None, torch.int32)
     dt = _dtype_code(logits)
     tr = _truncate_arg(logits.get_device(), rw.B, temperature, top_k, top_p, min_p, torch.int32, torch.float32)
-    out, po = _out_arg(logits, out, torch)
+    out, po = _out_arg(logits, out, stream)
     _launch(logits.get_device(), stream, lib().spec_logits_truncate, "spec_logits_truncate", logits.data_ptr(),
             ctypes.byref(rw), ctypes.byref(tr), logits.shape[1], dt, po)
     return out
@@ -788,7 +805,7 @@ def spec_logits_process_truncate(logits, temperature, offsets, draft_tokens=None
     ps = _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, presence, counts, seen, slots,
                      bias_offsets, bias_tokens, bias_values, mask, mask_rows, i32, f32)
     tr = _truncate_arg(logits.get_device(), rw.B, temperature, top_k, top_p, min_p, i32, f32)
-    out, po = _out_arg(logits, out, torch)
+    out, po = _out_arg(logits, out, stream)
     _launch(logits.get_device(), stream, lib().spec_logits_process_truncate, "spec_logits_process_truncate",
             logits.data_ptr(), ctypes.byref(rw), ctypes.byref(ps), ctypes.byref(tr), logits.shape[1], dt, po)
     return out

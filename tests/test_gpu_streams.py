@@ -1,0 +1,66 @@
+"""Calls on a stream other than the current one: the memory of the outputs that
+they make.  It has to be the call's stream's own (a buffer that the current
+stream has freed may still be in use there), and it must not come back from
+the allocator while either stream may still use it."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verification_61_gb300 as m
+    m.lib()
+    return m
+
+
+def outputs(y):
+    return [t for t in (y.values() if isinstance(y, dict) else y if isinstance(y, (tuple, list)) else [y])
+            for t in (t.values() if isinstance(t, dict) else [t])]
+
+
+def logit_calls(sv):
+    R, V = 6, 1 << 18
+    x = torch.randn(R, V, device="cuda")
+    off, T = torch.arange(R + 1, dtype=torch.int32, device="cuda")[:4].contiguous(), torch.ones(3, device="cuda")
+    tok = torch.zeros(3, dtype=torch.int32, device="cuda")
+    k = torch.full((3,), 5, dtype=torch.int32, device="cuda")
+    return {"process": lambda s: sv.spec_logits_process(x, off, tok, stream=s),
+            "truncate": lambda s: sv.spec_logits_truncate(x, T, off, top_k=k, stream=s),
+            "both": lambda s: sv.spec_logits_process_truncate(x, T, off, tok, top_k=k, stream=s)}
+
+
+def check(call):
+    """(The streams are idle wherever memory is taken from one and used on the other.)"""
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in outputs(call(None))]
+    torch.cuda.synchronize()
+    # buffers of the outputs' sizes that the current stream has freed
+    freed = [torch.empty_like(t) for t in want for _ in range(4)]
+    ptrs = {t.untyped_storage().data_ptr() for t in freed}
+    del freed
+    got = outputs(call(side))
+    torch.cuda.synchronize()
+    assert not ptrs & {t.untyped_storage().data_ptr() for t in got}
+    for a, b in zip(got, want):
+        assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) if a.is_floating_point() else torch.equal(a, b)
+    # the current stream reads them for another 20 ms or so: they stay its own until then
+    torch.cuda._sleep(40_000_000)
+    sizes = [t.shape for t in got]
+    types = [t.dtype for t in got]
+    ptrs = {t.untyped_storage().data_ptr() for t in got}
+    del got
+    with torch.cuda.stream(side):
+        again = [torch.empty(s, dtype=d, device="cuda") for s, d in zip(sizes, types)]
+    assert not ptrs & {t.untyped_storage().data_ptr() for t in again}
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["process", "truncate", "both"])
+def test_logit_outputs_on_another_stream(sv, name):
+    check(logit_calls(sv)[name])
