@@ -214,12 +214,12 @@ def spec_verify(target_logits, draft_logits, draft_tokens, u_accept, u_resample,
     R_t = u_resample.numel()
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty(R_t, dtype=torch.int32, device=dev)
+        out_tokens = _new(R_t, torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_num_accepted = _new(B, torch.int32, dev, stream)
     L = lib()
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (_p(workspace), workspace.numel() * workspace.element_size())
-    aux_out, ax = _aux_buffers(B, R_t, draft_tokens.numel(), dev) if aux else (None, None)
+    aux_out, ax = _aux_buffers(B, R_t, draft_tokens.numel(), dev, stream) if aux else (None, None)
     if ax is None and workspace is None:
         rc = L.spec_verify(_p(target_logits), _p(draft_logits), _p(draft_tokens), _p(u_accept),
                            _p(u_resample), _p(temperature), B, _p(k_offsets), V, dt,
@@ -248,7 +248,7 @@ def spec_draft_sample(draft_logits, temperature, u_draft, k_offsets, out_draft_t
     _check_dev("u_draft", u_draft, torch.float32)
     _check_dev("k_offsets", k_offsets, torch.int32)
     if out_draft_tokens is None:
-        out_draft_tokens = torch.empty(u_draft.numel(), dtype=torch.int32, device=draft_logits.device)
+        out_draft_tokens = _new(u_draft.numel(), torch.int32, draft_logits.device, stream)
     L = lib()
     if workspace is None:
         rc = L.spec_draft_sample(_p(draft_logits), _p(temperature), _p(u_draft), B, _p(k_offsets), V,
@@ -261,12 +261,12 @@ def spec_draft_sample(draft_logits, temperature, u_draft, k_offsets, out_draft_t
     return out_draft_tokens
 
 
-def _aux_buffers(B, R_t, R_d, dev):
+def _aux_buffers(B, R_t, R_d, dev, stream):
     import torch
-    out = dict(accept_prob=torch.full((R_d,), float("nan"), device=dev),
-               residual_mass=torch.full((B,), float("nan"), device=dev),
-               lse_target=torch.full((R_t,), float("nan"), device=dev),
-               lse_draft=torch.full((R_d,), float("nan"), device=dev))
+    out = dict(accept_prob=_new((R_d,), torch.float32, dev, stream, float("nan")),
+               residual_mass=_new((B,), torch.float32, dev, stream, float("nan")),
+               lse_target=_new((R_t,), torch.float32, dev, stream, float("nan")),
+               lse_draft=_new((R_d,), torch.float32, dev, stream, float("nan")))
     ax = _Aux(*(ctypes.c_void_p(out[k].data_ptr()) for k in
                 ("accept_prob", "residual_mass", "lse_target", "lse_draft")))
     return out, ax
@@ -288,9 +288,9 @@ def spec_draft_sample_lse(draft_logits, temperature, u_draft, k_offsets, out_dra
     R_d = u_draft.numel()
     dev = draft_logits.device
     if out_draft_tokens is None:
-        out_draft_tokens = torch.empty(R_d, dtype=torch.int32, device=dev)
+        out_draft_tokens = _new(R_d, torch.int32, dev, stream)
     if out_draft_lse2 is None:
-        out_draft_lse2 = torch.empty(max(R_d, 1), dtype=torch.float64, device=dev)
+        out_draft_lse2 = _new(max(R_d, 1), torch.float64, dev, stream)
     _check_dev("out_draft_lse2", out_draft_lse2, torch.float64)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (_p(workspace), workspace.numel() * workspace.element_size())
     rc = lib().spec_draft_sample_lse(_p(draft_logits), _p(temperature), _p(u_draft), B, _p(k_offsets), V, dt,
@@ -322,10 +322,10 @@ def spec_verify_lse(target_logits, draft_logits, draft_lse2, draft_tokens, u_acc
     R_t, R_d = u_resample.numel(), draft_tokens.numel()
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty(R_t, dtype=torch.int32, device=dev)
+        out_tokens = _new(R_t, torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
-    aux_out, ax = _aux_buffers(B, R_t, R_d, dev) if aux else (None, None)
+        out_num_accepted = _new(B, torch.int32, dev, stream)
+    aux_out, ax = _aux_buffers(B, R_t, R_d, dev, stream) if aux else (None, None)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (_p(workspace), workspace.numel() * workspace.element_size())
     rc = lib().spec_verify_lse(_p(target_logits), _p(draft_logits), _p(draft_lse2), _p(draft_tokens),
                                _p(u_accept), _p(u_resample), _p(temperature), B, _p(k_offsets), V, dt,
@@ -358,11 +358,11 @@ def spec_round(target_logits, draft_logits, u_draft, u_accept, u_resample, tempe
     R_t, R_d = u_resample.numel(), u_accept.numel()
     dev = target_logits.device
     if out_draft_tokens is None:
-        out_draft_tokens = torch.empty(R_d, dtype=torch.int32, device=dev)
+        out_draft_tokens = _new(R_d, torch.int32, dev, stream)
     if out_tokens is None:
-        out_tokens = torch.empty(R_t, dtype=torch.int32, device=dev)
+        out_tokens = _new(R_t, torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_num_accepted = _new(B, torch.int32, dev, stream)
     rc = lib().spec_round(_p(target_logits), _p(draft_logits), _p(u_draft), _p(u_accept), _p(u_resample),
                           _p(temperature), B, _p(k_offsets), V, dt, _p(out_draft_tokens), _p(out_tokens),
                           _p(out_num_accepted), _stream(stream))
@@ -391,11 +391,11 @@ def spec_tree_verify(target_logits, draft_logits, node_offsets, parent, tokens, 
         raise ValueError("node_offsets must have B + 1 entries")
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty(N, dtype=torch.int32, device=dev)
+        out_tokens = _new(N, torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_num_accepted = _new(B, torch.int32, dev, stream)
     if out_last_node is None:
-        out_last_node = torch.empty(B, dtype=torch.int32, device=dev)
+        out_last_node = _new(B, torch.int32, dev, stream)
     rc = lib().spec_tree_verify(_p(target_logits), _p(draft_logits), _p(node_offsets), _p(parent), _p(tokens),
                                 _p(u_accept), _p(u_resample), _p(temperature), B, N, V, dt, _p(out_tokens),
                                 _p(out_num_accepted), _p(out_last_node), _stream(stream))
@@ -418,7 +418,7 @@ def spec_tree_draft_sample(draft_logits, node_offsets, parent, temperature, u_dr
     _check_dev("temperature", temperature, torch.float32)
     _check_dev("u_draft", u_draft, torch.float32)
     if out_tokens is None:
-        out_tokens = torch.empty(N, dtype=torch.int32, device=draft_logits.device)
+        out_tokens = _new(N, torch.int32, draft_logits.device, stream)
     rc = lib().spec_tree_draft_sample(_p(draft_logits), _p(node_offsets), _p(parent), _p(temperature), _p(u_draft),
                                       B, N, V, dt, _p(out_tokens), _stream(stream))
     _raise(rc, "spec_tree_draft_sample")
@@ -496,7 +496,7 @@ def spec_shard_stats(target_shard, draft_shard, draft_tokens, temperature, k_off
     _check_dev("k_offsets", k_offsets, torch.int32)
     rows = target_shard.shape[0] + draft_shard.shape[0]
     if out_stats is None:
-        out_stats = torch.empty((rows, 4), dtype=torch.int32, device=target_shard.device)
+        out_stats = _new((rows, 4), torch.int32, target_shard.device, stream)
     bounds, G = _bounds(shard_bounds)
     wp, wb = _ws_args(workspace)
     rc = lib().spec_shard_stats(_p(target_shard), _p(draft_shard), _p(draft_tokens), _p(temperature), B,
@@ -525,11 +525,11 @@ def spec_shard_decide(target_shard, draft_shard, all_stats, draft_tokens, u_acce
         _check_dev(name, t, torch.float32)
     dev = target_shard.device
     if out_tokens is None:
-        out_tokens = torch.empty(R_t, dtype=torch.int32, device=dev)
+        out_tokens = _new(R_t, torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_num_accepted = _new(B, torch.int32, dev, stream)
     if out_mass is None:
-        out_mass = torch.empty((B, 2), dtype=torch.float64, device=dev)
+        out_mass = _new((B, 2), torch.float64, dev, stream)
     wp, wb = _ws_args(workspace)
     rc = lib().spec_shard_decide(_p(target_shard), _p(draft_shard), _p(all_stats), _p(draft_tokens), _p(u_accept),
                                  _p(temperature), B, _p(k_offsets), bounds, G, rank, dt, _p(out_tokens),
@@ -618,9 +618,9 @@ def spec_verify_noalloc(target_logits, draft_logits, draft_tokens, u_accept, u_r
     R_t = u_resample.numel()
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty(R_t, dtype=torch.int32, device=dev)
+        out_tokens = _new(R_t, torch.int32, dev, stream)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_num_accepted = _new(B, torch.int32, dev, stream)
     _check_dev("out_tokens", out_tokens, torch.int32)
     _check_dev("out_num_accepted", out_num_accepted, torch.int32)
     if out_tokens.numel() < R_t or out_num_accepted.numel() < B:
@@ -643,8 +643,8 @@ class AdaptiveK:
         if nbytes == 0:
             raise SpecError(-1, "spec_adapt_state_bytes")
         self.B, self.min_k, self.max_k = B, min_k, max_k
-        self.state = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        self.k_offsets = torch.empty(B + 1, dtype=torch.int32, device=device)
+        self.state = _new(nbytes, torch.uint8, device, stream)
+        self.k_offsets = _new(B + 1, torch.int32, device, stream)
         _raise(lib().spec_adapt_init(_p(self.state), B, min_k, max_k, _p(self.k_offsets), _stream(stream)),
                "spec_adapt_init")
 

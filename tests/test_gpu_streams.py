@@ -64,3 +64,45 @@ def check(call):
 @pytest.mark.parametrize("name", ["process", "truncate", "both"])
 def test_logit_outputs_on_another_stream(sv, name):
     check(logit_calls(sv)[name])
+
+
+def verify_calls(sv):
+    import workloads
+    w = workloads.make_config(1)
+    t = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    tl, dl, ua, ur, ud, T, ko = (t(a) for a in (w.target_logits, w.draft_logits, w.u_accept, w.u_resample, w.u_draft, w.temperature, w.k_offsets))
+    tok, lse = sv.spec_draft_sample_lse(dl, T, ud, ko)
+    n = dl.shape[0]
+    # a chain of the draft rows as one tree
+    node_off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    parent = torch.arange(-1, n - 1, dtype=torch.int32, device="cuda")
+    one, ui = T[:1].clamp(min=0.5), ua.clone()
+    B, V = T.numel(), tl.shape[1]
+    bounds = [0, V]
+    ws = sv.shard_workspace(B, V, 0)
+    stats = sv.spec_shard_stats(tl, dl, tok, T, ko, bounds, 0, ws)
+
+    def adapt(s):
+        a = sv.AdaptiveK(B, 1, 4, stream=s)
+        return a.k_offsets, a.state
+
+    return {"draft": lambda s: sv.spec_draft_sample(dl, T, ud, ko, stream=s),
+            "draft_lse": lambda s: sv.spec_draft_sample_lse(dl, T, ud, ko, stream=s),
+            "verify": lambda s: sv.spec_verify(tl, dl, tok, ua, ur, T, ko, stream=s),
+            "verify_aux": lambda s: sv.spec_verify(tl, dl, tok, ua, ur, T, ko, aux=True, stream=s),
+            "verify_lse": lambda s: sv.spec_verify_lse(tl, dl, lse, tok, ua, ur, T, ko, aux=True, stream=s),
+            "verify_noalloc": lambda s: sv.spec_verify_noalloc(tl, dl, tok, ua, ur, T, ko, stream=s),
+            "round": lambda s: sv.spec_round(tl, dl, ud, ua, ur, T, ko, stream=s),
+            "tree_draft": lambda s: sv.spec_tree_draft_sample(dl, node_off, parent, one, ui, stream=s),
+            "tree_verify": lambda s: sv.spec_tree_verify(tl[:n].contiguous(), dl, node_off, parent, tok, ui, ui, one, stream=s),
+            "shard_stats": lambda s: sv.spec_shard_stats(tl, dl, tok, T, ko, bounds, 0, ws, stream=s),
+            "shard_decide": lambda s: sv.spec_shard_decide(tl, dl, stats, tok, ua, T, ko, bounds, 0, ws, stream=s),
+            "adapt": adapt}
+
+
+@pytest.mark.parametrize("name", ["draft", "draft_lse", "verify", "verify_aux", "verify_lse", "verify_noalloc", "round", "tree_draft",
+                                  "tree_verify", "shard_stats", "shard_decide", "adapt"])
+def test_outputs_on_another_stream(sv, name):
+    call = verify_calls(sv)[name]
+    torch.cuda.synchronize()  # the inputs are there
+    check(call)
