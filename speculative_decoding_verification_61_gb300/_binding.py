@@ -742,7 +742,8 @@ def _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, p
         M = mask.shape[0]
         if mask_rows is None and M < R:
             raise ValueError("mask needs a row for each row of logits, or mask_rows")
-        masks = _ptr(mask, "mask", i32, dev, M * W), _ptr(mask_rows, "mask_rows", i32, dev, R), M
+        pm, pr = _ptr(mask, "mask", i32, dev, M * W), _ptr(mask_rows, "mask_rows", i32, dev, R)
+        masks = pm or pr, pr, M  # (no mask to name: an address that is not read)
     elif mask_rows is not None:
         raise ValueError("mask_rows without mask")
     return _Logits(*pen, *bias, *masks)

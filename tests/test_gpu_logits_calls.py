@@ -79,3 +79,37 @@ def test_padded_buffers(sv, mode, in_place):
     sv.spec_logits_process(x, dev(off), dev(tokens), rows=mode, parent=None if parent is None else dev(parent), out=out,
                            **{k: dev(v) for k, v in p.items()})
     assert np.array_equal(host(out), np.concatenate([want[:n], z[n:]]))
+
+
+# ----------------------------------------------------------------- empty arguments
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_pool_without_masks(sv, dtype, in_place):
+    """No grammar is in use: M = 0 and every row names none.  A row that names one is NaN."""
+    rng = np.random.default_rng(2)
+    V, off = 264, i32([0, 2, 3])
+    z = rng.standard_normal((5, V)).astype(f32)
+    z = ref.to_bf16(z) if dtype == "bf16" else z
+    pool = torch.zeros((0, (V + 31) // 32), dtype=torch.int32, device="cuda")
+    bias = dict(bias_offsets=dev(i32([0, 0, 1])), bias_tokens=dev(i32([7])), bias_values=dev(f32([2.0])))
+    want = z.copy()
+    want[3:, 7] += 2
+    want = ref.to_bf16(want) if dtype == "bf16" else want
+    for names in ([-1] * 5, [-1, 0, -1, -1, -1]):
+        x = dev(z, dtype)
+        y = host(sv.spec_logits_process(x, dev(off), dev(i32([1, 2, 3])), mask=pool, mask_rows=dev(i32(names)), out=x if in_place else None, **bias))
+        none = np.array(names) == -1
+        assert np.array_equal(y[none], want[none]) and np.isnan(y[~none]).all()
+
+
+def test_empty_lists(sv):
+    """Lists without entries are as no lists: biases, drafted tokens, prompts."""
+    V = 1032
+    x = torch.randn(2, V, device="cuda")
+    off, none, zero = dev(i32([0, 0, 0])), torch.zeros(0, dtype=torch.int32, device="cuda"), dev(i32([0, 0, 0]))
+    st = sv.PenaltyState(2, V)
+    st.reset(dev(i32([0, 1])), zero, none, zero, none)
+    assert not st.counts.any() and not st.seen.any()
+    y = sv.spec_logits_process(x, off, none, counts=st.counts, seen=st.seen, bias_offsets=zero, bias_tokens=none,
+                               bias_values=torch.zeros(0, device="cuda"))
+    assert torch.equal(x, y)
