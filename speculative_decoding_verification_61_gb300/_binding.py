@@ -673,6 +673,13 @@ def _ptr(t, name, dtype, dev, n=-1):
     return t.data_ptr()
 
 
+def _size(n, name):
+    """A number of entries, which the C ABI takes as an int."""
+    if n > 0x7fffffff:
+        raise ValueError(f"{name} has {n} entries, more than 2147483647")
+    return n
+
+
 def _launch(dev, stream, fn, what, *args):
     """Calls fn(*args, stream) with device `dev` current, on its current stream if none is given."""
     import torch
@@ -695,10 +702,11 @@ def _rows_arg(logits, offsets, rows, draft_tokens, parent, i32):
     if not logits.is_cuda or not logits.is_contiguous():
         _check_dev("logits", logits)
     dev = logits.get_device()
-    R, B = logits.shape[0], offsets.numel() - 1
+    R, B = _size(logits.shape[0], "logits"), _size(offsets.numel() - 1, "offsets")
+    _size(logits.shape[1], "a row")
     if B < 0:
         raise ValueError("offsets must have B + 1 entries")
-    n_tokens = 0 if draft_tokens is None else draft_tokens.numel()
+    n_tokens = 0 if draft_tokens is None else _size(draft_tokens.numel(), "draft_tokens")
     if mode == 3 and parent is not None:
         if parent.numel() > R:
             raise ValueError("parent has more nodes than logits has rows")
@@ -724,7 +732,7 @@ def _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, p
             raise ValueError("penalties need counts, seen and draft_tokens")
         if rows == "tree" and parent is None:
             raise ValueError("penalties on a tree need parent")
-        S = counts.shape[0]
+        S = _size(counts.shape[0], "counts")
         pen = (_ptr(repetition, "repetition", f32, dev, B), _ptr(frequency, "frequency", f32, dev, B),
                _ptr(presence, "presence", f32, dev, B), _ptr(counts, "counts", i32, dev, S * V),
                _ptr(seen, "seen", i32, dev, S * 2 * W), _ptr(slots, "slots", i32, dev, B), S)
@@ -733,13 +741,13 @@ def _logits_arg(logits, rw, rows, draft_tokens, parent, repetition, frequency, p
     if bias_offsets is not None:
         if bias_tokens is None or bias_values is None:
             raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
-        n = bias_tokens.numel()
+        n = _size(bias_tokens.numel(), "bias_tokens")
         bias = (_ptr(bias_offsets, "bias_offsets", i32, dev, B + 1), _ptr(bias_tokens, "bias_tokens", i32, dev),
                 _ptr(bias_values, "bias_values", f32, dev, n), n)
     elif not (bias_tokens is None and bias_values is None):
         raise ValueError("biases need bias_offsets, bias_tokens and bias_values")
     if mask is not None:
-        M = mask.shape[0]
+        M = _size(mask.shape[0], "mask")
         if mask_rows is None and M < R:
             raise ValueError("mask needs a row for each row of logits, or mask_rows")
         pm, pr = _ptr(mask, "mask", i32, dev, M * W), _ptr(mask_rows, "mask_rows", i32, dev, R)
@@ -815,7 +823,7 @@ def spec_logits_process_truncate(logits, temperature, offsets, draft_tokens=None
 def _state_arg(counts, seen, i32):
     if counts.dim() != 2:
         raise ValueError("counts must be [S, V]")
-    S, V = counts.shape
+    S, V = _size(counts.shape[0], "counts"), _size(counts.shape[1], "a row")
     if not counts.is_cuda:
         _check_dev("counts", counts)
     dev = counts.get_device()
@@ -830,14 +838,14 @@ def spec_penalty_reset(counts, seen, slots, prompt_offsets=None, prompt_tokens=N
     import torch
     i32 = torch.int32
     S, V, dev, pc, ps = _state_arg(counts, seen, i32)
-    n = slots.numel()
+    n = _size(slots.numel(), "slots")
     if (prompt_offsets is None) != (prompt_tokens is None) or (output_offsets is None) != (output_tokens is None):
         raise ValueError("offsets and tokens go together")
     _launch(dev, stream, lib().spec_penalty_reset, "spec_penalty_reset", pc, ps, S, V, _ptr(slots, "slots", i32, dev), n,
             _ptr(prompt_offsets, "prompt_offsets", i32, dev, n + 1), _ptr(prompt_tokens, "prompt_tokens", i32, dev),
-            0 if prompt_tokens is None else prompt_tokens.numel(),
+            0 if prompt_tokens is None else _size(prompt_tokens.numel(), "prompt_tokens"),
             _ptr(output_offsets, "output_offsets", i32, dev, n + 1), _ptr(output_tokens, "output_tokens", i32, dev),
-            0 if output_tokens is None else output_tokens.numel())
+            0 if output_tokens is None else _size(output_tokens.numel(), "output_tokens"))
     return counts, seen
 
 
@@ -851,10 +859,10 @@ def spec_penalty_update(counts, seen, out_tokens, out_num_accepted, offsets, *, 
     S, V, dev, pc, ps = _state_arg(counts, seen, i32)
     if rows not in ("target", "tree"):
         raise ValueError(f"rows must be 'target' or 'tree', got {rows!r}")
-    B = offsets.numel() - 1
+    B = _size(offsets.numel() - 1, "offsets")
     if B < 0:
         raise ValueError("offsets must have B + 1 entries")
-    rw = _Rows(ROWS[rows], B, out_tokens.numel(), _ptr(offsets, "offsets", i32, dev), None, None, 0)
+    rw = _Rows(ROWS[rows], B, _size(out_tokens.numel(), "out_tokens"), _ptr(offsets, "offsets", i32, dev), None, None, 0)
     _launch(dev, stream, lib().spec_penalty_update, "spec_penalty_update", pc, ps, S, V,
             _ptr(slots, "slots", i32, dev, B), ctypes.byref(rw), _ptr(out_tokens, "out_tokens", i32, dev),
             _ptr(out_num_accepted, "out_num_accepted", i32, dev, B))

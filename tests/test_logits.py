@@ -176,3 +176,62 @@ def test_binding_refusals(sv):
     with pytest.raises(ValueError, match="CUDA"):
         sv.PenaltyState(2, 16, device="cpu").reset(off)
     assert sv.ROWS == {"target": 0, "draft": 1, "next": 2, "tree": 3}
+
+
+class Sized:
+    """A tensor of a given size as the binding's checks see one, without its memory."""
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype, self.is_cuda = shape, dtype, True
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return int(np.prod(self.shape, dtype=np.int64))
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return FAKE
+
+
+def test_binding_refuses_counts_past_31_bits(sv):
+    """What the C ABI takes as an int: a larger number would arrive as another one."""
+    torch = pytest.importorskip("torch")
+    from speculative_decoding_verification_61_gb300 import _binding as bd
+    i32, fl = torch.int32, torch.float32
+    most = (1 << 31) - 1
+    off, z = Sized((3,), i32), Sized((4, 8), fl)
+    for n in (most + 1, 1 << 32, (1 << 32) + 4):
+        with pytest.raises(ValueError, match="2147483647"):
+            bd._rows_arg(Sized((n, 8), fl), off, "target", None, None, i32)
+        with pytest.raises(ValueError, match="2147483647"):
+            bd._rows_arg(Sized((4, n), fl), off, "target", None, None, i32)
+        with pytest.raises(ValueError, match="2147483647"):
+            bd._state_arg(Sized((2, n), i32), Sized((2, 2, 1), i32), i32)
+        with pytest.raises(ValueError, match="2147483647"):
+            bd._rows_arg(z, off, "target", Sized((n,), i32), None, i32)
+        rw = bd._rows_arg(z, off, "target", Sized((2,), i32), None, i32)
+        lists = dict.fromkeys(("repetition", "frequency", "presence", "counts", "seen", "slots", "bias_offsets", "bias_tokens",
+                               "bias_values", "mask", "mask_rows"))
+        for big in (dict(counts=Sized((n, 8), i32), seen=Sized((n, 2, 1), i32)),
+                    dict(bias_offsets=off, bias_tokens=Sized((n,), i32), bias_values=Sized((n,), fl)),
+                    dict(mask=Sized((n, 1), i32), mask_rows=Sized((4,), i32))):
+            with pytest.raises(ValueError, match="2147483647"):
+                bd._logits_arg(z, rw, "target", Sized((2,), i32), None, **{**lists, **big}, i32=i32, f32=fl)
+        with pytest.raises(ValueError, match="2147483647"):
+            bd._state_arg(Sized((n, 8), i32), Sized((n, 2, 1), i32), i32)
+        st = Sized((2, 8), i32), Sized((2, 2, 1), i32)
+        for a, k in ((dict(slots=Sized((2,), i32), prompt_offsets=off, prompt_tokens=Sized((n,), i32)), "prompt_tokens"),
+                     (dict(slots=Sized((2,), i32), output_offsets=off, output_tokens=Sized((n,), i32)), "output_tokens")):
+            with pytest.raises(ValueError, match=f"{k}.*2147483647"):
+                sv.spec_penalty_reset(*st, **a)
+        with pytest.raises(ValueError, match="2147483647"):
+            sv.spec_penalty_update(*st, Sized((n,), i32), Sized((2,), i32), off)
+    rw = bd._rows_arg(Sized((most, 8), fl), off, "target", Sized((most,), i32), None, i32)
+    assert rw.R == most and rw.n_tokens == most
