@@ -321,12 +321,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
             }
         }
     }
-    for (int e = e0 + me; e < e1; e += G::kSize) {
+    for (uint32_t e = e0 + me; e < static_cast<uint32_t>(e1); e += G::kSize) {  // (the step behind the last may pass 31 bits)
         const int t = __ldg(ps.bias_tokens + e);
         const bool in = t >= 0 && t < V;
         const float v = __ldg(ps.bias_values + e);
         bad |= !in || !(v < __int_as_float(0x7f800000));  // NaN and +inf
-        if (e - e0 < kBias) {
+        if (static_cast<int>(e - e0) < kBias) {
             sm.bias_token[e - e0] = t;
             sm.bias_value[e - e0] = v;
         }
@@ -509,8 +509,9 @@ __global__ void __launch_bounds__(kResetThreads)
     for (int i = tid; i < kResetChunk / 32; i += kResetThreads) s_prompt[i] = 0;
     if (__syncthreads_or(skip)) return;
     // every chunk's CTA reads the whole lists (from L2), several tokens in flight a thread
-    auto each = [&](const int32_t *tokens, int first, int end, auto &&f) {
-        for (int i = first + tid; i < end; i += kResetThreads * kResetAhead) {
+    // (unsigned: the step behind the last may pass 31 bits)
+    auto each = [&](const int32_t *tokens, uint32_t first, uint32_t end, auto &&f) {
+        for (uint32_t i = first + tid; i < end; i += kResetThreads * kResetAhead) {
             int t[kResetAhead];
 #pragma unroll
             for (int u = 0; u < kResetAhead; ++u) t[u] = i + u * kResetThreads < end ? __ldg(tokens + i + u * kResetThreads) : -1;

@@ -113,3 +113,31 @@ def test_empty_lists(sv):
     y = sv.spec_logits_process(x, off, none, counts=st.counts, seen=st.seen, bias_offsets=zero, bias_tokens=none,
                                bias_values=torch.zeros(0, device="cuda"))
     assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------- the longest lists
+def test_lists_that_end_at_31_bits(sv):
+    """Lists of 2^31 - 1 entries, of which the last few hundred are a sequence's: no index passes 31 bits."""
+    n, V = (1 << 31) - 1, 4104
+    rng = np.random.default_rng(5)
+    tail = rng.integers(0, V, 700).astype(i32)
+    tokens = torch.zeros(n, dtype=torch.int32, device="cuda")
+    tokens[-700:] = dev(tail)
+    st = sv.PenaltyState(2, V)
+    off = dev(np.array([n - 700, n], i32))
+    st.reset(dev(i32([1])), off, tokens, off, tokens)
+    counts = np.bincount(tail, minlength=V).astype(i32)
+    assert np.array_equal(st.counts.cpu().numpy(), np.stack([np.zeros(V, i32), counts]))
+    words = ref.pack(np.stack([counts > 0, counts > 0]))
+    assert np.array_equal(st.seen.cpu().numpy()[1], words) and not st.seen[0].any()
+    values = torch.zeros(n, device="cuda")
+    v = rng.choice(f32([1, -2, 0.25]), 700)
+    values[-700:] = dev(v)
+    z = rng.standard_normal((1, V)).astype(f32)
+    want, _, _ = ref.process(z, ref.Rows("next", i32([0, 0]), np.zeros(0, i32)),
+                             dict(bias_offsets=i32([0, 700]), bias_tokens=tail, bias_values=v), ref.F32)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    x = dev(z)
+    for out in (None, x):
+        y = sv.spec_logits_process(x, dev(i32([0, 0])), none, rows="next", bias_offsets=off, bias_tokens=tokens, bias_values=values, out=out)
+        assert np.array_equal(host(y), want)
