@@ -539,7 +539,9 @@ typedef struct {
  *   bias_offsets int32 [B+1]     sequence b has the entries bias_offsets[b] ..
  *                                bias_offsets[b+1] - 1 of bias_tokens and
  *                                bias_values [n_bias]; NULL: no biases.  Values
- *                                are finite or -inf.
+ *                                are finite or -inf.  Lists are for few tokens: one
+ *                                is read once per 4096 columns, and again per 256
+ *                                of them that are touched.
  *   mask         int32 [M, W]    bit arrays, a set bit allows the token; NULL: none
  *   mask_rows    int32 [R]       the mask of each row, -1: none; NULL: row r has
  *                                mask r (then M >= R)

@@ -86,10 +86,13 @@ struct GroupShared {
     int token[kMaxPath];
     int up[kMaxPath];           // tree: parent within the sequence
     uint64_t before[kMaxPath];  // tree: the nodes whose tokens a row follows
+    // by word of the unit; once a thread has read its own, with biases: the touched columns, and how many
+    // of them are listed before the word's
     uint32_t drafted[Group<STREAM>::kWords], biased[Group<STREAM>::kWords];
     int warp_sum[kWarps];
     int column[kList];
     uint8_t flags[kList];
+    float bias[kList];
     int bias_token[kBias];
     float bias_value[kBias];
 };
@@ -219,12 +222,60 @@ __device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0,
         }
 }
 
+// The entries of a bias list (all valid) added up per listed column, in list order,
+// for the `len` columns listed from number `base` on: a warp takes a share of the
+// columns and goes through the list once, the entries of one token by turns.  Where
+// each column searches the whole list instead, its cost is the square of its length:
+// lists of 300 cost 51 us beside the 45 of 384 rows of 128256, now 18; one of every token
+// 265 ms a row, now 13; lists of 32 and 64 the same.
+template <bool STREAM>
+__device__ __forceinline__ void add_biases(GroupShared<STREAM> &sm, const Units &un, const int32_t *tokens, const float *values, uint32_t n,
+                                           int base, int len) {
+    using G = Group<STREAM>;
+    constexpr int kShare = kList / (G::kSize / 32), kAhead = STREAM ? 8 : 4;
+    const int me = G::thread(), lane = threadIdx.x & 31;
+    for (int e = me; e < len; e += G::kSize) sm.bias[e] = -0.0f;  // (leaves every value as it is)
+    G::sync();
+#pragma unroll 1
+    for (uint32_t x0 = 0; x0 < n; x0 += 32 * kAhead) {
+        int t[kAhead], to[kAhead], most = -1;  // the entries' tokens, their places among the warp's columns
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const uint32_t x = x0 + u * 32 + lane;
+            t[u] = x < n ? *(x < kBias ? sm.bias_token + x : tokens + x) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            to[u] = -1;
+            if (t[u] >= 0) {
+                const int d = G::place(un, t[u] >> 5);
+                if (d >= 0) to[u] = static_cast<int>(sm.biased[d] + __popc(sm.drafted[d] & ((1u << (t[u] & 31)) - 1))) - base;
+                if (to[u] < 0 || to[u] >= len || to[u] / kShare != me >> 5) to[u] = -1;
+            }
+            most = max(most, to[u]);
+        }
+        if (!__any_sync(0xffffffffu, most >= 0)) continue;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (!__any_sync(0xffffffffu, to[u] >= 0)) continue;
+            const uint32_t x = x0 + u * 32 + lane;
+            float v = 0.0f;
+            if (to[u] >= 0) v = x < kBias ? sm.bias_value[x] : __ldg(values + x);
+            const int turn = __popc(__match_any_sync(0xffffffffu, to[u]) & ((1u << lane) - 1));
+            for (int i = 0; __any_sync(0xffffffffu, to[u] >= 0 && turn >= i); ++i) {
+                if (to[u] >= 0 && turn == i) sm.bias[to[u]] = __fadd_rn(sm.bias[to[u]], v);
+                __syncwarp();
+            }
+        }
+    }
+}
+
 // A group takes one unit of one sequence's columns, for all its rows or an even
 // part of them, so that what depends on the sequence and the columns alone
 // (its seen tokens, their counts, its biases) is read once.  CTAs in the order
 // (sequence, unit): the ones that run at a time stream through one window of
 // memory.
-template <int DT, bool STREAM>
+template <int DT, bool STREAM, bool BIAS>
 __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
     process_kernel(const char *logits, char *out, Rows rw, Process ps, int V, int units, int piece, int parts) {
     using G = Group<STREAM>;
@@ -285,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
         }
     }
     int e0 = 0, e1 = 0;
-    if (ps.bias_offsets) {
+    if (BIAS) {
         e0 = __ldg(ps.bias_offsets + b), e1 = __ldg(ps.bias_offsets + b + 1);
         if (e0 < 0 || e1 < e0 || e1 > ps.n_bias) {
             bad = true;
@@ -340,13 +391,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
     } else {
         uint32_t touched[G::kWordsEach], drafted[G::kWordsEach], biased[G::kWordsEach];
         int rank = 0;
+        uint32_t any_biased = 0;
 #pragma unroll
         for (int i = 0; i < G::kWordsEach; ++i) {
             const int word = G::word(un, i * G::kSize + me);
             // bits behind the vocabulary say nothing
             const uint32_t in_v = word >= W ? 0u : word == W - 1 && (V & 31) ? (1u << (V & 31)) - 1 : 0xffffffffu;
             drafted[i] = sm.drafted[i * G::kSize + me];
-            biased[i] = sm.biased[i * G::kSize + me];
+            biased[i] = BIAS ? sm.biased[i * G::kSize + me] : 0;
+            any_biased |= biased[i];
             touched[i] = (prompt[i] | emitted[i] | drafted[i] | biased[i]) & in_v;
             rank += __popc(touched[i]);
         }
@@ -358,13 +411,26 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
         }
         int listed = __shfl_sync(0xffffffffu, rank, 31);
         rank -= own;
+        constexpr int kBiasedBit = 1 << 16;  // (at most 4096 columns are listed)
+        if (BIAS && __any_sync(0xffffffffu, any_biased != 0)) listed += kBiasedBit;
         if (STREAM) {
             if (lane == 0) sm.warp_sum[threadIdx.x >> 5] = listed;
             __syncthreads();
             listed = 0;
             for (int i = 0; i < kWarps; ++i) {
-                if (i == static_cast<int>(threadIdx.x >> 5)) rank += listed;
+                if (i == static_cast<int>(threadIdx.x >> 5)) rank += listed & (kBiasedBit - 1);
                 listed += sm.warp_sum[i];
+            }
+        }
+        const bool has_biased = BIAS && listed >= kBiasedBit;
+        listed &= kBiasedBit - 1;
+        if (has_biased) {
+            int at = rank;
+#pragma unroll
+            for (int i = 0; i < G::kWordsEach; ++i) {
+                sm.drafted[i * G::kSize + me] = touched[i];
+                sm.biased[i * G::kSize + me] = at;
+                at += __popc(touched[i]);
             }
         }
         if (listed && tree && pen) {
@@ -403,23 +469,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
                 }
                 at += n_i;
             }
+            if (has_biased) add_biases<STREAM>(sm, un, ps.bias_tokens + e0, ps.bias_values + e0, e1 - e0, base, len);
             G::sync();
             // a thread takes a column, all its rows
             for (int e = me; e < len; e += G::kSize) {
                 const int col = sm.column[e];
                 const uint32_t f = sm.flags[e];
                 const int count = f & kEmitted ? __ldg(ps.counts + slot * V + col) : 0;
-                float bias = 0.0f;
-                if (f & kBiased) {
-                    // the same token twice: the entries add, in list order
-                    bool any = false;
-                    for (int x = 0; x < e1 - e0; ++x) {
-                        if ((x < kBias ? sm.bias_token[x] : __ldg(ps.bias_tokens + e0 + x)) != col) continue;
-                        const float v = x < kBias ? sm.bias_value[x] : __ldg(ps.bias_values + e0 + x);
-                        bias = any ? __fadd_rn(bias, v) : v;
-                        any = true;
-                    }
-                }
+                const float bias = BIAS && f & kBiased ? sm.bias[e] : 0.0f;
                 constexpr int kRows = 4;  // in flight
                 for (int i = i0; i < i1; i += kRows) {
                     float z[kRows];
@@ -444,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
                             for (uint64_t d = before; d; d &= d - 1) c += sm.token[__ffsll(d) - 1] == col;
                         }
                         if ((f & kPrompt) || c > 0) z[u] = penalised(z[u], c, p);
-                        if (f & kBiased) z[u] = __fadd_rn(z[u], bias);
+                        if (BIAS && f & kBiased) z[u] = __fadd_rn(z[u], bias);
                         store_logit<DT>(out + static_cast<int64_t>(row0 + i + u) * row_bytes, col, z[u]);
                     }
                 }
@@ -568,7 +625,8 @@ int launch_process(const void *logits, void *out, const Rows &rw, const Process 
     const int64_t room = static_cast<int64_t>(sms) * kPerSm<STREAM> * G::kCount, each = std::min<int64_t>(rw.R / rw.B, most);
     const int parts = static_cast<int>(std::max<int64_t>({1, std::min(room / pairs, each), each / 8}));
     const int64_t ctas = (pairs * parts + G::kCount - 1) / G::kCount;
-    process_kernel<DT, STREAM><<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(
+    const auto kernel = ps.bias_offsets ? process_kernel<DT, STREAM, true> : process_kernel<DT, STREAM, false>;
+    kernel<<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(
         static_cast<const char *>(logits), static_cast<char *>(out), rw, ps, V, units, piece, parts);
     return specv::cuda_ok(cudaGetLastError(), "launch process_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -141,3 +141,37 @@ def test_lists_that_end_at_31_bits(sv):
     for out in (None, x):
         y = sv.spec_logits_process(x, dev(i32([0, 0])), none, rows="next", bias_offsets=off, bias_tokens=tokens, bias_values=values, out=out)
         assert np.array_equal(host(y), want)
+
+
+# ---------------------------------------------------------------------- long lists
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype,V", [("bf16", 4104), ("fp32", 32000), ("bf16", 128256)])
+@pytest.mark.parametrize("what", ["every", "one", "twice", "blocks"])
+def test_long_bias_lists(sv, what, dtype, V, in_place):
+    """A bias on every token, thousands for one token, tokens named twice anywhere in the list: the entries of a
+    token are added up in list order, bit for bit."""
+    rng = np.random.default_rng(V + len(what))
+    if what == "every":
+        lists = [rng.permutation(V), np.arange(V)[::-1]]
+    elif what == "one":
+        lists = [np.full(5000, V - 1), np.repeat([3, 70, 3], [40, 33, 2000])]
+    elif what == "twice":
+        lists = [np.concatenate([rng.permutation(V)[:3000]] * 2), np.tile(np.arange(0, V, 100), 3)]
+    else:  # columns of one word and of neighbouring ones, more than are listed at a time
+        lists = [np.arange(min(V, 4096)), np.concatenate([np.arange(600, 1500), np.arange(700, 720), np.arange(640, 672)])]
+    n = np.array([len(t) for t in lists])
+    tokens = np.concatenate(lists).astype(i32)
+    values = (rng.standard_normal(len(tokens)) * rng.choice([1e-3, 1, 30], len(tokens))).astype(f32)
+    values[rng.random(len(tokens)) < 0.02] = -0.0
+    counts = np.where(rng.random((2, V)) < 0.01, 2, 0).astype(i32)
+    p = dict(counts=counts, seen=ref.pack(np.stack([rng.random((2, V)) < 0.01, counts > 0], 1)), frequency=f32([0.5, 0.1]),
+             bias_offsets=np.concatenate([[0], np.cumsum(n)]).astype(i32), bias_tokens=tokens, bias_values=values)
+    off = i32([0, 1, 1])
+    rows = ref.Rows("target", off, i32([5]))
+    z = rng.standard_normal((3, V)).astype(f32)
+    z[:, ::97] = -0.0
+    z = ref.to_bf16(z) if dtype == "bf16" else z
+    want, _, _ = ref.process(z, rows, p, dtype)
+    x = dev(z, dtype)
+    got = host(sv.spec_logits_process(x, dev(off), dev(i32([5])), out=x if in_place else None, **{k: dev(v) for k, v in p.items()}))
+    assert np.array_equal(got, want) and np.array_equal(np.signbit(got), np.signbit(want))
