@@ -469,7 +469,10 @@ int spec_adapt_update(void *state, const int32_t *num_accepted, int B, int min_k
  * spec_draft_sample, process (and truncate) the target rows, spec_verify,
  * spec_penalty_update.  The rule is one for both sides: the verify is lossless for
  * the target distribution as these calls leave it.  The pages have no
- * counterpart; the definitions are this library's and stand below.
+ * counterpart; the definitions are this library's and stand below.  A row is
+ * the whole vocabulary's: the ranks of spec_shard_stats hold some columns
+ * each, and what is to be verified there is processed and truncated before
+ * its columns are given out.
  *
  * Rows.  `rows` says which rows a call has:
  *   SPEC_ROWS_TARGET  the target rows of a chain: offsets = k_offsets, sequence
@@ -520,7 +523,8 @@ typedef struct {
  *   seen = c > 0, or v in the prompt
  *   y    = seen ? (z > 0 ? z / repetition[b] : z * repetition[b]) : z
  *   y    = (y - frequency[b] * c) - presence[b] * [c > 0]
- *   y    = y + the biases of v in b's list, in list order
+ *   y    = y + the sum of v's biases in b's list, added up in list order first
+ *          (if there are any)
  *   y    = -inf where r's mask has bit v clear (whatever z is, NaN included)
  * A logit that nothing applies to keeps its bits.  A mask that allows nothing
  * leaves a row of -inf, which the verify reports as a data error.

@@ -7,7 +7,8 @@
 //          tokens before row r
 //   seen = c > 0 or v in the prompt
 //   y    = seen ? (z > 0 ? z / rho : z * rho) - phi c - pi [c > 0] : z
-//   y    = y + bias_b(v);  y = allowed_r(v) ? y : -inf;  rounded once.
+//   y    = y + bias_b(v), v's entries of the list added up first;
+//   y    = allowed_r(v) ? y : -inf;  rounded once.
 //
 // The pass reads and writes every logit once and computes next to nothing, so
 // memory bounds it.  Few columns of a sequence are seen, drafted or biased

@@ -235,3 +235,11 @@ def test_binding_refuses_counts_past_31_bits(sv):
             sv.spec_penalty_update(*st, Sized((n,), i32), Sized((2,), i32), off)
     rw = bd._rows_arg(Sized((most, 8), fl), off, "target", Sized((most,), i32), None, i32)
     assert rw.R == most and rw.n_tokens == most
+
+
+def test_biases_of_one_token_are_added_up_first():
+    """z = 1 with biases 2^-24 and 2^-24: 1 + 2^-23 by the definition, 1 if they were added one after the other."""
+    rows = ref.Rows("next", np.array([0, 0]), np.zeros(0, np.int64))
+    p = dict(bias_offsets=np.array([0, 2]), bias_tokens=np.array([1, 1]), bias_values=f32([2.0 ** -24, 2.0 ** -24]))
+    out, _, _ = ref.process(f32([[0, 1, 0, 0]]), rows, p, ref.F32)
+    assert out[0, 1] == f32(1 + 2.0 ** -23)
