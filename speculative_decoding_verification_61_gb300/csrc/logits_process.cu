@@ -35,7 +35,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 256;    // columns listed at once
-constexpr int kBias = 64;     // bias entries kept in shared memory
+constexpr int kBias = 64;     // entries of the bias lists that are searched, in shared memory (see add_biases)
 template <bool STREAM>
 constexpr int kPerSm = STREAM ? 6 : 8;  // resident CTAs
 
@@ -225,10 +225,11 @@ __device__ __forceinline__ void nan_rows(char *out, int V, int64_t row0, int i0,
 
 // The entries of a bias list (all valid) added up per listed column, in list order,
 // for the `len` columns listed from number `base` on: a warp takes a share of the
-// columns and goes through the list once, the entries of one token by turns.  Where
-// each column searches the whole list instead, its cost is the square of its length:
-// lists of 300 cost 51 us beside the 45 of 384 rows of 128256, now 18; one of every token
-// 265 ms a row, now 13; lists of 32 and 64 the same.
+// columns and goes through the list once, the entries of one token by turns.  A search of the
+// list by each biased column costs the square of its length: lists of 300 took 96 us
+// for 384 rows of 128256, now 63, one of every token 265 ms a row, now 13.  Lists of up to
+// kBias entries, which lie in shared memory, are searched all the same: B=512 with
+// 32 entries each takes 321 us so and 331 by passes.
 template <bool STREAM>
 __device__ __forceinline__ void add_biases(GroupShared<STREAM> &sm, const Units &un, const int32_t *tokens, const float *values, uint32_t n,
                                            int base, int len) {
@@ -241,10 +242,7 @@ __device__ __forceinline__ void add_biases(GroupShared<STREAM> &sm, const Units 
     for (uint32_t x0 = 0; x0 < n; x0 += 32 * kAhead) {
         int t[kAhead], to[kAhead], most = -1;  // the entries' tokens, their places among the warp's columns
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const uint32_t x = x0 + u * 32 + lane;
-            t[u] = x < n ? *(x < kBias ? sm.bias_token + x : tokens + x) : -1;
-        }
+        for (int u = 0; u < kAhead; ++u) t[u] = x0 + u * 32 + lane < n ? __ldg(tokens + x0 + u * 32 + lane) : -1;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             to[u] = -1;
@@ -259,9 +257,7 @@ __device__ __forceinline__ void add_biases(GroupShared<STREAM> &sm, const Units 
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (!__any_sync(0xffffffffu, to[u] >= 0)) continue;
-            const uint32_t x = x0 + u * 32 + lane;
-            float v = 0.0f;
-            if (to[u] >= 0) v = x < kBias ? sm.bias_value[x] : __ldg(values + x);
+            const float v = to[u] >= 0 ? __ldg(values + x0 + u * 32 + lane) : 0.0f;
             const int turn = __popc(__match_any_sync(0xffffffffu, to[u]) & ((1u << lane) - 1));
             for (int i = 0; __any_sync(0xffffffffu, to[u] >= 0 && turn >= i); ++i) {
                 if (to[u] >= 0 && turn == i) sm.bias[to[u]] = __fadd_rn(sm.bias[to[u]], v);
@@ -392,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
     } else {
         uint32_t touched[G::kWordsEach], drafted[G::kWordsEach], biased[G::kWordsEach];
         int rank = 0;
-        uint32_t any_biased = 0;
 #pragma unroll
         for (int i = 0; i < G::kWordsEach; ++i) {
             const int word = G::word(un, i * G::kSize + me);
@@ -400,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
             const uint32_t in_v = word >= W ? 0u : word == W - 1 && (V & 31) ? (1u << (V & 31)) - 1 : 0xffffffffu;
             drafted[i] = sm.drafted[i * G::kSize + me];
             biased[i] = BIAS ? sm.biased[i * G::kSize + me] : 0;
-            any_biased |= biased[i];
             touched[i] = (prompt[i] | emitted[i] | drafted[i] | biased[i]) & in_v;
             rank += __popc(touched[i]);
         }
@@ -412,20 +406,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
         }
         int listed = __shfl_sync(0xffffffffu, rank, 31);
         rank -= own;
-        constexpr int kBiasedBit = 1 << 16;  // (at most 4096 columns are listed)
-        if (BIAS && __any_sync(0xffffffffu, any_biased != 0)) listed += kBiasedBit;
         if (STREAM) {
             if (lane == 0) sm.warp_sum[threadIdx.x >> 5] = listed;
             __syncthreads();
             listed = 0;
             for (int i = 0; i < kWarps; ++i) {
-                if (i == static_cast<int>(threadIdx.x >> 5)) rank += listed & (kBiasedBit - 1);
+                if (i == static_cast<int>(threadIdx.x >> 5)) rank += listed;
                 listed += sm.warp_sum[i];
             }
         }
-        const bool has_biased = BIAS && listed >= kBiasedBit;
-        listed &= kBiasedBit - 1;
-        if (has_biased) {
+        // short lists are searched by each biased column
+        const bool long_list = BIAS && e1 - e0 > kBias;
+        if (long_list) {
             int at = rank;
 #pragma unroll
             for (int i = 0; i < G::kWordsEach; ++i) {
@@ -470,14 +462,21 @@ __global__ void __launch_bounds__(kThreads, kPerSm<STREAM>)
                 }
                 at += n_i;
             }
-            if (has_biased) add_biases<STREAM>(sm, un, ps.bias_tokens + e0, ps.bias_values + e0, e1 - e0, base, len);
+            if (long_list) add_biases<STREAM>(sm, un, ps.bias_tokens + e0, ps.bias_values + e0, e1 - e0, base, len);
             G::sync();
             // a thread takes a column, all its rows
             for (int e = me; e < len; e += G::kSize) {
                 const int col = sm.column[e];
                 const uint32_t f = sm.flags[e];
                 const int count = f & kEmitted ? __ldg(ps.counts + slot * V + col) : 0;
-                const float bias = BIAS && f & kBiased ? sm.bias[e] : 0.0f;
+                float bias = -0.0f;  // (leaves every value as it is)
+                if (BIAS && f & kBiased) {
+                    if (long_list)
+                        bias = sm.bias[e];
+                    else
+                        for (int x = 0; x < e1 - e0; ++x)
+                            if (sm.bias_token[x] == col) bias = __fadd_rn(bias, sm.bias_value[x]);
+                }
                 constexpr int kRows = 4;  // in flight
                 for (int i = i0; i < i1; i += kRows) {
                     float z[kRows];
