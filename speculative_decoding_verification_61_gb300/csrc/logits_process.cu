@@ -610,10 +610,12 @@ template <int DT, bool STREAM>
 int launch_process(const void *logits, void *out, const Rows &rw, const Process &ps, int V, int sms,
                    cudaStream_t stream) {
     using G = Group<STREAM>;
-    // Spread pieces even out the frequent ids, whole units keep the CTAs that run at
-    // a time in one window of memory.  384 rows of 128256 bf16 (98 MB) took 48 us spread
-    // and 62 whole, 1024 rows 119 and 130; 3267 rows (838 MB) 620 spread and 349 whole.
-    const bool spread = !STREAM || static_cast<int64_t>(rw.R) * V * Elem<DT>::kBytes <= static_cast<int64_t>(300) << 20;
+    // Spread pieces even out the frequent ids, whole units keep the CTAs that run at a time
+    // in one window of memory, which counts where many sequences run at a time. Spread and whole,
+    // bf16: B=64 (384 rows of 128256) 48 and 62 us, B=512 (3267 rows) 304 and 331, B=1024 (2048
+    // rows of 8000) 45 and 48, B=2048 (one row of 128256 each) 467 and 424, B=4096 (4 rows of 32000
+    // each) 508 and 482, (one of 128256) 1238 and 992.
+    const bool spread = !STREAM || rw.B < 2048;
     const int piece = !STREAM ? 0 : spread ? 1 : 7;
     const int units = G::units(V, piece);
     const int64_t pairs = static_cast<int64_t>(rw.B) * units;

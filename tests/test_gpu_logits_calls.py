@@ -175,3 +175,33 @@ def test_long_bias_lists(sv, what, dtype, V, in_place):
     x = dev(z, dtype)
     got = host(sv.spec_logits_process(x, dev(off), dev(i32([5])), out=x if in_place else None, **{k: dev(v) for k, v in p.items()}))
     assert np.array_equal(got, want) and np.array_equal(np.signbit(got), np.signbit(want))
+
+
+# ----------------------------------------------------------------- many sequences
+@pytest.mark.parametrize("B", [2047, 2048, 4096])
+@pytest.mark.parametrize("dtype,V", [("bf16", 9000), ("fp32", 4100)])
+def test_rows_of_few_and_of_many_sequences(sv, dtype, V, B):
+    """The layouts for up to 2047 sequences and for more of them give the definition's rows."""
+    rng = np.random.default_rng(B)
+    ks = rng.integers(0, 3, B)
+    off = np.concatenate([[0], np.cumsum(ks)]).astype(i32)
+    tokens = rng.integers(0, V, off[-1]).astype(i32)
+    R = int(off[-1]) + B
+    z = rng.standard_normal((40, V)).astype(f32)
+    z = (ref.to_bf16(z) if dtype == "bf16" else z)[rng.integers(0, 40, R)]
+    counts = np.where(rng.random((5, V)) < 0.1, 3, 0).astype(i32)
+    counts[:, :100] = 1
+    n = rng.integers(0, 5, B)
+    e = np.concatenate([[0], np.cumsum(n)]).astype(i32)
+    p = dict(counts=counts, seen=ref.pack(np.stack([rng.random((5, V)) < 0.1, counts > 0], 1)), slots=rng.integers(0, 5, B).astype(i32),
+             repetition=rng.choice(f32([1, 1.3]), B), frequency=rng.choice(f32([0, 0.4]), B), presence=rng.choice(f32([0, 0.2]), B),
+             bias_offsets=e, bias_tokens=rng.integers(0, V, e[-1]).astype(i32), bias_values=rng.standard_normal(e[-1]).astype(f32),
+             mask=ref.pack(rng.random((6, V)) < 0.6), mask_rows=rng.integers(-1, 6, R).astype(i32))
+    got = host(sv.spec_logits_process(dev(z, dtype), dev(off), dev(tokens), **{k: dev(v) for k, v in p.items()}))
+    for b in np.concatenate([[0, 1, B - 2, B - 1], rng.choice(B, 12, replace=False)]):
+        rows = slice(off[b] + b, off[b + 1] + b + 1)
+        q = {k: v for k, v in p.items() if k in ("counts", "seen", "mask")}
+        q.update({k: p[k][b:b + 1] for k in ("slots", "repetition", "frequency", "presence")}, mask_rows=p["mask_rows"][rows],
+                 bias_offsets=i32([0, n[b]]), bias_tokens=p["bias_tokens"][e[b]:e[b + 1]], bias_values=p["bias_values"][e[b]:e[b + 1]])
+        want, _, _ = ref.process(z[rows], ref.Rows("target", i32([0, ks[b]]), tokens[off[b]:off[b + 1]]), q, dtype)
+        assert np.array_equal(got[rows], want), b
