@@ -205,3 +205,78 @@ def test_rows_of_few_and_of_many_sequences(sv, dtype, V, B):
                  bias_offsets=i32([0, n[b]]), bias_tokens=p["bias_tokens"][e[b]:e[b + 1]], bias_values=p["bias_values"][e[b]:e[b + 1]])
         want, _, _ = ref.process(z[rows], ref.Rows("target", i32([0, ks[b]]), tokens[off[b]:off[b + 1]]), q, dtype)
         assert np.array_equal(got[rows], want), b
+
+
+# ------------------------------------------------------------------- the smallest rows
+@pytest.mark.parametrize("dtype,V", [("fp32", 4), ("bf16", 8)])
+def test_smallest_rows(sv, dtype, V):
+    """One vector a row: state, processing, truncation."""
+    rng = np.random.default_rng(V)
+    st = sv.PenaltyState(2, V)
+    st.reset(dev(i32([1, 0])), dev(i32([0, 2, 3])), dev(i32([0, V - 1, 1])), dev(i32([0, 0, 2])), dev(i32([2, 2])))
+    st.update(dev(i32([3, 3, 1])), dev(i32([1, 0])), dev(i32([0, 1, 1])), slots=dev(i32([1, 0])))
+    counts = np.zeros((2, V), i32)
+    counts[0, 2], counts[1, 3], counts[0, 1] = 2, 2, 1
+    assert np.array_equal(st.counts.cpu().numpy(), counts)
+    off, tokens = i32([0, 2, 2]), i32([0, V - 1])
+    rows = ref.Rows("target", off, tokens)
+    z = rng.standard_normal((4, V)).astype(f32)
+    z = ref.to_bf16(z) if dtype == "bf16" else z
+    p = dict(counts=counts, seen=st.seen.cpu().numpy(), repetition=f32([1.5, 0.5]), frequency=f32([0.25, 0]), presence=f32([0, 1]),
+             mask=ref.pack(rng.random((4, V)) < 0.8))
+    want, _, _ = ref.process(z, rows, p, dtype)
+    T, s = f32([1, 0.5]), dict(top_k=i32([3, V - 1]), top_p=f32([0.8, 0.6]), min_p=f32([0, 0.01]))
+    cut, margin = ref.truncate(want, ref.row_sequences(rows), T, **s)
+    assert margin.min() > 1e-6
+    got = sv.spec_logits_process_truncate(dev(z, dtype), dev(T), dev(off), dev(tokens), **{k: dev(v) for k, v in {**p, **s}.items()})
+    assert np.array_equal(host(got), cut)
+
+
+# --------------------------------------------------------------------- captured calls
+CAPTURED = {"cluster": ("bf16", 128256, 2, False), "cluster in place": ("bf16", 128256, 2, True), "rows": ("bf16", 32000, 200, False),
+            "held": ("fp32", 32000, 3, False), "fp32": ("fp32", 128256, 3, True), "small": ("fp32", 4100, 40, True)}
+
+
+@pytest.mark.parametrize("name", sorted(CAPTURED))
+def test_captured_calls(sv, name):
+    """Processing and truncation of every kind of row, captured beside another graph of the same buffers, replayed
+    in turn with it on inputs that change."""
+    dtype, V, B, in_place = CAPTURED[name]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    off = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    tokens = torch.randint(V, (B,), generator=g, device="cuda").int()
+    T = torch.full((B,), 0.8, device="cuda")
+    st = sv.PenaltyState(B, V)
+    n = 50
+    a = dict(counts=st.counts, seen=st.seen, frequency=torch.full((B,), 0.3, device="cuda"), bias_offsets=off * n,
+             bias_tokens=torch.randint(V, (B * n,), generator=g, device="cuda").int(),
+             bias_values=torch.randn(B * n, generator=g, device="cuda"))
+    t = dict(top_k=torch.randint(1, 200, (B,), generator=g, device="cuda").int(), top_p=torch.full((B,), 0.95, device="cuda"))
+    kind = torch.float32 if dtype == "fp32" else torch.bfloat16
+    x = torch.zeros(2 * B, V, dtype=kind, device="cuda")
+    out = x if in_place else torch.empty_like(x)
+    emitted, accepted = torch.randint(V, (2 * B,), generator=g, device="cuda").int(), torch.ones(B, dtype=torch.int32, device="cuda")
+
+    def both():
+        return sv.spec_logits_process_truncate(x, T, off, tokens, out=out, **a, **t)
+
+    def update():
+        st.update(emitted, accepted, off)
+
+    both(), update()
+    st.reset(torch.arange(B, dtype=torch.int32, device="cuda"))
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for graph, call in zip(graphs, (both, update)):
+        with torch.cuda.graph(graph):
+            call()
+    for i in range(3):
+        z = (torch.randn(2 * B, V, generator=g, device="cuda") * 3).to(kind)
+        tokens.copy_(torch.randint(V, (B,), generator=g, device="cuda"))
+        emitted.copy_(torch.randint(V, (2 * B,), generator=g, device="cuda"))
+        want = sv.spec_logits_truncate(sv.spec_logits_process(z, off, tokens, **a), T, off, **t)
+        x.copy_(z)
+        graphs[0].replay()
+        assert torch.equal(out, want)
+        graphs[1].replay()
+        assert int(st.counts.sum()) == 2 * B * (i + 1)
