@@ -588,7 +588,8 @@ int spec_logits_process(const void *logits, const spec_rows_t *rows, const spec_
  * set is the defined one unless the border lies as near as that to another
  * token's, and the same on every run.  Rows of greedy sequences (T_b = 0: their arg-max is kept
  * anyway), and rows that hold NaN or +inf or only -inf, keep their bits.
- * Invalid sequences: T_b < 0, NaN or infinite, or a setting outside its range.
+ * Invalid sequences: T_b < 0, NaN, infinite or so small that log2(e) / T_b is
+ * (below 4.24e-39), or a setting outside its range.
  */
 typedef struct {
     const float *temperature; /* [B] */

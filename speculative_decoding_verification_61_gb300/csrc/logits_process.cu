@@ -17,8 +17,8 @@
 // list of the few columns, whose logits are taken one a lane afterwards.  In
 // place the stream touches only what a mask takes away.  Working the touched
 // columns inside the stream instead took 830 us at B=512 (3267 rows of 128256
-// bf16, a quarter of them under a grammar); this split takes 320 us, 5.3 TB/s of
-// the bytes it has to move, 78 % of the copy rate.  What is left is latency: a
+// bf16, a quarter of them under a grammar); this split takes 305 us, 5.6 TB/s of
+// the bytes it has to move, 82 % of the copy rate.  What is left is latency: a
 // CTA's set-up, its rows two at a time and its list are dependent loads, and
 // 24 warps an SM do not cover all of it (30 % of the warps' slots, DRAM 75-80 %).
 #include <algorithm>
@@ -621,7 +621,7 @@ int launch_process(const void *logits, void *out, const Rows &rw, const Process 
     const int64_t pairs = static_cast<int64_t>(rw.B) * units;
     // few sequences: their rows are split until every SM has its CTAs; long ones into parts
     // of about 8 rows, so that the last CTAs are short (64 trees of 16 rows: 119 us whole,
-    // 108 in halves; halves of 6 rows cost more set-up than they gain: 320 and 367 us at B=512)
+    // 108 in halves; halves of 6 rows cost more set-up than they gain: 14 % at B=512)
     // (a buffer may have more rows than its sequences can own)
     const int64_t most = rw.mode == SPEC_ROWS_TREE ? SPEC_MAX_TREE_NODES : rw.mode == SPEC_ROWS_NEXT ? 1 : SPEC_MAX_K + 1;
     const int64_t room = static_cast<int64_t>(sms) * kPerSm<STREAM> * G::kCount, each = std::min<int64_t>(rw.R / rw.B, most);

@@ -1220,7 +1220,7 @@ __device__ __forceinline__ uint32_t max_key(const uint4 &q) {
 // translations), the hardware's scheduling of a CTA per row 7 % faster than a
 // fixed share each.
 // CL CTAs of a cluster share a row, each a run of its groups: CTA 0 adds up the
-// histograms and finds the border for all.  One row: 25 us alone, 17 by eight.
+// histograms and finds the border for all.  One row: 25 us alone, 18 by eight.
 template <int CL>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     truncate_bf16_kernel(const char *logits, char *out, Rows rw, Truncate tr, int V) {
