@@ -106,3 +106,26 @@ def test_outputs_on_another_stream(sv, name):
     call = verify_calls(sv)[name]
     torch.cuda.synchronize()  # the inputs are there
     check(call)
+
+
+@pytest.mark.parametrize("name", ["process", "truncate", "both"])
+def test_logit_outputs_on_a_forked_stream_of_a_capture(sv, name):
+    """A captured call on a stream that the capture forked: its new output is the graph's, and replays rewrite it."""
+    call, side = logit_calls(sv)[name], torch.cuda.Stream()
+    want = call(None).clone()
+    call(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        other = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    assert got.data_ptr() != other.data_ptr()
+    for _ in range(2):
+        got.zero_()
+        graph.replay()
+        assert torch.equal(got, want) and torch.equal(other, want)
+    del got, other
+    torch.cuda.synchronize()
+    assert torch.equal(call(None), want)
