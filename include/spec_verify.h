@@ -632,6 +632,156 @@ int spec_penalty_reset(int32_t *counts, int32_t *seen, int S, int V, const int32
 int spec_penalty_update(int32_t *counts, int32_t *seen, int S, int V, const int32_t *slots, const spec_rows_t *rows,
                         const int32_t *out_tokens, const int32_t *num_accepted, void *stream);
 
+/*
+ * What a round leaves behind: the hypotheses that a beam keeps, and the states
+ * (token counts, a cache of keys and values) that follow what was kept or
+ * accepted.  The pages leave these to the model's runtime; the definitions are
+ * this library's and stand below.  Calls are asynchronous on `stream`, keep
+ * no workspace of the library's own (calls on different streams are
+ * independent), and may be captured into a graph.  B <= SPEC_MAX_B; without
+ * sequences or rows nothing is read.
+ *
+ * Beam selection.  Group b owns the rows offsets[b] .. offsets[b+1] - 1 (0 to
+ * SPEC_MAX_BEAMS of them, offsets[0] = 0, offsets[B] <= R), one per hypothesis.
+ * Row r with the score s_r offers every token v with z_{r,v} > -inf as a
+ * candidate of the score
+ *   s_r + z_{r,v} - ln sum_v exp z_{r,v};
+ * a row with s_r = -inf offers none; a row that has ended offers one, the
+ * token end_token with the score s_r.  The logits of such rows are not read.
+ * The n best candidates of each group are written in the order score
+ * descending, then row, then token; places without a candidate get -inf, -1, -1.
+ * Scores are compared in 64 bits and rounded to fp32 at the end.  The row sums are of
+ * fp32 terms: candidates of different rows whose scores differ by less than
+ * about 1e-7 may change places, those of one row never; the result is the
+ * same on every run.
+ *   logits       [R, V] row-major, 16-byte aligned, V * sizeof(element) a
+ *                multiple of 16, as for spec_verify
+ *   scores       float [R]
+ *   ended        uint8 [R], not 0: the hypothesis has ended; NULL: none has
+ *   end_token    in [0, V) (ignored where ended is NULL)
+ *   n            1 .. SPEC_MAX_CANDIDATES candidates per group
+ *   out_scores   float [B, n]; out_tokens, out_rows int32 [B, n] (a row's
+ *                index in logits)
+ *   out_lse      float [R] or NULL: ln sum_v exp z_{r,v}, NaN where the row was not
+ *                read; rows behind the last group's are left as they were
+ *   workspace    device, 256-byte aligned, spec_beam_workspace_bytes(R, V, dtype)
+ *                bytes, needs no initialisation; not shared by calls that may overlap
+ * Data errors: a score that is NaN or +inf, or a row that is read and holds NaN or
+ * +inf, makes its group NaN, -1, -1; invalid offsets make all groups so (and
+ * all of out_lse NaN).  Host errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_ALIGNMENT,
+ * SPEC_ERR_WORKSPACE, SPEC_ERR_CUDA.
+ */
+#define SPEC_MAX_BEAMS 64       /* rows of one group */
+#define SPEC_MAX_CANDIDATES 128 /* candidates kept of one group */
+
+size_t spec_beam_workspace_bytes(int R, int V, int dtype);
+int spec_beam_select(const void *logits, const float *scores, const uint8_t *ended, int32_t end_token,
+                     const int32_t *offsets, int B, int R, int V, int dtype, int n, float *out_scores,
+                     int32_t *out_tokens, int32_t *out_rows, float *out_lse, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * Reordering of states, in place: with s(i) = slots[i] (NULL: i), slot s(i) of
+ * every state gets what slot s(rows[i]) held before the call, for each entry i
+ * of group b (offsets as above).  rows are out_rows of spec_beam_select, or any
+ * map of a group into itself; rows[i] = -1 leaves slot s(i) as it is.
+ *
+ * A state is an array of bytes [planes, S, runs, T, unit], contiguous: S slots of
+ * T positions each.  With lengths (int32 [S]), the first
+ * min(lengths[s(rows[i])], T) positions of each run are moved (of a negative length none)
+ * and the others stay as they are; without, all T.
+ *   states       HOST array of n_states <= SPEC_MAX_STATES states; no two overlap
+ *   rows         int32 [R]; an entry behind the last group's is not read
+ *   slots        int32 [R]: one slot is named at most once in a call
+ *   lengths      int32 [S] or NULL; none of the states
+ * A group that holds a slot outside [0, S), a slot twice, or a row that is neither -1
+ * nor of the group is left as it is, as all are if the offsets are invalid.
+ * (A slot that two groups name is not found: which of its contents
+ * the groups then see is not defined.)
+ */
+#define SPEC_MAX_STATES 64
+
+typedef struct {
+    void *data;
+    int64_t planes; /* layers, e.g.: dimensions before the slots */
+    int64_t runs;   /* dimensions between the slots and the positions */
+    int64_t T;      /* positions */
+    int64_t unit;   /* bytes of a position */
+} spec_state_t;
+
+int spec_state_reorder(const spec_state_t *states, int n_states, int S, const int32_t *rows, const int32_t *offsets,
+                       int B, int R, const int32_t *slots, const int32_t *lengths, void *stream);
+
+/*
+ * A cache of keys and values in 8 bits.  Blocks of 32 elements along a head
+ * (the last one shorter if D is not a multiple of 32) share a scale 2^e: with
+ * a the block's largest finite |x|, e is the least integer >= -127 with
+ * a <= 448 * 2^e.  Held are the byte e + 127 and, per element, x * 2^-e rounded to
+ * e4m3 (to nearest, ties to even; NaN and infinities become NaN).  Scaling by
+ * a power of two is exact, so an element is rounded once, by at most 2^-4 of
+ * itself (or half of the smallest step, 2^-10 * 2^e), and what is read back in
+ * fp32 is exactly what is held (2^128, which values next to fp32's largest round
+ * to, as infinity).
+ *
+ *   k, v         e4m3 [L, P, T, H, D], k_scale, v_scale uint8
+ *                [L, P, T, H, ceil(D / 32)]: P pages of T positions, 16-byte
+ *                aligned; v and v_scale NULL: a cache of one tensor
+ *   pages        int32 [S, M]: slot s has its positions j * T .. j * T + T - 1 on page
+ *                pages[s, j]; NULL: slot s has the page s alone (P = S, M = 1)
+ *   lengths      int32 [S]: the positions of each slot that are held; a negative one: the slot is invalid
+ * D a multiple of 16, at most 1024; H * D at most 65536.
+ */
+typedef struct {
+    void *k;
+    uint8_t *k_scale;
+    void *v;
+    uint8_t *v_scale;
+    int L, P, T, H, D;
+    const int32_t *pages;
+    int S, M;
+    const int32_t *lengths;
+} spec_cache_t;
+
+/*
+ * Writes rows into the cache, from position lengths[slots[b]] of sequence b's slot on.
+ * `rows` and `offsets` say which rows b has, num_accepted which are kept:
+ *   SPEC_ROWS_TARGET  a verify's rows: the first num_accepted[b] + 1
+ *   SPEC_ROWS_TREE    a tree verify's: the path from the root to last_node[b]
+ *                     (num_accepted[b] + 1 nodes), in its order; parent as in
+ *                     spec_tree_verify
+ *   SPEC_ROWS_NEXT    one row per sequence (offsets are not read)
+ *   SPEC_ROWS_PROMPT  rows offsets[b] .. offsets[b+1] - 1, any number, all kept
+ * Rows that are not kept are neither read nor written.
+ *   keys, values [L, R, H, D] of dtype: element (l, r, h, d) at
+ *                l * layer_stride + r * row_stride + h * D + d, strides and pointers
+ *                multiples of 16 elements (32 bytes)
+ *   slots        int32 [B], distinct; NULL: b
+ *   out_lengths  int32 [S]: lengths with the kept rows of each sequence added;
+ *                lengths itself for in place; NULL: not written (all calls of a
+ *                step but the last, where layers are written one by one)
+ * A sequence with num_accepted < 0 or more than it drafted, a slot outside [0, S), a negative
+ * length, or a tree path that is not one of num_accepted + 1 nodes, is
+ * skipped.  A sequence that a kept row of has no room (its position is M * T or more) or a page
+ * outside [0, P) gets the length -1; its rows that do have room are written.  Invalid
+ * offsets: nothing is written but out_lengths, as lengths.
+ */
+#define SPEC_ROWS_PROMPT 4
+
+int spec_cache_write(const spec_cache_t *cache, const void *keys, const void *values, int64_t layer_stride,
+                     int64_t row_stride, int dtype, const spec_rows_t *rows, const int32_t *num_accepted,
+                     const int32_t *last_node, const int32_t *slots, int32_t *out_lengths, void *stream);
+
+/*
+ * Reads positions back: row offsets[b] + i of the outputs gets position first[b] + i
+ * of sequence b's slot (first NULL: 0), each value rounded once to dtype.  Positions outside [0,
+ * lengths[slot]), invalid slots and invalid pages read as NaN; rows behind the last
+ * sequence's are left as they were, all of them if the offsets are invalid.
+ *   out_keys, out_values  [L, R, H, D] of dtype, contiguous, 32-byte aligned;
+ *                out_values NULL if the cache has no v
+ */
+int spec_cache_read(const spec_cache_t *cache, const int32_t *offsets, int B, int R, const int32_t *first,
+                    const int32_t *slots, int dtype, void *out_keys, void *out_values, void *stream);
+
 /* Bytes of device workspace needed by spec_verify_ex / spec_draft_sample_ex
  * for a call with B sequences over vocabulary V (0 for invalid arguments). */
 size_t spec_workspace_bytes(int B, int V, int dtype);

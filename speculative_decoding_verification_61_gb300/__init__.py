@@ -14,10 +14,15 @@ from ._binding import (  # noqa: F401
     ABI_VERSION,
     AdaptiveK,
     BF16,
+    CACHE_ROWS,
+    CacheState,
     F32,
     MAX_B,
+    MAX_BEAMS,
+    MAX_CANDIDATES,
     MAX_K,
     MAX_SHARDS,
+    MAX_STATES,
     MAX_TREE_NODES,
     MAX_V,
     NOALLOC_SCRATCH_BYTES,
@@ -25,6 +30,7 @@ from ._binding import (  # noqa: F401
     ROWS,
     SPEC_ERRORS,
     SpecError,
+    beam_workspace_bytes,
     exported_symbols,
     lib,
     lib_path,
@@ -33,6 +39,9 @@ from ._binding import (  # noqa: F401
     shard_workspace,
     shard_workspace_bytes,
     shutdown,
+    spec_beam_select,
+    spec_cache_read,
+    spec_cache_write,
     spec_draft_sample,
     spec_draft_sample_lse,
     spec_logits_process,
@@ -45,6 +54,7 @@ from ._binding import (  # noqa: F401
     spec_shard_decide,
     spec_shard_draw,
     spec_shard_stats,
+    spec_state_reorder,
     spec_tree_draft_sample,
     spec_tree_verify,
     spec_verify,

@@ -11,7 +11,9 @@ F32, BF16 = 0, 1
 MAX_K, MAX_B, MAX_V = 32, 4096, 1 << 24
 MAX_TREE_NODES = 64
 MAX_SHARDS = 64
+MAX_BEAMS, MAX_CANDIDATES, MAX_STATES = 64, 128, 64
 ROWS = {"target": 0, "draft": 1, "next": 2, "tree": 3}  # SPEC_ROWS_*
+CACHE_ROWS = {"target": 0, "next": 2, "tree": 3, "prompt": 4}
 NOALLOC_SCRATCH_BYTES = 48 << 20  # spec_verify_noalloc's fixed scratch array
 ABI_VERSION = 1
 SPEC_ERRORS = {0: "SPEC_OK", -1: "SPEC_ERR_INVALID_ARG", -2: "SPEC_ERR_ALIGNMENT",
@@ -26,7 +28,8 @@ EXPORTS = ("spec_verify", "spec_verify_ex", "spec_draft_sample", "spec_draft_sam
            "spec_tree_draft_sample", "spec_shard_workspace_bytes", "spec_shard_stats",
            "spec_shard_decide", "spec_shard_draw", "spec_shutdown", "spec_selfcheck_wait_timeout",
            "spec_logits_process", "spec_logits_truncate", "spec_logits_process_truncate",
-           "spec_penalty_reset", "spec_penalty_update")
+           "spec_penalty_reset", "spec_penalty_update", "spec_beam_workspace_bytes", "spec_beam_select",
+           "spec_state_reorder", "spec_cache_write", "spec_cache_read")
 
 
 class SpecError(RuntimeError):
@@ -57,6 +60,18 @@ class _Logits(ctypes.Structure):
 class _Truncate(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
                 ("min_p", ctypes.c_void_p)]
+
+
+class _State(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("planes", ctypes.c_int64), ("runs", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("unit", ctypes.c_int64)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("L", ctypes.c_int), ("P", ctypes.c_int), ("T", ctypes.c_int),
+                ("H", ctypes.c_int), ("D", ctypes.c_int), ("pages", ctypes.c_void_p), ("S", ctypes.c_int),
+                ("M", ctypes.c_int), ("lengths", ctypes.c_void_p)]
 
 
 _lib = None
@@ -124,6 +139,15 @@ def lib():
     L.spec_penalty_update.argtypes = [vp, vp, ip, ip, vp, rp, vp, vp, vp]
     for name in ("spec_logits_process", "spec_logits_truncate", "spec_logits_process_truncate",
                  "spec_penalty_reset", "spec_penalty_update"):
+        getattr(L, name).restype = ip
+    i64, cp = ctypes.c_int64, ctypes.POINTER(_Cache)
+    L.spec_beam_workspace_bytes.argtypes = [ip, ip, ip]
+    L.spec_beam_workspace_bytes.restype = sz
+    L.spec_beam_select.argtypes = [vp, vp, vp, ip, vp, ip, ip, ip, ip, ip, vp, vp, vp, vp, vp, sz, vp]
+    L.spec_state_reorder.argtypes = [ctypes.POINTER(_State), ip, ip, vp, vp, ip, ip, vp, vp, vp]
+    L.spec_cache_write.argtypes = [cp, vp, vp, i64, i64, ip, rp, vp, vp, vp, vp, vp]
+    L.spec_cache_read.argtypes = [cp, vp, ip, ip, vp, vp, ip, vp, vp, vp]
+    for name in ("spec_beam_select", "spec_state_reorder", "spec_cache_write", "spec_cache_read"):
         getattr(L, name).restype = ip
     for name in ("spec_verify", "spec_verify_ex", "spec_draft_sample", "spec_draft_sample_ex",
                  "spec_round_host", "spec_workspace_status", "spec_abi_version",
@@ -891,3 +915,259 @@ class PenaltyState:
         """spec_penalty_update on this state."""
         spec_penalty_update(self.counts, self.seen, out_tokens, out_num_accepted, offsets, rows=rows, slots=slots,
                             stream=stream)
+
+    def reorder(self, rows, offsets, *, slots=None, stream=None):
+        """spec_state_reorder on this state: the counts and prompts follow the
+        hypotheses that a beam kept."""
+        spec_state_reorder([self.counts, self.seen], rows, offsets, slots=slots, stream=stream)
+
+
+# --------------------------------------------------- beams, states, the cache
+def beam_workspace_bytes(R: int, V: int, dtype: int) -> int:
+    return int(lib().spec_beam_workspace_bytes(R, V, dtype))
+
+
+def spec_beam_select(logits, scores, offsets, n, *, ended=None, end_token=0, lse=False, workspace=None, stream=None):
+    """The n best continuations of each group of hypotheses: logits [R, V] and
+    scores [R] (float32) hold a row per hypothesis, offsets [B+1] says which
+    rows a group has; ended [R] (bool): hypotheses that have ended go on with
+    end_token and their score.  Returns (scores [B, n] float32, tokens [B, n]
+    int32, rows [B, n] int32: the row each comes from), best first, -inf and
+    -1 where there are fewer, and with lse=True each row's log-sum-exp [R]."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, V]")
+    if not logits.is_cuda or not logits.is_contiguous():
+        _check_dev("logits", logits)
+    dt = _dtype_code(logits)
+    dev, device = logits.get_device(), logits.device
+    R, V, B = _size(logits.shape[0], "logits"), _size(logits.shape[1], "a row"), _size(offsets.numel() - 1, "offsets")
+    if B < 0:
+        raise ValueError("offsets must have B + 1 entries")
+    if not 1 <= n <= MAX_CANDIDATES:
+        raise ValueError(f"n must be 1 to {MAX_CANDIDATES}, got {n}")
+    if ended is not None and ended.dtype is torch.bool:
+        ended = ended.view(torch.uint8)
+    args = (logits.data_ptr(), _ptr(scores, "scores", f32, dev, R), _ptr(ended, "ended", torch.uint8, dev, R), end_token,
+            _ptr(offsets, "offsets", i32, dev), B, R, V, dt, n)
+    if workspace is None:
+        workspace = _new(max(256, beam_workspace_bytes(R, V, dt)), torch.uint8, device, stream)
+    out = (_new((B, n), f32, device, stream), _new((B, n), i32, device, stream), _new((B, n), i32, device, stream))
+    if lse:
+        out += (_new(R, f32, device, stream),)
+    _launch(dev, stream, lib().spec_beam_select, "spec_beam_select", *args, *(t.data_ptr() for t in out),
+            *(() if lse else (None,)), _ptr(workspace, "workspace", torch.uint8, dev), workspace.numel())
+    return out
+
+
+def _state_of(x, S, dev):
+    """(tensor, slot dimension, position dimension or None), or a tensor with the slots first, as a _State."""
+    t, at, pos = (x, 0, None) if not isinstance(x, (tuple, list)) else x
+    if not t.is_cuda or not t.is_contiguous():
+        _check_dev("a state", t)
+    if t.get_device() != dev:
+        raise ValueError(f"a state is on {t.device}, the call's other tensors on cuda:{dev}")
+    shape = t.shape
+    if not 0 <= at < len(shape) or (pos is not None and not at < pos < len(shape)):
+        raise ValueError("a state is (tensor, slot dimension, position dimension behind it or None)")
+    if shape[at] != S:
+        raise ValueError(f"a state has {shape[at]} slots, another {S}")
+    end = len(shape) if pos is None else pos + 1
+    planes, unit = 1, t.element_size()
+    for d in shape[:at]:
+        planes *= d
+    for d in shape[end:]:
+        unit *= d
+    if pos is None:  # one position: everything a slot holds
+        for d in shape[at + 1:]:
+            unit *= d
+        return _State(t.data_ptr(), planes, 1, 1, unit)
+    runs = 1
+    for d in shape[at + 1:pos]:
+        runs *= d
+    return _State(t.data_ptr(), planes, runs, shape[pos], unit)
+
+
+def spec_state_reorder(states, rows, offsets, *, slots=None, lengths=None, stream=None):
+    """The states of the hypotheses put in the order of what a beam kept, in
+    place: slot slots[i] (None: i) of every state gets what slot
+    slots[rows[i]] held, for the entries i of each group (offsets [B+1]);
+    rows[i] is -1 or an entry of the same group.  A state is a tensor with the
+    slots first, or (tensor, slot dimension, position dimension or None); of a state
+    with positions the first lengths[slot] (int32 [S], by source) are moved,
+    without lengths all.  Lengths go with the slots of all states; a state without
+    positions moves as one whole where its source's length is not 0.  Returns states."""
+    import torch
+    i32 = torch.int32
+    R, B = _size(rows.numel(), "rows"), _size(offsets.numel() - 1, "offsets")
+    if B < 0:
+        raise ValueError("offsets must have B + 1 entries")
+    if not rows.is_cuda:
+        _check_dev("rows", rows)
+    dev = rows.get_device()
+    args = (_ptr(rows, "rows", i32, dev), _ptr(offsets, "offsets", i32, dev), B, R, _ptr(slots, "slots", i32, dev, R))
+    if not states:
+        return states
+    first = states[0]
+    S = _size(first.shape[0] if not isinstance(first, (tuple, list)) else first[0].shape[first[1]], "a state")
+    made = [_state_of(x, S, dev) for x in states]
+    pl = _ptr(lengths, "lengths", i32, dev, S)
+    for at in range(0, len(made), MAX_STATES):
+        part = made[at:at + MAX_STATES]
+        _launch(dev, stream, lib().spec_state_reorder, "spec_state_reorder", (_State * len(part))(*part), len(part), S,
+                *args, pl)
+    return states
+
+
+def _cache_arg(k, k_scale, v, v_scale, lengths, pages):
+    import torch
+    if k.dim() != 5:
+        raise ValueError("k must be [L, P, T, H, D]")
+    if not k.is_cuda:
+        _check_dev("k", k)
+    dev, i32 = k.get_device(), torch.int32
+    L, P, T, H, D = k.shape
+    if (v is None) != (v_scale is None):
+        raise ValueError("v and v_scale go together")
+    scales = L * P * T * H * ((D + 31) // 32)
+    if pages is not None and pages.dim() != 2:
+        raise ValueError("pages must be [S, M]")
+    S, M = (P, 1) if pages is None else pages.shape
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    return dev, _Cache(_ptr(k, "k", f8, dev), _ptr(k_scale, "k_scale", u8, dev, scales), _ptr(v, "v", f8, dev, k.numel()),
+                       _ptr(v_scale, "v_scale", u8, dev, scales), _size(L, "k"), _size(P, "k"), _size(T, "k"),
+                       _size(H, "k"), _size(D, "k"), _ptr(pages, "pages", i32, dev), _size(S, "pages"),
+                       _size(M, "pages"), _ptr(lengths, "lengths", i32, dev, S))
+
+
+def spec_cache_write(k, k_scale, v, v_scale, lengths, keys, values, offsets=None, *, rows="target", num_accepted=None,
+                     parent=None, last_node=None, slots=None, pages=None, out_lengths=None, stream=None):
+    """Writes the rows that a round kept into an 8-bit cache: k, v e4m3
+    [L, P, T, H, D] with a scale's byte per 32 elements of a head (k_scale,
+    v_scale uint8), lengths [S] the positions held, pages [S, M] or None (slot s
+    is page s).  keys, values [L, R, H, D], or [R, H, D] for L = 1; strided in
+    layers and rows.  rows: "target" (a verify's rows with its k_offsets and
+    num_accepted: the first num_accepted + 1 of each sequence), "tree"
+    (node_offsets, parent, num_accepted, last_node: the accepted path), "next"
+    (a row per sequence) or "prompt" (offsets of any lengths: all).  out_lengths: the lengths after it
+    (lengths for in place), None: not written.  v, v_scale, values None: a
+    cache of one tensor.  Returns out_lengths."""
+    import torch
+    i32 = torch.int32
+    dev, cache = _cache_arg(k, k_scale, v, v_scale, lengths, pages)
+    mode = CACHE_ROWS.get(rows)
+    if mode is None:
+        raise ValueError(f"rows must be one of {sorted(CACHE_ROWS)}, got {rows!r}")
+    if (values is None) != (v is None):
+        raise ValueError("values and v go together")
+    x = keys if keys.dim() == 4 else keys.unsqueeze(0)
+    y = None if values is None else values if values.dim() == 4 else values.unsqueeze(0)
+    L, H, D = cache.L, cache.H, cache.D
+    R = x.shape[1] if x.dim() == 4 else -1
+    for name, t in (("keys", x), ("values", y)):
+        if t is None:
+            continue
+        if not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{name} must be on the cache's device")
+        if t.shape != (L, R, H, D):
+            raise ValueError(f"{name} must be [{L}, R, {H}, {D}], got {tuple(t.shape)}")
+        if t.dtype != x.dtype or t.stride() != x.stride():
+            raise ValueError("keys and values must have one type and one layout")
+        if t.numel() and (t.stride(3) != 1 or (H > 1 and t.stride(2) != D)):
+            raise ValueError(f"{name} must be contiguous in heads and elements")
+    dt = _dtype_code(x)
+    if mode == 2:
+        if slots is None:
+            raise ValueError("rows 'next' need slots: one per sequence")
+        B = _size(slots.numel(), "slots")
+        if B > R:
+            raise ValueError("keys have fewer rows than there are sequences")
+    else:
+        if offsets is None:
+            raise ValueError("offsets must have B + 1 entries")
+        B = _size(offsets.numel() - 1, "offsets")
+    if B < 0:
+        raise ValueError("offsets must have B + 1 entries")
+    if (mode in (0, 3)) != (num_accepted is not None) or (mode == 3) != (last_node is not None and parent is not None):
+        raise ValueError("num_accepted goes with rows 'target' and 'tree', parent and last_node with 'tree'")
+    if parent is not None and parent.numel() < R:
+        raise ValueError("parent must have an entry for each row")
+    rw = _Rows(mode, B, _size(R, "keys"), _ptr(offsets, "offsets", i32, dev), _ptr(parent, "parent", i32, dev), None, 0)
+    _launch(dev, stream, lib().spec_cache_write, "spec_cache_write", ctypes.byref(cache), x.data_ptr(),
+            None if y is None else y.data_ptr(), x.stride(0) if L > 1 else 0, x.stride(1) if R > 1 else H * D, dt,
+            ctypes.byref(rw), _ptr(num_accepted, "num_accepted", i32, dev, B), _ptr(last_node, "last_node", i32, dev, B),
+            _ptr(slots, "slots", i32, dev, B), _ptr(out_lengths, "out_lengths", i32, dev, cache.S))
+    return out_lengths
+
+
+def spec_cache_read(k, k_scale, v, v_scale, lengths, offsets, R, *, first=None, slots=None, pages=None, dtype=None,
+                    out=None, stream=None):
+    """Positions of an 8-bit cache (as in spec_cache_write) read back: row
+    offsets[b] + i of the outputs gets position first[b] + i (first None: 0) of
+    sequence b's slot, NaN where it holds none.  R: rows of the outputs, at least
+    offsets[B].  dtype: bfloat16 (None) or float32.  Returns (keys, values)
+    [L, R, H, D], values None for a cache of one tensor; out: the two to write to."""
+    import torch
+    i32 = torch.int32
+    dev, cache = _cache_arg(k, k_scale, v, v_scale, lengths, pages)
+    B = _size(offsets.numel() - 1, "offsets")
+    if B < 0:
+        raise ValueError("offsets must have B + 1 entries")
+    R = _size(R, "the output")
+    shape = (cache.L, R, cache.H, cache.D)
+    if out is None:
+        kind = torch.bfloat16 if dtype is None else dtype
+        out = (_new(shape, kind, k.device, stream), None if v is None else _new(shape, kind, k.device, stream))
+    dt = _dtype_code(out[0])
+    if (out[1] is None) != (v is None) or (dtype is not None and out[0].dtype != dtype):
+        raise ValueError("out must be (keys, values) of the type asked for, values None if there is no v")
+    size = cache.L * R * cache.H * cache.D
+    _launch(dev, stream, lib().spec_cache_read, "spec_cache_read", ctypes.byref(cache),
+            _ptr(offsets, "offsets", i32, dev), B, R, _ptr(first, "first", i32, dev, B), _ptr(slots, "slots", i32, dev, B), dt,
+            _ptr(out[0], "out", out[0].dtype, dev, size), _ptr(out[1], "out", out[0].dtype, dev, size))
+    return out
+
+
+class CacheState:
+    """An 8-bit cache of keys and values for S slots (spec_cache_write's
+    layout): T positions per slot, or, with pages, `pages` pages of T
+    positions that the caller gives out through page_table [S, M] (-1:
+    none).  Starts empty."""
+
+    def __init__(self, L: int, S: int, T: int, H: int, D: int, *, pages=None, max_pages=None, values: bool = True,
+                 device="cuda"):
+        import torch
+        if min(L, S, T, H) <= 0 or D <= 0 or D % 16 or D > 1024 or H * D > 65536:
+            raise ValueError(f"invalid cache L={L}, S={S}, T={T}, H={H}, D={D}")
+        if (pages is None) != (max_pages is None):
+            raise ValueError("pages and max_pages go together")
+        P = S if pages is None else pages
+        shape, scales = (L, P, T, H, D), (L, P, T, H, (D + 31) // 32)
+        self.k = torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.k_scale = torch.zeros(scales, dtype=torch.uint8, device=device)
+        self.v = torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) if values else None
+        self.v_scale = torch.zeros(scales, dtype=torch.uint8, device=device) if values else None
+        self.lengths = torch.zeros(S, dtype=torch.int32, device=device)
+        self.page_table = None if pages is None else torch.full((S, max_pages), -1, dtype=torch.int32, device=device)
+
+    def write(self, keys, values, offsets=None, *, rows="target", num_accepted=None, parent=None, last_node=None,
+              slots=None, stream=None):
+        """spec_cache_write of all layers; the lengths grow in place."""
+        spec_cache_write(self.k, self.k_scale, self.v, self.v_scale, self.lengths, keys, values, offsets, rows=rows,
+                         num_accepted=num_accepted, parent=parent, last_node=last_node, slots=slots,
+                         pages=self.page_table, out_lengths=self.lengths, stream=stream)
+
+    def read(self, offsets, R, *, first=None, slots=None, dtype=None, out=None, stream=None):
+        """spec_cache_read."""
+        return spec_cache_read(self.k, self.k_scale, self.v, self.v_scale, self.lengths, offsets, R, first=first,
+                               slots=slots, pages=self.page_table, dtype=dtype, out=out, stream=stream)
+
+    def reorder(self, rows, offsets, *, slots=None, stream=None):
+        """spec_state_reorder of the held positions and of the lengths (a cache
+        without pages; with pages it is the caller that gives them out)."""
+        if self.page_table is not None:
+            raise ValueError("a cache with pages is reordered through its page table")
+        states = [(t, 1, 2) for t in (self.k, self.k_scale, self.v, self.v_scale) if t is not None]
+        spec_state_reorder(states, rows, offsets, slots=slots, lengths=self.lengths, stream=stream)
+        spec_state_reorder([self.lengths], rows, offsets, slots=slots, stream=stream)
