@@ -3,16 +3,13 @@
 //   s_r + z_{r,v} - ln sum_v exp z_{r,v}.
 //
 // Within a row the order is that of the logits, so the rows are streamed once
-// without any selecting: a 2 KB piece of a row leaves its largest logit m and
-// sum_v exp(z - m).  The best candidates are then found by narrowing down.  Of any
-// cut of the candidates into pieces that are contiguous in (row, token), the n
-// pieces that come first by (score of the piece's best descending, then
+// without any selecting: a 2 KB piece of a row leaves its largest logit, and
+// a unit of four pieces its largest, m, with sum_v exp(z - m).  The best candidates are then found by
+// narrowing down.  Of any cut of the candidates into pieces that are contiguous in (row, token),
+// the n pieces that come first by (score of the piece's best descending, then
 // position) hold the n best candidates: a candidate of any other piece has n
-// others before it, the best of each of those pieces.  So
-//   1. of all 2 KB pieces of the group, the first n;
-//   2. of their cells of 64 bytes, the first n;
-//   3. of the cells' candidates, the first n,
-// and beyond the partial results only n pieces per group are read again.
+// others before it, the best of each of those pieces.  So beyond the partial results only
+// about n pieces per group are read again.
 #include <algorithm>
 #include <cstdint>
 
@@ -35,14 +32,22 @@ constexpr int kCells = kPieceBytes / kCellBytes;  // of a piece: one per lane
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // ------------------------------------------------------------ rows, streamed
-constexpr int kRowThreads = 256;
-constexpr int kWarpPieces = 2;  // of a warp
-constexpr int kBlockPieces = kRowThreads / 32 * kWarpPieces;
+constexpr int kRowThreads = 128;
+constexpr int kUnitPieces = 4;  // of a warp
+constexpr int kBlockUnits = kRowThreads / 32;
 
+// What a row leaves, and where.
+struct Partial {
+    float2 *unit;  // [R, n_units] (largest logit, sum of exp(z - largest))
+    float *piece;  // [R, n_pieces] largest logits
+    int n_units, n_pieces;
+};
+
+// The largest of a warp's values; NaN if one is NaN.
 __device__ __forceinline__ float warp_max_nan(float m) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = specv::fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-    return m;
+    float r;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+    return r;
 }
 
 __device__ __forceinline__ uint4 load_stream(const uint4 *p) {
@@ -53,71 +58,101 @@ __device__ __forceinline__ uint4 load_stream(const uint4 *p) {
     return v;
 }
 
-// A row of the call is read if its hypothesis lives.
-__device__ __forceinline__ bool row_is_read(const float *scores, const uint8_t *ended, int64_t r) {
-    return __ldg(scores + r) != kNegInf && !(ended && __ldg(ended + r));
-}
-
-// part[r * n_pieces + p] = (largest logit, sum of exp(z - largest)) of piece p of row r.
+// A warp per unit; CTAs blocks_per_row * r .. of row r.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const void *__restrict__ logits,
                                                            const float *__restrict__ scores,
                                                            const uint8_t *__restrict__ ended,
-                                                           const int32_t *__restrict__ offsets, int B, int R, int V,
-                                                           int n_pieces, int blocks_per_row, float2 *__restrict__ part) {
+                                                           const int32_t *__restrict__ offsets, int B, int V,
+                                                           int blocks_per_row, const Partial part) {
+    specv::grid_launch_dependents();
     const int r = blockIdx.x / blocks_per_row;
     const int lane = threadIdx.x & 31;
-    const int p0 = (blockIdx.x - r * blocks_per_row) * kBlockPieces + (threadIdx.x >> 5) * kWarpPieces;
-    if (r >= __ldg(offsets + B) || p0 >= n_pieces || !row_is_read(scores, ended, r)) return;
+    const int u = (blockIdx.x - r * blocks_per_row) * kBlockUnits + (threadIdx.x >> 5);
+    // a row that is not a group's, or whose hypothesis has ended or does not live, is not read
+    if (u >= part.n_units || r >= __ldg(offsets + B) || __ldg(scores + r) == kNegInf || (ended && __ldg(ended + r))) return;
     const int n_vec = V / Elem<DT>::kPerVec;
     const uint4 *row = reinterpret_cast<const uint4 *>(logits) + static_cast<int64_t>(r) * n_vec;
     constexpr uint32_t ni = Elem<DT>::kNegInfWord;
-    uint4 v[kWarpPieces][4];
+    uint4 v[kUnitPieces][4];
+    const int first = u * kUnitPieces * 128 + lane;
+    if ((u + 1) * kUnitPieces * 128 <= n_vec) {
 #pragma unroll
-    for (int k = 0; k < kWarpPieces; ++k)
+        for (int k = 0; k < kUnitPieces; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int at = (p0 + k) * 128 + j * 32 + lane;
-            v[k][j] = at < n_vec ? load_stream(row + at) : make_uint4(ni, ni, ni, ni);
-        }
+            for (int j = 0; j < 4; ++j) v[k][j] = load_stream(row + first + (k * 4 + j) * 32);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kWarpPieces; ++k) {
-        if (p0 + k >= n_pieces) break;
-        const float m = warp_max_nan(Elem<DT>::vmax4_nan(v[k]));
-        float sum = 0.0f;
-        if (m != kNegInf) {  // (of +inf or NaN: a NaN)
-            const float2 nm = make_float2(-m, -m), c = make_float2(specv::kLog2e, specv::kLog2e);
-            float2 acc[4];
+        for (int k = 0; k < kUnitPieces; ++k)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                acc[j] = make_float2(0.0f, 0.0f);
+                const int at = first + (k * 4 + j) * 32;
+                v[k][j] = at < n_vec ? load_stream(row + at) : make_uint4(ni, ni, ni, ni);
+            }
+    }
+    float m = kNegInf, own = 0.0f;  // own: of the lane's piece
+#pragma unroll
+    for (int k = 0; k < kUnitPieces; ++k) {
+        const float x = warp_max_nan(Elem<DT>::vmax4_nan(v[k]));
+        m = specv::fmax_nan(m, x);
+        if (lane == k) own = x;
+    }
+    float sum = 0.0f;
+    if (m != kNegInf) {  // (of +inf or NaN: a NaN)
+        const float2 nm = make_float2(-m, -m), c = make_float2(specv::kLog2e, specv::kLog2e);
+        float2 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kUnitPieces; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < Elem<DT>::kPairs; ++i) {
                     // z - m before the product: the lowest finite value does not overflow
                     const float2 d = specv::ffma2(specv::fadd2(Elem<DT>::pair(v[k][j], i), nm), c, make_float2(0.0f, 0.0f));
                     acc[j] = specv::fadd2(acc[j], make_float2(specv::ex2(d.x), specv::ex2(d.y)));
                 }
-            }
-            const float2 t = specv::fadd2(specv::fadd2(acc[0], acc[1]), specv::fadd2(acc[2], acc[3]));
-            sum = t.x + t.y;
+        const float2 t = specv::fadd2(specv::fadd2(acc[0], acc[1]), specv::fadd2(acc[2], acc[3]));
+        sum = t.x + t.y;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        }
-        if (lane == 0) part[static_cast<int64_t>(r) * n_pieces + p0 + k] = make_float2(m, sum);
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     }
+    if (lane == 0) part.unit[static_cast<int64_t>(r) * part.n_units + u] = make_float2(m, sum);
+    const int p = u * kUnitPieces + lane;
+    if (lane < kUnitPieces && p < part.n_pieces) part.piece[static_cast<int64_t>(r) * part.n_pieces + p] = own;
 }
 
 // ------------------------------------------------------------ the n best
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 512;
-constexpr float kBinsPerNat = 16.0f;
-constexpr int kList = 512;        // what is put in order by counting
-constexpr float kMagnitude = 1e4f;  // bases and scores up to here: an fp32 score is off by less than 2^-9
+constexpr int kBins = 256;
+constexpr int kList = 512;          // candidates that are put in order by counting
+constexpr int kChosen = 256;        // pieces that are read again
+constexpr int kValues = kMaxN * kCells;
+constexpr int kTaken = kValues * 4 / kCellBytes;  // cells that are looked at one candidate a thread
+constexpr float kMagnitude = 1e4f;  // bases up to here: an fp32 score is off by less than 2^-9
+constexpr int kHeld = 4;            // pieces whose scores a lane holds
 
 // The score in fp32; -inf for no candidate alone.
 __device__ __forceinline__ float approx_score(float z, float top, float base) {
     return z == kNegInf ? z : fmaxf(base + (z - top), -3.402823466e38f);
+}
+
+// Exact scores are kept in two fp32 terms, x the value rounded and y the rest (48 bits): a step of
+// 64-bit arithmetic takes 65 cycles on this GPU.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
+}
+// a + b, a in two terms
+__device__ __forceinline__ float2 add_to(float2 a, float b) {
+    const float2 s = two_sum(a.x, b);
+    return make_float2(s.x, __fadd_rn(a.y, s.y));
+}
+__device__ __forceinline__ float2 rounded(float2 a) {
+    const float s = __fadd_rn(a.x, a.y);
+    return make_float2(s, __fsub_rn(a.y, __fsub_rn(s, a.x)));
 }
 
 struct Item {
@@ -125,122 +160,290 @@ struct Item {
     int at;                  // then its position: smaller first
 };
 
-__device__ __forceinline__ unsigned long long key_of(double s) {
-    const unsigned long long u = __double_as_longlong(s + 0.0);
-    return u >> 63 ? ~u : u | 1ull << 63;
+// A position: row, then token (up to 2^24 of them).
+constexpr int kRowShift = 25;
+static_assert(SPEC_MAX_V <= 1 << (kRowShift - 1) && kMaxBeams <= 1 << (31 - kRowShift), "a position in 31 bits");
+
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
-__device__ __forceinline__ double score_of(unsigned long long k) {
-    return __longlong_as_double(k >> 63 ? k & ~(1ull << 63) : ~k);
+__device__ __forceinline__ float score_of(unsigned long long key) {
+    const uint32_t u = static_cast<uint32_t>(key >> 32);
+    return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xffffffffu));
+}
+// The key of base + (z - top).
+__device__ __forceinline__ unsigned long long key_of(float z, float top, float2 base) {
+    const float2 d = two_sum(z, -top);
+    float2 s = make_float2(fmaxf(d.x, -3.402823466e38f), 0.0f);
+    if (d.x > -1e30f) {  // (below, it is nowhere near another row's)
+        s = add_to(base, d.x);
+        s = rounded(make_float2(s.x, s.y + d.y));
+    }
+    return static_cast<unsigned long long>(ordered(s.x)) << 32 | ordered(s.y);
 }
 
 struct Shared {
     // a candidate's score is base + (z - top): top the row's largest logit, base the
     // row's score less ln sum exp(z - top).  An ended row: 0 and its score.
-    double base[kMaxBeams];
-    float base32[kMaxBeams], top[kMaxBeams];
+    float2 base[kMaxBeams];
+    float top[kMaxBeams];
     int live[kMaxBeams];      // 0: no candidates, 1: read, 2: ended
-    float value[kMaxN * kCells];
-    int first[kMaxN];         // the places chosen by the last narrowing
+    float2 sum[kMaxBeams];    // of exp(z - top), in two terms
+    int first[kChosen];       // the pieces chosen
     unsigned long long key[kList];
     int at[kList];
-    int bins[kBins];
-    float red[kWarps];
-    int count, bad, cut;
-    float big;  // largest |base|
+    int bins[2][kBins];       // of the pieces, of the candidates
+    int n_pieces, n_cells, count;  // chosen, taken, listed
+    int cell[kTaken];         // row << 20 | cell
+    float best[kMaxBeams / 32];
+    int bad, large;           // a data error; a base that fp32 scores are too coarse for
+    alignas(16) float value[kValues];  // the cells taken; where digits decide, cells' or candidates' logits
 };
+static_assert(kChosen >= kMaxN && kList >= kMaxN, "what the digits' path keeps");
+static_assert(SPEC_MAX_V * 4ll / kCellBytes <= 1 << 20 && kMaxBeams <= 1 << 11, "a row and a cell in 31 bits");
 
-__device__ __forceinline__ float block_max(Shared &sh, float m) {
-    m = warp_max_nan(m);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = sh.red[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = specv::fmax_nan(m, sh.red[w]);
-    return m;
+// Bins by how far a score lies below the best one: 32 to each doubling of
+// 1 + d, so a thirty-second of a nat wide at the best score and an eighth at three nats below it; up to 255 nats.
+constexpr int kBinShift = 18, kBinBase = 0x3f800000 >> kBinShift;
+__device__ __forceinline__ void count_in_bins(int *bins, float most, float a) {
+    const int bin = (__float_as_int(1.0f + (most - a)) >> kBinShift) - kBinBase;  // (a <= most but for rounding)
+    if (bin < kBins) atomicAdd(&bins[max(bin, 0)], 1);
 }
 
-// The n first items of `count` in the order (score descending, then
-// position) into sh.key / sh.at [0 .. result).  approx(i): the score in fp32, -inf for no item;
-// item(i): exactly.
-// Usually: a histogram of the fp32 scores gives a border that the n-th of
-// them lies above; what lies above it (with twice the fp32 scores' error as a
-// margin) is put in order by counting, for each, the ones before it.  Where scores are too
-// large for that margin, or too many lie close together: digit by digit.
-template <class Approx, class Exact>
-__device__ int narrow(Shared &sh, int64_t count, int n, Approx approx, Exact item) {
-    const int tid = threadIdx.x;
-    float m = kNegInf;
-    for (int64_t i = tid; i < count; i += kThreads) m = fmaxf(m, approx(i));
-    for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
-    if (tid == 0) sh.count = 0, sh.cut = kBins;
-    m = block_max(sh, m);
-    if (m == kNegInf) return 0;
-    bool listed = fabsf(m) <= kMagnitude && sh.big <= kMagnitude;
-    if (listed) {
-        for (int64_t i = tid; i < count; i += kThreads) {
-            const float a = approx(i);
-            const float d = (m - a) * kBinsPerNat;
-            if (d < static_cast<float>(kBins)) atomicAdd(&sh.bins[static_cast<int>(d)], 1);
-        }
-        __syncthreads();
-        if (tid < 32) {
-            constexpr int per = kBins / 32;
-            int own = 0;
-            for (int j = 0; j < per; ++j) own += sh.bins[tid * per + j];
-            int incl = own;
+// A border that the n-th counted score lies above: the lower end of its bin, less a sixty-fourth (twice an
+// fp32 score's error is 2^-8).  -inf: fewer than n are in the bins.  By each warp for itself.
+__device__ __forceinline__ float border_of(const int *bins, float most, int n) {
+    const int lane = threadIdx.x & 31;
+    int own[8], sum = 0;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, incl, off);
-                if (tid >= off) incl += t;
-            }
-            if (incl >= n && incl - own < n) {
-                int c = incl - own, j = 0;
-                while ((c += sh.bins[tid * per + j]) < n) ++j;
-                sh.cut = tid * per + j;
-            }
-        }
-        __syncthreads();
-        // a quarter of a bin: twice an fp32 score's error is a sixteenth
-        const float border = sh.cut == kBins ? kNegInf : m - (sh.cut + 1.25f) / kBinsPerNat;
-        for (int64_t i = tid; i < count; i += kThreads) {
-            const float a = approx(i);
-            if (a != kNegInf && a >= border) {
-                const int p = atomicAdd(&sh.count, 1);
-                if (p < kList) {
-                    const Item x = item(i);
-                    sh.key[p] = x.key, sh.at[p] = x.at;
-                }
-            }
-        }
-        __syncthreads();
-        listed = sh.count <= kList;
+    for (int k = 0; k < 2; ++k) {
+        const int4 v = reinterpret_cast<const int4 *>(bins)[lane * 2 + k];
+        own[4 * k] = v.x, own[4 * k + 1] = v.y, own[4 * k + 2] = v.z, own[4 * k + 3] = v.w;
     }
-    if (!listed) {
-        // the n-th key, eight bits at a time, then the n-th position of those that have it
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += own[k], own[k] = sum;
+    int before = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += t;
+    }
+    const unsigned reach = __ballot_sync(0xffffffffu, before >= n);
+    if (!reach) return kNegInf;
+    before -= sum;
+    int bin = lane * 8;
+#pragma unroll
+    for (int k = 0; k < 7; ++k) bin += before + own[k] < n;
+    bin = __shfl_sync(0xffffffffu, bin, __ffs(reach) - 1);
+    return most - (__int_as_float((bin + 1 + kBinBase) << kBinShift) - 1.0f) - 0.015625f;
+}
+
+// The place of each listed item: the number of those before it, counted by eight
+// lanes.  put(item, place) is called once for each, by one thread.
+template <class Put>
+__device__ __forceinline__ void by_rank(const Shared &sh, int found, Put put) {
+    const int part = threadIdx.x & 7;
+#pragma unroll 1
+    for (int p0 = 0; p0 < found; p0 += kThreads / 8) {
+        const int p = p0 + (threadIdx.x >> 3);
+        const Item x = p < found ? Item{sh.key[p], sh.at[p]} : Item{0, 0};
+        int before = 0;
+        if (p < found)
+#pragma unroll 1
+            for (int q = part; q < found; q += 8) {
+                const unsigned long long k = sh.key[q];
+                before += k > x.key || (k == x.key && sh.at[q] < x.at);
+            }
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+        if (p < found && part == 0) put(x, before);
+    }
+}
+
+template <int DT>
+struct Group {
+    const uint4 *logits;  // of its first row
+    const float *piece;   // its pieces' largest logits
+    int W, V, n_vec, n_pieces;
+
+    // Lane's cell of piece p of row w, which is read.
+    __device__ __forceinline__ void load_cell(int w, int p, int lane, uint4 (&v)[kCellBytes / 16]) const {
+        const uint4 *row = logits + static_cast<int64_t>(w) * n_vec;
+        constexpr uint32_t ni = Elem<DT>::kNegInfWord;
+#pragma unroll
+        for (int j = 0; j < kCellBytes / 16; ++j) {
+            const int at = p * 128 + lane * (kCellBytes / 16) + j;
+            v[j] = at < n_vec ? __ldg(row + at) : make_uint4(ni, ni, ni, ni);
+        }
+    }
+};
+
+// The usual way: a histogram of the pieces' fp32 scores gives a border that
+// the n-th best of them lies above; of the pieces above it, the candidates above
+// it are listed, by way of the cells above it.  If the cells or the candidates are too many (tokens in
+// order of their frequency: the best ones lie in a few pieces; or short rows), a histogram of theirs gives a
+// nearer border.  Returns how many are listed, -1 if they are too many still.
+template <int DT>
+__device__ __forceinline__ int list_candidates(Shared &sh, const Group<DT> &g, const float (&mine)[kHeld], int share, float most, int n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float border = 0.0f;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {  // counted, then chosen
+#pragma unroll 1
+        for (int w = warp >> share; w < g.W; w += kWarps >> share) {
+            const int live = sh.live[w];
+            if (live == 0) continue;
+            const float top = sh.top[w], base = sh.base[w].x;
+            const int first = ((warp & ((1 << share) - 1)) << 5) + lane;
+            const auto see = [&](float z, int p) {
+                const float a = approx_score(z, top, base);
+                if (a == kNegInf) return;
+                if (pass == 0) {
+                    count_in_bins(sh.bins[0], most, a);
+                } else if (a >= border) {
+                    const int i = atomicAdd(&sh.n_pieces, 1);
+                    if (i < kChosen) sh.first[i] = w << 16 | p;  // (at most 2^15 pieces)
+                }
+            };
+            if (live == 2) {
+                if (first == 0) see(0.0f, 0);
+                continue;
+            }
+            int p = first;
+            if (w < kWarps) {  // the lane holds the first of them
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k, p += 32 << share) see(mine[k], p);
+            }
+#pragma unroll 1
+            for (; p < g.n_pieces; p += 32 << share) see(g.piece[static_cast<int64_t>(w) * g.n_pieces + p], p);
+        }
         __syncthreads();
+        if (pass == 0) border = border_of(sh.bins[0], most, n);
+    }
+    const int chosen = sh.n_pieces;
+    if (chosen > kChosen) return -1;
+    constexpr int cell_vecs = kCellBytes / 16, per_cell = kCellBytes / Elem<DT>::kBytes;
+    sh.bins[0][threadIdx.x & (kBins - 1)] = 0;
+    // the chosen pieces' cells that reach above the border
+    int taken;
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+        constexpr int flight = 3;  // pieces of a warp under way before the first is looked at
+#pragma unroll 1
+        for (int c0 = warp; c0 < chosen; c0 += flight * kWarps) {
+            uint4 v[flight][cell_vecs];
+            int f[flight];
+#pragma unroll
+            for (int k = 0; k < flight; ++k) {
+                f[k] = c0 + k * kWarps < chosen ? sh.first[c0 + k * kWarps] : -1;
+                if (f[k] >= 0 && sh.live[f[k] >> 16] == 1) g.load_cell(f[k] >> 16, f[k] & 0xffff, lane, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < flight; ++k) {
+                if (f[k] < 0) break;
+                const int w = f[k] >> 16;
+                float z = lane == 0 ? 0.0f : kNegInf;  // of an ended row
+                if (sh.live[w] == 1) z = Elem<DT>::vmax4_nan(v[k]);
+                const float a = approx_score(z, sh.top[w], sh.base[w].x);
+                if (a == kNegInf || a < border) continue;
+                if (round == 0) count_in_bins(sh.bins[1], most, a);
+                const int i = atomicAdd(&sh.n_cells, 1);
+                if (i >= kTaken) continue;
+                sh.cell[i] = w << 20 | ((f[k] & 0xffff) * kCells + lane);
+#pragma unroll
+                for (int j = 0; j < cell_vecs; ++j) reinterpret_cast<uint4 *>(sh.value)[i * cell_vecs + j] = v[k][j];
+            }
+        }
+        __syncthreads();
+        taken = sh.n_cells;
+        if (taken <= kTaken) break;
+        if (round == 1) return -1;
+        border = border_of(sh.bins[1], most, n);
+        __syncthreads();
+        if (threadIdx.x == 0) sh.n_cells = 0;
+        __syncthreads();
+    }
+    // of those, a candidate per thread
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < taken * per_cell; i += kThreads) {
+            const int c = sh.cell[i / per_cell], w = c >> 20, in_cell = i % per_cell;
+            float z = DT == SPEC_F32 ? sh.value[i] : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(sh.value)[i]) << 16);
+            if (sh.live[w] == 2) z = in_cell == 0 ? 0.0f : kNegInf;
+            const float2 base = sh.base[w];
+            const float a = approx_score(z, sh.top[w], base.x);
+            if (a == kNegInf || a < border) continue;
+            if (round == 0) count_in_bins(sh.bins[0], most, a);
+            const int k = atomicAdd(&sh.count, 1);
+            if (k < kList) {
+                sh.key[k] = key_of(z, sh.top[w], base);
+                sh.at[k] = w << kRowShift | ((c & 0xfffff) * per_cell + in_cell);
+            }
+        }
+        __syncthreads();
+        const int found = sh.count;
+        if (found <= kList) return found;
+        if (round == 1) return -1;
+        border = border_of(sh.bins[0], most, n);
+        __syncthreads();
+        if (threadIdx.x == 0) sh.count = 0;
+        __syncthreads();
+    }
+}
+
+// Any scores and any number of equal ones: the first n pieces, of their cells the first n, of those the
+// first n candidates, each by digits.  Rare, so it is kept small: the code of a
+// kernel that runs each instruction once is fetched from memory.
+template <int DT>
+struct Digits {
+    static constexpr int kCellVecs = kCellBytes / 16, kPerCell = kCellBytes / Elem<DT>::kBytes;
+
+    // Whether there is an item i of a level (0: pieces, 1: cells of sh.first's pieces, 2: candidates of sh.first's
+    // cells), and it.  An ended row is a piece, a cell, a candidate of its own.
+    __device__ static __noinline__ bool item(const Shared &sh, const Group<DT> &g, int level, int i, Item *x) {
+        const int from = level == 0 ? i : sh.first[i / (level == 1 ? kCells : kPerCell)];
+        const int w = from / (level == 2 ? g.n_pieces * kCells : g.n_pieces);
+        float z;
+        if (level > 0) z = sh.value[i];
+        else z = sh.live[w] == 1 ? g.piece[i] : sh.live[w] == 2 && i == w * g.n_pieces ? 0.0f : kNegInf;
+        x->key = key_of(z, sh.top[w], sh.base[w]);
+        x->at = level == 0 ? i : level == 1 ? from * kCells + i % kCells : w << kRowShift | ((from - w * g.n_pieces * kCells) * kPerCell + i % kPerCell);
+        return z != kNegInf;
+    }
+
+    // The n first of a level's items in the order (score descending, then position) into sh.key / sh.at
+    // [0 .. result), in no order: the n-th key, eight bits at a time, then the n-th position of
+    // those that have it.
+    __device__ static __noinline__ int first(Shared &sh, const Group<DT> &g, int level, int count, int n) {
+        const int tid = threadIdx.x;
         unsigned long long key = 0;
         int at = -1, left = n;
         bool all = false;
+        Item x;
+        __syncthreads();
+#pragma unroll 1
         for (int digit = 0; digit < 12 && !all; ++digit) {
             const bool by_key = digit < 8;
             const int shift = by_key ? 56 - 8 * digit : 24 - 8 * (digit - 8);
             if (digit == 8) at = 0;
-            for (int i = tid; i < 256; i += kThreads) sh.bins[i] = 0;
+            if (tid < 256) sh.bins[0][tid] = 0;
             __syncthreads();
-            for (int64_t i = tid; i < count; i += kThreads) {
-                if (approx(i) == kNegInf) continue;
-                const Item x = item(i);
+#pragma unroll 1
+            for (int i = tid; i < count; i += kThreads) {
+                if (!item(sh, g, level, i, &x)) continue;
                 if (by_key) {
                     if (digit == 0 || x.key >> (shift + 8) == key >> (shift + 8))
-                        atomicAdd(&sh.bins[255 - static_cast<int>(x.key >> shift & 255)], 1);
+                        atomicAdd(&sh.bins[0][255 - static_cast<int>(x.key >> shift & 255)], 1);
                 } else if (x.key == key && (digit == 8 || x.at >> (shift + 8) == at >> (shift + 8))) {
-                    atomicAdd(&sh.bins[x.at >> shift & 255], 1);
+                    atomicAdd(&sh.bins[0][x.at >> shift & 255], 1);
                 }
             }
             __syncthreads();
             int c = 0, j = 0;
-            while (j < 256 && c + sh.bins[j] < left) c += sh.bins[j++];
+#pragma unroll 1
+            while (j < 256 && c + sh.bins[0][j] < left) c += sh.bins[0][j++];
             all = j == 256;  // fewer than n items
             if (!all) {
                 left -= c;
@@ -251,40 +454,70 @@ __device__ int narrow(Shared &sh, int64_t count, int n, Approx approx, Exact ite
         }
         if (tid == 0) sh.count = 0;
         __syncthreads();
-        for (int64_t i = tid; i < count; i += kThreads) {
-            if (approx(i) == kNegInf) continue;
-            const Item x = item(i);
-            if (all || x.key > key || (x.key == key && x.at <= at)) {
+#pragma unroll 1
+        for (int i = tid; i < count; i += kThreads)
+            if (item(sh, g, level, i, &x) && (all || x.key > key || (x.key == key && x.at <= at))) {
                 const int p = atomicAdd(&sh.count, 1);
                 if (p < kList) sh.key[p] = x.key, sh.at[p] = x.at;
             }
-        }
         __syncthreads();
+        const int found = min(sh.count, n);
+        if (level < 2 && tid < found) sh.first[tid] = sh.at[tid];
+        __syncthreads();
+        return found;
     }
-    // in order: each goes to the place that the number of those before it says
-    const int found = min(sh.count, kList);
-    Item mine[kList / kThreads];
-    int rank[kList / kThreads];
-#pragma unroll
-    for (int k = 0; k < kList / kThreads; ++k) {
-        const int p = tid + k * kThreads;
-        rank[k] = kList;
-        if (p < found) {
-            mine[k] = Item{sh.key[p], sh.at[p]};
-            int before = 0;
-            for (int q = 0; q < found; ++q) {
-                const unsigned long long kq = sh.key[q];
-                before += kq > mine[k].key || (kq == mine[k].key && sh.at[q] < mine[k].at);
+
+    __device__ static __noinline__ int narrow(Shared &sh, const Group<DT> &g, int n) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        int chosen = first(sh, g, 0, g.W * g.n_pieces, n);
+#pragma unroll 1
+        for (int c = tid >> 5; c < chosen; c += kWarps) {
+            const int w = sh.first[c] / g.n_pieces, p = sh.first[c] - w * g.n_pieces;
+            float z = lane == 0 ? 0.0f : kNegInf;
+            if (sh.live[w] == 1) {
+                uint4 v[kCellVecs];
+                g.load_cell(w, p, lane, v);
+                z = Elem<DT>::vmax4_nan(v);
             }
-            rank[k] = before;
+            sh.value[c * kCells + lane] = z;
         }
+        chosen = first(sh, g, 1, chosen * kCells, n);
+        const int row_cells = g.n_pieces * kCells;
+#pragma unroll 1
+        for (int i = tid; i < chosen * kPerCell; i += kThreads) {
+            const int cell = sh.first[i / kPerCell], w = cell / row_cells, place = (cell - w * row_cells) * kPerCell + i % kPerCell;
+            float z = kNegInf;
+            if (sh.live[w] == 2) z = i % kPerCell == 0 ? 0.0f : kNegInf;
+            else if (place < g.V) z = Elem<DT>::load1(g.logits + static_cast<int64_t>(w) * g.n_vec, place);
+            sh.value[i] = z;
+        }
+        return first(sh, g, 2, chosen * kPerCell, n);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kList / kThreads; ++k)
-        if (rank[k] < n) sh.key[rank[k]] = mine[k].key, sh.at[rank[k]] = mine[k].at;
-    __syncthreads();
-    return min(found, n);
+};
+
+// ln(s.x + s.y), s.x >= 1, to 5e-9, in two terms: with s.x = 2^k m, 0.75 <= m < 1.5, and t = (m - 1) / (m + 1),
+// ln m = 2 (t + t^3 / 3 + t^5 / 5 + ..).  t is wanted in two terms, the others are below 2^-7 of one.
+__device__ __forceinline__ float2 log_of(float2 s) {
+    const uint32_t u = __float_as_uint(s.x);
+    const int k = static_cast<int>((u - 0x3f400000u) >> 23);
+    const float m = __uint_as_float(u - (static_cast<uint32_t>(k) << 23));
+    const float a = __fsub_rn(m, 1.0f);  // exact
+    const float d = __fadd_rn(m, 1.0f), dl = __fsub_rn(m, __fsub_rn(d, 1.0f));  // m + 1 in two terms
+    const float t = __fdividef(a, d);
+    const float r = __fmaf_rn(-t, dl, __fmaf_rn(-t, d, a));  // what t leaves of the quotient, times d
+    const float q = t * t;
+    float y = 1.0f / 13;
+    y = __fmaf_rn(y, q, 1.0f / 11);
+    y = __fmaf_rn(y, q, 1.0f / 9);
+    y = __fmaf_rn(y, q, 1.0f / 7);
+    y = __fmaf_rn(y, q, 1.0f / 5);
+    y = __fmaf_rn(y, q, 1.0f / 3);
+    // the smaller terms: t^3 y, t's second term, and s.y / s.x
+    const float small = 2.0f * __fmaf_rn(t * q, y, __fdividef(r, d)) + __fdividef(s.y, s.x);
+    constexpr float ln2_hi = 0x1.62e400p-1f;  // 15 bits: k times it is exact
+    constexpr float ln2_lo = static_cast<float>(specv::kLn2D - static_cast<double>(ln2_hi));
+    const float2 h = two_sum(k * ln2_hi, 2.0f * t);
+    return rounded(make_float2(h.x, h.y + __fmaf_rn(static_cast<float>(k), ln2_lo, small)));
 }
 
 // A CTA per group.
@@ -293,16 +526,17 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const void *__restrict
                                                           const float *__restrict__ scores,
                                                           const uint8_t *__restrict__ ended, int end_token,
                                                           const int32_t *__restrict__ offsets, int B, int R, int V,
-                                                          int n_pieces, const float2 *__restrict__ part, int n,
+                                                          const Partial part, int n,
                                                           float *__restrict__ out_scores,
                                                           int32_t *__restrict__ out_tokens,
                                                           int32_t *__restrict__ out_rows, float *__restrict__ out_lse) {
-    __shared__ Shared sh;
+    __shared__ __align__(16) Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x;
     constexpr float nan = __builtin_nanf("");
-    if (tid == 0) sh.bad = 0;
+    static_assert(sizeof(sh.bins) == kThreads * sizeof(int), "a thread clears one");
     bool bad = __ldg(offsets) != 0;
+#pragma unroll 1
     for (int i = tid; i < B; i += kThreads) {
         const int w = __ldg(offsets + i + 1) - __ldg(offsets + i);
         bad |= w < 0 || w > kMaxBeams;
@@ -310,181 +544,135 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const void *__restrict
     bad |= __ldg(offsets + B) > R;
     const bool invalid = __syncthreads_or(bad);
     const int r0 = __ldg(offsets + b), W = invalid ? 0 : __ldg(offsets + b + 1) - r0;
-    // each row's sum, by a warp
+    // where there are fewer rows than warps, 2^share warps take a row's pieces
+    const int share = W == 0 || W > kWarps ? 0 : 31 - __clz(kWarps / W);
+    float score = kNegInf;  // of row tid
+    if (tid < W) {
+        score = __ldg(scores + r0 + tid);
+        sh.live[tid] = score == kNegInf ? 0 : ended && __ldg(ended + r0 + tid) ? 2 : 1;
+    }
+    const Group<DT> g{static_cast<const uint4 *>(logits) + static_cast<int64_t>(r0) * (V / Elem<DT>::kPerVec),
+                      part.piece + static_cast<int64_t>(r0) * part.n_pieces, W, V, V / Elem<DT>::kPerVec, part.n_pieces};
+    if (tid == 0) sh.bad = 0, sh.large = 0, sh.count = 0, sh.n_pieces = 0, sh.n_cells = 0;
+    (&sh.bins[0][0])[tid] = 0;
+    __syncthreads();
     specv::grid_dependency_wait();
     if (invalid && out_lse) {
+#pragma unroll 1
         for (int64_t i = static_cast<int64_t>(b) * kThreads + tid; i < R; i += static_cast<int64_t>(gridDim.x) * kThreads) out_lse[i] = nan;
     }
+    // the largest logits of the pieces that this lane is to look at, and each row's sum, a warp a row
+    float mine[kHeld];
+    if ((warp >> share) < W) {
+        const float *piece = g.piece + static_cast<int64_t>(warp >> share) * g.n_pieces;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int p = ((warp & ((1 << share) - 1)) << 5) + lane + (k * 32 << share);
+            mine[k] = p < g.n_pieces ? piece[p] : kNegInf;
+        }
+    }
+#pragma unroll 1
     for (int w = warp; w < W; w += kWarps) {
-        const float s = __ldg(scores + r0 + w);
-        const int live = s == kNegInf ? 0 : ended && __ldg(ended + r0 + w) ? 2 : 1;
-        bool wrong = s != s || s == -kNegInf;
-        double base = s, lse = nan;
-        float top = 0.0f;
-        if (live == 1) {
-            const float2 *p = part + static_cast<int64_t>(r0 + w) * n_pieces;
-            float m = kNegInf;
-            for (int i = lane; i < n_pieces; i += 32) m = specv::fmax_nan(m, p[i].x);
-            m = warp_max_nan(m);
-            const bool finite = fabsf(m) < -kNegInf;
-            double sum = 0.0;
-            if (finite)
-                for (int i = lane; i < n_pieces; i += 32) {
-                    const float2 x = p[i];
-                    sum += static_cast<double>(x.y * specv::ex2((x.x - m) * specv::kLog2e));
-                }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (m == kNegInf) {
-                base = 0.0, lse = m;
-            } else if (!finite) {
-                wrong = true;
-            } else {
-                const double log_sum = log(sum);
-                top = m, base = static_cast<double>(s) - log_sum, lse = static_cast<double>(m) + log_sum;
-            }
+        if (sh.live[w] != 1) continue;
+        const float2 *unit = part.unit + static_cast<int64_t>(r0 + w) * part.n_units;
+        float top = kNegInf, from = 0.0f;  // from: what the lane's sum is relative to
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+        for (int u = lane; u < part.n_units; u += 32) {
+            const float2 x = unit[u];
+            const float now = specv::fmax_nan(top, x.x), to = now == kNegInf ? 0.0f : now;
+            const float old = top == kNegInf ? 0.0f : specv::ex2((from - to) * specv::kLog2e);
+            sum = add_to(make_float2(sum.x * old, sum.y * old), x.y * specv::ex2((x.x - to) * specv::kLog2e));
+            top = now, from = to;
         }
-        if (lane == 0) {
-            sh.base[w] = base;
-            sh.base32[w] = static_cast<float>(base);
-            sh.top[w] = top;
-            sh.live[w] = live;
+        const float all = warp_max_nan(top);
+        const float old = specv::ex2((top - (all == kNegInf ? 0.0f : all)) * specv::kLog2e);
+        sum.x *= old, sum.y *= old;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const float hi = __shfl_xor_sync(0xffffffffu, sum.x, off), lo = __shfl_xor_sync(0xffffffffu, sum.y, off);
+            sum = add_to(make_float2(sum.x, sum.y + lo), hi);
+        }
+        if (lane == 0) sh.top[w] = all, sh.sum[w] = sum;
+    }
+    __syncthreads();
+    if (tid < kMaxBeams) {
+        float best = kNegInf;
+        if (tid < W) {
+            const int live = sh.live[tid];
+            float2 base = make_float2(score, 0.0f);
+            float lse = nan, top = 0.0f;
+            bool wrong = score != score || score == -kNegInf;
+            if (live == 1) {
+                top = sh.top[tid];
+                if (top == kNegInf) {
+                    lse = top;
+                } else if (!(fabsf(top) < -kNegInf)) {
+                    wrong = true;
+                } else {
+                    const float2 log_sum = log_of(sh.sum[tid]);
+                    base = add_to(make_float2(-log_sum.x, -log_sum.y), score);
+                    base = rounded(base);
+                    const float2 sum = add_to(log_sum, top);
+                    lse = sum.x + sum.y;
+                }
+            }
+            if (out_lse) out_lse[r0 + tid] = lse;
             if (wrong) sh.bad = 1;
-            if (out_lse) out_lse[r0 + w] = static_cast<float>(lse);
+            sh.base[tid] = base, sh.top[tid] = top;
+            if (live && top != kNegInf) {
+                best = base.x;  // of a row's best candidate
+                if (!(fabsf(best) <= kMagnitude)) sh.large = 1;
+            }
         }
+        best = warp_max_nan(best);
+        if (lane == 0) sh.best[warp] = best;
     }
     __syncthreads();
-    if (tid == 0) {
-        float big = 0.0f;
-        for (int w = 0; w < W; ++w)
-            if (sh.live[w]) big = fmaxf(big, fabsf(sh.base32[w]));
-        sh.big = big;
-    }
-    __syncthreads();
-    const auto exact_score = [&](float z, int w) {
-        return key_of(sh.base[w] + (static_cast<double>(z) - static_cast<double>(sh.top[w])));
-    };
+    const float most = fmaxf(sh.best[0], sh.best[1]);
+    const bool fine = !invalid && !sh.bad;
     int found = 0;
-    if (!invalid && !sh.bad && W > 0) {
-        // 1: pieces.  An ended row is a piece of its own.
-        const auto piece = [&](int64_t i, int *w) -> float {  // its largest logit
-            *w = static_cast<int>(i / n_pieces);
-            const int p = static_cast<int>(i) - *w * n_pieces;
-            const int live = sh.live[*w];
-            return live == 1 ? part[static_cast<int64_t>(r0) * n_pieces + i].x : live == 2 && p == 0 ? 0.0f : kNegInf;
-        };
-        int chosen = narrow(
-            sh, static_cast<int64_t>(W) * n_pieces, n,
-            [&](int64_t i) {
-                int w;
-                const float z = piece(i, &w);
-                return approx_score(z, sh.top[w], sh.base32[w]);
-            },
-            [&](int64_t i) {
-                int w;
-                const float z = piece(i, &w);
-                return Item{exact_score(z, w), static_cast<int>(i)};
-            });
-        // 2: cells of the pieces
-        if (tid < chosen) sh.first[tid] = sh.at[tid];
-        __syncthreads();
-        const int n_vec = V / Elem<DT>::kPerVec;
-        constexpr int cell_vecs = kCellBytes / 16, per_cell = kCellBytes / Elem<DT>::kBytes;
-        for (int c = warp; c < chosen; c += kWarps) {
-            const int i = sh.first[c], w = i / n_pieces, p = i - w * n_pieces;
-            float z = lane == 0 ? 0.0f : kNegInf;
-            if (sh.live[w] == 1) {
-                const uint4 *row = reinterpret_cast<const uint4 *>(logits) + static_cast<int64_t>(r0 + w) * n_vec;
-                constexpr uint32_t ni = Elem<DT>::kNegInfWord;
-                uint4 v[cell_vecs];
-#pragma unroll
-                for (int j = 0; j < cell_vecs; ++j) {
-                    const int at = p * 128 + lane * cell_vecs + j;
-                    v[j] = at < n_vec ? __ldg(row + at) : make_uint4(ni, ni, ni, ni);
-                }
-                z = Elem<DT>::vmax4_nan(v);
-            }
-            sh.value[c * kCells + lane] = z;
-        }
-        __syncthreads();
-        const auto row_of = [&](int c) { return sh.first[c] / n_pieces; };
-        chosen = narrow(
-            sh, static_cast<int64_t>(chosen) * kCells, n,
-            [&](int64_t i) {
-                const int w = row_of(static_cast<int>(i) / kCells);
-                return approx_score(sh.value[i], sh.top[w], sh.base32[w]);
-            },
-            [&](int64_t i) {
-                const int c = static_cast<int>(i) / kCells;
-                return Item{exact_score(sh.value[i], row_of(c)), sh.first[c] * kCells + static_cast<int>(i) % kCells};
-            });
-        // 3: the cells' candidates
-        if (tid < chosen) sh.first[tid] = sh.at[tid];
-        __syncthreads();
-        const int row_cells = n_pieces * kCells;
-        for (int i = tid; i < chosen * cell_vecs; i += kThreads) {
-            const int cell = sh.first[i / cell_vecs], w = cell / row_cells;
-            const int at = (cell - w * row_cells) * cell_vecs + i % cell_vecs;
-            float x[Elem<DT>::kPerVec];
-#pragma unroll
-            for (int j = 0; j < Elem<DT>::kPerVec; ++j) x[j] = kNegInf;
-            if (sh.live[w] == 2) {
-                if (i % cell_vecs == 0) x[0] = 0.0f;
-            } else if (at < n_vec) {
-                Elem<DT>::unpack(__ldg(reinterpret_cast<const uint4 *>(logits) + static_cast<int64_t>(r0 + w) * n_vec + at), x);
-            }
-#pragma unroll
-            for (int j = 0; j < Elem<DT>::kPerVec; ++j) sh.value[i * Elem<DT>::kPerVec + j] = x[j];
-        }
-        __syncthreads();
-        const auto row_at = [&](int64_t i) { return sh.first[static_cast<int>(i) / per_cell] / row_cells; };
-        found = narrow(
-            sh, static_cast<int64_t>(chosen) * per_cell, n,
-            [&](int64_t i) {
-                const int w = row_at(i);
-                return approx_score(sh.value[i], sh.top[w], sh.base32[w]);
-            },
-            [&](int64_t i) {
-                return Item{exact_score(sh.value[i], row_at(i)),
-                            sh.first[static_cast<int>(i) / per_cell] * per_cell + static_cast<int>(i) % per_cell};
-            });
+    if (fine && most != kNegInf) {
+        found = sh.large ? -1 : list_candidates(sh, g, mine, share, most, n);
+        if (found < 0) found = Digits<DT>::narrow(sh, g, n);
+        by_rank(sh, found, [&](const Item &x, int place) {
+            if (place >= n) return;
+            const int w = x.at >> kRowShift;
+            const int64_t o = static_cast<int64_t>(b) * n + place;
+            out_scores[o] = score_of(x.key);
+            out_tokens[o] = sh.live[w] == 2 ? end_token : x.at & ((1 << kRowShift) - 1);
+            out_rows[o] = r0 + w;
+        });
     }
-    if (tid < n) {
-        const bool is_bad = invalid || sh.bad;
-        float s = is_bad ? nan : kNegInf;
-        int token = -1, row = -1;
-        if (tid < found) {
-            const int padded = n_pieces * (kPieceBytes / Elem<DT>::kBytes);  // a row's positions
-            const int w = sh.at[tid] / padded;
-            s = static_cast<float>(score_of(sh.key[tid]));
-            token = sh.live[w] == 2 ? end_token : sh.at[tid] - w * padded;
-            row = r0 + w;
-        }
+    if (tid < n && tid >= found) {
         const int64_t o = static_cast<int64_t>(b) * n + tid;
-        out_scores[o] = s, out_tokens[o] = token, out_rows[o] = row;
+        out_scores[o] = fine ? kNegInf : nan, out_tokens[o] = -1, out_rows[o] = -1;
     }
 }
 
-int pieces_of(int V, int dtype) {
+// The partial results of R rows, from `base` on; their bytes.
+size_t partial_of(void *base, int64_t R, int V, int dtype, Partial *part) {
     const int64_t bytes = static_cast<int64_t>(V) * (dtype == SPEC_F32 ? 4 : 2);
-    return static_cast<int>((bytes + kPieceBytes - 1) / kPieceBytes);
+    part->n_pieces = static_cast<int>((bytes + kPieceBytes - 1) / kPieceBytes);
+    part->n_units = (part->n_pieces + kUnitPieces - 1) / kUnitPieces;
+    const size_t units = static_cast<size_t>(R) * part->n_units * sizeof(float2);
+    part->unit = static_cast<float2 *>(base);
+    part->piece = reinterpret_cast<float *>(static_cast<char *>(base) + units);
+    return specv::align_up(units + static_cast<size_t>(R) * part->n_pieces * sizeof(float), 256);
 }
 
 template <int DT>
 int launch(const void *logits, const float *scores, const uint8_t *ended, int32_t end_token, const int32_t *offsets,
            int B, int R, int V, int n, float *out_scores, int32_t *out_tokens, int32_t *out_rows, float *out_lse,
-           float2 *part, cudaStream_t s) {
-    const int n_pieces = pieces_of(V, DT);
-    const int blocks = (n_pieces + kBlockPieces - 1) / kBlockPieces;
-    const int rows = static_cast<int>(std::min<int64_t>(R, static_cast<int64_t>(B) * kMaxBeams));
+           const Partial &part, int rows, cudaStream_t s) {
+    const int blocks = (part.n_units + kBlockUnits - 1) / kBlockUnits;
     if (rows > 0 &&
         !specv::cuda_ok(specv::launch_k(false, rows_kernel<DT>, dim3(static_cast<unsigned>(rows) * blocks), dim3(kRowThreads),
-                                        0, s, logits, scores, ended, offsets, B, R, V, n_pieces, blocks, part),
+                                        0, s, logits, scores, ended, offsets, B, V, blocks, part),
                         "rows_kernel"))
         return SPEC_ERR_CUDA;
     if (!specv::cuda_ok(specv::launch_k(rows > 0, select_kernel<DT>, dim3(B), dim3(kThreads), 0, s, logits, scores, ended,
-                                        end_token, offsets, B, R, V, n_pieces, static_cast<const float2 *>(part), n,
-                                        out_scores, out_tokens, out_rows, out_lse),
+                                        end_token, offsets, B, R, V, part, n, out_scores, out_tokens, out_rows, out_lse),
                         "select_kernel"))
         return SPEC_ERR_CUDA;
     return SPEC_OK;
@@ -498,7 +686,8 @@ extern "C" {
 size_t spec_beam_workspace_bytes(int R, int V, int dtype) {
     if (R < 0 || specv::check_common(0, V, dtype) != SPEC_OK) return 0;
     const int64_t rows = std::min<int64_t>(R, static_cast<int64_t>(SPEC_MAX_B) * SPEC_MAX_BEAMS);
-    return specv::align_up(static_cast<size_t>(std::max<int64_t>(rows, 1)) * specbeam::pieces_of(V, dtype) * sizeof(float2), 256);
+    specbeam::Partial part;
+    return specbeam::partial_of(nullptr, std::max<int64_t>(rows, 1), V, dtype, &part);
 }
 
 int spec_beam_select(const void *logits, const float *scores, const uint8_t *ended, int32_t end_token,
@@ -512,11 +701,13 @@ int spec_beam_select(const void *logits, const float *scores, const uint8_t *end
     if (!offsets || !out_scores || !out_tokens || !out_rows || (R > 0 && (!logits || !scores || !workspace)))
         return SPEC_ERR_INVALID_ARG;
     if (!specv::aligned16(logits) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SPEC_ERR_ALIGNMENT;
-    if (R > 0 && workspace_bytes < spec_beam_workspace_bytes(std::min<int64_t>(R, static_cast<int64_t>(B) * SPEC_MAX_BEAMS), V, dtype))
-        return SPEC_ERR_WORKSPACE;
+    // rows of no group are not read
+    const int rows = static_cast<int>(std::min<int64_t>(R, static_cast<int64_t>(B) * SPEC_MAX_BEAMS));
+    specbeam::Partial part;
+    if (specbeam::partial_of(workspace, rows, V, dtype, &part) > workspace_bytes && rows > 0) return SPEC_ERR_WORKSPACE;
     const auto run = dtype == SPEC_F32 ? specbeam::launch<SPEC_F32> : specbeam::launch<SPEC_BF16>;
     return run(logits, scores, ended, end_token, offsets, B, R, V, n, out_scores, out_tokens, out_rows, out_lse,
-               static_cast<float2 *>(workspace), static_cast<cudaStream_t>(stream));
+               part, rows, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

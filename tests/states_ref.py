@@ -26,7 +26,8 @@ def beam_rows(z, scores, ended=None):
 
 
 def beam_select(z, scores, offsets, n, ended=None, end_token=0):
-    """(scores [B, n] float64, tokens, rows, lse [R], every candidate's score [R, V])."""
+    """(scores [B, n] float64, tokens, rows, lse [R], every candidate's score [R, V], z).  Within a row the order is the
+    logits', also where scores are so large that 64 bits do not tell them apart."""
     B, V = len(offsets) - 1, z.shape[1]
     every, lse = beam_rows(z, scores, ended)
     os, ot, orow = np.full((B, n), -np.inf), np.full((B, n), -1, np.int32), np.full((B, n), -1, np.int32)
@@ -41,13 +42,13 @@ def beam_select(z, scores, offsets, n, ended=None, end_token=0):
             if scores[r] == -np.inf:
                 continue
             if ended is not None and ended[r]:
-                found.append((-np.float64(scores[r]), int(r), end_token))
+                found.append((-np.float64(scores[r]), int(r), 0.0, end_token))
                 continue
-            top = np.lexsort((np.arange(V), -every[r]))[:n]
-            found += [(-every[r, v], int(r), int(v)) for v in top if every[r, v] > -np.inf]
-        for i, (s, r, v) in enumerate(sorted(found)[:n]):
+            top = np.lexsort((np.arange(V), -z[r].astype(np.float64)))[:n]
+            found += [(-every[r, v], int(r), -float(z[r, v]), int(v)) for v in top if every[r, v] > -np.inf]
+        for i, (s, r, _, v) in enumerate(sorted(found)[:n]):
             os[b, i], orow[b, i], ot[b, i] = -s, r, v
-    return os, ot, orow, lse, every
+    return os, ot, orow, lse, every, z
 
 
 def reorder(x, rows, offsets, slots=None, lengths=None, position=None):

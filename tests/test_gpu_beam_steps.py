@@ -76,7 +76,7 @@ def test_steps(sv):
                 z0 = model(h)[0]
                 zs[w] = np.where(c > 0, z0 - f32(0.7) * c, z0)
             sc = np.array([p[0] for p in plain[b]]).astype(f32)
-            os, ot, orow, _, _ = ref.beam_select(zs, sc, [0, W], W, np.array([p[2] for p in plain[b]]), END)
+            os, ot, orow = ref.beam_select(zs, sc, [0, W], W, np.array([p[2] for p in plain[b]]), END)[:3]
             assert np.diff(os[0]).max() < -1e-5  # no two so close that their order is open
             plain[b] = [(os[0, i], plain[b][orow[0, i]][1] + [int(ot[0, i])], ot[0, i] == END) for i in range(W)]
         assert histories == [h for b in range(B) for _, h, _ in plain[b]]

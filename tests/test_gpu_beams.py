@@ -44,7 +44,7 @@ def logits(z, dtype):
 
 def compare(got, want, rows=None):
     s, t, r = (x.cpu().numpy() for x in got[:3])
-    ws, wt, wr, wlse, every = want
+    ws, wt, wr, wlse, every, z = want
     assert (np.isnan(s) == np.isnan(ws)).all()
     for b in range(len(ws)):
         if np.isnan(ws[b, 0]):
@@ -67,8 +67,7 @@ def compare(got, want, rows=None):
             assert abs(every[r[b, i], t[b, i]] - ws[b, i]) <= 2 * TOL, (b, i)
             assert r[b, i] != wr[b, i], (b, i)
         for row in set(r[b][~empty]):
-            own = [every[row, v] for rr, v in pairs if rr == row]
-            order = [(-e, v) for e, (rr, v) in zip(own, [p for p in pairs if p[0] == row])]
+            order = [(-z[row, v], v) for rr, v in pairs if rr == row]
             assert order == sorted(order)
     if len(got) > 3:
         lse, wlse = got[3].cpu().numpy()[:rows], wlse[:rows]  # (rows behind the last group's are not written)
