@@ -3,12 +3,12 @@
 // include/spec_verify.h.
 //
 // A move copies slot s(rows[i]) to slot s(i), for every entry i of a group whose two
-// slots differ, as if all moves of the group were made at once.  A thread
-// takes one column (the same 16 bytes or fewer of every slot) of a whole
-// group, so that threads never wait on one another.  It loads the column of up to
-// kBatch moves' sources before it stores any; with more moves they are put in
-// an order in which none reads what an earlier one wrote, except that of each cycle
-// the first destination is kept in a register for the cycle's last move.
+// slots differ, as if all moves of the group were made at once.  A CTA takes some
+// bytes of one run, the same of all the group's slots: it has read them of every source
+// before it writes any, so that no CTA waits on another and nothing is kept
+// outside of it.  Where positions are multiples of 16 bytes the copy engine moves the
+// bytes, by way of shared memory: each distinct source once in, and out to every
+// destination of it; a warp does no more than to start the copies and to wait for them.
 #include <algorithm>
 #include <cstdint>
 
@@ -20,38 +20,43 @@
 namespace specstate {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxGroup = SPEC_MAX_BEAMS;
 constexpr int kMaxStates = SPEC_MAX_STATES;
-constexpr int kBatch = 8;       // moves whose columns a thread holds at once
-constexpr int kColumns = 4096;  // of a CTA: 64 KB of a slot in columns of 16 bytes
+constexpr int kStages = 4;          // chunks of a CTA under way
+constexpr int kRing = 44 * 1024;    // bytes of them: 4 CTAs and 176 KB to an SM
+constexpr int kMinSpan = 16 * 1024;
+constexpr int kMaxSpan = 128 * 1024;
+constexpr int kCtas = 152 * 16;     // a span is made shorter until there are so many
 
 struct State {
     unsigned char *data;
     int64_t plane, slot, run, unit;  // bytes from one to the next; run holds run / unit positions
-    int planes, runs, chunks;        // chunks: CTAs of a run
-    int width;                       // bytes of a column
+    int planes, runs, spans;         // spans: CTAs of a run
+    int width;                       // bytes of a column; 16: moved by the copy engine
     int first;                       // its first CTA of a group
 };
 
 struct Job {
     State state[kMaxStates];
     int n_states, S, B, R;
-    int ctas, columns;  // CTAs of a group, columns of a CTA
+    int ctas, span;  // CTAs of a group, bytes of a CTA (of each slot)
     const int32_t *rows, *offsets, *slots, *lengths;
 };
 
-// The moves of a group in their order.
+// The moves of a group.
 struct Moves {
-    int count;
-    int from[kMaxGroup], to[kMaxGroup], length[kMaxGroup];
-    int keep[kMaxGroup];  // positions of its destination to keep before it is overwritten; 0: none
-    bool kept[kMaxGroup];  // takes what was kept instead of its source
+    int count, n_sources;
+    // of each distinct source: its slot and the positions that are moved
+    int source[kMaxGroup], length[kMaxGroup];
+    // of each move: its destination and which source it has
+    int to[kMaxGroup], from[kMaxGroup];
 };
 
 struct Scratch {
-    int slot[kMaxGroup], source[kMaxGroup], length[kMaxGroup];
-    int readers[kMaxGroup];  // moves to come that read the slot; a move made: -1
+    int slot[kMaxGroup];
+    int index[kMaxGroup];  // entries that are sources: which one; else -1
+    unsigned sources[2], moves[2];
 };
 
 // Leaves mv.count = 0 for a group that stays as it is.
@@ -63,7 +68,6 @@ __device__ void find_moves(const Job &job, int b, Moves &mv, Scratch &sc) {
         bad |= w < 0 || w > kMaxGroup;
     }
     if (tid == 0) mv.count = 0;
-    if (tid < kMaxGroup) sc.readers[tid] = 0;
     const int r0 = __ldg(job.offsets + b);
     if (__syncthreads_or(bad)) return;
     const int W = __ldg(job.offsets + b + 1) - r0;
@@ -77,93 +81,135 @@ __device__ void find_moves(const Job &job, int b, Moves &mv, Scratch &sc) {
     }
     if (__syncthreads_or(bad)) return;
     int length = 0x7fffffff;
+    if (tid < kMaxGroup) sc.index[tid] = -1;
+    __syncthreads();
     if (tid < W) {
         for (int i = 0; i < W; ++i) bad |= i != tid && sc.slot[i] == slot;
         if (source != tid && job.lengths) length = __ldg(job.lengths + sc.slot[source]);
         if (length <= 0) source = tid;
-        sc.source[tid] = source, sc.length[tid] = length;
-        if (source != tid) atomicAdd(&sc.readers[source], 1);
+        if (source != tid) sc.index[source] = 0;
     }
     if (__syncthreads_or(bad)) return;
-    if (tid == 0) {
-        int n = 0;
-        const auto make = [&](int e) {
-            mv.from[n] = sc.slot[sc.source[e]], mv.to[n] = sc.slot[e], mv.length[n] = sc.length[e];
-            mv.keep[n] = 0, mv.kept[n] = false;
-            sc.readers[e] = -1;
-            ++n;
-        };
-        // moves into slots that nothing reads any more; each may free its source's slot
-        for (int i = 0; i < W; ++i)
-            for (int e = i; sc.readers[e] == 0 && sc.source[e] != e; e = sc.source[e]) {
-                make(e);
-                if (--sc.readers[sc.source[e]] != 0) break;
-            }
-        // what is left are cycles
-        for (int i = 0; i < W; ++i) {
-            if (sc.readers[i] < 0 || sc.source[i] == i) continue;
-            const int first = n;
-            int e = i;
-            do {
-                const int next = sc.source[e];
-                make(e);
-                e = next;
-            } while (e != i);
-            mv.keep[first] = mv.length[n - 1], mv.kept[n - 1] = true;
-        }
-        mv.count = n;
+    const bool moves = tid < W && source != tid, is_source = tid < kMaxGroup && sc.index[tid] == 0;
+    const unsigned with_move = __ballot_sync(0xffffffffu, moves), with_source = __ballot_sync(0xffffffffu, is_source);
+    if ((tid & 31) == 0 && tid < kMaxGroup) sc.moves[tid >> 5] = with_move, sc.sources[tid >> 5] = with_source;
+    __syncthreads();
+    const unsigned below = (1u << (tid & 31)) - 1;
+    if (is_source) {
+        const int at = __popc(with_source & below) + (tid >= 32 ? __popc(sc.sources[0]) : 0);
+        sc.index[tid] = at;
+        mv.source[at] = slot;
     }
+    __syncthreads();
+    if (moves) {
+        const int at = __popc(with_move & below) + (tid >= 32 ? __popc(sc.moves[0]) : 0);
+        mv.to[at] = slot, mv.from[at] = sc.index[source];
+        mv.length[sc.index[source]] = length;  // (the same of all moves of a source)
+    }
+    if (tid == 0) mv.count = __popc(sc.moves[0]) + __popc(sc.moves[1]), mv.n_sources = __popc(sc.sources[0]) + __popc(sc.sources[1]);
     __syncthreads();
 }
 
-template <class Vec>
-__device__ __forceinline__ void move_columns(const State &st, unsigned char *base, const Moves &mv, int64_t c0,
-                                             int columns) {
-    const int n = mv.count;
-    for (int k = threadIdx.x; k < columns; k += kThreads) {
-        const int64_t byte = (c0 + k) * static_cast<int64_t>(sizeof(Vec));
-        if (byte >= st.run) break;
-        const int position = static_cast<int>(byte / st.unit);
-        Vec kept{};
-        for (int i0 = 0; i0 < n; i0 += kBatch) {
-            Vec v[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int i = i0 + j;
-                if (i < n) {
-                    if (mv.kept[i]) v[j] = kept;
-                    else if (position < mv.length[i]) v[j] = *reinterpret_cast<const Vec *>(base + mv.from[i] * st.slot + byte);
-                    if (position < mv.keep[i]) kept = *reinterpret_cast<const Vec *>(base + mv.to[i] * st.slot + byte);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int i = i0 + j;
-                if (i < n && position < mv.length[i]) *reinterpret_cast<Vec *>(base + mv.to[i] * st.slot + byte) = v[j];
-            }
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src_smem, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(specv::smem_u32(src_smem)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+
+// Bytes [begin, end) of a run, in chunks through a ring, by one warp.  A wait that runs out (2 s; a copy
+// that never comes) leaves the rest as it was.
+__device__ void move_bulk(const State &st, unsigned char *base, const Moves &mv, int64_t begin, int64_t end, unsigned char *ring, uint64_t *full) {
+    const int lane = threadIdx.x, D = mv.n_sources, n = mv.count;
+    // (at least 128 bytes)
+    const int chunk = static_cast<int>(min(int64_t{kRing} / (kStages * D), int64_t{16384})) & ~63;
+    const int chunks = static_cast<int>((end - begin + chunk - 1) / chunk);
+    // what is moved of source k in chunk c
+    const auto bytes_of = [&](int k, int c) {
+        const int64_t most = min(end, static_cast<int64_t>(mv.length[k]) * st.unit) - (begin + static_cast<int64_t>(c) * chunk);
+        return static_cast<uint32_t>(max(int64_t{0}, min(most, static_cast<int64_t>(chunk))));
+    };
+    const auto load = [&](int c) {
+        unsigned char *stage = ring + (c % kStages) * D * chunk;
+        uint64_t *bar = full + c % kStages;
+        uint32_t sum = 0;
+        for (int k = lane; k < D; k += 32) sum += bytes_of(k, c);
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) specv::mbar_arrive_expect_tx(bar, sum);
+        __syncwarp();
+        for (int k = lane; k < D; k += 32) {
+            const uint32_t bytes = bytes_of(k, c);
+            if (bytes) specv::bulk_g2s(stage + k * chunk, base + mv.source[k] * st.slot + begin + static_cast<int64_t>(c) * chunk, bytes, bar);
         }
+    };
+    for (int c = 0; c < min(chunks, kStages - 1); ++c) load(c);
+    int c = 0;
+    for (; c < chunks; ++c) {
+        if (!__all_sync(0xffffffffu, specv::mbar_wait_bounded(full + c % kStages, (c / kStages) & 1))) break;
+        const unsigned char *stage = ring + (c % kStages) * D * chunk;
+        for (int i = lane; i < n; i += 32) {
+            const uint32_t bytes = bytes_of(mv.from[i], c);
+            if (bytes) bulk_s2g(base + mv.to[i] * st.slot + begin + static_cast<int64_t>(c) * chunk, stage + mv.from[i] * chunk, bytes);
+        }
+        bulk_commit();
+        if (c + kStages - 1 < chunks) {  // into the stage whose chunk was written the turn before
+            bulk_wait_read<1>();
+            __syncwarp();
+            load(c + kStages - 1);
+        }
+    }
+    for (int k = c + 1; c < chunks && k < min(chunks, c + kStages - 1); ++k) specv::mbar_wait_bounded(full + k % kStages, (k / kStages) & 1);
+    bulk_wait_read<0>();
+}
+
+// The same by columns, a thread a column, for states of any alignment.  All sources of a column are read
+// before one is written: as many columns at a time as the ring holds sources of.
+template <class Vec>
+__device__ __forceinline__ void move_columns(const State &st, unsigned char *base, const Moves &mv, int64_t begin, int64_t end, unsigned char *ring) {
+    Vec *mine = reinterpret_cast<Vec *>(ring) + threadIdx.x;  // the thread's own places: source k at k * kThreads
+    static_assert(kMaxGroup * kThreads * sizeof(Vec) <= kRing, "a column of each source per thread");
+    for (int64_t byte = begin + threadIdx.x * sizeof(Vec); byte < end; byte += kThreads * sizeof(Vec)) {
+        for (int k = 0; k < mv.n_sources; ++k)
+            if (byte < static_cast<int64_t>(mv.length[k]) * st.unit) mine[k * kThreads] = *reinterpret_cast<const Vec *>(base + mv.source[k] * st.slot + byte);
+        for (int i = 0; i < mv.count; ++i)
+            if (byte < static_cast<int64_t>(mv.length[mv.from[i]]) * st.unit)
+                *reinterpret_cast<Vec *>(base + mv.to[i] * st.slot + byte) = mine[mv.from[i] * kThreads];
     }
 }
 
-// CTAs ctas * b .. of group b: each takes some columns of one run of one plane of one state.
+// CTAs ctas * b .. of group b: each takes a span of one run of one plane of one state.
 __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ Job job) {
+    extern __shared__ __align__(128) unsigned char ring[];
     __shared__ Moves mv;
     __shared__ Scratch sc;
+    __shared__ uint64_t full[kStages];
     const int b = blockIdx.x / job.ctas;
     int at = blockIdx.x - b * job.ctas;
     int k = 0;
     while (k + 1 < job.n_states && at >= job.state[k + 1].first) ++k;
     const State &st = job.state[k];
     at -= st.first;
-    const int line = at / st.chunks, chunk = at - line * st.chunks;
-    const int plane = line / st.runs, run = line - plane * st.runs;
+    const int line = at / st.spans, plane = line / st.runs;
+    const int64_t begin = static_cast<int64_t>(at - line * st.spans) * job.span;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) specv::mbar_init(full + i, 1);
+        specv::fence_barrier_init();
+    }
     find_moves(job, b, mv, sc);
     if (mv.count == 0) return;
-    unsigned char *base = st.data + plane * st.plane + run * st.run;
-    const int64_t c0 = static_cast<int64_t>(chunk) * job.columns;
-    if (st.width == 16) move_columns<uint4>(st, base, mv, c0, job.columns);
-    else if (st.width == 4) move_columns<uint32_t>(st, base, mv, c0, job.columns);
-    else move_columns<unsigned char>(st, base, mv, c0, job.columns);
+    // the span ends where the longest source does
+    int longest = 0;
+    for (int i = 0; i < mv.n_sources; ++i) longest = max(longest, mv.length[i]);
+    const int64_t end = min(min(begin + job.span, st.run), static_cast<int64_t>(longest) * st.unit);
+    if (begin >= end) return;
+    unsigned char *base = st.data + plane * st.plane + (line - plane * st.runs) * st.run;
+    if (st.width == 16) {
+        if (threadIdx.x < 32) move_bulk(st, base, mv, begin, end, ring, full);
+    } else if (st.width == 4) {
+        move_columns<uint32_t>(st, base, mv, begin, end, ring);
+    } else {
+        move_columns<unsigned char>(st, base, mv, begin, end, ring);
+    }
 }
 
 }  // namespace
@@ -206,27 +252,30 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
     }
     if (n == 0) return SPEC_OK;
     job.n_states = n;
-    for (job.columns = kColumns;; job.columns *= 2) {
+    // spans as long as leave enough CTAs; longer where there would be too many for a launch
+    const auto ctas_of = [&](int64_t span) {
         int64_t ctas = 0;
         for (int k = 0; k < n; ++k) {
             State &st = job.state[k];
-            const int64_t chunks = (st.run / st.width + job.columns - 1) / job.columns;
+            const int64_t spans = (st.run + span - 1) / span;
             int64_t all;
-            if (chunks > 0x7fffffff || __builtin_mul_overflow(chunks, static_cast<int64_t>(st.planes), &all) ||
-                __builtin_mul_overflow(all, static_cast<int64_t>(st.runs), &all) || all > 0x7fffffff) {
-                ctas = int64_t{1} << 40;
-                break;
-            }
-            st.chunks = static_cast<int>(chunks), st.first = static_cast<int>(std::min<int64_t>(ctas, 0x7fffffff));
+            if (spans > 0x7fffffff || __builtin_mul_overflow(spans, static_cast<int64_t>(st.planes), &all) ||
+                __builtin_mul_overflow(all, static_cast<int64_t>(st.runs), &all) || all > 0x7fffffff)
+                return int64_t{1} << 40;
+            st.spans = static_cast<int>(spans), st.first = static_cast<int>(std::min<int64_t>(ctas, 0x7fffffff));
             ctas += all;
         }
-        if (ctas * B <= 0x7fffffff) {
-            job.ctas = static_cast<int>(ctas);
-            break;
-        }
-        if (job.columns > 0x20000000) return SPEC_ERR_INVALID_ARG;  // more planes and runs than CTAs can be
+        return ctas * B;
+    };
+    int64_t span = kMaxSpan;
+    while (span > kMinSpan && ctas_of(span) < kCtas) span /= 2;
+    while (ctas_of(span) > 0x7fffffff) {
+        if (span >= int64_t{1} << 30) return SPEC_ERR_INVALID_ARG;  // more planes and runs than CTAs can be
+        span *= 2;
     }
-    return specv::cuda_ok(specv::launch_k(false, reorder_kernel, dim3(static_cast<unsigned>(job.ctas) * B), dim3(kThreads), 0,
+    job.span = static_cast<int>(span);
+    job.ctas = static_cast<int>(ctas_of(span) / B);
+    return specv::cuda_ok(specv::launch_k(false, reorder_kernel, dim3(static_cast<unsigned>(job.ctas) * B), dim3(kThreads), kRing,
                                           static_cast<cudaStream_t>(stream), job),
                           "reorder_kernel")
                ? SPEC_OK
