@@ -20,8 +20,10 @@ namespace speccache {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGranule = 16;  // elements of a thread's access: half a block
+constexpr int kBlock = 32;    // elements that share a scale: a thread's
+constexpr int kGranule = 16;  // heads are multiples of it
 constexpr int64_t kMaxCtas = 0x7ffffff0;
+constexpr int kMaxRows = 32;  // of a CTA
 
 // Division of n < 2^31 by d < 2^31, by a product: floor(n * m / 2^(32 + s)), m = ceil(2^(32 + s) / d), 2^s >= d
 // (m < 2^33, its upper bit apart).
@@ -45,12 +47,15 @@ Divide divide_by(int d) {
 struct Cache {
     unsigned char *data[2], *scale[2];  // keys, values
     int n;                              // of them: 1 or 2
+    bool wide;                          // blocks lie at multiples of 32 bytes
     int L, P, T, D, blocks;             // blocks: of a head
-    int row_blocks;                     // of a position: H * blocks
+    int row_blocks, row_elements;       // of a position: H * blocks, H * D
     int S, M;
     const int32_t *pages, *lengths;
-    int work;            // threads' accesses of one layer's and tensor's position, two per block
-    Divide by_work, by_head;  // by_head: by the accesses of a head
+    // A line is one layer's and tensor's part of a position: row_blocks blocks, in chunks of `width` that a CTA's threads
+    // take `abreast` at a time.  Parts of a position: lines * chunks.
+    int width, chunks, abreast, parts;
+    Divide by_parts, by_chunks, by_blocks, by_width;
 
     // Where position p of a slot lies: page * T + place in it; -1: nowhere.
     __device__ __forceinline__ int64_t entry(int slot, int64_t p) const {
@@ -75,44 +80,98 @@ __device__ __forceinline__ Words8 load32(const void *p) {
                  : "l"(p));
     return v;
 }
+__device__ __forceinline__ Words8 load16(const void *p) {
+    Words8 v{};
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void store16(void *p, const Words8 &v) {
+    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]) : "memory");
+}
 __device__ __forceinline__ void store32(void *p, const Words8 &v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]),
                  "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
                  : "memory");
 }
 
+// A block of the pool, the upper half of it only if it has one.
+__device__ __forceinline__ Words8 load_pool(const Cache &c, const unsigned char *p, bool half) {
+    if (c.wide) return load32(p);
+    Words8 v = load16(p);
+    if (!half) {
+        const Words8 u = load16(p + 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v.w[4 + k] = u.w[k];
+    }
+    return v;
+}
+__device__ __forceinline__ void store_pool(const Cache &c, unsigned char *p, const Words8 &v, bool half) {
+    if (c.wide) return store32(p, v);
+    store16(p, v);
+    if (!half) store16(p + 16, Words8{{v.w[4], v.w[5], v.w[6], v.w[7]}});
+}
+
+// 32 elements in their type; the upper 16 are 0 where a head ends.
 template <int DT>
-struct Granule;  // 16 elements in their type
+struct Block;
 template <>
-struct Granule<SPEC_BF16> {
-    static constexpr int kBytes = 32;
-    Words8 v;
-    __device__ __forceinline__ void load(const void *p) { v = load32(p); }
-    __device__ __forceinline__ float get(int i) const {
-        return __uint_as_float(i & 1 ? v.w[i / 2] & 0xffff0000u : v.w[i / 2] << 16);
+struct Block<SPEC_BF16> {
+    static constexpr int kBytes = 2;
+    Words8 v[2];
+    __device__ __forceinline__ void load(const void *p, bool half) {
+        v[0] = load32(p);
+        v[1] = half ? Words8{} : load32(static_cast<const char *>(p) + 32);
+    }
+    __device__ __forceinline__ __nv_bfloat162 pair(int i) const { return *reinterpret_cast<const __nv_bfloat162 *>(&v[i / 8].w[i % 8]); }
+    // the largest |x|, NaN passed over
+    __device__ __forceinline__ float largest() const {
+        __nv_bfloat162 m[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m[j] = __habs2(pair(j));
+#pragma unroll
+        for (int j = 8; j > 0; j /= 2)
+#pragma unroll
+            for (int k = 0; k < j; ++k) m[k] = __hmax2(m[k], m[k + j]);
+        return fmaxf(__bfloat162float(__hmax(__low2bfloat16(m[0]), __high2bfloat16(m[0]))), 0.0f);
+    }
+    __device__ __forceinline__ float get(int i) const { return i & 1 ? __high2float(pair(i / 2)) : __low2float(pair(i / 2)); }
+    // pair i times a power of two; exact
+    __device__ __forceinline__ float2 scaled(int i, float up) const {
+        return __bfloat1622float2(__hmul2(pair(i), __float2bfloat162_rn(up)));
     }
     __device__ __forceinline__ void set2(int i, float a, float b) {
         const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
-        v.w[i / 2] = *reinterpret_cast<const uint32_t *>(&t);
+        v[i / 16].w[i % 16 / 2] = *reinterpret_cast<const uint32_t *>(&t);
     }
-    __device__ __forceinline__ void store(void *p) const { store32(p, v); }
+    __device__ __forceinline__ void store(void *p, bool half) const {
+        store32(p, v[0]);
+        if (!half) store32(static_cast<char *>(p) + 32, v[1]);
+    }
 };
 template <>
-struct Granule<SPEC_F32> {
-    static constexpr int kBytes = 64;
-    Words8 v[2];
-    __device__ __forceinline__ void load(const void *p) {
-        v[0] = load32(p);
-        v[1] = load32(static_cast<const char *>(p) + 32);
+struct Block<SPEC_F32> {
+    static constexpr int kBytes = 4;
+    Words8 v[4];
+    __device__ __forceinline__ void load(const void *p, bool half) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = half && k >= 2 ? Words8{} : load32(static_cast<const char *>(p) + 32 * k);
     }
     __device__ __forceinline__ float get(int i) const { return __uint_as_float(v[i / 8].w[i % 8]); }
+    __device__ __forceinline__ float largest() const {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) m = fmaxf(m, fabsf(get(j)));
+        return m;
+    }
+    __device__ __forceinline__ float2 scaled(int i, float up) const { return make_float2(get(2 * i) * up, get(2 * i + 1) * up); }
     __device__ __forceinline__ void set2(int i, float a, float b) {
         v[i / 8].w[i % 8] = __float_as_uint(a);
         v[i / 8].w[i % 8 + 1] = __float_as_uint(b);
     }
-    __device__ __forceinline__ void store(void *p) const {
-        store32(p, v[0]);
-        store32(static_cast<char *>(p) + 32, v[1]);
+    __device__ __forceinline__ void store(void *p, bool half) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (!half || k < 2) store32(static_cast<char *>(p) + 32 * k, v[k]);
     }
 };
 
@@ -141,25 +200,24 @@ __device__ __forceinline__ int first_row(const Write &w, int b) {
     return w.mode == SPEC_ROWS_NEXT ? b : __ldg(w.offsets + b) + (w.mode == SPEC_ROWS_TARGET ? b : 0);
 }
 
-// Whether the offsets are valid; the sequence of row r into *s_seq (-1: none).  The whole block.
-__device__ bool check_offsets(const Write &w, int r, int *s_seq) {
-    if (w.mode == SPEC_ROWS_NEXT) {
-        if (threadIdx.x == 0) *s_seq = r < w.B ? r : -1;
-        __syncthreads();
-        return w.B <= w.R;
-    }
-    if (threadIdx.x == 0) *s_seq = -1;
+// Whether the offsets are valid; the sequences of the rows r0 .. r0 + rows - 1 into s_seq (-1: none).  The whole
+// block.
+__device__ bool check_offsets(const Write &w, int r0, int rows, int *s_seq) {
+    const int tid = threadIdx.x;
+    if (tid < rows) s_seq[tid] = w.mode == SPEC_ROWS_NEXT && r0 + tid < w.B ? r0 + tid : -1;
     __syncthreads();
+    if (w.mode == SPEC_ROWS_NEXT) return w.B <= w.R;
     const int lo = w.mode == SPEC_ROWS_TREE ? 1 : 0;
     const int hi = w.mode == SPEC_ROWS_TREE ? SPEC_MAX_TREE_NODES : w.mode == SPEC_ROWS_TARGET ? SPEC_MAX_K : 0x7fffffff;
+    const int one = w.mode == SPEC_ROWS_TARGET ? 1 : 0;
     bool bad = __ldg(w.offsets) != 0;
-    for (int b = threadIdx.x; b < w.B; b += blockDim.x) {
+    for (int b = tid; b < w.B; b += kThreads) {
         const int64_t o = __ldg(w.offsets + b), e = __ldg(w.offsets + b + 1);
         bad |= e - o < lo || e - o > hi;
-        const int64_t shift = w.mode == SPEC_ROWS_TARGET ? b : 0, one = w.mode == SPEC_ROWS_TARGET ? 1 : 0;
-        if (r >= o + shift && r < e + shift + one) *s_seq = b;
+        const int64_t first = max(o + one * b, int64_t{r0}), end = min(e + one * (b + 1), int64_t{r0} + rows);
+        for (int64_t r = first; r < end; ++r) s_seq[r - r0] = b;
     }
-    bad |= static_cast<int64_t>(__ldg(w.offsets + w.B)) + (w.mode == SPEC_ROWS_TARGET ? w.B : 0) > w.R;
+    bad |= static_cast<int64_t>(__ldg(w.offsets + w.B)) + one * w.B > w.R;
     return __syncthreads_or(bad) == 0;
 }
 
@@ -193,7 +251,7 @@ __device__ int place_on_path(const int32_t *parent, int o, int last, int nodes, 
 
 // out_lengths, by one CTA (in place: after the rows are written).
 __device__ void write_lengths(const Write &w, int *s_seq) {
-    const bool valid = check_offsets(w, -1, s_seq);
+    const bool valid = check_offsets(w, 0, 0, s_seq);
     if (w.out_lengths != w.c.lengths)
         for (int i = threadIdx.x; i < w.c.S; i += kThreads) w.out_lengths[i] = w.c.lengths[i];
     __syncthreads();
@@ -223,93 +281,148 @@ __device__ void write_lengths(const Write &w, int *s_seq) {
     }
 }
 
-// CTAs of row r: splits * r ..; one more at the end for the lengths.
+// The rows of a CTA that are kept: which they are, and their entries in the pool.
+struct Rows {
+    int count;
+    int row[kMaxRows];
+    int64_t entry[kMaxRows];
+};
+// By the first warp: the lane's row is kept (or not) at `entry`.
+__device__ __forceinline__ void keep_rows(Rows &rows, int row, bool kept, int64_t entry) {
+    const unsigned all = __ballot_sync(0xffffffffu, kept);
+    if (kept) {
+        const int at = __popc(all & ((1u << threadIdx.x) - 1));
+        rows.row[at] = row, rows.entry[at] = entry;
+    }
+    if (threadIdx.x == 0) rows.count = __popc(all);
+}
+
+// A thread's way through the blocks of a CTA's kept rows: a block of one chunk, line and row at a time.
+struct Walk {
+    int k, part;            // row and part of it
+    int step_k, step_part;  // from one to the next
+    int in_chunk;           // the thread's block of a chunk; -1: the thread has none
+    __device__ __forceinline__ Walk(const Cache &c, int split, int splits) {
+        const int first = c.by_width(threadIdx.x);
+        in_chunk = first < c.abreast ? static_cast<int>(threadIdx.x) - first * c.width : -1;
+        const int start = split * c.abreast + first, step = c.abreast * splits;
+        k = c.by_parts(start), part = start - k * c.parts;
+        step_k = c.by_parts(step), step_part = step - step_k * c.parts;
+    }
+    __device__ __forceinline__ void next(const Cache &c) {
+        k += step_k, part += step_part;
+        if (part >= c.parts) part -= c.parts, ++k;
+    }
+};
+
+// One block: where it lies.
+struct Place {
+    bool mine, half;
+    int row, tensor, layer, element, block;  // element, block: of a position
+    int64_t position;                        // in the pool, of all layers; -1: nowhere
+    __device__ __forceinline__ Place(const Cache &c, const Rows &rows, const Walk &w) {
+        mine = w.k < rows.count && w.in_chunk >= 0;
+        const int k = mine ? w.k : 0, line = c.chunks == 1 ? w.part : c.by_chunks(w.part);
+        block = w.in_chunk + (c.chunks == 1 ? 0 : (w.part - line * c.chunks) * c.width);
+        mine = mine && block < c.row_blocks;
+        const int h = c.by_blocks(block), in_head = block - h * c.blocks;
+        element = h * c.D + in_head * kBlock;
+        half = in_head * kBlock + kGranule == c.D;
+        tensor = c.n == 2 ? line & 1 : 0, layer = c.n == 2 ? line >> 1 : line;
+        row = rows.row[k];
+        const int64_t entry = rows.entry[k];
+        position = entry < 0 ? -1 : static_cast<int64_t>(layer) * c.P * c.T + entry;
+    }
+    __device__ __forceinline__ unsigned char *data(const Cache &c) const {
+        return (tensor ? c.data[1] : c.data[0]) + position * c.row_elements + element;
+    }
+    __device__ __forceinline__ unsigned char *scale(const Cache &c) const {
+        return (tensor ? c.scale[1] : c.scale[0]) + position * c.row_blocks + block;
+    }
+};
+
+// CTAs splits * k .. of the rows per_cta * k ..; one more at the end for the lengths.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Write w, int splits) {
-    __shared__ int s_seq;
-    __shared__ int64_t s_entry;
-    const int r = blockIdx.x / splits;
-    if (r >= w.R) {
-        write_lengths(w, &s_seq);
+__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Write w, int per_cta, int splits) {
+    constexpr int U = DT == SPEC_BF16 ? 2 : 1;  // blocks of a thread under way
+    __shared__ int s_seq[kMaxRows];
+    __shared__ Rows rows;
+    const int k = blockIdx.x / splits;
+    const int64_t r64 = static_cast<int64_t>(k) * per_cta;
+    if (r64 >= w.R) {
+        write_lengths(w, s_seq);
         return;
     }
-    const bool valid = check_offsets(w, r, &s_seq);
-    const int b = s_seq;
-    if (!valid || b < 0) return;
-    if (threadIdx.x == 0) {
-        int slot;
-        const int n = kept_rows(w, b, &slot);
+    const int r0 = static_cast<int>(r64);
+    const bool valid = check_offsets(w, r0, per_cta, s_seq);
+    if (!valid) return;
+    const Cache &c = w.c;
+    const int tid = threadIdx.x;
+    if (tid < kMaxRows) {
+        const int b = tid < per_cta ? s_seq[tid] : -1, r = r0 + tid;
         int64_t entry = -1;
-        if (n > 0) {
-            int i = r - first_row(w, b);
-            if (w.mode == SPEC_ROWS_TREE) {
-                const int o = __ldg(w.offsets + b);
-                bool is_path;
-                i = place_on_path(w.parent, o, __ldg(w.last_node + b), __ldg(w.offsets + b + 1) - o, n, r, &is_path);
+        if (b >= 0 && r < w.R) {
+            int slot;
+            const int n = kept_rows(w, b, &slot);
+            if (n > 0) {
+                const int length = __ldg(c.lengths + slot);
+                int i = r - first_row(w, b);  // which kept row this is
+                if (w.mode == SPEC_ROWS_TREE) {
+                    const int o = __ldg(w.offsets + b);
+                    bool is_path;
+                    i = place_on_path(w.parent, o, __ldg(w.last_node + b), __ldg(w.offsets + b + 1) - o, n, r, &is_path);
+                }
+                if (i >= 0 && i < n && length >= 0) entry = c.entry(slot, static_cast<int64_t>(length) + i);
             }
-            const int length = __ldg(w.c.lengths + slot);
-            if (i >= 0 && i < n && length >= 0) entry = w.c.entry(slot, static_cast<int64_t>(length) + i);
         }
-        s_entry = entry;
+        keep_rows(rows, r, entry >= 0, entry);
     }
     __syncthreads();
-    const int64_t entry = s_entry;
-    if (entry < 0) return;
-    const Cache &c = w.c;
-    const int total = c.L * c.n * c.work;
-    const int head = 2 * c.blocks;  // accesses of a head; the last one is empty where D is an odd number of them
-    const int split = blockIdx.x - r * splits;
-    // whole warps, so that both threads of a block are there
-    for (int at = split * kThreads + threadIdx.x; at < (total + 31 & ~31); at += splits * kThreads) {
-        const int line = c.by_work(at), in_row = at - line * c.work;
-        const int h = c.by_head(in_row), g = in_row - h * head;
-        const int tensor = c.n == 2 ? line & 1 : 0, layer = c.n == 2 ? line >> 1 : line;
-        const bool mine = at < total && g * kGranule < c.D;
-        Granule<DT> x;
-        float big = 0.0f;
-        if (mine) {
-            x.load(w.in[tensor] + layer * w.layer_stride + r * w.row_stride + (static_cast<int64_t>(h) * c.D + g * kGranule) * (Granule<DT>::kBytes / kGranule));
+    for (Walk at(c, blockIdx.x - k * splits, splits); at.k < rows.count;) {
+        Walk from = at;
+        Block<DT> x[U];
 #pragma unroll
-            for (int i = 0; i < kGranule; ++i) big = fmaxf(big, fabsf(x.get(i)));
+        for (int u = 0; u < U; ++u, at.next(c)) {
+            const Place a(c, rows, at);
+            if (a.mine)
+                x[u].load((a.tensor ? w.in[1] : w.in[0]) + a.layer * w.layer_stride + a.row * w.row_stride + a.element * Block<DT>::kBytes, a.half);
         }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        const bool infinite = __float_as_uint(big) == 0x7f800000u;  // (fmaxf passes over NaN)
-        if (__any_sync(0xffffffffu, infinite)) {
-            float finite = 0.0f;
-            if (mine)
 #pragma unroll
-                for (int i = 0; i < kGranule; ++i) {
-                    const float a = fabsf(x.get(i));
-                    if (a < __int_as_float(0x7f800000)) finite = fmaxf(finite, a);
+        for (int u = 0; u < U; ++u, from.next(c)) {
+            const Place a(c, rows, from);
+            if (!a.mine) continue;
+            float big = x[u].largest();
+            const bool infinite = __float_as_uint(big) == 0x7f800000u;
+            if (infinite) {
+                big = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kBlock; ++j) {
+                    const float y = fabsf(x[u].get(j));
+                    if (y < __int_as_float(0x7f800000)) big = fmaxf(big, y);
                 }
-            big = fmaxf(finite, __shfl_xor_sync(0xffffffffu, finite, 1));
+            }
+            const int e = max(0, static_cast<int>((__float_as_uint(big) + 0x1fffffu) >> 23) - 8);  // e + 127
+            const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+            Words8 q;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 y = x[u].scaled(2 * j, up), z = x[u].scaled(2 * j + 1, up);
+                q.w[j] = e4m3x2(y.x, y.y) | e4m3x2(z.x, z.y) << 16;
+            }
+            if (infinite) {  // (converted, they are the largest values)
+#pragma unroll
+                for (int j = 0; j < kBlock; ++j)
+                    if (fabsf(x[u].get(j)) == __int_as_float(0x7f800000)) q.w[j / 4] |= 0x7fu << 8 * (j % 4);
+            }
+            store_pool(c, a.data(c), q, a.half);
+            *a.scale(c) = static_cast<unsigned char>(e);
         }
-        if (!mine) continue;
-        const int e = max(0, static_cast<int>((__float_as_uint(big) + 0x1fffffu) >> 23) - 8);  // e + 127
-        const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        uint32_t q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = x.get(4 * i + j) * up;
-            if (infinite)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (fabsf(x.get(4 * i + j)) == __int_as_float(0x7f800000)) y[j] = nan32();
-            q[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
-        }
-        const int64_t place = (static_cast<int64_t>(layer) * c.P * c.T + entry);
-        const int64_t H_D = static_cast<int64_t>(c.row_blocks / c.blocks) * c.D;
-        *reinterpret_cast<uint4 *>(c.data[tensor] + place * H_D + h * c.D + g * kGranule) = make_uint4(q[0], q[1], q[2], q[3]);
-        if ((g & 1) == 0) c.scale[tensor][place * c.row_blocks + h * c.blocks + g / 2] = static_cast<unsigned char>(e);
     }
 }
 
 __global__ void __launch_bounds__(kThreads) lengths_kernel(const __grid_constant__ Write w) {
-    __shared__ int s_seq;
     specv::grid_dependency_wait();
-    write_lengths(w, &s_seq);
+    write_lengths(w, nullptr);
 }
 
 // ------------------------------------------------------------------- reading
@@ -321,60 +434,68 @@ struct Read {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Read w, int splits) {
-    __shared__ int s_seq;
-    __shared__ int64_t s_entry;
-    const int r = blockIdx.x / splits;
-    if (threadIdx.x == 0) s_seq = -1;
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Read w, int per_cta, int splits) {
+    constexpr int U = 2;  // blocks of a thread under way
+    __shared__ int s_seq[kMaxRows];
+    __shared__ Rows rows;
+    const int tid = threadIdx.x;
+    const int k = blockIdx.x / splits, r0 = k * per_cta;
+    if (tid < kMaxRows) s_seq[tid] = -1;
     __syncthreads();
     bool bad = __ldg(w.offsets) != 0 || __ldg(w.offsets + w.B) > w.R;
-    for (int b = threadIdx.x; b < w.B; b += kThreads) {
-        const int o = __ldg(w.offsets + b), e = __ldg(w.offsets + b + 1);
+    for (int b = tid; b < w.B; b += kThreads) {
+        const int64_t o = __ldg(w.offsets + b), e = __ldg(w.offsets + b + 1);
         bad |= e < o;
-        if (r >= o && r < e) s_seq = b;
+        for (int64_t r = max(o, int64_t{r0}); r < min(e, int64_t{r0} + per_cta); ++r) s_seq[r - r0] = b;
     }
-    if (__syncthreads_or(bad) || s_seq < 0) return;
+    if (__syncthreads_or(bad)) return;
     const Cache &c = w.c;
-    if (threadIdx.x == 0) {
-        const int b = s_seq, slot = w.slots ? __ldg(w.slots + b) : b;
+    if (tid < kMaxRows) {
+        const int b = s_seq[tid], r = r0 + tid;
         int64_t entry = -1;
-        if (slot >= 0 && slot < c.S) {
+        if (b >= 0) {
+            const int slot = w.slots ? __ldg(w.slots + b) : b;
             const int64_t p = static_cast<int64_t>(r) - __ldg(w.offsets + b) + (w.first ? __ldg(w.first + b) : 0);
-            if (p >= 0 && p < __ldg(c.lengths + slot)) entry = c.entry(slot, p);
+            if (slot >= 0 && slot < c.S && p >= 0 && p < __ldg(c.lengths + slot)) entry = c.entry(slot, p);
         }
-        s_entry = entry;
+        keep_rows(rows, r, b >= 0, entry);
     }
     __syncthreads();
-    const int64_t entry = s_entry;
-    const int total = c.L * c.n * c.work, head = 2 * c.blocks;
-    const int split = blockIdx.x - r * splits;
-    const int64_t H_D = static_cast<int64_t>(c.row_blocks / c.blocks) * c.D;
-    for (int at = split * kThreads + threadIdx.x; at < total; at += splits * kThreads) {
-        const int line = c.by_work(at), in_row = at - line * c.work;
-        const int h = c.by_head(in_row), g = in_row - h * head;
-        const int tensor = c.n == 2 ? line & 1 : 0, layer = c.n == 2 ? line >> 1 : line;
-        if (g * kGranule >= c.D) continue;
-        Granule<DT> x;
-        uint4 q = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-        uint32_t e = 127;
-        const int64_t place = static_cast<int64_t>(layer) * c.P * c.T + entry;
-        if (entry >= 0) {
-            q = __ldg(reinterpret_cast<const uint4 *>(c.data[tensor] + place * H_D + h * c.D + g * kGranule));
-            e = __ldg(c.scale[tensor] + place * c.row_blocks + h * c.blocks + g / 2);
-        }
-        // 2^(e - 127); a byte of 255 is not written: NaN
-        const float scale = e == 0 ? __uint_as_float(0x00400000u) : e == 255 ? nan32() : __uint_as_float(e << 23);
-        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+    for (Walk at(c, blockIdx.x - k * splits, splits); at.k < rows.count;) {
+        Walk from = at;
+        Words8 q[U];
+        uint32_t e[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 y = from_e4m3x2(words[i / 2] >> (i & 1 ? 16 : 0));
-            x.set2(2 * i, y.x * scale, y.y * scale);
+        for (int u = 0; u < U; ++u, at.next(c)) {
+            const Place a(c, rows, at);
+            if (a.mine && a.position >= 0) {
+                q[u] = load_pool(c, a.data(c), a.half);
+                e[u] = __ldg(a.scale(c));
+            }
         }
-        x.store(w.out[tensor] + ((static_cast<int64_t>(layer) * w.R + r) * H_D + h * c.D + g * kGranule) * (Granule<DT>::kBytes / kGranule));
+#pragma unroll
+        for (int u = 0; u < U; ++u, from.next(c)) {
+            const Place a(c, rows, from);
+            if (!a.mine) continue;
+            // 2^(e - 127); a byte of 255 is not written: NaN
+            float scale = e[u] == 0 ? __uint_as_float(0x00400000u) : e[u] == 255 ? nan32() : __uint_as_float(e[u] << 23);
+            if (a.position < 0) scale = nan32(), q[u] = Words8{};
+            Block<DT> x;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float2 y = from_e4m3x2(q[u].w[j / 2] >> (j & 1 ? 16 : 0));
+                x.set2(2 * j, y.x * scale, y.y * scale);
+            }
+            x.store((a.tensor ? w.out[1] : w.out[0]) +
+                        ((static_cast<int64_t>(a.layer) * w.R + a.row) * c.row_elements + a.element) * Block<DT>::kBytes,
+                    a.half);
+        }
     }
 }
 
 // ---------------------------------------------------------------------- host
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 int check_cache(const spec_cache_t *in, Cache *c) {
     if (!in) return SPEC_ERR_INVALID_ARG;
     if (in->L < 0 || in->P < 0 || in->T <= 0 || in->H <= 0 || in->D <= 0 || in->S < 0 || in->M < 0) return SPEC_ERR_INVALID_ARG;
@@ -385,24 +506,36 @@ int check_cache(const spec_cache_t *in, Cache *c) {
     c->data[0] = static_cast<unsigned char *>(in->k), c->data[1] = static_cast<unsigned char *>(in->v);
     c->scale[0] = in->k_scale, c->scale[1] = in->v_scale;
     c->n = in->v ? 2 : 1;
+    c->wide = in->D % kBlock == 0 && aligned32(in->k) && aligned32(in->v);
     c->L = in->L, c->P = in->P, c->T = in->T, c->D = in->D, c->S = in->S, c->M = in->pages ? in->M : 1;
-    c->blocks = (in->D + 31) / 32, c->row_blocks = in->H * c->blocks;
+    c->blocks = (in->D + 31) / 32, c->row_blocks = in->H * c->blocks, c->row_elements = in->H * in->D;
     c->pages = in->pages, c->lengths = in->lengths;
-    c->work = 2 * c->row_blocks;
-    if (static_cast<int64_t>(c->L) * c->n * c->work > (1 << 30)) return SPEC_ERR_INVALID_ARG;
-    c->by_work = divide_by(c->work), c->by_head = divide_by(2 * c->blocks);
+    if (static_cast<int64_t>(c->L) * c->n * c->row_blocks * kMaxRows > 0x3fffffff) return SPEC_ERR_INVALID_ARG;
+    c->width = std::min(c->row_blocks, kThreads), c->chunks = (c->row_blocks + c->width - 1) / c->width, c->abreast = kThreads / c->width;
+    c->parts = c->L * c->n * c->chunks;
+    c->by_parts = divide_by(std::max(c->parts, 1)), c->by_chunks = divide_by(c->chunks);
+    c->by_blocks = divide_by(c->blocks), c->by_width = divide_by(c->width);
     return SPEC_OK;
 }
 
-// CTAs of a row: enough of them to fill the GPU, none with less than an access per thread.
-int splits_of(const Cache &c, int R) {
-    const int64_t total = static_cast<int64_t>(c.L) * c.n * c.work;
-    const int64_t most = (total + kThreads - 1) / kThreads;
-    const int64_t wanted = std::max<int64_t>((total + 4 * kThreads - 1) / (4 * kThreads), 152 * 8 / std::max(R, 1));
-    return static_cast<int>(std::min({most, std::max<int64_t>(wanted, 1), kMaxCtas / (int64_t{R} + 1)}));
+// How the rows are shared out: rows of a CTA and CTAs of a row (one of the two is 1), so that a thread has up to
+// 8 blocks, for the CTA to set out on once, but fewer where the GPU would not be full.
+struct Shares {
+    int per_cta, splits;
+    int64_t ctas;
+};
+Shares share_rows(const Cache &c, int R) {
+    Shares s{1, 1, 0};
+    if (c.parts == 0) return s;
+    for (int each = 8; each >= 1; each /= 2) {
+        const int64_t parts = static_cast<int64_t>(each) * c.abreast;  // of a CTA
+        s.per_cta = static_cast<int>(std::min<int64_t>(std::max<int64_t>(parts / c.parts, 1), kMaxRows));
+        s.splits = static_cast<int>(std::min((c.parts + parts - 1) / parts, std::max<int64_t>(kMaxCtas / (int64_t{R} + 1), 1)));
+        s.ctas = (int64_t{R} + s.per_cta - 1) / s.per_cta * s.splits;
+        if (s.ctas >= 152 * 6) break;
+    }
+    return s;
 }
-
-bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 }  // namespace
 }  // namespace speccache
@@ -436,14 +569,14 @@ int spec_cache_write(const spec_cache_t *cache, const void *keys, const void *va
     w.mode = mode, w.B = rows->B, w.R = rows->R;
     w.offsets = rows->offsets, w.parent = rows->parent, w.num_accepted = num_accepted, w.last_node = last_node, w.slots = slots;
     w.out_lengths = out_lengths;
-    const int splits = splits_of(w.c, w.R);
-    const int64_t ctas = static_cast<int64_t>(w.R) * splits;
+    const Shares shares = share_rows(w.c, w.R);
+    const int64_t ctas = shares.ctas;
     // in place, the lengths are read by every CTA before one may write them
     const bool apart = out_lengths && (out_lengths == cache->lengths || ctas == 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (ctas > 0) {
         const auto kernel = dtype == SPEC_F32 ? write_kernel<SPEC_F32> : write_kernel<SPEC_BF16>;
-        if (!specv::cuda_ok(specv::launch_k(false, kernel, dim3(static_cast<unsigned>(ctas + (out_lengths && !apart))), dim3(kThreads), 0, s, w, splits),
+        if (!specv::cuda_ok(specv::launch_k(false, kernel, dim3(static_cast<unsigned>(ctas + (out_lengths && !apart))), dim3(kThreads), 0, s, w, shares.per_cta, shares.splits),
                             "write_kernel"))
             return SPEC_ERR_CUDA;
     }
@@ -464,10 +597,10 @@ int spec_cache_read(const spec_cache_t *cache, const int32_t *offsets, int B, in
     if (!aligned32(out_keys) || !aligned32(out_values)) return SPEC_ERR_ALIGNMENT;
     w.out[0] = static_cast<char *>(out_keys), w.out[1] = static_cast<char *>(out_values);
     w.B = B, w.R = R, w.offsets = offsets, w.first = first, w.slots = slots;
-    const int splits = splits_of(w.c, R);
+    const Shares shares = share_rows(w.c, R);
     const auto kernel = dtype == SPEC_F32 ? read_kernel<SPEC_F32> : read_kernel<SPEC_BF16>;
-    return specv::cuda_ok(specv::launch_k(false, kernel, dim3(static_cast<unsigned>(R) * splits), dim3(kThreads), 0,
-                                          static_cast<cudaStream_t>(stream), w, splits),
+    return specv::cuda_ok(specv::launch_k(false, kernel, dim3(static_cast<unsigned>(shares.ctas)), dim3(kThreads), 0,
+                                          static_cast<cudaStream_t>(stream), w, shares.per_cta, shares.splits),
                           "read_kernel")
                ? SPEC_OK
                : SPEC_ERR_CUDA;
