@@ -196,40 +196,54 @@ struct Write {
     int32_t *out_lengths;
 };
 
-__device__ __forceinline__ int first_row(const Write &w, int b) {
-    return w.mode == SPEC_ROWS_NEXT ? b : __ldg(w.offsets + b) + (w.mode == SPEC_ROWS_TARGET ? b : 0);
+// How many rows of sequence b, which has the tokens (or nodes, or rows) o .. e - 1, are kept, and the slot they go to;
+// 0: it is skipped.
+__device__ __forceinline__ int kept_rows(const Write &w, int b, int64_t o, int64_t e, int *slot) {
+    *slot = w.slots ? __ldg(w.slots + b) : b;
+    const int n = w.num_accepted ? __ldg(w.num_accepted + b) : 0;
+    if (*slot < 0 || *slot >= w.c.S) return 0;
+    if (w.mode == SPEC_ROWS_NEXT) return 1;
+    if (w.mode == SPEC_ROWS_PROMPT) return static_cast<int>(e - o);
+    return n < 0 || n >= e - o + (w.mode == SPEC_ROWS_TARGET ? 1 : 0) ? 0 : n + 1;
 }
 
-// Whether the offsets are valid; the sequences of the rows r0 .. r0 + rows - 1 into s_seq (-1: none).  The whole
-// block.
-__device__ bool check_offsets(const Write &w, int r0, int rows, int *s_seq) {
+// The rows of a CTA, as they are found: the sequence (-1: none), which of its rows it is, how many of them are kept,
+// the slot.
+struct Found {
+    int seq[kMaxRows], at[kMaxRows], kept[kMaxRows], slot[kMaxRows];
+};
+
+// Whether the offsets are valid; the rows r0 .. r0 + rows - 1 into *f.  The whole block.
+__device__ __forceinline__ bool find_rows(const Write &w, int r0, int rows, Found *f) {
     const int tid = threadIdx.x;
-    if (tid < rows) s_seq[tid] = w.mode == SPEC_ROWS_NEXT && r0 + tid < w.B ? r0 + tid : -1;
+    if (w.mode == SPEC_ROWS_NEXT) {
+        if (tid < rows) {
+            const int r = r0 + tid;
+            f->seq[tid] = r < w.B ? r : -1, f->at[tid] = 0;
+            f->kept[tid] = r < w.B ? kept_rows(w, r, 0, 0, &f->slot[tid]) : 0;
+        }
+        __syncthreads();
+        return w.B <= w.R;
+    }
+    if (tid < rows) f->seq[tid] = -1;
     __syncthreads();
-    if (w.mode == SPEC_ROWS_NEXT) return w.B <= w.R;
     const int lo = w.mode == SPEC_ROWS_TREE ? 1 : 0;
     const int hi = w.mode == SPEC_ROWS_TREE ? SPEC_MAX_TREE_NODES : w.mode == SPEC_ROWS_TARGET ? SPEC_MAX_K : 0x7fffffff;
     const int one = w.mode == SPEC_ROWS_TARGET ? 1 : 0;
     bool bad = __ldg(w.offsets) != 0;
     for (int b = tid; b < w.B; b += kThreads) {
         const int64_t o = __ldg(w.offsets + b), e = __ldg(w.offsets + b + 1);
+        int slot;
+        const int kept = kept_rows(w, b, o, e, &slot);  // (fetched with the offsets, whether they are wanted or not)
         bad |= e - o < lo || e - o > hi;
-        const int64_t first = max(o + one * b, int64_t{r0}), end = min(e + one * (b + 1), int64_t{r0} + rows);
-        for (int64_t r = first; r < end; ++r) s_seq[r - r0] = b;
+        const int64_t first = o + one * b, end = min(e + one * (b + 1), int64_t{r0} + rows);
+        for (int64_t r = max(first, int64_t{r0}); r < end; ++r) {
+            const int k = static_cast<int>(r - r0);
+            f->seq[k] = b, f->at[k] = static_cast<int>(r - first), f->kept[k] = kept, f->slot[k] = slot;
+        }
     }
     bad |= static_cast<int64_t>(__ldg(w.offsets + w.B)) + one * w.B > w.R;
     return __syncthreads_or(bad) == 0;
-}
-
-// How many rows of sequence b are kept and the slot they go to; 0: it is skipped.
-__device__ int kept_rows(const Write &w, int b, int *slot) {
-    *slot = w.slots ? __ldg(w.slots + b) : b;
-    if (*slot < 0 || *slot >= w.c.S) return 0;
-    if (w.mode == SPEC_ROWS_NEXT) return 1;
-    const int rows = __ldg(w.offsets + b + 1) - __ldg(w.offsets + b) + (w.mode == SPEC_ROWS_TARGET ? 1 : 0);
-    if (w.mode == SPEC_ROWS_PROMPT) return rows;
-    const int n = __ldg(w.num_accepted + b);
-    return n < 0 || n >= rows ? 0 : n + 1;
 }
 
 // The place of node r (-1: any) on the path of n nodes from the root o to
@@ -250,8 +264,8 @@ __device__ int place_on_path(const int32_t *parent, int o, int last, int nodes, 
 }
 
 // out_lengths, by one CTA (in place: after the rows are written).
-__device__ void write_lengths(const Write &w, int *s_seq) {
-    const bool valid = check_offsets(w, 0, 0, s_seq);
+__device__ void write_lengths(const Write &w) {
+    const bool valid = find_rows(w, 0, 0, nullptr);
     if (w.out_lengths != w.c.lengths)
         for (int i = threadIdx.x; i < w.c.S; i += kThreads) w.out_lengths[i] = w.c.lengths[i];
     __syncthreads();
@@ -259,7 +273,8 @@ __device__ void write_lengths(const Write &w, int *s_seq) {
     const int lane = threadIdx.x & 31;
     for (int b = threadIdx.x >> 5; b < w.B; b += kThreads / 32) {
         int slot;
-        int n = kept_rows(w, b, &slot);
+        const bool any = w.mode != SPEC_ROWS_NEXT;
+        int n = kept_rows(w, b, any ? __ldg(w.offsets + b) : 0, any ? __ldg(w.offsets + b + 1) : 0, &slot);
         if (n == 0) continue;
         const int64_t length = w.c.lengths[slot];
         if (length < 0) continue;
@@ -343,36 +358,33 @@ struct Place {
 
 // CTAs splits * k .. of the rows per_cta * k ..; one more at the end for the lengths.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Write w, int per_cta, int splits) {
+__global__ void __launch_bounds__(kThreads, 4) write_kernel(const __grid_constant__ Write w, int per_cta, int splits) {
     constexpr int U = DT == SPEC_BF16 ? 2 : 1;  // blocks of a thread under way
-    __shared__ int s_seq[kMaxRows];
+    __shared__ Found found;
     __shared__ Rows rows;
     const int k = blockIdx.x / splits;
     const int64_t r64 = static_cast<int64_t>(k) * per_cta;
     if (r64 >= w.R) {
-        write_lengths(w, s_seq);
+        write_lengths(w);
         return;
     }
-    const int r0 = static_cast<int>(r64);
-    const bool valid = check_offsets(w, r0, per_cta, s_seq);
-    if (!valid) return;
+    const int r0 = static_cast<int>(r64), tid = threadIdx.x;
+    if (!find_rows(w, r0, per_cta, &found)) return;
     const Cache &c = w.c;
-    const int tid = threadIdx.x;
     if (tid < kMaxRows) {
-        const int b = tid < per_cta ? s_seq[tid] : -1, r = r0 + tid;
+        const int b = tid < per_cta ? found.seq[tid] : -1, r = r0 + tid;
         int64_t entry = -1;
-        if (b >= 0 && r < w.R) {
-            int slot;
-            const int n = kept_rows(w, b, &slot);
-            if (n > 0) {
+        if (b >= 0 && found.kept[tid] > 0) {
+            const int n = found.kept[tid], slot = found.slot[tid];
+            int i = found.at[tid];
+            if (w.mode == SPEC_ROWS_TREE || i < n) {
                 const int length = __ldg(c.lengths + slot);
-                int i = r - first_row(w, b);  // which kept row this is
                 if (w.mode == SPEC_ROWS_TREE) {
                     const int o = __ldg(w.offsets + b);
                     bool is_path;
                     i = place_on_path(w.parent, o, __ldg(w.last_node + b), __ldg(w.offsets + b + 1) - o, n, r, &is_path);
                 }
-                if (i >= 0 && i < n && length >= 0) entry = c.entry(slot, static_cast<int64_t>(length) + i);
+                if (i >= 0 && length >= 0) entry = c.entry(slot, static_cast<int64_t>(length) + i);
             }
         }
         keep_rows(rows, r, entry >= 0, entry);
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
 
 __global__ void __launch_bounds__(kThreads) lengths_kernel(const __grid_constant__ Write w) {
     specv::grid_dependency_wait();
-    write_lengths(w, nullptr);
+    write_lengths(w);
 }
 
 // ------------------------------------------------------------------- reading
@@ -518,21 +530,22 @@ int check_cache(const spec_cache_t *in, Cache *c) {
     return SPEC_OK;
 }
 
-// How the rows are shared out: rows of a CTA and CTAs of a row (one of the two is 1), so that a thread has up to
-// 8 blocks, for the CTA to set out on once, but fewer where the GPU would not be full.
+// How the rows are shared out: rows of a CTA, and CTAs of these rows, so that a thread has up to
+// 8 blocks, for the CTA to set out on once, but fewer where the GPU would not be full.  `together`: rows that a CTA takes
+// at least, where some of them are dropped, so that the CTAs are left with about as much.
 struct Shares {
     int per_cta, splits;
     int64_t ctas;
 };
-Shares share_rows(const Cache &c, int R) {
+Shares share_rows(const Cache &c, int R, int together) {
     Shares s{1, 1, 0};
-    if (c.parts == 0) return s;
+    if (c.parts == 0 || R == 0) return s;
     for (int each = 8; each >= 1; each /= 2) {
         const int64_t parts = static_cast<int64_t>(each) * c.abreast;  // of a CTA
-        s.per_cta = static_cast<int>(std::min<int64_t>(std::max<int64_t>(parts / c.parts, 1), kMaxRows));
-        s.splits = static_cast<int>(std::min((c.parts + parts - 1) / parts, std::max<int64_t>(kMaxCtas / (int64_t{R} + 1), 1)));
+        s.per_cta = static_cast<int>(std::min<int64_t>({std::max<int64_t>(parts / c.parts, together), kMaxRows, R}));
+        s.splits = static_cast<int>(std::min((static_cast<int64_t>(s.per_cta) * c.parts + parts - 1) / parts, std::max<int64_t>(kMaxCtas / (int64_t{R} + 1), 1)));
         s.ctas = (int64_t{R} + s.per_cta - 1) / s.per_cta * s.splits;
-        if (s.ctas >= 152 * 6) break;
+        if (s.ctas >= 152 * 2) break;
     }
     return s;
 }
@@ -569,7 +582,7 @@ int spec_cache_write(const spec_cache_t *cache, const void *keys, const void *va
     w.mode = mode, w.B = rows->B, w.R = rows->R;
     w.offsets = rows->offsets, w.parent = rows->parent, w.num_accepted = num_accepted, w.last_node = last_node, w.slots = slots;
     w.out_lengths = out_lengths;
-    const Shares shares = share_rows(w.c, w.R);
+    const Shares shares = share_rows(w.c, w.R, verified ? 16 : 1);
     const int64_t ctas = shares.ctas;
     // in place, the lengths are read by every CTA before one may write them
     const bool apart = out_lengths && (out_lengths == cache->lengths || ctas == 0);
@@ -597,7 +610,7 @@ int spec_cache_read(const spec_cache_t *cache, const int32_t *offsets, int B, in
     if (!aligned32(out_keys) || !aligned32(out_values)) return SPEC_ERR_ALIGNMENT;
     w.out[0] = static_cast<char *>(out_keys), w.out[1] = static_cast<char *>(out_values);
     w.B = B, w.R = R, w.offsets = offsets, w.first = first, w.slots = slots;
-    const Shares shares = share_rows(w.c, R);
+    const Shares shares = share_rows(w.c, R, 1);
     const auto kernel = dtype == SPEC_F32 ? read_kernel<SPEC_F32> : read_kernel<SPEC_BF16>;
     return specv::cuda_ok(specv::launch_k(false, kernel, dim3(static_cast<unsigned>(shares.ctas)), dim3(kThreads), 0,
                                           static_cast<cudaStream_t>(stream), w, shares.per_cta, shares.splits),
