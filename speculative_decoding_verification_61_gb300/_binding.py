@@ -2,6 +2,8 @@
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -196,6 +198,8 @@ def _new(shape, dtype, dev, stream, fill=None):
     """A call's output: memory of the stream that the call runs on (what the current stream has freed may still
     be in use there), not given to others before the current stream, too, is done with it."""
     import torch
+    if stream is None and fill is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
 
     def make():
         return torch.empty(shape, dtype=dtype, device=dev) if fill is None else torch.full(shape, fill, dtype=dtype, device=dev)
@@ -923,6 +927,7 @@ class PenaltyState:
 
 
 # --------------------------------------------------- beams, states, the cache
+@functools.lru_cache(maxsize=256)
 def beam_workspace_bytes(R: int, V: int, dtype: int) -> int:
     return int(lib().spec_beam_workspace_bytes(R, V, dtype))
 
@@ -940,25 +945,28 @@ def spec_beam_select(logits, scores, offsets, n, *, ended=None, end_token=0, lse
         raise ValueError("logits must be [rows, V]")
     if not logits.is_cuda or not logits.is_contiguous():
         _check_dev("logits", logits)
-    dt = _dtype_code(logits)
-    dev, device = logits.get_device(), logits.device
-    R, V, B = _size(logits.shape[0], "logits"), _size(logits.shape[1], "a row"), _size(offsets.numel() - 1, "offsets")
+    dt, dev, device = _dtype_code(logits), logits.get_device(), logits.device
+    R, V = logits.shape
+    B = _size(offsets.numel() - 1, "offsets")
+    _size(R, "logits"), _size(V, "a row")
     if B < 0:
         raise ValueError("offsets must have B + 1 entries")
     if not 1 <= n <= MAX_CANDIDATES:
         raise ValueError(f"n must be 1 to {MAX_CANDIDATES}, got {n}")
     if ended is not None and ended.dtype is torch.bool:
         ended = ended.view(torch.uint8)
-    args = (logits.data_ptr(), _ptr(scores, "scores", f32, dev, R), _ptr(ended, "ended", torch.uint8, dev, R), end_token,
-            _ptr(offsets, "offsets", i32, dev), B, R, V, dt, n)
+    ps, pe, po = _ptr(scores, "scores", f32, dev, R), _ptr(ended, "ended", torch.uint8, dev, R), _ptr(offsets, "offsets", i32, dev)
     if workspace is None:
         workspace = _new(max(256, beam_workspace_bytes(R, V, dt)), torch.uint8, device, stream)
-    out = (_new((B, n), f32, device, stream), _new((B, n), i32, device, stream), _new((B, n), i32, device, stream))
-    if lse:
-        out += (_new(R, f32, device, stream),)
-    _launch(dev, stream, lib().spec_beam_select, "spec_beam_select", *args, *(t.data_ptr() for t in out),
-            *(() if lse else (None,)), _ptr(workspace, "workspace", torch.uint8, dev), workspace.numel())
-    return out
+        pw = workspace.data_ptr()
+    else:
+        pw = _ptr(workspace, "workspace", torch.uint8, dev)
+    out_scores, out_tokens, out_rows = _new((B, n), f32, device, stream), _new((B, n), i32, device, stream), _new((B, n), i32, device, stream)
+    out_lse = _new(R, f32, device, stream) if lse else None
+    _launch(dev, stream, lib().spec_beam_select, "spec_beam_select", logits.data_ptr(), ps, pe, end_token, po, B, R, V, dt,
+            n, out_scores.data_ptr(), out_tokens.data_ptr(), out_rows.data_ptr(), out_lse.data_ptr() if lse else None, pw,
+            workspace.numel())
+    return (out_scores, out_tokens, out_rows, out_lse) if lse else (out_scores, out_tokens, out_rows)
 
 
 def _state_of(x, S, dev):
@@ -973,20 +981,11 @@ def _state_of(x, S, dev):
         raise ValueError("a state is (tensor, slot dimension, position dimension behind it or None)")
     if shape[at] != S:
         raise ValueError(f"a state has {shape[at]} slots, another {S}")
-    end = len(shape) if pos is None else pos + 1
-    planes, unit = 1, t.element_size()
-    for d in shape[:at]:
-        planes *= d
-    for d in shape[end:]:
-        unit *= d
+    planes = math.prod(shape[:at]) if at else 1
     if pos is None:  # one position: everything a slot holds
-        for d in shape[at + 1:]:
-            unit *= d
-        return _State(t.data_ptr(), planes, 1, 1, unit)
-    runs = 1
-    for d in shape[at + 1:pos]:
-        runs *= d
-    return _State(t.data_ptr(), planes, runs, shape[pos], unit)
+        return _State(t.data_ptr(), planes, 1, 1, math.prod(shape[at + 1:]) * t.element_size())
+    return _State(t.data_ptr(), planes, math.prod(shape[at + 1:pos]), shape[pos],
+                  math.prod(shape[pos + 1:]) * t.element_size())
 
 
 def spec_state_reorder(states, rows, offsets, *, slots=None, lengths=None, stream=None):

@@ -58,21 +58,26 @@ __device__ __forceinline__ uint4 load_stream(const uint4 *p) {
     return v;
 }
 
-// A warp per unit; CTAs blocks_per_row * r .. of row r.
+// The arguments of a call.
+struct Call {
+    const void *logits;
+    const float *scores;
+    const uint8_t *ended;
+    const int32_t *offsets;
+    int end_token, B, R, V, n;
+    Partial part;
+    float *out_scores;
+    int32_t *out_tokens, *out_rows;
+    float *out_lse;
+};
+
+// Unit u of row r, by a warp.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const void *__restrict__ logits,
-                                                           const float *__restrict__ scores,
-                                                           const uint8_t *__restrict__ ended,
-                                                           const int32_t *__restrict__ offsets, int B, int V,
-                                                           int blocks_per_row, const Partial part) {
-    specv::grid_launch_dependents();
-    const int r = blockIdx.x / blocks_per_row;
+__device__ __forceinline__ void stream_unit(const Call &call, int r, int u) {
+    const Partial &part = call.part;
     const int lane = threadIdx.x & 31;
-    const int u = (blockIdx.x - r * blocks_per_row) * kBlockUnits + (threadIdx.x >> 5);
-    // a row that is not a group's, or whose hypothesis has ended or does not live, is not read
-    if (u >= part.n_units || r >= __ldg(offsets + B) || __ldg(scores + r) == kNegInf || (ended && __ldg(ended + r))) return;
-    const int n_vec = V / Elem<DT>::kPerVec;
-    const uint4 *row = reinterpret_cast<const uint4 *>(logits) + static_cast<int64_t>(r) * n_vec;
+    const int n_vec = call.V / Elem<DT>::kPerVec;
+    const uint4 *row = reinterpret_cast<const uint4 *>(call.logits) + static_cast<int64_t>(r) * n_vec;
     constexpr uint32_t ni = Elem<DT>::kNegInfWord;
     uint4 v[kUnitPieces][4];
     const int first = u * kUnitPieces * 128 + lane;
@@ -123,9 +128,24 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const void *__restric
     if (lane < kUnitPieces && p < part.n_pieces) part.piece[static_cast<int64_t>(r) * part.n_pieces + p] = own;
 }
 
+// A row that is not a group's, or whose hypothesis has ended or does not live, is not read.
+__device__ __forceinline__ bool row_is_read(const Call &call, int r) {
+    return __ldg(call.scores + r) != kNegInf && !(call.ended && __ldg(call.ended + r));
+}
+
+// A warp per unit; CTAs blocks_per_row * r .. of row r.
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ Call call, int blocks_per_row) {
+    specv::grid_launch_dependents();
+    const int r = blockIdx.x / blocks_per_row;
+    const int u = (blockIdx.x - r * blocks_per_row) * kBlockUnits + (threadIdx.x >> 5);
+    if (u < call.part.n_units && r < __ldg(call.offsets + call.B) && row_is_read(call, r)) stream_unit<DT>(call, r, u);
+}
+
 // ------------------------------------------------------------ the n best
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
 constexpr int kBins = 256;
 constexpr int kList = 512;          // candidates that are put in order by counting
 constexpr int kChosen = 256;        // pieces that are read again
@@ -520,46 +540,43 @@ __device__ __forceinline__ float2 log_of(float2 s) {
     return rounded(make_float2(h.x, h.y + __fmaf_rn(static_cast<float>(k), ln2_lo, small)));
 }
 
-// A CTA per group.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) select_kernel(const void *__restrict__ logits,
-                                                          const float *__restrict__ scores,
-                                                          const uint8_t *__restrict__ ended, int end_token,
-                                                          const int32_t *__restrict__ offsets, int B, int R, int V,
-                                                          const Partial part, int n,
-                                                          float *__restrict__ out_scores,
-                                                          int32_t *__restrict__ out_tokens,
-                                                          int32_t *__restrict__ out_rows, float *__restrict__ out_lse) {
-    __shared__ __align__(16) Shared sh;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x;
-    constexpr float nan = __builtin_nanf("");
-    static_assert(sizeof(sh.bins) == kThreads * sizeof(int), "a thread clears one");
-    bool bad = __ldg(offsets) != 0;
+// Group b's rows, and whether the call's offsets are valid (else W = 0).  The whole block.
+__device__ __forceinline__ bool find_group(Shared &sh, const Call &call, int b, int *first, int *width) {
+    const int tid = threadIdx.x;
+    bool bad = __ldg(call.offsets) != 0;
 #pragma unroll 1
-    for (int i = tid; i < B; i += kThreads) {
-        const int w = __ldg(offsets + i + 1) - __ldg(offsets + i);
+    for (int i = tid; i < call.B; i += kThreads) {
+        const int w = __ldg(call.offsets + i + 1) - __ldg(call.offsets + i);
         bad |= w < 0 || w > kMaxBeams;
     }
-    bad |= __ldg(offsets + B) > R;
-    const bool invalid = __syncthreads_or(bad);
-    const int r0 = __ldg(offsets + b), W = invalid ? 0 : __ldg(offsets + b + 1) - r0;
-    // where there are fewer rows than warps, 2^share warps take a row's pieces
-    const int share = W == 0 || W > kWarps ? 0 : 31 - __clz(kWarps / W);
-    float score = kNegInf;  // of row tid
-    if (tid < W) {
-        score = __ldg(scores + r0 + tid);
-        sh.live[tid] = score == kNegInf ? 0 : ended && __ldg(ended + r0 + tid) ? 2 : 1;
-    }
-    const Group<DT> g{static_cast<const uint4 *>(logits) + static_cast<int64_t>(r0) * (V / Elem<DT>::kPerVec),
-                      part.piece + static_cast<int64_t>(r0) * part.n_pieces, W, V, V / Elem<DT>::kPerVec, part.n_pieces};
+    bad |= __ldg(call.offsets + call.B) > call.R;
+    const bool valid = !__syncthreads_or(bad);
+    const int r0 = __ldg(call.offsets + b), W = valid ? __ldg(call.offsets + b + 1) - r0 : 0;
+    if (tid < W) sh.live[tid] = __ldg(call.scores + r0 + tid) == kNegInf ? 0 : call.ended && __ldg(call.ended + r0 + tid) ? 2 : 1;
     if (tid == 0) sh.bad = 0, sh.large = 0, sh.count = 0, sh.n_pieces = 0, sh.n_cells = 0;
+    static_assert(sizeof(sh.bins) == kThreads * sizeof(int), "a thread clears one");
     (&sh.bins[0][0])[tid] = 0;
     __syncthreads();
-    specv::grid_dependency_wait();
-    if (invalid && out_lse) {
+    *first = r0, *width = W;
+    return valid;
+}
+
+// The candidates of group b, by a CTA, from what its rows have left.
+template <int DT>
+__device__ __forceinline__ void select_group(Shared &sh, const Call &call, int b, bool valid, int r0, int W) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Partial &part = call.part;
+    const int n = call.n;
+    constexpr float nan = __builtin_nanf("");
+    const float score = tid < W ? __ldg(call.scores + r0 + tid) : kNegInf;
+    // where there are fewer rows than warps, 2^share warps take a row's pieces
+    const int share = W == 0 || W > kWarps ? 0 : 31 - __clz(kWarps / W);
+    const int n_vec = call.V / Elem<DT>::kPerVec;
+    const Group<DT> g{static_cast<const uint4 *>(call.logits) + static_cast<int64_t>(r0) * n_vec,
+                      part.piece + static_cast<int64_t>(r0) * part.n_pieces, W, call.V, n_vec, part.n_pieces};
+    if (!valid && call.out_lse) {
 #pragma unroll 1
-        for (int64_t i = static_cast<int64_t>(b) * kThreads + tid; i < R; i += static_cast<int64_t>(gridDim.x) * kThreads) out_lse[i] = nan;
+        for (int64_t i = static_cast<int64_t>(b) * kThreads + tid; i < call.R; i += static_cast<int64_t>(call.B) * kThreads) call.out_lse[i] = nan;
     }
     // the largest logits of the pieces that this lane is to look at, and each row's sum, a warp a row
     float mine[kHeld];
@@ -617,7 +634,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const void *__restrict
                     lse = sum.x + sum.y;
                 }
             }
-            if (out_lse) out_lse[r0 + tid] = lse;
+            if (call.out_lse) call.out_lse[r0 + tid] = lse;
             if (wrong) sh.bad = 1;
             sh.base[tid] = base, sh.top[tid] = top;
             if (live && top != kNegInf) {
@@ -630,7 +647,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const void *__restrict
     }
     __syncthreads();
     const float most = fmaxf(sh.best[0], sh.best[1]);
-    const bool fine = !invalid && !sh.bad;
+    const bool fine = valid && !sh.bad;
     int found = 0;
     if (fine && most != kNegInf) {
         found = sh.large ? -1 : list_candidates(sh, g, mine, share, most, n);
@@ -639,15 +656,42 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const void *__restrict
             if (place >= n) return;
             const int w = x.at >> kRowShift;
             const int64_t o = static_cast<int64_t>(b) * n + place;
-            out_scores[o] = score_of(x.key);
-            out_tokens[o] = sh.live[w] == 2 ? end_token : x.at & ((1 << kRowShift) - 1);
-            out_rows[o] = r0 + w;
+            call.out_scores[o] = score_of(x.key);
+            call.out_tokens[o] = sh.live[w] == 2 ? call.end_token : x.at & ((1 << kRowShift) - 1);
+            call.out_rows[o] = r0 + w;
         });
     }
     if (tid < n && tid >= found) {
         const int64_t o = static_cast<int64_t>(b) * n + tid;
-        out_scores[o] = fine ? kNegInf : nan, out_tokens[o] = -1, out_rows[o] = -1;
+        call.out_scores[o] = fine ? kNegInf : nan, call.out_tokens[o] = -1, call.out_rows[o] = -1;
     }
+}
+
+// Behind rows_kernel: a CTA per group.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Call call) {
+    __shared__ __align__(16) Shared sh;
+    int r0, W;
+    const bool valid = find_group(sh, call, blockIdx.x, &r0, &W);
+    specv::grid_dependency_wait();
+    select_group<DT>(sh, call, blockIdx.x, valid, r0, W);
+}
+
+// Few and small groups: a cluster of CTAs streams a group's rows, its first CTA then selects.  One launch.
+template <int DT>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) group_kernel(const __grid_constant__ Call call) {
+    __shared__ __align__(16) Shared sh;
+    const int b = blockIdx.x / kCluster, rank = blockIdx.x - b * kCluster;
+    int r0, W;
+    const bool valid = find_group(sh, call, b, &r0, &W);
+    const int units = W * call.part.n_units;
+#pragma unroll 1
+    for (int i = rank * kWarps + (threadIdx.x >> 5); i < units; i += kCluster * kWarps) {
+        const int w = i / call.part.n_units;
+        if (sh.live[w] == 1) stream_unit<DT>(call, r0 + w, i - w * call.part.n_units);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0) select_group<DT>(sh, call, b, valid, r0, W);
 }
 
 // The partial results of R rows, from `base` on; their bytes.
@@ -662,20 +706,20 @@ size_t partial_of(void *base, int64_t R, int V, int dtype, Partial *part) {
 }
 
 template <int DT>
-int launch(const void *logits, const float *scores, const uint8_t *ended, int32_t end_token, const int32_t *offsets,
-           int B, int R, int V, int n, float *out_scores, int32_t *out_tokens, int32_t *out_rows, float *out_lse,
-           const Partial &part, int rows, cudaStream_t s) {
+int launch(const Call &call, int rows, cudaStream_t s) {
+    const Partial &part = call.part;
+    // A cluster per group where they fill no more than the GPU's SMs and a warp has two units at most on average: the launch of a
+    // second kernel costs more than the SMs that stay idle (one group of 4 rows of 32000 in fp32: see the table of times in
+    // this file's head).
+    if (rows > 0 && call.B * kCluster <= 152 && static_cast<int64_t>(rows) * part.n_units <= int64_t{2} * call.B * kCluster * kWarps)
+        return specv::cuda_ok(specv::launch_k(false, group_kernel<DT>, dim3(call.B * kCluster), dim3(kThreads), 0, s, call), "group_kernel")
+                   ? SPEC_OK
+                   : SPEC_ERR_CUDA;
     const int blocks = (part.n_units + kBlockUnits - 1) / kBlockUnits;
-    if (rows > 0 &&
-        !specv::cuda_ok(specv::launch_k(false, rows_kernel<DT>, dim3(static_cast<unsigned>(rows) * blocks), dim3(kRowThreads),
-                                        0, s, logits, scores, ended, offsets, B, V, blocks, part),
-                        "rows_kernel"))
+    if (rows > 0 && !specv::cuda_ok(specv::launch_k(false, rows_kernel<DT>, dim3(static_cast<unsigned>(rows) * blocks), dim3(kRowThreads), 0, s, call, blocks),
+                                    "rows_kernel"))
         return SPEC_ERR_CUDA;
-    if (!specv::cuda_ok(specv::launch_k(rows > 0, select_kernel<DT>, dim3(B), dim3(kThreads), 0, s, logits, scores, ended,
-                                        end_token, offsets, B, R, V, part, n, out_scores, out_tokens, out_rows, out_lse),
-                        "select_kernel"))
-        return SPEC_ERR_CUDA;
-    return SPEC_OK;
+    return specv::cuda_ok(specv::launch_k(rows > 0, select_kernel<DT>, dim3(call.B), dim3(kThreads), 0, s, call), "select_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace
@@ -705,9 +749,9 @@ int spec_beam_select(const void *logits, const float *scores, const uint8_t *end
     const int rows = static_cast<int>(std::min<int64_t>(R, static_cast<int64_t>(B) * SPEC_MAX_BEAMS));
     specbeam::Partial part;
     if (specbeam::partial_of(workspace, rows, V, dtype, &part) > workspace_bytes && rows > 0) return SPEC_ERR_WORKSPACE;
+    const specbeam::Call call{logits, scores, ended, offsets, end_token, B, R, V, n, part, out_scores, out_tokens, out_rows, out_lse};
     const auto run = dtype == SPEC_F32 ? specbeam::launch<SPEC_F32> : specbeam::launch<SPEC_BF16>;
-    return run(logits, scores, ended, end_token, offsets, B, R, V, n, out_scores, out_tokens, out_rows, out_lse,
-               part, rows, static_cast<cudaStream_t>(stream));
+    return run(call, rows, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
