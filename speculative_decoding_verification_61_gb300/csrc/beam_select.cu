@@ -677,18 +677,25 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     select_group<DT>(sh, call, blockIdx.x, valid, r0, W);
 }
 
-// Few and small groups: a cluster of CTAs streams a group's rows, its first CTA then selects.  One launch.
+// Few and small groups, in one launch: of a cluster, the first CTA finds out about the group while the others stream its
+// rows (those without a candidate too: whether one has them is not waited for), and then selects.
 template <int DT>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) group_kernel(const __grid_constant__ Call call) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) group_kernel(const __grid_constant__ Call call, int rows) {
     __shared__ __align__(16) Shared sh;
     const int b = blockIdx.x / kCluster, rank = blockIdx.x - b * kCluster;
-    int r0, W;
-    const bool valid = find_group(sh, call, b, &r0, &W);
-    const int units = W * call.part.n_units;
+    int r0 = 0, W = 0;
+    bool valid = false;
+    if (rank == 0) {
+        valid = find_group(sh, call, b, &r0, &W);
+    } else {
+        r0 = __ldg(call.offsets + b);
+        const int end = __ldg(call.offsets + b + 1);
+        const int units = r0 >= 0 && end > r0 && end <= rows && end - r0 <= kMaxBeams ? (end - r0) * call.part.n_units : 0;
 #pragma unroll 1
-    for (int i = rank * kWarps + (threadIdx.x >> 5); i < units; i += kCluster * kWarps) {
-        const int w = i / call.part.n_units;
-        if (sh.live[w] == 1) stream_unit<DT>(call, r0 + w, i - w * call.part.n_units);
+        for (int i = (rank - 1) * kWarps + (threadIdx.x >> 5); i < units; i += (kCluster - 1) * kWarps) {
+            const int w = i / call.part.n_units;
+            stream_unit<DT>(call, r0 + w, i - w * call.part.n_units);
+        }
     }
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0) select_group<DT>(sh, call, b, valid, r0, W);
@@ -712,7 +719,7 @@ int launch(const Call &call, int rows, cudaStream_t s) {
     // second kernel costs more than the SMs that stay idle (one group of 4 rows of 32000 in fp32: see the table of times in
     // this file's head).
     if (rows > 0 && call.B * kCluster <= 152 && static_cast<int64_t>(rows) * part.n_units <= int64_t{2} * call.B * kCluster * kWarps)
-        return specv::cuda_ok(specv::launch_k(false, group_kernel<DT>, dim3(call.B * kCluster), dim3(kThreads), 0, s, call), "group_kernel")
+        return specv::cuda_ok(specv::launch_k(false, group_kernel<DT>, dim3(call.B * kCluster), dim3(kThreads), 0, s, call, rows), "group_kernel")
                    ? SPEC_OK
                    : SPEC_ERR_CUDA;
     const int blocks = (part.n_units + kBlockUnits - 1) / kBlockUnits;
