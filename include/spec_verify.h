@@ -647,7 +647,7 @@ int spec_penalty_update(int32_t *counts, int32_t *seen, int S, int V, const int3
  * candidate of the score
  *   s_r + z_{r,v} - ln sum_v exp z_{r,v};
  * a row with s_r = -inf offers none; a row that has ended offers one, the
- * token end_token with the score s_r.  The logits of such rows are not read.
+ * token end_token with the score s_r.  The logits of such rows do not matter.
  * The n best candidates of each group are written in the order score
  * descending, then row, then token; places without a candidate get -inf, -1, -1.
  * Scores are compared in two fp32 terms (48 bits) and rounded to fp32 at the
@@ -662,8 +662,8 @@ int spec_penalty_update(int32_t *counts, int32_t *seen, int S, int V, const int3
  *   n            1 .. SPEC_MAX_CANDIDATES candidates per group
  *   out_scores   float [B, n]; out_tokens, out_rows int32 [B, n] (a row's
  *                index in logits)
- *   out_lse      float [R] or NULL: ln sum_v exp z_{r,v}, NaN where the row was not
- *                read; rows behind the last group's are left as they were
+ *   out_lse      float [R] or NULL: ln sum_v exp z_{r,v}, NaN where the logits do
+ *                not matter; rows behind the last group's are left as they were
  *   workspace    device, 256-byte aligned, spec_beam_workspace_bytes(R, V, dtype)
  *                bytes, needs no initialisation; not shared by calls that may overlap
  * Data errors: a score that is NaN or +inf, or a row that is read and holds NaN or

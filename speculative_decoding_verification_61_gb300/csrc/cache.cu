@@ -270,29 +270,45 @@ __device__ void write_lengths(const Write &w) {
         for (int i = threadIdx.x; i < w.c.S; i += kThreads) w.out_lengths[i] = w.c.lengths[i];
     __syncthreads();
     if (!valid) return;
+    // a sequence per lane; the pages that a long one needs are looked at by the whole warp
     const int lane = threadIdx.x & 31;
-    for (int b = threadIdx.x >> 5; b < w.B; b += kThreads / 32) {
-        int slot;
-        const bool any = w.mode != SPEC_ROWS_NEXT;
-        int n = kept_rows(w, b, any ? __ldg(w.offsets + b) : 0, any ? __ldg(w.offsets + b + 1) : 0, &slot);
-        if (n == 0) continue;
-        const int64_t length = w.c.lengths[slot];
-        if (length < 0) continue;
-        if (w.mode == SPEC_ROWS_TREE) {
-            const int o = __ldg(w.offsets + b);
-            bool is_path;
-            place_on_path(w.parent, o, __ldg(w.last_node + b), __ldg(w.offsets + b + 1) - o, n, -1, &is_path);
-            if (!is_path) continue;
+    for (int b0 = threadIdx.x & ~31; b0 < w.B; b0 += kThreads) {
+        const int b = b0 + lane;
+        int slot = 0, n = 0;
+        int64_t length = -1;
+        if (b < w.B) {
+            const bool any = w.mode != SPEC_ROWS_NEXT;
+            n = kept_rows(w, b, any ? __ldg(w.offsets + b) : 0, any ? __ldg(w.offsets + b + 1) : 0, &slot);
+            if (n > 0) length = w.c.lengths[slot];
+            if (length >= 0 && w.mode == SPEC_ROWS_TREE) {
+                const int o = __ldg(w.offsets + b);
+                bool is_path;
+                place_on_path(w.parent, o, __ldg(w.last_node + b), __ldg(w.offsets + b + 1) - o, n, -1, &is_path);
+                if (!is_path) length = -1;
+            }
         }
         const int64_t end = length + n;
         bool room = end <= static_cast<int64_t>(w.c.M) * w.c.T && end <= 0x7fffffff;
-        if (room && w.c.pages)
-            for (int64_t p = length / w.c.T + lane; p * w.c.T < end; p += 32) {
-                const int page = __ldg(w.c.pages + static_cast<int64_t>(slot) * w.c.M + p);
-                room &= page >= 0 && page < w.c.P;
-            }
-        room = __all_sync(0xffffffffu, room);
-        if (lane == 0) w.out_lengths[slot] = room ? static_cast<int>(end) : -1;
+        const bool look = length >= 0 && room && w.c.pages;
+        const int first = look ? static_cast<int>(length / w.c.T) : 0, pages = look ? static_cast<int>((end - 1) / w.c.T) + 1 - first : 0;
+        const auto is_page = [&](int64_t at) {
+            const int page = __ldg(w.c.pages + at);
+            return page >= 0 && page < w.c.P;
+        };
+        const int64_t at = static_cast<int64_t>(slot) * w.c.M + first;
+        constexpr int few = 4;
+        if (pages <= few) {
+            for (int p = 0; p < pages; ++p) room &= is_page(at + p);
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, pages > few); left; left &= left - 1) {
+            const int from = __ffs(left) - 1, count = __shfl_sync(0xffffffffu, pages, from);
+            const int64_t start = __shfl_sync(0xffffffffu, at, from);
+            bool all = true;
+            for (int p = lane; p < count; p += 32) all &= is_page(start + p);
+            all = __all_sync(0xffffffffu, all);
+            if (lane == from) room &= all;
+        }
+        if (length >= 0) w.out_lengths[slot] = room ? static_cast<int>(end) : -1;
     }
 }
 

@@ -6,7 +6,7 @@
 // slots differ, as if all moves of the group were made at once.  A CTA takes some
 // bytes of one run, the same of all the group's slots: it has read them of every source
 // before it writes any, so that no CTA waits on another and nothing is kept
-// outside of it.  Where positions are multiples of 16 bytes the copy engine moves the
+// outside of it.  Where runs are multiples of 16 bytes the copy engine moves the
 // bytes, by way of shared memory: each distinct source once in, and out to every
 // destination of it; a warp does no more than to start the copies and to wait for them.
 #include <algorithm>
@@ -25,14 +25,16 @@ constexpr int kMaxGroup = SPEC_MAX_BEAMS;
 constexpr int kMaxStates = SPEC_MAX_STATES;
 constexpr int kStages = 4;          // chunks of a CTA under way
 constexpr int kRing = 44 * 1024;    // bytes of them: 4 CTAs and 176 KB to an SM
-constexpr int kMinSpan = 16 * 1024;
+constexpr int kMinSpan = 16 * 1024;  // of a group of up to 4; of more, so that a CTA has as much to move
 constexpr int kMaxSpan = 128 * 1024;
-constexpr int kCtas = 152 * 16;     // a span is made shorter until there are so many
+constexpr int kNarrow = 8;          // spans of narrow columns are shorter by this
+constexpr int kCtas = 152 * 8;     // a span is made shorter until there are so many
 
 struct State {
     unsigned char *data;
     int64_t plane, slot, run, unit;  // bytes from one to the next; run holds run / unit positions
-    int planes, runs, spans;         // spans: CTAs of a run
+    int planes, runs;
+    int spans, span;                 // CTAs of a run, bytes of one (of each slot)
     int width;                       // bytes of a column; 16: moved by the copy engine
     int first;                       // its first CTA of a group
 };
@@ -40,7 +42,7 @@ struct State {
 struct Job {
     State state[kMaxStates];
     int n_states, S, B, R;
-    int ctas, span;  // CTAs of a group, bytes of a CTA (of each slot)
+    int ctas;  // of a group
     const int32_t *rows, *offsets, *slots, *lengths;
 };
 
@@ -117,21 +119,26 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 
-// Bytes [begin, end) of a run, in chunks through a ring, by one warp.  A wait that runs out (2 s; a copy
-// that never comes) leaves the rest as it was.
+// What is moved of source k of a run, in bytes.
+__device__ __forceinline__ int64_t limit_of(const State &st, const Moves &mv, int k) {
+    return min(st.run, static_cast<int64_t>(mv.length[k]) * st.unit);
+}
+
+// Bytes [begin, end) of a run, each source's as far as a multiple of 16, in chunks through a ring, by one warp.  A wait
+// that runs out (2 s; a copy that never comes) leaves the rest as it was.
 __device__ void move_bulk(const State &st, unsigned char *base, const Moves &mv, int64_t begin, int64_t end, unsigned char *ring, uint64_t *full) {
     const int lane = threadIdx.x, D = mv.n_sources, n = mv.count;
-    // (at least 128 bytes)
-    const int chunk = static_cast<int>(min(int64_t{kRing} / (kStages * D), int64_t{16384})) & ~63;
+    const int stages = D > 8 ? 2 : kStages;  // (copies of a few hundred bytes are slow)
+    const int chunk = static_cast<int>(min(int64_t{kRing} / (stages * D), int64_t{16384})) & ~63;  // at least 320 bytes
     const int chunks = static_cast<int>((end - begin + chunk - 1) / chunk);
     // what is moved of source k in chunk c
     const auto bytes_of = [&](int k, int c) {
-        const int64_t most = min(end, static_cast<int64_t>(mv.length[k]) * st.unit) - (begin + static_cast<int64_t>(c) * chunk);
+        const int64_t most = (min(end, limit_of(st, mv, k)) & ~int64_t{15}) - (begin + static_cast<int64_t>(c) * chunk);
         return static_cast<uint32_t>(max(int64_t{0}, min(most, static_cast<int64_t>(chunk))));
     };
     const auto load = [&](int c) {
-        unsigned char *stage = ring + (c % kStages) * D * chunk;
-        uint64_t *bar = full + c % kStages;
+        unsigned char *stage = ring + (c % stages) * D * chunk;
+        uint64_t *bar = full + c % stages;
         uint32_t sum = 0;
         for (int k = lane; k < D; k += 32) sum += bytes_of(k, c);
         sum = __reduce_add_sync(0xffffffffu, sum);
@@ -142,38 +149,62 @@ __device__ void move_bulk(const State &st, unsigned char *base, const Moves &mv,
             if (bytes) specv::bulk_g2s(stage + k * chunk, base + mv.source[k] * st.slot + begin + static_cast<int64_t>(c) * chunk, bytes, bar);
         }
     };
-    for (int c = 0; c < min(chunks, kStages - 1); ++c) load(c);
+    for (int c = 0; c < min(chunks, stages - 1); ++c) load(c);
     int c = 0;
     for (; c < chunks; ++c) {
-        if (!__all_sync(0xffffffffu, specv::mbar_wait_bounded(full + c % kStages, (c / kStages) & 1))) break;
-        const unsigned char *stage = ring + (c % kStages) * D * chunk;
+        if (!__all_sync(0xffffffffu, specv::mbar_wait_bounded(full + c % stages, (c / stages) & 1))) break;
+        const unsigned char *stage = ring + (c % stages) * D * chunk;
         for (int i = lane; i < n; i += 32) {
             const uint32_t bytes = bytes_of(mv.from[i], c);
             if (bytes) bulk_s2g(base + mv.to[i] * st.slot + begin + static_cast<int64_t>(c) * chunk, stage + mv.from[i] * chunk, bytes);
         }
         bulk_commit();
-        if (c + kStages - 1 < chunks) {  // into the stage whose chunk was written the turn before
+        if (c + stages - 1 < chunks) {  // into the stage whose chunk was written the turn before
             bulk_wait_read<1>();
             __syncwarp();
-            load(c + kStages - 1);
+            load(c + stages - 1);
         }
     }
-    for (int k = c + 1; c < chunks && k < min(chunks, c + kStages - 1); ++k) specv::mbar_wait_bounded(full + k % kStages, (k / kStages) & 1);
+    for (int k = c + 1; c < chunks && k < min(chunks, c + stages - 1); ++k) specv::mbar_wait_bounded(full + k % stages, (k / stages) & 1);
     bulk_wait_read<0>();
 }
 
-// The same by columns, a thread a column, for states of any alignment.  All sources of a column are read
-// before one is written: as many columns at a time as the ring holds sources of.
+// The same by columns, a thread a column, for states of any alignment.  The thread has read its column of all
+// sources, into places of its own in the ring, before it writes one.
 template <class Vec>
 __device__ __forceinline__ void move_columns(const State &st, unsigned char *base, const Moves &mv, int64_t begin, int64_t end, unsigned char *ring) {
-    Vec *mine = reinterpret_cast<Vec *>(ring) + threadIdx.x;  // the thread's own places: source k at k * kThreads
-    static_assert(kMaxGroup * kThreads * sizeof(Vec) <= kRing, "a column of each source per thread");
-    for (int64_t byte = begin + threadIdx.x * sizeof(Vec); byte < end; byte += kThreads * sizeof(Vec)) {
-        for (int k = 0; k < mv.n_sources; ++k)
-            if (byte < static_cast<int64_t>(mv.length[k]) * st.unit) mine[k * kThreads] = *reinterpret_cast<const Vec *>(base + mv.source[k] * st.slot + byte);
-        for (int i = 0; i < mv.count; ++i)
-            if (byte < static_cast<int64_t>(mv.length[mv.from[i]]) * st.unit)
-                *reinterpret_cast<Vec *>(base + mv.to[i] * st.slot + byte) = mine[mv.from[i] * kThreads];
+    constexpr int w = sizeof(Vec), batch = 4;
+    static_assert(kMaxGroup * kThreads * w <= kRing || w == 8, "a column of each source per thread");
+    const int threads = min(kThreads, kRing / (w * mv.n_sources));  // (8 bytes of 64 sources are more than the ring holds of 128)
+    if (static_cast<int>(threadIdx.x) >= threads) return;
+    Vec *mine = reinterpret_cast<Vec *>(ring) + threadIdx.x;  // source k at k * threads
+    for (int64_t byte = begin + threadIdx.x * w; byte < end; byte += threads * w) {
+        for (int k0 = 0; k0 < mv.n_sources; k0 += batch) {
+            Vec v[batch];
+#pragma unroll
+            for (int k = 0; k < batch; ++k)
+                if (k0 + k < mv.n_sources && byte + w <= limit_of(st, mv, k0 + k))
+                    v[k] = *reinterpret_cast<const Vec *>(base + mv.source[k0 + k] * st.slot + byte);
+#pragma unroll
+            for (int k = 0; k < batch; ++k)
+                if (k0 + k < mv.n_sources) {
+                    if (byte + w <= limit_of(st, mv, k0 + k)) {
+                        mine[(k0 + k) * threads] = v[k];
+                    } else {  // a column that ends inside
+                        unsigned char *to = reinterpret_cast<unsigned char *>(mine + (k0 + k) * threads);
+                        for (int64_t j = byte; j < limit_of(st, mv, k0 + k); ++j) to[j - byte] = base[mv.source[k0 + k] * st.slot + j];
+                    }
+                }
+        }
+        for (int i = 0; i < mv.count; ++i) {
+            const int k = mv.from[i];
+            if (byte + w <= limit_of(st, mv, k)) {
+                *reinterpret_cast<Vec *>(base + mv.to[i] * st.slot + byte) = mine[k * threads];
+            } else {
+                const unsigned char *from = reinterpret_cast<const unsigned char *>(mine + k * threads);
+                for (int64_t j = byte; j < limit_of(st, mv, k); ++j) base[mv.to[i] * st.slot + j] = from[j - byte];
+            }
+        }
     }
 }
 
@@ -183,6 +214,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     __shared__ Moves mv;
     __shared__ Scratch sc;
     __shared__ uint64_t full[kStages];
+    __shared__ unsigned char tail[kMaxGroup][16];
     const int b = blockIdx.x / job.ctas;
     int at = blockIdx.x - b * job.ctas;
     int k = 0;
@@ -190,21 +222,37 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     const State &st = job.state[k];
     at -= st.first;
     const int line = at / st.spans, plane = line / st.runs;
-    const int64_t begin = static_cast<int64_t>(at - line * st.spans) * job.span;
-    if (threadIdx.x == 0) {
+    const int64_t begin = static_cast<int64_t>(at - line * st.spans) * st.span;
+    const int tid = threadIdx.x;
+    if (tid == 0) {
         for (int i = 0; i < kStages; ++i) specv::mbar_init(full + i, 1);
         specv::fence_barrier_init();
     }
     find_moves(job, b, mv, sc);
     if (mv.count == 0) return;
     // the span ends where the longest source does
-    int longest = 0;
-    for (int i = 0; i < mv.n_sources; ++i) longest = max(longest, mv.length[i]);
-    const int64_t end = min(min(begin + job.span, st.run), static_cast<int64_t>(longest) * st.unit);
+    int64_t end = 0;
+    for (int i = 0; i < mv.n_sources; ++i) end = max(end, limit_of(st, mv, i));
+    end = min(begin + st.span, end);
     if (begin >= end) return;
     unsigned char *base = st.data + plane * st.plane + (line - plane * st.runs) * st.run;
     if (st.width == 16) {
-        if (threadIdx.x < 32) move_bulk(st, base, mv, begin, end, ring, full);
+        // bytes behind a source's last multiple of 16: read before anything is written, written when all is read
+        const auto tail_of = [&](int k, int64_t *from) {
+            const int64_t limit = limit_of(st, mv, k);
+            *from = limit & ~int64_t{15};
+            return *from >= begin && *from < begin + st.span ? static_cast<int>(limit - *from) : 0;
+        };
+        int64_t from;
+        if (tid < mv.n_sources)
+            for (int j = 0, n = tail_of(tid, &from); j < n; ++j) tail[tid][j] = base[mv.source[tid] * st.slot + from + j];
+        __syncthreads();
+        if (tid < 32 && begin < (end & ~int64_t{15})) move_bulk(st, base, mv, begin, end, ring, full);
+        __syncthreads();
+        if (tid < mv.count)
+            for (int j = 0, n = tail_of(mv.from[tid], &from); j < n; ++j) base[mv.to[tid] * st.slot + from + j] = tail[mv.from[tid]][j];
+    } else if (st.width == 8) {
+        move_columns<uint2>(st, base, mv, begin, end, ring);
     } else if (st.width == 4) {
         move_columns<uint32_t>(st, base, mv, begin, end, ring);
     } else {
@@ -245,9 +293,8 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
         const unsigned char *l = reinterpret_cast<const unsigned char *>(lengths);
         if (l && st.data < l + static_cast<int64_t>(S) * 4 && l < st.data + all) return SPEC_ERR_INVALID_ARG;
         st.planes = static_cast<int>(in.planes), st.runs = static_cast<int>(in.runs);
-        // a column lies in one position, so that a length cuts none
-        const uintptr_t low = reinterpret_cast<uintptr_t>(st.data) | static_cast<uintptr_t>(in.unit);
-        st.width = (low & 15) == 0 ? 16 : (low & 3) == 0 ? 4 : 1;
+        const uintptr_t low = reinterpret_cast<uintptr_t>(st.data) | static_cast<uintptr_t>(st.run);
+        st.width = (low & 15) == 0 ? 16 : (low & 7) == 0 ? 8 : (low & 3) == 0 ? 4 : 1;
         bytes[n++] = all;
     }
     if (n == 0) return SPEC_OK;
@@ -257,7 +304,8 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
         int64_t ctas = 0;
         for (int k = 0; k < n; ++k) {
             State &st = job.state[k];
-            const int64_t spans = (st.run + span - 1) / span;
+            st.span = static_cast<int>(st.width == 16 ? span : std::max<int64_t>(span / kNarrow, 1024));
+            const int64_t spans = (st.run + st.span - 1) / st.span;
             int64_t all;
             if (spans > 0x7fffffff || __builtin_mul_overflow(spans, static_cast<int64_t>(st.planes), &all) ||
                 __builtin_mul_overflow(all, static_cast<int64_t>(st.runs), &all) || all > 0x7fffffff)
@@ -267,13 +315,13 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
         }
         return ctas * B;
     };
-    int64_t span = kMaxSpan;
-    while (span > kMinSpan && ctas_of(span) < kCtas) span /= 2;
+    int64_t span = kMaxSpan, least = kMinSpan;
+    for (int64_t w = 4; w < R / B && least > 2048; w *= 2) least /= 2;
+    while (span > least && ctas_of(span) < kCtas) span /= 2;
     while (ctas_of(span) > 0x7fffffff) {
         if (span >= int64_t{1} << 30) return SPEC_ERR_INVALID_ARG;  // more planes and runs than CTAs can be
         span *= 2;
     }
-    job.span = static_cast<int>(span);
     job.ctas = static_cast<int>(ctas_of(span) / B);
     return specv::cuda_ok(specv::launch_k(false, reorder_kernel, dim3(static_cast<unsigned>(job.ctas) * B), dim3(kThreads), kRing,
                                           static_cast<cudaStream_t>(stream), job),

@@ -70,7 +70,7 @@ def test_maps(sv, W, kind):
 
 
 @pytest.mark.parametrize("W", [4, 12, 40])
-@pytest.mark.parametrize("T,unit,runs", [(5, 16, 1), (300, 48, 1), (37, 20, 3), (64, 3, 2), (5000, 32, 1)])
+@pytest.mark.parametrize("T,unit,runs", [(5, 16, 1), (300, 48, 1), (37, 20, 3), (64, 3, 2), (5000, 32, 1), (5, 8, 1), (1001, 24, 2), (333, 15, 1), (2000, 15, 1), (4096, 5, 1)])
 def test_lengths(sv, W, T, unit, runs):
     """Ragged lengths (none, more than there is room for, negative) of states with layers before the slots
     and heads before the positions."""
