@@ -270,7 +270,7 @@ __device__ __forceinline__ void by_rank(const Shared &sh, int found, Put put) {
         const Item x = p < found ? Item{sh.key[p], sh.at[p]} : Item{0, 0};
         int before = 0;
         if (p < found)
-#pragma unroll 1
+#pragma unroll 4
             for (int q = part; q < found; q += 8) {
                 const unsigned long long k = sh.key[q];
                 before += k > x.key || (k == x.key && sh.at[q] < x.at);
@@ -330,13 +330,19 @@ __device__ __forceinline__ int list_candidates(Shared &sh, const Group<DT> &g, c
                 if (first == 0) see(0.0f, 0);
                 continue;
             }
-            int p = first;
-            if (w < kWarps) {  // the lane holds the first of them
-#pragma unroll
-                for (int k = 0; k < kHeld; ++k, p += 32 << share) see(mine[k], p);
-            }
+            const float *piece = g.piece + static_cast<int64_t>(w) * g.n_pieces;
 #pragma unroll 1
-            for (; p < g.n_pieces; p += 32 << share) see(g.piece[static_cast<int64_t>(w) * g.n_pieces + p], p);
+            for (int p0 = first; p0 < g.n_pieces; p0 += kHeld * 32 << share) {
+                float z[kHeld];
+                const bool held = w < kWarps && p0 == first;  // the first of them
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) {
+                    const int p = p0 + (k * 32 << share);
+                    z[k] = held ? mine[k] : p < g.n_pieces ? piece[p] : kNegInf;
+                }
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) see(z[k], p0 + (k * 32 << share));
+            }
         }
         __syncthreads();
         if (pass == 0) border = border_of(sh.bins[0], most, n);
@@ -404,7 +410,8 @@ __device__ __forceinline__ int list_candidates(Shared &sh, const Group<DT> &g, c
         }
         __syncthreads();
         const int found = sh.count;
-        if (found <= kList) return found;
+        // (putting them in order takes the square of their number)
+        if (found <= (round == 0 ? n + 64 : kList)) return found;
         if (round == 1) return -1;
         border = border_of(sh.bins[0], most, n);
         __syncthreads();
