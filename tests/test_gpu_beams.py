@@ -222,11 +222,13 @@ def test_many_groups(sv):
     run(sv, rng.standard_normal((off[-1], 256)), rng.standard_normal(off[-1]), off, 3, "bf16")
 
 
-def test_streams_workspace_and_capture(sv):
-    """The same bits on another stream, with a workspace of the caller's that holds anything, and replayed."""
+@pytest.mark.parametrize("B", [3, 24])
+def test_streams_workspace_and_capture(sv, B):
+    """The same bits on another stream, with a workspace of the caller's that holds anything, and replayed; few groups
+    in one launch, more in two."""
     rng = np.random.default_rng(15)
     t, _ = logits(rng.standard_normal((24, 20000)), "bf16")
-    s, off = dev(rng.standard_normal(24).astype(f32)), dev(np.array([0, 8, 16, 24], i32))
+    s, off = dev(rng.standard_normal(24).astype(f32)), dev((np.arange(B + 1) * (24 // B)).astype(i32))
     want = sv.spec_beam_select(t, s, off, 16, lse=True)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -248,6 +250,35 @@ def test_streams_workspace_and_capture(sv):
     torch.cuda.synchronize()
     again = sv.spec_beam_select(t2, s, off, 16, lse=True)
     assert all(torch.equal(a, b) for a, b in zip(again, got)) and not torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("B", [2, 30])
+def test_many_more_rows_than_groups_hold(sv, B):
+    """A buffer of far more rows than B groups can have."""
+    rng = np.random.default_rng(17)
+    z = rng.standard_normal((64 * B + 700, 264))
+    off = np.concatenate([[0], np.cumsum(rng.integers(0, 65, B))])
+    off[-1] = min(off[-2] + 64, off[-1])
+    run(sv, z, rng.standard_normal(len(z)), off, 9, "bf16")
+
+
+def test_two_calls_at_once(sv):
+    """Calls on two streams, which may overlap, give what they give alone."""
+    rng = np.random.default_rng(19)
+    calls = []
+    for B in (40, 4):
+        t, _ = logits(rng.standard_normal((8 * B, 30000)), "bf16")
+        calls.append((t, dev(rng.standard_normal(8 * B).astype(f32)), dev((np.arange(B + 1) * 8).astype(i32)), 16))
+    want = [sv.spec_beam_select(*c, lse=True) for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for k in range(2):
+            got[k].append(sv.spec_beam_select(*calls[k], lse=True, stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(a, b) for g in got[k] for a, b in zip(want[k], g))
 
 
 def test_binding_refusals(sv):
