@@ -970,22 +970,22 @@ def spec_beam_select(logits, scores, offsets, n, *, ended=None, end_token=0, lse
 
 
 def _state_of(x, S, dev):
-    """(tensor, slot dimension, position dimension or None), or a tensor with the slots first, as a _State."""
-    t, at, pos = (x, 0, None) if not isinstance(x, (tuple, list)) else x
+    """A tensor with the slots first, or (tensor, slot dimension, position dimension or None), as a _State's fields."""
+    t, at, pos = x if isinstance(x, (tuple, list)) else (x, 0, None)
     if not t.is_cuda or not t.is_contiguous():
         _check_dev("a state", t)
     if t.get_device() != dev:
         raise ValueError(f"a state is on {t.device}, the call's other tensors on cuda:{dev}")
-    shape = t.shape
+    shape = tuple(t.shape)
     if not 0 <= at < len(shape) or (pos is not None and not at < pos < len(shape)):
         raise ValueError("a state is (tensor, slot dimension, position dimension behind it or None)")
     if shape[at] != S:
         raise ValueError(f"a state has {shape[at]} slots, another {S}")
-    planes = math.prod(shape[:at]) if at else 1
+    planes = math.prod(shape[:at])
     if pos is None:  # one position: everything a slot holds
-        return _State(t.data_ptr(), planes, 1, 1, math.prod(shape[at + 1:]) * t.element_size())
-    return _State(t.data_ptr(), planes, math.prod(shape[at + 1:pos]), shape[pos],
-                  math.prod(shape[pos + 1:]) * t.element_size())
+        return t.data_ptr(), planes, 1, 1, math.prod(shape[at + 1:]) * t.element_size()
+    return (t.data_ptr(), planes, math.prod(shape[at + 1:pos]), shape[pos],
+            math.prod(shape[pos + 1:]) * t.element_size())
 
 
 def spec_state_reorder(states, rows, offsets, *, slots=None, lengths=None, stream=None):
@@ -1026,18 +1026,37 @@ def _cache_arg(k, k_scale, v, v_scale, lengths, pages):
     if not k.is_cuda:
         _check_dev("k", k)
     dev, i32 = k.get_device(), torch.int32
-    L, P, T, H, D = k.shape
+    L, P, T, H, D = shape = tuple(k.shape)
     if (v is None) != (v_scale is None):
         raise ValueError("v and v_scale go together")
     scales = L * P * T * H * ((D + 31) // 32)
-    if pages is not None and pages.dim() != 2:
-        raise ValueError("pages must be [S, M]")
-    S, M = (P, 1) if pages is None else pages.shape
+    if pages is None:
+        S, M = P, 1
+    else:
+        if pages.dim() != 2:
+            raise ValueError("pages must be [S, M]")
+        S, M = pages.shape
+    if max(*shape, S, M) > 0x7fffffff:
+        raise ValueError(f"k {shape} and pages [{S}, {M}] must have dimensions below 2147483648")
     f8, u8 = torch.float8_e4m3fn, torch.uint8
     return dev, _Cache(_ptr(k, "k", f8, dev), _ptr(k_scale, "k_scale", u8, dev, scales), _ptr(v, "v", f8, dev, k.numel()),
-                       _ptr(v_scale, "v_scale", u8, dev, scales), _size(L, "k"), _size(P, "k"), _size(T, "k"),
-                       _size(H, "k"), _size(D, "k"), _ptr(pages, "pages", i32, dev), _size(S, "pages"),
-                       _size(M, "pages"), _ptr(lengths, "lengths", i32, dev, S))
+                       _ptr(v_scale, "v_scale", u8, dev, scales), L, P, T, H, D, _ptr(pages, "pages", i32, dev), S, M,
+                       _ptr(lengths, "lengths", i32, dev, S))
+
+
+def _lines_of(t, name, dev, L, H, D):
+    """(rows, elements from one layer to the next, from one row to the next) of keys or values [L, R, H, D] or [R, H, D]."""
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device")
+    shape, strides = tuple(t.shape), t.stride()
+    if len(shape) == 3 and L == 1:
+        shape, strides = (1, *shape), (0, *strides)
+    if len(shape) != 4 or shape[0] != L or shape[2] != H or shape[3] != D:
+        raise ValueError(f"{name} must be [{L}, R, {H}, {D}], got {tuple(t.shape)}")
+    R = shape[1]
+    if R and L and (strides[3] != 1 or (H > 1 and strides[2] != D)):
+        raise ValueError(f"{name} must be contiguous in heads and elements")
+    return R, strides[0] if L > 1 else 0, strides[1] if R > 1 else H * D
 
 
 def spec_cache_write(k, k_scale, v, v_scale, lengths, keys, values, offsets=None, *, rows="target", num_accepted=None,
@@ -1060,22 +1079,11 @@ def spec_cache_write(k, k_scale, v, v_scale, lengths, keys, values, offsets=None
         raise ValueError(f"rows must be one of {sorted(CACHE_ROWS)}, got {rows!r}")
     if (values is None) != (v is None):
         raise ValueError("values and v go together")
-    x = keys if keys.dim() == 4 else keys.unsqueeze(0)
-    y = None if values is None else values if values.dim() == 4 else values.unsqueeze(0)
     L, H, D = cache.L, cache.H, cache.D
-    R = x.shape[1] if x.dim() == 4 else -1
-    for name, t in (("keys", x), ("values", y)):
-        if t is None:
-            continue
-        if not t.is_cuda or t.get_device() != dev:
-            raise ValueError(f"{name} must be on the cache's device")
-        if t.shape != (L, R, H, D):
-            raise ValueError(f"{name} must be [{L}, R, {H}, {D}], got {tuple(t.shape)}")
-        if t.dtype != x.dtype or t.stride() != x.stride():
-            raise ValueError("keys and values must have one type and one layout")
-        if t.numel() and (t.stride(3) != 1 or (H > 1 and t.stride(2) != D)):
-            raise ValueError(f"{name} must be contiguous in heads and elements")
-    dt = _dtype_code(x)
+    R, layer, row = layout = _lines_of(keys, "keys", dev, L, H, D)
+    if values is not None and (_lines_of(values, "values", dev, L, H, D) != layout or values.dtype is not keys.dtype):
+        raise ValueError("keys and values must have one type and one layout")
+    dt = _dtype_code(keys)
     if mode == 2:
         if slots is None:
             raise ValueError("rows 'next' need slots: one per sequence")
@@ -1093,8 +1101,8 @@ def spec_cache_write(k, k_scale, v, v_scale, lengths, keys, values, offsets=None
     if parent is not None and parent.numel() < R:
         raise ValueError("parent must have an entry for each row")
     rw = _Rows(mode, B, _size(R, "keys"), _ptr(offsets, "offsets", i32, dev), _ptr(parent, "parent", i32, dev), None, 0)
-    _launch(dev, stream, lib().spec_cache_write, "spec_cache_write", ctypes.byref(cache), x.data_ptr(),
-            None if y is None else y.data_ptr(), x.stride(0) if L > 1 else 0, x.stride(1) if R > 1 else H * D, dt,
+    _launch(dev, stream, lib().spec_cache_write, "spec_cache_write", ctypes.byref(cache), keys.data_ptr(),
+            None if values is None else values.data_ptr(), layer, row, dt,
             ctypes.byref(rw), _ptr(num_accepted, "num_accepted", i32, dev, B), _ptr(last_node, "last_node", i32, dev, B),
             _ptr(slots, "slots", i32, dev, B), _ptr(out_lengths, "out_lengths", i32, dev, cache.S))
     return out_lengths

@@ -264,7 +264,7 @@ __device__ int place_on_path(const int32_t *parent, int o, int last, int nodes, 
 }
 
 // out_lengths, by one CTA (in place: after the rows are written).
-__device__ void write_lengths(const Write &w) {
+__device__ __noinline__ void write_lengths(const Write &w) {
     const bool valid = find_rows(w, 0, 0, nullptr);
     if (w.out_lengths != w.c.lengths)
         for (int i = threadIdx.x; i < w.c.S; i += kThreads) w.out_lengths[i] = w.c.lengths[i];
