@@ -39,12 +39,19 @@ struct State {
     int first;                       // its first CTA of a group
 };
 
-struct Job {
-    State state[kMaxStates];
-    int n_states, S, B, R;
+struct Map {
+    int S, B, R;
     int ctas;  // of a group
     const int32_t *rows, *offsets, *slots, *lengths;
 };
+// A call's arguments, with room for N states: a launch copies them.
+template <int N>
+struct Job {
+    Map map;
+    int n_states;
+    State state[N];
+};
+constexpr int kFewStates = 8;
 
 // The moves of a group.
 struct Moves {
@@ -62,7 +69,7 @@ struct Scratch {
 };
 
 // Leaves mv.count = 0 for a group that stays as it is.
-__device__ void find_moves(const Job &job, int b, Moves &mv, Scratch &sc) {
+__device__ void find_moves(const Map &job, int b, Moves &mv, Scratch &sc) {
     const int tid = threadIdx.x;
     bool bad = __ldg(job.offsets) != 0 || __ldg(job.offsets + job.B) > job.R;
     for (int i = tid; i < job.B; i += kThreads) {
@@ -209,14 +216,15 @@ __device__ __forceinline__ void move_columns(const State &st, unsigned char *bas
 }
 
 // CTAs ctas * b .. of group b: each takes a span of one run of one plane of one state.
-__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ Job job) {
+template <int N>
+__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ Job<N> job) {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ Moves mv;
     __shared__ Scratch sc;
     __shared__ uint64_t full[kStages];
     __shared__ unsigned char tail[kMaxGroup][16];
-    const int b = blockIdx.x / job.ctas;
-    int at = blockIdx.x - b * job.ctas;
+    const int b = blockIdx.x / job.map.ctas;
+    int at = blockIdx.x - b * job.map.ctas;
     int k = 0;
     while (k + 1 < job.n_states && at >= job.state[k + 1].first) ++k;
     const State &st = job.state[k];
@@ -228,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         for (int i = 0; i < kStages; ++i) specv::mbar_init(full + i, 1);
         specv::fence_barrier_init();
     }
-    find_moves(job, b, mv, sc);
+    find_moves(job.map, b, mv, sc);
     if (mv.count == 0) return;
     // the span ends where the longest source does
     int64_t end = 0;
@@ -260,6 +268,16 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     }
 }
 
+template <int N>
+int launch(const Map &map, const State *states, int n, cudaStream_t s) {
+    Job<N> job;
+    job.map = map, job.n_states = n;
+    std::copy(states, states + n, job.state);
+    return specv::cuda_ok(specv::launch_k(false, reorder_kernel<N>, dim3(static_cast<unsigned>(map.ctas) * map.B), dim3(kThreads), kRing, s, job), "reorder_kernel")
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace specstate
 
@@ -270,15 +288,14 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
     if (n_states < 0 || n_states > kMaxStates || S < 0 || B < 0 || B > SPEC_MAX_B || R < 0) return SPEC_ERR_INVALID_ARG;
     if (B == 0 || R == 0 || n_states == 0) return SPEC_OK;
     if (!states || !rows || !offsets) return SPEC_ERR_INVALID_ARG;
-    Job job;
-    job.S = S, job.B = B, job.R = R;
-    job.rows = rows, job.offsets = offsets, job.slots = slots, job.lengths = lengths;
+    Map map{S, B, R, 0, rows, offsets, slots, lengths};
+    State state[kMaxStates];
     int n = 0;
     int64_t bytes[kMaxStates];
     for (int k = 0; k < n_states; ++k) {
         const spec_state_t &in = states[k];
         if (in.planes < 0 || in.runs < 0 || in.T < 0 || in.unit < 0 || in.T > 0x7fffffff) return SPEC_ERR_INVALID_ARG;
-        State &st = job.state[n];
+        State &st = state[n];
         int64_t all;
         if (__builtin_mul_overflow(in.T, in.unit, &st.run) || __builtin_mul_overflow(st.run, in.runs, &st.slot) ||
             __builtin_mul_overflow(st.slot, static_cast<int64_t>(S), &st.plane) ||
@@ -289,7 +306,7 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
         if (in.planes > 0x7fffffff || in.runs > 0x7fffffff) return SPEC_ERR_INVALID_ARG;
         st.data = static_cast<unsigned char *>(in.data), st.unit = in.unit;
         for (int i = 0; i < n; ++i)
-            if (st.data < job.state[i].data + bytes[i] && job.state[i].data < st.data + all) return SPEC_ERR_INVALID_ARG;
+            if (st.data < state[i].data + bytes[i] && state[i].data < st.data + all) return SPEC_ERR_INVALID_ARG;
         const unsigned char *l = reinterpret_cast<const unsigned char *>(lengths);
         if (l && st.data < l + static_cast<int64_t>(S) * 4 && l < st.data + all) return SPEC_ERR_INVALID_ARG;
         st.planes = static_cast<int>(in.planes), st.runs = static_cast<int>(in.runs);
@@ -298,12 +315,11 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
         bytes[n++] = all;
     }
     if (n == 0) return SPEC_OK;
-    job.n_states = n;
     // spans as long as leave enough CTAs; longer where there would be too many for a launch
     const auto ctas_of = [&](int64_t span) {
         int64_t ctas = 0;
         for (int k = 0; k < n; ++k) {
-            State &st = job.state[k];
+            State &st = state[k];
             st.span = static_cast<int>(st.width == 16 ? span : std::max<int64_t>(span / kNarrow, 1024));
             const int64_t spans = (st.run + st.span - 1) / st.span;
             int64_t all;
@@ -322,10 +338,7 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
         if (span >= int64_t{1} << 30) return SPEC_ERR_INVALID_ARG;  // more planes and runs than CTAs can be
         span *= 2;
     }
-    job.ctas = static_cast<int>(ctas_of(span) / B);
-    return specv::cuda_ok(specv::launch_k(false, reorder_kernel, dim3(static_cast<unsigned>(job.ctas) * B), dim3(kThreads), kRing,
-                                          static_cast<cudaStream_t>(stream), job),
-                          "reorder_kernel")
-               ? SPEC_OK
-               : SPEC_ERR_CUDA;
+    map.ctas = static_cast<int>(ctas_of(span) / B);
+    const auto run = n <= kFewStates ? launch<kFewStates> : launch<kMaxStates>;
+    return run(map, state, n, static_cast<cudaStream_t>(stream));
 }
