@@ -10,6 +10,11 @@
 // position) hold the n best candidates: a candidate of any other piece has n
 // others before it, the best of each of those pieces.  So beyond the partial results only
 // about n pieces per group are read again.
+//
+// Times (GB300, events over captured calls): 64 groups of 8 rows of 128256 bf16, 26.6 us, of which the rows are 20
+// (118 MB; 17.8 us at the copy rate) and the selection behind them 6.5: a chain of eight
+// block-wide steps on 64 SMs, bound by latency.  128 groups of 16 rows of 152064, 93.8 us: 84 (7.0 TB/s of
+// reads) and 9.  One group of 4 rows of 32000 fp32, 7.7 us, all latency.
 #include <algorithm>
 #include <cstdint>
 
@@ -32,8 +37,8 @@ constexpr int kCells = kPieceBytes / kCellBytes;  // of a piece: one per lane
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // ------------------------------------------------------------ rows, streamed
-constexpr int kRowThreads = 128;
-constexpr int kUnitPieces = 4;  // of a warp
+constexpr int kRowThreads = 128;  // (256: 104 us for the 128 groups)
+constexpr int kUnitPieces = 4;  // of a warp: 8 KB under way each, 192 KB per SM
 constexpr int kBlockUnits = kRowThreads / 32;
 
 // What a row leaves, and where.
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------ the n best
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;  // (256: 28.7 us for the 64 groups, 101 for the 128)
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kBins = 256;
@@ -355,7 +360,7 @@ __device__ __forceinline__ int list_candidates(Shared &sh, const Group<DT> &g, c
     int taken;
 #pragma unroll 1
     for (int round = 0;; ++round) {
-        constexpr int flight = 3;  // pieces of a warp under way before the first is looked at
+        constexpr int flight = 3;  // pieces of a warp under way before the first is looked at (2: 96.3 us, 4 and 5 as 3)
 #pragma unroll 1
         for (int c0 = warp; c0 < chosen; c0 += flight * kWarps) {
             uint4 v[flight][cell_vecs];
@@ -722,9 +727,9 @@ size_t partial_of(void *base, int64_t R, int V, int dtype, Partial *part) {
 template <int DT>
 int launch(const Call &call, int rows, cudaStream_t s) {
     const Partial &part = call.part;
-    // A cluster per group where they fill no more than the GPU's SMs and a warp has two units at most on average: the launch of a
-    // second kernel costs more than the SMs that stay idle (one group of 4 rows of 32000 in fp32: see the table of times in
-    // this file's head).
+    // A cluster per group where they fill no more than the GPU's 152 SMs and a warp has two units at most on average: the
+    // host's part of a second launch costs more than the SMs that stay idle.  One group of 4 rows of 32000 in fp32: 25.5 us a
+    // call against 31.8 in two launches (on the device 7.7 against 6.9).
     if (rows > 0 && call.B * kCluster <= 152 && static_cast<int64_t>(rows) * part.n_units <= int64_t{2} * call.B * kCluster * kWarps)
         return specv::cuda_ok(specv::launch_k(false, group_kernel<DT>, dim3(call.B * kCluster), dim3(kThreads), 0, s, call, rows), "group_kernel")
                    ? SPEC_OK

@@ -6,6 +6,15 @@
 // e = p - 8 + (f > 1.75): an addition to the float's bits, whose carry out of the
 // mantissa is that comparison.  x * 2^-e is exact, so that rounding to e4m3 is the
 // only one, and reading back multiplies exactly.
+//
+// Both ways are bound by memory: a thread takes a block of 32 (64 bytes of bf16 in, 32 out and a byte), so that it needs no
+// other thread's values and the arithmetic of addresses is shared by as many as share a scale; half a block per thread came to
+// 287 instructions per 16 elements and 218 us for the prompts below.  A CTA takes several rows, for the dependent loads that find
+// a row's place (offsets; length; page) to be waited for once.
+//
+// Times (GB300, events over captured calls): 9676 rows of 8 prompts, 16 layers of 8 heads of 128, 142 us (6.75 TB/s, 101 % of the copy
+// rate); what 64 verifies kept, 32 layers, 14 us (7.2 at the copy rate: launch, three dependent loads, one wave); 16 sequences of
+// 1000 to 8192 tokens read back, 274 us (101 %); the smallest calls 3.6 us.
 #include <algorithm>
 #include <cstdint>
 

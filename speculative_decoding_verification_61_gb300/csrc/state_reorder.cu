@@ -9,6 +9,11 @@
 // outside of it.  Where runs are multiples of 16 bytes the copy engine moves the
 // bytes, by way of shared memory: each distinct source once in, and out to every
 // destination of it; a warp does no more than to start the copies and to wait for them.
+//
+// Times (GB300, events over captured calls): 8 groups of 8 ragged 8-bit caches, 3.9 GB read and written, 600 us (6.5 TB/s,
+// 97 % of the copy rate; by columns in registers it took 1400); the token counts of 64 groups of
+// 4, 134 MB, 28.3 us (20.1 at the copy rate: the three dependent loads of finding the moves, and the
+// first copies); one group's short cache 6.4 us, latency.
 #include <algorithm>
 #include <cstdint>
 
@@ -23,12 +28,12 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxGroup = SPEC_MAX_BEAMS;
 constexpr int kMaxStates = SPEC_MAX_STATES;
-constexpr int kStages = 4;          // chunks of a CTA under way
-constexpr int kRing = 44 * 1024;    // bytes of them: 4 CTAs and 176 KB to an SM
+constexpr int kStages = 4;           // chunks of a CTA under way
+constexpr int kRing = 44 * 1024;     // bytes of them: 4 CTAs and 176 KB to an SM (32 KB: 611 us for the caches)
 constexpr int kMinSpan = 16 * 1024;  // of a group of up to 4; of more, so that a CTA has as much to move
 constexpr int kMaxSpan = 128 * 1024;
-constexpr int kNarrow = 8;          // spans of narrow columns are shorter by this
-constexpr int kCtas = 152 * 8;     // a span is made shorter until there are so many
+constexpr int kNarrow = 8;           // spans of narrow columns are shorter by this
+constexpr int kCtas = 152 * 8;       // a span is made shorter until there are so many (152 * 2: 39 us for the counts)
 
 struct State {
     unsigned char *data;
