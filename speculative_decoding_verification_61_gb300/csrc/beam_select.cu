@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 constexpr int kThreads = 512;  // (256: 28.7 us for the 64 groups, 101 for the 128)
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
+constexpr int kSms = 152;
 constexpr int kBins = 256;
 constexpr int kList = 512;          // candidates that are put in order by counting
 constexpr int kChosen = 256;        // pieces that are read again
@@ -309,7 +310,7 @@ struct Group {
 // it are listed, by way of the cells above it.  If the cells or the candidates are too many (tokens in
 // order of their frequency: the best ones lie in a few pieces; or short rows), a histogram of theirs gives a
 // nearer border.  Returns how many are listed, -1 if they are too many still.
-template <int DT>
+template <int DT, int kFlight>
 __device__ __forceinline__ int list_candidates(Shared &sh, const Group<DT> &g, const float (&mine)[kHeld], int share, float most, int n) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float border = 0.0f;
@@ -360,18 +361,18 @@ __device__ __forceinline__ int list_candidates(Shared &sh, const Group<DT> &g, c
     int taken;
 #pragma unroll 1
     for (int round = 0;; ++round) {
-        constexpr int flight = 3;  // pieces of a warp under way before the first is looked at (2: 96.3 us, 4 and 5 as 3)
 #pragma unroll 1
-        for (int c0 = warp; c0 < chosen; c0 += flight * kWarps) {
-            uint4 v[flight][cell_vecs];
-            int f[flight];
+        for (int c0 = warp; c0 < chosen; c0 += kFlight * kWarps) {
+            // some pieces of a warp under way before the first is looked at
+            uint4 v[kFlight][cell_vecs];
+            int f[kFlight];
 #pragma unroll
-            for (int k = 0; k < flight; ++k) {
+            for (int k = 0; k < kFlight; ++k) {
                 f[k] = c0 + k * kWarps < chosen ? sh.first[c0 + k * kWarps] : -1;
                 if (f[k] >= 0 && sh.live[f[k] >> 16] == 1) g.load_cell(f[k] >> 16, f[k] & 0xffff, lane, v[k]);
             }
 #pragma unroll
-            for (int k = 0; k < flight; ++k) {
+            for (int k = 0; k < kFlight; ++k) {
                 if (f[k] < 0) break;
                 const int w = f[k] >> 16;
                 float z = lane == 0 ? 0.0f : kNegInf;  // of an ended row
@@ -574,7 +575,7 @@ __device__ __forceinline__ bool find_group(Shared &sh, const Call &call, int b, 
 }
 
 // The candidates of group b, by a CTA, from what its rows have left.
-template <int DT>
+template <int DT, int kFlight>
 __device__ __forceinline__ void select_group(Shared &sh, const Call &call, int b, bool valid, int r0, int W) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Partial &part = call.part;
@@ -662,7 +663,7 @@ __device__ __forceinline__ void select_group(Shared &sh, const Call &call, int b
     const bool fine = valid && !sh.bad;
     int found = 0;
     if (fine && most != kNegInf) {
-        found = sh.large ? -1 : list_candidates(sh, g, mine, share, most, n);
+        found = sh.large ? -1 : list_candidates<DT, kFlight>(sh, g, mine, share, most, n);
         if (found < 0) found = Digits<DT>::narrow(sh, g, n);
         by_rank(sh, found, [&](const Item &x, int place) {
             if (place >= n) return;
@@ -679,14 +680,16 @@ __device__ __forceinline__ void select_group(Shared &sh, const Call &call, int b
     }
 }
 
-// Behind rows_kernel: a CTA per group.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Call call) {
+// Behind rows_kernel: a CTA per group.  One per SM where there are no more groups than SMs, with three pieces of a warp
+// under way; else two, with the registers for two (400 groups of 8 rows of 8000: 35.4 -> 30 us; 64 groups of 8 rows of 128256
+// 26.7 -> 27.8, 128 of 16 rows of 152064 94 -> 96.5.  Four and five pieces are as three).
+template <int DT, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const __grid_constant__ Call call) {
     __shared__ __align__(16) Shared sh;
     int r0, W;
     const bool valid = find_group(sh, call, blockIdx.x, &r0, &W);
     specv::grid_dependency_wait();
-    select_group<DT>(sh, call, blockIdx.x, valid, r0, W);
+    select_group<DT, kPerSm == 1 ? 3 : 2>(sh, call, blockIdx.x, valid, r0, W);
 }
 
 // Few and small groups, in one launch: of a cluster, the first CTA finds out about the group while the others stream its
@@ -710,7 +713,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) gro
         }
     }
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (rank == 0) select_group<DT>(sh, call, b, valid, r0, W);
+    if (rank == 0) select_group<DT, 3>(sh, call, b, valid, r0, W);
 }
 
 // The partial results of R rows, from `base` on; their bytes.
@@ -727,10 +730,10 @@ size_t partial_of(void *base, int64_t R, int V, int dtype, Partial *part) {
 template <int DT>
 int launch(const Call &call, int rows, cudaStream_t s) {
     const Partial &part = call.part;
-    // A cluster per group where they fill no more than the GPU's 152 SMs and a warp has two units at most on average: the
+    // A cluster per group where they fill no more than the GPU's SMs and a warp has two units at most on average: the
     // host's part of a second launch costs more than the SMs that stay idle.  One group of 4 rows of 32000 in fp32: 25.5 us a
     // call against 31.8 in two launches (on the device 7.7 against 6.9).
-    if (rows > 0 && call.B * kCluster <= 152 && static_cast<int64_t>(rows) * part.n_units <= int64_t{2} * call.B * kCluster * kWarps)
+    if (rows > 0 && call.B * kCluster <= kSms && static_cast<int64_t>(rows) * part.n_units <= int64_t{2} * call.B * kCluster * kWarps)
         return specv::cuda_ok(specv::launch_k(false, group_kernel<DT>, dim3(call.B * kCluster), dim3(kThreads), 0, s, call, rows), "group_kernel")
                    ? SPEC_OK
                    : SPEC_ERR_CUDA;
@@ -738,7 +741,8 @@ int launch(const Call &call, int rows, cudaStream_t s) {
     if (rows > 0 && !specv::cuda_ok(specv::launch_k(false, rows_kernel<DT>, dim3(static_cast<unsigned>(rows) * blocks), dim3(kRowThreads), 0, s, call, blocks),
                                     "rows_kernel"))
         return SPEC_ERR_CUDA;
-    return specv::cuda_ok(specv::launch_k(rows > 0, select_kernel<DT>, dim3(call.B), dim3(kThreads), 0, s, call), "select_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
+    const auto select = call.B <= kSms ? select_kernel<DT, 1> : select_kernel<DT, 2>;
+    return specv::cuda_ok(specv::launch_k(rows > 0, select, dim3(call.B), dim3(kThreads), 0, s, call), "select_kernel") ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace
