@@ -32,7 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kBlock = 32;    // elements that share a scale: a thread's
 constexpr int kGranule = 16;  // heads are multiples of it
 constexpr int64_t kMaxCtas = 0x7ffffff0;
-constexpr int kMaxRows = 32;  // of a CTA
+constexpr int kMaxRows = 128;  // of a CTA
 
 // Division of n < 2^31 by d < 2^31, by a product: floor(n * m / 2^(32 + s)), m = ceil(2^(32 + s) / d), 2^s >= d
 // (m < 2^33, its upper bit apart).
@@ -324,17 +324,28 @@ __device__ __noinline__ void write_lengths(const Write &w) {
 // The rows of a CTA that are kept: which they are, and their entries in the pool.
 struct Rows {
     int count;
+    int warp[kMaxRows / 32];  // kept by each of the first warps
     int row[kMaxRows];
     int64_t entry[kMaxRows];
 };
-// By the first warp: the lane's row is kept (or not) at `entry`.
+// By the whole block: the row of each of the first threads is kept (or not) at `entry`.
 __device__ __forceinline__ void keep_rows(Rows &rows, int row, bool kept, int64_t entry) {
+    const int tid = threadIdx.x, lane = tid & 31;
     const unsigned all = __ballot_sync(0xffffffffu, kept);
+    if (lane == 0 && tid < kMaxRows) rows.warp[tid >> 5] = __popc(all);
+    __syncthreads();
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kMaxRows / 32; ++w) {
+        if (w < tid >> 5) before += rows.warp[w];
+        sum += rows.warp[w];
+    }
     if (kept) {
-        const int at = __popc(all & ((1u << threadIdx.x) - 1));
+        const int at = before + __popc(all & ((1u << lane) - 1));
         rows.row[at] = row, rows.entry[at] = entry;
     }
-    if (threadIdx.x == 0) rows.count = __popc(all);
+    if (tid == 0) rows.count = sum;
+    __syncthreads();
 }
 
 // A thread's way through the blocks of a CTA's kept rows: a block of one chunk, line and row at a time.
@@ -396,25 +407,22 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(const __grid_constan
     const int r0 = static_cast<int>(r64), tid = threadIdx.x;
     if (!find_rows(w, r0, per_cta, &found)) return;
     const Cache &c = w.c;
-    if (tid < kMaxRows) {
-        const int b = tid < per_cta ? found.seq[tid] : -1, r = r0 + tid;
-        int64_t entry = -1;
-        if (b >= 0 && found.kept[tid] > 0) {
-            const int n = found.kept[tid], slot = found.slot[tid];
-            int i = found.at[tid];
-            if (w.mode == SPEC_ROWS_TREE || i < n) {
-                const int length = __ldg(c.lengths + slot);
-                if (w.mode == SPEC_ROWS_TREE) {
-                    const int o = __ldg(w.offsets + b);
-                    bool is_path;
-                    i = place_on_path(w.parent, o, __ldg(w.last_node + b), __ldg(w.offsets + b + 1) - o, n, r, &is_path);
-                }
-                if (i >= 0 && length >= 0) entry = c.entry(slot, static_cast<int64_t>(length) + i);
+    const int b = tid < per_cta ? found.seq[tid] : -1, r = r0 + tid;
+    int64_t entry = -1;
+    if (b >= 0 && found.kept[tid] > 0) {
+        const int n = found.kept[tid], slot = found.slot[tid];
+        int i = found.at[tid];
+        if (w.mode == SPEC_ROWS_TREE || i < n) {
+            const int length = __ldg(c.lengths + slot);
+            if (w.mode == SPEC_ROWS_TREE) {
+                const int o = __ldg(w.offsets + b);
+                bool is_path;
+                i = place_on_path(w.parent, o, __ldg(w.last_node + b), __ldg(w.offsets + b + 1) - o, n, r, &is_path);
             }
+            if (i >= 0 && length >= 0) entry = c.entry(slot, static_cast<int64_t>(length) + i);
         }
-        keep_rows(rows, r, entry >= 0, entry);
     }
-    __syncthreads();
+    keep_rows(rows, r, entry >= 0, entry);
     for (Walk at(c, blockIdx.x - k * splits, splits); at.k < rows.count;) {
         Walk from = at;
         Block<DT> x[U];
@@ -487,17 +495,14 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     }
     if (__syncthreads_or(bad)) return;
     const Cache &c = w.c;
-    if (tid < kMaxRows) {
-        const int b = s_seq[tid], r = r0 + tid;
-        int64_t entry = -1;
-        if (b >= 0) {
-            const int slot = w.slots ? __ldg(w.slots + b) : b;
-            const int64_t p = static_cast<int64_t>(r) - __ldg(w.offsets + b) + (w.first ? __ldg(w.first + b) : 0);
-            if (slot >= 0 && slot < c.S && p >= 0 && p < __ldg(c.lengths + slot)) entry = c.entry(slot, p);
-        }
-        keep_rows(rows, r, b >= 0, entry);
+    const int b = tid < kMaxRows ? s_seq[tid] : -1, r = r0 + tid;
+    int64_t entry = -1;
+    if (b >= 0) {
+        const int slot = w.slots ? __ldg(w.slots + b) : b;
+        const int64_t p = static_cast<int64_t>(r) - __ldg(w.offsets + b) + (w.first ? __ldg(w.first + b) : 0);
+        if (slot >= 0 && slot < c.S && p >= 0 && p < __ldg(c.lengths + slot)) entry = c.entry(slot, p);
     }
-    __syncthreads();
+    keep_rows(rows, r, b >= 0, entry);
     for (Walk at(c, blockIdx.x - k * splits, splits); at.k < rows.count;) {
         Walk from = at;
         Words8 q[U];
