@@ -698,6 +698,9 @@ int spec_beam_select(const void *logits, const float *scores, const uint8_t *end
  * nor of the group is left as it is, as all are if the offsets are invalid.
  * (A slot that two groups name is not found: which of its contents
  * the groups then see is not defined.)
+ * A device-side wait for the copy engine that runs out (2 s, see Time-outs above)
+ * leaves the bytes that were still to be moved as they were; without a workspace
+ * there is no status word to say so.
  */
 #define SPEC_MAX_STATES 64
 

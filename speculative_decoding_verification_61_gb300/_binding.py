@@ -953,16 +953,19 @@ def spec_beam_select(logits, scores, offsets, n, *, ended=None, end_token=0, lse
         raise ValueError("offsets must have B + 1 entries")
     if not 1 <= n <= MAX_CANDIDATES:
         raise ValueError(f"n must be 1 to {MAX_CANDIDATES}, got {n}")
-    if ended is not None and ended.dtype is torch.bool:
-        ended = ended.view(torch.uint8)
-    ps, pe, po = _ptr(scores, "scores", f32, dev, R), _ptr(ended, "ended", torch.uint8, dev, R), _ptr(offsets, "offsets", i32, dev)
+    truth = torch.bool if ended is not None and ended.dtype is torch.bool else torch.uint8
+    ps, pe, po = _ptr(scores, "scores", f32, dev, R), _ptr(ended, "ended", truth, dev, R), _ptr(offsets, "offsets", i32, dev)
     if workspace is None:
         workspace = _new(max(256, beam_workspace_bytes(R, V, dt)), torch.uint8, device, stream)
         pw = workspace.data_ptr()
     else:
         pw = _ptr(workspace, "workspace", torch.uint8, dev)
-    out_scores, out_tokens, out_rows = _new((B, n), f32, device, stream), _new((B, n), i32, device, stream), _new((B, n), i32, device, stream)
-    out_lse = _new(R, f32, device, stream) if lse else None
+    if stream is None:
+        out_scores, out_tokens = torch.empty((B, n), dtype=f32, device=device), torch.empty((B, n), dtype=i32, device=device)
+        out_rows, out_lse = torch.empty_like(out_tokens), torch.empty(R, dtype=f32, device=device) if lse else None
+    else:
+        out_scores, out_tokens, out_rows = (_new((B, n), d, device, stream) for d in (f32, i32, i32))
+        out_lse = _new(R, f32, device, stream) if lse else None
     _launch(dev, stream, lib().spec_beam_select, "spec_beam_select", logits.data_ptr(), ps, pe, end_token, po, B, R, V, dt,
             n, out_scores.data_ptr(), out_tokens.data_ptr(), out_rows.data_ptr(), out_lse.data_ptr() if lse else None, pw,
             workspace.numel())
@@ -1125,7 +1128,8 @@ def spec_cache_read(k, k_scale, v, v_scale, lengths, offsets, R, *, first=None, 
     shape = (cache.L, R, cache.H, cache.D)
     if out is None:
         kind = torch.bfloat16 if dtype is None else dtype
-        out = (_new(shape, kind, k.device, stream), None if v is None else _new(shape, kind, k.device, stream))
+        out_k = _new(shape, kind, k.device, stream)
+        out = out_k, None if v is None else torch.empty_like(out_k) if stream is None else _new(shape, kind, k.device, stream)
     dt = _dtype_code(out[0])
     if (out[1] is None) != (v is None) or (dtype is not None and out[0].dtype != dtype):
         raise ValueError("out must be (keys, values) of the type asked for, values None if there is no v")
