@@ -1,6 +1,7 @@
 """ctypes marshalling for libspecverify.so (argument marshalling only)."""
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import math
@@ -146,7 +147,7 @@ def lib():
     L.spec_beam_workspace_bytes.argtypes = [ip, ip, ip]
     L.spec_beam_workspace_bytes.restype = sz
     L.spec_beam_select.argtypes = [vp, vp, vp, ip, vp, ip, ip, ip, ip, ip, vp, vp, vp, vp, vp, sz, vp]
-    L.spec_state_reorder.argtypes = [ctypes.POINTER(_State), ip, ip, vp, vp, ip, ip, vp, vp, vp]
+    L.spec_state_reorder.argtypes = [vp, ip, ip, vp, vp, ip, ip, vp, vp, vp]
     L.spec_cache_write.argtypes = [cp, vp, vp, i64, i64, ip, rp, vp, vp, vp, vp, vp]
     L.spec_cache_read.argtypes = [cp, vp, ip, ip, vp, vp, ip, vp, vp, vp]
     for name in ("spec_beam_select", "spec_state_reorder", "spec_cache_write", "spec_cache_read"):
@@ -1013,12 +1014,14 @@ def spec_state_reorder(states, rows, offsets, *, slots=None, lengths=None, strea
         return states
     first = states[0]
     S = _size(first.shape[0] if not isinstance(first, (tuple, list)) else first[0].shape[first[1]], "a state")
-    made = [_state_of(x, S, dev) for x in states]
     pl = _ptr(lengths, "lengths", i32, dev, S)
-    for at in range(0, len(made), MAX_STATES):
-        part = made[at:at + MAX_STATES]
-        _launch(dev, stream, lib().spec_state_reorder, "spec_state_reorder", (_State * len(part))(*part), len(part), S,
-                *args, pl)
+    made = array.array("q")  # five fields of 64 bits each, as in _State
+    for x in states:
+        made.extend(_state_of(x, S, dev))
+    start, size = made.buffer_info()[0], ctypes.sizeof(_State)
+    for at in range(0, len(states), MAX_STATES):
+        _launch(dev, stream, lib().spec_state_reorder, "spec_state_reorder", start + at * size,
+                min(len(states) - at, MAX_STATES), S, *args, pl)
     return states
 
 
