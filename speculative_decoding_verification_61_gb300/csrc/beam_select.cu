@@ -237,9 +237,9 @@ __device__ __forceinline__ void count_in_bins(int *bins, float most, float a) {
     if (bin < kBins) atomicAdd(&bins[max(bin, 0)], 1);
 }
 
-// A border that the n-th counted score lies above: the lower end of its bin, less a sixty-fourth (twice an
-// fp32 score's error is 2^-8).  -inf: fewer than n are in the bins.  By each warp for itself.
-__device__ __forceinline__ float border_of(const int *bins, float most, int n) {
+// The bin that the n-th counted item lies in, and how many are in those before it; -1: fewer than n are in
+// the bins.  By each warp for itself.
+__device__ __forceinline__ int nth_bin(const int *bins, int n, int *before) {
     const int lane = threadIdx.x & 31;
     int own[8], sum = 0;
 #pragma unroll
@@ -249,20 +249,29 @@ __device__ __forceinline__ float border_of(const int *bins, float most, int n) {
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum += own[k], own[k] = sum;
-    int before = sum;
+    int below = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, before, off);
-        if (lane >= off) before += t;
+        const int t = __shfl_up_sync(0xffffffffu, below, off);
+        if (lane >= off) below += t;
     }
-    const unsigned reach = __ballot_sync(0xffffffffu, before >= n);
-    if (!reach) return kNegInf;
-    before -= sum;
-    int bin = lane * 8;
+    const unsigned reach = __ballot_sync(0xffffffffu, below >= n);
+    if (!reach) return -1;
+    below -= sum;
+    int bin = lane * 8, count = below;
 #pragma unroll
-    for (int k = 0; k < 7; ++k) bin += before + own[k] < n;
-    bin = __shfl_sync(0xffffffffu, bin, __ffs(reach) - 1);
-    return most - (__int_as_float((bin + 1 + kBinBase) << kBinShift) - 1.0f) - 0.015625f;
+    for (int k = 0; k < 7; ++k)
+        if (below + own[k] < n) ++bin, count = below + own[k];
+    *before = __shfl_sync(0xffffffffu, count, __ffs(reach) - 1);
+    return __shfl_sync(0xffffffffu, bin, __ffs(reach) - 1);
+}
+
+// A border that the n-th counted score lies above: the lower end of its bin, less a sixty-fourth (twice an
+// fp32 score's error is 2^-8).  -inf: fewer than n are in the bins.
+__device__ __forceinline__ float border_of(const int *bins, float most, int n) {
+    int before;
+    const int bin = nth_bin(bins, n, &before);
+    return bin < 0 ? kNegInf : most - (__int_as_float((bin + 1 + kBinBase) << kBinShift) - 1.0f) - 0.015625f;
 }
 
 // The place of each listed item: the number of those before it, counted by eight
@@ -474,10 +483,9 @@ struct Digits {
                 }
             }
             __syncthreads();
-            int c = 0, j = 0;
-#pragma unroll 1
-            while (j < 256 && c + sh.bins[0][j] < left) c += sh.bins[0][j++];
-            all = j == 256;  // fewer than n items
+            int c = 0;
+            const int j = nth_bin(sh.bins[0], left, &c);
+            all = j < 0;  // fewer than n items
             if (!all) {
                 left -= c;
                 if (by_key) key |= static_cast<unsigned long long>(255 - j) << shift;
