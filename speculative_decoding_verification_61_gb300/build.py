@@ -23,7 +23,7 @@ SOURCES = [os.path.join(CSRC, n)
            for n in ("spec_verify.cu", "tree_verify.cu", "shard_verify.cu", "adapt_k.cu", "noalloc.cu",
                      "logits_process.cu", "logits_truncate.cu", "beam_select.cu", "state_reorder.cu", "cache.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, n) for n in ("device_utils.cuh", "verify_common.cuh", "host_common.h",
-                                                         "logits_common.cuh", "logits_host.h")] + [
+                                                         "logits_common.cuh", "logits_host.h", "state_bytes.h")] + [
     os.path.join(INCLUDE, "spec_verify.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -21,6 +21,7 @@
 
 #include "host_common.h"
 #include "spec_verify.h"
+#include "state_bytes.h"
 
 namespace specstate {
 namespace {
@@ -39,6 +40,7 @@ struct State {
     unsigned char *data;
     int64_t plane, slot, run, unit;  // bytes from one to the next; run holds run / unit positions
     int planes, runs;
+    int T;                           // positions of a run
     int spans, span;                 // CTAs of a run, bytes of one (of each slot)
     int width;                       // bytes of a column; 16: moved by the copy engine
     int first;                       // its first CTA of a group
@@ -61,7 +63,7 @@ constexpr int kFewStates = 8;
 // The moves of a group.
 struct Moves {
     int count, n_sources;
-    // of each distinct source: its slot and the positions that are moved
+    // of each distinct source: its slot and the positions that are moved, at least one (past T: all)
     int source[kMaxGroup], length[kMaxGroup];
     // of each move: its destination and which source it has
     int to[kMaxGroup], from[kMaxGroup];
@@ -133,7 +135,7 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 
 // What is moved of source k of a run, in bytes.
 __device__ __forceinline__ int64_t limit_of(const State &st, const Moves &mv, int k) {
-    return min(st.run, static_cast<int64_t>(mv.length[k]) * st.unit);
+    return moved_bytes(st.run, st.unit, st.T, mv.length[k]);
 }
 
 // Bytes [begin, end) of a run, each source's as far as a multiple of 16, in chunks through a ring, by one warp.  A wait
@@ -309,7 +311,7 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
         if (all == 0) continue;
         if (!in.data) return SPEC_ERR_INVALID_ARG;
         if (in.planes > 0x7fffffff || in.runs > 0x7fffffff) return SPEC_ERR_INVALID_ARG;
-        st.data = static_cast<unsigned char *>(in.data), st.unit = in.unit;
+        st.data = static_cast<unsigned char *>(in.data), st.unit = in.unit, st.T = static_cast<int>(in.T);
         for (int i = 0; i < n; ++i)
             if (st.data < state[i].data + bytes[i] && state[i].data < st.data + all) return SPEC_ERR_INVALID_ARG;
         const unsigned char *l = reinterpret_cast<const unsigned char *>(lengths);
