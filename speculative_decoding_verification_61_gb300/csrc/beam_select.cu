@@ -195,18 +195,29 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float score_of(unsigned long long key) {
-    const uint32_t u = static_cast<uint32_t>(key >> 32);
+    const uint32_t u = max(static_cast<uint32_t>(key >> 32), 0x00800000u);  // ordered(the lowest value)
     return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xffffffffu));
 }
-// The key of base + (z - top).
+// The key of base + (z - top).  A place without a candidate has the score -inf, so a score below the lowest value is
+// written as that value; such scores have the codes below the lowest value's, of which the upper word
+// has 2^23.
 __device__ __forceinline__ unsigned long long key_of(float z, float top, float2 base) {
-    const float2 d = two_sum(z, -top);
-    float2 s = make_float2(fmaxf(d.x, -3.402823466e38f), 0.0f);
-    if (d.x > -1e30f) {  // (below, it is nowhere near another row's)
-        s = add_to(base, d.x);
+    if (__fsub_rn(z, top) > -1e30f) {  // no sum passes the largest value: at most half a step of it is added
+        const float2 d = two_sum(z, -top);
+        float2 s = add_to(base, d.x);
         s = rounded(make_float2(s.x, s.y + d.y));
+        return static_cast<unsigned long long>(ordered(s.x)) << 32 | ordered(s.y);
     }
-    return static_cast<unsigned long long>(ordered(s.x)) << 32 | ordered(s.y);
+    // of far distances a 16th, which is exact: three of the largest values stay below 2^126
+    constexpr float part = 0.0625f;
+    const float2 e = two_sum(z * part, -top * part);
+    float2 s = add_to(make_float2(base.x * part, base.y * part), e.x);
+    s = rounded(make_float2(s.x, s.y + e.y));
+    const float x = s.x * 16.0f;
+    if (x != kNegInf) return static_cast<unsigned long long>(ordered(x)) << 32 | ordered(s.y * 16.0f);
+    // s.x is in [-3 * 2^124, -2^124]: 3 * 2^22 codes, so that with half of the lower word's they are fewer than 2^55
+    constexpr uint32_t least = 0x01bfffffu;  // ordered(-3 * 2^124)
+    return (static_cast<unsigned long long>(ordered(s.x) - least) << 32 | ordered(s.y)) >> 1;
 }
 
 struct Shared {
