@@ -652,9 +652,11 @@ int spec_penalty_update(int32_t *counts, int32_t *seen, int S, int V, const int3
  * descending, then row, then token; places without a candidate get -inf, -1, -1.
  * Scores are compared in two fp32 terms (48 bits) and rounded to fp32 at the
  * end; one below fp32's lowest finite value is compared all the same and
- * written as that value.  The row sums are of fp32 terms: candidates of different rows whose scores
- * differ by less than about 1e-7 may change places, those of one row only if 2^-46 of the
- * score does not tell them apart.  The result is the same on every run.
+ * written as that value.  The row sums are of fp32 terms, whose roundings may
+ * all be alike (equal logits): a row's ln sum is off by at most 128 * 2^-24 = 7.6e-6,
+ * so that candidates of different rows whose scores differ by less than twice that may
+ * change places; those of one row only if 2^-46 of the score does not tell them
+ * apart.  The result is the same on every run.
  *   logits       [R, V] row-major, 16-byte aligned, V * sizeof(element) a
  *                multiple of 16, as for spec_verify
  *   scores       float [R]

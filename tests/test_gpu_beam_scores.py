@@ -83,6 +83,21 @@ def test_ordered_by_its_logits_at_a_very_low_score(sv):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("G", [1, 24])
+def test_equal_logits_below_the_largest(sv, dtype, G):
+    """Terms whose roundings are all alike and do not average out: a row's sum is off by more than float32's
+    step, as far as the header says and no further."""
+    rng = np.random.default_rng(G)
+    V = 128256
+    z = np.empty((2 * G, V), f32)
+    for i in range(2 * G):
+        z[i] = rng.uniform(-20, 20)
+        z[i, rng.integers(V)] = z[i, 0] + rng.uniform(5, 15)
+    z[0], z[0, 5] = 8.823372, 20.057129
+    run(sv, z, np.zeros(2 * G, f32), np.arange(0, 2 * G + 1, 2), 8, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("mask", [-1e9, -1e30, -1e31, LOWEST_BF16])
 @pytest.mark.parametrize("B", [2, 24])
 def test_a_search_with_too_few_tokens(sv, dtype, mask, B):
