@@ -939,7 +939,9 @@ def spec_beam_select(logits, scores, offsets, n, *, ended=None, end_token=0, lse
     rows a group has; ended [R] (bool): hypotheses that have ended go on with
     end_token and their score.  Returns (scores [B, n] float32, tokens [B, n]
     int32, rows [B, n] int32: the row each comes from), best first, -inf and
-    -1 where there are fewer, and with lse=True each row's log-sum-exp [R]."""
+    -1 where there are fewer, and with lse=True each row's log-sum-exp [R] (of
+    rows behind the last group's nothing is written: fresh memory, of any contents).
+    Invalid offsets make everything NaN and -1."""
     import torch
     i32, f32 = torch.int32, torch.float32
     if logits.dim() != 2:
@@ -1120,7 +1122,9 @@ def spec_cache_read(k, k_scale, v, v_scale, lengths, offsets, R, *, first=None, 
     offsets[b] + i of the outputs gets position first[b] + i (first None: 0) of
     sequence b's slot, NaN where it holds none.  R: rows of the outputs, at least
     offsets[B].  dtype: bfloat16 (None) or float32.  Returns (keys, values)
-    [L, R, H, D], values None for a cache of one tensor; out: the two to write to."""
+    [L, R, H, D], values None for a cache of one tensor; out: the two to write to.
+    Rows behind offsets[B] are not written, and no row is if the offsets are
+    invalid: they are as `out` had them, without `out` fresh memory of any contents."""
     import torch
     i32 = torch.int32
     dev, cache = _cache_arg(k, k_scale, v, v_scale, lengths, pages)
@@ -1173,7 +1177,7 @@ class CacheState:
                          pages=self.page_table, out_lengths=self.lengths, stream=stream)
 
     def read(self, offsets, R, *, first=None, slots=None, dtype=None, out=None, stream=None):
-        """spec_cache_read."""
+        """spec_cache_read (rows behind offsets[B], all if the offsets are invalid, are not written)."""
         return spec_cache_read(self.k, self.k_scale, self.v, self.v_scale, self.lengths, offsets, R, first=first,
                                slots=slots, pages=self.page_table, dtype=dtype, out=out, stream=stream)
 
