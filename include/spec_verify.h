@@ -702,8 +702,8 @@ int spec_beam_select(const void *logits, const float *scores, const uint8_t *end
  * (A slot that two groups name is not found: which of its contents
  * the groups then see is not defined.)
  * A device-side wait for the copy engine that runs out (2 s, see Time-outs above)
- * leaves the bytes that were still to be moved as they were; without a workspace
- * there is no status word to say so.
+ * leaves the bytes that were still to be moved as they were, so that the states
+ * are no longer to be used, and is recorded for the device: spec_state_reorder_status.
  */
 #define SPEC_MAX_STATES 64
 
@@ -717,6 +717,24 @@ typedef struct {
 
 int spec_state_reorder(const spec_state_t *states, int n_states, int S, const int32_t *rows, const int32_t *offsets,
                        int B, int R, const int32_t *slots, const int32_t *lengths, void *stream);
+
+/*
+ * SPEC_OK, or SPEC_ERR_TIMEOUT if a wait of a spec_state_reorder call on the
+ * current device has run out since it was last cleared (clear != 0 resets it).  Synchronous:
+ * it waits for the device.  Later calls do not look at it.
+ */
+int spec_state_reorder_status(int *status_out, int clear);
+
+/*
+ * Self-check of that wait (for tests): spec_state_reorder, but for states
+ * that are moved by the copy engine (contiguous runs of a multiple of 16 bytes) every wait
+ * is for one arrival more than there is, so that it gives up (2 s each, up to
+ * 6 s in all), SPEC_ERR_TIMEOUT is recorded and the states stay as they were.  Nothing traps
+ * or faults.
+ */
+int spec_selfcheck_reorder_timeout(const spec_state_t *states, int n_states, int S, const int32_t *rows,
+                                   const int32_t *offsets, int B, int R, const int32_t *slots, const int32_t *lengths,
+                                   void *stream);
 
 /*
  * A cache of keys and values in 8 bits.  Blocks of 32 elements along a head

@@ -35,6 +35,7 @@ from ._binding import (  # noqa: F401
     lib,
     lib_path,
     noalloc_bytes,
+    selfcheck_reorder_timeout,
     selfcheck_wait_timeout,
     shard_workspace,
     shard_workspace_bytes,
@@ -60,6 +61,7 @@ from ._binding import (  # noqa: F401
     spec_verify,
     spec_verify_lse,
     spec_verify_noalloc,
+    state_reorder_status,
     workspace_bytes,
     workspace_status,
 )

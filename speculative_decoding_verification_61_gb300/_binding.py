@@ -32,7 +32,8 @@ EXPORTS = ("spec_verify", "spec_verify_ex", "spec_draft_sample", "spec_draft_sam
            "spec_shard_decide", "spec_shard_draw", "spec_shutdown", "spec_selfcheck_wait_timeout",
            "spec_logits_process", "spec_logits_truncate", "spec_logits_process_truncate",
            "spec_penalty_reset", "spec_penalty_update", "spec_beam_workspace_bytes", "spec_beam_select",
-           "spec_state_reorder", "spec_cache_write", "spec_cache_read")
+           "spec_state_reorder", "spec_state_reorder_status", "spec_selfcheck_reorder_timeout", "spec_cache_write",
+           "spec_cache_read")
 
 
 class SpecError(RuntimeError):
@@ -148,9 +149,12 @@ def lib():
     L.spec_beam_workspace_bytes.restype = sz
     L.spec_beam_select.argtypes = [vp, vp, vp, ip, vp, ip, ip, ip, ip, ip, vp, vp, vp, vp, vp, sz, vp]
     L.spec_state_reorder.argtypes = [vp, ip, ip, vp, vp, ip, ip, vp, vp, vp]
+    L.spec_selfcheck_reorder_timeout.argtypes = L.spec_state_reorder.argtypes
+    L.spec_state_reorder_status.argtypes = [ctypes.POINTER(ctypes.c_int), ip]
     L.spec_cache_write.argtypes = [cp, vp, vp, i64, i64, ip, rp, vp, vp, vp, vp, vp]
     L.spec_cache_read.argtypes = [cp, vp, ip, ip, vp, vp, ip, vp, vp, vp]
-    for name in ("spec_beam_select", "spec_state_reorder", "spec_cache_write", "spec_cache_read"):
+    for name in ("spec_beam_select", "spec_state_reorder", "spec_state_reorder_status", "spec_selfcheck_reorder_timeout",
+                 "spec_cache_write", "spec_cache_read"):
         getattr(L, name).restype = ip
     for name in ("spec_verify", "spec_verify_ex", "spec_draft_sample", "spec_draft_sample_ex",
                  "spec_round_host", "spec_workspace_status", "spec_abi_version",
@@ -1002,7 +1006,8 @@ def spec_state_reorder(states, rows, offsets, *, slots=None, lengths=None, strea
     slots first, or (tensor, slot dimension, position dimension or None); of a state
     with positions the first lengths[slot] (int32 [S], by source) are moved,
     without lengths all.  Lengths go with the slots of all states; a state without
-    positions moves as one whole where its source's length is not 0.  Returns states."""
+    positions moves as one whole where its source's length is not 0.  Returns states.
+    (state_reorder_status: whether a device-side wait has run out.)"""
     import torch
     i32 = torch.int32
     R, B = _size(rows.numel(), "rows"), _size(offsets.numel() - 1, "offsets")
@@ -1025,6 +1030,25 @@ def spec_state_reorder(states, rows, offsets, *, slots=None, lengths=None, strea
         _launch(dev, stream, lib().spec_state_reorder, "spec_state_reorder", start + at * size,
                 min(len(states) - at, MAX_STATES), S, *args, pl)
     return states
+
+
+def state_reorder_status(clear: bool = False) -> int:
+    """SPEC_OK, or SPEC_ERR_TIMEOUT if a spec_state_reorder call's wait has run out on the current device (its
+    states are then no longer to be used).  Waits for the device."""
+    v = ctypes.c_int(0)
+    _raise(lib().spec_state_reorder_status(ctypes.byref(v), 1 if clear else 0), "spec_state_reorder_status")
+    return v.value
+
+
+def selfcheck_reorder_timeout(state, rows, offsets, stream=None):
+    """spec_state_reorder of one tensor with waits that give up (2 to 6 s);
+    afterwards state_reorder_status() is SPEC_ERR_TIMEOUT."""
+    import torch
+    dev, i32 = state.get_device(), torch.int32
+    S = state.shape[0]
+    made = _State(*_state_of(state, S, dev))
+    _launch(dev, stream, lib().spec_selfcheck_reorder_timeout, "spec_selfcheck_reorder_timeout", ctypes.byref(made), 1, S,
+            _ptr(rows, "rows", i32, dev), _ptr(offsets, "offsets", i32, dev), offsets.numel() - 1, rows.numel(), None, None)
 
 
 def _cache_arg(k, k_scale, v, v_scale, lengths, pages):

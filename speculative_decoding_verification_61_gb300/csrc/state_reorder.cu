@@ -48,7 +48,8 @@ struct State {
 
 struct Map {
     int S, B, R;
-    int ctas;  // of a group
+    int ctas;      // of a group
+    int arrivals;  // that a stage's barrier waits for: 1; 2, of which one never comes, in the self-check
     const int32_t *rows, *offsets, *slots, *lengths;
 };
 // A call's arguments, with room for N states: a launch copies them.
@@ -74,6 +75,9 @@ struct Scratch {
     int index[kMaxGroup];  // entries that are sources: which one; else -1
     unsigned sources[2], moves[2];
 };
+
+// SPEC_ERR_TIMEOUT from when a wait has run out on this device; there is no workspace to hold it.
+__device__ int g_status;
 
 // Leaves mv.count = 0 for a group that stays as it is.
 __device__ void find_moves(const Map &job, int b, Moves &mv, Scratch &sc) {
@@ -139,8 +143,8 @@ __device__ __forceinline__ int64_t limit_of(const State &st, const Moves &mv, in
 }
 
 // Bytes [begin, end) of a run, each source's as far as a multiple of 16, in chunks through a ring, by one warp.  A wait
-// that runs out (2 s; a copy that never comes) leaves the rest as it was.
-__device__ void move_bulk(const State &st, unsigned char *base, const Moves &mv, int64_t begin, int64_t end, unsigned char *ring, uint64_t *full) {
+// that runs out (2 s; a copy that never comes) leaves the rest as it was and is recorded: false.
+__device__ bool move_bulk(const State &st, unsigned char *base, const Moves &mv, int64_t begin, int64_t end, unsigned char *ring, uint64_t *full) {
     const int lane = threadIdx.x, D = mv.n_sources, n = mv.count;
     const int stages = D > 8 ? 2 : kStages;  // (copies of a few hundred bytes are slow)
     const int chunk = static_cast<int>(min(int64_t{kRing} / (stages * D), int64_t{16384})) & ~63;  // at least 320 bytes
@@ -179,8 +183,11 @@ __device__ void move_bulk(const State &st, unsigned char *base, const Moves &mv,
             load(c + stages - 1);
         }
     }
-    for (int k = c + 1; c < chunks && k < min(chunks, c + stages - 1); ++k) specv::mbar_wait_bounded(full + k % stages, (k / stages) & 1);
+    const bool ok = c == chunks;
+    if (!ok && lane == 0) specv::set_status(&g_status, SPEC_ERR_TIMEOUT);
+    for (int k = c + 1; !ok && k < min(chunks, c + stages - 1); ++k) specv::mbar_wait_bounded(full + k % stages, (k / stages) & 1);
     bulk_wait_read<0>();
+    return ok;
 }
 
 // The same by columns, a thread a column, for states of any alignment.  The thread has read its column of all
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     const int64_t begin = static_cast<int64_t>(at - line * st.spans) * st.span;
     const int tid = threadIdx.x;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) specv::mbar_init(full + i, 1);
+        for (int i = 0; i < kStages; ++i) specv::mbar_init(full + i, job.map.arrivals);
         specv::fence_barrier_init();
     }
     find_moves(job.map, b, mv, sc);
@@ -262,8 +269,8 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         if (tid < mv.n_sources)
             for (int j = 0, n = tail_of(tid, &from); j < n; ++j) tail[tid][j] = base[mv.source[tid] * st.slot + from + j];
         __syncthreads();
-        if (tid < 32 && begin < (end & ~int64_t{15})) move_bulk(st, base, mv, begin, end, ring, full);
-        __syncthreads();
+        const bool ok = tid >= 32 || begin >= (end & ~int64_t{15}) || move_bulk(st, base, mv, begin, end, ring, full);
+        if (!__syncthreads_and(ok)) return;
         if (tid < mv.count)
             for (int j = 0, n = tail_of(mv.from[tid], &from); j < n; ++j) base[mv.to[tid] * st.slot + from + j] = tail[mv.from[tid]][j];
     } else if (st.width == 8) {
@@ -285,17 +292,12 @@ int launch(const Map &map, const State *states, int n, cudaStream_t s) {
                : SPEC_ERR_CUDA;
 }
 
-}  // namespace
-}  // namespace specstate
-
-extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int S, const int32_t *rows,
-                                  const int32_t *offsets, int B, int R, const int32_t *slots, const int32_t *lengths,
-                                  void *stream) {
-    using namespace specstate;
+int reorder(const spec_state_t *states, int n_states, int S, const int32_t *rows, const int32_t *offsets, int B, int R,
+            const int32_t *slots, const int32_t *lengths, void *stream, int arrivals) {
     if (n_states < 0 || n_states > kMaxStates || S < 0 || B < 0 || B > SPEC_MAX_B || R < 0) return SPEC_ERR_INVALID_ARG;
     if (B == 0 || R == 0 || n_states == 0) return SPEC_OK;
     if (!states || !rows || !offsets) return SPEC_ERR_INVALID_ARG;
-    Map map{S, B, R, 0, rows, offsets, slots, lengths};
+    Map map{S, B, R, 0, arrivals, rows, offsets, slots, lengths};
     State state[kMaxStates];
     int n = 0;
     int64_t bytes[kMaxStates];
@@ -349,3 +351,33 @@ extern "C" int spec_state_reorder(const spec_state_t *states, int n_states, int 
     const auto run = n <= kFewStates ? launch<kFewStates> : launch<kMaxStates>;
     return run(map, state, n, static_cast<cudaStream_t>(stream));
 }
+
+}  // namespace
+}  // namespace specstate
+
+extern "C" {
+
+int spec_state_reorder(const spec_state_t *states, int n_states, int S, const int32_t *rows, const int32_t *offsets,
+                       int B, int R, const int32_t *slots, const int32_t *lengths, void *stream) {
+    return specstate::reorder(states, n_states, S, rows, offsets, B, R, slots, lengths, stream, 1);
+}
+
+int spec_state_reorder_status(int *status_out, int clear) {
+    if (!status_out) return SPEC_ERR_INVALID_ARG;
+    int v = 0;
+    if (!specv::cuda_ok(cudaDeviceSynchronize(), "cudaDeviceSynchronize(reorder status)") ||
+        !specv::cuda_ok(cudaMemcpyFromSymbol(&v, specstate::g_status, sizeof v), "cudaMemcpyFromSymbol(reorder status)"))
+        return SPEC_ERR_CUDA;
+    *status_out = v;
+    const int ok = SPEC_OK;
+    if (clear && !specv::cuda_ok(cudaMemcpyToSymbol(specstate::g_status, &ok, sizeof ok), "cudaMemcpyToSymbol(reorder status)")) return SPEC_ERR_CUDA;
+    return SPEC_OK;
+}
+
+int spec_selfcheck_reorder_timeout(const spec_state_t *states, int n_states, int S, const int32_t *rows,
+                                   const int32_t *offsets, int B, int R, const int32_t *slots, const int32_t *lengths,
+                                   void *stream) {
+    return specstate::reorder(states, n_states, S, rows, offsets, B, R, slots, lengths, stream, 2);
+}
+
+}  // extern "C"
