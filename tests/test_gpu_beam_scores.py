@@ -5,6 +5,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
+import states_ref as ref
 from beam_check import LOWEST, check
 
 torch = pytest.importorskip("torch")
@@ -80,6 +81,28 @@ def test_ordered_by_its_logits_at_a_very_low_score(sv):
     z = rng.standard_normal((3, 3000)).astype(f32)
     z[:, ::3] = -1e31
     run(sv, z, np.array([-1e31, -1e31, LOWEST], f32), [0, 2, 3], 100, "fp32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mask", [-1e18, -1e20, -1e29, -1e30, -1e31, -1e35, LOWEST_BF16, LOWEST])
+@pytest.mark.parametrize("G,V", [(1, 64), (24, 2048), (160, 64)])
+def test_masked_tokens_of_several_rows_tie(sv, dtype, mask, G, V):
+    """More candidates than tokens that are not masked: those masked by one value have equal scores in 64 bits, whatever
+    their rows' scores, and go by row, then token."""
+    rng = np.random.default_rng(G)
+    W, n = 3, 48
+    R = G * W
+    z = np.full((R, V), max(mask, LOWEST_BF16) if dtype == "bf16" else mask, f32)
+    for r in range(R):  # ten tokens, an eighth and more apart from each other within the group
+        at = rng.permutation(V)[:10]
+        z[r, at] = np.arange(10) * 0.5
+    scores = (rng.permutation(R) % 7 - 20 + 0.125 * (np.arange(R) % W)).astype(f32)
+    t = dev(z).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    off = np.arange(0, R + 1, W)
+    want = ref.beam_select(t.float().cpu().numpy(), scores, off, n)
+    got = sv.spec_beam_select(t, dev(scores), dev(off.astype(i32)), n)
+    assert (np.abs(np.diff(want[0][:, :30])) > 1e-3).all()  # no two of the others so close that their order is open
+    assert (got[1].cpu().numpy() == want[1]).all() and (got[2].cpu().numpy() == want[2]).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
