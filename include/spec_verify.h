@@ -652,7 +652,9 @@ int spec_penalty_update(int32_t *counts, int32_t *seen, int S, int V, const int3
  * descending, then row, then token; places without a candidate get -inf, -1, -1.
  * Scores are compared in two fp32 terms (48 bits) and rounded to fp32 at the
  * end; one below fp32's lowest finite value is compared all the same and
- * written as that value.  The row sums are of fp32 terms, whose roundings may
+ * written as that value.  Of a logit more than 2^33 below its row's best the score is
+ * compared to 2^-52 of that distance: tokens masked by one large value tie between
+ * rows.  The row sums are of fp32 terms, whose roundings may
  * all be alike (equal logits): a row's ln sum is off by at most 128 * 2^-24 = 7.6e-6,
  * so that candidates of different rows whose scores differ by less than twice that may
  * change places; those of one row only if 2^-46 of the score does not tell them
