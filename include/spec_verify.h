@@ -695,10 +695,11 @@ int spec_beam_select(const void *logits, const float *scores, const uint8_t *end
  * T positions each.  With lengths (int32 [S]), the first
  * min(lengths[s(rows[i])], T) positions of each run are moved (of a negative length none)
  * and the others stay as they are; without, all T.
- *   states       HOST array of n_states <= SPEC_MAX_STATES states; no two overlap
+ *   states       HOST array of n_states <= SPEC_MAX_STATES states; no two overlap, and none
+ *                overlaps rows, offsets, slots or lengths
  *   rows         int32 [R]; an entry behind the last group's is not read
  *   slots        int32 [R]: one slot is named at most once in a call
- *   lengths      int32 [S] or NULL; none of the states
+ *   lengths      int32 [S] or NULL
  * A group that holds a slot outside [0, S), a slot twice, or a row that is neither -1
  * nor of the group is left as it is, as all are if the offsets are invalid.
  * (A slot that two groups name is not found: which of its contents

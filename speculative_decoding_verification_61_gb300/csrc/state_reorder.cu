@@ -316,8 +316,12 @@ int reorder(const spec_state_t *states, int n_states, int S, const int32_t *rows
         st.data = static_cast<unsigned char *>(in.data), st.unit = in.unit, st.T = static_cast<int>(in.T);
         for (int i = 0; i < n; ++i)
             if (st.data < state[i].data + bytes[i] && state[i].data < st.data + all) return SPEC_ERR_INVALID_ARG;
-        const unsigned char *l = reinterpret_cast<const unsigned char *>(lengths);
-        if (l && st.data < l + static_cast<int64_t>(S) * 4 && l < st.data + all) return SPEC_ERR_INVALID_ARG;
+        // nor one that overlaps what says how it is moved: other CTAs still read that
+        const auto overlaps = [&](const int32_t *p, int64_t entries) {
+            const unsigned char *l = reinterpret_cast<const unsigned char *>(p);
+            return l && st.data < l + entries * 4 && l < st.data + all;
+        };
+        if (overlaps(lengths, S) || overlaps(rows, R) || overlaps(slots, R) || overlaps(offsets, int64_t{B} + 1)) return SPEC_ERR_INVALID_ARG;
         st.planes = static_cast<int>(in.planes), st.runs = static_cast<int>(in.runs);
         const uintptr_t low = reinterpret_cast<uintptr_t>(st.data) | static_cast<uintptr_t>(st.run);
         st.width = (low & 15) == 0 ? 16 : (low & 7) == 0 ? 8 : (low & 3) == 0 ? 4 : 1;

@@ -1,0 +1,28 @@
+"""CPU: calls of the state and cache operators whose buffers overlap are refused."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+FAKE = 1 << 20  # never read: the checks come first
+FAR = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def sv():
+    from speculative_decoding_verification_61_gb300 import build
+    build.build()
+    import speculative_decoding_verification_61_gb300 as m
+    return m
+
+
+@pytest.mark.parametrize("which", ["rows", "offsets", "slots", "lengths"])
+@pytest.mark.parametrize("at", [0, -4, 508])
+def test_a_state_that_says_how_it_is_moved(sv, which, at):
+    """4 slots of 128 bytes; an array of 4 entries (2 offsets) that starts in front of it, with it, with its last word."""
+    from speculative_decoding_verification_61_gb300._binding import _State
+    a = dict(rows=FAR, offsets=FAR + 4096, slots=FAR + 8192, lengths=None)
+    a[which] = FAKE + at
+    state = _State(FAKE, 1, 1, 8, 16)
+    assert sv.lib().spec_state_reorder(ctypes.byref(state), 1, 4, a["rows"], a["offsets"], 1, 4, a["slots"], a["lengths"], None) == -1
