@@ -784,7 +784,7 @@ typedef struct {
  *                multiples of 16 elements (32 bytes)
  *   slots        int32 [B], distinct; NULL: b
  *   out_lengths  int32 [S]: lengths with the kept rows of each sequence added;
- *                lengths itself for in place; NULL: not written (all calls of a
+ *                lengths itself for in place (else it may not overlap them); NULL: not written (all calls of a
  *                step but the last, where layers are written one by one)
  * A sequence with num_accepted < 0 or more than it drafted, a slot outside [0, S), a negative
  * length, or a tree path that is not one of num_accepted + 1 nodes, is

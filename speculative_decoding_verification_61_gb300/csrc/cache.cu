@@ -606,6 +606,9 @@ int spec_cache_write(const spec_cache_t *cache, const void *keys, const void *va
     if (!aligned32(keys) || !aligned32(values) || layer_stride % kGranule != 0 || row_stride % kGranule != 0) return SPEC_ERR_ALIGNMENT;
     if (row_stride < static_cast<int64_t>(cache->H) * cache->D || layer_stride < 0) return SPEC_ERR_INVALID_ARG;
     if (rows->R >= kMaxCtas) return SPEC_ERR_INVALID_ARG;
+    // the lengths themselves, or clear of them: written while they are still read
+    if (out_lengths && out_lengths != cache->lengths && out_lengths < cache->lengths + cache->S && cache->lengths < out_lengths + cache->S)
+        return SPEC_ERR_INVALID_ARG;
     if (rows->B == 0 && (!out_lengths || out_lengths == cache->lengths)) return SPEC_OK;
     w.in[0] = static_cast<const char *>(keys), w.in[1] = static_cast<const char *>(values);
     w.layer_stride = layer_stride * size, w.row_stride = row_stride * size;

@@ -26,3 +26,12 @@ def test_a_state_that_says_how_it_is_moved(sv, which, at):
     a[which] = FAKE + at
     state = _State(FAKE, 1, 1, 8, 16)
     assert sv.lib().spec_state_reorder(ctypes.byref(state), 1, 4, a["rows"], a["offsets"], 1, 4, a["slots"], a["lengths"], None) == -1
+
+
+@pytest.mark.parametrize("at,B,code", [(4, 2, -1), (-4, 2, -1), (4, 0, -1), (-12, 2, -1), (12, 2, -1), (0, 0, 0)])
+def test_lengths_written_beside_themselves(sv, at, B, code):
+    """4 lengths, and 4 to be written that start some bytes from them."""
+    from speculative_decoding_verification_61_gb300._binding import _Cache, _Rows
+    cache = _Cache(FAR, FAR, None, None, 1, 4, 16, 2, 64, None, 4, 1, FAKE)
+    rows = _Rows(4, B, 8, FAR, None, None, 0)
+    assert sv.lib().spec_cache_write(ctypes.byref(cache), FAR, None, 0, 128, 1, ctypes.byref(rows), None, None, None, FAKE + at, None) == code
