@@ -1025,6 +1025,10 @@ def spec_state_reorder(states, rows, offsets, *, slots=None, lengths=None, strea
     made = array.array("q")  # five fields of 64 bits each, as in _State
     for x in states:
         made.extend(_state_of(x, S, dev))
+    if len(states) > MAX_STATES:  # each launch looks at its own states only
+        parts = sorted((made[i], made[i] + S * math.prod(made[i + 1:i + 5])) for i in range(0, len(made), 5) if math.prod(made[i + 1:i + 5]))
+        if any(b[0] < a[1] for a, b in zip(parts, parts[1:])):
+            raise ValueError("no two states may overlap")
     start, size = made.buffer_info()[0], ctypes.sizeof(_State)
     for at in range(0, len(states), MAX_STATES):
         _launch(dev, stream, lib().spec_state_reorder, "spec_state_reorder", start + at * size,

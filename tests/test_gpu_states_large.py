@@ -53,3 +53,15 @@ def test_positions_of_4_gib(sv, lengths):
     sv.spec_state_reorder([(t, 0, 1)], dev(np.array(rows, i32)), dev(np.array([0, S], i32)), lengths=dev(np.array(lengths, i32)))
     assert torch.equal(t[:, :, at], want)
     assert int(t.count_nonzero()) == S * 2 * len(at)
+
+
+def test_states_of_different_launches_that_overlap(sv):
+    """More states than one launch takes, one of them twice (or a part of another): refused before anything is moved."""
+    ts = [torch.arange(12, dtype=torch.int32, device="cuda").view(4, 3) for _ in range(70)]
+    rows, off = dev(np.array([1, 2, 3, 0], i32)), dev(np.array([0, 4], i32))
+    for bad in (ts + ts[:1], ts + [ts[5].flatten()[4:8].view(4, 1)]):
+        with pytest.raises(ValueError, match="overlap"):
+            sv.spec_state_reorder(bad, rows, off)
+    assert all(torch.equal(t, ts[0]) and int(t[0, 0]) == 0 for t in ts)
+    sv.spec_state_reorder(ts + [torch.empty((4, 0), device="cuda")] * 2, rows, off)
+    assert all(int(t[0, 0]) == 3 for t in ts)
