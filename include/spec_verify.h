@@ -756,7 +756,8 @@ int spec_selfcheck_reorder_timeout(const spec_state_t *states, int n_states, int
  *   pages        int32 [S, M]: slot s has its positions j * T .. j * T + T - 1 on page
  *                pages[s, j]; NULL: slot s has the page s alone (P = S, M = 1)
  *   lengths      int32 [S]: the positions of each slot that are held; a negative one: the slot is invalid
- * D a multiple of 16, at most 1024; H * D at most 65536.
+ * D a multiple of 16, at most 1024; H * D at most 65536; of a position's blocks, in all layers and tensors,
+ * less than 2^23.
  */
 typedef struct {
     void *k;

@@ -1184,7 +1184,7 @@ class CacheState:
     def __init__(self, L: int, S: int, T: int, H: int, D: int, *, pages=None, max_pages=None, values: bool = True,
                  device="cuda"):
         import torch
-        if min(L, S, T, H) <= 0 or D <= 0 or D % 16 or D > 1024 or H * D > 65536:
+        if min(L, S, T, H) <= 0 or D <= 0 or D % 16 or D > 1024 or H * D > 65536 or L * (1 + values) * H * ((D + 31) // 32) >= 1 << 23:
             raise ValueError(f"invalid cache L={L}, S={S}, T={T}, H={H}, D={D}")
         if (pages is None) != (max_pages is None):
             raise ValueError("pages and max_pages go together")

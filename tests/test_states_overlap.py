@@ -1,4 +1,4 @@
-"""CPU: calls of the state and cache operators whose buffers overlap are refused."""
+"""CPU: what the state and cache operators refuse: buffers that overlap, and more layers than a position's blocks allow."""
 from __future__ import annotations
 
 import ctypes
@@ -35,3 +35,14 @@ def test_lengths_written_beside_themselves(sv, at, B, code):
     cache = _Cache(FAR, FAR, None, None, 1, 4, 16, 2, 64, None, 4, 1, FAKE)
     rows = _Rows(4, B, 8, FAR, None, None, 0)
     assert sv.lib().spec_cache_write(ctypes.byref(cache), FAR, None, 0, 128, 1, ctypes.byref(rows), None, None, None, FAKE + at, None) == code
+
+
+@pytest.mark.parametrize("L,H,D,values,fits", [(1023, 4096, 16, True, True), (1024, 4096, 16, True, False), (2047, 4096, 16, False, True),
+                                               (2048, 4096, 16, False, False), (2048, 64, 1024, True, False), (2047, 64, 1024, True, True)])
+def test_a_positions_blocks(sv, L, H, D, values, fits):
+    from speculative_decoding_verification_61_gb300._binding import _Cache
+    cache = _Cache(FAR, FAR, FAR if values else None, FAR if values else None, L, 1, 1, H, D, None, 1, 1, FAKE)
+    assert sv.lib().spec_cache_read(ctypes.byref(cache), FAR, 0, 8, None, None, 1, FAR, FAR if values else None, None) == (0 if fits else -1)
+    if not fits:
+        with pytest.raises(ValueError, match="invalid cache"):
+            sv.CacheState(L, 1, 1, H, D, values=values, device="cpu")
